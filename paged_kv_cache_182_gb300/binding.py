@@ -22,6 +22,8 @@ k, v [B, HK, SK, D]).
 from __future__ import annotations
 
 import ctypes
+import math
+from fractions import Fraction
 from pathlib import Path
 
 import torch
@@ -70,6 +72,42 @@ class VjpOpts(ctypes.Structure):
         ("workspace_bytes", ctypes.c_size_t),
         ("status", ctypes.c_void_p),
         ("kernel", ctypes.c_int),
+        ("wait_limit_ns", ctypes.c_ulonglong),
+    ]
+
+
+class RotaryOpts(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int),
+        ("interleaved", ctypes.c_int),
+        ("inverse", ctypes.c_int),
+        ("factor", ctypes.c_float),
+        ("q_strides", ctypes.c_longlong * 3),
+        ("k_strides", ctypes.c_longlong * 3),
+        ("v_strides", ctypes.c_longlong * 3),
+        ("slot_mapping", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_cache", ctypes.c_void_p),
+        ("v_cache", ctypes.c_void_p),
+        ("BLOCK", ctypes.c_int),
+        ("num_blocks", ctypes.c_int),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class EvictOpts(ctypes.Structure):
+    _fields_ = [
+        ("max_blocks", ctypes.c_int),
+        ("num_blocks", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("budget", ctypes.c_int),
+        ("keep_first", ctypes.c_int),
+        ("keep_last", ctypes.c_int),
+        ("dst_table", ctypes.c_void_p),
+        ("dst_max_blocks", ctypes.c_int),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("status", ctypes.c_void_p),
         ("wait_limit_ns", ctypes.c_ulonglong),
     ]
 
@@ -125,6 +163,12 @@ def load(path: Path = LIBRARY) -> ctypes.CDLL:
                                      ctypes.POINTER(VjpOpts), P]
     lib.pa_attention_vjp_workspace_bytes.restype = ctypes.c_size_t
     lib.pa_attention_vjp_workspace_bytes.argtypes = [I, I, I, I, I, I]
+    lib.pa_rotary.restype = I
+    lib.pa_rotary.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, ctypes.POINTER(RotaryOpts), P]
+    lib.pa_cache_evict.restype = I
+    lib.pa_cache_evict.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, ctypes.POINTER(EvictOpts), P]
+    lib.pa_cache_evict_workspace_bytes.restype = ctypes.c_size_t
+    lib.pa_cache_evict_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
     lib.pa_cache_append.restype = I
     lib.pa_cache_append.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, P, P]
     return lib
@@ -653,3 +697,289 @@ def attention_vjp(q, k, v, y, g, mask=None, *, scale: float, causal: bool = Fals
     """dq, dk, dv of attention (pa_attention_vjp): see ``VjpPlan``."""
     return VjpPlan(q, k, v, y, g, mask, scale=scale, causal=causal, out_dtype=out_dtype,
                    kernel=kernel, status=status, out=out).run(stream)
+
+
+# ------------------------------------------------------------------- rotary positions
+class RotaryTable:
+    """Angles per position of a rotary embedding (``rotary_table``): ``turns``
+    (int64 [rot / 2] on the device, 2^64 = one turn), the ``factor`` on the
+    rotated columns and ``rot``, the columns that turn."""
+
+    def __init__(self, turns, factor: float, rot: int):
+        self.turns, self.factor, self.rot = turns, float(factor), int(rot)
+
+
+def rotary_frequencies(rot: int, *, base: float = 10000.0, scaling=None):
+    """(radians per position of the ``rot`` / 2 pairs, factor) in 64 bits.
+
+    Pair i turns by base^(-2 i / rot) per position.  ``scaling`` stretches
+    that to contexts longer than the model was trained on:
+      None
+      ("linear", f)                     every frequency divided by f
+      ("ntk", f)                        base times f^(rot / (rot - 2))
+      ("bands", f, L, low, high)        pairs with at least ``high`` turns in
+                                        the original length L are kept, those
+                                        with at most ``low`` divided by f,
+                                        those between mixed by their turns
+      ("yarn", f, L, fast, slow)        the same by pair index: kept up to the
+                                        pair with ``fast`` turns in L, divided
+                                        by f from the one with ``slow`` on,
+                                        a linear ramp between; factor
+                                        0.1 ln f + 1
+    """
+    if rot < 2 or rot % 2:
+        raise ValueError("rot must be even and at least 2")
+    if not base > 1.0:
+        raise ValueError("base must be greater than 1")
+    kind, args = (None, ()) if scaling is None else (scaling[0], tuple(float(a) for a in scaling[1:]))
+    need = {None: 0, "linear": 1, "ntk": 1, "bands": 4, "yarn": 4}
+    if kind not in need or len(args) != need[kind] or any(not a > 0.0 for a in args):
+        raise ValueError(f"unknown rotary scaling {scaling!r}")
+    factor = 1.0
+    if kind == "ntk":
+        if rot < 4:
+            raise ValueError("ntk scaling needs rot >= 4")
+        base = base * args[0] ** (rot / (rot - 2))
+    inv = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    if kind == "linear":
+        inv = [x / args[0] for x in inv]
+    elif kind == "bands":
+        f, length, low, high = args
+        if not high > low:
+            raise ValueError("bands: high must be greater than low")
+        for i, x in enumerate(inv):
+            keep = min(1.0, max(0.0, (length * x / (2 * math.pi) - low) / (high - low)))
+            inv[i] = x * (keep + (1.0 - keep) / f)
+    elif kind == "yarn":
+        f, length, fast, slow = args
+        at = [rot * math.log(length / (2 * math.pi * n)) / (2 * math.log(base)) for n in (fast, slow)]
+        low, high = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rot - 1)
+        for i, x in enumerate(inv):
+            ramp = min(1.0, max(0.0, (i - low) / max(high - low, 0.001)))
+            inv[i] = x * (1.0 - ramp + ramp / f)
+        factor = 0.1 * math.log(f) + 1.0
+    return inv, factor
+
+
+# 1 / (2 pi) to 2^-192: the table entries below need more than 64 bits of it
+_INV_2PI = (Fraction(1) / 2 / Fraction("3.14159265358979323846264338327950288419716939937510582097494459"))
+
+
+def rotary_table(rot: int, *, base: float = 10000.0, scaling=None, device="cuda") -> RotaryTable:
+    """The table of a rotary embedding (see ``rotary_frequencies``), made once
+    and kept: each pair's angle per position as a 64-bit fraction of a turn."""
+    inv, factor = rotary_frequencies(rot, base=base, scaling=scaling)
+    turns = [int(Fraction(x) * _INV_2PI * 2 ** 64 + Fraction(1, 2)) % 2 ** 64 for x in inv]
+    signed = [t - 2 ** 64 if t >= 2 ** 63 else t for t in turns]
+    return RotaryTable(torch.tensor(signed, dtype=torch.int64, device=device), factor, rot)
+
+
+def _row_strides(t):
+    s = t.stride()
+    if t.shape[-1] > 1 and s[3] != 1:
+        raise ValueError("the last dimension of q, k and v must be contiguous")
+    # a dimension of one element has no stride that matters
+    return tuple(0 if n == 1 else int(x) for n, x in zip(t.shape[:3], s[:3]))
+
+
+class RotaryPlan:
+    """One prepared rotary call (pa_rotary) on fixed device tensors: q
+    [B, H, N, D] and k [B, KV, N, D] (either may be None) turned by
+    ``positions`` (int32 [B, N]).  q and k may be strided views (slices of a
+    fused projection) with contiguous columns; the outputs are contiguous.
+    ``inverse=True`` turns back: with q and k the gradients arriving at the
+    outputs, the result is the gradient of the inputs.  ``run()`` returns
+    (q_out, k_out)."""
+
+    def __init__(self, q, k, positions, table: RotaryTable, *, interleaved: bool = False,
+                 inverse: bool = False, q_out=None, k_out=None):
+        self._prepare(q, k, None, positions, table, interleaved, inverse, q_out, k_out)
+
+    def _prepare(self, q, k, v, positions, table, interleaved, inverse, q_out, k_out, slots=None,
+                 caches=None, status=None):
+        rows = [t for t in (q, k) if t is not None]
+        if not rows or any(t.dim() != 4 for t in rows):
+            raise ValueError("shapes: q [B, H, N, D], k [B, KV, N, D]")
+        B, _, N, D = rows[0].shape
+        H, KV = (0 if t is None else int(t.shape[1]) for t in (q, k))
+        dt, dev = rows[0].dtype, rows[0].device
+        if dt not in _DT or any(t.dtype != dt for t in rows):
+            raise TypeError("q and k must share one supported dtype")
+        if tuple(rows[-1].shape) != (B, rows[-1].shape[1], N, D):
+            raise ValueError("q and k must agree in batch, rows and head size")
+        if tuple(positions.shape) != (B, N) or positions.dtype != torch.int32:
+            raise ValueError("positions must be an int32 [B, N] tensor")
+        if not positions.is_contiguous():
+            raise ValueError("positions must be contiguous")
+        if table.rot > D:
+            raise ValueError("the table turns more columns than a head has")
+        for t in (*rows, positions, table.turns):
+            if not t.is_cuda or t.device != dev:
+                raise ValueError("all tensors must be CUDA tensors on one device")
+        outs = []
+        for t, o in ((q, q_out), (k, k_out)):
+            if t is None:
+                outs.append(None)
+                continue
+            if o is None:
+                o = torch.empty(t.shape, dtype=dt, device=dev)
+            elif tuple(o.shape) != tuple(t.shape) or o.dtype != dt or not o.is_contiguous() or o.device != dev:
+                raise ValueError("q_out and k_out must be contiguous tensors like q and k")
+            outs.append(o)
+        self.q_out, self.k_out = outs
+        o = RotaryOpts()
+        o.dtype, o.interleaved, o.inverse = _DT[dt], int(bool(interleaved)), int(bool(inverse))
+        o.factor = table.factor
+        for name, t in (("q_strides", q), ("k_strides", k), ("v_strides", v)):
+            if t is not None:
+                getattr(o, name)[:] = _row_strides(t)
+        if slots is not None:
+            o.slot_mapping, o.v = slots.data_ptr(), v.data_ptr()
+            o.k_cache, o.v_cache = caches[0].data_ptr(), caches[1].data_ptr()
+            o.num_blocks, o.BLOCK = int(caches[0].shape[0]), int(caches[0].shape[1])
+            o.status = None if status is None else status.data_ptr()
+        self.opts, self.device = o, dev
+        self._keep = (q, k, v, positions, table, slots, caches, status)
+        self._args = (_ptr(q), _ptr(k), _ptr(positions), _ptr(table.turns), _ptr(self.q_out),
+                      _ptr(self.k_out), B, H, KV, N, D, table.rot, ctypes.byref(self.opts))
+
+    def run(self, stream=None):
+        """Enqueue on ``stream`` (default: torch's current stream); returns (q_out, k_out)."""
+        if torch.cuda.current_device() == self.device.index:
+            rc = LIB.pa_rotary(*self._args, _stream_handle(stream))
+        else:
+            with torch.cuda.device(self.device):
+                rc = LIB.pa_rotary(*self._args, _stream_handle(stream))
+        if rc != 0:
+            raise PagedAttentionError(rc)
+        return self.q_out, self.k_out
+
+
+class RotaryAppendPlan(RotaryPlan):
+    """A rotary call that also stores the step's rows in the paged cache: the
+    rotated k and the untouched v of row n of sequence b go to slot
+    ``slot_mapping[b, n]`` of ``k_cache`` / ``v_cache`` [num_blocks, BLOCK, KV, D]
+    (as ``cache_append`` does; -1 stores nothing).  ``run()`` returns the
+    rotated (q_out, k_out), ready for ``decode``."""
+
+    def __init__(self, q, k, v, positions, slot_mapping, k_cache, v_cache, table: RotaryTable, *,
+                 interleaved: bool = False, q_out=None, k_out=None, status=None):
+        if k is None or tuple(v.shape) != tuple(k.shape) or v.dtype != k.dtype:
+            raise ValueError("k and v must share one shape and dtype")
+        if k_cache.dim() != 4 or tuple(v_cache.shape) != tuple(k_cache.shape) or \
+                tuple(k_cache.shape[2:]) != (k.shape[1], k.shape[3]):
+            raise ValueError("shapes: caches [num_blocks, BLOCK, KV, D]")
+        if k_cache.dtype != k.dtype or v_cache.dtype != k.dtype:
+            raise TypeError("the caches must have the dtype of k and v")
+        if tuple(slot_mapping.shape) != (k.shape[0], k.shape[2]) or slot_mapping.dtype != torch.int32:
+            raise ValueError("slot_mapping must be an int32 [B, N] tensor")
+        for t in (v, k_cache, v_cache, slot_mapping):
+            if not t.is_cuda or t.device != k.device:
+                raise ValueError("all tensors must be CUDA tensors on one device")
+        for t in (k_cache, v_cache, slot_mapping):
+            if not t.is_contiguous():
+                raise ValueError("the caches and slot_mapping must be contiguous")
+        self._prepare(q, k, v, positions, table, interleaved, False, q_out, k_out, slot_mapping,
+                      (k_cache, v_cache), status)
+
+
+def rotary(q, k, positions, table: RotaryTable, *, interleaved: bool = False, inverse: bool = False,
+           q_out=None, k_out=None, stream=None):
+    """q and k turned by their positions (pa_rotary): see ``RotaryPlan``."""
+    return RotaryPlan(q, k, positions, table, interleaved=interleaved, inverse=inverse, q_out=q_out,
+                      k_out=k_out).run(stream)
+
+
+def rotary_append(q, k, v, positions, slot_mapping, k_cache, v_cache, table: RotaryTable, *,
+                  interleaved: bool = False, q_out=None, k_out=None, status=None, stream=None):
+    """``rotary`` with the store of the new rows in the cache: see ``RotaryAppendPlan``."""
+    return RotaryAppendPlan(q, k, v, positions, slot_mapping, k_cache, v_cache, table,
+                            interleaved=interleaved, q_out=q_out, k_out=k_out, status=status).run(stream)
+
+
+# ------------------------------------------------------------------- cache eviction
+class EvictPlan:
+    """One prepared eviction (pa_cache_evict) on fixed device tensors: every
+    sequence of more than ``budget`` cached tokens keeps its first
+    ``keep_first``, its last ``keep_last`` and, of those between, the ones
+    with the largest ``key_weights`` (float32 [B, max_blocks * BLOCK], as
+    ``ScoredPlan`` accumulates them; equal weights: the lowest index), in
+    order.  Their K and V rows move to the sequence's first slots, or with
+    ``dst_table`` (int32 [B, dst_max_blocks]) into that table's blocks.
+
+    ``run()`` returns (new_lens [B], kept [B, budget], weights_out like
+    ``key_weights``): the shortened lengths, the kept tokens' old indices (-1
+    behind them) and their weights (0 behind them).  ``seq_lens`` and
+    ``key_weights`` are left as they are: the loop goes on with the returned
+    ones.  Blocks shared between sequences must not be moved in place."""
+
+    def __init__(self, k_cache, v_cache, block_table, seq_lens, key_weights, *, budget: int,
+                 keep_first: int = 0, keep_last: int = 0, dst_table=None, new_lens=None, kept=None,
+                 weights_out=None, status=None):
+        if k_cache.dim() != 4 or tuple(v_cache.shape) != tuple(k_cache.shape):
+            raise ValueError("shapes: caches [num_blocks, BLOCK, KV, D]")
+        NB, BLOCK, KV, D = k_cache.shape
+        if k_cache.dtype not in _DT or v_cache.dtype != k_cache.dtype:
+            raise TypeError("k_cache and v_cache must share one supported dtype")
+        if block_table.dim() != 2 or tuple(seq_lens.shape) != (block_table.shape[0],):
+            raise ValueError("block_table must be [B, max_blocks] and seq_lens [B]")
+        B, maxb = (int(x) for x in block_table.shape)
+        if dst_table is not None and (dst_table.dim() != 2 or dst_table.shape[0] != B):
+            raise ValueError("dst_table must be [B, dst_max_blocks]")
+        if any(t.dtype != torch.int32 for t in (block_table, seq_lens, dst_table) if t is not None):
+            raise TypeError("block_table, seq_lens and dst_table must be int32")
+        if tuple(key_weights.shape) != (B, maxb * BLOCK) or key_weights.dtype != torch.float32:
+            raise ValueError("key_weights must be float32 [B, max_blocks * BLOCK]")
+        budget = int(budget)
+        if budget < 1:
+            raise ValueError("budget must be at least 1")
+        dev = k_cache.device
+
+        def output(t, shape, dtype, name):
+            if t is None:
+                return torch.empty(shape, dtype=dtype, device=dev)
+            if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+                raise ValueError(f"{name} must be {dtype} {list(shape)}")
+            return t
+
+        self.new_lens = output(new_lens, (B,), torch.int32, "new_lens")
+        self.kept = output(kept, (B, budget), torch.int32, "kept")
+        self.weights_out = output(weights_out, (B, maxb * BLOCK), torch.float32, "weights_out")
+        tensors = (k_cache, v_cache, block_table, seq_lens, key_weights, self.new_lens, self.kept,
+                   self.weights_out)
+        for t in tensors + (() if dst_table is None else (dst_table,)):
+            if not t.is_cuda or t.device != dev:
+                raise ValueError("all tensors must be CUDA tensors on one device")
+            if not t.is_contiguous():
+                raise ValueError("all tensors must be contiguous")
+        need = int(LIB.pa_cache_evict_workspace_bytes(B, KV, D, maxb, BLOCK, budget, _DT[k_cache.dtype]))
+        self.workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        self.opts = EvictOpts(
+            max_blocks=maxb, num_blocks=NB, dtype=_DT[k_cache.dtype], budget=budget,
+            keep_first=int(keep_first), keep_last=int(keep_last),
+            dst_table=None if dst_table is None else dst_table.data_ptr(),
+            dst_max_blocks=0 if dst_table is None else int(dst_table.shape[1]),
+            workspace=self.workspace.data_ptr(), workspace_bytes=need,
+            status=None if status is None else status.data_ptr())
+        self.device = dev
+        self._keep = (tensors, dst_table, status)
+        self._args = (*(_ptr(t) for t in tensors), B, KV, D, BLOCK, ctypes.byref(self.opts))
+
+    def run(self, stream=None):
+        """Enqueue on ``stream`` (default: torch's current stream)."""
+        if torch.cuda.current_device() == self.device.index:
+            rc = LIB.pa_cache_evict(*self._args, _stream_handle(stream))
+        else:
+            with torch.cuda.device(self.device):
+                rc = LIB.pa_cache_evict(*self._args, _stream_handle(stream))
+        if rc != 0:
+            raise PagedAttentionError(rc)
+        return self.new_lens, self.kept, self.weights_out
+
+
+def cache_evict(k_cache, v_cache, block_table, seq_lens, key_weights, *, budget: int,
+                keep_first: int = 0, keep_last: int = 0, dst_table=None, status=None, stream=None):
+    """Shortens every sequence to its budget (pa_cache_evict): see ``EvictPlan``."""
+    return EvictPlan(k_cache, v_cache, block_table, seq_lens, key_weights, budget=budget,
+                     keep_first=keep_first, keep_last=keep_last, dst_table=dst_table,
+                     status=status).run(stream)
