@@ -1106,17 +1106,7 @@ __device__ void merge_segment(const SplitParams& p, const Sched& sc, const int4 
     int TPI = (kConsumerWarps * 32) / NI;
     TPI = TPI >= 8 ? 8 : TPI >= 4 ? 4 : TPI >= 2 ? 2 : 1;
     const int per_pass = kT / TPI;
-    const int sub = tid % TPI, i0 = tid / TPI;
-    float4 O[4];
-    int rl_of[4];
-    bool act[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        O[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int item = i0 + j * per_pass;
-        act[j] = item < NI;
-        rl_of[j] = act[j] ? item >> LG4 : 0;
-    }
+    const int sub = tid % TPI;
     // (M, L) of each row: warp w takes rows w, w + nwarps, ...; lanes split
     // the records.  With at most 32 records, four rows' loads are in flight.
     if (n <= 32) {
@@ -1179,81 +1169,95 @@ __device__ void merge_segment(const SplitParams& p, const Sched& sc, const int4 
         a.z = fmaf(f, v.z, a.z);
         a.w = fmaf(f, v.w, a.w);
     };
-    {
-        auto add_record = [&](int c, float4* v, float* f) {
-            const size_t rec = seg_record(p, sp, c, it.rsg, it.kh);
+    // four items a thread at a time: one round for up to 32 rows at D = 128
+    // (every 16-bit pass), two for the 64 rows of a float32 pass
+    for (int i0 = tid / TPI; i0 - tid / TPI < NI; i0 += 4 * per_pass) {
+        float4 O[4];
+        int rl_of[4];
+        bool act[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (!act[j])
-                    continue;
-                const int item = i0 + j * per_pass;
-                const size_t wrow = rec * p.row_stride + rl_of[j];
-                v[j] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + wrow * D) + (item & (D4 - 1)));
-                f[j] = fac_smem ? fac[c * R_cta + rl_of[j]]
-                                : fast_exp2(__ldcg(&p.ws_ml[wrow]).x - tot[rl_of[j]].x);
-            }
-        };
-        int c = sub;
-        if (NI <= per_pass) {
-            // one item per thread: eight records in flight
-            const int rl = rl_of[0];
-            const int d4 = i0 & (D4 - 1);
-            for (; c + 7 * TPI < n; c += 8 * TPI) {
-                float4 v[8];
-                float f[8];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const size_t wrow = seg_record(p, sp, c + u * TPI, it.rsg, it.kh) * p.row_stride + rl;
-                    v[u] = act[0] ? __ldcg(reinterpret_cast<const float4*>(p.ws_o + wrow * D) + d4)
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-                    f[u] = fac_smem ? fac[(c + u * TPI) * R_cta + rl]
-                                    : fast_exp2(__ldcg(&p.ws_ml[wrow]).x - tot[rl].x);
-                }
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    fma4(O[0], f[u], v[u]);
-            }
-        }
-        // items of up to four rows per thread: two records in flight per item
-        for (; c + TPI < n; c += 2 * TPI) {
-            float4 va[4], vb[4];
-            float fa[4], fb[4];
-            add_record(c, va, fa);
-            add_record(c + TPI, vb, fb);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (act[j]) {
-                    fma4(O[j], fa[j], va[j]);
-                    fma4(O[j], fb[j], vb[j]);
-                }
-        }
-        if (c < n) {
-            float4 va[4];
-            float fa[4];
-            add_record(c, va, fa);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (act[j])
-                    fma4(O[j], fa[j], va[j]);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        for (int o = 1; o < TPI; o <<= 1) {
-            O[j].x += __shfl_xor_sync(kFull, O[j].x, o);
-            O[j].y += __shfl_xor_sync(kFull, O[j].y, o);
-            O[j].z += __shfl_xor_sync(kFull, O[j].z, o);
-            O[j].w += __shfl_xor_sync(kFull, O[j].w, o);
-        }
-        if (act[j] && sub == 0) {
-            const float2 ml = tot[rl_of[j]];
-            const float inv = ml.y == 0.f ? 1.f : 1.f / ml.y;
+        for (int j = 0; j < 4; ++j) {
+            O[j] = make_float4(0.f, 0.f, 0.f, 0.f);
             const int item = i0 + j * per_pass;
-            TO* dst = static_cast<TO*>(p.out) + (out_row0 + rl_of[j]) * D + 4 * (item & (D4 - 1));
-            dst[0] = from_float<TO>(O[j].x * inv);
-            dst[1] = from_float<TO>(O[j].y * inv);
-            dst[2] = from_float<TO>(O[j].z * inv);
-            dst[3] = from_float<TO>(O[j].w * inv);
+            act[j] = item < NI;
+            rl_of[j] = act[j] ? item >> LG4 : 0;
+        }
+        {
+            auto add_record = [&](int c, float4* v, float* f) {
+                const size_t rec = seg_record(p, sp, c, it.rsg, it.kh);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (!act[j])
+                        continue;
+                    const int item = i0 + j * per_pass;
+                    const size_t wrow = rec * p.row_stride + rl_of[j];
+                    v[j] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + wrow * D) + (item & (D4 - 1)));
+                    f[j] = fac_smem ? fac[c * R_cta + rl_of[j]]
+                                    : fast_exp2(__ldcg(&p.ws_ml[wrow]).x - tot[rl_of[j]].x);
+                }
+            };
+            int c = sub;
+            if (NI <= per_pass) {
+                // one item per thread: eight records in flight
+                const int rl = rl_of[0];
+                const int d4 = i0 & (D4 - 1);
+                for (; c + 7 * TPI < n; c += 8 * TPI) {
+                    float4 v[8];
+                    float f[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const size_t wrow = seg_record(p, sp, c + u * TPI, it.rsg, it.kh) * p.row_stride + rl;
+                        v[u] = act[0] ? __ldcg(reinterpret_cast<const float4*>(p.ws_o + wrow * D) + d4)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+                        f[u] = fac_smem ? fac[(c + u * TPI) * R_cta + rl]
+                                        : fast_exp2(__ldcg(&p.ws_ml[wrow]).x - tot[rl].x);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        fma4(O[0], f[u], v[u]);
+                }
+            }
+            // items of up to four rows per thread: two records in flight per item
+            for (; c + TPI < n; c += 2 * TPI) {
+                float4 va[4], vb[4];
+                float fa[4], fb[4];
+                add_record(c, va, fa);
+                add_record(c + TPI, vb, fb);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (act[j]) {
+                        fma4(O[j], fa[j], va[j]);
+                        fma4(O[j], fb[j], vb[j]);
+                    }
+            }
+            if (c < n) {
+                float4 va[4];
+                float fa[4];
+                add_record(c, va, fa);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (act[j])
+                        fma4(O[j], fa[j], va[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            for (int o = 1; o < TPI; o <<= 1) {
+                O[j].x += __shfl_xor_sync(kFull, O[j].x, o);
+                O[j].y += __shfl_xor_sync(kFull, O[j].y, o);
+                O[j].z += __shfl_xor_sync(kFull, O[j].z, o);
+                O[j].w += __shfl_xor_sync(kFull, O[j].w, o);
+            }
+            if (act[j] && sub == 0) {
+                const float2 ml = tot[rl_of[j]];
+                const float inv = ml.y == 0.f ? 1.f : 1.f / ml.y;
+                const int item = i0 + j * per_pass;
+                TO* dst = static_cast<TO*>(p.out) + (out_row0 + rl_of[j]) * D + 4 * (item & (D4 - 1));
+                dst[0] = from_float<TO>(O[j].x * inv);
+                dst[1] = from_float<TO>(O[j].y * inv);
+                dst[2] = from_float<TO>(O[j].z * inv);
+                dst[3] = from_float<TO>(O[j].w * inv);
+            }
         }
     }
 }
