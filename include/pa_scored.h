@@ -1,0 +1,87 @@
+/*
+ * pa_scored.h -- C ABI of decode attention with modified scores: capped by a
+ * tanh, biased by distance, limited to a sliding window beside a prefix; and
+ * of the weight that each cached key got.
+ *
+ * As pa_decode, with row r of sequence b at position i = seq_lens[b] + r and
+ * key j at position j:
+ *
+ *   t = scale * q[b][h][r] . key_j
+ *   t = softcap * tanh(t / softcap)                    if softcap > 0
+ *   t = t - slopes[h] * |i - j|                        if slopes
+ *   key j is visible to row r when j < seq_lens[b] + NQ and
+ *       j < prefix[b], or
+ *       (j <= i or not causal) and (|i - j| < window or window == 0)
+ *   out[b][h][r] = sum_j softmax_j(t) * value_j over the visible keys
+ *
+ * So prefix[b] is a prefix mask: those keys are visible to every row, also
+ * across the causal rule and the window (a bidirectional prompt, or the first
+ * tokens kept beside a sliding window).  Every row sees its own key.  Cache
+ * blocks that lie wholly between the prefix and the window of the first row
+ * are not read, and keys that no row of the sequence sees have no effect
+ * whatever they hold (a key that some row sees is used with weight 0 for the
+ * others: its value must be finite).
+ *
+ * Key weights (weights != NULL): with p the softmax weights,
+ *
+ *   out[b][j] = decay * in[b][j] + sum_{h, r} p[b][h][r][j]   for j < seq_lens[b]
+ *   out[b][j] =                    sum_{h, r} p[b][h][r][j]   for the new rows' keys
+ *
+ * in and out are float32 [B][max_blocks * BLOCK] and may be the same array; in
+ * may be NULL (zeros); keys at max_blocks * BLOCK and beyond are dropped and
+ * entries behind the last new row are left as they were.  The sums are formed
+ * in one order, whatever the split.
+ *
+ * Layouts, ownership, streams, opts and errors as pa_decode, with these
+ * differences: opts->partitions must be 0 or 1 and opts->merge_kernel 0
+ * (PA_ERR_UNSUPPORTED); opts->inputs_unchanged and opts->kernel are ignored.
+ * slopes [H] float32 and prefix [B] int32 are device pointers or NULL (a
+ * negative prefix counts as 0).  PA_ERR_BAD_DIMS: a softcap that is negative
+ * or not finite, a negative window, a decay that is not finite, scores whose
+ * scratch passes 2^40 bytes.  PA_ERR_NULL_POINTER: weights without out.
+ * PA_ERR_WORKSPACE / PA_ERR_ALIGNMENT: scratch below
+ * pa_scored_scratch_bytes() or not 256-byte aligned.  Two calls that run at
+ * the same time need a workspace and a scratch each.
+ */
+#ifndef PA_SCORED_H
+#define PA_SCORED_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "pa_decode.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef struct pa_score {
+    float softcap;         /* 0: no cap */
+    int window;            /* 0: no window */
+    const float *slopes;   /* device [H], or NULL */
+    const int32_t *prefix; /* device [B], or NULL */
+} pa_score;
+
+typedef struct pa_key_weights {
+    const float *in;
+    float *out;
+    float decay;
+    void *scratch; /* device scratch, 256-byte aligned, contents ignored */
+    size_t scratch_bytes;
+} pa_key_weights;
+
+int pa_decode_scored(const void *q, const void *k_cache, const void *v_cache,
+                     const int32_t *block_table, const int32_t *seq_lens, const void *k_new,
+                     const void *v_new, void *out, float scale, int H, int KV, int D, int BLOCK,
+                     int NQ, int causal, const pa_score *score, const pa_key_weights *weights,
+                     const pa_opts *opts, void *stream);
+
+/* Scratch bytes of the key weights: every score of the call in float32, and
+ * the rows' softmax denominators.  0 for invalid sizes. */
+size_t pa_scored_scratch_bytes(int batch, int max_blocks, int BLOCK, int H, int KV, int NQ);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* PA_SCORED_H */

@@ -112,6 +112,25 @@ class EvictOpts(ctypes.Structure):
     ]
 
 
+class Score(ctypes.Structure):
+    _fields_ = [
+        ("softcap", ctypes.c_float),
+        ("window", ctypes.c_int),
+        ("slopes", ctypes.c_void_p),
+        ("prefix", ctypes.c_void_p),
+    ]
+
+
+class KeyWeights(ctypes.Structure):
+    _fields_ = [
+        ("in_", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("decay", ctypes.c_float),
+        ("scratch", ctypes.c_void_p),
+        ("scratch_bytes", ctypes.c_size_t),
+    ]
+
+
 class SplitPlan(ctypes.Structure):
     _fields_ = [(name, ctypes.c_int) for name in (
         "grid", "active", "segments", "pieces", "split_segments", "records", "max_pieces")]
@@ -163,6 +182,12 @@ def load(path: Path = LIBRARY) -> ctypes.CDLL:
                                      ctypes.POINTER(VjpOpts), P]
     lib.pa_attention_vjp_workspace_bytes.restype = ctypes.c_size_t
     lib.pa_attention_vjp_workspace_bytes.argtypes = [I, I, I, I, I, I]
+    lib.pa_decode_scored.restype = I
+    lib.pa_decode_scored.argtypes = [P, P, P, P, P, P, P, P, ctypes.c_float, I, I, I, I, I, I,
+                                     ctypes.POINTER(Score), ctypes.POINTER(KeyWeights),
+                                     ctypes.POINTER(PaOpts), P]
+    lib.pa_scored_scratch_bytes.restype = ctypes.c_size_t
+    lib.pa_scored_scratch_bytes.argtypes = [I, I, I, I, I, I]
     lib.pa_rotary.restype = I
     lib.pa_rotary.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, ctypes.POINTER(RotaryOpts), P]
     lib.pa_cache_evict.restype = I
@@ -697,6 +722,95 @@ def attention_vjp(q, k, v, y, g, mask=None, *, scale: float, causal: bool = Fals
     """dq, dk, dv of attention (pa_attention_vjp): see ``VjpPlan``."""
     return VjpPlan(q, k, v, y, g, mask, scale=scale, causal=causal, out_dtype=out_dtype,
                    kernel=kernel, status=status, out=out).run(stream)
+
+
+# ------------------------------------------------------------------- modified scores
+def _score(softcap, slopes, window, prefix, B, H, device):
+    """The checked pa_score of a call (the tensors stay with the caller's plan)."""
+    if slopes is not None and (tuple(slopes.shape) != (H,) or slopes.dtype != torch.float32):
+        raise ValueError("slopes must be a float32 [H] tensor")
+    if prefix is not None and (tuple(prefix.shape) != (B,) or prefix.dtype != torch.int32):
+        raise ValueError("prefix must be an int32 [B] tensor")
+    for t in (slopes, prefix):
+        if t is not None and (not t.is_cuda or t.device != device or not t.is_contiguous()):
+            raise ValueError("slopes and prefix must be contiguous CUDA tensors on the inputs' device")
+    return Score(softcap=float(softcap), window=int(window),
+                 slopes=None if slopes is None else slopes.data_ptr(),
+                 prefix=None if prefix is None else prefix.data_ptr())
+
+
+class ScoredPlan(Plan):
+    """One prepared decode call with modified scores (pa_decode_scored): as
+    ``Plan``, with
+
+      softcap   scores t -> softcap * tanh(t / softcap) (0: none)
+      slopes    float32 [H]: slopes[h] * |row - key| subtracted (None: none)
+      window    keys within ``window`` positions of the row only (0: all)
+      prefix    int32 [B]: the first prefix[b] keys are visible to every row
+
+    and optionally the weight that every key got, summed over heads and rows:
+    ``key_weights`` and ``key_weights_out`` are float32 [B, max_blocks * BLOCK];
+    out = decay * key_weights + this step's weights.  Without
+    ``key_weights_out``, ``key_weights`` is updated in place; without
+    ``key_weights``, the weights start at zero.  ``run()`` returns ``out``, or
+    (out, key_weights_out)."""
+
+    def __init__(self, q, k_cache, v_cache, block_table, seq_lens, k_new, v_new, *, scale: float,
+                 causal: bool = False, softcap: float = 0.0, slopes=None, window: int = 0,
+                 prefix=None, key_weights=None, key_weights_out=None, decay: float = 1.0,
+                 partitions: int = 0, out=None, out_dtype=None, workspace=None, status=None,
+                 checked: bool = False):
+        super().__init__(q, k_cache, v_cache, block_table, seq_lens, k_new, v_new, scale=scale,
+                         causal=causal, partitions=partitions, out=out, out_dtype=out_dtype,
+                         workspace=workspace, status=status, checked=checked)
+        s = self.shape
+        self.score = _score(softcap, slopes, window, prefix, s["B"], s["H"], self.device)
+        self.key_weights = key_weights if key_weights_out is None else key_weights_out
+        self.weights = None
+        if self.key_weights is not None:
+            for t in (key_weights, self.key_weights):
+                if t is not None and (tuple(t.shape) != (s["B"], s["max_blocks"] * s["BLOCK"])
+                                      or t.dtype != torch.float32):
+                    raise ValueError("key weights must be float32 [B, max_blocks * BLOCK]")
+                if t is not None and (not t.is_cuda or t.device != self.device or not t.is_contiguous()):
+                    raise ValueError("key weights must be contiguous CUDA tensors on the inputs' device")
+            need = int(LIB.pa_scored_scratch_bytes(s["B"], s["max_blocks"], s["BLOCK"], s["H"], s["KV"],
+                                                   s["NQ"]))
+            self.scratch = torch.empty(max(need, 1), dtype=torch.uint8, device=self.device)
+            self.weights = KeyWeights(in_=None if key_weights is None else key_weights.data_ptr(),
+                                      out=self.key_weights.data_ptr(), decay=float(decay),
+                                      scratch=self.scratch.data_ptr(), scratch_bytes=need)
+        self._scored_keep = (slopes, prefix, key_weights)
+        self._args = self._args[:-1] + [ctypes.byref(self.score),
+                                        None if self.weights is None else ctypes.byref(self.weights),
+                                        ctypes.byref(self.opts)]
+
+    def _result(self, rc):
+        if rc != 0:
+            raise PagedAttentionError(rc)
+        return self.out if self.weights is None else (self.out, self.key_weights)
+
+    def run_bound(self):
+        return self._result(LIB.pa_decode_scored(*self._bound))
+
+    def run(self, stream=None):
+        if torch.cuda.current_device() == self.device.index:
+            return self._result(LIB.pa_decode_scored(*self._args, _stream_handle(stream)))
+        with torch.cuda.device(self.device):
+            return self._result(LIB.pa_decode_scored(*self._args, _stream_handle(stream)))
+
+
+def decode_scored(q, k_cache, v_cache, block_table, seq_lens, k_new, v_new, *, scale: float,
+                  causal: bool = False, softcap: float = 0.0, slopes=None, window: int = 0,
+                  prefix=None, key_weights=None, key_weights_out=None, decay: float = 1.0,
+                  partitions: int = 0, out=None, out_dtype=None, workspace=None, status=None,
+                  checked: bool = False, stream=None):
+    """Decode attention with modified scores (pa_decode_scored): see ``ScoredPlan``."""
+    return ScoredPlan(q, k_cache, v_cache, block_table, seq_lens, k_new, v_new, scale=scale,
+                      causal=causal, softcap=softcap, slopes=slopes, window=window, prefix=prefix,
+                      key_weights=key_weights, key_weights_out=key_weights_out, decay=decay,
+                      partitions=partitions, out=out, out_dtype=out_dtype, workspace=workspace,
+                      status=status, checked=checked).run(stream)
 
 
 # ------------------------------------------------------------------- rotary positions

@@ -93,6 +93,25 @@ struct SplitParams {
     int stages_v;      // tcgen05 kernel: V ring depth (stages: the K ring's; stage_bytes: one tile)
 };
 
+// Decode with modified scores (pa_decode_scored): what the partition kernels
+// need on top.  Lengths, key indices and limits inside the kernels are those of
+// the compressed sequence: the whole stages between the prefix and the window
+// (sequence b: `gap` tokens from token `pend` on, both multiples of TT, kept in
+// shared memory) are left out, and key c of the compressed sequence is key
+// c + (c >= pend ? gap : 0) of the real one.
+struct ScoredParams : SplitParams {
+    const float* slopes;    // [H] distance slopes, or NULL
+    const int32_t* prefix;  // [B] keys visible to every row, or NULL
+    float* scores;          // [B * KV][score_tokens][R] modified scores in base-2 units
+                            // (-inf: hidden; keys in a gap are not written), or NULL
+    float* lse;             // [B * KV * R] log2 of the softmax denominators, or NULL
+    float cap_in;           // scale / cap: the dot's factor inside the tanh
+    float cap_out;          // cap * log2(e), or 0 without a cap
+    int window;             // |row - key| < window; INT_MAX: none
+    int score_tokens;       // tokens per segment of `scores`
+    int gap_off, pend_off;  // shared memory: gap [B], pend [B]
+};
+
 struct CombineParams {
     const int2* sched;
     const float2* ws_ml;
@@ -108,6 +127,7 @@ struct CombineParams {
 };
 
 using SplitFn = void (*)(SplitParams, CUtensorMap, CUtensorMap);
+using ScoredFn = void (*)(ScoredParams, CUtensorMap, CUtensorMap);
 using SplitTcFn = void (*)(SplitParams, CUtensorMap, CUtensorMap, CUtensorMap);  // + the query map
 using CombineFn = void (*)(CombineParams);
 
@@ -126,6 +146,22 @@ __host__ __device__ constexpr int q_row_bytes(int D) { return D * 2 + 16; }
 SplitFn pick_split_f32(int D, int RG);
 SplitFn pick_split_f16(bool f32_out, int D, int MT);
 SplitFn pick_split_bf16(bool f32_out, int D, int MT);
+// The same kernels with modified scores (pa_scored_*.cu).
+ScoredFn pick_scored_f32(int D, int RG);
+ScoredFn pick_scored_f16(bool f32_out, int D, int MT);
+ScoredFn pick_scored_bf16(bool f32_out, int D, int MT);
+// The weight each key got (pa_scored.cu): after the partition kernel, on its stream.
+struct KeyWeightParams {
+    const float* scores;  // as in ScoredParams
+    const float* lse;
+    const float* in;      // [B][cap] earlier weights, or NULL
+    float* out;           // [B][cap]
+    const int32_t* seq_lens;
+    const int32_t* prefix;
+    float decay;
+    int B, KV, R, NQ, TT, cap, window, score_tokens;
+};
+int launch_key_weights(const KeyWeightParams& w, cudaStream_t st);
 // Tensor-core prefill (pa_prefill_tc.cu): whether a prefill of these sizes
 // takes it, and its launch (the new rows already stored in the cache).
 bool prefill_tc_supported(int dtype, int D, int H, int KV, int NQ);

@@ -149,7 +149,7 @@ __device__ void produce_tc(const SplitParams& p, const Sched& sc, const Smem& sm
     TileIter cur, ahead;
     cur.start(p, sc);
     ahead = cur;
-    fetch_entries(p, ahead, entries, lane);
+    fetch_entries<false>(p, sc, ahead, entries, lane);
     if (ahead.valid())
         ahead.next(p, sc);
     uint32_t gt = 0;  // tiles issued by this role
@@ -160,7 +160,7 @@ __device__ void produce_tc(const SplitParams& p, const Sched& sc, const Smem& sm
         if (gt == 0) {
             asm volatile("cp.async.wait_group 0;" ::: "memory");
         } else {
-            fetch_entries(p, ahead, entries + ((gt + kTableAhead) % kTableSlots) * kSlotInts, lane);
+            fetch_entries<false>(p, sc, ahead, entries + ((gt + kTableAhead) % kTableSlots) * kSlotInts, lane);
             if (ahead.valid())
                 ahead.next(p, sc);
             asm volatile("cp.async.wait_group %0;" ::"n"(kTableAhead) : "memory");
@@ -246,7 +246,7 @@ __device__ void produce_tc(const SplitParams& p, const Sched& sc, const Smem& sm
         }
         if (gt == 0)
             for (int k = 1; k <= kTableAhead; ++k) {
-                fetch_entries(p, ahead, entries + (k % kTableSlots) * kSlotInts, lane);
+                fetch_entries<false>(p, sc, ahead, entries + (k % kTableSlots) * kSlotInts, lane);
                 if (ahead.valid())
                     ahead.next(p, sc);
             }

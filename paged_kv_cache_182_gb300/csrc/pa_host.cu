@@ -25,6 +25,7 @@
 
 #include "pa_common.cuh"
 #include "pa_decode.h"
+#include "pa_scored.h"
 #include "pa_vjp.cuh"
 
 namespace pa {
@@ -527,11 +528,13 @@ static int launch_append(void* k_cache, void* v_cache, const void* k_new, const 
 // pa_decode, and pa_decode_positions when `positions` is not NULL: then the
 // new rows are first stored at their slots in the (writable) caches, after
 // every argument has been checked.  With launch == false: the checks alone.
+// With `score`: pa_decode_scored, its own arguments checked by the caller.
 static int decode_impl(const void* q, const void* k_cache, const void* v_cache,
                        const int32_t* block_table, const int32_t* seq_lens, const void* k_new,
                        const void* v_new, const int32_t* positions, void* out, float scale,
                        int H, int KV, int D, int BLOCK, int NQ, int causal, const pa_opts* opts,
-                       void* stream, bool launch = true)
+                       void* stream, bool launch = true, const pa_score* score = nullptr,
+                       const pa_key_weights* weights = nullptr)
 {
     if (!opts)
         return PA_ERR_NULL_POINTER;
@@ -607,8 +610,10 @@ static int decode_impl(const void* q, const void* k_cache, const void* v_cache,
     const int ROWS = rows_per_cta;  // tensor-core path: query-row buffer rows
     // shared memory: header | lens[B] | prefix[B+1] | consumer scratch | ring
     const int lens_off = kHeaderBytes;
+    // (modified scores: | gap[B] | pend[B] after the prefix)
     const int prefix_off = static_cast<int>(align_up(lens_off + 4 * B, 16));
-    const int merge_off = static_cast<int>(align_up(prefix_off + 4 * (B + 1), 128));
+    const int gap_off = static_cast<int>(align_up(prefix_off + 4 * (B + 1), 16));
+    const int merge_off = static_cast<int>(align_up(score ? gap_off + 8 * B : prefix_off + 4 * (B + 1), 128));
     // stage: tensor-core path K tile | V tile | K new rows | V new rows (tiles
     // 1024-aligned for the swizzle); CUDA-core path K tile | K new | V tile | V new
     int v_off, knew_off, vnew_off, stage_end;
@@ -642,7 +647,7 @@ static int decode_impl(const void* q, const void* k_cache, const void* v_cache,
     // stay in global memory), when each ring gets two tiles at least.
     int tc_off = 0, stages_v = 0;
     bool tc32 = false;
-    if (mma && MT == 2 && D == 128 && opts->kernel == 0) {
+    if (mma && MT == 2 && D == 128 && opts->kernel == 0 && !score) {
         const int t_off = static_cast<int>(align_up(merge_off, 1024));
         const int t_stage = static_cast<int>(align_up(t_off + kTcRegionBytes, 1024));
         const int tiles = (smem_optin - slack - t_stage) / kTcTileBytes;
@@ -673,7 +678,10 @@ static int decode_impl(const void* q, const void* k_cache, const void* v_cache,
         return rc;
 
     const bool f32_out = out_dtype == PA_F32 && dtype != PA_F32;
-    const void* split = tc32 ? reinterpret_cast<const void*>(pick_split_tc(dtype, f32_out))
+    const void* split = score ? (dtype == PA_F32   ? reinterpret_cast<const void*>(pick_scored_f32(D, RG))
+                                 : dtype == PA_F16 ? reinterpret_cast<const void*>(pick_scored_f16(f32_out, D, MT))
+                                                   : reinterpret_cast<const void*>(pick_scored_bf16(f32_out, D, MT)))
+                        : tc32 ? reinterpret_cast<const void*>(pick_split_tc(dtype, f32_out))
                              : reinterpret_cast<const void*>(pick_split(dtype, f32_out, D, mma ? MT : RG));
     int occ = 1, sms = 1;
     const int threads = tc32 ? kUmmaThreads : kThreads;
@@ -681,7 +689,8 @@ static int decode_impl(const void* q, const void* k_cache, const void* v_cache,
     if (rc != PA_OK)
         return rc;
 
-    SplitParams p{};
+    ScoredParams sp{};
+    SplitParams& p = sp;
     p.q = q;
     p.k_new = k_new;
     p.v_new = v_new;
@@ -750,7 +759,23 @@ static int decode_impl(const void* q, const void* k_cache, const void* v_cache,
     p.wait_ns = opts->wait_limit_ns ? opts->wait_limit_ns : kWaitLimitNs;
     p.withhold = opts->debug_withhold_stage > 0 ? opts->debug_withhold_stage : 0;
     // the slot-patched decode runs right after its own append kernel
-    p.early = opts->inputs_unchanged && !positions ? 1 : 0;
+    // (with modified scores the consumers write scores before a piece ends)
+    p.early = opts->inputs_unchanged && !positions && !score ? 1 : 0;
+    if (score) {
+        sp.slopes = score->slopes;
+        sp.prefix = score->prefix;
+        sp.cap_in = score->softcap > 0.f ? scale / score->softcap : 0.f;
+        sp.cap_out = score->softcap > 0.f ? score->softcap * kLog2e : 0.f;
+        sp.window = score->window > 0 ? score->window : INT_MAX;
+        sp.gap_off = gap_off;
+        sp.pend_off = gap_off + 4 * B;
+        sp.score_tokens = opts->max_blocks * BLOCK + NQ;
+        if (weights) {
+            const size_t lse_bytes = align_up(static_cast<size_t>(B) * KV * R * sizeof(float), 256);
+            sp.lse = static_cast<float*>(weights->scratch);
+            sp.scores = reinterpret_cast<float*>(static_cast<unsigned char*>(weights->scratch) + lse_bytes);
+        }
+    }
 
     if (!launch)
         return PA_OK;
@@ -778,7 +803,7 @@ static int decode_impl(const void* q, const void* k_cache, const void* v_cache,
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    void* args[4] = {&p, &kmap, &vmap, &qmap};
+    void* args[4] = {&sp, &kmap, &vmap, &qmap};  // the plain kernels take its SplitParams
     if (cudaLaunchKernelExC(&cfg, split, args) != cudaSuccess)
         return PA_ERR_CUDA;
     g_launches.fetch_add(1);
@@ -820,7 +845,68 @@ static int decode_impl(const void* q, const void* k_cache, const void* v_cache,
             return PA_ERR_CUDA;
         g_launches.fetch_add(1);
     }
+    if (score && weights) {
+        KeyWeightParams w{};
+        w.scores = sp.scores;
+        w.lse = sp.lse;
+        w.in = weights->in;
+        w.out = weights->out;
+        w.seq_lens = seq_lens;
+        w.prefix = sp.prefix;
+        w.decay = weights->decay;
+        w.B = B;
+        w.KV = KV;
+        w.R = R;
+        w.NQ = NQ;
+        w.TT = TT;
+        w.cap = opts->max_blocks * BLOCK;
+        w.window = sp.window;
+        w.score_tokens = sp.score_tokens;
+        return launch_key_weights(w, st);
+    }
     return PA_OK;
+}
+
+// lse [B * KV * R] (256-byte padded) | scores [B * KV][max_blocks * BLOCK + NQ][R]
+size_t pa_scored_scratch_bytes(int batch, int max_blocks, int BLOCK, int H, int KV, int NQ)
+{
+    if (batch < 1 || batch > kMaxBatch || max_blocks < 1 || BLOCK < 1 || H < 1 || KV < 1 || H % KV != 0 || NQ < 1 ||
+        NQ > PA_MAX_NQ || static_cast<long long>(max_blocks) * BLOCK >= (1ll << 30))
+        return 0;
+    const size_t rows = static_cast<size_t>(batch) * H * NQ;
+    const size_t tokens = static_cast<size_t>(max_blocks) * BLOCK + NQ;
+    if (static_cast<double>(rows) * static_cast<double>(tokens) >= 1e18)
+        return 0;
+    return align_up(rows * sizeof(float), 256) + rows * tokens * sizeof(float);
+}
+
+int pa_decode_scored(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                     const int32_t* seq_lens, const void* k_new, const void* v_new, void* out, float scale,
+                     int H, int KV, int D, int BLOCK, int NQ, int causal, const pa_score* score,
+                     const pa_key_weights* weights, const pa_opts* opts, void* stream)
+{
+    if (!score || !opts)
+        return PA_ERR_NULL_POINTER;
+    if (!(score->softcap >= 0.f) || !std::isfinite(score->softcap) || score->window < 0 ||
+        (weights && !std::isfinite(weights->decay)))
+        return PA_ERR_BAD_DIMS;
+    if ((opts->partitions != 0 && opts->partitions != 1) || opts->merge_kernel)
+        return PA_ERR_UNSUPPORTED;
+    if (!aligned(score->slopes, 4) || !aligned(score->prefix, 4))
+        return PA_ERR_ALIGNMENT;
+    if (weights && opts->batch > 0) {
+        const size_t need = pa_scored_scratch_bytes(opts->batch, opts->max_blocks, BLOCK, H, KV, NQ);
+        if (need == 0 || need >= (static_cast<size_t>(1) << 40))
+            return opts->batch > kMaxBatch || NQ < 1 || NQ > PA_MAX_NQ ? PA_ERR_UNSUPPORTED : PA_ERR_BAD_DIMS;
+        if (!weights->out)
+            return PA_ERR_NULL_POINTER;
+        if (!weights->scratch || weights->scratch_bytes < need)
+            return PA_ERR_WORKSPACE;
+        if (!aligned(weights->scratch, 256) || !aligned(weights->in, 4) || !aligned(weights->out, 4))
+            return PA_ERR_ALIGNMENT;
+    }
+    return decode_impl(q, k_cache, v_cache, block_table, seq_lens, k_new, v_new, nullptr, out, scale, H, KV, D,
+                       BLOCK, NQ, causal, opts, stream, true, score, weights);
 }
 
 int pa_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,

@@ -148,6 +148,8 @@ struct Sched {
     const int* lens;    // [B] clamped cached lengths
     const int* prefix;  // [B + 1] automatic: units before sequence b (all its segments);
                         //         fixed: ranges before sequence b (one segment's worth)
+    const int* gap;     // modified scores: [B] tokens left out after token pend[b]
+    const int* pend;
     int total;          // automatic: W units; fixed: number of items
     long long cost;     // automatic: C = W + vunits * (number of segments)
     int pos0, stop0;    // automatic: this CTA's units [pos0, stop0)
@@ -200,7 +202,14 @@ __device__ __forceinline__ SegSpan seg_span(int x0, int nu, int g, int V, int C,
 // segments of a sequence; fixed partitions: its key ranges), up to four
 // 32-sequence chunks of loads in flight at once.  CTA 0 also records every
 // sequence's (prefix, count) for the merge kernel.  Returns the prefix total.
-__device__ __forceinline__ int scan_lengths(const SplitParams& p, int* lens, int* prefix, int lane)
+// With modified scores (kMod) the lengths are compressed: the stages that lie
+// wholly between the prefix and the first row's window are taken out.
+template <bool kMod>
+using ParamsOf = std::conditional_t<kMod, ScoredParams, SplitParams>;
+
+template <bool kMod>
+__device__ __forceinline__ int scan_lengths(const ParamsOf<kMod>& p, int* lens, int* prefix, int* gap, int* pend,
+                                            int lane)
 {
     const int U = p.NRS * p.KV;
     const bool stream = p.partitions == 0;
@@ -225,6 +234,14 @@ __device__ __forceinline__ int scan_lengths(const SplitParams& p, int* lens, int
                     if (blockIdx.x == 0 && p.status)
                         atomicOr(p.status, PA_STATUS_BAD_LENGTH);
                     v = v < 0 ? 0 : cap;
+                }
+                if constexpr (kMod) {
+                    const int pl = p.prefix ? min(max(__ldg(p.prefix + b), 0), v + p.NQ) : 0;
+                    const int P = (pl + p.TT - 1) & ~(p.TT - 1);
+                    const int cut = max(0, (max(v - p.window + 1, 0) & ~(p.TT - 1)) - P);
+                    gap[b] = cut;
+                    pend[b] = P;
+                    v -= cut;
                 }
                 lens[b] = v;
                 const int total = v + p.NQ;
@@ -488,12 +505,125 @@ __device__ __forceinline__ void flag_timeout(const SplitParams& p, volatile int*
         atomicOr(p.status, PA_STATUS_TIMEOUT);
 }
 
+// ------------------------------------------------------- modified scores
+// Offset of a tile's keys in the real sequence (tiles never straddle the gap).
+template <bool kMod>
+struct TileOff {
+    __device__ __forceinline__ TileOff(const Sched&, const Item&, int) {}
+};
+template <>
+struct TileOff<true> {
+    int off;   // real key - compressed key
+    int rest;  // gap tokens behind this tile (they lie between its keys and the rows)
+    __device__ __forceinline__ TileOff(const Sched& sc, const Item& it, int t0)
+    {
+        const int gap = sc.gap[it.b];
+        off = t0 >= sc.pend[it.b] ? gap : 0;
+        rest = gap - off;
+    }
+};
+
+// The factor of the raw dot products: scale * log2(e), or scale / cap.
+template <bool kMod>
+__device__ __forceinline__ float score_qscale(const ParamsOf<kMod>& p)
+{
+    if constexpr (kMod)
+        return p.cap_out != 0.f ? p.cap_in : p.qscale;
+    else
+        return p.qscale;
+}
+
+// One query row of a piece: its limits among the compressed keys, its slope and
+// where its scores go.
+template <bool kMod>
+struct ScoreRow {
+    __device__ __forceinline__ void begin(const SplitParams&, const Sched&, const Item&, int, int&) {}
+    __device__ __forceinline__ void none() {}
+};
+template <>
+struct ScoreRow<true> {
+    int wlo;      // first key of the window
+    int pl;       // keys below are visible whatever the window
+    int row;      // the row's own key
+    float slope;  // distance slope * log2(e)
+    size_t at;    // scores: element of (segment, token 0, row)
+
+    // `limit` is the causal limit on entry; a prefix that reaches into the new
+    // rows raises it, a window without the causal rule lowers it.
+    __device__ __forceinline__ void begin(const ScoredParams& p, const Sched& sc, const Item& it, int rho, int& limit)
+    {
+        const int total = it.past + p.NQ;
+        const int rn = rho % p.NQ;
+        row = it.past + rn;
+        wlo = row - p.window + 1;  // window INT_MAX: far below 0
+        if (!p.causal && p.window < p.NQ)
+            limit = min(limit, row + p.window);
+        // a prefix beyond pend's stage would have no gap before it, so real
+        // and compressed keys agree below pl
+        pl = p.prefix ? min(max(__ldg(p.prefix + it.b), 0), total) : 0;
+        if (sc.gap[it.b] > 0)
+            pl = min(pl, sc.pend[it.b]);
+        limit = max(limit, pl);
+        slope = p.slopes ? __ldg(p.slopes + it.kh * (p.H / p.KV) + rho / p.NQ) * kLog2e : 0.f;
+        at = (static_cast<size_t>(it.b) * p.KV + it.kh) * p.score_tokens * p.R + rho;
+    }
+    __device__ __forceinline__ void none()
+    {
+        wlo = INT_MAX;
+        pl = 0;
+        row = 0;
+        slope = 0.f;
+        at = ~static_cast<size_t>(0);
+    }
+    __device__ __forceinline__ bool sees(int c) const { return c >= wlo || c < pl; }
+    // The modified score, in base-2 units, of a dot product already times
+    // score_qscale.  tanhf, not the hardware's approximation: its relative
+    // error of 2^-11 would move a score of 10 under a cap of 50 by 0.005, and
+    // every weight with it; the scores are few beside the K and V bytes.
+    __device__ __forceinline__ float score(const ScoredParams& p, float x, int c, const TileOff<true>& to) const
+    {
+        if (p.cap_out != 0.f)
+            x = p.cap_out * tanhf(x);
+        return fmaf(-slope, static_cast<float>(abs(row + to.rest - c)), x);
+    }
+    __device__ __forceinline__ void store(const ScoredParams& p, const TileOff<true>& to, int c, float s) const
+    {
+        if (p.scores && at != ~static_cast<size_t>(0))
+            p.scores[at + static_cast<size_t>(c + to.off) * p.R] = s;
+    }
+};
+
+// What all rows of a warp together see (padding rows do not count): every row
+// sees [0, pl) and [wlo, its limit); no row sees a key outside [0, pl) and
+// [wlo_any, lim_any) -- pl is the same for all rows.  The value rows of keys
+// that no row sees are replaced by zeros: their weight is 0, but 0 times an
+// infinity or NaN is not.
+template <bool kMod>
+struct ScoreSpan {
+    __device__ __forceinline__ ScoreSpan(const ScoreRow<kMod>*, const int*) {}
+    __device__ __forceinline__ bool whole(int, int) const { return true; }
+    __device__ __forceinline__ bool any(int) const { return true; }
+};
+template <>
+struct ScoreSpan<true> {
+    int wlo, wlo_any, lim_any, pl;
+    __device__ __forceinline__ ScoreSpan(const ScoreRow<true>* r, const int* lim)
+    {
+        wlo = __reduce_max_sync(kFull, max(lim[0] > 0 ? r[0].wlo : INT_MIN, lim[1] > 0 ? r[1].wlo : INT_MIN));
+        wlo_any = __reduce_min_sync(kFull, min(r[0].wlo, r[1].wlo));
+        lim_any = __reduce_max_sync(kFull, max(lim[0], lim[1]));
+        pl = __reduce_max_sync(kFull, max(r[0].pl, r[1].pl));
+    }
+    __device__ __forceinline__ bool whole(int c0, int c1) const { return c0 >= wlo || c1 <= pl; }
+    __device__ __forceinline__ bool any(int c) const { return c < pl || (c >= wlo_any && c < lim_any); }
+};
+
 // ------------------------------------------------------- float32 CUDA-core math
 // One warp: RG query rows, a subset of the tokens of each tile.  A token row
 // of D elements is split over LPT lanes (16 bytes each); TPW tokens per warp
 // step.  State per lane: running max m and sum l per row (replicated over the
 // lanes of a token) and the accumulator slice o[row][VEC].
-template <typename T, int D, int RG>
+template <typename T, int D, int RG, bool kMod = false>
 struct SimtMath {
     using E = Elem<T>;
     static constexpr int VEC = E::kVec;
@@ -507,8 +637,9 @@ struct SimtMath {
     float m[RG], l[RG];
     int limit[RG];
     int lg, li, ts, TS;
+    ScoreRow<kMod> mod[RG];
 
-    __device__ void begin(const SplitParams& p, const Item& it, int row0, int R_cta, int lane,
+    __device__ void begin(const ParamsOf<kMod>& p, const Sched& sc, const Item& it, int row0, int R_cta, int lane,
                           int ts_, int TS_)
     {
         lg = lane / LPT;
@@ -517,7 +648,9 @@ struct SimtMath {
         TS = TS_;
         const T* qbase =
             static_cast<const T*>(p.q) + (static_cast<size_t>(it.b) * p.KV + it.kh) * p.R * D;
-        const float2 sc2 = make_float2(p.qscale, p.qscale);
+        // the scale goes into q; under a cap, the factor inside the tanh does
+        const float qs = score_qscale<kMod>(p);
+        const float2 sc2 = make_float2(qs, qs);
 #pragma unroll
         for (int r = 0; r < RG; ++r) {
             const int rl = row0 + r;
@@ -528,11 +661,13 @@ struct SimtMath {
                 for (int v = 0; v < V2; ++v)
                     q[r][v] = __fmul2_rn(q[r][v], sc2);
                 limit[r] = it.past + (p.causal ? (rho % p.NQ) + 1 : p.NQ);
+                mod[r].begin(p, sc, it, rho, limit[r]);
             } else {
 #pragma unroll
                 for (int v = 0; v < V2; ++v)
                     q[r][v] = make_float2(0.f, 0.f);
                 limit[r] = 0;
+                mod[r].none();
             }
             m[r] = -FLT_MAX;
             l[r] = 0.f;
@@ -544,8 +679,8 @@ struct SimtMath {
 
     // Tile of n_tile tokens starting at absolute key t0: rows < past come from
     // the cache tile (ks / vs), rows >= past from the new rows (kn / vn).
-    __device__ void tile(const T* ks, const T* kn, const T* vs, const T* vn, int t0, int n_tile,
-                         int past)
+    __device__ void tile(const ParamsOf<kMod>& p, const T* ks, const T* kn, const T* vs, const T* vn, int t0,
+                         int n_tile, int past, const TileOff<kMod>& to)
     {
         const int step = TS * TPW;
         for (int base = 0; base < n_tile; base += kSubBatch * step) {
@@ -574,7 +709,14 @@ struct SimtMath {
 #pragma unroll
                     for (int off = LPT / 2; off > 0; off >>= 1)
                         acc += __shfl_xor_sync(kFull, acc, off);
-                    sc[i][r] = (live && t_abs < limit[r]) ? acc : -INFINITY;
+                    if constexpr (kMod) {
+                        const bool valid = live && t_abs < limit[r] && mod[r].sees(t_abs);
+                        sc[i][r] = valid ? mod[r].score(p, acc, t_abs, to) : -INFINITY;
+                        if (live && li == 0)
+                            mod[r].store(p, to, t_abs, sc[i][r]);
+                    } else {
+                        sc[i][r] = (live && t_abs < limit[r]) ? acc : -INFINITY;
+                    }
                 }
             }
 #pragma unroll
@@ -598,6 +740,15 @@ struct SimtMath {
                 if (t_rel >= n_tile)
                     continue;
                 const int t_abs = t0 + t_rel;
+                if constexpr (kMod) {
+                    // a key that no row of the warp sees: 0 times its value, which may not be finite
+                    bool any = false;
+#pragma unroll
+                    for (int r = 0; r < RG; ++r)
+                        any |= t_abs < limit[r] && mod[r].sees(t_abs);
+                    if (!any)
+                        continue;
+                }
                 const T* row = t_abs < past ? vs + t_rel * D : vn + (t_abs - past) * D;
                 float2 v2[V2];
                 E::load2(row + li * VEC, v2);
@@ -753,16 +904,26 @@ __device__ __forceinline__ void kernel_entry(const SplitParams& p, const CUtenso
 }
 
 // All threads, after kernel_entry: clamped lengths, the schedule.
-__device__ __forceinline__ Sched setup_cta(const SplitParams& p, const Smem& sm)
+template <bool kMod = false>
+__device__ __forceinline__ Sched setup_cta(const ParamsOf<kMod>& p, const Smem& sm)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Sched sc;
     sc.lens = sm.lens;
     sc.prefix = sm.prefix;
+    if constexpr (kMod) {
+        sc.gap = sm.lens + (p.gap_off - p.lens_off) / 4;
+        sc.pend = sm.lens + (p.pend_off - p.lens_off) / 4;
+    }
     // Warp 0 alone: lengths, schedule and (automatic mode) this CTA's range,
     // with warp barriers in between and one CTA barrier at the end.
     if (warp == 0) {
-        const int run = scan_lengths(p, sm.lens, sm.prefix, lane);
+        int *gap = nullptr, *pend = nullptr;
+        if constexpr (kMod) {
+            gap = sm.lens + (p.gap_off - p.lens_off) / 4;
+            pend = sm.lens + (p.pend_off - p.lens_off) / 4;
+        }
+        const int run = scan_lengths<kMod>(p, sm.lens, sm.prefix, gap, pend, lane);
         __syncwarp();
         sc.total = p.partitions == 0 ? run : run * p.NRS * p.KV;
         sc.cost = sc.total + static_cast<long long>(p.vunits) * p.B * p.NRS * p.KV;
@@ -844,7 +1005,8 @@ constexpr int kSlotInts = 16;    // entries per slot (boxes per tile at most)
 
 // Starts a non-blocking copy of the table entries of the tile at `t` into
 // entry slot `slot` (lane i copies entry i), as one cp.async group.
-__device__ __forceinline__ void fetch_entries(const SplitParams& p, const TileIter& t, int* slot,
+template <bool kMod>
+__device__ __forceinline__ void fetch_entries(const SplitParams& p, const Sched& sc, const TileIter& t, int* slot,
                                               int lane)
 {
     if (t.valid()) {
@@ -853,8 +1015,9 @@ __device__ __forceinline__ void fetch_entries(const SplitParams& p, const TileIt
         const int cache_end = min(min(t0 + p.TT, it.end), it.past);
         const int nb = cache_end > t0 ? (cache_end - t0 + p.box_rows - 1) >> p.lg_box : 0;
         if (lane < nb) {
+            const int off = kMod && t0 >= sc.pend[it.b] ? sc.gap[it.b] : 0;
             const int32_t* src = p.table + static_cast<size_t>(it.b) * p.maxb +
-                                 ((t0 + (lane << p.lg_box)) >> p.lg_block);
+                                 ((t0 + off + (lane << p.lg_box)) >> p.lg_block);
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(slot + lane)),
                          "l"(src)
                          : "memory");
@@ -871,7 +1034,7 @@ __device__ __forceinline__ void fetch_entries(const SplitParams& p, const TileIt
 // role counts its bytes on the stage's full barrier (two arrivals).  Table
 // entries are fetched kTableAhead tiles ahead with cp.async, so no dependent
 // global load sits on the issue path.
-template <typename T, int D, bool kSwizzled>
+template <typename T, int D, bool kSwizzled, bool kMod = false>
 __device__ void produce(const SplitParams& p, const Sched& sc, const Smem& sm, const CUtensorMap* kmap,
                         const CUtensorMap* vmap, int role, int lane)
 {
@@ -886,7 +1049,7 @@ __device__ void produce(const SplitParams& p, const Sched& sc, const Smem& sm, c
     ahead = cur;
     // tile 0's entries first: its boxes go out before the rest of the
     // look-ahead window is fetched (tiles 1 .. kTableAhead, after its issue)
-    fetch_entries(p, ahead, entries, lane);
+    fetch_entries<kMod>(p, sc, ahead, entries, lane);
     if (ahead.valid())
         ahead.next(p, sc);
     const int HB = p.box_rows;
@@ -899,7 +1062,7 @@ __device__ void produce(const SplitParams& p, const Sched& sc, const Smem& sm, c
             asm volatile("cp.async.wait_group 0;" ::: "memory");
         } else {
             // one group per tile: tile gt's group is the oldest of kTableAhead + 1
-            fetch_entries(p, ahead, entries + ((gt + kTableAhead) % kTableSlots) * kSlotInts, lane);
+            fetch_entries<kMod>(p, sc, ahead, entries + ((gt + kTableAhead) % kTableSlots) * kSlotInts, lane);
             if (ahead.valid())
                 ahead.next(p, sc);
             asm volatile("cp.async.wait_group %0;" ::"n"(kTableAhead) : "memory");
@@ -989,7 +1152,7 @@ __device__ void produce(const SplitParams& p, const Sched& sc, const Smem& sm, c
         }
         if (gt == 0)
             for (int k = 1; k <= kTableAhead; ++k) {
-                fetch_entries(p, ahead, entries + (k % kTableSlots) * kSlotInts, lane);
+                fetch_entries<kMod>(p, sc, ahead, entries + (k % kTableSlots) * kSlotInts, lane);
                 if (ahead.valid())
                     ahead.next(p, sc);
             }
@@ -1009,6 +1172,16 @@ __device__ void produce(const SplitParams& p, const Sched& sc, const Smem& sm, c
 }
 
 // ---------------------------------------------------------- in-kernel merge
+// log2 of a row's softmax denominator, for the keys' weights (modified scores).
+template <bool kMod>
+__device__ __forceinline__ void store_lse(const ParamsOf<kMod>& p, size_t row, bool first, float M, float L)
+{
+    if constexpr (kMod) {
+        if (first && p.lse)
+            p.lse[row] = L > 0.f ? M + log2f(L) : INFINITY;
+    }
+}
+
 // Counter increment with acquire-release semantics at GPU scope: after a CTA
 // barrier, the release publishes every record store of the CTA's threads
 // (cumulativity through the barrier); the acquire makes the records of the
@@ -1028,8 +1201,8 @@ __device__ __forceinline__ int count_piece(int* counter)
 // `tot` (rows_per_cta pairs) and `fac` (fac_cap floats) of shared scratch,
 // then the accumulators).  Records written by other CTAs are read through L2
 // (ld.global.cg).
-template <int D, typename TO>
-__device__ void merge_segment(const SplitParams& p, const Sched& sc, const int4 seg, float2* tot,
+template <int D, typename TO, bool kMod>
+__device__ void merge_segment(const ParamsOf<kMod>& p, const Sched& sc, const int4 seg, float2* tot,
                               float* fac, int fac_cap, int t0, int kT, int bar_id)
 {
     const int tid = threadIdx.x - t0, warp = tid >> 5, lane = tid & 31;
@@ -1095,6 +1268,7 @@ __device__ void merge_segment(const SplitParams& p, const Sched& sc, const int4 
                 M = Mb;
             }
             const float inv = L == 0.f ? 1.f : 1.f / L;
+            store_lse<kMod>(p, out_row0 + rl, d4 == 0, M, L);
             TO* dst = static_cast<TO*>(p.out) + (out_row0 + rl) * D + 4 * d4;
             dst[0] = from_float<TO>(O.x * inv);
             dst[1] = from_float<TO>(O.y * inv);
@@ -1252,6 +1426,7 @@ __device__ void merge_segment(const SplitParams& p, const Sched& sc, const int4 
                 const float2 ml = tot[rl_of[j]];
                 const float inv = ml.y == 0.f ? 1.f : 1.f / ml.y;
                 const int item = i0 + j * per_pass;
+                store_lse<kMod>(p, out_row0 + rl_of[j], (item & (D4 - 1)) == 0, ml.x, ml.y);
                 TO* dst = static_cast<TO*>(p.out) + (out_row0 + rl_of[j]) * D + 4 * (item & (D4 - 1));
                 dst[0] = from_float<TO>(O[j].x * inv);
                 dst[1] = from_float<TO>(O[j].y * inv);
@@ -1271,8 +1446,8 @@ constexpr int kSplitList = 32;  // list capacity (the automatic schedule needs t
 // atomics in flight together); the CTA that finishes the last piece of a
 // segment merges the segment's records and resets its counter for the next
 // call.  Counting at the end keeps merges out of the CTA's stream.
-template <int D, typename TO>
-__device__ void flush_split_pieces(const SplitParams& p, const Sched& sc, int4* list, int n, float2* tot,
+template <int D, typename TO, bool kMod = false>
+__device__ void flush_split_pieces(const ParamsOf<kMod>& p, const Sched& sc, int4* list, int n, float2* tot,
                                    int tot_cap, float* fac, int fac_cap)
 {
     const int tid = threadIdx.x;
@@ -1306,7 +1481,7 @@ __device__ void flush_split_pieces(const SplitParams& p, const Sched& sc, int4* 
             ++j;
         const bool pair = j < n && fits_half(list[i]) && fits_half(list[j]);
         const bool upper = pair && tid >= kHalf;
-        merge_segment<D, TO>(p, sc, list[upper ? j : i], tot + (upper ? p.rows_per_cta : 0),
+        merge_segment<D, TO, kMod>(p, sc, list[upper ? j : i], tot + (upper ? p.rows_per_cta : 0),
                              fac + (upper ? fac_cap / 2 : 0), pair ? fac_cap / 2 : fac_cap,
                              upper ? kHalf : 0, pair ? kHalf : 2 * kHalf, pair ? (upper ? 3 : 2) : 1);
         i = pair ? j + 1 : i + 1;
@@ -1317,9 +1492,9 @@ __device__ void flush_split_pieces(const SplitParams& p, const Sched& sc, int4* 
 // ------------------------------------------- float32 CUDA-core partition kernel
 // T: element type of q/K/V; D: head size; RG: query rows per consumer warp;
 // TO: output element type.  One CTA per SM (persistent).
-template <typename T, int D, int RG, typename TO>
+template <typename T, int D, int RG, typename TO, bool kMod = false>
 __global__ void __launch_bounds__(kThreads, 1)
-    pa_split_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ CUtensorMap kmap,
+    pa_split_kernel(const __grid_constant__ ParamsOf<kMod> p, const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap vmap)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -1336,10 +1511,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // inputs may be produced by the previous kernel on the stream
     kernel_entry(p, kmap, vmap, sm);
-    const Sched sc = setup_cta(p, sm);
+    const Sched sc = setup_cta<kMod>(p, sm);
 
     if (warp >= kConsumerWarps) {
-        produce<T, D, false>(p, sc, sm, &kmap, &vmap, warp - kConsumerWarps, lane);
+        produce<T, D, false, kMod>(p, sc, sm, &kmap, &vmap, warp - kConsumerWarps, lane);
         return;
     }
     // consumers: with p.early (the inputs read before the previous kernel
@@ -1347,7 +1522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // before any write of the output or the workspace
     bool dep_ok = !p.early;
 
-    using Math = SimtMath<T, D, RG>;
+    using Math = SimtMath<T, D, RG, kMod>;
     uint32_t gt = 0;
     int nsplit = 0;  // split pieces listed since the last flush (uniform)
     const int tid = threadIdx.x;  // 0 .. kConsumerWarps*32-1
@@ -1363,7 +1538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ts = warp / nrg;
 
         Math mt;
-        mt.begin(p, it, rg * RG, R_cta, lane, ts, TS);
+        mt.begin(p, sc, it, rg * RG, R_cta, lane, ts, TS);
         bool alive = true;
         for (int j = 0; j < ntiles; ++j, ++gt) {
             const int s = gt % S;
@@ -1378,10 +1553,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             const unsigned char* st = sm.ring + static_cast<size_t>(s) * p.stage_bytes;
             const int t0 = it.start + j * TT;
-            mt.tile(reinterpret_cast<const T*>(st), reinterpret_cast<const T*>(st + p.knew_off),
+            mt.tile(p, reinterpret_cast<const T*>(st), reinterpret_cast<const T*>(st + p.knew_off),
                     reinterpret_cast<const T*>(st + p.v_off),
                     reinterpret_cast<const T*>(st + p.vnew_off), t0, min(TT, it.end - t0),
-                    it.past);
+                    it.past, TileOff<kMod>(sc, it, t0));
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sm.empty[s]);
@@ -1415,6 +1590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (it.whole) {
                 const float val = L == 0.f ? O : O / L;
                 static_cast<TO*>(p.out)[(out_row0 + rl) * D + d] = from_float<TO>(val);
+                store_lse<kMod>(p, out_row0 + rl, d == 0, M, L);
             } else {
                 const size_t wrow = static_cast<size_t>(it.rec) * p.row_stride + rl;
                 p.ws_o[wrow * D + d] = O;
@@ -1431,7 +1607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // uniform over the consumer warps (a late abort flag must not split them)
     if (nsplit > 0 && !consumer_bar_or(*sm.abort_flag != 0))
-        flush_split_pieces<D, TO>(p, sc, sm.split_list, nsplit, merge_tot, p.rows_per_cta, mb_o,
+        flush_split_pieces<D, TO, kMod>(p, sc, sm.split_list, nsplit, merge_tot, p.rows_per_cta, mb_o,
                                   kConsumerWarps * RG * D);
 }
 
@@ -1522,8 +1698,8 @@ __device__ __forceinline__ int obuf_lg(int D, int RU, int cap = kObufFloats)
 // every row: M = max m_t, L = sum l_t 2^(m_t - M), acc = sum o_t 2^(m_t - M);
 // writes out = acc / L for a whole segment, else the partial record
 // (acc, (M, L)).  Warp w holds rows of row group w % MT.  All consumer threads.
-template <int D, int MT, typename TO>
-__device__ __forceinline__ void sum_warps(const SplitParams& p, const Item& it, int R_cta, int RU, int lg,
+template <int D, int MT, typename TO, bool kMod = false>
+__device__ __forceinline__ void sum_warps(const ParamsOf<kMod>& p, const Item& it, int R_cta, int RU, int lg,
                                           int r, const float2* ml_buf, const float* obuf)
 {
     constexpr int TS = kConsumerWarps / MT;
@@ -1535,6 +1711,7 @@ __device__ __forceinline__ void sum_warps(const SplitParams& p, const Item& it, 
         if (it.whole) {
             const float val = L == 0.f ? acc : acc / L;
             static_cast<TO*>(p.out)[(out_row0 + rl) * D + d] = from_float<TO>(val);
+            store_lse<kMod>(p, out_row0 + rl, d == 0, M, L);
         } else {
             const size_t wrow = static_cast<size_t>(it.rec) * p.row_stride + rl;
             p.ws_o[wrow * D + d] = acc;
@@ -1609,9 +1786,9 @@ __device__ __forceinline__ void sum_warps(const SplitParams& p, const Item& it, 
 // through shared memory, in the piece's last stage, whose slot the warps keep
 // until the merge is done.  The query rows of each piece arrive in one of two
 // shared buffers filled by the producer.
-template <typename T, int D, int MT, typename TO>
+template <typename T, int D, int MT, typename TO, bool kMod = false>
 __global__ void __launch_bounds__(kThreads, 1)
-    pa_mma_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ CUtensorMap kmap,
+    pa_mma_kernel(const __grid_constant__ ParamsOf<kMod> p, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap)
 {
     constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
@@ -1633,10 +1810,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // inputs may be produced by the previous kernel on the stream
     kernel_entry(p, kmap, vmap, sm);
-    const Sched sc = setup_cta(p, sm);
+    const Sched sc = setup_cta<kMod>(p, sm);
 
     if (warp >= kConsumerWarps) {
-        produce<T, D, true>(p, sc, sm, &kmap, &vmap, warp - kConsumerWarps, lane);
+        produce<T, D, true, kMod>(p, sc, sm, &kmap, &vmap, warp - kConsumerWarps, lane);
         return;
     }
     // consumers: with p.early (the inputs read before the previous kernel
@@ -1655,6 +1832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tb = ((warp % WS) / MT) * TPW;  // this warp's first token in a stage
     const uint32_t zero = smem_u32(sm.zero16);
     const uint32_t qbuf = smem_u32(sm.scratch + p.qbuf_off);
+    [[maybe_unused]] const float qs = score_qscale<kMod>(p);
     uint32_t gt = 0;
     int piece = 0;
     int nsplit = 0;  // split pieces listed since the last flush (uniform)
@@ -1669,12 +1847,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         // causal / length limits of this thread's two rows (0 for padding rows)
         int lim[2];
+        ScoreRow<kMod> mod[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int rl = row0 + g + 8 * h;
             const int rho = it.rsg * ROWS + rl;
             lim[h] = rl < R_cta ? it.past + (p.causal ? (rho % p.NQ) + 1 : p.NQ) : 0;
+            if (rl < R_cta)
+                mod[h].begin(p, sc, it, rho, lim[h]);
+            else
+                mod[h].none();
         }
+        const ScoreSpan<kMod> span(mod, lim);
         const int lim_min = __reduce_min_sync(kFull, min(lim[0] > 0 ? lim[0] : INT_MAX,
                                                          lim[1] > 0 ? lim[1] : INT_MAX));
 
@@ -1750,8 +1934,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int u = 0; u < TG; ++u) {
                 const int tu = tb + u * kMmaTokens;
-                full_tile[u] = tu + kMmaTokens <= n_tile && t0 + tu + kMmaTokens <= lim_min;
+                full_tile[u] = tu + kMmaTokens <= n_tile && t0 + tu + kMmaTokens <= lim_min &&
+                               span.whole(t0 + tu, t0 + tu + kMmaTokens);
             }
+            const TileOff<kMod> to(sc, it, t0);
 
             // ---- S = Q K^T (per group, two accumulator sets per 8-token tile:
             // shorter chains; the groups' MMAs interleave)
@@ -1791,9 +1977,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 4; ++e) {
                         const int h = e >> 1;
                         const int tk = tb + u * kMmaTokens + nt * 8 + 2 * qd + (e & 1);
-                        const float v = (sa[u][0][nt][e] + sa[u][1][nt][e]) * p.qscale;
-                        const bool valid = full_tile[u] || (tk < n_tile && t0 + tk < lim[h]);
-                        sv[u][nt][e] = valid ? v : -INFINITY;
+                        if constexpr (kMod) {
+                            const float x = (sa[u][0][nt][e] + sa[u][1][nt][e]) * qs;
+                            const float v = mod[h].score(p, x, t0 + tk, to);
+                            const bool valid = full_tile[u] || (tk < n_tile && t0 + tk < lim[h] && mod[h].sees(t0 + tk));
+                            sv[u][nt][e] = valid ? v : -INFINITY;
+                            if (tk < n_tile)
+                                mod[h].store(p, to, t0 + tk, sv[u][nt][e]);
+                        } else {
+                            const float v = (sa[u][0][nt][e] + sa[u][1][nt][e]) * p.qscale;
+                            const bool valid = full_tile[u] || (tk < n_tile && t0 + tk < lim[h]);
+                            sv[u][nt][e] = valid ? v : -INFINITY;
+                        }
                         mx[h] = fmaxf(mx[h], sv[u][nt][e]);
                     }
             bool grow = false;
@@ -1838,6 +2033,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 vr[u] = row_addr<D>(v_tile, v_new, zero,
                                     tb + u * kMmaTokens + (lane & 7) + (((lane >> 3) & 1) << 3),
                                     n_tile, t0, it.past);
+            if constexpr (kMod) {
+#pragma unroll
+                for (int u = 0; u < TG; ++u)
+                    if (!full_tile[u] && !span.any(t0 + tb + u * kMmaTokens + (lane & 7) + (((lane >> 3) & 1) << 3)))
+                        vr[u] = RowAddr{zero, 0, 0};
+            }
 #pragma unroll
             for (int pp = 0; pp < NT / 2; ++pp)
 #pragma unroll
@@ -1914,7 +2115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         make_float2(o[i][2], o[i][3]);
             }
             consumer_bar_sync();
-            sum_warps<D, MT, TO>(p, it, R_cta, RU, lg, r, ml_buf, mbuf);
+            sum_warps<D, MT, TO, kMod>(p, it, R_cta, RU, lg, r, ml_buf, mbuf);
         }
         // the stage goes back to the producer (its TMA writes follow these
         // generic-proxy accesses)
@@ -1931,7 +2132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // uniform over the consumer warps (a late abort flag must not split them)
     if (nsplit > 0 && !consumer_bar_or(*sm.abort_flag != 0))
-        flush_split_pieces<D, TO>(p, sc, sm.split_list, nsplit, tot, 2 * ROWS, obuf, kObufFloats);
+        flush_split_pieces<D, TO, kMod>(p, sc, sm.split_list, nsplit, tot, 2 * ROWS, obuf, kObufFloats);
 }
 
 // T: __half or __nv_bfloat16; D: head size; TO: output element type.  The
@@ -1944,9 +2145,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // movmatrix transposes.  Half the MMAs and half the accumulator registers of
 // the 16-row kernel; pipeline, schedule, piece-end and split merges are the
 // same.
-template <typename T, int D, typename TO>
+template <typename T, int D, typename TO, bool kMod = false>
 __global__ void __launch_bounds__(kThreads, 1)
-    pa_mmat_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ CUtensorMap kmap,
+    pa_mmat_kernel(const __grid_constant__ ParamsOf<kMod> p, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap)
 {
     constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
@@ -1967,10 +2168,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // inputs may be produced by the previous kernel on the stream
     kernel_entry(p, kmap, vmap, sm);
-    const Sched sc = setup_cta(p, sm);
+    const Sched sc = setup_cta<kMod>(p, sm);
 
     if (warp >= kConsumerWarps) {
-        produce<T, D, true>(p, sc, sm, &kmap, &vmap, warp - kConsumerWarps, lane);
+        produce<T, D, true, kMod>(p, sc, sm, &kmap, &vmap, warp - kConsumerWarps, lane);
         return;
     }
     // consumers: with p.early (the inputs read before the previous kernel
@@ -1989,6 +2190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tb = (warp % WS) * TPW;  // this warp's first token in a stage
     const uint32_t zero = smem_u32(sm.zero16);
     const uint32_t qbuf = smem_u32(sm.scratch + p.qbuf_off);
+    [[maybe_unused]] const float qs = score_qscale<kMod>(p);
     uint32_t gt = 0;
     int piece = 0;
     int nsplit = 0;  // split pieces listed since the last flush (uniform)
@@ -2002,12 +2204,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         // causal / length limits of this thread's rows 2 qd + e (0 for padding rows)
         int lim[2];
+        ScoreRow<kMod> mod[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int rl = 2 * qd + e;
             const int rho = it.rsg * ROWS + rl;
             lim[e] = rl < R_cta ? it.past + (p.causal ? (rho % p.NQ) + 1 : p.NQ) : 0;
+            if (rl < R_cta)
+                mod[e].begin(p, sc, it, rho, lim[e]);
+            else
+                mod[e].none();
         }
+        const ScoreSpan<kMod> span(mod, lim);
         const int lim_min = __reduce_min_sync(kFull, min(lim[0] > 0 ? lim[0] : INT_MAX,
                                                          lim[1] > 0 ? lim[1] : INT_MAX));
 
@@ -2075,8 +2283,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int u = 0; u < TG; ++u) {
                 const int tu = tb + u * kMmaTokens;
-                full_tile[u] = tu + kMmaTokens <= n_tile && t0 + tu + kMmaTokens <= lim_min;
+                full_tile[u] = tu + kMmaTokens <= n_tile && t0 + tu + kMmaTokens <= lim_min &&
+                               span.whole(t0 + tu, t0 + tu + kMmaTokens);
             }
+            const TileOff<kMod> to(sc, it, t0);
 
             // ---- S^T = K Q^T: operand A = 16 token rows of K (ldmatrix gives
             // (tokens 0-7 | 8-15) x (columns 0-7 | 8-15) as a0 a2 a1 a3); two
@@ -2113,9 +2323,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = 0; e < 4; ++e) {
                     const int h = e & 1;
                     const int tk = tb + u * kMmaTokens + g + ((e >> 1) << 3);
-                    const float v = (sa[u][0][e] + sa[u][1][e]) * p.qscale;
-                    const bool valid = full_tile[u] || (tk < n_tile && t0 + tk < lim[h]);
-                    sv[u][e] = valid ? v : -INFINITY;
+                    if constexpr (kMod) {
+                        const float x = (sa[u][0][e] + sa[u][1][e]) * qs;
+                        const float v = mod[h].score(p, x, t0 + tk, to);
+                        const bool valid = full_tile[u] || (tk < n_tile && t0 + tk < lim[h] && mod[h].sees(t0 + tk));
+                        sv[u][e] = valid ? v : -INFINITY;
+                        if (tk < n_tile)
+                            mod[h].store(p, to, t0 + tk, sv[u][e]);
+                    } else {
+                        const float v = (sa[u][0][e] + sa[u][1][e]) * p.qscale;
+                        const bool valid = full_tile[u] || (tk < n_tile && t0 + tk < lim[h]);
+                        sv[u][e] = valid ? v : -INFINITY;
+                    }
                     mx[h] = fmaxf(mx[h], sv[u][e]);
                 }
             bool grow = false;
@@ -2171,6 +2390,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 vr[u] = row_addr<D>(v_tile, v_new, zero,
                                     tb + u * kMmaTokens + (lane & 7) + (((lane >> 3) & 1) << 3),
                                     n_tile, t0, it.past);
+            if constexpr (kMod) {
+#pragma unroll
+                for (int u = 0; u < TG; ++u)
+                    if (!full_tile[u] && !span.any(t0 + tb + u * kMmaTokens + (lane & 7) + (((lane >> 3) & 1) << 3)))
+                        vr[u] = RowAddr{zero, 0, 0};
+            }
 #pragma unroll
             for (int mt = 0; mt < KS; ++mt)
 #pragma unroll
@@ -2231,7 +2456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             consumer_bar_sync();
-            sum_warps<D, 1, TO>(p, it, R_cta, RU, lg, r, ml_buf, obuf);
+            sum_warps<D, 1, TO, kMod>(p, it, R_cta, RU, lg, r, ml_buf, obuf);
         }
         // automatic schedule: the CTA's first and last pieces at most
         if (!it.whole && p.counters && nsplit < kSplitList) {
@@ -2242,7 +2467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // uniform over the consumer warps (a late abort flag must not split them)
     if (nsplit > 0 && !consumer_bar_or(*sm.abort_flag != 0))
-        flush_split_pieces<D, TO>(p, sc, sm.split_list, nsplit, tot, 2 * ROWS, obuf, kObufFloats);
+        flush_split_pieces<D, TO, kMod>(p, sc, sm.split_list, nsplit, tot, 2 * ROWS, obuf, kObufFloats);
 }
 
 // -------------------------------------------------------------- merge kernel
@@ -2422,6 +2647,26 @@ SplitFn pick_split_mma(int D, int MT)
     return MT == 0   ? pa_mmat_kernel<T, 128, TO>
            : MT == 1 ? pa_mma_kernel<T, 128, 1, TO>
                      : pa_mma_kernel<T, 128, 2, TO>;
+}
+
+template <typename T, typename TO>
+ScoredFn pick_scored_simt(int D, int RG)
+{
+    if (D == 64)
+        return RG == 4 ? pa_split_kernel<T, 64, 4, TO, true> : pa_split_kernel<T, 64, 8, TO, true>;
+    return RG == 4 ? pa_split_kernel<T, 128, 4, TO, true> : pa_split_kernel<T, 128, 8, TO, true>;
+}
+
+template <typename T, typename TO>
+ScoredFn pick_scored_mma(int D, int MT)
+{
+    if (D == 64)
+        return MT == 0   ? pa_mmat_kernel<T, 64, TO, true>
+               : MT == 1 ? pa_mma_kernel<T, 64, 1, TO, true>
+                         : pa_mma_kernel<T, 64, 2, TO, true>;
+    return MT == 0   ? pa_mmat_kernel<T, 128, TO, true>
+           : MT == 1 ? pa_mma_kernel<T, 128, 1, TO, true>
+                     : pa_mma_kernel<T, 128, 2, TO, true>;
 }
 
 template <typename TO>
