@@ -49,6 +49,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "pa_attention_vjp.h"
 #include "pa_decode.h"
 
 #ifdef __cplusplus
@@ -79,6 +80,32 @@ int pa_decode_scored(const void *q, const void *k_cache, const void *v_cache,
 /* Scratch bytes of the key weights: every score of the call in float32, and
  * the rows' softmax denominators.  0 for invalid sizes. */
 size_t pa_scored_scratch_bytes(int batch, int max_blocks, int BLOCK, int H, int KV, int NQ);
+
+/*
+ * The gradient of dense attention with modified scores: pa_attention_vjp
+ * (pa_attention_vjp.h: arguments, layouts, opts, workspace, errors) of
+ *
+ *   y = softmax(score(scale * q k^T) + mask) v
+ *
+ * with row i and key j at positions i and j (top-left aligned, as that
+ * entry's causal rule), key j visible when j < prefix[b], or j <= i (causal)
+ * and |i - j| < window, and
+ *
+ *   ds = p * (dp - delta) * (1 - tanh^2(scale q.k / softcap))   under a cap.
+ *
+ * A mask of opts (mask_kind != 0) adds its bias to the modified score and
+ * hides what it hides, prefix or not.  Rows that see no key get dq = 0.
+ * 16-bit inputs with D = 128 and no mask run on the tensor cores; tiles
+ * outside prefix and window are skipped.  dq is accumulated by float32
+ * reductions whose order varies: its last bits may differ from call to call.
+ * More errors: PA_ERR_NULL_POINTER without score, PA_ERR_BAD_DIMS for a
+ * softcap that is negative or not finite or a negative window,
+ * PA_ERR_ALIGNMENT for slopes or prefix not 4-byte aligned.
+ */
+int pa_attention_vjp_scored(const void *q, const void *k, const void *v, const void *y,
+                            const void *g, const void *mask, void *dq, void *dk, void *dv,
+                            float scale, int B, int HQ, int HK, int SQ, int SK, int D,
+                            const pa_score *score, const pa_vjp_opts *opts, void *stream);
 
 #ifdef __cplusplus
 }

@@ -188,6 +188,9 @@ def load(path: Path = LIBRARY) -> ctypes.CDLL:
                                      ctypes.POINTER(PaOpts), P]
     lib.pa_scored_scratch_bytes.restype = ctypes.c_size_t
     lib.pa_scored_scratch_bytes.argtypes = [I, I, I, I, I, I]
+    lib.pa_attention_vjp_scored.restype = I
+    lib.pa_attention_vjp_scored.argtypes = [P, P, P, P, P, P, P, P, P, ctypes.c_float, I, I, I, I, I, I,
+                                            ctypes.POINTER(Score), ctypes.POINTER(VjpOpts), P]
     lib.pa_rotary.restype = I
     lib.pa_rotary.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, ctypes.POINTER(RotaryOpts), P]
     lib.pa_cache_evict.restype = I
@@ -811,6 +814,42 @@ def decode_scored(q, k_cache, v_cache, block_table, seq_lens, k_new, v_new, *, s
                       key_weights=key_weights, key_weights_out=key_weights_out, decay=decay,
                       partitions=partitions, out=out, out_dtype=out_dtype, workspace=workspace,
                       status=status, checked=checked).run(stream)
+
+
+class ScoredVjpPlan(VjpPlan):
+    """One prepared attention backward with modified scores
+    (pa_attention_vjp_scored): as ``VjpPlan``, with the ``softcap``, ``slopes``
+    [HQ], ``window`` and ``prefix`` [B] of ``ScoredPlan``; row i and key j are
+    at positions i and j."""
+
+    def __init__(self, q, k, v, y, g, mask=None, *, scale: float, causal: bool = False,
+                 softcap: float = 0.0, slopes=None, window: int = 0, prefix=None, out_dtype=None,
+                 kernel: int = 0, status=None, wait_limit_ns: int = 0, out=None):
+        super().__init__(q, k, v, y, g, mask, scale=scale, causal=causal, out_dtype=out_dtype,
+                         kernel=kernel, status=status, wait_limit_ns=wait_limit_ns, out=out)
+        self.score = _score(softcap, slopes, window, prefix, int(q.shape[0]), int(q.shape[1]), q.device)
+        self._scored_keep = (slopes, prefix)
+        self._args = self._args[:-1] + (ctypes.byref(self.score), ctypes.byref(self.opts))
+
+    def run(self, stream=None):
+        if torch.cuda.current_device() == self.device.index:
+            rc = LIB.pa_attention_vjp_scored(*self._args, _stream_handle(stream))
+        else:
+            with torch.cuda.device(self.device):
+                rc = LIB.pa_attention_vjp_scored(*self._args, _stream_handle(stream))
+        if rc != 0:
+            raise PagedAttentionError(rc)
+        return self.dq, self.dk, self.dv
+
+
+def attention_vjp_scored(q, k, v, y, g, mask=None, *, scale: float, causal: bool = False,
+                         softcap: float = 0.0, slopes=None, window: int = 0, prefix=None,
+                         out_dtype=None, kernel: int = 0, status=None, stream=None, out=None):
+    """dq, dk, dv of attention with modified scores (pa_attention_vjp_scored):
+    see ``ScoredVjpPlan``."""
+    return ScoredVjpPlan(q, k, v, y, g, mask, scale=scale, causal=causal, softcap=softcap,
+                         slopes=slopes, window=window, prefix=prefix, out_dtype=out_dtype,
+                         kernel=kernel, status=status, out=out).run(stream)
 
 
 # ------------------------------------------------------------------- rotary positions

@@ -30,6 +30,7 @@
 
 #include "pa_attention_vjp.h"
 #include "pa_common.cuh"
+#include "pa_scored.h"
 #include "pa_vjp.cuh"
 
 namespace pa {
@@ -81,11 +82,42 @@ __device__ __forceinline__ float warp_sum(float x)
     return x;
 }
 
+// Score (i, j) in base-2 units of a dot product (already times `cap_in` under a
+// cap, else times scale_log2), and the cap's factor on its gradient.
+template <bool kMod>
+__device__ __forceinline__ float simt_score(const VjpParamsOf<kMod>& p, float x, int b, int h, int i, int j, int pl,
+                                            float* slope)
+{
+    *slope = 1.f;
+    if constexpr (kMod) {
+        if (!vjp_seen(p, pl, i, j))
+            return -INFINITY;
+        if (p.cap_out != 0.f) {
+            const float th = tanhf(x);
+            *slope = 1.f - th * th;
+            x = p.cap_out * th;
+        }
+        const float far = p.slopes ? __ldg(p.slopes + h) * static_cast<float>(abs(i - j)) : 0.f;
+        return x + (vjp_bias(p, b, h, i, j, false) - far) * kVjpLog2e;
+    } else {
+        return x + vjp_bias(p, b, h, i, j, p.causal) * kVjpLog2e;
+    }
+}
+
+template <bool kMod>
+__device__ __forceinline__ float simt_factor(const VjpParamsOf<kMod>& p)
+{
+    if constexpr (kMod)
+        return p.cap_out != 0.f ? p.cap_in : p.scale_log2;
+    else
+        return p.scale_log2;
+}
+
 // Step 1.  grid (ceil(SQ / 8), HQ, B), 256 threads: warp w owns query row
 // blockIdx.x * 8 + w; the CTA stages 32 keys at a time (float, rows padded
 // to D + 1 so that 32 lanes reading 32 different keys hit 32 banks).
-template <typename T>
-__global__ void __launch_bounds__(256) vjp_stats_simt(VjpParams p)
+template <typename T, bool kMod = false>
+__global__ void __launch_bounds__(256) vjp_stats_simt(VjpParamsOf<kMod> p)
 {
     extern __shared__ float sm[];
     const int D = p.D, DP = D + 1;
@@ -97,8 +129,9 @@ __global__ void __launch_bounds__(256) vjp_stats_simt(VjpParams p)
     float* kt = sm + kStatRows * D;
     const int64_t row = (static_cast<int64_t>(b) * p.HQ + h) * p.SQ + (live ? i : 0);
     const T* q = static_cast<const T*>(p.q) + row * D;
+    const float factor = simt_factor<kMod>(p);
     for (int d = lane; d < D; d += 32)
-        qrow[d] = live ? ldf(q, d) * p.scale_log2 : 0.f;
+        qrow[d] = live ? ldf(q, d) * factor : 0.f;
     if (live) {
         const T* y = static_cast<const T*>(p.y) + row * D;
         const T* g = static_cast<const T*>(p.g) + row * D;
@@ -116,8 +149,17 @@ __global__ void __launch_bounds__(256) vjp_stats_simt(VjpParams p)
     int kend = p.SK;
     if (p.causal)
         kend = min(kend, static_cast<int>(blockIdx.x) * kStatRows + kStatRows);
+    int pl = 0, kskip = 0;
+    if constexpr (kMod) {
+        pl = vjp_prefix(p, b);
+        kend = max(kend, pl);
+        // keys before the first row's window, less those of the prefix
+        kskip = max(static_cast<int>(blockIdx.x) * kStatRows - p.window + 1, 0);
+    }
     float m = -INFINITY, l = 0.f;
     for (int j0 = 0; j0 < kend; j0 += kStatKeys) {
+        if (kMod && j0 >= pl && j0 + kStatKeys <= kskip)
+            continue;
         __syncthreads();
         for (int e = threadIdx.x; e < kStatKeys * D; e += blockDim.x) {
             const int jj = e / D, d = e - jj * D;
@@ -130,7 +172,8 @@ __global__ void __launch_bounds__(256) vjp_stats_simt(VjpParams p)
             float dot = 0.f;
             for (int d = 0; d < D; ++d)
                 dot = fmaf(qrow[d], kt[lane * DP + d], dot);
-            s = dot + vjp_bias(p, b, h, i, j) * kVjpLog2e;
+            float unused;
+            s = simt_score<kMod>(p, dot, b, h, i, j, pl, &unused);
         }
         const float mn = fmaxf(m, warp_max(s));
         if (mn != -INFINITY) {
@@ -148,8 +191,8 @@ __global__ void __launch_bounds__(256) vjp_stats_simt(VjpParams p)
 // t % 16) entries of p and ds, then owns key t / 16 and columns t % 16 +
 // 16 m of dk and dv (registers), then row t / 16 and the same columns of
 // the step's dq (atomics into the accumulator).
-template <typename T, typename TO>
-__global__ void __launch_bounds__(256) vjp_main_simt(VjpParams p)
+template <typename T, typename TO, bool kMod = false>
+__global__ void __launch_bounds__(256) vjp_main_simt(VjpParamsOf<kMod> p)
 {
     extern __shared__ float sm[];
     const int D = p.D, DP = D + 1;
@@ -176,12 +219,20 @@ __global__ void __launch_bounds__(256) vjp_main_simt(VjpParams p)
     for (int m = 0; m < kM; ++m)
         dk[m] = dv[m] = 0.f;
     const int pj = t >> 4, pr = t & 15;  // phase 1: key, row
-    const int i_start = p.causal ? min(k0, p.SQ) : 0;
+    int i_start = p.causal ? min(k0, p.SQ) : 0, i_end = p.SQ, pl = 0;
+    if constexpr (kMod) {
+        pl = vjp_prefix(p, b);
+        if (k0 < pl)
+            i_start = 0;
+        else if (p.window < p.SQ)
+            i_end = min(p.SQ, k0 + kMainKeys - 1 + p.window);  // SQ < 2^31 and the window is below it
+    }
+    const float factor = simt_factor<kMod>(p);
     for (int gi = 0; gi < p.groups; ++gi) {
         const int h = kh * p.groups + gi;
         const int64_t qbase = (static_cast<int64_t>(b) * p.HQ + h) * p.SQ;
         const int64_t sbase = (static_cast<int64_t>(b) * p.HQ + h) * p.sqp;
-        for (int i0 = i_start; i0 < p.SQ; i0 += kMainRows) {
+        for (int i0 = i_start; i0 < i_end; i0 += kMainRows) {
             __syncthreads();  // the previous step is done with Qs, Gs, Ps, Ss
             for (int e = t; e < kMainRows * D; e += blockDim.x) {
                 const int rr = e / D, d = e - rr * D;
@@ -204,9 +255,10 @@ __global__ void __launch_bounds__(256) vjp_main_simt(VjpParams p)
                         s = fmaf(Qs[pr * DP + d], Ks[pj * DP + d], s);
                         dp = fmaf(Gs[pr * DP + d], Vs[pj * DP + d], dp);
                     }
-                    const float s2 = s * p.scale_log2 + vjp_bias(p, b, h, i, key) * kVjpLog2e;
+                    float slope;
+                    const float s2 = simt_score<kMod>(p, s * factor, b, h, i, key, pl, &slope);
                     pv = exp2f(s2 - rl[pr]);
-                    dsv = pv * (dp - rd[pr]) * p.scale;
+                    dsv = pv * (dp - rd[pr]) * p.scale * slope;
                 }
                 Ps[pj * 17 + pr] = pv;
                 Ss[pj * 17 + pr] = dsv;
@@ -296,12 +348,12 @@ bool layout(int B, int HQ, int SQ, int D, int dtype, int out_dtype, VjpLayout* L
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-template <typename T, typename TO>
-int launch_simt(const VjpParams& p, cudaStream_t st, uint64_t* launches)
+template <typename T, typename TO, bool kMod>
+int launch_simt(const VjpParamsOf<kMod>& p, cudaStream_t st, uint64_t* launches)
 {
     if (p.SQ > 0) {
         const size_t smem = (kStatRows * p.D + kStatKeys * (p.D + 1)) * sizeof(float);
-        auto fn = vjp_stats_simt<T>;
+        auto fn = vjp_stats_simt<T, kMod>;
         if (cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
             cudaSuccess)
@@ -316,7 +368,7 @@ int launch_simt(const VjpParams& p, cudaStream_t st, uint64_t* launches)
         const size_t smem = ((kMainKeys + kMainKeys + kMainRows + kMainRows) * (p.D + 1) +
                              2 * kMainKeys * 17 + 2 * kMainRows) *
                             sizeof(float);
-        auto fn = vjp_main_simt<T, TO>;
+        auto fn = vjp_main_simt<T, TO, kMod>;
         if (cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
             cudaSuccess)
@@ -330,15 +382,17 @@ int launch_simt(const VjpParams& p, cudaStream_t st, uint64_t* launches)
     return PA_OK;
 }
 
-using SimtFn = int (*)(const VjpParams&, cudaStream_t, uint64_t*);
+template <bool kMod>
+using SimtFn = int (*)(const VjpParamsOf<kMod>&, cudaStream_t, uint64_t*);
 
-SimtFn pick_simt(int dtype, bool f32_out)
+template <bool kMod>
+SimtFn<kMod> pick_simt(int dtype, bool f32_out)
 {
     if (dtype == PA_F32)
-        return launch_simt<float, float>;
+        return launch_simt<float, float, kMod>;
     if (dtype == PA_F16)
-        return f32_out ? launch_simt<__half, float> : launch_simt<__half, __half>;
-    return f32_out ? launch_simt<__nv_bfloat16, float> : launch_simt<__nv_bfloat16, __nv_bfloat16>;
+        return f32_out ? launch_simt<__half, float, kMod> : launch_simt<__half, __half, kMod>;
+    return f32_out ? launch_simt<__nv_bfloat16, float, kMod> : launch_simt<__nv_bfloat16, __nv_bfloat16, kMod>;
 }
 
 }  // namespace
@@ -358,9 +412,10 @@ extern "C" size_t pa_attention_vjp_workspace_bytes(int B, int HQ, int SQ, int D,
     return L.total;
 }
 
-extern "C" int pa_attention_vjp(const void* q, const void* k, const void* v, const void* y, const void* g,
-                                const void* mask, void* dq, void* dk, void* dv, float scale, int B, int HQ,
-                                int HK, int SQ, int SK, int D, const pa_vjp_opts* opts, void* stream)
+// pa_attention_vjp, and pa_attention_vjp_scored when `score` is not NULL.
+static int vjp_impl(const void* q, const void* k, const void* v, const void* y, const void* g, const void* mask,
+                    void* dq, void* dk, void* dv, float scale, int B, int HQ, int HK, int SQ, int SK, int D,
+                    const pa_score* score, const pa_vjp_opts* opts, void* stream)
 {
     if (!opts)
         return PA_ERR_NULL_POINTER;
@@ -410,7 +465,8 @@ extern "C" int pa_attention_vjp(const void* q, const void* k, const void* v, con
         return PA_ERR_WORKSPACE;
     const int odt = out_type(o.dtype, o.out_dtype);
     unsigned char* ws = static_cast<unsigned char*>(o.workspace);
-    VjpParams p{};
+    VjpScoredParams sp{};
+    VjpParams& p = sp;
     p.q = q;
     p.k = k;
     p.v = v;
@@ -440,13 +496,23 @@ extern "C" int pa_attention_vjp(const void* q, const void* k, const void* v, con
         p.md[e] = o.mask_kind ? o.mask_dims[e] : 1;
     p.scale = scale;
     p.scale_log2 = scale * kVjpLog2e;
+    if (score) {
+        sp.slopes = score->slopes;
+        sp.prefix = score->prefix;
+        sp.cap_in = score->softcap > 0.f ? scale / score->softcap : 0.f;
+        sp.cap_out = score->softcap > 0.f ? score->softcap * kVjpLog2e : 0.f;
+        sp.window = score->window > 0 ? score->window : INT_MAX;
+    }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint64_t launches = 0;
     int rc;
-    if (o.kernel != 1 && vjp_tc_supported(o.dtype, D, HQ / HK, o.mask_kind))
-        rc = launch_vjp_tc(p, o.dtype, odt == PA_F32, st, &launches);
+    const bool tc = o.kernel != 1 && vjp_tc_supported(o.dtype, D, HQ / HK, o.mask_kind);
+    if (score)
+        rc = tc ? launch_vjp_tc_scored(sp, o.dtype, odt == PA_F32, st, &launches)
+                : pick_simt<true>(o.dtype, odt == PA_F32)(sp, st, &launches);
     else
-        rc = pick_simt(o.dtype, odt == PA_F32)(p, st, &launches);
+        rc = tc ? launch_vjp_tc(p, o.dtype, odt == PA_F32, st, &launches)
+                : pick_simt<false>(o.dtype, odt == PA_F32)(p, st, &launches);
     if (rc == PA_OK && p.dq_acc && SQ > 0) {
         const int64_t n = qn;
         const int blocks = static_cast<int>(std::min<int64_t>((n + 255) / 256, 152 * 16));
@@ -459,4 +525,25 @@ extern "C" int pa_attention_vjp(const void* q, const void* k, const void* v, con
     }
     count_launches(launches);
     return rc;
+}
+
+extern "C" int pa_attention_vjp(const void* q, const void* k, const void* v, const void* y, const void* g,
+                                const void* mask, void* dq, void* dk, void* dv, float scale, int B, int HQ,
+                                int HK, int SQ, int SK, int D, const pa_vjp_opts* opts, void* stream)
+{
+    return vjp_impl(q, k, v, y, g, mask, dq, dk, dv, scale, B, HQ, HK, SQ, SK, D, nullptr, opts, stream);
+}
+
+extern "C" int pa_attention_vjp_scored(const void* q, const void* k, const void* v, const void* y, const void* g,
+                                       const void* mask, void* dq, void* dk, void* dv, float scale, int B, int HQ,
+                                       int HK, int SQ, int SK, int D, const pa_score* score, const pa_vjp_opts* opts,
+                                       void* stream)
+{
+    if (!score)
+        return PA_ERR_NULL_POINTER;
+    if (!(score->softcap >= 0.f) || !std::isfinite(score->softcap) || score->window < 0)
+        return PA_ERR_BAD_DIMS;
+    if ((reinterpret_cast<uintptr_t>(score->slopes) & 3) || (reinterpret_cast<uintptr_t>(score->prefix) & 3))
+        return PA_ERR_ALIGNMENT;
+    return vjp_impl(q, k, v, y, g, mask, dq, dk, dv, scale, B, HQ, HK, SQ, SK, D, score, opts, stream);
 }

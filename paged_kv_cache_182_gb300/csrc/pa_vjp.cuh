@@ -5,7 +5,9 @@
 
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cstdint>
+#include <type_traits>
 
 namespace pa {
 
@@ -35,12 +37,38 @@ struct VjpParams {
     float scale, scale_log2;
 };
 
+// Modified scores (pa_attention_vjp_scored):
+//   t = scale q.k; under a cap t = cap tanh(t / cap); t -= slopes[h] |i - j|;
+//   key j visible to row i when j < prefix[b], or within the causal rule and
+//   |i - j| < window.
+// The cap leaves the factor 1 - tanh^2 on ds; bias and masks leave none.
+struct VjpScoredParams : VjpParams {
+    const float* slopes;    // [HQ], or NULL
+    const int32_t* prefix;  // [B], or NULL
+    float cap_in, cap_out;  // scale / cap, cap * log2(e); 0 without a cap
+    int window;             // INT_MAX: none
+};
+
+template <bool kMod>
+using VjpParamsOf = std::conditional_t<kMod, VjpScoredParams, VjpParams>;
+
+// Keys below are visible to every row of sequence b.
+__device__ __forceinline__ int vjp_prefix(const VjpScoredParams& p, int b)
+{
+    return p.prefix ? min(max(__ldg(p.prefix + b), 0), p.SK) : 0;
+}
+
+__device__ __forceinline__ bool vjp_seen(const VjpScoredParams& p, int pl, int i, int j)
+{
+    return j < pl || ((!p.causal || j <= i) && abs(i - j) < p.window);
+}
+
 // Additive bias of score (b, h, i, j) in natural-log units: the causal rule
 // (key j hidden from row i when j > i), then the mask (boolean: 0 or -inf;
 // additive: the value; keys at or past a width W > 1 hidden).
-__device__ __forceinline__ float vjp_bias(const VjpParams& p, int b, int h, int i, int j)
+__device__ __forceinline__ float vjp_bias(const VjpParams& p, int b, int h, int i, int j, bool causal)
 {
-    if (p.causal && j > i)
+    if (causal && j > i)
         return -INFINITY;
     if (p.mask_kind == 0)
         return 0.f;
@@ -63,6 +91,7 @@ __device__ __forceinline__ float vjp_bias(const VjpParams& p, int b, int h, int 
 // caller).  Returns PA_OK or a PA_ERR_* code.
 bool vjp_tc_supported(int dtype, int D, int groups, int mask_kind);
 int launch_vjp_tc(const VjpParams& p, int dtype, bool f32_out, cudaStream_t st, uint64_t* launches);
+int launch_vjp_tc_scored(const VjpScoredParams& p, int dtype, bool f32_out, cudaStream_t st, uint64_t* launches);
 
 // Adds to the library's count of kernel launches (pa_kernel_launches).
 void count_launches(uint64_t n);

@@ -94,9 +94,13 @@ __device__ __forceinline__ int stats_item(int k, int c, int G) { return (k & 1) 
 
 struct StatsItem {
     int b, h, i0, nk, ntiles;
+    int skip_at, skip;  // modified scores: `skip` key tiles left out before the skip_at-th
+    int pl;             // and the sequence's prefix
+    __device__ __forceinline__ int tile(int t) const { return t >= skip_at ? t + skip : t; }
 };
 
-__device__ __forceinline__ StatsItem stats_item_at(const VjpParams& p, int n, int tiles)
+template <bool kMod>
+__device__ __forceinline__ StatsItem stats_item_at(const VjpParamsOf<kMod>& p, int n, int tiles)
 {
     StatsItem it;
     const int bh = n % (p.B * p.HQ);
@@ -105,7 +109,60 @@ __device__ __forceinline__ StatsItem stats_item_at(const VjpParams& p, int n, in
     it.i0 = (tiles - 1 - n / (p.B * p.HQ)) * kSRows;
     it.nk = p.causal ? min(p.SK, it.i0 + kSRows) : p.SK;
     it.ntiles = (it.nk + kKeys - 1) / kKeys;
+    it.skip_at = it.skip = it.pl = 0;
+    if constexpr (kMod) {
+        // tiles [0, pt) hold the prefix, [lt, et) the rows' windows
+        it.pl = vjp_prefix(p, it.b);
+        if (!p.causal && p.window < p.SK)
+            it.nk = min(p.SK, it.i0 + kSRows - 1 + p.window);
+        const int et = (it.nk + kKeys - 1) / kKeys, pt = (it.pl + kKeys - 1) / kKeys;
+        const int lt = max(it.i0 - p.window + 1, 0) / kKeys;
+        it.skip_at = pt;
+        it.skip = max(0, lt - pt);
+        it.ntiles = lt > pt ? pt + max(0, et - lt) : max(pt, et);
+    }
     return it;
+}
+
+// tanh of N scores (times 1 / cap): an odd polynomial of degree 11 where every
+// score of the warp is within 0.7 -- fitted here for the least largest relative
+// error of tanh(y) / y in y^2, 1.4e-8 -- two scores an instruction and no
+// special-function operation (the exponentials of the softmax fill that unit);
+// else 1 - 2 / (1 + e^(2 |y|)) where a score is beyond.
+constexpr float kTanhMax = 0.7f;
+
+template <int N>
+__device__ __forceinline__ void tanh_block(float (&y)[N])
+{
+    constexpr float kTanhC[6] = {0.999999986f,   -0.333331304f, 0.133284148f,
+                                 -0.0535260093f, 0.0200244578f, -0.00508833599f};
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        top = fmaxf(top, fabsf(y[j]));
+    const bool wide = __any_sync(kAll, !(top <= kTanhMax));
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+        const float2 v = make_float2(y[j], y[j + 1]);
+        const float2 z = __fmul2_rn(v, v);
+        float2 a = make_float2(kTanhC[5], kTanhC[5]);
+#pragma unroll
+        for (int e = 4; e >= 0; --e)
+            a = __ffma2_rn(a, z, make_float2(kTanhC[e], kTanhC[e]));
+        a = __fmul2_rn(a, v);
+        if (wide) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float x = u ? v.y : v.x;
+                const float e = fast_exp2(fabsf(x) * 2.8853900817779268f);  // 2 log2(e)
+                const float far = copysignf(1.f - __fdividef(2.f, 1.f + e), x);
+                if (!(fabsf(x) <= kTanhMax))
+                    (u ? a.y : a.x) = far;
+            }
+        }
+        y[j] = a.x;
+        y[j + 1] = a.y;
+    }
 }
 
 struct MainBars {
@@ -153,9 +210,9 @@ __device__ __forceinline__ float2 unpack2(uint32_t w)
 // Row statistics.  grid = min(items, SMs); items = B * HQ * ceil(SQ / 128),
 // numbered row tile slowest, the row tiles that see the most keys (causal)
 // first.
-template <typename T>
+template <typename T, bool kMod>
 __global__ void __launch_bounds__(kStatsThreads, 1)
-    vjp_stats_tc(const __grid_constant__ VjpParams p, const __grid_constant__ CUtensorMap qmap,
+    vjp_stats_tc(const __grid_constant__ VjpParamsOf<kMod> p, const __grid_constant__ CUtensorMap qmap,
                  const __grid_constant__ CUtensorMap kmap)
 {
     constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
@@ -219,7 +276,7 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
                 const int n = stats_item(k, C, G);
                 if (n >= total)
                     break;
-                const StatsItem it = stats_item_at(p, n, tiles);
+                const StatsItem it = stats_item_at<kMod>(p, n, tiles);
                 if (it.ntiles == 0)
                     continue;
                 const int u = qn & 1;
@@ -242,7 +299,7 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
                     }
                     mbar_arrive_expect_tx(&bars.k_full[s], 2 * kHalf128);
                     for (int hh = 0; hh < 2; ++hh)
-                        tma_load_4d(sK + s * 2 * kHalf128 + hh * kHalf128, &kmap, 0, hh, t * kKeys, it.b * p.HK + kh,
+                        tma_load_4d(sK + s * 2 * kHalf128 + hh * kHalf128, &kmap, 0, hh, it.tile(t) * kKeys, it.b * p.HK + kh,
                                     &bars.k_full[s]);
                 }
             }
@@ -266,7 +323,7 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
                 const int n = stats_item(k, C, G);
                 if (n >= total)
                     break;
-                const StatsItem it = stats_item_at(p, n, tiles);
+                const StatsItem it = stats_item_at<kMod>(p, n, tiles);
                 if (it.ntiles == 0)
                     continue;
                 const int u = qn & 1;
@@ -314,9 +371,12 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
             const int n = stats_item(k, C, G);
             if (n >= total)
                 break;
-            const StatsItem it = stats_item_at(p, n, tiles);
+            const StatsItem it = stats_item_at<kMod>(p, n, tiles);
             const int i = it.i0 + row;
             float m = -INFINITY, l = 0.f;
+            float slope2 = 0.f;
+            if constexpr (kMod)
+                slope2 = p.slopes ? __ldg(p.slopes + it.h) * kVjpLog2e : 0.f;
             for (int t = 0; t < it.ntiles && !fault; ++t, ++g) {
                 const int s = g & 1;
                 const bool got = __all_sync(
@@ -335,12 +395,56 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     pm8[e] = -INFINITY;
-                const int kbase = t * kKeys + part * 64;
+                const int kbase = it.tile(t) * kKeys + part * 64;
                 Cols32 xs[2];
                 tmem_ld32_issue(xs[0], tS + s * kKeys + lane_off + part * 64);
                 tmem_ld32_issue(xs[1], tS + s * kKeys + lane_off + part * 64 + 32);
                 tmem_ld_wait(xs[1]);
                 tmem_ld_wait(xs[0]);
+                if constexpr (kMod) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&bars.s_free[s]);
+                    // modified scores in base-2 units
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float y[32];
+                        const float f = p.cap_out != 0.f ? p.cap_in : p.scale_log2;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            y[j] = __uint_as_float(xs[c].r[j]) * f;
+                        if (p.cap_out != 0.f) {
+                            tanh_block(y);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                y[j] *= p.cap_out;
+                        }
+                        if (p.slopes) {
+                            const float d0 = static_cast<float>(i - kbase - c * 32);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                y[j] = fmaf(-slope2, fabsf(d0 - static_cast<float>(j)), y[j]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            sc[c * 32 + j] = y[j];
+                    }
+                    // the warp's rows i_w .. i_w + 31 all see the block's keys?
+                    const int i_w = it.i0 + (warp & 3) * 32;
+                    const bool plain = kbase + 64 <= it.pl ||
+                                       (kbase + 64 <= p.SK && (!p.causal || kbase + 63 <= i_w) &&
+                                        i_w + 31 - kbase < p.window && (p.causal || kbase + 63 - i_w < p.window));
+                    if (!plain) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            if (!(kbase + j < p.SK && vjp_seen(p, it.pl, i, kbase + j)))
+                                sc[j] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 64; ++j)
+                        pm8[j & 7] = fmaxf(pm8[j & 7], sc[j]);
+                } else {
                 // the mask test is taken once per tile (warp-uniform), never per
                 // score: a branch per score cost more than the rest of the tile
                 if (kbase + 63 >= it.nk || (p.causal && kbase + 63 > it.i0)) {
@@ -368,11 +472,12 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&bars.s_free[s]);
+                }
                 const float pm = fmaxf(fmaxf(fmaxf(pm8[0], pm8[1]), fmaxf(pm8[2], pm8[3])),
                                        fmaxf(fmaxf(pm8[4], pm8[5]), fmaxf(pm8[6], pm8[7])));
-                const float mt = fmaxf(m, pm * p.scale_log2);  // base-2 units
+                const float c2 = kMod ? 1.f : p.scale_log2;
+                const float mt = fmaxf(m, pm * c2);  // base-2 units
                 if (mt != -INFINITY) {
-                    const float c2 = p.scale_log2;
                     float s8[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
@@ -414,7 +519,7 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
             const int n = stats_item(k, C, G);
             if (n >= total)
                 break;
-            const StatsItem it = stats_item_at(p, n, tiles);
+            const StatsItem it = stats_item_at<kMod>(p, n, tiles);
             const int64_t r0 = (static_cast<int64_t>(it.b) * p.HQ + it.h) * p.SQ;
             const int64_t s0 = (static_cast<int64_t>(it.b) * p.HQ + it.h) * p.sqp;
 #pragma unroll 1
@@ -468,9 +573,9 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
 // ---------------------------------------------------------------------------
 // Backward.  grid = ceil(SK / 128) * B * HK, (batch, key/value head) fastest:
 // the key tiles that the most (causal) rows see are launched first.
-template <typename T, typename TO>
+template <typename T, typename TO, bool kMod>
 __global__ void __launch_bounds__(kMainThreads, 1)
-    vjp_main_tc(const __grid_constant__ VjpParams p, const __grid_constant__ CUtensorMap qmap,
+    vjp_main_tc(const __grid_constant__ VjpParamsOf<kMod> p, const __grid_constant__ CUtensorMap qmap,
                 const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap)
 {
@@ -495,8 +600,22 @@ __global__ void __launch_bounds__(kMainThreads, 1)
     const int b = (blockIdx.x % BH) / p.HK;
     const int kh = blockIdx.x % p.HK;
     const int k0 = kt * kKeys;
-    const int nrt = (p.SQ + kBRows - 1) / kBRows;
-    const int r_first = p.causal ? min(k0 / kBRows, nrt) : 0;
+    int nrt = (p.SQ + kBRows - 1) / kBRows;
+    int r_first = p.causal ? min(k0 / kBRows, nrt) : 0;
+    int pl = 0;
+    if constexpr (kMod) {
+        // a key of the prefix is seen by every row; others only within the window
+        pl = vjp_prefix(p, b);
+        if (k0 < pl) {
+            r_first = 0;
+        } else {
+            if (p.window < p.SQ)  // rows up to the last key's window (no overflow: both below 2^31 - 256)
+                nrt = min(nrt, static_cast<int>((static_cast<int64_t>(k0) + kKeys - 1 + p.window + kBRows - 1) / kBRows));
+            if (!p.causal)
+                r_first = max(k0 - p.window + 1, 0) / kBRows;
+            r_first = min(r_first, nrt);
+        }
+    }
     const int per_head = nrt - r_first;
     const int n = per_head * p.groups;
     const uint64_t wait_ns = p.wait_ns;
@@ -717,10 +836,65 @@ __global__ void __launch_bounds__(kMainThreads, 1)
             const int rb = i0 + part * 32;  // first row of this thread's columns
             // no mask on this thread's block: every key real, every row real,
             // and (causal) the last key at or before the first row (warp-uniform)
-            const bool plain = keys_all && rb + 32 <= p.SQ && (!p.causal || k0 + kKeys - 1 <= rb);
+            bool plain = keys_all && rb + 32 <= p.SQ && (!p.causal || k0 + kKeys - 1 <= rb);
             const float4* l4 = reinterpret_cast<const float4*>(sStat + st * 256 + part * 32);
             const float4* d4 = reinterpret_cast<const float4*>(sStat + st * 256 + 128 + part * 32);
             float pv[32];
+            if constexpr (kMod) {
+                const float slope2 = p.slopes ? __ldg(p.slopes + h) * kVjpLog2e : 0.f;
+                // every row of the block sees every key of the tile, as far as the rule goes
+                const bool in_rule = k0 + kKeys <= pl ||
+                                     ((!p.causal || k0 + kKeys - 1 <= rb) && rb + 31 - k0 < p.window &&
+                                      (p.causal || k0 + kKeys - 1 - rb < p.window));
+                plain = keys_all && rb + 32 <= p.SQ && in_rule;
+                uint32_t w[16];
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    Cols16 x;
+                    tmem_ld16(x, tS + lane_off + part * 32 + hf * 16);
+                    const float f = p.cap_out != 0.f ? p.cap_in : p.scale_log2;
+                    float y[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        y[e] = __uint_as_float(x.r[e]) * f;
+                    float c = 1.f;
+                    if (p.cap_out != 0.f) {
+                        tanh_block(y);
+                        c = p.cap_out;
+                    }
+                    const float d0 = static_cast<float>(rb + hf * 16 - key);
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        const float4 l = l4[hf * 4 + q4];
+                        const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = 4 * q4 + e;
+                            const float bias = fmaf(-slope2, fabsf(d0 + static_cast<float>(j)), -lv[e]);
+                            pv[hf * 16 + j] = fast_exp2(fmaf(y[j], c, bias));
+                        }
+                    }
+                    if (!plain) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const int row = rb + hf * 16 + j;
+                            if (!(key_ok && row < p.SQ && vjp_seen(p, pl, row, key)))
+                                pv[hf * 16 + j] = 0.f;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        w[hf * 8 + e] = pack2<T>(pv[hf * 16 + 2 * e], pv[hf * 16 + 2 * e + 1]);
+                    // from here on p times the cap's factor
+                    if (p.cap_out != 0.f) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            pv[hf * 16 + j] *= fmaf(-y[j], y[j], 1.f);
+                    }
+                }
+                tmem_st16(w, tS + lane_off + part * 32);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            } else {
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 Cols16 x;
@@ -751,6 +925,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                     w[e] = pack2<T>(pv[2 * e], pv[2 * e + 1]);
                 tmem_st16(w, tS + lane_off + part * 32);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            }
             }
             tc_fence_before();
             __syncwarp();
@@ -873,8 +1048,10 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(bars.tmem), "r"(512) : "memory");
 }
 
-using StatsFn = void (*)(VjpParams, CUtensorMap, CUtensorMap);
-using MainFn = void (*)(VjpParams, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap);
+template <bool kMod>
+using StatsFn = void (*)(VjpParamsOf<kMod>, CUtensorMap, CUtensorMap);
+template <bool kMod>
+using MainFn = void (*)(VjpParamsOf<kMod>, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap);
 
 // [B * heads][rows][128] 16-bit as {64, 2, rows, B * heads}; box {64, 1, box_rows, 1}:
 // one 64-column half of box_rows rows of one head
@@ -894,14 +1071,8 @@ int encode_rows(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int 
                : PA_ERR_CUDA;
 }
 
-}  // namespace
-
-bool vjp_tc_supported(int dtype, int D, int groups, int mask_kind)
-{
-    return (dtype == PA_F16 || dtype == PA_BF16) && D == kD && groups >= 1 && mask_kind == 0;
-}
-
-int launch_vjp_tc(const VjpParams& p, int dtype, bool f32_out, cudaStream_t st, uint64_t* launches)
+template <bool kMod>
+int launch_tc(const VjpParamsOf<kMod>& p, int dtype, bool f32_out, cudaStream_t st, uint64_t* launches)
 {
     const CUtensorMapDataType dt =
         dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -915,7 +1086,7 @@ int launch_vjp_tc(const VjpParams& p, int dtype, bool f32_out, cudaStream_t st, 
             kmap = qmap;  // no key tile is ever loaded
         if (rc != PA_OK)
             return rc;
-        const StatsFn fn = bf ? vjp_stats_tc<__nv_bfloat16> : vjp_stats_tc<__half>;
+        const StatsFn<kMod> fn = bf ? vjp_stats_tc<__nv_bfloat16, kMod> : vjp_stats_tc<__half, kMod>;
         if (cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kStatsSmem) != cudaSuccess)
             return PA_ERR_CUDA;
@@ -947,11 +1118,11 @@ int launch_vjp_tc(const VjpParams& p, int dtype, bool f32_out, cudaStream_t st, 
         }
         if (rc != PA_OK)
             return rc;
-        MainFn fn;
+        MainFn<kMod> fn;
         if (bf)
-            fn = f32_out ? vjp_main_tc<__nv_bfloat16, float> : vjp_main_tc<__nv_bfloat16, __nv_bfloat16>;
+            fn = f32_out ? vjp_main_tc<__nv_bfloat16, float, kMod> : vjp_main_tc<__nv_bfloat16, __nv_bfloat16, kMod>;
         else
-            fn = f32_out ? vjp_main_tc<__half, float> : vjp_main_tc<__half, __half>;
+            fn = f32_out ? vjp_main_tc<__half, float, kMod> : vjp_main_tc<__half, __half, kMod>;
         if (cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kMainSmem) != cudaSuccess)
             return PA_ERR_CUDA;
@@ -964,6 +1135,23 @@ int launch_vjp_tc(const VjpParams& p, int dtype, bool f32_out, cudaStream_t st, 
         ++*launches;
     }
     return PA_OK;
+}
+
+}  // namespace
+
+bool vjp_tc_supported(int dtype, int D, int groups, int mask_kind)
+{
+    return (dtype == PA_F16 || dtype == PA_BF16) && D == kD && groups >= 1 && mask_kind == 0;
+}
+
+int launch_vjp_tc(const VjpParams& p, int dtype, bool f32_out, cudaStream_t st, uint64_t* launches)
+{
+    return launch_tc<false>(p, dtype, f32_out, st, launches);
+}
+
+int launch_vjp_tc_scored(const VjpScoredParams& p, int dtype, bool f32_out, cudaStream_t st, uint64_t* launches)
+{
+    return launch_tc<true>(p, dtype, f32_out, st, launches);
 }
 
 }  // namespace pa
