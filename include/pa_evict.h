@@ -35,9 +35,9 @@
  * PA_STATUS_BAD_LENGTH; a row whose source or destination block is outside the
  * pool is not moved and reported as PA_STATUS_BAD_BLOCK.
  *
- * Asynchronous on `stream`; the library keeps nothing.  Two calls that run at
- * the same time need a workspace each.  Returns PA_OK or, before anything is
- * launched, a PA_ERR_* code of pa_decode.h:
+ * Asynchronous on `stream`; the library keeps nothing and needs no workspace.
+ * Returns PA_OK or, before anything is launched, a PA_ERR_* code of
+ * pa_decode.h:
  *   PA_ERR_NULL_POINTER  a needed pointer is NULL
  *   PA_ERR_BAD_DIMS      a size < 1 (B < 0), keep_first or keep_last < 0,
  *                        keep_first + keep_last > budget, max_blocks * BLOCK
@@ -48,8 +48,7 @@
  *                        (KV * D elements) that is not a multiple of 16 bytes
  *                        or above 64 KB; B > 4096
  *   PA_ERR_ALIGNMENT     a cache not 16-byte aligned, another tensor not
- *                        4-byte aligned, a workspace not 256-byte aligned
- *   PA_ERR_WORKSPACE     workspace NULL or below pa_cache_evict_workspace_bytes
+ *                        4-byte aligned
  */
 #ifndef PA_EVICT_H
 #define PA_EVICT_H
@@ -72,15 +71,8 @@ typedef struct pa_evict_opts {
     int keep_last;
     const int32_t *dst_table; /* NULL: in place */
     int dst_max_blocks;       /* row stride of dst_table */
-    void *workspace;          /* device scratch, 256-byte aligned, contents ignored */
-    size_t workspace_bytes;
-    int *status;                      /* device int32 for PA_STATUS_* bits, or NULL */
-    unsigned long long wait_limit_ns; /* 0 = default (2 s): bound of every internal wait
-                                         (PA_STATUS_TIMEOUT; the caches are then undefined) */
+    int *status;              /* device int32 for PA_STATUS_* bits, or NULL */
 } pa_evict_opts;
-
-size_t pa_cache_evict_workspace_bytes(int B, int KV, int D, int max_blocks, int BLOCK, int budget,
-                                      int dtype);
 
 int pa_cache_evict(void *k_cache, void *v_cache, const int32_t *block_table,
                    const int32_t *seq_lens, const float *weights, int32_t *new_lens, int32_t *kept,

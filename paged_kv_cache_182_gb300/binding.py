@@ -105,10 +105,7 @@ class EvictOpts(ctypes.Structure):
         ("keep_last", ctypes.c_int),
         ("dst_table", ctypes.c_void_p),
         ("dst_max_blocks", ctypes.c_int),
-        ("workspace", ctypes.c_void_p),
-        ("workspace_bytes", ctypes.c_size_t),
         ("status", ctypes.c_void_p),
-        ("wait_limit_ns", ctypes.c_ulonglong),
     ]
 
 
@@ -195,8 +192,6 @@ def load(path: Path = LIBRARY) -> ctypes.CDLL:
     lib.pa_rotary.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, ctypes.POINTER(RotaryOpts), P]
     lib.pa_cache_evict.restype = I
     lib.pa_cache_evict.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, ctypes.POINTER(EvictOpts), P]
-    lib.pa_cache_evict_workspace_bytes.restype = ctypes.c_size_t
-    lib.pa_cache_evict_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
     lib.pa_cache_append.restype = I
     lib.pa_cache_append.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, P, P]
     return lib
@@ -257,8 +252,10 @@ def _ptr(t):
 
 
 def _stream_handle(stream):
+    # the raw handle of torch's current stream: building a Stream object costs
+    # as much host time as the launch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -1105,14 +1102,11 @@ class EvictPlan:
                 raise ValueError("all tensors must be CUDA tensors on one device")
             if not t.is_contiguous():
                 raise ValueError("all tensors must be contiguous")
-        need = int(LIB.pa_cache_evict_workspace_bytes(B, KV, D, maxb, BLOCK, budget, _DT[k_cache.dtype]))
-        self.workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
         self.opts = EvictOpts(
             max_blocks=maxb, num_blocks=NB, dtype=_DT[k_cache.dtype], budget=budget,
             keep_first=int(keep_first), keep_last=int(keep_last),
             dst_table=None if dst_table is None else dst_table.data_ptr(),
             dst_max_blocks=0 if dst_table is None else int(dst_table.shape[1]),
-            workspace=self.workspace.data_ptr(), workspace_bytes=need,
             status=None if status is None else status.data_ptr())
         self.device = dev
         self._keep = (tensors, dst_table, status)

@@ -11,13 +11,17 @@
 //   warp owns a contiguous range of tokens, the ranges' counts are summed
 //   over warps and CTAs, and ballots place the tokens inside a range.
 //
-// pa_evict_move -- the rows.  kept[r] >= r, so a destination slot is either
-//   unmoved or the source of a lower or equal rank: an item (sequence, run of
-//   ranks, K or V) reads all of its rows into shared memory, raises its flag,
-//   and writes them once the items whose sources it overwrites have raised
-//   theirs.  Those items have lower ranks, items are dealt in rank order by a
-//   ticket, and reading never waits, so every wait ends.  Into fresh blocks
-//   there is nothing to wait for.
+// The rows then move by one of two kernels:
+//
+// pa_evict_shift (in place) -- kept[r] >= r, so a destination slot is either
+//   unmoved or the source of a lower or equal rank.  A CTA owns a slice of the
+//   columns of one sequence's K or V and walks the ranks in order, several
+//   runs of rows in flight: a run is written when it and all runs before it
+//   have been read, which is all that the overlap asks for, and no CTA waits
+//   for another.
+//
+// pa_evict_gather (into other blocks) -- nothing overlaps: one CTA per run of
+//   whole rows.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -32,12 +36,12 @@
 namespace pa {
 namespace {
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kKeys = 8;            // weights in flight per thread of the selection
 constexpr int kMoveThreads = 256;
-constexpr int kMoveBytes = 32768;   // rows of one item, at most (one row when longer)
-constexpr int kMoveRows = 256;      // rows of one item, at most
+constexpr int kRun = 128;           // in place: rows of a run
+constexpr int kMoveBytes = 32768;   // other blocks: rows of one item, at most (one row when longer)
+constexpr int kMoveRows = 256;
 constexpr int kMaxRowBytes = 65536;
 constexpr unsigned kAll32 = 0xffffffffu;
 
@@ -50,14 +54,12 @@ struct EvictParams {
     int32_t* new_lens;
     int32_t* kept;
     float* weights_out;
-    int* ticket;             // workspace: ticket, then the items' flags
-    int* flags;
     int* status;
-    unsigned long long wait_ns;
     int B, BLOCK, maxb, dst_maxb, num_blocks, budget, first, last, in_place;
     int cap;                 // max_blocks * BLOCK
     int row_bytes;           // KV * D * element bytes
-    int rows_item, chunks;   // ranks per item, items per sequence and pool
+    int rows_item;           // other blocks: rows per item
+    int slices;              // in place: column slices of a row
 };
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -86,6 +88,13 @@ __device__ __forceinline__ uint32_t cluster_load(const uint32_t* p, uint32_t ran
     return v;
 }
 
+// Exclusive sum of v[0 .. n-1] below `warp` (n at most 32, the same in every lane).
+__device__ __forceinline__ uint32_t sum_below(const uint32_t* v, int stride, int n, int warp)
+{
+    const int lane = threadIdx.x & 31;
+    return __reduce_add_sync(kAll32, lane < n && lane < warp ? v[lane * stride] : 0u);
+}
+
 // Unsigned integers in the order of the weights: NaN lowest, -0 equal to 0.
 __device__ __forceinline__ uint32_t order_of(float w)
 {
@@ -105,30 +114,46 @@ __device__ __forceinline__ int clamped_len(const EvictParams& p, int b, bool rep
     return n < 0 ? 0 : p.cap;
 }
 
-template <int C>
-__global__ void __launch_bounds__(kSelThreads) pa_evict_select(const __grid_constant__ EvictParams p)
+// T threads a CTA, C CTAs a cluster.
+template <int T, int C>
+__global__ void __launch_bounds__(T) pa_evict_select(const __grid_constant__ EvictParams p)
 {
+    constexpr int kSelThreads = T, kSelWarps = T / 32, kOwn = kBins / T;
     __shared__ uint32_t hist[2][kBins];
     __shared__ uint32_t wsum[kSelWarps];
     __shared__ uint32_t pick[3];               // chosen digit, still needed in it, its count
     __shared__ uint32_t cnt[kSelWarps][2];     // tokens taken outright / at the threshold, by warp
     __shared__ uint32_t tot[2];                // the same of the CTA
+    grid_dependents_launch();  // the move waits for this grid before it reads the kept list
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = C == 1 ? 0 : static_cast<int>(cluster_rank());
     const int b = blockIdx.x / C;
     const int step = C * kSelThreads, me = rank * kSelThreads + tid;
-    const int n = clamped_len(p, b, me == 0);
     const float* w = p.weights + static_cast<int64_t>(b) * p.cap;
+    // This CTA's and warp's tokens: contiguous ranges of the table's capacity, in
+    // token order, so that the weights are on their way before the length is
+    // known.  A warp's batch is kKeys * 32 weights, loaded together; ranges of one
+    // batch stay in registers, longer ones are read again in every pass.
+    const int per = (p.cap + C - 1) / C;
+    const int sub = ((per + kSelWarps - 1) / kSelWarps + 31) & ~31;
+    const int64_t first_j = static_cast<int64_t>(rank) * per + static_cast<int64_t>(warp) * sub;
+    int w0 = static_cast<int>(min(first_j, static_cast<int64_t>(p.cap)));
+    int w1 = min(w0 + min(sub, max(0, per - warp * sub)), p.cap);
+    float x[kKeys];
+    auto load = [&](int base) {
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u) {
+            const int j = base + u * 32 + lane;
+            x[u] = j < w1 ? __ldg(w + j) : 0.f;
+        }
+    };
+    const bool resident = sub <= kKeys * 32;
+    if (resident)
+        load(w0);
+    const int n = clamped_len(p, b, me == 0);
     float* wo = p.weights_out + static_cast<int64_t>(b) * p.cap;
     int32_t* kept = p.kept + static_cast<int64_t>(b) * p.budget;
 
-    if (p.in_place) {
-        // the move's flags and ticket start at zero
-        for (int i = me; i < 2 * p.chunks; i += step)
-            p.flags[static_cast<int64_t>(b) * 2 * p.chunks + i] = 0;
-        if (b == 0 && me == 0)
-            *p.ticket = 0;
-    }
     const int m = min(n, p.budget);
     if (me == 0)
         p.new_lens[b] = m;
@@ -153,11 +178,10 @@ __global__ void __launch_bounds__(kSelThreads) pa_evict_select(const __grid_cons
     }
     if (need == 0)
         return;
-    // this CTA's and warp's tokens: contiguous ranges in token order
-    const int per = (hi - lo + C - 1) / C;
-    const int c0 = min(lo + rank * per, hi), c1 = min(c0 + per, hi);
-    const int sub = ((c1 - c0 + kSelWarps - 1) / kSelWarps + 31) & ~31;
-    const int w0 = min(c0 + warp * sub, c1), w1 = min(w0 + sub, c1);
+    // of them, the tokens to choose from: [lo, hi)
+    const int batch0 = w0;
+    w1 = min(w1, hi);
+    const int j_lo = max(w0, lo);
 
     // taken: order >= t_ge, and of those with order == t_eq the first n_eq
     uint32_t prefix = 0, mask = 0, t_ge = 0, t_eq = 0, n_eq = 0;
@@ -169,26 +193,30 @@ __global__ void __launch_bounds__(kSelThreads) pa_evict_select(const __grid_cons
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const uint32_t digits = pass == 2 ? 1023u : 2047u;
         uint32_t* h = hist[pass & 1];
-        for (int j0 = w0; j0 < w1; j0 += 32) {
-            const int j = j0 + lane;
-            const uint32_t key = j < w1 ? order_of(__ldg(w + j)) : 0u;
-            const bool in = j < w1 && (key & mask) == prefix;
-            // one addition per distinct digit of the warp: accumulated weights
-            // crowd into few digits
-            const uint32_t d = in ? (key >> shift) & digits : 0xffffffffu;
-            const uint32_t same = __match_any_sync(kAll32, d);
-            if (in && (same & ((1u << lane) - 1)) == 0)
-                atomicAdd(&h[d], static_cast<uint32_t>(__popc(same)));
+        for (int base = batch0; base < w1; base += kKeys * 32) {
+            if (!resident)
+                load(base);
+#pragma unroll
+            for (int u = 0; u < kKeys; ++u) {
+                const int j = base + u * 32 + lane;
+                const uint32_t key = order_of(x[u]);
+                const bool in = j >= j_lo && j < w1 && (key & mask) == prefix;
+                // weights crowd into few digits, but counting up by one is
+                // combined within the warp by the hardware: aggregating equal
+                // digits by hand (match, then one add) took twice as long
+                if (in)
+                    atomicAdd(&h[(key >> shift) & digits], 1u);
+            }
         }
         if (C > 1)
             cluster_sync();
         else
             __syncthreads();
-        // four bins a thread, from the top
-        uint32_t v[4], sum = 0;
-        const int top = kBins - 1 - 4 * tid;
+        // kOwn bins a thread, from the top
+        uint32_t v[kOwn], sum = 0;
+        const int top = kBins - 1 - kOwn * tid;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kOwn; ++i) {
             v[i] = 0;
             if (C == 1) {
                 v[i] = h[top - i];
@@ -209,13 +237,11 @@ __global__ void __launch_bounds__(kSelThreads) pa_evict_select(const __grid_cons
         if (lane == 31)
             wsum[warp] = incl;
         __syncthreads();
-        uint32_t before = incl - sum;
-        for (int i = 0; i < warp; ++i)
-            before += wsum[i];
+        const uint32_t before = incl - sum + sum_below(wsum, 1, kSelWarps, warp);
         if (before < k && k <= before + sum) {
             uint32_t at = before;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kOwn; ++i) {
                 if (at < k && k <= at + v[i]) {
                     pick[0] = static_cast<uint32_t>(top - i);
                     pick[1] = k - at;
@@ -247,10 +273,17 @@ __global__ void __launch_bounds__(kSelThreads) pa_evict_select(const __grid_cons
 
     // counts of the ranges, then the places
     uint32_t ge = 0, eq = 0;
-    for (int j = w0 + lane; j < w1; j += 32) {
-        const uint32_t key = order_of(__ldg(w + j));
-        ge += key >= t_ge;
-        eq += n_eq > 0 && key == t_eq;
+    for (int base = batch0; base < w1; base += kKeys * 32) {
+        if (!resident)
+            load(base);
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u) {
+            const int j = base + u * 32 + lane;
+            const bool in = j >= j_lo && j < w1;
+            const uint32_t key = order_of(x[u]);
+            ge += in && key >= t_ge;
+            eq += in && n_eq > 0 && key == t_eq;
+        }
     }
     ge = __reduce_add_sync(kAll32, ge);
     eq = __reduce_add_sync(kAll32, eq);
@@ -259,96 +292,168 @@ __global__ void __launch_bounds__(kSelThreads) pa_evict_select(const __grid_cons
         cnt[warp][1] = eq;
     }
     __syncthreads();
-    if (tid < 2) {
-        uint32_t s = 0;
-        for (int i = 0; i < kSelWarps; ++i)
-            s += cnt[i][tid];
-        tot[tid] = s;
-    }
-    if (C > 1)
+    uint32_t bge = sum_below(&cnt[0][0], 2, kSelWarps, warp), beq = sum_below(&cnt[0][1], 2, kSelWarps, warp);
+    if (C > 1) {
+        if (tid == kSelThreads - 1) {
+            tot[0] = bge + ge;  // the last warp's: all of the CTA's
+            tot[1] = beq + eq;
+        }
         cluster_sync();
-    uint32_t bge = 0, beq = 0;
-    for (int c = 0; c < rank; ++c) {
-        bge += cluster_load(&tot[0], c);
-        beq += cluster_load(&tot[1], c);
-    }
-    for (int i = 0; i < warp; ++i) {
-        bge += cnt[i][0];
-        beq += cnt[i][1];
+        for (int c = 0; c < rank; ++c) {
+            bge += cluster_load(&tot[0], c);
+            beq += cluster_load(&tot[1], c);
+        }
     }
     const uint32_t below = (1u << lane) - 1;
-    for (int j0 = w0; j0 < w1; j0 += 32) {
-        const int j = j0 + lane;
-        const float x = j < w1 ? __ldg(w + j) : 0.f;
-        const uint32_t key = order_of(x);
-        const bool is_ge = j < w1 && key >= t_ge, is_eq = j < w1 && n_eq > 0 && key == t_eq;
-        const uint32_t mg = __ballot_sync(kAll32, is_ge), me_ = __ballot_sync(kAll32, is_eq);
-        const uint32_t g = bge + __popc(mg & below), e = beq + __popc(me_ & below);
-        if (is_ge || (is_eq && e < n_eq)) {
-            const int r = p.first + static_cast<int>(g + min(e, n_eq));
-            kept[r] = j;
-            wo[r] = x;
+    for (int base = batch0; base < w1; base += kKeys * 32) {
+        if (!resident)
+            load(base);
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u) {
+            const int j = base + u * 32 + lane;
+            const uint32_t key = order_of(x[u]);
+            const bool in = j >= j_lo && j < w1;
+            const bool is_ge = in && key >= t_ge, is_eq = in && n_eq > 0 && key == t_eq;
+            const uint32_t mg = __ballot_sync(kAll32, is_ge), me_ = __ballot_sync(kAll32, is_eq);
+            const uint32_t g = bge + __popc(mg & below), e = beq + __popc(me_ & below);
+            if (is_ge || (is_eq && e < n_eq)) {
+                const int r = p.first + static_cast<int>(g + min(e, n_eq));
+                kept[r] = j;
+                wo[r] = x[u];
+            }
+            bge += __popc(mg);
+            beq += __popc(me_);
         }
-        bge += __popc(mg);
-        beq += __popc(me_);
     }
     if (C > 1)
         cluster_sync();  // the others have read this CTA's shared memory
 }
 
-__device__ __forceinline__ int load_acquire(const int* p)
+// Slot of token j by a table row, or -1 (reported) when its block is outside the pool.
+__device__ __forceinline__ int slot_of(const EvictParams& p, int phys, int j, bool report)
 {
-    int v;
-    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
+    if (phys >= 0 && phys < p.num_blocks)
+        return phys * p.BLOCK + j % p.BLOCK;
+    if (report && p.status)
+        atomicOr(p.status, PA_STATUS_BAD_BLOCK);
+    return -1;
 }
 
-__device__ __forceinline__ void store_release(int* p, int v)
+// grid (slices * 2, B): a slice of VS 16-byte vectors of K or V of a sequence.
+// Thread t < kRun looks up the rows of a run, three steps ahead of their copy:
+// kept index, then table entries, then slots.
+template <int VS, int S>
+__global__ void __launch_bounds__(kMoveThreads) pa_evict_shift(const __grid_constant__ EvictParams p)
 {
-    asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+    extern __shared__ __align__(16) unsigned char ring[];  // [S runs][kRun rows][VS vectors]
+    __shared__ int src[2][kRun], dst[S + 1][kRun];
+    const int tid = threadIdx.x;
+    const int kv = blockIdx.x & 1, slice = blockIdx.x >> 1, b = blockIdx.y;
+    const int n = clamped_len(p, b, false);
+    grid_dependency_wait();  // the kept list
+    if (n <= p.budget)
+        return;
+    const int runs = (p.budget + kRun - 1) / kRun;
+    const int32_t* kept = p.kept + static_cast<int64_t>(b) * p.budget;
+    const int32_t* table = p.table + static_cast<int64_t>(b) * p.maxb;
+    const bool report = blockIdx.x == 0;
+    const int v0 = slice * VS, nv = min(VS, (p.row_bytes >> 4) - v0);  // vectors of this slice
+    unsigned char* pool = p.pool[kv] + v0 * 16;
+    const int v = tid % VS, rr = tid / VS;
+    constexpr int kStep = kMoveThreads / VS;  // rows the CTA copies at once
+
+    int j1 = -1, j2 = -1, ps = -1, pd = -1;  // the run three and two ahead: kept; its entries
+    auto fetch_kept = [&](int run) {
+        const int r = run * kRun + tid;
+        j1 = tid < kRun && r < p.budget ? kept[r] : -1;
+    };
+    auto fetch_entries = [&](int run) {
+        j2 = j1;
+        if (j2 >= 0) {
+            ps = __ldg(table + j2 / p.BLOCK);
+            pd = __ldg(table + (run * kRun + tid) / p.BLOCK);
+        }
+    };
+    auto put_slots = [&](int run) {
+        if (tid < kRun) {
+            const int r = run * kRun + tid;
+            int s = -1, d = -1;
+            if (j2 >= 0 && j2 != r) {
+                s = slot_of(p, ps, j2, report);
+                d = slot_of(p, pd, r, report);
+            }
+            src[run & 1][tid] = d < 0 ? -1 : s;
+            dst[run % (S + 1)][tid] = s < 0 ? -1 : d;
+        }
+    };
+    auto issue = [&](int run) {  // reads of a run
+        if (v < nv) {
+#pragma unroll
+            for (int k = 0; k < kRun / kStep; ++k) {
+                const int row = rr + k * kStep;
+                const int s = src[run & 1][row];
+                if (s >= 0)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                     smem_u32(ring + (((run % S) * kRun + row) * VS + v) * 16)),
+                                 "l"(pool + static_cast<int64_t>(s) * p.row_bytes + v * 16)
+                                 : "memory");
+            }
+        }
+    };
+    fetch_kept(0);
+    fetch_entries(0);
+    fetch_kept(1);
+    for (int run = 0; run < runs + S - 1; ++run) {
+        // reads of `run`; writes of run - (S - 1)
+        if (run < runs) {
+            put_slots(run);
+            fetch_entries(run + 1);
+            fetch_kept(run + 2);
+        }
+        __syncthreads();  // the slots are there; the ring's run - S has been written out
+        if (run < runs)
+            issue(run);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        const int done = run - (S - 1);
+        if (done >= 0) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+            __syncthreads();  // run `done` has been read by every thread, and all before it
+            if (v < nv) {
+#pragma unroll
+                for (int k = 0; k < kRun / kStep; ++k) {
+                    const int row = rr + k * kStep;
+                    const int d = dst[done % (S + 1)][row];
+                    if (d >= 0)
+                        *reinterpret_cast<uint4*>(pool + static_cast<int64_t>(d) * p.row_bytes + v * 16) =
+                            *reinterpret_cast<const uint4*>(ring + (((done % S) * kRun + row) * VS + v) * 16);
+                }
+            }
+        }
+    }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) pa_evict_move(const __grid_constant__ EvictParams p)
+// grid (items of a sequence's rows * 2, B): whole rows of K or V.
+__global__ void __launch_bounds__(kMoveThreads) pa_evict_gather(const __grid_constant__ EvictParams p)
 {
     extern __shared__ __align__(16) unsigned char rows[];
-    __shared__ int s_item;
     __shared__ int src[kMoveRows], dst[kMoveRows];
     const int tid = threadIdx.x;
-    int item = blockIdx.x;
-    if (p.in_place) {
-        if (tid == 0)
-            s_item = atomicAdd(p.ticket, 1);
-        __syncthreads();
-        item = s_item;
-    }
-    // ranks slowest: an item's predecessors were dealt long before it
-    const int kv = item & 1;
-    const int c = (item >> 1) / p.B, b = (item >> 1) - c * p.B;
-    const int n = clamped_len(p, b, false);
-    const int m = min(n, p.budget);
-    const int r0 = c * p.rows_item;
-    if (r0 >= m || (p.in_place && n <= p.budget))
-        return;  // nothing moves (and nothing is waited for: no source lies here)
+    const int kv = blockIdx.x & 1, b = blockIdx.y;
+    const int r0 = (blockIdx.x >> 1) * p.rows_item;
+    const int m = min(clamped_len(p, b, false), p.budget);
     const int nr = min(p.rows_item, m - r0);
+    grid_dependency_wait();  // the kept list
+    if (nr <= 0)
+        return;
     const int32_t* kept = p.kept + static_cast<int64_t>(b) * p.budget;
-    int* flag = p.flags + static_cast<int64_t>(b) * 2 * p.chunks + kv;
     const int32_t* table = p.table + static_cast<int64_t>(b) * p.maxb;
     const int32_t* to = p.dst + static_cast<int64_t>(b) * p.dst_maxb;
     for (int i = tid; i < nr; i += kMoveThreads) {
-        const int r = r0 + i, j = kept[r];
-        int s = -1, d = -1;
-        if (!p.in_place || j != r) {
-            const int ps = table[j / p.BLOCK], pd = to[r / p.BLOCK];
-            if (ps < 0 || ps >= p.num_blocks || pd < 0 || pd >= p.num_blocks) {
-                if (p.status)
-                    atomicOr(p.status, PA_STATUS_BAD_BLOCK);
-            } else {
-                s = ps * p.BLOCK + j % p.BLOCK;
-                d = pd * p.BLOCK + r % p.BLOCK;
-            }
-        }
-        src[i] = s;
-        dst[i] = d;
+        const int r = r0 + i;
+        const int pd = __ldg(to + r / p.BLOCK), j = kept[r];
+        const int s = slot_of(p, __ldg(table + j / p.BLOCK), j, kv == 0), d = slot_of(p, pd, r, kv == 0);
+        src[i] = d < 0 ? -1 : s;
+        dst[i] = s < 0 ? -1 : d;
     }
     __syncthreads();
     const int vpr = p.row_bytes >> 4;
@@ -362,37 +467,7 @@ __global__ void __launch_bounds__(kMoveThreads) pa_evict_move(const __grid_const
                          : "memory");
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
-    if (p.in_place) {
-        if (tid == 0) {
-            __threadfence();
-            store_release(flag + 2 * c, 1);
-            // ranks whose sources are this item's destinations r0 .. r0 + nr - 1:
-            // kept ascends and kept[r] >= r, so they lie in [lo, r0 + nr)
-            int lo = 0, up = r0;  // first rank with kept >= r0
-            while (lo < up) {
-                const int mid = (lo + up) >> 1;
-                if (kept[mid] >= r0)
-                    up = mid;
-                else
-                    lo = mid + 1;
-            }
-            bool ok = true;
-            const uint64_t start = global_timer_ns();
-            for (int k = lo / p.rows_item; k < c && ok; ++k)
-                while (load_acquire(flag + 2 * k) == 0)
-                    if (global_timer_ns() - start > p.wait_ns) {
-                        ok = false;
-                        break;
-                    }
-            if (!ok && p.status)
-                atomicOr(p.status, PA_STATUS_TIMEOUT);
-            s_item = ok;
-        }
-        __syncthreads();
-        if (!s_item)
-            return;
-    }
+    // every thread writes what it has read itself
     for (int i = tid; i < total; i += kMoveThreads) {
         const int r = i / vpr, v = i - r * vpr;
         if (dst[r] >= 0)
@@ -405,14 +480,6 @@ int rows_per_item(int row_bytes)
 {
     int r = kMoveBytes / row_bytes;
     return r < 1 ? 1 : r > kMoveRows ? kMoveRows : r;
-}
-
-// ticket (256 bytes) | flags [B][chunks][2]
-size_t evict_workspace(int B, int row_bytes, int cap, int budget)
-{
-    const int m = budget < cap ? budget : cap;
-    const int chunks = (m + rows_per_item(row_bytes) - 1) / rows_per_item(row_bytes);
-    return 256 + static_cast<size_t>(B) * 2 * chunks * sizeof(int);
 }
 
 bool a4(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 3) == 0; }
@@ -444,14 +511,6 @@ int evict_sizes(int B, int KV, int D, int max_blocks, int BLOCK, int budget, int
 
 using namespace pa;
 
-extern "C" size_t pa_cache_evict_workspace_bytes(int B, int KV, int D, int max_blocks, int BLOCK, int budget, int dtype)
-{
-    int rb, cap;
-    if (evict_sizes(B, KV, D, max_blocks, BLOCK, budget, dtype, &rb, &cap) != PA_OK || B == 0)
-        return 0;
-    return evict_workspace(B, rb, cap, budget);
-}
-
 extern "C" int pa_cache_evict(void* k_cache, void* v_cache, const int32_t* block_table, const int32_t* seq_lens,
                               const float* weights, int32_t* new_lens, int32_t* kept, float* weights_out, int B, int KV,
                               int D, int BLOCK, const pa_evict_opts* opts, void* stream)
@@ -475,11 +534,6 @@ extern "C" int pa_cache_evict(void* k_cache, void* v_cache, const int32_t* block
     if ((reinterpret_cast<uintptr_t>(k_cache) & 15) || (reinterpret_cast<uintptr_t>(v_cache) & 15) || !a4(block_table) ||
         !a4(seq_lens) || !a4(weights) || !a4(new_lens) || !a4(kept) || !a4(weights_out) || !a4(o.dst_table))
         return PA_ERR_ALIGNMENT;
-    const size_t need = evict_workspace(B, rb, cap, o.budget);
-    if (!o.workspace || o.workspace_bytes < need)
-        return PA_ERR_WORKSPACE;
-    if (reinterpret_cast<uintptr_t>(o.workspace) & 255)
-        return PA_ERR_ALIGNMENT;
     const size_t pool = static_cast<size_t>(o.num_blocks) * BLOCK * rb;
     const struct {
         const void* x;
@@ -490,12 +544,11 @@ extern "C" int pa_cache_evict(void* k_cache, void* v_cache, const int32_t* block
                {new_lens, static_cast<size_t>(B) * 4, true},
                {kept, static_cast<size_t>(B) * o.budget * 4, true},
                {weights_out, static_cast<size_t>(B) * cap * 4, true},
-               {o.workspace, need, true},
                {block_table, static_cast<size_t>(B) * o.max_blocks * 4, false},
                {seq_lens, static_cast<size_t>(B) * 4, false},
                {weights, static_cast<size_t>(B) * cap * 4, false},
                {o.dst_table, o.dst_table ? static_cast<size_t>(B) * o.dst_max_blocks * 4 : 0, false}};
-    for (int i = 0; i < 10; ++i)
+    for (int i = 0; i < 9; ++i)
         for (int j = 0; j < i; ++j)
             if ((all[i].written || all[j].written) && overlap(all[i].x, all[i].bytes, all[j].x, all[j].bytes))
                 return PA_ERR_BAD_DIMS;
@@ -510,10 +563,7 @@ extern "C" int pa_cache_evict(void* k_cache, void* v_cache, const int32_t* block
     p.new_lens = new_lens;
     p.kept = kept;
     p.weights_out = weights_out;
-    p.ticket = static_cast<int*>(o.workspace);
-    p.flags = p.ticket + 64;
     p.status = o.status;
-    p.wait_ns = o.wait_limit_ns ? o.wait_limit_ns : kWaitLimitNs;
     p.B = B;
     p.BLOCK = BLOCK;
     p.maxb = o.max_blocks;
@@ -526,15 +576,17 @@ extern "C" int pa_cache_evict(void* k_cache, void* v_cache, const int32_t* block
     p.cap = cap;
     p.row_bytes = rb;
     p.rows_item = rows_per_item(rb);
-    p.chunks = (m + p.rows_item - 1) / p.rows_item;
-    const long long items = 2ll * p.chunks * B;
-    if (items >= (1ll << 31))
-        return PA_ERR_BAD_DIMS;
-    const size_t smem = static_cast<size_t>(p.rows_item) * rb;
 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // one CTA of a cluster per 4096 tokens of capacity, at most 8
-    const int C = cap <= 4096 ? 1 : cap <= 16384 ? 4 : 8;
+    // short sequences: a CTA of 256 threads holds 2048 weights in registers;
+    // else 1024 threads and 8192, and a cluster of up to 8 of them
+    const bool small = cap <= 2048;
+    const int C = cap <= 8192 ? 1 : cap <= 16384 ? 2 : cap <= 32768 ? 4 : 8;
+    const void* sel = small    ? reinterpret_cast<const void*>(pa_evict_select<256, 1>)
+                      : C == 1 ? reinterpret_cast<const void*>(pa_evict_select<1024, 1>)
+                      : C == 2 ? reinterpret_cast<const void*>(pa_evict_select<1024, 2>)
+                      : C == 4 ? reinterpret_cast<const void*>(pa_evict_select<1024, 4>)
+                               : reinterpret_cast<const void*>(pa_evict_select<1024, 8>);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = C;
@@ -542,22 +594,42 @@ extern "C" int pa_cache_evict(void* k_cache, void* v_cache, const int32_t* block
     attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(B) * C);
-    cfg.blockDim = dim3(kSelThreads);
+    cfg.blockDim = dim3(small ? 256 : 1024);
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = C > 1 ? 1 : 0;
     void* args[1] = {&p};
-    const void* sel = C == 1   ? reinterpret_cast<const void*>(pa_evict_select<1>)
-                      : C == 4 ? reinterpret_cast<const void*>(pa_evict_select<4>)
-                               : reinterpret_cast<const void*>(pa_evict_select<8>);
-    const void* move = reinterpret_cast<const void*>(pa_evict_move);
+    // The move sets up while the selection runs.  In place, about 96 KB of rows in
+    // flight per CTA: slices of 128 bytes, or of 64 where those would leave SMs
+    // idle (half a memory burst wastes nothing, but a row's bytes are fetched apart).
+    const void* move;
+    size_t smem;
+    dim3 grid;
+    if (p.in_place) {
+        const bool narrow = 2ll * B * ((rb + 127) / 128) < 152;
+        p.slices = narrow ? (rb + 63) / 64 : (rb + 127) / 128;
+        grid = dim3(2u * p.slices, static_cast<unsigned>(B));
+        move = narrow ? reinterpret_cast<const void*>(pa_evict_shift<4, 12>) : reinterpret_cast<const void*>(pa_evict_shift<8, 6>);
+        smem = narrow ? 12 * kRun * 64 : 6 * kRun * 128;
+    } else {
+        grid = dim3(2u * ((m + p.rows_item - 1) / p.rows_item), static_cast<unsigned>(B));
+        move = reinterpret_cast<const void*>(pa_evict_gather);
+        smem = static_cast<size_t>(p.rows_item) * rb;
+    }
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(move, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return PA_ERR_CUDA;
     if (cudaLaunchKernelExC(&cfg, sel, args) != cudaSuccess)
         return PA_ERR_CUDA;
-    pa_evict_move<<<static_cast<unsigned>(items), kMoveThreads, smem, st>>>(p);
-    if (cudaGetLastError() != cudaSuccess)
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelExC(&cfg, move, args) != cudaSuccess)
         return PA_ERR_CUDA;
     count_launches(2);
     return PA_OK;

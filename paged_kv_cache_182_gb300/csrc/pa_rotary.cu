@@ -6,8 +6,10 @@
 // more), three multiply-adds an element.  What it must not do is compute a
 // cosine and a sine per element: the angle depends on the position and the
 // pair alone, so a CTA takes a few positions of one sequence and all (or a
-// share) of their heads, and keeps the positions' cosines and sines in shared
-// memory.  The rows are in flight while the table is computed.
+// share) of their heads.  Its threads compute the positions' cosines and sines
+// together into shared memory; then each keeps those of its own 16 bytes of a
+// row in registers and walks the heads with them.  The first heads' rows are in
+// flight while the table is computed.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -26,7 +28,7 @@ namespace pa {
 namespace {
 
 constexpr int kRotThreads = 256;
-constexpr int kRotItems = 4;  // items in flight per thread
+constexpr int kRotHeads = 4;  // heads in flight per thread
 
 struct RotaryParams {
     const void* x[3];       // q, k, v
@@ -130,19 +132,21 @@ struct Vec<__nv_bfloat16> {
 };
 
 // How the 16-byte vectors of a row meet their pairs:
-//   kHalves  rot / 2 is whole vectors: an item is vector i of the first half
-//            and the one rot / 2 columns on, then the untouched vectors, one
-//            an item
-//   kSide    interleaved pairs: an item is one vector, its pairs inside it
-//   kAny     halves of any other length: an item is one vector, its elements'
-//            partners read one at a time (they are in the same row, so in the
-//            lines that the vectors fetch)
+//   kHalves  rot / 2 is whole vectors: a thread takes vector i of the first half
+//            and the one rot / 2 columns on, or one of the untouched vectors
+//   kSide    interleaved pairs: a thread takes one vector, its pairs inside it
+//   kAny     halves of any other length: a thread takes one vector, its
+//            elements' partners read one at a time (they are in the same row,
+//            so in the lines that the vectors fetch)
 enum { kHalves = 0, kSide = 1, kAny = 2 };
 
+// Thread t of a CTA: unit t % units (row, vector), head group t / units.
 template <typename T, int MODE>
 __global__ void __launch_bounds__(kRotThreads) pa_rotary_kernel(const __grid_constant__ RotaryParams p)
 {
     constexpr int V = Vec<T>::n;
+    constexpr int NP = MODE == kSide ? V / 2 : V;  // pairs of a thread
+    constexpr int U = kRotHeads;
     // a kernel launched after this one with programmatic launch may set up
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ float2 tab[];  // [rows_cta][rot / 2] (cos, sin)
@@ -151,69 +155,85 @@ __global__ void __launch_bounds__(kRotThreads) pa_rotary_kernel(const __grid_con
     const int b = blockIdx.x / chunks;
     const int n0 = (blockIdx.x - b * chunks) * p.rows_cta;
     const int rows = min(p.rows_cta, p.N - n0);
-    const int h0 = blockIdx.y * p.head_cta;
-    const int nh = min(p.head_cta, p.heads - h0);
-    const int per_row = MODE == kHalves ? (p.D - half) / V : p.D / V;  // items of one row of one head
-    const int pairs = MODE == kHalves ? half / V : 0;                  // of them, two-vector items
-    const int total = nh * rows * per_row;
+    const int per_row = MODE == kHalves ? (p.D - half) / V : p.D / V;
+    const int units = p.rows_cta * per_row;
+    const int groups = kRotThreads / units;
+    const int unit = threadIdx.x % units, group = threadIdx.x / units;
+    const int row = unit / per_row, v = unit - row * per_row;
+    const bool live = group < groups && row < rows;
+    const bool two = MODE == kHalves && v < half / V;
+    const int col = MODE == kHalves && !two ? v * V + half : v * V;
+    const int n = n0 + row;
+    const int h1 = min(p.heads, (static_cast<int>(blockIdx.y) + 1) * p.head_cta);
+    int h = blockIdx.y * p.head_cta + group;
 
-    for (int base = 0; base < total; base += kRotThreads * kRotItems) {
-        uint4 a[kRotItems], c[kRotItems];
-        int tens[kRotItems], hh[kRotItems], rr[kRotItems], vv[kRotItems];
+    auto source = [&](int head) {
+        const int t = head < p.H ? 0 : head < p.H + p.KV ? 1 : 2;
+        const int hl = t == 0 ? head : t == 1 ? head - p.H : head - p.H - p.KV;
+        return static_cast<const T*>(p.x[t]) + b * p.st[t][0] + hl * p.st[t][1] + n * p.st[t][2];
+    };
+    uint4 a[U], c[U];
+    auto load = [&]() {
 #pragma unroll
-        for (int u = 0; u < kRotItems; ++u) {
-            const int i = base + u * kRotThreads + static_cast<int>(threadIdx.x);
-            tens[u] = -1;
-            if (i < total) {
-                const int hr = i / per_row;
-                vv[u] = i - hr * per_row;
-                const int hl = hr / rows;
-                rr[u] = hr - hl * rows;
-                int h = h0 + hl;
-                tens[u] = 0;
-                if (h >= p.H) {
-                    h -= p.H;
-                    tens[u] = 1;
-                    if (h >= p.KV) {
-                        h -= p.KV;
-                        tens[u] = 2;
-                    }
-                }
-                hh[u] = h;
-                const T* row = static_cast<const T*>(p.x[tens[u]]) + b * p.st[tens[u]][0] + h * p.st[tens[u]][1] +
-                               (n0 + rr[u]) * p.st[tens[u]][2];
-                const int col = MODE == kHalves && vv[u] >= pairs ? vv[u] * V + half : vv[u] * V;
-                a[u] = __ldg(reinterpret_cast<const uint4*>(row + col));
-                if (MODE == kHalves && vv[u] < pairs)
-                    c[u] = __ldg(reinterpret_cast<const uint4*>(row + col + half));
+        for (int u = 0; u < U; ++u) {
+            const int head = h + u * groups;
+            if (live && head < h1) {
+                const T* x = source(head) + col;
+                a[u] = __ldg(reinterpret_cast<const uint4*>(x));
+                if (two)
+                    c[u] = __ldg(reinterpret_cast<const uint4*>(x + half));
             }
         }
-        if (base == 0) {
-            // the positions' table, while the first rows are in flight
-            for (int i = threadIdx.x; i < rows * half; i += kRotThreads) {
-                const int r = i / half, j = i - r * half;
-                tab[i] = turn(__ldg(p.positions + static_cast<long long>(b) * p.N + n0 + r), __ldg(p.table + j),
-                              p.factor, p.inverse);
-            }
-            __syncthreads();
+    };
+    load();
+    for (int i = threadIdx.x; i < rows * half; i += kRotThreads) {
+        const int r = i / half;
+        tab[i] = turn(__ldg(p.positions + static_cast<int64_t>(b) * p.N + n0 + r), __ldg(p.table + (i - r * half)), p.factor,
+                      p.inverse);
+    }
+    // the row's slot; -1: nothing is stored
+    int slot = -1;
+    if (p.slots && live) {
+        const int32_t* sl = p.slots + static_cast<int64_t>(b) * p.N;
+        slot = __ldg(sl + n);
+        if (slot < -1 || slot >= p.num_slots) {
+            if (p.status && v == 0 && group == 0 && blockIdx.y == 0)
+                atomicOr(p.status, PA_STATUS_BAD_SLOT);
+            slot = -1;
         }
+        for (int j = n + 1; slot >= 0 && j < p.N; ++j)
+            if (__ldg(sl + j) == slot)
+                slot = -1;  // a later row of this sequence lands there
+    }
+    __syncthreads();
+    float2 w[NP];
+    if (live) {
 #pragma unroll
-        for (int u = 0; u < kRotItems; ++u) {
-            if (tens[u] < 0)
+        for (int e = 0; e < NP; ++e) {
+            int i = MODE == kSide ? (col >> 1) + e : col + e;
+            if (MODE == kAny && i >= half)
+                i -= half;
+            // columns past rot: the identity, so that one loop serves all
+            w[e] = i < half && (MODE != kHalves || two) ? tab[row * half + i] : make_float2(1.f, 0.f);
+        }
+    }
+    for (; h < h1; h += U * groups) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int head = h + u * groups;
+            if (!live || head >= h1)
                 continue;
-            const int col = MODE == kHalves && vv[u] >= pairs ? vv[u] * V + half : vv[u] * V;
-            const bool two = MODE == kHalves && vv[u] < pairs;
-            if (tens[u] < 2) {
-                const float2* t = tab + rr[u] * half;
+            const int t = head < p.H ? 0 : head < p.H + p.KV ? 1 : 2;
+            const int hl = t == 0 ? head : t == 1 ? head - p.H : head - p.H - p.KV;
+            if (t < 2) {
                 if (two) {
                     float x[V], y[V];
                     Vec<T>::get(a[u], x);
                     Vec<T>::get(c[u], y);
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
-                        const float2 w = t[col + e];
-                        const float nx = x[e] * w.x - y[e] * w.y;
-                        y[e] = fmaf(x[e], w.y, y[e] * w.x);
+                        const float nx = x[e] * w[e].x - y[e] * w[e].y;
+                        y[e] = fmaf(x[e], w[e].y, y[e] * w[e].x);
                         x[e] = nx;
                     }
                     a[u] = Vec<T>::put(x);
@@ -222,56 +242,46 @@ __global__ void __launch_bounds__(kRotThreads) pa_rotary_kernel(const __grid_con
                     float x[V];
                     Vec<T>::get(a[u], x);
 #pragma unroll
-                    for (int e = 0; e < V; e += 2) {
-                        if (col + e < p.rot) {
-                            const float2 w = t[(col + e) >> 1];
-                            const float nx = x[e] * w.x - x[e + 1] * w.y;
-                            x[e + 1] = fmaf(x[e], w.y, x[e + 1] * w.x);
-                            x[e] = nx;
+                    for (int e = 0; e < V / 2; ++e)
+                        if (col + 2 * e < p.rot) {
+                            const float nx = x[2 * e] * w[e].x - x[2 * e + 1] * w[e].y;
+                            x[2 * e + 1] = fmaf(x[2 * e], w[e].y, x[2 * e + 1] * w[e].x);
+                            x[2 * e] = nx;
                         }
-                    }
                     a[u] = Vec<T>::put(x);
                 } else if (MODE == kAny && col < p.rot) {
-                    const T* row = static_cast<const T*>(p.x[tens[u]]) + b * p.st[tens[u]][0] + hh[u] * p.st[tens[u]][1] +
-                                   (n0 + rr[u]) * p.st[tens[u]][2];
+                    const T* xr = source(head);
                     float x[V];
                     Vec<T>::get(a[u], x);
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
                         const int i = col + e;
-                        if (i < half) {
-                            const float2 w = t[i];
-                            x[e] = x[e] * w.x - static_cast<float>(row[i + half]) * w.y;
-                        } else if (i < p.rot) {
-                            const float2 w = t[i - half];
-                            x[e] = fmaf(static_cast<float>(row[i - half]), w.y, x[e] * w.x);
-                        }
+                        if (i < half)
+                            x[e] = x[e] * w[e].x - static_cast<float>(xr[i + half]) * w[e].y;
+                        else if (i < p.rot)
+                            x[e] = fmaf(static_cast<float>(xr[i - half]), w[e].y, x[e] * w[e].x);
                     }
                     a[u] = Vec<T>::put(x);
                 }
-            }
-            long long at = ((static_cast<long long>(b) * (tens[u] == 0 ? p.H : p.KV) + hh[u]) * p.N + n0 + rr[u]) * p.D + col;
-            if (tens[u] < 2 && p.out[tens[u]]) {
-                T* o = static_cast<T*>(p.out[tens[u]]) + at;
-                *reinterpret_cast<uint4*>(o) = a[u];
-                if (two)
-                    *reinterpret_cast<uint4*>(o + half) = c[u];
-            }
-            if (tens[u] >= 1 && p.slots) {
-                const int32_t* sl = p.slots + static_cast<long long>(b) * p.N;
-                const int s = __ldg(sl + n0 + rr[u]);
-                bool store = s >= 0 && s < p.num_slots;
-                if (!store && s != -1 && p.status && tens[u] == 1 && hh[u] == 0 && vv[u] == 0)
-                    atomicOr(p.status, PA_STATUS_BAD_SLOT);
-                for (int j = n0 + rr[u] + 1; store && j < p.N; ++j)
-                    store = __ldg(sl + j) != s;  // a later row of this sequence lands there
-                if (store) {
-                    T* o = static_cast<T*>(p.cache[tens[u] - 1]) + (static_cast<long long>(s) * p.KV + hh[u]) * p.D + col;
+                if (p.out[t]) {
+                    T* o = static_cast<T*>(p.out[t]) +
+                           ((static_cast<int64_t>(b) * (t == 0 ? p.H : p.KV) + hl) * p.N + n) * p.D + col;
                     *reinterpret_cast<uint4*>(o) = a[u];
                     if (two)
                         *reinterpret_cast<uint4*>(o + half) = c[u];
                 }
             }
+            if (t >= 1 && slot >= 0) {
+                T* o = static_cast<T*>(p.cache[t - 1]) + (static_cast<int64_t>(slot) * p.KV + hl) * p.D + col;
+                *reinterpret_cast<uint4*>(o) = a[u];
+                if (two)
+                    *reinterpret_cast<uint4*>(o + half) = c[u];
+            }
+        }
+        if (h + U * groups < h1) {
+            h += U * groups;
+            load();
+            h -= U * groups;
         }
     }
 }
@@ -394,28 +404,24 @@ extern "C" int pa_rotary(const void* q, const void* k, const int32_t* positions,
     p.factor = o.factor;
     p.inverse = o.inverse ? 1 : 0;
     const int mode = o.interleaved ? kSide : (rot / 2) % V == 0 ? kHalves : kAny;
-    // A CTA takes about two passes of its threads' items (1024 a pass) over
-    // consecutive positions; a short call spreads over the SMs instead, its
-    // heads split so that a CTA still fills its threads once.
+    // A CTA: a few positions (about 64 units of 16 or 32 bytes, so that four
+    // threads share a unit's heads), 32 KB of table at most; and as many heads as
+    // two rounds of its threads take, fewer where the call would leave SMs idle.
     const int per_row = mode == kHalves ? (D - rot / 2) / V : D / V;
-    const long long row_items = static_cast<long long>(p.heads) * per_row;
-    const long long want = (2 * kRotThreads * kRotItems + row_items - 1) / row_items;
-    p.rows_cta = static_cast<int>(want < 1 ? 1 : want > 16 ? 16 : want);
-    const int fit = 32768 / (rot / 2 * static_cast<int>(sizeof(float2)));  // 32 KB of table at most
-    if (p.rows_cta > fit)
-        p.rows_cta = fit;
-    if (p.rows_cta > N)
-        p.rows_cta = N;
-    while (p.rows_cta > 1 && static_cast<long long>(B) * ((N + p.rows_cta - 1) / p.rows_cta) < 304)
-        --p.rows_cta;
-    p.head_cta = p.heads;
-    const long long ctas = static_cast<long long>(B) * ((N + p.rows_cta - 1) / p.rows_cta);
-    if (ctas < 152) {
-        const long long split = (row_items * p.rows_cta + kRotThreads - 1) / kRotThreads;
-        const long long parts = split < 152 / ctas ? split : 152 / ctas;
-        if (parts > 1)
-            p.head_cta = static_cast<int>((p.heads + parts - 1) / parts);
-    }
+    int rows = 64 / per_row;
+    const int fit = 32768 / (rot / 2 * static_cast<int>(sizeof(float2)));
+    rows = rows < 1 ? 1 : rows;
+    rows = rows > fit ? fit : rows;
+    rows = rows > N ? N : rows;
+    const auto ctas = [&](int r) { return static_cast<long long>(B) * ((N + r - 1) / r); };
+    while (rows > 1 && ctas(rows) < 304)
+        --rows;
+    p.rows_cta = rows;
+    const int groups = kRotThreads / (rows * per_row);
+    int rounds = 2;
+    p.head_cta = groups * kRotHeads * rounds;
+    while (p.head_cta > groups && ctas(rows) * ((p.heads + p.head_cta - 1) / p.head_cta) < 152)
+        p.head_cta -= groups;
     const long long gx = static_cast<long long>(B) * ((N + p.rows_cta - 1) / p.rows_cta);
     const int gy = (p.heads + p.head_cta - 1) / p.head_cta;
     if (gx >= (1ll << 31))

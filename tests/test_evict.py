@@ -54,9 +54,9 @@ def expect(kc, vc, table, lens, w, budget, first, last, dst):
 
 
 # ------------------------------------------------------------------ CPU: refusals
-def call(pa, B=2, KV=2, D=64, BLOCK=16, ptr=None, nopts=False, null_ws=False, **o):
+def call(pa, B=2, KV=2, D=64, BLOCK=16, ptr=None, nopts=False, **o):
     vals = dict(max_blocks=8, num_blocks=32, dtype=1, budget=20, keep_first=2, keep_last=3, dst_table=None, dst_max_blocks=0,
-                workspace=None if null_ws else 12 * A, workspace_bytes=1 << 20, status=None, wait_limit_ns=0)
+                status=None)
     vals.update(o)
     opts = pa.EvictOpts(**vals)
     p = [(i + 1) * A for i in range(8)]
@@ -66,7 +66,7 @@ def call(pa, B=2, KV=2, D=64, BLOCK=16, ptr=None, nopts=False, null_ws=False, **
     return pa.LIB.pa_cache_evict(*p, B, KV, D, BLOCK, None if nopts else ctypes.byref(opts), None)
 
 
-NULL, DIMS, UNSUP, ALIGN, WS = -1, -2, -3, -4, -5
+NULL, DIMS, UNSUP, ALIGN = -1, -2, -3, -4
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -76,20 +76,15 @@ NULL, DIMS, UNSUP, ALIGN, WS = -1, -2, -3, -4, -5
     (dict(max_blocks=1 << 26), DIMS), (dict(num_blocks=1 << 27), DIMS), (dict(budget=1 << 30), DIMS),
     (dict(dst_table=13 * A, dst_max_blocks=1), DIMS), (dict(dst_table=13 * A, dst_max_blocks=0), DIMS),
     (dict(ptr={7: 5 * A}), DIMS), (dict(ptr={6: 2 * A + 64}), DIMS), (dict(ptr={5: 4 * A}), DIMS), (dict(ptr={1: 1 * A}), DIMS),
-    (dict(workspace=6 * A), DIMS),
     (dict(dtype=7), UNSUP), (dict(KV=1, D=4), UNSUP), (dict(KV=512, D=128), UNSUP), (dict(B=4097), UNSUP),
-    (dict(ptr={0: A + 8}), ALIGN), (dict(ptr={4: 5 * A + 2}), ALIGN), (dict(workspace=12 * A + 16), ALIGN),
-    (dict(null_ws=True), WS), (dict(workspace_bytes=16), WS),
+    (dict(ptr={0: A + 8}), ALIGN), (dict(ptr={4: 5 * A + 2}), ALIGN),
 ])
 def test_refusals(pa, kw, code):
     assert call(pa, **kw) == code
 
 
-def test_nothing_to_do_and_workspace_sizes(pa):
+def test_nothing_to_do(pa):
     assert call(pa, B=0) == 0
-    f = pa.LIB.pa_cache_evict_workspace_bytes
-    assert f(2, 2, 64, 8, 16, 20, 1) > 0
-    assert f(0, 2, 64, 8, 16, 20, 1) == f(2, 2, 64, 8, 16, 0, 1) == f(2, 1, 4, 8, 16, 20, 1) == 0
 
 
 # ------------------------------------------------------------------ GPU
@@ -173,6 +168,17 @@ def test_ties_and_odd_weights(pa, n, kind):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [16384, 16385, 70000, 131072, 200000])
+def test_long_sequences_whose_weights_crowd(pa, n):
+    # up to eight CTAs a sequence, and weights read again in every pass past 131072
+    kc, vc, table, _, ln, w, g = make(n, "f32", [n, n // 2], 1, 8, 64)
+    w = torch.where(torch.rand(w.shape, generator=g) < 0.5, (w * 64).floor() / 64, w)
+    budget = n // 3
+    want = expect(kc, vc, table, [n, n // 2], w, budget, 3, 100, None)
+    same(run(pa, kc, vc, table, None, ln, w, budget, 3, 100), want)
+
+
+@pytest.mark.gpu
 def test_bad_lengths_and_blocks_are_reported_and_skipped(pa):
     kc, vc, table, _, ln, w, _ = make(3, "f16", [100, 100, 100], 2, 64, 16)
     cap = table.shape[1] * 16
@@ -220,7 +226,7 @@ def test_graph_replay_streams_and_two_plans(pa):
         torch.cuda.synchronize()
         same([x.cpu() for x in (plan.new_lens, plan.kept, plan.weights_out, d[0], d[1])],
              expect(kc, vc, table, lens, w, 100, 2, 10, None))
-    # two plans at the same time on two streams, each with its own caches and workspace
+    # two plans at the same time on two streams, each with its own caches
     other = [x.clone() for x in d]
     other[3].fill_(300)
     want = expect(other[0].cpu(), other[1].cpu(), table, [300] * 3, other[4].cpu(), 77, 0, 0, None)
