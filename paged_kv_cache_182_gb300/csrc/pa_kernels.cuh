@@ -52,6 +52,7 @@
 #include "pa_common.cuh"
 #include "pa_decode.h"
 #include "pa_ptx.cuh"
+#include "pa_tanh.cuh"
 
 namespace pa {
 
@@ -506,23 +507,6 @@ __device__ __forceinline__ void flag_timeout(const SplitParams& p, volatile int*
 }
 
 // ------------------------------------------------------- modified scores
-// Offset of a tile's keys in the real sequence (tiles never straddle the gap).
-template <bool kMod>
-struct TileOff {
-    __device__ __forceinline__ TileOff(const Sched&, const Item&, int) {}
-};
-template <>
-struct TileOff<true> {
-    int off;   // real key - compressed key
-    int rest;  // gap tokens behind this tile (they lie between its keys and the rows)
-    __device__ __forceinline__ TileOff(const Sched& sc, const Item& it, int t0)
-    {
-        const int gap = sc.gap[it.b];
-        off = t0 >= sc.pend[it.b] ? gap : 0;
-        rest = gap - off;
-    }
-};
-
 // The factor of the raw dot products: scale * log2(e), or scale / cap.
 template <bool kMod>
 __device__ __forceinline__ float score_qscale(const ParamsOf<kMod>& p)
@@ -533,90 +517,125 @@ __device__ __forceinline__ float score_qscale(const ParamsOf<kMod>& p)
         return p.qscale;
 }
 
-// One query row of a piece: its limits among the compressed keys, its slope and
-// where its scores go.
+// A piece's share of the modifications, and one query row's.  Keys, rows and
+// limits are those of the compressed sequence.
+template <bool kMod>
+struct ScorePiece {
+    __device__ __forceinline__ ScorePiece(const SplitParams&, const Sched&, const Item&) {}
+};
+template <>
+struct ScorePiece<true> {
+    int pl;         // keys below are visible whatever the window
+    int gap, pend;  // the tokens left out, and where
+    __device__ __forceinline__ ScorePiece(const ScoredParams& p, const Sched& sc, const Item& it)
+    {
+        gap = sc.gap[it.b];
+        pend = sc.pend[it.b];
+        pl = p.prefix ? min(max(__ldg(p.prefix + it.b), 0), it.past + p.NQ) : 0;
+        if (gap > 0)
+            pl = min(pl, pend);  // (pend covers the prefix)
+    }
+    // real key - compressed key in the tile at t0 (tiles never straddle the gap)
+    __device__ __forceinline__ int off(int t0) const { return t0 >= pend ? gap : 0; }
+};
+
 template <bool kMod>
 struct ScoreRow {
-    __device__ __forceinline__ void begin(const SplitParams&, const Sched&, const Item&, int, int&) {}
-    __device__ __forceinline__ void none() {}
+    __device__ __forceinline__ void begin(const SplitParams&, const ScorePiece<kMod>&, const Item&, int, int&) {}
 };
 template <>
 struct ScoreRow<true> {
-    int wlo;      // first key of the window
-    int pl;       // keys below are visible whatever the window
-    int row;      // the row's own key
-    float slope;  // distance slope * log2(e)
-    size_t at;    // scores: element of (segment, token 0, row)
-
-    // `limit` is the causal limit on entry; a prefix that reaches into the new
-    // rows raises it, a window without the causal rule lowers it.
-    __device__ __forceinline__ void begin(const ScoredParams& p, const Sched& sc, const Item& it, int rho, int& limit)
+    int row = 0;        // the row's own key
+    float slope = 0.f;  // distance slope * log2(e)
+    // `limit` is the causal limit on entry (0: a padding row, which sees nothing):
+    // a prefix that reaches into the new rows raises it, a window without the
+    // causal rule lowers it.
+    __device__ __forceinline__ void begin(const ScoredParams& p, const ScorePiece<true>& sp, const Item& it, int rho,
+                                          int& limit)
     {
-        const int total = it.past + p.NQ;
-        const int rn = rho % p.NQ;
-        row = it.past + rn;
-        wlo = row - p.window + 1;  // window INT_MAX: far below 0
+        if (limit == 0)
+            return;
+        row = it.past + rho % p.NQ;
         if (!p.causal && p.window < p.NQ)
             limit = min(limit, row + p.window);
-        // a prefix beyond pend's stage would have no gap before it, so real
-        // and compressed keys agree below pl
-        pl = p.prefix ? min(max(__ldg(p.prefix + it.b), 0), total) : 0;
-        if (sc.gap[it.b] > 0)
-            pl = min(pl, sc.pend[it.b]);
-        limit = max(limit, pl);
+        limit = max(limit, sp.pl);
         slope = p.slopes ? __ldg(p.slopes + it.kh * (p.H / p.KV) + rho / p.NQ) * kLog2e : 0.f;
-        at = (static_cast<size_t>(it.b) * p.KV + it.kh) * p.score_tokens * p.R + rho;
     }
-    __device__ __forceinline__ void none()
+    // key c within this row's limit: visible by window or prefix?
+    __device__ __forceinline__ bool sees(const ScoredParams& p, const ScorePiece<true>& sp, int c) const
     {
-        wlo = INT_MAX;
-        pl = 0;
-        row = 0;
-        slope = 0.f;
-        at = ~static_cast<size_t>(0);
-    }
-    __device__ __forceinline__ bool sees(int c) const { return c >= wlo || c < pl; }
-    // The modified score, in base-2 units, of a dot product already times
-    // score_qscale.  tanhf, not the hardware's approximation: its relative
-    // error of 2^-11 would move a score of 10 under a cap of 50 by 0.005, and
-    // every weight with it; the scores are few beside the K and V bytes.
-    __device__ __forceinline__ float score(const ScoredParams& p, float x, int c, const TileOff<true>& to) const
-    {
-        if (p.cap_out != 0.f)
-            x = p.cap_out * tanhf(x);
-        return fmaf(-slope, static_cast<float>(abs(row + to.rest - c)), x);
-    }
-    __device__ __forceinline__ void store(const ScoredParams& p, const TileOff<true>& to, int c, float s) const
-    {
-        if (p.scores && at != ~static_cast<size_t>(0))
-            p.scores[at + static_cast<size_t>(c + to.off) * p.R] = s;
+        return row - c < p.window || c < sp.pl;
     }
 };
 
 // What all rows of a warp together see (padding rows do not count): every row
 // sees [0, pl) and [wlo, its limit); no row sees a key outside [0, pl) and
-// [wlo_any, lim_any) -- pl is the same for all rows.  The value rows of keys
-// that no row sees are replaced by zeros: their weight is 0, but 0 times an
-// infinity or NaN is not.
+// [wlo_any, lim_any).  The value rows of keys that no row sees are replaced by
+// zeros: their weight is 0, but 0 times an infinity or NaN is not.
 template <bool kMod>
 struct ScoreSpan {
-    __device__ __forceinline__ ScoreSpan(const ScoreRow<kMod>*, const int*) {}
+    __device__ __forceinline__ ScoreSpan(const SplitParams&, const ScorePiece<kMod>&, const ScoreRow<kMod>*, const int*) {}
     __device__ __forceinline__ bool whole(int, int) const { return true; }
-    __device__ __forceinline__ bool any(int) const { return true; }
 };
 template <>
 struct ScoreSpan<true> {
     int wlo, wlo_any, lim_any, pl;
-    __device__ __forceinline__ ScoreSpan(const ScoreRow<true>* r, const int* lim)
+    __device__ __forceinline__ ScoreSpan(const ScoredParams& p, const ScorePiece<true>& sp, const ScoreRow<true>* r,
+                                         const int* lim)
     {
-        wlo = __reduce_max_sync(kFull, max(lim[0] > 0 ? r[0].wlo : INT_MIN, lim[1] > 0 ? r[1].wlo : INT_MIN));
-        wlo_any = __reduce_min_sync(kFull, min(r[0].wlo, r[1].wlo));
+        const int hi = max(lim[0] > 0 ? r[0].row : INT_MIN, lim[1] > 0 ? r[1].row : INT_MIN);
+        const int lo = min(lim[0] > 0 ? r[0].row : INT_MAX, lim[1] > 0 ? r[1].row : INT_MAX);
+        // (rows are at most 2^30: no overflow against a window of INT_MAX)
+        wlo = max(__reduce_max_sync(kFull, hi), 0) - p.window + 1;
+        wlo_any = min(__reduce_min_sync(kFull, lo), 1 << 30) - p.window + 1;
         lim_any = __reduce_max_sync(kFull, max(lim[0], lim[1]));
-        pl = __reduce_max_sync(kFull, max(r[0].pl, r[1].pl));
+        pl = sp.pl;
     }
     __device__ __forceinline__ bool whole(int c0, int c1) const { return c0 >= wlo || c1 <= pl; }
     __device__ __forceinline__ bool any(int c) const { return c < pl || (c >= wlo_any && c < lim_any); }
 };
+
+// Modifies a thread's N scores (dot products times score_qscale) of a tile: the
+// cap, the distance bias, the masks, the store for the key weights, each in a
+// pass of its own under one test, so that a call runs (and fetches) only the
+// code of what it asks for.  Score i belongs to row R[i % 2 or as row_of says]
+// and key c0 + tok_of(i), both of which the caller's functions give at compile
+// time of the unrolled loops.
+template <int N, typename RowOf, typename TokOf>
+__device__ __forceinline__ void modify_scores(const ScoredParams& p, const ScorePiece<true>& sp, const ScoreRow<true>* rows,
+                                              const int* lim, float (&x)[N], int c0, int off, bool whole, int n_left,
+                                              float* scores, RowOf row_of, TokOf tok_of)
+{
+    if (p.cap_out != 0.f) {
+        tanh_block(x);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            x[i] *= p.cap_out;
+    }
+    if (p.slopes) {
+        // distances as float differences from the first key (exact below 2^24)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const ScoreRow<true>& r = rows[row_of(i)];
+            const float d0 = static_cast<float>(r.row + sp.gap - off - c0);
+            x[i] = fmaf(-r.slope, fabsf(d0 - static_cast<float>(tok_of(i))), x[i]);
+        }
+    }
+    if (!whole) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int c = c0 + tok_of(i);
+            if (!(tok_of(i) < n_left && c < lim[row_of(i)] && rows[row_of(i)].sees(p, sp, c)))
+                x[i] = -INFINITY;
+        }
+    }
+    if (scores) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (tok_of(i) < n_left && lim[row_of(i)] > 0)
+                scores[static_cast<size_t>(c0 + off + tok_of(i)) * p.R + row_of(i)] = x[i];
+    }
+}
 
 // ------------------------------------------------------- float32 CUDA-core math
 // One warp: RG query rows, a subset of the tokens of each tile.  A token row
@@ -638,8 +657,9 @@ struct SimtMath {
     int limit[RG];
     int lg, li, ts, TS;
     ScoreRow<kMod> mod[RG];
+    int wlo, lim_min;  // modified scores: keys [wlo, lim_min) are visible to every row
 
-    __device__ void begin(const ParamsOf<kMod>& p, const Sched& sc, const Item& it, int row0, int R_cta, int lane,
+    __device__ void begin(const ParamsOf<kMod>& p, const ScorePiece<kMod>& sp, const Item& it, int row0, int R_cta, int lane,
                           int ts_, int TS_)
     {
         lg = lane / LPT;
@@ -661,13 +681,12 @@ struct SimtMath {
                 for (int v = 0; v < V2; ++v)
                     q[r][v] = __fmul2_rn(q[r][v], sc2);
                 limit[r] = it.past + (p.causal ? (rho % p.NQ) + 1 : p.NQ);
-                mod[r].begin(p, sc, it, rho, limit[r]);
+                mod[r].begin(p, sp, it, rho, limit[r]);
             } else {
 #pragma unroll
                 for (int v = 0; v < V2; ++v)
                     q[r][v] = make_float2(0.f, 0.f);
                 limit[r] = 0;
-                mod[r].none();
             }
             m[r] = -FLT_MAX;
             l[r] = 0.f;
@@ -675,13 +694,27 @@ struct SimtMath {
             for (int v = 0; v < V2; ++v)
                 o[r][v] = make_float2(0.f, 0.f);
         }
+        if constexpr (kMod) {
+            wlo = INT_MIN;
+            lim_min = INT_MAX;
+#pragma unroll
+            for (int r = 0; r < RG; ++r)
+                if (limit[r] > 0) {
+                    wlo = max(wlo, mod[r].row - p.window + 1);
+                    lim_min = min(lim_min, limit[r]);
+                }
+        }
     }
 
     // Tile of n_tile tokens starting at absolute key t0: rows < past come from
     // the cache tile (ks / vs), rows >= past from the new rows (kn / vn).
-    __device__ void tile(const ParamsOf<kMod>& p, const T* ks, const T* kn, const T* vs, const T* vn, int t0,
-                         int n_tile, int past, const TileOff<kMod>& to)
+    // (scores: where row row0 of token 0 of the segment goes, or NULL)
+    __device__ void tile(const ParamsOf<kMod>& p, const ScorePiece<kMod>& sp, const T* ks, const T* kn, const T* vs,
+                         const T* vn, int t0, int n_tile, int past, float* scores)
     {
+        bool whole = true;
+        if constexpr (kMod)
+            whole = t0 + n_tile <= lim_min && (t0 >= wlo || t0 + n_tile <= sp.pl);
         const int step = TS * TPW;
         for (int base = 0; base < n_tile; base += kSubBatch * step) {
             float sc[kSubBatch][RG];
@@ -709,15 +742,19 @@ struct SimtMath {
 #pragma unroll
                     for (int off = LPT / 2; off > 0; off >>= 1)
                         acc += __shfl_xor_sync(kFull, acc, off);
-                    if constexpr (kMod) {
-                        const bool valid = live && t_abs < limit[r] && mod[r].sees(t_abs);
-                        sc[i][r] = valid ? mod[r].score(p, acc, t_abs, to) : -INFINITY;
-                        if (live && li == 0)
-                            mod[r].store(p, to, t_abs, sc[i][r]);
-                    } else {
+                    if constexpr (kMod)
+                        sc[i][r] = acc;
+                    else
                         sc[i][r] = (live && t_abs < limit[r]) ? acc : -INFINITY;
-                    }
                 }
+            }
+            if constexpr (kMod) {
+                // token of sub-step i: base + (i TS + ts) TPW + lg
+                const int first = base + ts * TPW + lg;
+                modify_scores(
+                    p, sp, mod, limit, reinterpret_cast<float(&)[kSubBatch * RG]>(sc), t0 + first, sp.off(t0),
+                    whole && base + kSubBatch * step <= n_tile, n_tile - first, li == 0 ? scores : nullptr,
+                    [](int i) { return i % RG; }, [&](int i) { return (i / RG) * step; });
             }
 #pragma unroll
             for (int r = 0; r < RG; ++r) {
@@ -742,10 +779,12 @@ struct SimtMath {
                 const int t_abs = t0 + t_rel;
                 if constexpr (kMod) {
                     // a key that no row of the warp sees: 0 times its value, which may not be finite
-                    bool any = false;
+                    bool any = whole;
+                    if (!whole) {
 #pragma unroll
-                    for (int r = 0; r < RG; ++r)
-                        any |= t_abs < limit[r] && mod[r].sees(t_abs);
+                        for (int r = 0; r < RG; ++r)
+                            any |= t_abs < limit[r] && mod[r].sees(p, sp, t_abs);
+                    }
                     if (!any)
                         continue;
                 }
@@ -1538,7 +1577,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ts = warp / nrg;
 
         Math mt;
-        mt.begin(p, sc, it, rg * RG, R_cta, lane, ts, TS);
+        const ScorePiece<kMod> sp(p, sc, it);
+        float* scores = nullptr;
+        if constexpr (kMod)
+            if (p.scores)
+                scores = p.scores + (static_cast<size_t>(it.b) * p.KV + it.kh) * p.score_tokens * p.R +
+                         it.rsg * p.rows_per_cta + rg * RG;
+        mt.begin(p, sp, it, rg * RG, R_cta, lane, ts, TS);
         bool alive = true;
         for (int j = 0; j < ntiles; ++j, ++gt) {
             const int s = gt % S;
@@ -1553,10 +1598,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             const unsigned char* st = sm.ring + static_cast<size_t>(s) * p.stage_bytes;
             const int t0 = it.start + j * TT;
-            mt.tile(p, reinterpret_cast<const T*>(st), reinterpret_cast<const T*>(st + p.knew_off),
+            mt.tile(p, sp, reinterpret_cast<const T*>(st), reinterpret_cast<const T*>(st + p.knew_off),
                     reinterpret_cast<const T*>(st + p.v_off),
                     reinterpret_cast<const T*>(st + p.vnew_off), t0, min(TT, it.end - t0),
-                    it.past, TileOff<kMod>(sc, it, t0));
+                    it.past, scores);
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sm.empty[s]);
@@ -1847,18 +1892,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         // causal / length limits of this thread's two rows (0 for padding rows)
         int lim[2];
+        const ScorePiece<kMod> sp(p, sc, it);
         ScoreRow<kMod> mod[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int rl = row0 + g + 8 * h;
             const int rho = it.rsg * ROWS + rl;
             lim[h] = rl < R_cta ? it.past + (p.causal ? (rho % p.NQ) + 1 : p.NQ) : 0;
-            if (rl < R_cta)
-                mod[h].begin(p, sc, it, rho, lim[h]);
-            else
-                mod[h].none();
+            mod[h].begin(p, sp, it, rho, lim[h]);
         }
-        const ScoreSpan<kMod> span(mod, lim);
+        const ScoreSpan<kMod> span(p, sp, mod, lim);
+        float* scores = nullptr;  // of row row0 + g, token 0
+        if constexpr (kMod)
+            if (p.scores)
+                scores = p.scores + (static_cast<size_t>(it.b) * p.KV + it.kh) * p.score_tokens * p.R + it.rsg * ROWS +
+                         row0 + g;
         const int lim_min = __reduce_min_sync(kFull, min(lim[0] > 0 ? lim[0] : INT_MAX,
                                                          lim[1] > 0 ? lim[1] : INT_MAX));
 
@@ -1937,7 +1985,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 full_tile[u] = tu + kMmaTokens <= n_tile && t0 + tu + kMmaTokens <= lim_min &&
                                span.whole(t0 + tu, t0 + tu + kMmaTokens);
             }
-            const TileOff<kMod> to(sc, it, t0);
 
             // ---- S = Q K^T (per group, two accumulator sets per 8-token tile:
             // shorter chains; the groups' MMAs interleave)
@@ -1977,20 +2024,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 4; ++e) {
                         const int h = e >> 1;
                         const int tk = tb + u * kMmaTokens + nt * 8 + 2 * qd + (e & 1);
-                        if constexpr (kMod) {
-                            const float x = (sa[u][0][nt][e] + sa[u][1][nt][e]) * qs;
-                            const float v = mod[h].score(p, x, t0 + tk, to);
-                            const bool valid = full_tile[u] || (tk < n_tile && t0 + tk < lim[h] && mod[h].sees(t0 + tk));
-                            sv[u][nt][e] = valid ? v : -INFINITY;
-                            if (tk < n_tile)
-                                mod[h].store(p, to, t0 + tk, sv[u][nt][e]);
-                        } else {
-                            const float v = (sa[u][0][nt][e] + sa[u][1][nt][e]) * p.qscale;
-                            const bool valid = full_tile[u] || (tk < n_tile && t0 + tk < lim[h]);
-                            sv[u][nt][e] = valid ? v : -INFINITY;
-                        }
-                        mx[h] = fmaxf(mx[h], sv[u][nt][e]);
+                        const float v = (sa[u][0][nt][e] + sa[u][1][nt][e]) * (kMod ? qs : p.qscale);
+                        const bool valid = kMod || full_tile[u] || (tk < n_tile && t0 + tk < lim[h]);
+                        sv[u][nt][e] = valid ? v : -INFINITY;
+                        if (!kMod)
+                            mx[h] = fmaxf(mx[h], sv[u][nt][e]);
                     }
+            if constexpr (kMod) {
+                // rows row0 + g (+ 8) and tokens tb + 16 u + 8 nt + 2 qd + e % 2 of score (u, nt, e)
+                bool whole = true;
+#pragma unroll
+                for (int u = 0; u < TG; ++u)
+                    whole &= full_tile[u];
+                const int off = sp.off(t0);
+                modify_scores(
+                    p, sp, mod, lim, reinterpret_cast<float(&)[TG * 8]>(sv), t0 + tb + 2 * qd, off, whole,
+                    n_tile - tb - 2 * qd, nullptr, [](int i) { return (i >> 1) & 1; },
+                    [](int i) { return (i >> 3) * kMmaTokens + ((i >> 2) & 1) * 8 + (i & 1); });
+                if (scores) {
+#pragma unroll
+                    for (int i = 0; i < TG * 8; ++i) {
+                        const int tk = tb + 2 * qd + (i >> 3) * kMmaTokens + ((i >> 2) & 1) * 8 + (i & 1), h = (i >> 1) & 1;
+                        if (tk < n_tile && lim[h] > 0)
+                            scores[static_cast<size_t>(t0 + off + tk) * p.R + 8 * h] = reinterpret_cast<float*>(sv)[i];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < TG * 8; ++i)
+                    mx[(i >> 1) & 1] = fmaxf(mx[(i >> 1) & 1], reinterpret_cast<float*>(sv)[i]);
+            }
             bool grow = false;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -2204,18 +2266,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         // causal / length limits of this thread's rows 2 qd + e (0 for padding rows)
         int lim[2];
+        const ScorePiece<kMod> sp(p, sc, it);
         ScoreRow<kMod> mod[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int rl = 2 * qd + e;
             const int rho = it.rsg * ROWS + rl;
             lim[e] = rl < R_cta ? it.past + (p.causal ? (rho % p.NQ) + 1 : p.NQ) : 0;
-            if (rl < R_cta)
-                mod[e].begin(p, sc, it, rho, lim[e]);
-            else
-                mod[e].none();
+            mod[e].begin(p, sp, it, rho, lim[e]);
         }
-        const ScoreSpan<kMod> span(mod, lim);
+        const ScoreSpan<kMod> span(p, sp, mod, lim);
+        float* scores = nullptr;  // of row 2 qd, token 0
+        if constexpr (kMod)
+            if (p.scores)
+                scores = p.scores + (static_cast<size_t>(it.b) * p.KV + it.kh) * p.score_tokens * p.R + it.rsg * ROWS +
+                         2 * qd;
         const int lim_min = __reduce_min_sync(kFull, min(lim[0] > 0 ? lim[0] : INT_MAX,
                                                          lim[1] > 0 ? lim[1] : INT_MAX));
 
@@ -2286,7 +2351,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 full_tile[u] = tu + kMmaTokens <= n_tile && t0 + tu + kMmaTokens <= lim_min &&
                                span.whole(t0 + tu, t0 + tu + kMmaTokens);
             }
-            const TileOff<kMod> to(sc, it, t0);
 
             // ---- S^T = K Q^T: operand A = 16 token rows of K (ldmatrix gives
             // (tokens 0-7 | 8-15) x (columns 0-7 | 8-15) as a0 a2 a1 a3); two
@@ -2323,20 +2387,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = 0; e < 4; ++e) {
                     const int h = e & 1;
                     const int tk = tb + u * kMmaTokens + g + ((e >> 1) << 3);
-                    if constexpr (kMod) {
-                        const float x = (sa[u][0][e] + sa[u][1][e]) * qs;
-                        const float v = mod[h].score(p, x, t0 + tk, to);
-                        const bool valid = full_tile[u] || (tk < n_tile && t0 + tk < lim[h] && mod[h].sees(t0 + tk));
-                        sv[u][e] = valid ? v : -INFINITY;
-                        if (tk < n_tile)
-                            mod[h].store(p, to, t0 + tk, sv[u][e]);
-                    } else {
-                        const float v = (sa[u][0][e] + sa[u][1][e]) * p.qscale;
-                        const bool valid = full_tile[u] || (tk < n_tile && t0 + tk < lim[h]);
-                        sv[u][e] = valid ? v : -INFINITY;
-                    }
-                    mx[h] = fmaxf(mx[h], sv[u][e]);
+                    const float v = (sa[u][0][e] + sa[u][1][e]) * (kMod ? qs : p.qscale);
+                    const bool valid = kMod || full_tile[u] || (tk < n_tile && t0 + tk < lim[h]);
+                    sv[u][e] = valid ? v : -INFINITY;
+                    if (!kMod)
+                        mx[h] = fmaxf(mx[h], sv[u][e]);
                 }
+            if constexpr (kMod) {
+                // row 2 qd + e % 2 and token tb + 16 u + g + 8 (e / 2) of score (u, e)
+                bool whole = true;
+#pragma unroll
+                for (int u = 0; u < TG; ++u)
+                    whole &= full_tile[u];
+                modify_scores(
+                    p, sp, mod, lim, reinterpret_cast<float(&)[TG * 4]>(sv), t0 + tb + g, sp.off(t0), whole,
+                    n_tile - tb - g, (p.R & 1) ? scores : nullptr, [](int i) { return i & 1; },
+                    [](int i) { return (i >> 2) * kMmaTokens + ((i >> 1) & 1) * 8; });
+                if (scores && !(p.R & 1) && lim[0] > 0) {  // both rows of a token together
+#pragma unroll
+                    for (int i = 0; i < TG * 4; i += 2) {
+                        const int tk = tb + g + (i >> 2) * kMmaTokens + ((i >> 1) & 1) * 8;
+                        if (tk < n_tile)
+                            *reinterpret_cast<float2*>(scores + static_cast<size_t>(t0 + sp.off(t0) + tk) * p.R) =
+                                make_float2(reinterpret_cast<float*>(sv)[i], reinterpret_cast<float*>(sv)[i + 1]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < TG * 4; ++i)
+                    mx[i & 1] = fmaxf(mx[i & 1], reinterpret_cast<float*>(sv)[i]);
+            }
             bool grow = false;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {

@@ -57,6 +57,7 @@
 
 #include "pa_decode.h"
 #include "pa_ptx.cuh"
+#include "pa_tanh.cuh"
 #include "pa_tc.cuh"
 #include "pa_tmem.cuh"
 #include "pa_vjp.cuh"
@@ -122,47 +123,6 @@ __device__ __forceinline__ StatsItem stats_item_at(const VjpParamsOf<kMod>& p, i
         it.ntiles = lt > pt ? pt + max(0, et - lt) : max(pt, et);
     }
     return it;
-}
-
-// tanh of N scores (times 1 / cap): an odd polynomial of degree 11 where every
-// score of the warp is within 0.7 -- fitted here for the least largest relative
-// error of tanh(y) / y in y^2, 1.4e-8 -- two scores an instruction and no
-// special-function operation (the exponentials of the softmax fill that unit);
-// else 1 - 2 / (1 + e^(2 |y|)) where a score is beyond.
-constexpr float kTanhMax = 0.7f;
-
-template <int N>
-__device__ __forceinline__ void tanh_block(float (&y)[N])
-{
-    constexpr float kTanhC[6] = {0.999999986f,   -0.333331304f, 0.133284148f,
-                                 -0.0535260093f, 0.0200244578f, -0.00508833599f};
-    float top = 0.f;
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-        top = fmaxf(top, fabsf(y[j]));
-    const bool wide = __any_sync(kAll, !(top <= kTanhMax));
-#pragma unroll
-    for (int j = 0; j < N; j += 2) {
-        const float2 v = make_float2(y[j], y[j + 1]);
-        const float2 z = __fmul2_rn(v, v);
-        float2 a = make_float2(kTanhC[5], kTanhC[5]);
-#pragma unroll
-        for (int e = 4; e >= 0; --e)
-            a = __ffma2_rn(a, z, make_float2(kTanhC[e], kTanhC[e]));
-        a = __fmul2_rn(a, v);
-        if (wide) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float x = u ? v.y : v.x;
-                const float e = fast_exp2(fabsf(x) * 2.8853900817779268f);  // 2 log2(e)
-                const float far = copysignf(1.f - __fdividef(2.f, 1.f + e), x);
-                if (!(fabsf(x) <= kTanhMax))
-                    (u ? a.y : a.x) = far;
-            }
-        }
-        y[j] = a.x;
-        y[j + 1] = a.y;
-    }
 }
 
 struct MainBars {
