@@ -96,7 +96,9 @@ size_t pa_scored_scratch_bytes(int batch, int max_blocks, int BLOCK, int H, int 
  * A mask of opts (mask_kind != 0) adds its bias to the modified score and
  * hides what it hides, prefix or not.  Rows that see no key get dq = 0.
  * 16-bit inputs with D = 128 and no mask run on the tensor cores; tiles
- * outside prefix and window are skipped.  dq is accumulated by float32
+ * outside prefix and window are skipped.  opts->workspace holds
+ * pa_attention_vjp_scored_workspace_bytes() for the current device (partial dk
+ * and dv of a small call come on top of pa_attention_vjp's).  dq is accumulated by float32
  * reductions whose order varies: its last bits may differ from call to call.
  * More errors: PA_ERR_NULL_POINTER without score, PA_ERR_BAD_DIMS for a
  * softcap that is negative or not finite or a negative window,
@@ -106,6 +108,9 @@ int pa_attention_vjp_scored(const void *q, const void *k, const void *v, const v
                             const void *g, const void *mask, void *dq, void *dk, void *dv,
                             float scale, int B, int HQ, int HK, int SQ, int SK, int D,
                             const pa_score *score, const pa_vjp_opts *opts, void *stream);
+
+size_t pa_attention_vjp_scored_workspace_bytes(int B, int HQ, int HK, int SQ, int SK, int D, int dtype,
+                                               int out_dtype);
 
 #ifdef __cplusplus
 }

@@ -188,6 +188,8 @@ def load(path: Path = LIBRARY) -> ctypes.CDLL:
     lib.pa_attention_vjp_scored.restype = I
     lib.pa_attention_vjp_scored.argtypes = [P, P, P, P, P, P, P, P, P, ctypes.c_float, I, I, I, I, I, I,
                                             ctypes.POINTER(Score), ctypes.POINTER(VjpOpts), P]
+    lib.pa_attention_vjp_scored_workspace_bytes.restype = ctypes.c_size_t
+    lib.pa_attention_vjp_scored_workspace_bytes.argtypes = [I, I, I, I, I, I, I, I]
     lib.pa_rotary.restype = I
     lib.pa_rotary.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, ctypes.POINTER(RotaryOpts), P]
     lib.pa_cache_evict.restype = I
@@ -692,7 +694,7 @@ class VjpPlan:
         for t, ref in zip(out, (q, k, k)):
             if t.dtype != odt or tuple(t.shape) != tuple(ref.shape) or not t.is_contiguous():
                 raise ValueError("out: dq like q, dk and dv like k, of the output dtype")
-        need = int(LIB.pa_attention_vjp_workspace_bytes(B, HQ, SQ, D, o.dtype, o.out_dtype))
+        need = self._workspace_bytes(B, HQ, HK, SQ, SK, D, o.dtype, o.out_dtype, dev)
         self.workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
         o.workspace = _ptr(self.workspace)
         o.workspace_bytes = int(self.workspace.numel())
@@ -705,6 +707,9 @@ class VjpPlan:
         self._args = (_ptr(q), _ptr(k), _ptr(v), _ptr(y), _ptr(g), _ptr(mask), _ptr(self.dq),
                       _ptr(self.dk), _ptr(self.dv), ctypes.c_float(scale), B, HQ, HK, SQ, SK, D,
                       ctypes.byref(self.opts))
+
+    def _workspace_bytes(self, B, HQ, HK, SQ, SK, D, dtype, out_dtype, device):
+        return int(LIB.pa_attention_vjp_workspace_bytes(B, HQ, SQ, D, dtype, out_dtype))
 
     def run(self, stream=None):
         if torch.cuda.current_device() == self.device.index:
@@ -827,6 +832,10 @@ class ScoredVjpPlan(VjpPlan):
         self.score = _score(softcap, slopes, window, prefix, int(q.shape[0]), int(q.shape[1]), q.device)
         self._scored_keep = (slopes, prefix)
         self._args = self._args[:-1] + (ctypes.byref(self.score), ctypes.byref(self.opts))
+
+    def _workspace_bytes(self, B, HQ, HK, SQ, SK, D, dtype, out_dtype, device):
+        with torch.cuda.device(device):
+            return int(LIB.pa_attention_vjp_scored_workspace_bytes(B, HQ, HK, SQ, SK, D, dtype, out_dtype))
 
     def run(self, stream=None):
         if torch.cuda.current_device() == self.device.index:

@@ -7,6 +7,18 @@
 
 namespace pa {
 
+// y *= f, two an instruction.
+template <int N>
+__device__ __forceinline__ void scale_block(float (&y)[N], float f)
+{
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+        const float2 r = __fmul2_rn(make_float2(y[j], y[j + 1]), make_float2(f, f));
+        y[j] = r.x;
+        y[j + 1] = r.y;
+    }
+}
+
 // tanh of N scores (times 1 / cap), N even: an odd polynomial of degree 11
 // where every score of the warp is within 0.7 -- fitted here for the least
 // largest relative error of tanh(y) / y in y^2, 1.4e-8 -- two scores an
@@ -21,14 +33,11 @@ __device__ __forceinline__ void tanh_block(float (&y)[N])
 {
     constexpr float kMax = 0.7f;
     constexpr float kC[6] = {0.999999986f, -0.333331304f, 0.133284148f, -0.0535260093f, 0.0200244578f, -0.00508833599f};
-    float top = 0.f;
-    bool wide = false;
+    float top = 0.f;  // (a NaN gives NaN either way)
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-        top = fmaxf(top, fabsf(y[j]));
-        wide |= y[j] != y[j];
-    }
-    wide = __any_sync(0xffffffffu, wide || top > kMax);
+    for (int j = 0; j < N; j += 2)
+        top = fmaxf(top, fmaxf(fabsf(y[j]), fabsf(y[j + 1])));
+    const bool wide = __any_sync(0xffffffffu, top > kMax);
 #pragma unroll
     for (int j = 0; j < N; j += 2) {
         const float2 v = make_float2(y[j], y[j + 1]);
@@ -44,7 +53,7 @@ __device__ __forceinline__ void tanh_block(float (&y)[N])
                 const float x = u ? v.y : v.x;
                 const float e = fast_exp2(fabsf(x) * -2.8853900817779268f);  // 2 log2(e)
                 const float far = copysignf(__fdividef(1.f - e, 1.f + e), x);
-                if (!(fabsf(x) <= kMax))  // NaN too
+                if (fabsf(x) > kMax)
                     (u ? a.y : a.x) = far;
             }
         }

@@ -332,6 +332,27 @@ struct VjpLayout {
     size_t lse, delta, acc, total;
 };
 
+// Multiprocessors of the current device, or an upper bound of this machine's
+// when there is none to ask (size queries on a host without a GPU).
+int device_sms()
+{
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
+        cudaGetLastError();
+        return 152;
+    }
+    return sms;
+}
+
+// Partial sums of split groups after the plain workspace (0 without a split).
+size_t part_bytes(int B, int HQ, int HK, int SK, int D, int dtype)
+{
+    if (!vjp_tc_supported(dtype, D, HQ / HK, 0) || !vjp_tc_splits(B, HQ, HK, SK, device_sms()))
+        return 0;
+    return static_cast<size_t>(B) * HQ * SK * D * 4;
+}
+
 bool layout(int B, int HQ, int SQ, int D, int dtype, int out_dtype, VjpLayout* L)
 {
     if (B < 0 || HQ < 1 || SQ < 0 || D < 1)
@@ -461,7 +482,10 @@ static int vjp_impl(const void* q, const void* k, const void* v, const void* y, 
         return PA_ERR_NULL_POINTER;
     if ((reinterpret_cast<uintptr_t>(o.workspace) & 255) != 0)
         return PA_ERR_ALIGNMENT;
-    if (o.workspace_bytes < L.total)
+    const bool tc = o.kernel != 1 && vjp_tc_supported(o.dtype, D, HQ / HK, o.mask_kind);
+    // split groups: dk's partial sums, then dv's, behind the rest
+    const size_t part = score && tc && keys ? part_bytes(B, HQ, HK, SK, D, o.dtype) : 0;
+    if (o.workspace_bytes < L.total + 2 * part)
         return PA_ERR_WORKSPACE;
     const int odt = out_type(o.dtype, o.out_dtype);
     unsigned char* ws = static_cast<unsigned char*>(o.workspace);
@@ -502,11 +526,13 @@ static int vjp_impl(const void* q, const void* k, const void* v, const void* y, 
         sp.cap_in = score->softcap > 0.f ? scale / score->softcap : 0.f;
         sp.cap_out = score->softcap > 0.f ? score->softcap * kVjpLog2e : 0.f;
         sp.window = score->window > 0 ? score->window : INT_MAX;
+        sp.split = part > 0;
+        for (int i = 0; i < 2; ++i)
+            sp.part[i] = part > 0 ? reinterpret_cast<float*>(ws + L.total + i * part) : nullptr;
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint64_t launches = 0;
     int rc;
-    const bool tc = o.kernel != 1 && vjp_tc_supported(o.dtype, D, HQ / HK, o.mask_kind);
     if (score)
         rc = tc ? launch_vjp_tc_scored(sp, o.dtype, odt == PA_F32, st, &launches)
                 : pick_simt<true>(o.dtype, odt == PA_F32)(sp, st, &launches);
@@ -546,4 +572,15 @@ extern "C" int pa_attention_vjp_scored(const void* q, const void* k, const void*
     if ((reinterpret_cast<uintptr_t>(score->slopes) & 3) || (reinterpret_cast<uintptr_t>(score->prefix) & 3))
         return PA_ERR_ALIGNMENT;
     return vjp_impl(q, k, v, y, g, mask, dq, dk, dv, scale, B, HQ, HK, SQ, SK, D, score, opts, stream);
+}
+
+extern "C" size_t pa_attention_vjp_scored_workspace_bytes(int B, int HQ, int HK, int SQ, int SK, int D, int dtype,
+                                                          int out_dtype)
+{
+    const size_t base = pa_attention_vjp_workspace_bytes(B, HQ, SQ, D, dtype, out_dtype);
+    if (HK < 1 || HQ < HK || HQ % HK != 0 || SK < 0 || B < 0)
+        return 0;
+    if (B == 0 || SK == 0)
+        return base;
+    return base == 0 && SQ > 0 ? 0 : base + 2 * part_bytes(B, HQ, HK, SK, D, dtype);
 }

@@ -47,6 +47,10 @@ struct VjpScoredParams : VjpParams {
     const int32_t* prefix;  // [B], or NULL
     float cap_in, cap_out;  // scale / cap, cap * log2(e); 0 without a cap
     int window;             // INT_MAX: none
+    // tensor cores, split: one CTA per query head instead of per group, its dk and
+    // dv in part[0] and part[1] [groups][B][HK][SK][D], summed in group order after
+    int split;
+    float* part[2];
 };
 
 template <bool kMod>
@@ -92,6 +96,8 @@ __device__ __forceinline__ float vjp_bias(const VjpParams& p, int b, int h, int 
 bool vjp_tc_supported(int dtype, int D, int groups, int mask_kind);
 int launch_vjp_tc(const VjpParams& p, int dtype, bool f32_out, cudaStream_t st, uint64_t* launches);
 int launch_vjp_tc_scored(const VjpScoredParams& p, int dtype, bool f32_out, cudaStream_t st, uint64_t* launches);
+// Whether that launch splits its groups (VjpScoredParams::split) on a device of `sms`.
+bool vjp_tc_splits(int B, int HQ, int HK, int SK, int sms);
 
 // Adds to the library's count of kernel launches (pa_kernel_launches).
 void count_launches(uint64_t n);

@@ -366,25 +366,24 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(&bars.s_free[s]);
-                    // modified scores in base-2 units
+                    // modified scores: base-2 units with a distance bias, else to be
+                    // multiplied by c2 in the exponential
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         float y[32];
-                        const float f = p.cap_out != 0.f ? p.cap_in : p.scale_log2;
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            y[j] = __uint_as_float(xs[c].r[j]) * f;
+                            y[j] = __uint_as_float(xs[c].r[j]);
                         if (p.cap_out != 0.f) {
+                            scale_block(y, p.cap_in);
                             tanh_block(y);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                y[j] *= p.cap_out;
                         }
                         if (p.slopes) {
+                            const float f = p.cap_out != 0.f ? p.cap_out : p.scale_log2;
                             const float d0 = static_cast<float>(i - kbase - c * 32);
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
-                                y[j] = fmaf(-slope2, fabsf(d0 - static_cast<float>(j)), y[j]);
+                                y[j] = fmaf(-slope2, fabsf(d0 - static_cast<float>(j)), y[j] * f);
                         }
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
@@ -435,7 +434,9 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
                 }
                 const float pm = fmaxf(fmaxf(fmaxf(pm8[0], pm8[1]), fmaxf(pm8[2], pm8[3])),
                                        fmaxf(fmaxf(pm8[4], pm8[5]), fmaxf(pm8[6], pm8[7])));
-                const float c2 = kMod ? 1.f : p.scale_log2;
+                float c2 = p.scale_log2;
+                if constexpr (kMod)
+                    c2 = p.slopes ? 1.f : p.cap_out != 0.f ? p.cap_out : p.scale_log2;
                 const float mt = fmaxf(m, pm * c2);  // base-2 units
                 if (mt != -INFINITY) {
                     float s8[8];
@@ -555,10 +556,21 @@ __global__ void __launch_bounds__(kMainThreads, 1)
     MainBars& bars = *reinterpret_cast<MainBars*>(sS + 2 * kHalf128 + 2048);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int BH = p.B * p.HK;
+    int heads = p.HK, groups = p.groups, g0 = 0;  // heads of the grid; query heads of this CTA, from g0
+    if constexpr (kMod)
+        if (p.split) {
+            heads = p.HQ;
+            groups = 1;
+        }
+    const int BH = p.B * heads;
     const int kt = blockIdx.x / BH;
-    const int b = (blockIdx.x % BH) / p.HK;
-    const int kh = blockIdx.x % p.HK;
+    const int b = (blockIdx.x % BH) / heads;
+    int kh = blockIdx.x % heads;
+    if constexpr (kMod)
+        if (p.split) {
+            g0 = kh % p.groups;
+            kh /= p.groups;
+        }
     const int k0 = kt * kKeys;
     int nrt = (p.SQ + kBRows - 1) / kBRows;
     int r_first = p.causal ? min(k0 / kBRows, nrt) : 0;
@@ -577,7 +589,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         }
     }
     const int per_head = nrt - r_first;
-    const int n = per_head * p.groups;
+    const int n = per_head * groups;
     const uint64_t wait_ns = p.wait_ns;
 
     if (tid == 0) {
@@ -618,7 +630,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
     };
     auto step_head = [&](int it, int& h, int& i0) {
         const int gi = it / per_head;
-        h = kh * p.groups + gi;
+        h = kh * p.groups + g0 + gi;
         i0 = (r_first + it - gi * per_head) * kBRows;
     };
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;  // this warp's TMEM lanes
@@ -812,27 +824,36 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                 for (int hf = 0; hf < 2; ++hf) {
                     Cols16 x;
                     tmem_ld16(x, tS + lane_off + part * 32 + hf * 16);
-                    const float f = p.cap_out != 0.f ? p.cap_in : p.scale_log2;
                     float y[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        y[e] = __uint_as_float(x.r[e]) * f;
-                    float c = 1.f;
+                        y[e] = __uint_as_float(x.r[e]);
+                    float c = p.scale_log2;
                     if (p.cap_out != 0.f) {
+                        scale_block(y, p.cap_in);
                         tanh_block(y);
                         c = p.cap_out;
                     }
-                    const float d0 = static_cast<float>(rb + hf * 16 - key);
+                    float z[16];  // minus lse2 and the distance bias
 #pragma unroll
                     for (int q4 = 0; q4 < 4; ++q4) {
                         const float4 l = l4[hf * 4 + q4];
-                        const float lv[4] = {l.x, l.y, l.z, l.w};
+                        z[4 * q4] = -l.x;
+                        z[4 * q4 + 1] = -l.y;
+                        z[4 * q4 + 2] = -l.z;
+                        z[4 * q4 + 3] = -l.w;
+                    }
+                    if (p.slopes) {
+                        const float d0 = static_cast<float>(rb + hf * 16 - key);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int j = 4 * q4 + e;
-                            const float bias = fmaf(-slope2, fabsf(d0 + static_cast<float>(j)), -lv[e]);
-                            pv[hf * 16 + j] = fast_exp2(fmaf(y[j], c, bias));
-                        }
+                        for (int j = 0; j < 16; ++j)
+                            z[j] = fmaf(-slope2, fabsf(d0 + static_cast<float>(j)), z[j]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float2 s = __ffma2_rn(make_float2(y[j], y[j + 1]), make_float2(c, c), make_float2(z[j], z[j + 1]));
+                        pv[hf * 16 + j] = fast_exp2(s.x);
+                        pv[hf * 16 + j + 1] = fast_exp2(s.y);
                     }
                     if (!plain) {
 #pragma unroll
@@ -848,8 +869,13 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                     // from here on p times the cap's factor
                     if (p.cap_out != 0.f) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            pv[hf * 16 + j] *= fmaf(-y[j], y[j], 1.f);
+                        for (int j = 0; j < 16; j += 2) {
+                            const float2 t2 = make_float2(y[j], y[j + 1]);
+                            const float2 f2 = __ffma2_rn(make_float2(-t2.x, -t2.y), t2, make_float2(1.f, 1.f));
+                            const float2 r = __fmul2_rn(make_float2(pv[hf * 16 + j], pv[hf * 16 + j + 1]), f2);
+                            pv[hf * 16 + j] = r.x;
+                            pv[hf * 16 + j + 1] = r.y;
+                        }
                     }
                 }
                 tmem_st16(w, tS + lane_off + part * 32);
@@ -989,7 +1015,15 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                 for (int j = 0; j < 32; ++j)
                     v[j] = 0.f;
             }
-            if (key_ok)
+            int64_t op = 0;  // of a split group's partial sums
+            bool split = false;
+            if constexpr (kMod) {
+                split = p.split;
+                op = (((static_cast<int64_t>(g0) * p.B + b) * p.HK + kh) * p.SK + key) * kD + part * 32;
+                if (split && key_ok)
+                    store_row<float>(p.part[0] + op, v);
+            }
+            if (key_ok && !split)
                 store_row<TO>(static_cast<TO*>(p.dk) + o, v);
             if (n > 0) {
                 Cols32 x;
@@ -998,7 +1032,10 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                 for (int j = 0; j < 32; ++j)
                     v[j] = __uint_as_float(x.r[j]);
             }
-            if (key_ok)
+            if constexpr (kMod)
+                if (split && key_ok)
+                    store_row<float>(p.part[1] + op, v);
+            if (key_ok && !split)
                 store_row<TO>(static_cast<TO*>(p.dv) + o, v);
         }
     }
@@ -1006,6 +1043,29 @@ __global__ void __launch_bounds__(kMainThreads, 1)
     __syncthreads();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(bars.tmem), "r"(512) : "memory");
+}
+
+// dk and dv of split groups: the partial sums in group order.  grid.y: dk, dv.
+template <typename TO>
+__global__ void __launch_bounds__(256) vjp_join_groups(const __grid_constant__ VjpScoredParams p)
+{
+    const int64_t n4 = static_cast<int64_t>(p.B) * p.HK * p.SK * (kD / 4);
+    const float4* part = reinterpret_cast<const float4*>(p.part[blockIdx.y]);
+    TO* out = static_cast<TO*>(blockIdx.y ? p.dv : p.dk);
+    for (int64_t e = blockIdx.x * 256ll + threadIdx.x; e < n4; e += gridDim.x * 256ll) {
+        float4 s = __ldcg(part + e);
+        for (int g = 1; g < p.groups; ++g) {
+            const float4 x = __ldcg(part + g * n4 + e);
+            s.x += x.x;
+            s.y += x.y;
+            s.z += x.z;
+            s.w += x.w;
+        }
+        if constexpr (std::is_same<TO, float>::value)
+            reinterpret_cast<float4*>(out)[e] = s;
+        else
+            reinterpret_cast<uint2*>(out)[e] = make_uint2(pack2<TO>(s.x, s.y), pack2<TO>(s.z, s.w));
+    }
 }
 
 template <bool kMod>
@@ -1086,18 +1146,44 @@ int launch_tc(const VjpParamsOf<kMod>& p, int dtype, bool f32_out, cudaStream_t 
         if (cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kMainSmem) != cudaSuccess)
             return PA_ERR_CUDA;
-        const long long grid = static_cast<long long>(p.B) * p.HK * ((p.SK + kKeys - 1) / kKeys);
+        int heads = p.HK;
+        if constexpr (kMod)
+            heads = p.split ? p.HQ : p.HK;
+        const long long grid = static_cast<long long>(p.B) * heads * ((p.SK + kKeys - 1) / kKeys);
         if (grid >= (1ll << 31))
             return PA_ERR_BAD_DIMS;
         fn<<<static_cast<unsigned>(grid), kMainThreads, kMainSmem, st>>>(p, qmap, gmap, kmap, vmap);
         if (cudaGetLastError() != cudaSuccess)
             return PA_ERR_CUDA;
         ++*launches;
+        if constexpr (kMod)
+            if (p.split) {
+                const long long n4 = static_cast<long long>(p.B) * p.HK * p.SK * (kD / 4);
+                const dim3 jg(static_cast<unsigned>((n4 + 255) / 256 < 152 * 8 ? (n4 + 255) / 256 : 152 * 8), 2);
+                if (f32_out)
+                    vjp_join_groups<float><<<jg, 256, 0, st>>>(p);
+                else if (bf)
+                    vjp_join_groups<__nv_bfloat16><<<jg, 256, 0, st>>>(p);
+                else
+                    vjp_join_groups<__half><<<jg, 256, 0, st>>>(p);
+                if (cudaGetLastError() != cudaSuccess)
+                    return PA_ERR_CUDA;
+                ++*launches;
+            }
     }
     return PA_OK;
 }
 
 }  // namespace
+
+// Few (batch, key/value head, key tile) triples leave SMs idle and, with a
+// prefix or a window, unequal work: below two CTAs an SM the groups' query
+// heads get a CTA each, and dk and dv are joined after (2, 12/4 heads, 1500
+// tokens, window and prefix: 24 triples of 36 steps among 72 of 15 took 186 us).
+bool vjp_tc_splits(int B, int HQ, int HK, int SK, int sms)
+{
+    return HQ > HK && static_cast<long long>(B) * HK * ((SK + kKeys - 1) / kKeys) < 2ll * sms;
+}
 
 bool vjp_tc_supported(int dtype, int D, int groups, int mask_kind)
 {

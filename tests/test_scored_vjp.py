@@ -290,6 +290,24 @@ def test_graph_replay_and_another_stream(pa):
     assert torch.allclose(got[0], plan.dq, rtol=1e-4, atol=1e-5)  # float32 reductions in another order
 
 
+def test_workspace_sizes(pa):
+    f, g = pa.LIB.pa_attention_vjp_scored_workspace_bytes, pa.LIB.pa_attention_vjp_workspace_bytes
+    # few key tiles and grouped heads: partial dk and dv of every query head
+    assert f(1, 4, 2, 200, 200, 128, 2, -1) == g(1, 4, 200, 128, 2, -1) + 2 * 4 * 200 * 128 * 4
+    # no groups, no tensor cores, many tiles: nothing on top
+    assert f(1, 4, 4, 200, 200, 128, 2, -1) == g(1, 4, 200, 128, 2, -1)
+    assert f(1, 4, 2, 200, 200, 64, 2, -1) == g(1, 4, 200, 64, 2, -1)
+    assert f(64, 32, 8, 2048, 2048, 128, 2, -1) == g(64, 32, 2048, 128, 2, -1)
+    assert f(1, 4, 3, 200, 200, 128, 2, -1) == f(1, 4, 2, 200, 200, 128, 9, -1) == 0
+
+
+@pytest.mark.gpu
+def test_more_key_tiles_than_the_split_takes(pa):
+    # 2 x 4 heads x 40 tiles: one CTA per group, no partial sums
+    x = make(80, "f16", 2, 8, 4, 70, 5000, 128)
+    compare(pa, x, modified(dict(softcap=12.0, prefix=700), 2, 8, False, 128), "f16", torch.float32)
+
+
 @pytest.mark.gpu
 def test_refused_arguments(pa):
     q, k, v, g = (t.cuda() for t in make(70, "f16", 1, 4, 2, 20, 20, 128))
