@@ -37,28 +37,33 @@ __device__ __forceinline__ void tanh_block(float (&y)[N])
 #pragma unroll
     for (int j = 0; j < N; j += 2)
         top = fmaxf(top, fmaxf(fabsf(y[j]), fabsf(y[j + 1])));
-    const bool wide = __any_sync(0xffffffffu, top > kMax);
+    // two loops, not a test per pair: a branch between the pairs would keep their
+    // chains from overlapping
+    if (!__any_sync(0xffffffffu, top > kMax)) {
 #pragma unroll
-    for (int j = 0; j < N; j += 2) {
-        const float2 v = make_float2(y[j], y[j + 1]);
-        const float2 z = __fmul2_rn(v, v);
-        float2 a = make_float2(kC[5], kC[5]);
+        for (int j = 0; j < N; j += 2) {
+            const float2 v = make_float2(y[j], y[j + 1]);
+            const float2 z = __fmul2_rn(v, v);
+            float2 a = make_float2(kC[5], kC[5]);
 #pragma unroll
-        for (int e = 4; e >= 0; --e)
-            a = __ffma2_rn(a, z, make_float2(kC[e], kC[e]));
-        a = __fmul2_rn(a, v);
-        if (wide) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float x = u ? v.y : v.x;
-                const float e = fast_exp2(fabsf(x) * -2.8853900817779268f);  // 2 log2(e)
-                const float far = copysignf(__fdividef(1.f - e, 1.f + e), x);
-                if (fabsf(x) > kMax)
-                    (u ? a.y : a.x) = far;
-            }
+            for (int e = 4; e >= 0; --e)
+                a = __ffma2_rn(a, z, make_float2(kC[e], kC[e]));
+            a = __fmul2_rn(a, v);
+            y[j] = a.x;
+            y[j + 1] = a.y;
         }
-        y[j] = a.x;
-        y[j + 1] = a.y;
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float x = y[j], z = x * x;
+            const float e = fast_exp2(fabsf(x) * -2.8853900817779268f);  // 2 log2(e)
+            const float far = copysignf(__fdividef(1.f - e, 1.f + e), x);
+            float a = kC[5];
+#pragma unroll
+            for (int k = 4; k >= 0; --k)
+                a = fmaf(a, z, kC[k]);
+            y[j] = fabsf(x) > kMax ? far : a * x;
+        }
     }
 }
 
