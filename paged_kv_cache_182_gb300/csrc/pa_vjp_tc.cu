@@ -71,9 +71,15 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kD = 128;         // head size of this path
 constexpr int kKeys = 128;      // keys per tile (both kernels)
 constexpr int kSRows = 128;     // query rows per CTA of the statistics kernel
-constexpr int kSoftmax = 256;   // statistics kernel: warps 0-7 softmax, 8 TMA, 9 MMA,
-constexpr int kDeltaWarps = 4;  // 10-13 delta and dq zeroing
-constexpr int kStatsThreads = kSoftmax + 64 + kDeltaWarps * 32;
+// Statistics kernel: softmax warps, then one TMA, one MMA, four for delta and
+// the zeroing of dq.  Plain scores: 8 softmax warps, two threads a row (four a
+// row were slower: the MMA issue is as long as the softmax).  Modified scores
+// take three times the arithmetic: 16, four threads a row.
+template <bool kMod>
+constexpr int kSoftWarps = kMod ? 16 : 8;
+constexpr int kDeltaWarps = 4;
+template <bool kMod>
+constexpr int kStatsThreads = (kSoftWarps<kMod> + 2 + kDeltaWarps) * 32;
 constexpr int kKStages = 4;     // statistics kernel: K ring depth
 constexpr int kHalf128 = 16384;  // one 64-column half of a 128-row tile, bytes
 
@@ -81,10 +87,10 @@ struct StatsBars {
     uint64_t q_full[2], q_empty[2], k_full[kKStages], k_empty[kKStages], s_full[2], s_free[2], fin;
     uint32_t tmem;
     int abort;
-    float xm[2][kSRows], xl[2][kSRows];  // the high-half thread's max and sum, by item parity
+    float xm[2][3][kSRows], xl[2][3][kSRows];  // the higher parts' max and sum of a row, by item parity
 };
 // Q (2 buffers x 2 halves), K ring (kKStages stages x 2 halves), then the barriers
-constexpr int kStatsBarBytes = 4096;
+constexpr int kStatsBarBytes = 8192;
 constexpr int kStatsSmem = (4 + 2 * kKStages) * kHalf128 + kStatsBarBytes;
 static_assert(sizeof(StatsBars) <= kStatsBarBytes, "statistics barrier area");
 static_assert(kStatsSmem <= 232448, "statistics shared memory");
@@ -171,11 +177,14 @@ __device__ __forceinline__ float2 unpack2(uint32_t w)
 // numbered row tile slowest, the row tiles that see the most keys (causal)
 // first.
 template <typename T, bool kMod>
-__global__ void __launch_bounds__(kStatsThreads, 1)
+__global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
     vjp_stats_tc(const __grid_constant__ VjpParamsOf<kMod> p, const __grid_constant__ CUtensorMap qmap,
                  const __grid_constant__ CUtensorMap kmap)
 {
     constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+    constexpr int SW = kSoftWarps<kMod>;   // softmax warps
+    constexpr int PARTS = SW / 4;          // threads a row
+    constexpr int COLS = kKeys / PARTS;    // key columns of a thread
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     if ((smem_u32(smem_raw) & 1023u) != 0) {
         if (threadIdx.x == 0 && p.status)
@@ -197,7 +206,7 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
             mbar_init(&bars.q_full[u], 1);
             mbar_init(&bars.q_empty[u], 1);
             mbar_init(&bars.s_full[u], 1);
-            mbar_init(&bars.s_free[u], kSoftmax / 32);  // one arrival per softmax warp
+            mbar_init(&bars.s_free[u], SW);  // one arrival per softmax warp
         }
         for (int s = 0; s < kKStages; ++s) {
             mbar_init(&bars.k_full[s], 1);
@@ -225,7 +234,7 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
             atomicOr(p.status, PA_STATUS_TIMEOUT);
     };
 
-    if (warp == 8) {
+    if (warp == SW) {
         // --------------------------------------------------------------- TMA
         if (lane == 0) {
             tma_prefetch_desc(&qmap);
@@ -272,7 +281,7 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
                 mbar_wait_bounded(&bars.q_full[q & 1], (q >> 1) & 1, wait_ns);
         }
         __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp == SW + 1) {
         // --------------------------------------------------------------- MMA
         if (lane == 0) {
             const uint32_t ka = smem_u32(sK);
@@ -320,10 +329,10 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp < kSoftmax / 32) {
-        // ------------------------------------------ statistics (two threads a row)
+    } else if (warp < SW) {
+        // --------------------------------------- statistics (PARTS threads a row)
         const int row = (warp & 3) * 32 + lane;
-        const int part = warp >> 2;  // key columns [64 part, 64 part + 64)
+        const int part = warp >> 2;  // key columns [COLS part, COLS part + COLS)
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         bool fault = false;
         int g = 0;
@@ -350,17 +359,19 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
                 tc_fence_after();
                 // raw scores (scale > 0 commutes with the maximum); eight
                 // independent partial maxima and sums keep the dependency chains short
-                float sc[64];
+                float sc[COLS];
                 float pm8[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     pm8[e] = -INFINITY;
-                const int kbase = it.tile(t) * kKeys + part * 64;
-                Cols32 xs[2];
-                tmem_ld32_issue(xs[0], tS + s * kKeys + lane_off + part * 64);
-                tmem_ld32_issue(xs[1], tS + s * kKeys + lane_off + part * 64 + 32);
-                tmem_ld_wait(xs[1]);
-                tmem_ld_wait(xs[0]);
+                const int kbase = it.tile(t) * kKeys + part * COLS;
+                Cols32 xs[COLS / 32];
+#pragma unroll
+                for (int c = 0; c < COLS / 32; ++c)
+                    tmem_ld32_issue(xs[c], tS + s * kKeys + lane_off + part * COLS + c * 32);
+#pragma unroll
+                for (int c = COLS / 32 - 1; c >= 0; --c)
+                    tmem_ld_wait(xs[c]);
                 if constexpr (kMod) {
                     tc_fence_before();
                     __syncwarp();
@@ -369,7 +380,7 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
                     // modified scores: base-2 units with a distance bias, else to be
                     // multiplied by c2 in the exponential
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < COLS / 32; ++c) {
                         float y[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
@@ -391,26 +402,26 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
                     }
                     // the warp's rows i_w .. i_w + 31 all see the block's keys?
                     const int i_w = it.i0 + (warp & 3) * 32;
-                    const bool plain = kbase + 64 <= it.pl ||
-                                       (kbase + 64 <= p.SK && (!p.causal || kbase + 63 <= i_w) &&
-                                        i_w + 31 - kbase < p.window && (p.causal || kbase + 63 - i_w < p.window));
+                    const bool plain = kbase + COLS <= it.pl ||
+                                       (kbase + COLS <= p.SK && (!p.causal || kbase + COLS - 1 <= i_w) &&
+                                        i_w + 31 - kbase < p.window && (p.causal || kbase + COLS - 1 - i_w < p.window));
                     if (!plain) {
 #pragma unroll
-                        for (int j = 0; j < 64; ++j)
+                        for (int j = 0; j < COLS; ++j)
                             if (!(kbase + j < p.SK && vjp_seen(p, it.pl, i, kbase + j)))
                                 sc[j] = -INFINITY;
                     }
 #pragma unroll
-                    for (int j = 0; j < 64; ++j)
+                    for (int j = 0; j < COLS; ++j)
                         pm8[j & 7] = fmaxf(pm8[j & 7], sc[j]);
                 } else {
                 // the mask test is taken once per tile (warp-uniform), never per
                 // score: a branch per score cost more than the rest of the tile
-                if (kbase + 63 >= it.nk || (p.causal && kbase + 63 > it.i0)) {
+                if (kbase + COLS - 1 >= it.nk || (p.causal && kbase + COLS - 1 > it.i0)) {
                     // keys kbase + jj with jj < lim are visible to row i
                     const int lim = min(p.SK, p.causal ? i + 1 : p.SK) - kbase;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < COLS / 32; ++c)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
                             const float v = c * 32 + j < lim ? __uint_as_float(xs[c].r[j]) : -INFINITY;
@@ -419,7 +430,7 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
                         }
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < COLS / 32; ++c)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
                             const float v = __uint_as_float(xs[c].r[j]);
@@ -444,28 +455,33 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
                     for (int e = 0; e < 8; ++e)
                         s8[e] = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 64; ++j)
+                    for (int j = 0; j < COLS; ++j)
                         s8[j & 7] += fast_exp2(fmaf(sc[j], c2, -mt));
                     const float sum = ((s8[0] + s8[1]) + (s8[2] + s8[3])) + ((s8[4] + s8[5]) + (s8[6] + s8[7]));
                     l = l * fast_exp2(m - mt) + sum;
                     m = mt;
                 }
             }
-            // merge the two halves of every row (both warps of a pair pass
-            // this barrier once per item, faulted or not)
-            if (part == 1) {
-                bars.xm[k & 1][row] = m;
-                bars.xl[k & 1][row] = l;
+            // merge the parts of every row (all warps of a row group pass this
+            // barrier once per item, faulted or not)
+            if (part > 0) {
+                bars.xm[k & 1][part - 1][row] = m;
+                bars.xl[k & 1][part - 1][row] = l;
             }
-            asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + (warp & 3)), "n"(PARTS * 32) : "memory");
             if (part == 0 && !fault) {
-                const float m1 = bars.xm[k & 1][row], l1 = bars.xl[k & 1][row];
-                const float mt = fmaxf(m, m1);
+                float mt = m;
+#pragma unroll
+                for (int q = 0; q < PARTS - 1; ++q)
+                    mt = fmaxf(mt, bars.xm[k & 1][q][row]);
                 const int64_t srow = (static_cast<int64_t>(it.b) * p.HQ + it.h) * p.sqp + i;
                 if (i >= p.SQ || mt == -INFINITY) {  // padding rows up to sqp, rows that see no key
                     p.lse[srow] = INFINITY;
                 } else {
-                    const float lt = l * exp2f(m - mt) + l1 * exp2f(m1 - mt);
+                    float lt = l * exp2f(m - mt);
+#pragma unroll
+                    for (int q = 0; q < PARTS - 1; ++q)
+                        lt += bars.xl[k & 1][q][row] * exp2f(bars.xm[k & 1][q][row] - mt);
                     p.lse[srow] = mt + log2f(lt);
                 }
             }
@@ -473,8 +489,10 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
     } else {
         // ------------------------------- delta = rowsum(y g), dq accumulator rows zeroed
         // warp dw takes rows 32 dw .. 32 dw + 31 of each item, two rows per
-        // load (16 lanes x 16 bytes a row), eight row pairs in flight
-        const int dw = warp - (kSoftmax / 32 + 2);
+        // load (16 lanes x 16 bytes a row), RP row pairs in flight (four where
+        // twice the softmax warps leave fewer registers)
+        constexpr int RP = kMod ? 4 : 8;
+        const int dw = warp - (SW + 2);
         const int half = lane >> 4, c16 = lane & 15;
         for (int k = 0;; ++k) {
             const int n = stats_item(k, C, G);
@@ -484,10 +502,10 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
             const int64_t r0 = (static_cast<int64_t>(it.b) * p.HQ + it.h) * p.SQ;
             const int64_t s0 = (static_cast<int64_t>(it.b) * p.HQ + it.h) * p.sqp;
 #pragma unroll 1
-            for (int rb = 0; rb < 32; rb += 16) {
-                uint4 yv[8], gv[8];
+            for (int rb = 0; rb < 32; rb += 2 * RP) {
+                uint4 yv[RP], gv[RP];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < RP; ++e) {
                     const int i = it.i0 + dw * 32 + rb + 2 * e + half;
                     if (i < p.SQ) {
                         const int64_t off = (r0 + i) * kD + c16 * 8;
@@ -499,7 +517,7 @@ __global__ void __launch_bounds__(kStatsThreads, 1)
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < RP; ++e) {
                     const uint32_t ya[4] = {yv[e].x, yv[e].y, yv[e].z, yv[e].w};
                     const uint32_t ga[4] = {gv[e].x, gv[e].y, gv[e].z, gv[e].w};
                     float acc[4];
@@ -1119,7 +1137,7 @@ int launch_tc(const VjpParamsOf<kMod>& p, int dtype, bool f32_out, cudaStream_t 
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
             return PA_ERR_CUDA;
         const long long grid = items < sms ? items : sms;
-        fn<<<static_cast<unsigned>(grid), kStatsThreads, kStatsSmem, st>>>(p, qmap, kmap);
+        fn<<<static_cast<unsigned>(grid), kStatsThreads<kMod>, kStatsSmem, st>>>(p, qmap, kmap);
         if (cudaGetLastError() != cudaSuccess)
             return PA_ERR_CUDA;
         ++*launches;
