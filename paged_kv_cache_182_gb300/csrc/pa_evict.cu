@@ -40,7 +40,7 @@ constexpr int kBins = 2048;
 constexpr int kKeys = 8;            // weights in flight per thread of the selection
 constexpr int kMoveThreads = 256;
 constexpr int kRun = 128;           // in place: rows of a run
-constexpr int kMoveBytes = 32768;   // other blocks: rows of one item, at most (one row when longer)
+constexpr int kMoveBytes = 16384;   // other blocks: rows of one item, at most (one row when longer)
 constexpr int kMoveRows = 256;
 constexpr int kMaxRowBytes = 65536;
 constexpr unsigned kAll32 = 0xffffffffu;
@@ -74,7 +74,21 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// The 32-bit word at the same shared-memory place in CTA `rank` of the cluster.
+// The two 32-bit words at the same shared-memory place in CTA `rank` of the cluster.
+__device__ __forceinline__ uint2 cluster_load2(const uint32_t* p, uint32_t rank)
+{
+    uint2 v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %2, %3;\n\t"
+        "ld.shared::cluster.v2.u32 {%0, %1}, [a];\n\t}"
+        : "=r"(v.x), "=r"(v.y)
+        : "r"(smem_u32(p)), "r"(rank)
+        : "memory");
+    return v;
+}
+
+// One of them.
 __device__ __forceinline__ uint32_t cluster_load(const uint32_t* p, uint32_t rank)
 {
     uint32_t v;
@@ -119,7 +133,7 @@ template <int T, int C>
 __global__ void __launch_bounds__(T) pa_evict_select(const __grid_constant__ EvictParams p)
 {
     constexpr int kSelThreads = T, kSelWarps = T / 32, kOwn = kBins / T;
-    __shared__ uint32_t hist[2][kBins];
+    __shared__ __align__(8) uint32_t hist[2][kBins];
     __shared__ uint32_t wsum[kSelWarps];
     __shared__ uint32_t pick[3];               // chosen digit, still needed in it, its count
     __shared__ uint32_t cnt[kSelWarps][2];     // tokens taken outright / at the threshold, by warp
@@ -216,16 +230,19 @@ __global__ void __launch_bounds__(T) pa_evict_select(const __grid_constant__ Evi
         uint32_t v[kOwn], sum = 0;
         const int top = kBins - 1 - kOwn * tid;
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-            v[i] = 0;
-            if (C == 1) {
-                v[i] = h[top - i];
-            } else {
+        for (int i = 0; i < kOwn; i += 2) {
+            uint2 two = C == 1 ? *reinterpret_cast<const uint2*>(&h[top - i - 1]) : make_uint2(0, 0);
+            if (C > 1) {
 #pragma unroll
-                for (int c = 0; c < C; ++c)
-                    v[i] += cluster_load(&h[top - i], c);
+                for (int c = 0; c < C; ++c) {
+                    const uint2 r = cluster_load2(&h[top - i - 1], c);
+                    two.x += r.x;
+                    two.y += r.y;
+                }
             }
-            sum += v[i];
+            v[i] = two.y;
+            v[i + 1] = two.x;
+            sum += two.x + two.y;
         }
         uint32_t incl = sum;
 #pragma unroll

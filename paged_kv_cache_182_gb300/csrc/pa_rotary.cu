@@ -27,8 +27,8 @@
 namespace pa {
 namespace {
 
-constexpr int kRotThreads = 256;
-constexpr int kRotHeads = 4;  // heads in flight per thread
+constexpr int kRotThreads = 256;  // at most
+constexpr int kRotHeads = 2;  // heads in flight per thread
 
 struct RotaryParams {
     const void* x[3];       // q, k, v
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kRotThreads) pa_rotary_kernel(const __grid_con
     const int rows = min(p.rows_cta, p.N - n0);
     const int per_row = MODE == kHalves ? (p.D - half) / V : p.D / V;
     const int units = p.rows_cta * per_row;
-    const int groups = kRotThreads / units;
+    const int groups = static_cast<int>(blockDim.x) / units;
     const int unit = threadIdx.x % units, group = threadIdx.x / units;
     const int row = unit / per_row, v = unit - row * per_row;
     const bool live = group < groups && row < rows;
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kRotThreads) pa_rotary_kernel(const __grid_con
         }
     };
     load();
-    for (int i = threadIdx.x; i < rows * half; i += kRotThreads) {
+    for (int i = threadIdx.x; i < rows * half; i += static_cast<int>(blockDim.x)) {
         const int r = i / half;
         tab[i] = turn(__ldg(p.positions + static_cast<int64_t>(b) * p.N + n0 + r), __ldg(p.table + (i - r * half)), p.factor,
                       p.inverse);
@@ -404,11 +404,15 @@ extern "C" int pa_rotary(const void* q, const void* k, const int32_t* positions,
     p.factor = o.factor;
     p.inverse = o.inverse ? 1 : 0;
     const int mode = o.interleaved ? kSide : (rot / 2) % V == 0 ? kHalves : kAny;
-    // A CTA: a few positions (about 64 units of 16 or 32 bytes, so that four
-    // threads share a unit's heads), 32 KB of table at most; and as many heads as
-    // two rounds of its threads take, fewer where the call would leave SMs idle.
+    // Small CTAs: 64 threads (more only where a row has more vectors), about 16
+    // units of 16 or 32 bytes, so that four threads share a unit's heads; 32 KB
+    // of table at most; and as many heads as four rounds of two take, fewer
+    // where the call would leave SMs idle.  [4, 32 + 8, 2048, 128] bf16 (168 MB):
+    // 30.7 us, 5.5 TB/s; 256 threads and 64 units 33.7, with four heads a round
+    // and two rounds 36.1.
     const int per_row = mode == kHalves ? (D - rot / 2) / V : D / V;
-    int rows = 64 / per_row;
+    const int threads = per_row > 128 ? 256 : per_row > 64 ? 128 : 64;
+    int rows = 16 / per_row;
     const int fit = 32768 / (rot / 2 * static_cast<int>(sizeof(float2)));
     rows = rows < 1 ? 1 : rows;
     rows = rows > fit ? fit : rows;
@@ -417,8 +421,8 @@ extern "C" int pa_rotary(const void* q, const void* k, const int32_t* positions,
     while (rows > 1 && ctas(rows) < 304)
         --rows;
     p.rows_cta = rows;
-    const int groups = kRotThreads / (rows * per_row);
-    int rounds = 2;
+    const int groups = threads / (rows * per_row);
+    int rounds = 4;
     p.head_cta = groups * kRotHeads * rounds;
     while (p.head_cta > groups && ctas(rows) * ((p.heads + p.head_cta - 1) / p.head_cta) < 152)
         p.head_cta -= groups;
@@ -428,7 +432,7 @@ extern "C" int pa_rotary(const void* q, const void* k, const int32_t* positions,
         return PA_ERR_BAD_DIMS;
     const RotFn fn = o.dtype == PA_F32 ? pick_rotary<float>(mode) : o.dtype == PA_F16 ? pick_rotary<__half>(mode) : pick_rotary<__nv_bfloat16>(mode);
     const size_t smem = static_cast<size_t>(p.rows_cta) * (rot / 2) * sizeof(float2);
-    fn<<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), kRotThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
+    fn<<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), threads, smem, static_cast<cudaStream_t>(stream)>>>(p);
     if (cudaGetLastError() != cudaSuccess)
         return PA_ERR_CUDA;
     count_launches(1);

@@ -7,18 +7,6 @@
 
 namespace pa {
 
-// y *= f, two an instruction.
-template <int N>
-__device__ __forceinline__ void scale_block(float (&y)[N], float f)
-{
-#pragma unroll
-    for (int j = 0; j < N; j += 2) {
-        const float2 r = __fmul2_rn(make_float2(y[j], y[j + 1]), make_float2(f, f));
-        y[j] = r.x;
-        y[j + 1] = r.y;
-    }
-}
-
 // tanh of N scores (times 1 / cap), N even: an odd polynomial of degree 11
 // where every score of the warp is within 0.7 -- fitted here for the least
 // largest relative error of tanh(y) / y in y^2, 1.4e-8 -- two scores an
@@ -63,6 +51,66 @@ __device__ __forceinline__ void tanh_block(float (&y)[N])
             for (int k = 4; k >= 0; --k)
                 a = fmaf(a, z, kC[k]);
             y[j] = fabsf(x) > kMax ? far : a * x;
+        }
+    }
+}
+
+// The same for raw dot products under a cap, tanh(f x), with the factor in the
+// polynomial's coefficients: of degree 7 for |f x| <= 0.5 (largest relative
+// error 5.4e-7, a thousandth of the 16-bit rounding of the weights that follow),
+// five operations a score.  The backward's kernels use it: they are bound by
+// the arithmetic of their scores.
+struct TanhScaled {
+    float2 c[4];  // c_k f^(2 k + 1), twice
+    float f;
+    float top;    // 0.5 / |f|; negative: f^7 is no normal number, scores are scaled first
+};
+
+inline TanhScaled tanh_scaled(float f)
+{
+    constexpr float kC[4] = {0.999999456f, -0.333263179f, 0.131902966f, -0.0444022255f};
+    TanhScaled t{};
+    t.f = f;
+    const float a = f < 0.f ? -f : f;
+    t.top = a >= 1e-5f && a <= 1e4f ? 0.5f / a : -1.f;
+    float pw = f;
+    for (int k = 0; k < 4; ++k, pw *= f * f)
+        t.c[k] = make_float2(kC[k] * pw, kC[k] * pw);
+    return t;
+}
+
+template <int N>
+__device__ __forceinline__ void tanh_block_scaled(float (&x)[N], const TanhScaled& t)
+{
+    if (t.top < 0.f) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            x[j] *= t.f;
+        tanh_block(x);
+        return;
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; j += 2)
+        top = fmaxf(top, fmaxf(fabsf(x[j]), fabsf(x[j + 1])));
+    if (!__any_sync(0xffffffffu, top > t.top)) {
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+            const float2 v = make_float2(x[j], x[j + 1]);
+            const float2 z = __fmul2_rn(v, v);
+            float2 a = __ffma2_rn(t.c[3], z, t.c[2]);
+            a = __ffma2_rn(a, z, t.c[1]);
+            a = __ffma2_rn(a, z, t.c[0]);
+            a = __fmul2_rn(a, v);
+            x[j] = a.x;
+            x[j + 1] = a.y;
+        }
+    } else {
+        const float g = fabsf(t.f) * -2.8853900817779268f;  // 2 log2(e)
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float e = fast_exp2(fabsf(x[j]) * g);
+            x[j] = copysignf(__fdividef(1.f - e, 1.f + e), x[j] * t.f);
         }
     }
 }

@@ -9,6 +9,8 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "pa_tanh.cuh"
+
 namespace pa {
 
 constexpr float kVjpLog2e = 1.4426950408889634f;
@@ -46,6 +48,8 @@ struct VjpScoredParams : VjpParams {
     const float* slopes;    // [HQ], or NULL
     const int32_t* prefix;  // [B], or NULL
     float cap_in, cap_out;  // scale / cap, cap * log2(e); 0 without a cap
+    TanhScaled tanh;        // of cap_in
+    int bounded;            // a cap of at most 69 and no slopes: 2^|score| needs no maximum taken off
     int window;             // INT_MAX: none
     // tensor cores, split: one CTA per query head instead of per group, its dk and
     // dv in part[0] and part[1] [groups][B][HK][SK][D], summed in group order after

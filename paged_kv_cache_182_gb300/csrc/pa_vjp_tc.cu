@@ -385,10 +385,8 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             y[j] = __uint_as_float(xs[c].r[j]);
-                        if (p.cap_out != 0.f) {
-                            scale_block(y, p.cap_in);
-                            tanh_block(y);
-                        }
+                        if (p.cap_out != 0.f)
+                            tanh_block_scaled(y, p.tanh);
                         if (p.slopes) {
                             const float f = p.cap_out != 0.f ? p.cap_out : p.scale_log2;
                             const float d0 = static_cast<float>(i - kbase - c * 32);
@@ -410,6 +408,18 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
                         for (int j = 0; j < COLS; ++j)
                             if (!(kbase + j < p.SK && vjp_seen(p, it.pl, i, kbase + j)))
                                 sc[j] = -INFINITY;
+                    }
+                    if (p.bounded) {
+                        // scores within +-100: the sum of their powers of two needs no maximum
+                        float2 s4[4] = {};
+#pragma unroll
+                        for (int j = 0; j < COLS; j += 2) {
+                            const float2 e = __fmul2_rn(make_float2(sc[j], sc[j + 1]), make_float2(p.cap_out, p.cap_out));
+                            s4[(j >> 1) & 3] = __fadd2_rn(s4[(j >> 1) & 3], make_float2(fast_exp2(e.x), fast_exp2(e.y)));
+                        }
+                        m = 0.f;
+                        l += ((s4[0].x + s4[0].y) + (s4[1].x + s4[1].y)) + ((s4[2].x + s4[2].y) + (s4[3].x + s4[3].y));
+                        continue;
                     }
 #pragma unroll
                     for (int j = 0; j < COLS; ++j)
@@ -482,7 +492,8 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
 #pragma unroll
                     for (int q = 0; q < PARTS - 1; ++q)
                         lt += bars.xl[k & 1][q][row] * exp2f(bars.xm[k & 1][q][row] - mt);
-                    p.lse[srow] = mt + log2f(lt);
+                    // (a bounded row that sees no key has summed zeros)
+                    p.lse[srow] = kMod && lt == 0.f ? INFINITY : mt + log2f(lt);
                 }
             }
         }
@@ -848,8 +859,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                         y[e] = __uint_as_float(x.r[e]);
                     float c = p.scale_log2;
                     if (p.cap_out != 0.f) {
-                        scale_block(y, p.cap_in);
-                        tanh_block(y);
+                        tanh_block_scaled(y, p.tanh);
                         c = p.cap_out;
                     }
                     float z[16];  // minus lse2 and the distance bias

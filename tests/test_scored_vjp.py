@@ -187,6 +187,23 @@ def test_tensor_cores_match_64_bits(pa, shape, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("cap", [0.3, 60.0, 75.0, 1e3, 1e6])
+def test_caps_of_every_size(pa, cap):
+    # a cap that saturates nearly all scores, both sides of the one that needs no
+    # maximum, and one so large that it changes nothing
+    x = make(15, "f16", 1, 2, 1, 200, 300, 128)
+    for mod in (dict(softcap=cap), dict(softcap=cap, slopes=True, window=90)):
+        compare(pa, x, modified(mod, 1, 2, False, 128), "f16", torch.float32)
+
+
+@pytest.mark.gpu
+def test_scores_on_both_sides_of_the_polynomial(pa):
+    q, k, v, g = make(16, "bf16", 1, 2, 1, 300, 300, 128)
+    q = torch.where(torch.rand(q.shape[2], 1, generator=torch.Generator().manual_seed(1)) < 0.3, 8 * q, q).to(q.dtype)
+    compare(pa, (q, k, v, g), modified(dict(softcap=15.0), 1, 2, True, 128), "bf16", torch.float32)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("causal", [False, True])
 def test_long_rows_windows_and_skipped_tiles(pa, causal):
     x = make(9, "bf16", 1, 2, 1, 1500, 1500, 128)
