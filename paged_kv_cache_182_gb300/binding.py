@@ -23,7 +23,6 @@ from __future__ import annotations
 
 import ctypes
 import math
-from fractions import Fraction
 from pathlib import Path
 
 import torch
@@ -920,15 +919,18 @@ def rotary_frequencies(rot: int, *, base: float = 10000.0, scaling=None):
     return inv, factor
 
 
-# 1 / (2 pi) to 2^-192: the table entries below need more than 64 bits of it
-_INV_2PI = (Fraction(1) / 2 / Fraction("3.14159265358979323846264338327950288419716939937510582097494459"))
+# floor(2^256 / (2 pi)): the table entries below need more than 64 bits of 1 / (2 pi)
+_INV_2PI = 10 ** 80 * 2 ** 255 // 314159265358979323846264338327950288419716939937510582097494459230781640628620899
 
 
 def rotary_table(rot: int, *, base: float = 10000.0, scaling=None, device="cuda") -> RotaryTable:
     """The table of a rotary embedding (see ``rotary_frequencies``), made once
     and kept: each pair's angle per position as a 64-bit fraction of a turn."""
     inv, factor = rotary_frequencies(rot, base=base, scaling=scaling)
-    turns = [int(Fraction(x) * _INV_2PI * 2 ** 64 + Fraction(1, 2)) % 2 ** 64 for x in inv]
+    turns = []
+    for x in inv:
+        n, d = x.as_integer_ratio()  # d is a power of two
+        turns.append(((n * _INV_2PI // d >> 191) + 1 >> 1) % 2 ** 64)
     signed = [t - 2 ** 64 if t >= 2 ** 63 else t for t in turns]
     return RotaryTable(torch.tensor(signed, dtype=torch.int64, device=device), factor, rot)
 
