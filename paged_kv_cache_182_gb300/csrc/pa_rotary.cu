@@ -406,16 +406,15 @@ extern "C" int pa_rotary(const void* q, const void* k, const int32_t* positions,
     const int mode = o.interleaved ? kSide : (rot / 2) % V == 0 ? kHalves : kAny;
     // Small CTAs: 64 threads (more only where a row has more vectors).  With many
     // heads about 16 units of 16 or 32 bytes, so that four threads share a
-    // unit's heads; with fewer heads more units, so that a CTA still has a few
-    // rows per thread; 32 KB of table at most; and as many heads as four rounds
+    // unit's heads; with fewer than 20 heads a unit per thread, so that a
+    // CTA still has enough to do; 32 KB of table at most; and as many heads as four rounds
     // of two take, fewer where the call would leave SMs idle.
     // [4, 32 + 8, 2048, 128] bf16 (168 MB): 30.7 us, 5.5 TB/s (256 threads and
     // 64 units 33.7); [31, 8 + 2, 1492, 64] f32 (237 MB): 61 us with 16 units,
-    // 48 with 32; [4, 1 + 1, 16384, 128] bf16: 43 us with 16, 23 with 64.
+    // 49 with 64; [4, 1 + 1, 16384, 128] bf16: 43 us with 16, 23 with 64.
     const int per_row = mode == kHalves ? (D - rot / 2) / V : D / V;
     const int threads = per_row > 128 ? 256 : per_row > 64 ? 128 : 64;
-    const int want = p.heads >= 20 ? 16 : p.heads >= 8 ? 32 : 64;
-    int rows = (want + per_row - 1) / per_row;
+    int rows = p.heads >= 20 ? (15 + per_row) / per_row : threads / per_row;
     if (rows * per_row > threads)
         rows = threads / per_row;
     const int fit = 32768 / (rot / 2 * static_cast<int>(sizeof(float2)));
