@@ -762,6 +762,12 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                 for (int ks = 0; ks < kBRows / 16; ++ks)
                     umma_ts(tdV, tS + (ks >> 1) * 32 + (ks & 1) * 8, at(dG_mn, qo + ks * 2048), id_o,
                             it > 0 || ks > 0);
+                // modified scores: S^T of the next step at once (in the pipe after
+                // dV, whose P it overwrites), so that its P is computed while this
+                // step's dK and dQ^T run
+                if constexpr (kMod)
+                    if (it + 1 < n && !(ok = issue_s(it + 1)))
+                        break;
                 ok = mbar_wait_bounded(&bars.ds_ready, it & 1, wait_ns);
                 if (!ok)
                     break;
@@ -779,8 +785,9 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                 umma_commit(&bars.dq_full);
                 umma_commit(&bars.qd_empty[st]);
                 if (it + 1 < n) {
-                    if (!(ok = issue_s(it + 1)))
-                        break;
+                    if constexpr (!kMod)
+                        if (!(ok = issue_s(it + 1)))
+                            break;
                     ok = mbar_wait_bounded(&bars.dq_free, it & 1, wait_ns);
                     if (!ok)
                         break;
@@ -823,25 +830,23 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                         red_add(dst + static_cast<int64_t>(j) * kD, v[j]);
             }
         };
-        for (int it = 0; it < n; ++it) {
-            const int st = it & 1;
-            int h, i0;
-            step_head(it, h, i0);
-            bool got = !fault && !*abort_flag && mbar_wait_bounded(&bars.s_full, it & 1, wait_ns);
-            got = got && mbar_wait_bounded(&bars.qd_full[st], (it >> 1) & 1, wait_ns);
-            if (!__all_sync(kAll, got)) {
-                fault = true;
-                break;
-            }
-            tc_fence_after();
-            const int rb = i0 + part * 32;  // first row of this thread's columns
-            // no mask on this thread's block: every key real, every row real,
-            // and (causal) the last key at or before the first row (warp-uniform)
-            bool plain = keys_all && rb + 32 <= p.SQ && (!p.causal || k0 + kKeys - 1 <= rb);
-            const float4* l4 = reinterpret_cast<const float4*>(sStat + st * 256 + part * 32);
-            const float4* d4 = reinterpret_cast<const float4*>(sStat + st * 256 + 128 + part * 32);
-            float pv[32];
-            if constexpr (kMod) {
+        if constexpr (kMod) {
+            // Modified scores: P of step it + 1 is computed between dS^T of step it
+            // and the wait for its dQ^T -- a third of the step's arithmetic, which
+            // would otherwise stand between S^T and everything after it.
+            float pv[32];        // p times the cap's factor, then ds
+            bool plain = false;  // of the step whose p is in pv: no mask on this thread's block
+            auto make_p = [&](int it) {
+                const int st = it & 1;
+                int h, i0;
+                step_head(it, h, i0);
+                bool got = !fault && !*abort_flag && mbar_wait_bounded(&bars.s_full, it & 1, wait_ns);
+                got = got && mbar_wait_bounded(&bars.qd_full[st], (it >> 1) & 1, wait_ns);
+                if (!__all_sync(kAll, got))
+                    return false;
+                tc_fence_after();
+                const int rb = i0 + part * 32;  // first row of this thread's columns
+                const float4* l4 = reinterpret_cast<const float4*>(sStat + st * 256 + part * 32);
                 const float slope2 = p.slopes ? __ldg(p.slopes + h) * kVjpLog2e : 0.f;
                 // every row of the block sees every key of the tile, as far as the rule goes
                 const bool in_rule = k0 + kKeys <= pl ||
@@ -908,114 +913,226 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                 }
                 tmem_st16(w, tS + lane_off + part * 32);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            } else {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bars.p_ready);
+                return true;
+            };
+            auto make_ds = [&](int it) {
+                if (!__all_sync(kAll, mbar_wait_bounded(&bars.dp_full, it & 1, wait_ns)))
+                    return false;
+                const float4* d4 = reinterpret_cast<const float4*>(sStat + (it & 1) * 256 + 128 + part * 32);
+                tc_fence_after();
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                Cols16 x;
-                tmem_ld16(x, tS + lane_off + part * 32 + hf * 16);
-                const float c = p.scale_log2;
+                for (int hf = 0; hf < 2; ++hf) {
+                    Cols16 x;
+                    tmem_ld16(x, tP + lane_off + part * 32 + hf * 16);
+                    const float sc = p.scale;
 #pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4) {
-                    const float4 l = l4[hf * 4 + q4];
-                    const float lv[4] = {l.x, l.y, l.z, l.w};
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        const float4 d = d4[hf * 4 + q4];
+                        const float dv[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        pv[hf * 16 + 4 * q4 + e] = fast_exp2(fmaf(__uint_as_float(x.r[4 * q4 + e]), c, -lv[e]));
-                }
-            }
-            if (!plain) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int row = rb + j;
-                    if (!(key_ok && row < p.SQ && (!p.causal || key <= row)))
-                        pv[j] = 0.f;
-                }
-            }
-            // P (16-bit pairs) into the first 16 of this thread's 32 S^T columns
-            {
-                uint32_t w[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    w[e] = pack2<T>(pv[2 * e], pv[2 * e + 1]);
-                tmem_st16(w, tS + lane_off + part * 32);
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&bars.p_ready);
-            got = __all_sync(kAll, mbar_wait_bounded(&bars.dp_full, it & 1, wait_ns));
-            if (!got) {
-                fault = true;
-                break;
-            }
-            tc_fence_after();
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                Cols16 x;
-                tmem_ld16(x, tP + lane_off + part * 32 + hf * 16);
-                const float sc = p.scale;
-#pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4) {
-                    const float4 d = d4[hf * 4 + q4];
-                    const float dv[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = hf * 16 + 4 * q4 + e;
-                        const float ds = pv[j] * sc * (__uint_as_float(x.r[4 * q4 + e]) - dv[e]);
-                        // rows past SQ: p = 0, and their delta is not defined
-                        pv[j] = plain || pv[j] != 0.f ? ds : 0.f;
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = hf * 16 + 4 * q4 + e;
+                            const float ds = pv[j] * sc * (__uint_as_float(x.r[4 * q4 + e]) - dv[e]);
+                            // rows past SQ: p = 0, and their delta is not defined
+                            pv[j] = plain || pv[j] != 0.f ? ds : 0.f;
+                        }
                     }
                 }
-            }
-            // dS^T (K-major over rows): rows 32 part .. + 31 are chunks 4 (part & 1) ..
-            // + 3 of the 128-byte row of this key in row half part >> 1
-            unsigned char* sb = sS + (part >> 1) * kHalf128;
+                // dS^T (K-major over rows): rows 32 part .. + 31 are chunks 4 (part & 1) ..
+                // + 3 of the 128-byte row of this key in row half part >> 1
+                unsigned char* sb = sS + (part >> 1) * kHalf128;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t w[4];
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t w[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w[e] = pack2<T>(pv[8 * c + 2 * e], pv[8 * c + 2 * e + 1]);
-                *reinterpret_cast<uint4*>(sb + sw128(ln, (part & 1) * 4 + c)) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&bars.ds_ready);
-            if (held_dst) {
-                reduce_half(held_dst, held, held_rows);
-                held_dst = nullptr;
-            }
-            // dQ^T of the step (lane = d, columns = rows): read, hand the columns
-            // back for the next dP^T, then add into the float32 accumulator
-            got = __all_sync(kAll, mbar_wait_bounded(&bars.dq_full, it & 1, wait_ns));
-            if (!got) {
-                fault = true;
-                break;
-            }
-            tc_fence_after();
-            {
-                Cols32 x;
-                tmem_ld32(x, tP + lane_off + part * 32);
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = pack2<T>(pv[8 * c + 2 * e], pv[8 * c + 2 * e + 1]);
+                    *reinterpret_cast<uint4*>(sb + sw128(ln, (part & 1) * 4 + c)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bars.ds_ready);
+                return true;
+            };
+            auto drain_dq = [&](int it) {
+                int h, i0;
+                step_head(it, h, i0);
+                if (!__all_sync(kAll, mbar_wait_bounded(&bars.dq_full, it & 1, wait_ns)))
+                    return false;
+                tc_fence_after();
+                const int rb = i0 + part * 32;
+                float* dst = p.dq_sum + ((static_cast<int64_t>(b) * p.HQ + h) * p.SQ + rb) * kD + ln;
+                const int rows = min(32, p.SQ - rb);
+                Cols16 x, y;
+                tmem_ld16(x, tP + lane_off + part * 32);
+                tmem_ld16(y, tP + lane_off + part * 32 + 16);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&bars.dq_free);
-                float* dst = p.dq_sum + ((static_cast<int64_t>(b) * p.HQ + h) * p.SQ + rb) * kD + ln;
-                const int rows = min(32, p.SQ - rb);
                 float v[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     v[j] = __uint_as_float(x.r[j]);
-                    held[j] = __uint_as_float(x.r[16 + j]);
+                    held[j] = __uint_as_float(y.r[j]);
                 }
                 reduce_half(dst, v, rows);
                 if (rows > 16) {
                     held_dst = dst + static_cast<int64_t>(16) * kD;
                     held_rows = rows - 16;
+                }
+                return true;
+            };
+            for (int it = -1; it < n; ++it) {
+                if (it >= 0 && !make_ds(it)) {
+                    fault = true;
+                    break;
+                }
+                if (held_dst) {
+                    reduce_half(held_dst, held, held_rows);
+                    held_dst = nullptr;
+                }
+                if (it + 1 < n && !make_p(it + 1)) {
+                    fault = true;
+                    break;
+                }
+                if (it >= 0 && !drain_dq(it)) {
+                    fault = true;
+                    break;
+                }
+            }
+        } else {
+            for (int it = 0; it < n; ++it) {
+                const int st = it & 1;
+                int h, i0;
+                step_head(it, h, i0);
+                bool got = !fault && !*abort_flag && mbar_wait_bounded(&bars.s_full, it & 1, wait_ns);
+                got = got && mbar_wait_bounded(&bars.qd_full[st], (it >> 1) & 1, wait_ns);
+                if (!__all_sync(kAll, got)) {
+                    fault = true;
+                    break;
+                }
+                tc_fence_after();
+                const int rb = i0 + part * 32;  // first row of this thread's columns
+                // no mask on this thread's block: every key real, every row real,
+                // and (causal) the last key at or before the first row (warp-uniform)
+                const bool plain = keys_all && rb + 32 <= p.SQ && (!p.causal || k0 + kKeys - 1 <= rb);
+                const float4* l4 = reinterpret_cast<const float4*>(sStat + st * 256 + part * 32);
+                const float4* d4 = reinterpret_cast<const float4*>(sStat + st * 256 + 128 + part * 32);
+                float pv[32];
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    Cols16 x;
+                    tmem_ld16(x, tS + lane_off + part * 32 + hf * 16);
+                    const float c = p.scale_log2;
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        const float4 l = l4[hf * 4 + q4];
+                        const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            pv[hf * 16 + 4 * q4 + e] = fast_exp2(fmaf(__uint_as_float(x.r[4 * q4 + e]), c, -lv[e]));
+                    }
+                }
+                if (!plain) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int row = rb + j;
+                        if (!(key_ok && row < p.SQ && (!p.causal || key <= row)))
+                            pv[j] = 0.f;
+                    }
+                }
+                // P (16-bit pairs) into the first 16 of this thread's 32 S^T columns
+                {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        w[e] = pack2<T>(pv[2 * e], pv[2 * e + 1]);
+                    tmem_st16(w, tS + lane_off + part * 32);
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bars.p_ready);
+                got = __all_sync(kAll, mbar_wait_bounded(&bars.dp_full, it & 1, wait_ns));
+                if (!got) {
+                    fault = true;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    Cols16 x;
+                    tmem_ld16(x, tP + lane_off + part * 32 + hf * 16);
+                    const float sc = p.scale;
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        const float4 d = d4[hf * 4 + q4];
+                        const float dv[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = hf * 16 + 4 * q4 + e;
+                            const float ds = pv[j] * sc * (__uint_as_float(x.r[4 * q4 + e]) - dv[e]);
+                            // rows past SQ: p = 0, and their delta is not defined
+                            pv[j] = plain || pv[j] != 0.f ? ds : 0.f;
+                        }
+                    }
+                }
+                // dS^T (K-major over rows): rows 32 part .. + 31 are chunks 4 (part & 1) ..
+                // + 3 of the 128-byte row of this key in row half part >> 1
+                unsigned char* sb = sS + (part >> 1) * kHalf128;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = pack2<T>(pv[8 * c + 2 * e], pv[8 * c + 2 * e + 1]);
+                    *reinterpret_cast<uint4*>(sb + sw128(ln, (part & 1) * 4 + c)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bars.ds_ready);
+                if (held_dst) {
+                    reduce_half(held_dst, held, held_rows);
+                    held_dst = nullptr;
+                }
+                // dQ^T of the step (lane = d, columns = rows): read, hand the columns
+                // back for the next dP^T, then add into the float32 accumulator
+                got = __all_sync(kAll, mbar_wait_bounded(&bars.dq_full, it & 1, wait_ns));
+                if (!got) {
+                    fault = true;
+                    break;
+                }
+                tc_fence_after();
+                {
+                    Cols32 x;
+                    tmem_ld32(x, tP + lane_off + part * 32);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&bars.dq_free);
+                    float* dst = p.dq_sum + ((static_cast<int64_t>(b) * p.HQ + h) * p.SQ + rb) * kD + ln;
+                    const int rows = min(32, p.SQ - rb);
+                    float v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        v[j] = __uint_as_float(x.r[j]);
+                        held[j] = __uint_as_float(x.r[16 + j]);
+                    }
+                    reduce_half(dst, v, rows);
+                    if (rows > 16) {
+                        held_dst = dst + static_cast<int64_t>(16) * kD;
+                        held_rows = rows - 16;
+                    }
                 }
             }
         }
