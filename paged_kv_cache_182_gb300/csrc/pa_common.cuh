@@ -99,6 +99,7 @@ struct SplitParams {
 // (sequence b: `gap` tokens from token `pend` on, both multiples of TT, kept in
 // shared memory) are left out, and key c of the compressed sequence is key
 // c + (c >= pend ? gap : 0) of the real one.
+constexpr int kNoWindow = (1 << 30) + 64;  // beyond every distance (lengths are below 2^30)
 struct ScoredParams : SplitParams {
     const float* slopes;    // [H] distance slopes, or NULL
     const int32_t* prefix;  // [B] keys visible to every row, or NULL
@@ -107,7 +108,7 @@ struct ScoredParams : SplitParams {
     float* lse;             // [B * KV * R] log2 of the softmax denominators, or NULL
     float cap_in;           // scale / cap: the dot's factor inside the tanh
     float cap_out;          // cap * log2(e), or 0 without a cap
-    int window;             // |row - key| < window; INT_MAX: none
+    int window;             // |row - key| < window; kNoWindow: none
     int score_tokens;       // tokens per segment of `scores`
     int gap_off, pend_off;  // shared memory: gap [B], pend [B]
 };

@@ -585,7 +585,7 @@ struct ScoreSpan<true> {
     {
         const int hi = max(lim[0] > 0 ? r[0].row : INT_MIN, lim[1] > 0 ? r[1].row : INT_MIN);
         const int lo = min(lim[0] > 0 ? r[0].row : INT_MAX, lim[1] > 0 ? r[1].row : INT_MAX);
-        // (rows are at most 2^30: no overflow against a window of INT_MAX)
+        // (rows and windows are about 2^30 at most: no overflow)
         wlo = max(__reduce_max_sync(kFull, hi), 0) - p.window + 1;
         wlo_any = min(__reduce_min_sync(kFull, lo), 1 << 30) - p.window + 1;
         lim_any = __reduce_max_sync(kFull, max(lim[0], lim[1]));

@@ -22,55 +22,65 @@ namespace {
 
 constexpr int kWThreads = 128;
 
-// grid (token tiles, B): one thread a key.  With whole vectors of rows (R a
-// multiple of 4) a key's scores of one head are 16-byte loads, the heads' loads
-// in flight together.
-template <bool kVec>
+// grid (token tiles, B): L threads a key, each a share of its rows, in vectors of
+// four where R is whole vectors; the heads' loads are in flight together.
+template <bool kVec, int L>
 __global__ void __launch_bounds__(kWThreads) pa_key_weights(const __grid_constant__ KeyWeightParams p)
 {
     grid_dependents_launch();
     grid_dependency_wait();
+    constexpr int W = kVec ? 4 : 1, U = 8;
     const int b = blockIdx.y;
     const int n = min(max(__ldg(p.seq_lens + b), 0), p.cap);
-    const int j = blockIdx.x * kWThreads + static_cast<int>(threadIdx.x);
-    if (j >= n + p.NQ || j >= p.cap)
-        return;
+    const int j = blockIdx.x * (kWThreads / L) + static_cast<int>(threadIdx.x) / L;
+    const int sub = static_cast<int>(threadIdx.x) % L;
+    if (blockIdx.x * (kWThreads / L) >= min(n + p.NQ, p.cap))
+        return;  // no key of this CTA
+    const bool key = j < n + p.NQ && j < p.cap;
     const size_t at = static_cast<size_t>(b) * p.cap + j;
-    const float old = p.in && j < n ? p.in[at] : 0.f;
+    const float old = key && p.in && sub == 0 && j < n ? p.in[at] : 0.f;
     // the stages that the partition kernel left out
     const int pl = p.prefix ? min(max(__ldg(p.prefix + b), 0), n + p.NQ) : 0;
     const int P = (pl + p.TT - 1) & ~(p.TT - 1);
     const int lo = max(n - p.window + 1, 0) & ~(p.TT - 1);
     float w = 0.f;
-    if (j < P || j >= lo) {
+    if (key && (j < P || j >= lo)) {
         const size_t seg0 = static_cast<size_t>(b) * p.KV;
         const size_t step = static_cast<size_t>(p.score_tokens) * p.R;
         const float* s = p.scores + seg0 * step + static_cast<size_t>(j) * p.R;
         const float* l = p.lse + seg0 * p.R;
-        if constexpr (kVec) {
-            const int n4 = p.R >> 2, total = p.KV * n4;  // vectors of the key, head by head
-            constexpr int U = 8;
-            for (int i0 = 0; i0 < total; i0 += U) {
-                float4 a[U], c[U];
+        const int per = p.R / W, total = p.KV * per;  // (vectors of) rows of the key, head by head
+        for (int i0 = sub; i0 < total; i0 += U * L) {
+            float a[U][W], c[U][W];
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (i0 + u < total) {
-                        const int kh = (i0 + u) / n4, r4 = (i0 + u) - kh * n4;
-                        a[u] = __ldcg(reinterpret_cast<const float4*>(s + kh * step) + r4);
-                        c[u] = __ldg(reinterpret_cast<const float4*>(l) + i0 + u);
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * L;
+                if (i < total) {
+                    const int kh = i / per, r = i - kh * per;
+                    const float* x = s + kh * step + r * W;
+                    if constexpr (kVec) {
+                        *reinterpret_cast<float4*>(a[u]) = __ldcg(reinterpret_cast<const float4*>(x));
+                        *reinterpret_cast<float4*>(c[u]) = __ldg(reinterpret_cast<const float4*>(l) + i);
+                    } else {
+                        a[u][0] = __ldcg(x);
+                        c[u][0] = __ldg(l + i);
                     }
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (i0 + u < total)
-                        w += (exp2f(a[u].x - c[u].x) + exp2f(a[u].y - c[u].y)) +
-                             (exp2f(a[u].z - c[u].z) + exp2f(a[u].w - c[u].w));
+                }
             }
-        } else {
-            for (int kh = 0; kh < p.KV; ++kh)
-                for (int r = 0; r < p.R; ++r)
-                    w += exp2f(__ldcg(s + kh * step + r) - __ldg(l + kh * p.R + r));
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u * L < total) {
+#pragma unroll
+                    for (int e = 0; e < W; ++e)
+                        w += exp2f(a[u][e] - c[u][e]);
+                }
         }
     }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1)
+        w += __shfl_xor_sync(0xffffffffu, w, o);
+    if (!key || sub != 0)
+        return;
     if (p.in && j < n)
         w = fmaf(p.decay, old, w);
     p.out[at] = w;
@@ -84,15 +94,24 @@ int launch_key_weights(const KeyWeightParams& w, cudaStream_t st)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((w.cap + kWThreads - 1) / kWThreads, w.B);
+    // a few loads a thread: 32 heads on 8 KV heads (8 loads a key) took 28.7 us with
+    // the decode on four threads a key, 31.7 on one
+    const bool vec = w.R % 4 == 0;
+    const long long loads = static_cast<long long>(w.KV) * (vec ? w.R / 4 : w.R);
+    const int L = loads <= 4 ? 1 : loads <= 16 ? 4 : 16;
+    const int keys = kWThreads / L;
+    cfg.gridDim = dim3((w.cap + keys - 1) / keys, w.B);
     cfg.blockDim = dim3(kWThreads);
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     KeyWeightParams p = w;
     void* args[1] = {&p};
-    const void* fn = w.R % 4 == 0 ? reinterpret_cast<const void*>(pa_key_weights<true>)
-                                  : reinterpret_cast<const void*>(pa_key_weights<false>);
+    using Fn = void (*)(KeyWeightParams);
+    const Fn fn1 = vec ? pa_key_weights<true, 1> : pa_key_weights<false, 1>;
+    const Fn fn4 = vec ? pa_key_weights<true, 4> : pa_key_weights<false, 4>;
+    const Fn fn16 = vec ? pa_key_weights<true, 16> : pa_key_weights<false, 16>;
+    const void* fn = reinterpret_cast<const void*>(L == 1 ? fn1 : L == 4 ? fn4 : fn16);
     if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess)
         return PA_ERR_CUDA;
     count_launches(1);

@@ -74,7 +74,9 @@ constexpr int kSRows = 128;     // query rows per CTA of the statistics kernel
 // Statistics kernel: softmax warps, then one TMA, one MMA, four for delta and
 // the zeroing of dq.  Plain scores: 8 softmax warps, two threads a row (four a
 // row were slower: the MMA issue is as long as the softmax).  Modified scores
-// take three times the arithmetic: 16, four threads a row.
+// take three times the arithmetic: 16, four threads a row (175 us of a capped
+// [4, 32/8, 2048] call; 8 warps 233; 16 in two sets that take the tiles in turn,
+// two threads a row, 194).
 template <bool kMod>
 constexpr int kSoftWarps = kMod ? 16 : 8;
 constexpr int kDeltaWarps = 4;

@@ -229,11 +229,37 @@ def test_long_sequences_windows_and_splits(pa, D, H, KV, NQ, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["f16", "bf16"])
+@pytest.mark.parametrize("H,KV,NQ", [(8, 1, 4), (16, 2, 7), (17, 1, 1), (6, 2, 16), (5, 1, 16)])
+def test_many_rows(pa, H, KV, NQ, fmt):
+    # 17 to 80 rows a KV head: two row groups a pass, up to three passes
+    x, _ = make(H + NQ, fmt, [1000, 385, 2], H, KV, 128, 16, NQ)
+    for i, mod in enumerate(MODS):
+        compare(pa, x, modified(mod, 3, H, 128 ** -0.5, fmt, i % 2 == 0))
+
+
+@pytest.mark.gpu
+def test_infinities_and_nans_in_hidden_keys_of_many_rows(pa):
+    x, _ = make(14, "bf16", [700, 300], 16, 2, 128, 16, 4)
+    kw = modified(dict(window=150, prefix=33), 2, 16, 0.09, "bf16", True)
+    call = {k: v for k, v in kw.items() if k != "fmt"}
+    want = pa.decode_scored(*x, **call)
+    for b, n in enumerate([700, 300]):
+        for j in range(33 - b, n - 149):
+            phys = int(x[3][b, j // 16])
+            x[1][phys, j % 16] = math.nan if j % 2 else math.inf
+            x[2][phys, j % 16] = math.inf if j % 3 else math.nan
+    assert torch.equal(pa.decode_scored(*x, **call), want)
+
+
+@pytest.mark.gpu
 def test_without_modification_equals_decode(pa):
     x, _ = make(2, "f16", [300, 77, 1300], 8, 2, 128, 16, 2)
     plain = pa.decode(*x, scale=0.1, causal=True)
     got = pa.decode_scored(*x, scale=0.1, causal=True)
     assert torch.equal(plain, got)
+    x, _ = make(2, "f16", [300, 77, 1300], 12, 1, 128, 16, 3)
+    assert torch.equal(pa.decode(*x, scale=0.1, causal=True, kernel=1), pa.decode_scored(*x, scale=0.1, causal=True))
 
 
 @pytest.mark.gpu
