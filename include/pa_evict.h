@@ -42,6 +42,7 @@
  *   PA_ERR_BAD_DIMS      a size < 1 (B < 0), keep_first or keep_last < 0,
  *                        keep_first + keep_last > budget, max_blocks * BLOCK
  *                        >= 2^30, num_blocks * BLOCK >= 2^31, budget >= 2^30,
+ *                        a dst_table that is block_table itself,
  *                        a dst_table too short for min(budget, max_blocks *
  *                        BLOCK) tokens, overlapping outputs
  *   PA_ERR_UNSUPPORTED   a dtype outside PA_F32, PA_F16, PA_BF16; a token row

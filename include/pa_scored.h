@@ -37,8 +37,9 @@
  * (PA_ERR_UNSUPPORTED); opts->inputs_unchanged and opts->kernel are ignored.
  * slopes [H] float32 and prefix [B] int32 are device pointers or NULL (a
  * negative prefix counts as 0).  PA_ERR_BAD_DIMS: a softcap that is negative
- * or not finite, a negative window, a decay that is not finite, scores whose
- * scratch passes 2^40 bytes.  PA_ERR_NULL_POINTER: weights without out.
+ * or not finite or so small that scale / softcap is not, a negative window, a
+ * decay that is not finite, weights in and out that overlap without being one
+ * array, scores whose scratch passes 2^40 bytes.  PA_ERR_NULL_POINTER: weights without out.
  * PA_ERR_WORKSPACE / PA_ERR_ALIGNMENT: scratch below
  * pa_scored_scratch_bytes() or not 256-byte aligned.  Two calls that run at
  * the same time need a workspace and a scratch each.
@@ -101,7 +102,7 @@ size_t pa_scored_scratch_bytes(int batch, int max_blocks, int BLOCK, int H, int 
  * and dv of a small call come on top of pa_attention_vjp's).  dq is accumulated by float32
  * reductions whose order varies: its last bits may differ from call to call.
  * More errors: PA_ERR_NULL_POINTER without score, PA_ERR_BAD_DIMS for a
- * softcap that is negative or not finite or a negative window,
+ * softcap as above or a negative window,
  * PA_ERR_ALIGNMENT for slopes or prefix not 4-byte aligned.
  */
 int pa_attention_vjp_scored(const void *q, const void *k, const void *v, const void *y,

@@ -12,12 +12,15 @@ from __future__ import annotations
 
 import importlib
 
-__all__ = ["binding", "workloads", "decode", "decode_host", "workspace_bytes"]
+_CALLS = ("decode", "decode_host", "decode_scored", "attention_vjp_scored", "rotary_table", "rotary",
+          "rotary_append", "cache_evict", "workspace_bytes")
+
+__all__ = ["binding", "workloads", *_CALLS]
 
 
 def __getattr__(name):
     if name in ("binding", "workloads"):
         return importlib.import_module(f"{__name__}.{name}")
-    if name in ("decode", "decode_host", "workspace_bytes"):
+    if name in _CALLS:
         return getattr(importlib.import_module(f"{__name__}.binding"), name)
     raise AttributeError(name)

@@ -542,7 +542,7 @@ extern "C" int pa_cache_evict(void* k_cache, void* v_cache, const int32_t* block
     const int m = o.budget < cap ? o.budget : cap;
     if (o.num_blocks < 1 || static_cast<long long>(o.num_blocks) * BLOCK >= (1ll << 31) || o.keep_first < 0 ||
         o.keep_last < 0 || static_cast<long long>(o.keep_first) + o.keep_last > o.budget ||
-        (o.dst_table && (o.dst_max_blocks < 1 || static_cast<long long>(o.dst_max_blocks) * BLOCK < m)))
+        (o.dst_table && (o.dst_table == block_table || o.dst_max_blocks < 1 || static_cast<long long>(o.dst_max_blocks) * BLOCK < m)))
         return PA_ERR_BAD_DIMS;
     if (B == 0)
         return PA_OK;

@@ -894,6 +894,8 @@ int pa_decode_scored(const void* q, const void* k_cache, const void* v_cache, co
     if (!(score->softcap >= 0.f) || !std::isfinite(score->softcap) || score->window < 0 ||
         (weights && !std::isfinite(weights->decay)))
         return PA_ERR_BAD_DIMS;
+    if (score->softcap > 0.f && !std::isfinite(scale / score->softcap))
+        return PA_ERR_BAD_DIMS;
     if ((opts->partitions != 0 && opts->partitions != 1) || opts->merge_kernel)
         return PA_ERR_UNSUPPORTED;
     if (!aligned(score->slopes, 4) || !aligned(score->prefix, 4))
@@ -904,6 +906,11 @@ int pa_decode_scored(const void* q, const void* k_cache, const void* v_cache, co
             return opts->batch > kMaxBatch || NQ < 1 || NQ > PA_MAX_NQ ? PA_ERR_UNSUPPORTED : PA_ERR_BAD_DIMS;
         if (!weights->out)
             return PA_ERR_NULL_POINTER;
+        // in place, or apart
+        const uintptr_t bytes = static_cast<uintptr_t>(opts->batch) * opts->max_blocks * BLOCK * sizeof(float);
+        const uintptr_t a = reinterpret_cast<uintptr_t>(weights->in), o = reinterpret_cast<uintptr_t>(weights->out);
+        if (a && a != o && a < o + bytes && o < a + bytes)
+            return PA_ERR_BAD_DIMS;
         if (!weights->scratch || weights->scratch_bytes < need)
             return PA_ERR_WORKSPACE;
         if (!aligned(weights->scratch, 256) || !aligned(weights->in, 4) || !aligned(weights->out, 4))

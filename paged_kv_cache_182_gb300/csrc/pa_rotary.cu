@@ -191,21 +191,35 @@ __global__ void __launch_bounds__(kRotThreads) pa_rotary_kernel(const __grid_con
         tab[i] = turn(__ldg(p.positions + static_cast<int64_t>(b) * p.N + n0 + r), __ldg(p.table + (i - r * half)), p.factor,
                       p.inverse);
     }
-    // the row's slot; -1: nothing is stored
-    int slot = -1;
-    if (p.slots && live) {
+    // The rows' slots, -1 where nothing is stored: skipped, outside the pool, or
+    // taken by a later row of the sequence, which the CTA's threads look for
+    // together (a prompt of N rows asks N / 2 of them for each).
+    const bool stores = p.slots && h1 > p.H;  // this CTA has keys or values
+    int* slots = reinterpret_cast<int*>(tab + p.rows_cta * half);  // [rows_cta]
+    if (stores) {
         const int32_t* sl = p.slots + static_cast<int64_t>(b) * p.N;
-        slot = __ldg(sl + n);
-        if (slot < -1 || slot >= p.num_slots) {
-            if (p.status && v == 0 && group == 0 && blockIdx.y == 0)
-                atomicOr(p.status, PA_STATUS_BAD_SLOT);
-            slot = -1;
+        for (int r = threadIdx.x; r < rows; r += static_cast<int>(blockDim.x)) {
+            int s = __ldg(sl + n0 + r);
+            if (s < -1 || s >= p.num_slots) {
+                if (p.status)
+                    atomicOr(p.status, PA_STATUS_BAD_SLOT);
+                s = -1;
+            }
+            slots[r] = s;
         }
-        for (int j = n + 1; slot >= 0 && j < p.N; ++j)
-            if (__ldg(sl + j) == slot)
-                slot = -1;  // a later row of this sequence lands there
+        __syncthreads();
+        for (int r = 0; r < rows; ++r) {
+            const int s = slots[r];
+            bool later = false;
+            if (s >= 0)
+                for (int j = n0 + r + 1 + threadIdx.x; j < p.N; j += static_cast<int>(blockDim.x))
+                    later |= __ldg(sl + j) == s;
+            if (__syncthreads_or(later) && threadIdx.x == 0)
+                slots[r] = -1;
+        }
     }
     __syncthreads();
+    const int slot = stores && live ? slots[row] : -1;
     float2 w[NP];
     if (live) {
 #pragma unroll
@@ -435,7 +449,7 @@ extern "C" int pa_rotary(const void* q, const void* k, const int32_t* positions,
     if (gx >= (1ll << 31))
         return PA_ERR_BAD_DIMS;
     const RotFn fn = o.dtype == PA_F32 ? pick_rotary<float>(mode) : o.dtype == PA_F16 ? pick_rotary<__half>(mode) : pick_rotary<__nv_bfloat16>(mode);
-    const size_t smem = static_cast<size_t>(p.rows_cta) * (rot / 2) * sizeof(float2);
+    const size_t smem = static_cast<size_t>(p.rows_cta) * (rot / 2 * sizeof(float2) + sizeof(int));
     fn<<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), threads, smem, static_cast<cudaStream_t>(stream)>>>(p);
     if (cudaGetLastError() != cudaSuccess)
         return PA_ERR_CUDA;

@@ -74,7 +74,7 @@ NULL, DIMS, UNSUP, ALIGN = -1, -2, -3, -4
     (dict(B=-1), DIMS), (dict(KV=0), DIMS), (dict(BLOCK=0), DIMS), (dict(budget=0), DIMS), (dict(keep_first=-1), DIMS),
     (dict(keep_last=-1), DIMS), (dict(keep_first=10, keep_last=11), DIMS), (dict(max_blocks=0), DIMS), (dict(num_blocks=0), DIMS),
     (dict(max_blocks=1 << 26), DIMS), (dict(num_blocks=1 << 27), DIMS), (dict(budget=1 << 30), DIMS),
-    (dict(dst_table=13 * A, dst_max_blocks=1), DIMS), (dict(dst_table=13 * A, dst_max_blocks=0), DIMS),
+    (dict(dst_table=3 * A, dst_max_blocks=8), DIMS), (dict(dst_table=13 * A, dst_max_blocks=1), DIMS), (dict(dst_table=13 * A, dst_max_blocks=0), DIMS),
     (dict(ptr={7: 5 * A}), DIMS), (dict(ptr={6: 2 * A + 64}), DIMS), (dict(ptr={5: 4 * A}), DIMS), (dict(ptr={1: 1 * A}), DIMS),
     (dict(dtype=7), UNSUP), (dict(KV=1, D=4), UNSUP), (dict(KV=512, D=128), UNSUP), (dict(B=4097), UNSUP),
     (dict(ptr={0: A + 8}), ALIGN), (dict(ptr={4: 5 * A + 2}), ALIGN),

@@ -228,6 +228,25 @@ def test_append_stores_rotated_keys_and_values(pa, N, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt,D,H,KV", [("bf16", 64, 4, 2), ("f32", 128, 0, 3), ("f16", 64, 40, 8)])
+def test_append_of_a_long_prompt_with_repeated_slots(pa, fmt, D, H, KV):
+    B, N, BLOCK, NB = 2, 300, 16, 8  # 128 slots a sequence: rows come round more than twice
+    q, k, v, pos = make(31, fmt, B, max(H, 1), KV, N, D, 70000, True)
+    kc = torch.zeros((2 * NB, BLOCK, KV, D), dtype=DT[fmt], device="cuda")
+    vc = torch.zeros_like(kc)
+    slots = (torch.arange(N) % 128 + 128 * torch.arange(B).view(-1, 1)).to(torch.int32)
+    slots[0, 250:] = -1
+    table = pa.rotary_table(D)
+    _, ko = pa.rotary_append(q if H else None, k, v, pos, slots.cuda(), kc, vc, table)
+    wk, wv = torch.zeros_like(kc).view(-1, KV, D), torch.zeros_like(vc).view(-1, KV, D)
+    for b in range(B):
+        for n in range(N):
+            if slots[b, n] >= 0:
+                wk[slots[b, n]], wv[slots[b, n]] = ko[b, :, n], v[b, :, n]
+    assert torch.equal(kc.view(-1, KV, D), wk) and torch.equal(vc.view(-1, KV, D), wv)
+
+
+@pytest.mark.gpu
 def test_graph_replay_other_stream_and_refused_arguments(pa):
     q, k, v, pos = make(21, "f16", 3, 4, 2, 2, 64, 5000, False)
     table = pa.rotary_table(64)

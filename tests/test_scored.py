@@ -168,7 +168,7 @@ NULL, DIMS, UNSUP, ALIGN, WS = -1, -2, -3, -4, -5
 @pytest.mark.parametrize("kw,code", [
     (dict(score=False), NULL), (dict(softcap=-1.0), DIMS), (dict(softcap=math.inf), DIMS), (dict(softcap=math.nan), DIMS),
     (dict(window=-1), DIMS), (dict(weights=dict(decay=math.nan)), DIMS), (dict(partitions=2), UNSUP), (dict(merge_kernel=1), UNSUP),
-    (dict(slopes=A + 2), ALIGN), (dict(prefix=A + 1), ALIGN), (dict(weights=dict(out=None)), NULL),
+    (dict(softcap=1e-40), DIMS), (dict(weights=dict(in_=31 * A + 64)), DIMS), (dict(slopes=A + 2), ALIGN), (dict(prefix=A + 1), ALIGN), (dict(weights=dict(out=None)), NULL),
     (dict(weights=dict(scratch=None)), WS), (dict(weights=dict(scratch_bytes=100)), WS), (dict(weights=dict(scratch=32 * A + 64)), ALIGN),
     (dict(weights=dict(out=31 * A + 2)), ALIGN), (dict(weights={}, NQ=17), UNSUP), (dict(NQ=17), UNSUP), (dict(H=5), DIMS),
     (dict(weights={}, H=5), DIMS), (dict(D=96), UNSUP), (dict(scale=math.nan), DIMS), (dict(workspace_bytes=10), WS),

@@ -148,7 +148,7 @@ def call(pa, score=True, softcap=0.0, window=0, slopes=None, prefix=None, scale=
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(score=False), -1), (dict(softcap=-1.0), -2), (dict(softcap=math.nan), -2), (dict(softcap=math.inf), -2), (dict(window=-3), -2),
+    (dict(score=False), -1), (dict(softcap=-1.0), -2), (dict(softcap=math.nan), -2), (dict(softcap=math.inf), -2), (dict(softcap=1e-40), -2), (dict(window=-3), -2),
     (dict(slopes=A + 1), -4), (dict(prefix=A + 2), -4), (dict(scale=-1.0), -2), (dict(HQ=3), -2), (dict(dtype=9), -3),
     (dict(workspace=None), -1), (dict(workspace_bytes=4), -5), (dict(mask_kind=1), -1),
 ])
