@@ -260,6 +260,24 @@ def _stream_handle(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _ready(args):
+    """Arguments that ctypes passes on as they are (plain ints are converted anew by every call)."""
+    return tuple(ctypes.c_int(a) if type(a) is int else a for a in args)
+
+
+def _call(fn, args, device, stream):
+    """fn(*args, stream) with the plan's device current; raises on an error code."""
+    index = torch.cuda.current_device()
+    if index == device.index:
+        rc = fn(*args, ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(index) if stream is None
+                                       else stream.cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _stream_handle(stream))
+    if rc != 0:
+        raise PagedAttentionError(rc)
+
+
 class Plan:
     """One prepared decode call on fixed device tensors.
 
@@ -785,23 +803,19 @@ class ScoredPlan(Plan):
                                       out=self.key_weights.data_ptr(), decay=float(decay),
                                       scratch=self.scratch.data_ptr(), scratch_bytes=need)
         self._scored_keep = (slopes, prefix, key_weights)
-        self._args = self._args[:-1] + [ctypes.byref(self.score),
-                                        None if self.weights is None else ctypes.byref(self.weights),
-                                        ctypes.byref(self.opts)]
-
-    def _result(self, rc):
-        if rc != 0:
-            raise PagedAttentionError(rc)
-        return self.out if self.weights is None else (self.out, self.key_weights)
+        self._args = [*_ready(self._args[:-1]), ctypes.byref(self.score),
+                      None if self.weights is None else ctypes.byref(self.weights), ctypes.byref(self.opts)]
+        self._result = self.out if self.weights is None else (self.out, self.key_weights)
 
     def run_bound(self):
-        return self._result(LIB.pa_decode_scored(*self._bound))
+        rc = LIB.pa_decode_scored(*self._bound)
+        if rc != 0:
+            raise PagedAttentionError(rc)
+        return self._result
 
     def run(self, stream=None):
-        if torch.cuda.current_device() == self.device.index:
-            return self._result(LIB.pa_decode_scored(*self._args, _stream_handle(stream)))
-        with torch.cuda.device(self.device):
-            return self._result(LIB.pa_decode_scored(*self._args, _stream_handle(stream)))
+        _call(LIB.pa_decode_scored, self._args, self.device, stream)
+        return self._result
 
 
 def decode_scored(q, k_cache, v_cache, block_table, seq_lens, k_new, v_new, *, scale: float,
@@ -830,20 +844,14 @@ class ScoredVjpPlan(VjpPlan):
                          kernel=kernel, status=status, wait_limit_ns=wait_limit_ns, out=out)
         self.score = _score(softcap, slopes, window, prefix, int(q.shape[0]), int(q.shape[1]), q.device)
         self._scored_keep = (slopes, prefix)
-        self._args = self._args[:-1] + (ctypes.byref(self.score), ctypes.byref(self.opts))
+        self._args = _ready(self._args[:-1]) + (ctypes.byref(self.score), ctypes.byref(self.opts))
 
     def _workspace_bytes(self, B, HQ, HK, SQ, SK, D, dtype, out_dtype, device):
         with torch.cuda.device(device):
             return int(LIB.pa_attention_vjp_scored_workspace_bytes(B, HQ, HK, SQ, SK, D, dtype, out_dtype))
 
     def run(self, stream=None):
-        if torch.cuda.current_device() == self.device.index:
-            rc = LIB.pa_attention_vjp_scored(*self._args, _stream_handle(stream))
-        else:
-            with torch.cuda.device(self.device):
-                rc = LIB.pa_attention_vjp_scored(*self._args, _stream_handle(stream))
-        if rc != 0:
-            raise PagedAttentionError(rc)
+        _call(LIB.pa_attention_vjp_scored, self._args, self.device, stream)
         return self.dq, self.dk, self.dv
 
 
@@ -1001,18 +1009,12 @@ class RotaryPlan:
             o.status = None if status is None else status.data_ptr()
         self.opts, self.device = o, dev
         self._keep = (q, k, v, positions, table, slots, caches, status)
-        self._args = (_ptr(q), _ptr(k), _ptr(positions), _ptr(table.turns), _ptr(self.q_out),
-                      _ptr(self.k_out), B, H, KV, N, D, table.rot, ctypes.byref(self.opts))
+        self._args = _ready((_ptr(q), _ptr(k), _ptr(positions), _ptr(table.turns), _ptr(self.q_out),
+                             _ptr(self.k_out), B, H, KV, N, D, table.rot, ctypes.byref(self.opts)))
 
     def run(self, stream=None):
         """Enqueue on ``stream`` (default: torch's current stream); returns (q_out, k_out)."""
-        if torch.cuda.current_device() == self.device.index:
-            rc = LIB.pa_rotary(*self._args, _stream_handle(stream))
-        else:
-            with torch.cuda.device(self.device):
-                rc = LIB.pa_rotary(*self._args, _stream_handle(stream))
-        if rc != 0:
-            raise PagedAttentionError(rc)
+        _call(LIB.pa_rotary, self._args, self.device, stream)
         return self.q_out, self.k_out
 
 
@@ -1121,17 +1123,11 @@ class EvictPlan:
             status=None if status is None else status.data_ptr())
         self.device = dev
         self._keep = (tensors, dst_table, status)
-        self._args = (*(_ptr(t) for t in tensors), B, KV, D, BLOCK, ctypes.byref(self.opts))
+        self._args = _ready((*(_ptr(t) for t in tensors), B, KV, D, BLOCK, ctypes.byref(self.opts)))
 
     def run(self, stream=None):
         """Enqueue on ``stream`` (default: torch's current stream)."""
-        if torch.cuda.current_device() == self.device.index:
-            rc = LIB.pa_cache_evict(*self._args, _stream_handle(stream))
-        else:
-            with torch.cuda.device(self.device):
-                rc = LIB.pa_cache_evict(*self._args, _stream_handle(stream))
-        if rc != 0:
-            raise PagedAttentionError(rc)
+        _call(LIB.pa_cache_evict, self._args, self.device, stream)
         return self.new_lens, self.kept, self.weights_out
 
 
