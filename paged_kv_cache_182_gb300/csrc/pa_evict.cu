@@ -3,25 +3,34 @@
 //
 // Two kernels:
 //
-// pa_evict_select -- one cluster of CTAs per sequence finds the weight of the
-//   last token that is kept (a radix select: histograms of 11, 11 and 10 bits
-//   of the weights' ordered bit patterns, summed over the cluster through
-//   distributed shared memory; it ends early once the chosen bin is taken
-//   whole), then writes the kept indices and weights in token order: each
-//   warp owns a contiguous range of tokens, the ranges' counts are summed
-//   over warps and CTAs, and ballots place the tokens inside a range.
+// pa_evict_select -- a CTA or a cluster of CTAs per sequence finds the weight
+//   of the last token that is kept: a radix select over the weights' ordered
+//   bit patterns, histograms of 11, 11 and 10 bits summed over the cluster
+//   through distributed shared memory.  It ends early once the chosen bin is
+//   taken whole (two passes for distinct weights).  The weights stay in
+//   registers, 8 a thread, loaded before the length is known (the ranges are
+//   those of the table's capacity).  Then it writes the kept indices and
+//   weights in token order: each warp owns a contiguous range of tokens, the
+//   ranges' counts are summed over warps and CTAs, and ballots place the
+//   tokens inside a range.  Bound by latency: 12 us for 64 sequences of up to
+//   16384 tokens, 10.5 for one of 32768, of which a third are cluster barriers
+//   and remote histogram reads.
 //
-// The rows then move by one of two kernels:
+// The rows then move by one of two kernels, which set up while the selection
+// runs (programmatic launch):
 //
 // pa_evict_shift (in place) -- kept[r] >= r, so a destination slot is either
 //   unmoved or the source of a lower or equal rank.  A CTA owns a slice of the
 //   columns of one sequence's K or V and walks the ranks in order, several
 //   runs of rows in flight: a run is written when it and all runs before it
 //   have been read, which is all that the overlap asks for, and no CTA waits
-//   for another.
+//   for another.  (Runs of whole rows dealt to all CTAs, each waiting for the
+//   flags of the runs that it overwrites, took 34 us where this takes 22.)
+//   Bound by memory: 25 of 64 sequences over a budget of 2048, 100 MB read and
+//   written at 6.9 TB/s once the pipeline is full, 5 us to fill it.
 //
 // pa_evict_gather (into other blocks) -- nothing overlaps: one CTA per run of
-//   whole rows.
+//   whole rows, 16 KB.  8192 rows of 2 KB of K and of V: 13 us, 5.2 TB/s.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -596,7 +605,9 @@ extern "C" int pa_cache_evict(void* k_cache, void* v_cache, const int32_t* block
 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // short sequences: a CTA of 256 threads holds 2048 weights in registers;
-    // else 1024 threads and 8192, and a cluster of up to 8 of them
+    // else 1024 threads and 8192, and a cluster of up to 8 of them (16 weights a
+    // thread and half the CTAs: 29.4 against 23.7 us for a call of 32768 tokens,
+    // 36.4 against 33.4 for 64 of up to 16384; twice the CTAs: 25.5)
     const bool small = cap <= 2048;
     const int C = cap <= 8192 ? 1 : cap <= 16384 ? 2 : cap <= 32768 ? 4 : 8;
     const void* sel = small    ? reinterpret_cast<const void*>(pa_evict_select<256, 1>)
@@ -616,9 +627,9 @@ extern "C" int pa_cache_evict(void* k_cache, void* v_cache, const int32_t* block
     cfg.attrs = attr;
     cfg.numAttrs = C > 1 ? 1 : 0;
     void* args[1] = {&p};
-    // The move sets up while the selection runs.  In place, about 96 KB of rows in
-    // flight per CTA: slices of 128 bytes, or of 64 where those would leave SMs
-    // idle (half a memory burst wastes nothing, but a row's bytes are fetched apart).
+    // In place, about 96 KB of rows in flight per CTA: slices of 128 bytes, or of
+    // 64 where those would leave SMs idle (on the 64 ragged sequences 64-byte
+    // slices took 44.9 us against 33.5).
     const void* move;
     size_t smem;
     dim3 grid;

@@ -598,9 +598,12 @@ struct ScoreSpan<true> {
 // Modifies a thread's N scores (dot products times score_qscale) of a tile: the
 // cap, the distance bias, the masks, the store for the key weights, each in a
 // pass of its own under one test, so that a call runs (and fetches) only the
-// code of what it asks for.  Score i belongs to row R[i % 2 or as row_of says]
-// and key c0 + tok_of(i), both of which the caller's functions give at compile
-// time of the unrolled loops.
+// code of what it asks for: every launch fetches its code anew, and with all
+// four in one loop over the scores the smallest call took 10.5 us instead of
+// 8.1, and one of 8 sequences 26.8 instead of 25.4 (23.9 without any).  Score i
+// belongs to row row_of(i) and key c0 + tok_of(i), known at compile time in the
+// unrolled loops; `whole`: no mask touches the tile; `n_left`: tokens of the
+// tile from c0 on.
 template <int N, typename RowOf, typename TokOf>
 __device__ __forceinline__ void modify_scores(const ScoredParams& p, const ScorePiece<true>& sp, const ScoreRow<true>* rows,
                                               const int* lim, float (&x)[N], int c0, int off, bool whole, int n_left,
