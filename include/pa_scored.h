@@ -33,7 +33,9 @@
  * in one order, whatever the split.
  *
  * Layouts, ownership, streams, opts and errors as pa_decode, with these
- * differences: opts->partitions must be 0 or 1 and opts->merge_kernel 0
+ * differences: the batch's lengths have to fit beside two pipeline stages in
+ * shared memory (any batch up to 1500; up to 4096 with few new rows), else
+ * PA_ERR_UNSUPPORTED; opts->partitions must be 0 or 1 and opts->merge_kernel 0
  * (PA_ERR_UNSUPPORTED); opts->inputs_unchanged and opts->kernel are ignored.
  * slopes [H] float32 and prefix [B] int32 are device pointers or NULL (a
  * negative prefix counts as 0).  PA_ERR_BAD_DIMS: a softcap that is negative

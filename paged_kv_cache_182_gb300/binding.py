@@ -18,6 +18,15 @@ patching), ``prefill`` / ``PrefillPlan`` (causal prefill of any number of
 new rows up to PA_MAX_PREFILL) and ``attention_vjp`` / ``VjpPlan`` (dense
 attention backward, ``include/pa_attention_vjp.h``: q, y, g [B, HQ, SQ, D],
 k, v [B, HK, SK, D]).
+
+Around them: ``rotary`` / ``RotaryPlan`` and ``rotary_append`` /
+``RotaryAppendPlan`` (rotary positions, their gradient, and with the store of
+the new rows in the cache, ``include/pa_rotary.h``), ``decode_scored`` /
+``ScoredPlan`` and ``attention_vjp_scored`` / ``ScoredVjpPlan`` (decode and
+backward with scores that are capped, biased by distance or limited to a
+window beside a prefix; the decode also accumulates the weight of every key,
+``include/pa_scored.h``) and ``cache_evict`` / ``EvictPlan`` (sequences
+shortened to their most attended keys, ``include/pa_evict.h``).
 """
 from __future__ import annotations
 
@@ -276,6 +285,17 @@ def _call(fn, args, device, stream):
             rc = fn(*args, _stream_handle(stream))
     if rc != 0:
         raise PagedAttentionError(rc)
+
+
+def _run_once(plan, stream, *made):
+    """``plan.run(stream)`` of a plan that is dropped right after: the tensors it
+    made itself stay allocated until ``stream`` has passed the call."""
+    result = plan.run(stream)
+    if stream is not None:
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+    return result
 
 
 class Plan:
@@ -788,7 +808,7 @@ class ScoredPlan(Plan):
         s = self.shape
         self.score = _score(softcap, slopes, window, prefix, s["B"], s["H"], self.device)
         self.key_weights = key_weights if key_weights_out is None else key_weights_out
-        self.weights = None
+        self.weights = self.scratch = None
         if self.key_weights is not None:
             for t in (key_weights, self.key_weights):
                 if t is not None and (tuple(t.shape) != (s["B"], s["max_blocks"] * s["BLOCK"])
@@ -824,11 +844,12 @@ def decode_scored(q, k_cache, v_cache, block_table, seq_lens, k_new, v_new, *, s
                   partitions: int = 0, out=None, out_dtype=None, workspace=None, status=None,
                   checked: bool = False, stream=None):
     """Decode attention with modified scores (pa_decode_scored): see ``ScoredPlan``."""
-    return ScoredPlan(q, k_cache, v_cache, block_table, seq_lens, k_new, v_new, scale=scale,
+    plan = ScoredPlan(q, k_cache, v_cache, block_table, seq_lens, k_new, v_new, scale=scale,
                       causal=causal, softcap=softcap, slopes=slopes, window=window, prefix=prefix,
                       key_weights=key_weights, key_weights_out=key_weights_out, decay=decay,
                       partitions=partitions, out=out, out_dtype=out_dtype, workspace=workspace,
-                      status=status, checked=checked).run(stream)
+                      status=status, checked=checked)
+    return _run_once(plan, stream, plan.out, plan.workspace, plan.scratch)
 
 
 class ScoredVjpPlan(VjpPlan):
@@ -860,9 +881,10 @@ def attention_vjp_scored(q, k, v, y, g, mask=None, *, scale: float, causal: bool
                          out_dtype=None, kernel: int = 0, status=None, stream=None, out=None):
     """dq, dk, dv of attention with modified scores (pa_attention_vjp_scored):
     see ``ScoredVjpPlan``."""
-    return ScoredVjpPlan(q, k, v, y, g, mask, scale=scale, causal=causal, softcap=softcap,
+    plan = ScoredVjpPlan(q, k, v, y, g, mask, scale=scale, causal=causal, softcap=softcap,
                          slopes=slopes, window=window, prefix=prefix, out_dtype=out_dtype,
-                         kernel=kernel, status=status, out=out).run(stream)
+                         kernel=kernel, status=status, out=out)
+    return _run_once(plan, stream, plan.workspace, plan.dq, plan.dk, plan.dv)
 
 
 # ------------------------------------------------------------------- rotary positions
@@ -1049,15 +1071,17 @@ class RotaryAppendPlan(RotaryPlan):
 def rotary(q, k, positions, table: RotaryTable, *, interleaved: bool = False, inverse: bool = False,
            q_out=None, k_out=None, stream=None):
     """q and k turned by their positions (pa_rotary): see ``RotaryPlan``."""
-    return RotaryPlan(q, k, positions, table, interleaved=interleaved, inverse=inverse, q_out=q_out,
-                      k_out=k_out).run(stream)
+    plan = RotaryPlan(q, k, positions, table, interleaved=interleaved, inverse=inverse, q_out=q_out,
+                      k_out=k_out)
+    return _run_once(plan, stream, plan.q_out, plan.k_out)
 
 
 def rotary_append(q, k, v, positions, slot_mapping, k_cache, v_cache, table: RotaryTable, *,
                   interleaved: bool = False, q_out=None, k_out=None, status=None, stream=None):
     """``rotary`` with the store of the new rows in the cache: see ``RotaryAppendPlan``."""
-    return RotaryAppendPlan(q, k, v, positions, slot_mapping, k_cache, v_cache, table,
-                            interleaved=interleaved, q_out=q_out, k_out=k_out, status=status).run(stream)
+    plan = RotaryAppendPlan(q, k, v, positions, slot_mapping, k_cache, v_cache, table,
+                            interleaved=interleaved, q_out=q_out, k_out=k_out, status=status)
+    return _run_once(plan, stream, plan.q_out, plan.k_out)
 
 
 # ------------------------------------------------------------------- cache eviction
@@ -1134,6 +1158,6 @@ class EvictPlan:
 def cache_evict(k_cache, v_cache, block_table, seq_lens, key_weights, *, budget: int,
                 keep_first: int = 0, keep_last: int = 0, dst_table=None, status=None, stream=None):
     """Shortens every sequence to its budget (pa_cache_evict): see ``EvictPlan``."""
-    return EvictPlan(k_cache, v_cache, block_table, seq_lens, key_weights, budget=budget,
-                     keep_first=keep_first, keep_last=keep_last, dst_table=dst_table,
-                     status=status).run(stream)
+    plan = EvictPlan(k_cache, v_cache, block_table, seq_lens, key_weights, budget=budget,
+                     keep_first=keep_first, keep_last=keep_last, dst_table=dst_table, status=status)
+    return _run_once(plan, stream, plan.new_lens, plan.kept, plan.weights_out)

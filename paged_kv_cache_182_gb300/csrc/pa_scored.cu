@@ -25,68 +25,67 @@ namespace {
 
 constexpr int kWThreads = 128;
 
-// grid (token tiles, B): L threads a key, each a share of its rows, in vectors of
-// four where R is whole vectors; the heads' loads are in flight together.
+// grid (CTAs a sequence, B): tiles of keys dealt to a sequence's CTAs, as many
+// as it has (a table may hold far more tokens than a sequence); L threads a
+// key, each a share of its rows, in vectors of four where R is whole vectors;
+// the heads' loads are in flight together.
 template <bool kVec, int L>
 __global__ void __launch_bounds__(kWThreads) pa_key_weights(const __grid_constant__ KeyWeightParams p)
 {
     grid_dependents_launch();
     grid_dependency_wait();
-    constexpr int W = kVec ? 4 : 1, U = 4;
+    constexpr int W = kVec ? 4 : 1, U = 4, KEYS = kWThreads / L;
     const int b = blockIdx.y;
     const int n = min(max(__ldg(p.seq_lens + b), 0), p.cap);
-    const int j = blockIdx.x * (kWThreads / L) + static_cast<int>(threadIdx.x) / L;
+    const int end = min(n + p.NQ, p.cap);
     const int sub = static_cast<int>(threadIdx.x) % L;
-    if (blockIdx.x * (kWThreads / L) >= min(n + p.NQ, p.cap))
-        return;  // no key of this CTA
-    const bool key = j < n + p.NQ && j < p.cap;
-    const size_t at = static_cast<size_t>(b) * p.cap + j;
-    const float old = key && p.in && sub == 0 && j < n ? p.in[at] : 0.f;
     // the stages that the partition kernel left out
     const int pl = p.prefix ? min(max(__ldg(p.prefix + b), 0), n + p.NQ) : 0;
     const int P = (pl + p.TT - 1) & ~(p.TT - 1);
     const int lo = max(n - p.window + 1, 0) & ~(p.TT - 1);
-    float w = 0.f;
-    if (key && (j < P || j >= lo)) {
-        const size_t seg0 = static_cast<size_t>(b) * p.KV;
-        const size_t step = static_cast<size_t>(p.score_tokens) * p.R;
-        const float* s = p.scores + seg0 * step + static_cast<size_t>(j) * p.R;
-        const float* l = p.lse + seg0 * p.R;
-        const int per = p.R / W, total = p.KV * per;  // (vectors of) rows of the key, head by head
-        for (int i0 = sub; i0 < total; i0 += U * L) {
-            float a[U][W], c[U][W];
+    const size_t seg0 = static_cast<size_t>(b) * p.KV;
+    const size_t step = static_cast<size_t>(p.score_tokens) * p.R;
+    const float* l = p.lse + seg0 * p.R;
+    const int per = p.R / W, total = p.KV * per;  // (vectors of) rows of a key, head by head
+    for (int j0 = blockIdx.x * KEYS; j0 < end; j0 += gridDim.x * KEYS) {
+        const int j = j0 + static_cast<int>(threadIdx.x) / L;
+        const size_t at = static_cast<size_t>(b) * p.cap + j;
+        const float old = p.in && sub == 0 && j < n ? p.in[at] : 0.f;
+        float w = 0.f;
+        if (j < end && (j < P || j >= lo)) {
+            const float* s = p.scores + seg0 * step + static_cast<size_t>(j) * p.R;
+            for (int i0 = sub; i0 < total; i0 += U * L) {
+                float a[U][W], c[U][W];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = i0 + u * L;
-                if (i < total) {
-                    const int kh = i / per, r = i - kh * per;
-                    const float* x = s + kh * step + r * W;
-                    if constexpr (kVec) {
-                        *reinterpret_cast<float4*>(a[u]) = __ldcg(reinterpret_cast<const float4*>(x));
-                        *reinterpret_cast<float4*>(c[u]) = __ldg(reinterpret_cast<const float4*>(l) + i);
-                    } else {
-                        a[u][0] = __ldcg(x);
-                        c[u][0] = __ldg(l + i);
+                for (int u = 0; u < U; ++u) {
+                    const int i = i0 + u * L;
+                    if (i < total) {
+                        const int kh = i / per, r = i - kh * per;
+                        const float* x = s + kh * step + r * W;
+                        if constexpr (kVec) {
+                            *reinterpret_cast<float4*>(a[u]) = __ldcg(reinterpret_cast<const float4*>(x));
+                            *reinterpret_cast<float4*>(c[u]) = __ldg(reinterpret_cast<const float4*>(l) + i);
+                        } else {
+                            a[u][0] = __ldcg(x);
+                            c[u][0] = __ldg(l + i);
+                        }
                     }
                 }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (i0 + u * L < total) {
+#pragma unroll
+                        for (int e = 0; e < W; ++e)
+                            w += exp2f(a[u][e] - c[u][e]);
+                    }
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (i0 + u * L < total) {
-#pragma unroll
-                    for (int e = 0; e < W; ++e)
-                        w += exp2f(a[u][e] - c[u][e]);
-                }
         }
-    }
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1)
-        w += __shfl_xor_sync(0xffffffffu, w, o);
-    if (!key || sub != 0)
-        return;
-    if (p.in && j < n)
-        w = fmaf(p.decay, old, w);
-    p.out[at] = w;
+        for (int o = L / 2; o > 0; o >>= 1)
+            w += __shfl_xor_sync(0xffffffffu, w, o);
+        if (j < end && sub == 0)
+            p.out[at] = p.in && j < n ? fmaf(p.decay, old, w) : w;
+    }
 }
 
 }  // namespace
@@ -103,7 +102,8 @@ int launch_key_weights(const KeyWeightParams& w, cudaStream_t st)
     const long long loads = static_cast<long long>(w.KV) * (vec ? w.R / 4 : w.R);
     const int L = loads <= 4 ? 1 : loads <= 16 ? 4 : 16;
     const int keys = kWThreads / L;
-    cfg.gridDim = dim3((w.cap + keys - 1) / keys, w.B);
+    const int tiles = (w.cap + keys - 1) / keys, most = (152 * 16 + w.B - 1) / w.B;
+    cfg.gridDim = dim3(tiles < most ? tiles : most, w.B);
     cfg.blockDim = dim3(kWThreads);
     cfg.stream = st;
     cfg.attrs = attr;

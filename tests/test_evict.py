@@ -132,7 +132,8 @@ def same(got, want):
     ("bf16", [20000, 16385], 2, 128, 64, 3000, 0, 500),
     ("f32", [513, 1024], 3, 8, 5, 200, 0, 199),
     ("f16", [900], 2, 64, 16, 40, 20, 20),   # nothing of the middle
-    ("f16", [64, 50], 128, 128, 16, 30, 0, 0),  # one long row an item
+    ("f16", [64, 50], 128, 128, 16, 30, 0, 0),  # rows of 32 KB
+    ("bf16", [40, 3, 64], 2, 64, 16, 5000, 10, 20),  # a budget beyond the table
 ])
 def test_selects_and_moves(pa, fmt, lens, KV, D, BLOCK, budget, first, last, fresh):
     kc, vc, table, dst, ln, w, _ = make(len(lens) + budget, fmt, lens, KV, D, BLOCK, budget if fresh else 0)
@@ -176,6 +177,31 @@ def test_long_sequences_whose_weights_crowd(pa, n):
     budget = n // 3
     want = expect(kc, vc, table, [n, n // 2], w, budget, 3, 100, None)
     same(run(pa, kc, vc, table, None, ln, w, budget, 3, 100), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fresh", [False, True])
+def test_pools_past_32_bits_of_offset(pa, fresh):
+    # blocks at both ends of pools of 4.8 GB each
+    NB, BLOCK, KV, D, n, budget = 150000, 16, 8, 128, 300, 100
+    kc = torch.empty(NB, BLOCK, KV, D, dtype=torch.float16, device="cuda")
+    vc = torch.empty_like(kc)
+    g = torch.Generator().manual_seed(1)
+    ids = torch.cat((torch.arange(10), torch.arange(NB - 40, NB)))[torch.randperm(50, generator=g)].to(torch.int32)
+    table, dst = ids[:19].view(1, 19).contiguous(), ids[19:26].view(1, 7).contiguous() if fresh else None
+    small = torch.randn(2, 50, BLOCK, KV, D, generator=g).half()
+    for pool, rows in ((kc, small[0]), (vc, small[1])):
+        pool[ids.long().cuda()] = rows.cuda()
+    w = torch.rand(1, 19 * BLOCK, generator=g)
+    to_small = {int(x): i for i, x in enumerate(ids)}
+    local = lambda t: None if t is None else torch.tensor([[to_small[int(x)] for x in t[0]]], dtype=torch.int32)  # noqa: E731
+    want = expect(small[0], small[1], local(table), [n], w, budget, 2, 30, local(dst))
+    plan = pa.EvictPlan(kc, vc, table.cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"), w.cuda(), budget=budget,
+                        keep_first=2, keep_last=30, dst_table=None if dst is None else dst.cuda())
+    new, kept, wout = plan.run()
+    torch.cuda.synchronize()
+    at = ids.long().cuda()
+    same((new.cpu(), kept.cpu(), wout.cpu(), kc[at].cpu(), vc[at].cpu()), want)
 
 
 @pytest.mark.gpu

@@ -253,6 +253,38 @@ def test_infinities_and_nans_in_hidden_keys_of_many_rows(pa):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt,B,D,NQ", [("f16", 1500, 64, 1), ("bf16", 1500, 128, 16), ("f32", 1500, 64, 16), ("f16", 4096, 128, 1)])
+def test_large_batches(pa, fmt, B, D, NQ):
+    g = torch.Generator().manual_seed(B + D)
+    lens = torch.randint(0, 60, (B,), generator=g).tolist()
+    x, _ = make(B, fmt, lens, 2, 1, D, 16, NQ)
+    kw = modified(dict(softcap=9.0, window=21, prefix=2 ** 20), B, 2, 0.1, fmt, True)
+    kw["prefix"] = (torch.arange(B) % 9).to(torch.int32).cuda()
+    some = list(range(0, B, 97))  # the reference for some sequences
+    out, w = pa.decode_scored(*x, **{k: v for k, v in kw.items() if k != "fmt"},
+                              key_weights_out=torch.zeros(B, x[3].shape[1] * 16, device="cuda"))
+    torch.cuda.synchronize()
+    part = [x[0][some], x[1], x[2], x[3][some], x[4][some], x[5][some], x[6][some]]
+    want, bound, ww, wb = reference(part, {**kw, "prefix": kw["prefix"][some]})
+    o = out[some].double().cpu().numpy()
+    assert np.all(np.abs(o - want) <= bound + HALF_STEP[fmt] * (np.abs(want) + bound) + 2.0 ** -25)
+    assert np.all(np.abs(w[some].double().cpu().numpy() - ww) <= wb + 2.0 ** -23 * ww)
+
+
+@pytest.mark.gpu
+def test_scores_past_32_bits_of_offset(pa):
+    # 2 x 8 heads x 16 rows of up to 16M tokens of capacity: 17 GB of scores
+    x, _ = make(17, "f16", [70, 33], 8, 1, 64, 16, 16)
+    wide = torch.full((2, 1 << 20), -1, dtype=torch.int32, device="cuda")
+    wide[:, : x[3].shape[1]] = x[3]
+    kw = dict(scale=0.1, causal=True, softcap=7.0)
+    a, wa = pa.decode_scored(*x, **kw, key_weights_out=torch.zeros(2, x[3].shape[1] * 16, device="cuda"))
+    x[3] = wide
+    b, wb = pa.decode_scored(*x, **kw, key_weights_out=torch.zeros(2, 16 << 20, device="cuda"))
+    assert torch.equal(a, b) and torch.equal(wa, wb[:, : wa.shape[1]]) and float(wb[:, 100:].abs().max()) == 0.0
+
+
+@pytest.mark.gpu
 def test_without_modification_equals_decode(pa):
     x, _ = make(2, "f16", [300, 77, 1300], 8, 2, 128, 16, 2)
     plain = pa.decode(*x, scale=0.1, causal=True)
