@@ -56,7 +56,7 @@
 //     the wait for its dQ^T: S^T of the next step is issued right after dV.
 //   * With few key tiles each query head of a group has a CTA of its own, and
 //     dk and dv are joined in group order (vjp_join_groups).
-// [4, 32/8, 2048, 128] bf16 causal with a cap: statistics 175 us, backward 470
+// [4, 32/8, 2048, 128] bf16 causal with a cap: statistics 175 us, backward 449
 // (without a cap 94 and 385), rounding 37.  Bound by the softmax warps' own
 // instructions (issue slots 52% and 49% busy) and, in the backward, by the dq
 // reductions into L2 (1.1 GB a call, as without a cap).
@@ -71,6 +71,7 @@
 
 #include <cstdint>
 #include <type_traits>
+#include <utility>
 
 #include "pa_decode.h"
 #include "pa_ptx.cuh"
@@ -168,6 +169,16 @@ static_assert(kMainSmem <= 232448, "backward shared memory");
 __device__ __forceinline__ void red_add(float* addr, float v)
 {
     asm volatile("red.global.add.f32 [%0], %1;" ::"l"(addr), "f"(v) : "memory");
+}
+
+// v[j] added at row j of a column of the accumulator (rows kD floats apart), the
+// offsets in the instructions.
+template <int... J>
+__device__ __forceinline__ void red_rows(float* column, const float* v, std::integer_sequence<int, J...>)
+{
+    (..., [&] {
+        asm volatile("red.global.add.f32 [%0+%2], %1;" ::"l"(column), "f"(v[J]), "n"(J * kD * 4) : "memory");
+    }());
 }
 
 template <typename T>
@@ -498,6 +509,8 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
                 bars.xl[k & 1][part - 1][row] = l;
             }
             asm volatile("bar.sync %0, %1;" ::"r"(1 + (warp & 3)), "n"(PARTS * 32) : "memory");
+            // (modified scores: minus lse2 and minus delta are kept, as the backward
+            // adds them two at a time)
             if (part == 0 && !fault) {
                 float mt = m;
 #pragma unroll
@@ -505,14 +518,17 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
                     mt = fmaxf(mt, bars.xm[k & 1][q][row]);
                 const int64_t srow = (static_cast<int64_t>(it.b) * p.HQ + it.h) * p.sqp + i;
                 if (i >= p.SQ || mt == -INFINITY) {  // padding rows up to sqp, rows that see no key
-                    p.lse[srow] = INFINITY;
+                    p.lse[srow] = kMod ? -INFINITY : INFINITY;
                 } else {
                     float lt = l * exp2f(m - mt);
 #pragma unroll
                     for (int q = 0; q < PARTS - 1; ++q)
                         lt += bars.xl[k & 1][q][row] * exp2f(bars.xm[k & 1][q][row] - mt);
                     // (a bounded row that sees no key has summed zeros)
-                    p.lse[srow] = kMod && lt == 0.f ? INFINITY : mt + log2f(lt);
+                    if constexpr (kMod)
+                        p.lse[srow] = lt == 0.f ? -INFINITY : -(mt + log2f(lt));
+                    else
+                        p.lse[srow] = mt + log2f(lt);
                 }
             }
         }
@@ -562,7 +578,8 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
                         d += __shfl_xor_sync(kAll, d, sh);
                     const int i = it.i0 + dw * 32 + rb + 2 * e + half;
                     if (c16 == 0)
-                        p.delta[s0 + i] = i < p.SQ ? d : 0.f;  // padding rows up to sqp: no gradient
+                        // padding rows up to sqp: no gradient
+                        p.delta[s0 + i] = i < p.SQ ? (kMod ? -d : d) : 0.f;
                 }
             }
             // the item's real rows of the accumulator: contiguous, 512 bytes a row
@@ -839,9 +856,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         int held_rows = 0;
         auto reduce_half = [&](float* dst, const float* v, int rows) {  // rows of this half present
             if (rows >= 16) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    red_add(dst + static_cast<int64_t>(j) * kD, v[j]);
+                red_rows(dst, v, std::make_integer_sequence<int, 16>{});
             } else {
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
@@ -886,14 +901,14 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                         tanh_block_scaled(y, p.tanh);
                         c = p.cap_out;
                     }
-                    float z[16];  // minus lse2 and the distance bias
+                    float z[16];  // minus lse2 (as the statistics kernel left it) and the distance bias
 #pragma unroll
                     for (int q4 = 0; q4 < 4; ++q4) {
                         const float4 l = l4[hf * 4 + q4];
-                        z[4 * q4] = -l.x;
-                        z[4 * q4 + 1] = -l.y;
-                        z[4 * q4 + 2] = -l.z;
-                        z[4 * q4 + 3] = -l.w;
+                        z[4 * q4] = l.x;
+                        z[4 * q4 + 1] = l.y;
+                        z[4 * q4 + 2] = l.z;
+                        z[4 * q4 + 3] = l.w;
                     }
                     if (p.slopes) {
                         const float d0 = static_cast<float>(rb + hf * 16 - key);
@@ -923,7 +938,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
                             const float2 t2 = make_float2(y[j], y[j + 1]);
-                            const float2 f2 = __ffma2_rn(make_float2(-t2.x, -t2.y), t2, make_float2(1.f, 1.f));
+                            const float2 f2 = __ffma2_rn(__fmul2_rn(t2, t2), make_float2(-1.f, -1.f), make_float2(1.f, 1.f));
                             const float2 r = __fmul2_rn(make_float2(pv[hf * 16 + j], pv[hf * 16 + j + 1]), f2);
                             pv[hf * 16 + j] = r.x;
                             pv[hf * 16 + j + 1] = r.y;
@@ -943,21 +958,27 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                     return false;
                 const float4* d4 = reinterpret_cast<const float4*>(sStat + (it & 1) * 256 + 128 + part * 32);
                 tc_fence_after();
+                const float2 sc = make_float2(p.scale, p.scale);
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     Cols16 x;
                     tmem_ld16(x, tP + lane_off + part * 32 + hf * 16);
-                    const float sc = p.scale;
+                    if (!plain) {  // a hidden key's dp may not be finite
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            x.r[j] = pv[hf * 16 + j] != 0.f ? x.r[j] : 0u;
+                    }
 #pragma unroll
                     for (int q4 = 0; q4 < 4; ++q4) {
-                        const float4 d = d4[hf * 4 + q4];
-                        const float dv[4] = {d.x, d.y, d.z, d.w};
+                        const float4 d = d4[hf * 4 + q4];  // minus delta
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
+                        for (int e = 0; e < 4; e += 2) {
                             const int j = hf * 16 + 4 * q4 + e;
-                            const float ds = pv[j] * sc * (__uint_as_float(x.r[4 * q4 + e]) - dv[e]);
-                            // rows past SQ: p = 0, and their delta is not defined
-                            pv[j] = plain || pv[j] != 0.f ? ds : 0.f;
+                            const float2 f = __fadd2_rn(make_float2(__uint_as_float(x.r[4 * q4 + e]), __uint_as_float(x.r[4 * q4 + e + 1])),
+                                                        e ? make_float2(d.z, d.w) : make_float2(d.x, d.y));
+                            const float2 r = __fmul2_rn(__fmul2_rn(make_float2(pv[j], pv[j + 1]), sc), f);
+                            pv[j] = r.x;
+                            pv[j + 1] = r.y;
                         }
                     }
                 }
