@@ -58,7 +58,7 @@
 //     dk and dv are joined in group order (vjp_join_groups).
 // [4, 32/8, 2048, 128] bf16 causal with a cap: statistics 175 us, backward 449
 // (without a cap 94 and 385), rounding 37.  Bound by the softmax warps' own
-// instructions (issue slots 52% and 49% busy) and, in the backward, by the dq
+// instructions (issue slots 55% and 46% busy) and, in the backward, by the dq
 // reductions into L2 (1.1 GB a call, as without a cap).
 //
 // Every wait is bounded (p.wait_ns); a wait that gives up ORs
