@@ -55,25 +55,33 @@ __device__ __forceinline__ void tanh_block(float (&y)[N])
     }
 }
 
-// The same for raw dot products under a cap, tanh(f x), with the factor in the
-// polynomial's coefficients: of degree 7 for |f x| <= 0.5 (largest relative
+// The same for raw dot products under a cap, out tanh(f x), with both factors in
+// the polynomial's coefficients: of degree 7 for |f x| <= 0.5 (largest relative
 // error 5.4e-7, a thousandth of the 16-bit rounding of the weights that follow),
 // five operations a score.  The backward's kernels use it: they are bound by
-// the arithmetic of their scores.
+// the arithmetic of their scores, and by the size of their code (a third path
+// for factors whose powers leave float32's range cost 21 and 8 us of the two
+// kernels of a capped [4, 32/8, 2048, 128] call without being run; those take
+// the second one here).
 struct TanhScaled {
-    float2 c[4];  // c_k f^(2 k + 1), twice
-    float f;
-    float top;    // 0.5 / |f|; negative: f^7 is no normal number, scores are scaled first
+    float2 c[4];  // c_k f^(2 k + 1) out, twice
+    float f, out;
+    float top;    // 0.5 / |f|; negative: never the polynomial
 };
 
-inline TanhScaled tanh_scaled(float f)
+inline TanhScaled tanh_scaled(float f, float out)
 {
     constexpr float kC[4] = {0.999999456f, -0.333263179f, 0.131902966f, -0.0444022255f};
     TanhScaled t{};
     t.f = f;
-    const float a = f < 0.f ? -f : f;
-    t.top = a >= 1e-5f && a <= 1e4f ? 0.5f / a : -1.f;
-    float pw = f;
+    t.out = out;
+    const float a = f < 0.f ? -f : f, o = out < 0.f ? -out : out;
+    if (!(a >= 1e-5f && a <= 1e4f && o >= 0.1f && o <= 1e6f)) {
+        t.top = -1.f;
+        return t;
+    }
+    t.top = 0.5f / a;
+    float pw = f * out;  // f^7 out stays within 1e-36 and 1e34
     for (int k = 0; k < 4; ++k, pw *= f * f)
         t.c[k] = make_float2(kC[k] * pw, kC[k] * pw);
     return t;
@@ -82,13 +90,6 @@ inline TanhScaled tanh_scaled(float f)
 template <int N>
 __device__ __forceinline__ void tanh_block_scaled(float (&x)[N], const TanhScaled& t)
 {
-    if (t.top < 0.f) {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            x[j] *= t.f;
-        tanh_block(x);
-        return;
-    }
     float top = 0.f;
 #pragma unroll
     for (int j = 0; j < N; j += 2)
@@ -106,11 +107,15 @@ __device__ __forceinline__ void tanh_block_scaled(float (&x)[N], const TanhScale
             x[j + 1] = a.y;
         }
     } else {
-        const float g = fabsf(t.f) * -2.8853900817779268f;  // 2 log2(e)
+        // (1 - e) / (1 + e) with e = exp(-2 |y|); y - y^3 / 3 up to 0.05, where
+        // 1 - e cancels: relative errors up to 1.2e-6 there and here
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const float e = fast_exp2(fabsf(x[j]) * g);
-            x[j] = copysignf(__fdividef(1.f - e, 1.f + e), x[j] * t.f);
+            const float y = x[j] * t.f;
+            const float e = fast_exp2(fabsf(y) * -2.8853900817779268f);  // 2 log2(e)
+            const float far = copysignf(__fdividef(1.f - e, 1.f + e), y);
+            const float near = fmaf(y * y, y * -0.333333333f, y);
+            x[j] = (fabsf(y) > 0.05f ? far : near) * t.out;
         }
     }
 }

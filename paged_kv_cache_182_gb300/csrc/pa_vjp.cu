@@ -525,7 +525,8 @@ static int vjp_impl(const void* q, const void* k, const void* v, const void* y, 
         sp.prefix = score->prefix;
         sp.cap_in = score->softcap > 0.f ? scale / score->softcap : 0.f;
         sp.cap_out = score->softcap > 0.f ? score->softcap * kVjpLog2e : 0.f;
-        sp.tanh = tanh_scaled(sp.cap_in);
+        sp.tanh = tanh_scaled(sp.cap_in, 1.f);
+        sp.tanh_cap = tanh_scaled(sp.cap_in, sp.cap_out);
         sp.bounded = sp.cap_out > 0.f && sp.cap_out <= 100.f && !sp.slopes;
         sp.window = score->window > 0 ? score->window : INT_MAX;
         sp.split = part > 0;

@@ -48,7 +48,7 @@ struct VjpScoredParams : VjpParams {
     const float* slopes;    // [HQ], or NULL
     const int32_t* prefix;  // [B], or NULL
     float cap_in, cap_out;  // scale / cap, cap * log2(e); 0 without a cap
-    TanhScaled tanh;        // of cap_in
+    TanhScaled tanh, tanh_cap;  // of cap_in; the same times cap_out
     int bounded;            // a cap of at most 69 and no slopes: 2^|score| needs no maximum taken off
     int window;             // INT_MAX: none
     // tensor cores, split: one CTA per query head instead of per group, its dk and

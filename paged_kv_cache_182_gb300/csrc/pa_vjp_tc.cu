@@ -56,7 +56,7 @@
 //     the wait for its dQ^T: S^T of the next step is issued right after dV.
 //   * With few key tiles each query head of a group has a CTA of its own, and
 //     dk and dv are joined in group order (vjp_join_groups).
-// [4, 32/8, 2048, 128] bf16 causal with a cap: statistics 175 us, backward 449
+// [4, 32/8, 2048, 128] bf16 causal with a cap: statistics 162 us, backward 430
 // (without a cap 94 and 385), rounding 37.  Bound by the softmax warps' own
 // instructions (issue slots 55% and 46% busy) and, in the backward, by the dq
 // reductions into L2 (1.1 GB a call, as without a cap).
@@ -92,7 +92,7 @@ constexpr int kSRows = 128;     // query rows per CTA of the statistics kernel
 // Statistics kernel: softmax warps, then one TMA, one MMA, four for delta and
 // the zeroing of dq.  Plain scores: 8 softmax warps, two threads a row (four a
 // row were slower: the MMA issue is as long as the softmax).  Modified scores
-// take three times the arithmetic: 16, four threads a row (175 us of a capped
+// take three times the arithmetic: 16, four threads a row (175 us then of a capped
 // [4, 32/8, 2048] call; 8 warps 233; 16 in two sets that take the tiles in turn,
 // two threads a row, 194).
 template <bool kMod>
@@ -150,6 +150,10 @@ __device__ __forceinline__ StatsItem stats_item_at(const VjpParamsOf<kMod>& p, i
     }
     return it;
 }
+
+// The factor of dp - delta in ds: under a cap p is kept with the sign of
+// tanh^2 - 1.
+__device__ __forceinline__ float vjp_ds_scale(const VjpScoredParams& p) { return p.cap_out != 0.f ? -p.scale : p.scale; }
 
 struct MainBars {
     uint64_t kv_full, qd_full[2], qd_empty[2], s_full, dp_full, p_ready, ds_ready, dq_full, dq_free, mma_done;
@@ -407,7 +411,7 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(&bars.s_free[s]);
-                    // modified scores: base-2 units with a distance bias, else to be
+                    // modified scores: base-2 units with a cap or a distance bias, else to be
                     // multiplied by c2 in the exponential
 #pragma unroll
                     for (int c = 0; c < COLS / 32; ++c) {
@@ -416,9 +420,9 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
                         for (int j = 0; j < 32; ++j)
                             y[j] = __uint_as_float(xs[c].r[j]);
                         if (p.cap_out != 0.f)
-                            tanh_block_scaled(y, p.tanh);
+                            tanh_block_scaled(y, p.tanh_cap);
                         if (p.slopes) {
-                            const float f = p.cap_out != 0.f ? p.cap_out : p.scale_log2;
+                            const float f = p.cap_out != 0.f ? 1.f : p.scale_log2;
                             const float d0 = static_cast<float>(i - kbase - c * 32);
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
@@ -444,8 +448,7 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
                         float2 s4[4] = {};
 #pragma unroll
                         for (int j = 0; j < COLS; j += 2) {
-                            const float2 e = __fmul2_rn(make_float2(sc[j], sc[j + 1]), make_float2(p.cap_out, p.cap_out));
-                            s4[(j >> 1) & 3] = __fadd2_rn(s4[(j >> 1) & 3], make_float2(fast_exp2(e.x), fast_exp2(e.y)));
+                            s4[(j >> 1) & 3] = __fadd2_rn(s4[(j >> 1) & 3], make_float2(fast_exp2(sc[j]), fast_exp2(sc[j + 1])));
                         }
                         m = 0.f;
                         l += ((s4[0].x + s4[0].y) + (s4[1].x + s4[1].y)) + ((s4[2].x + s4[2].y) + (s4[3].x + s4[3].y));
@@ -487,7 +490,7 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
                                        fmaxf(fmaxf(pm8[4], pm8[5]), fmaxf(pm8[6], pm8[7])));
                 float c2 = p.scale_log2;
                 if constexpr (kMod)
-                    c2 = p.slopes ? 1.f : p.cap_out != 0.f ? p.cap_out : p.scale_log2;
+                    c2 = p.slopes || p.cap_out != 0.f ? 1.f : p.scale_log2;
                 const float mt = fmaxf(m, pm * c2);  // base-2 units
                 if (mt != -INFINITY) {
                     float s8[8];
@@ -509,8 +512,7 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
                 bars.xl[k & 1][part - 1][row] = l;
             }
             asm volatile("bar.sync %0, %1;" ::"r"(1 + (warp & 3)), "n"(PARTS * 32) : "memory");
-            // (modified scores: minus lse2 and minus delta are kept, as the backward
-            // adds them two at a time)
+            // (modified scores: minus lse2 is kept, as the backward adds it)
             if (part == 0 && !fault) {
                 float mt = m;
 #pragma unroll
@@ -538,6 +540,9 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
         // load (16 lanes x 16 bytes a row), RP row pairs in flight (four where
         // twice the softmax warps leave fewer registers)
         constexpr int RP = kMod ? 4 : 8;
+        float f = 1.f;  // modified scores: what the backward adds to its scaled dp
+        if constexpr (kMod)
+            f = -vjp_ds_scale(p);
         const int dw = warp - (SW + 2);
         const int half = lane >> 4, c16 = lane & 15;
         for (int k = 0;; ++k) {
@@ -579,7 +584,7 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
                     const int i = it.i0 + dw * 32 + rb + 2 * e + half;
                     if (c16 == 0)
                         // padding rows up to sqp: no gradient
-                        p.delta[s0 + i] = i < p.SQ ? (kMod ? -d : d) : 0.f;
+                        p.delta[s0 + i] = i < p.SQ ? f * d : 0.f;
                 }
             }
             // the item's real rows of the accumulator: contiguous, 512 bytes a row
@@ -933,12 +938,13 @@ __global__ void __launch_bounds__(kMainThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         w[hf * 8 + e] = pack2<T>(pv[hf * 16 + 2 * e], pv[hf * 16 + 2 * e + 1]);
-                    // from here on p times the cap's factor
+                    // from here on minus p times the cap's factor 1 - tanh^2 (vjp_ds_scale
+                    // has the sign)
                     if (p.cap_out != 0.f) {
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
                             const float2 t2 = make_float2(y[j], y[j + 1]);
-                            const float2 f2 = __ffma2_rn(__fmul2_rn(t2, t2), make_float2(-1.f, -1.f), make_float2(1.f, 1.f));
+                            const float2 f2 = __ffma2_rn(t2, t2, make_float2(-1.f, -1.f));
                             const float2 r = __fmul2_rn(make_float2(pv[hf * 16 + j], pv[hf * 16 + j + 1]), f2);
                             pv[hf * 16 + j] = r.x;
                             pv[hf * 16 + j + 1] = r.y;
@@ -958,7 +964,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                     return false;
                 const float4* d4 = reinterpret_cast<const float4*>(sStat + (it & 1) * 256 + 128 + part * 32);
                 tc_fence_after();
-                const float2 sc = make_float2(p.scale, p.scale);
+                const float2 sc = make_float2(vjp_ds_scale(p), vjp_ds_scale(p));
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     Cols16 x;
@@ -970,13 +976,13 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                     }
 #pragma unroll
                     for (int q4 = 0; q4 < 4; ++q4) {
-                        const float4 d = d4[hf * 4 + q4];  // minus delta
+                        const float4 d = d4[hf * 4 + q4];  // minus delta, scaled as dp is here
 #pragma unroll
                         for (int e = 0; e < 4; e += 2) {
                             const int j = hf * 16 + 4 * q4 + e;
-                            const float2 f = __fadd2_rn(make_float2(__uint_as_float(x.r[4 * q4 + e]), __uint_as_float(x.r[4 * q4 + e + 1])),
-                                                        e ? make_float2(d.z, d.w) : make_float2(d.x, d.y));
-                            const float2 r = __fmul2_rn(__fmul2_rn(make_float2(pv[j], pv[j + 1]), sc), f);
+                            const float2 f = __ffma2_rn(make_float2(__uint_as_float(x.r[4 * q4 + e]), __uint_as_float(x.r[4 * q4 + e + 1])),
+                                                        sc, e ? make_float2(d.z, d.w) : make_float2(d.x, d.y));
+                            const float2 r = __fmul2_rn(make_float2(pv[j], pv[j + 1]), f);
                             pv[j] = r.x;
                             pv[j + 1] = r.y;
                         }
