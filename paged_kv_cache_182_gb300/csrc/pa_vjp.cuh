@@ -57,8 +57,8 @@ struct VjpScoredParams : VjpParams {
     float* part[2];
 };
 
-template <bool kMod>
-using VjpParamsOf = std::conditional_t<kMod, VjpScoredParams, VjpParams>;
+template <int kMod>
+using VjpParamsOf = std::conditional_t<kMod != 0, VjpScoredParams, VjpParams>;
 
 // Keys below are visible to every row of sequence b.
 __device__ __forceinline__ int vjp_prefix(const VjpScoredParams& p, int b)

@@ -44,19 +44,21 @@
 //   two-stage ring; warp 17 issues the MMAs (one thread).  Tensor memory
 //   (512 columns): dK | dV | S^T (then P) | dP^T (then dQ^T).
 //
-// Modified scores (template flag kMod, pa_attention_vjp_scored): capped by a
-// tanh, biased by distance, limited to a window beside a prefix.
+// Modified scores (kMod 1 and 2, pa_attention_vjp_scored): capped by a tanh,
+// biased by distance, limited to a window beside a prefix.
 //   * Key tiles (statistics) and row steps (backward) outside prefix and window
 //     are left out; masks are tested once per block of 32.
 //   * The cap's tanh is a polynomial without special-function operations
 //     (pa_tanh.cuh); its gradient's factor 1 - tanh^2 goes into p once P is
-//     packed, so it costs no register.  With a cap of at most 69 and no slopes
-//     the row sums need no running maximum.
+//     packed, so it costs no register.
+//   * kMod 2 is for a cap of at most 69 without slopes: the row sums need no
+//     running maximum.  A kernel of its own because both are bound by the size
+//     of their code too (one kernel for all: statistics 162, backward 430).
 //   * The backward computes P of the next step between dS^T of this one and
 //     the wait for its dQ^T: S^T of the next step is issued right after dV.
 //   * With few key tiles each query head of a group has a CTA of its own, and
 //     dk and dv are joined in group order (vjp_join_groups).
-// [4, 32/8, 2048, 128] bf16 causal with a cap: statistics 162 us, backward 430
+// [4, 32/8, 2048, 128] bf16 causal with a cap: statistics 153 us, backward 421
 // (without a cap 94 and 385), rounding 37.  Bound by the softmax warps' own
 // instructions (issue slots 55% and 46% busy) and, in the backward, by the dq
 // reductions into L2 (1.1 GB a call, as without a cap).
@@ -95,10 +97,10 @@ constexpr int kSRows = 128;     // query rows per CTA of the statistics kernel
 // take three times the arithmetic: 16, four threads a row (175 us then of a capped
 // [4, 32/8, 2048] call; 8 warps 233; 16 in two sets that take the tiles in turn,
 // two threads a row, 194).
-template <bool kMod>
+template <int kMod>
 constexpr int kSoftWarps = kMod ? 16 : 8;
 constexpr int kDeltaWarps = 4;
-template <bool kMod>
+template <int kMod>
 constexpr int kStatsThreads = (kSoftWarps<kMod> + 2 + kDeltaWarps) * 32;
 constexpr int kKStages = 4;     // statistics kernel: K ring depth
 constexpr int kHalf128 = 16384;  // one 64-column half of a 128-row tile, bytes
@@ -126,7 +128,7 @@ struct StatsItem {
     __device__ __forceinline__ int tile(int t) const { return t >= skip_at ? t + skip : t; }
 };
 
-template <bool kMod>
+template <int kMod>
 __device__ __forceinline__ StatsItem stats_item_at(const VjpParamsOf<kMod>& p, int n, int tiles)
 {
     StatsItem it;
@@ -210,7 +212,7 @@ __device__ __forceinline__ float2 unpack2(uint32_t w)
 // Row statistics.  grid = min(items, SMs); items = B * HQ * ceil(SQ / 128),
 // numbered row tile slowest, the row tiles that see the most keys (causal)
 // first.
-template <typename T, bool kMod>
+template <typename T, int kMod>
 __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
     vjp_stats_tc(const __grid_constant__ VjpParamsOf<kMod> p, const __grid_constant__ CUtensorMap qmap,
                  const __grid_constant__ CUtensorMap kmap)
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
             float m = -INFINITY, l = 0.f;
             float slope2 = 0.f;
             if constexpr (kMod)
-                slope2 = p.slopes ? __ldg(p.slopes + it.h) * kVjpLog2e : 0.f;
+                slope2 = kMod == 1 && p.slopes ? __ldg(p.slopes + it.h) * kVjpLog2e : 0.f;
             for (int t = 0; t < it.ntiles && !fault; ++t, ++g) {
                 const int s = g & 1;
                 const bool got = __all_sync(
@@ -419,9 +421,9 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             y[j] = __uint_as_float(xs[c].r[j]);
-                        if (p.cap_out != 0.f)
+                        if (kMod == 2 || p.cap_out != 0.f)
                             tanh_block_scaled(y, p.tanh_cap);
-                        if (p.slopes) {
+                        if (kMod == 1 && p.slopes) {
                             const float f = p.cap_out != 0.f ? 1.f : p.scale_log2;
                             const float d0 = static_cast<float>(i - kbase - c * 32);
 #pragma unroll
@@ -443,7 +445,7 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
                             if (!(kbase + j < p.SK && vjp_seen(p, it.pl, i, kbase + j)))
                                 sc[j] = -INFINITY;
                     }
-                    if (p.bounded) {
+                    if constexpr (kMod == 2) {
                         // scores within +-100: the sum of their powers of two needs no maximum
                         float2 s4[4] = {};
 #pragma unroll
@@ -453,10 +455,11 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
                         m = 0.f;
                         l += ((s4[0].x + s4[0].y) + (s4[1].x + s4[1].y)) + ((s4[2].x + s4[2].y) + (s4[3].x + s4[3].y));
                         continue;
-                    }
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < COLS; ++j)
-                        pm8[j & 7] = fmaxf(pm8[j & 7], sc[j]);
+                        for (int j = 0; j < COLS; ++j)
+                            pm8[j & 7] = fmaxf(pm8[j & 7], sc[j]);
+                    }
                 } else {
                 // the mask test is taken once per tile (warp-uniform), never per
                 // score: a branch per score cost more than the rest of the tile
@@ -604,7 +607,7 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
 // ---------------------------------------------------------------------------
 // Backward.  grid = ceil(SK / 128) * B * HK, (batch, key/value head) fastest:
 // the key tiles that the most (causal) rows see are launched first.
-template <typename T, typename TO, bool kMod>
+template <typename T, typename TO, int kMod>
 __global__ void __launch_bounds__(kMainThreads, 1)
     vjp_main_tc(const __grid_constant__ VjpParamsOf<kMod> p, const __grid_constant__ CUtensorMap qmap,
                 const __grid_constant__ CUtensorMap gmap, const __grid_constant__ CUtensorMap kmap,
@@ -886,7 +889,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                 tc_fence_after();
                 const int rb = i0 + part * 32;  // first row of this thread's columns
                 const float4* l4 = reinterpret_cast<const float4*>(sStat + st * 256 + part * 32);
-                const float slope2 = p.slopes ? __ldg(p.slopes + h) * kVjpLog2e : 0.f;
+                const float slope2 = kMod == 1 && p.slopes ? __ldg(p.slopes + h) * kVjpLog2e : 0.f;
                 // every row of the block sees every key of the tile, as far as the rule goes
                 const bool in_rule = k0 + kKeys <= pl ||
                                      ((!p.causal || k0 + kKeys - 1 <= rb) && rb + 31 - k0 < p.window &&
@@ -902,7 +905,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                     for (int e = 0; e < 16; ++e)
                         y[e] = __uint_as_float(x.r[e]);
                     float c = p.scale_log2;
-                    if (p.cap_out != 0.f) {
+                    if (kMod == 2 || p.cap_out != 0.f) {
                         tanh_block_scaled(y, p.tanh);
                         c = p.cap_out;
                     }
@@ -915,7 +918,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                         z[4 * q4 + 2] = l.z;
                         z[4 * q4 + 3] = l.w;
                     }
-                    if (p.slopes) {
+                    if (kMod == 1 && p.slopes) {
                         const float d0 = static_cast<float>(rb + hf * 16 - key);
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
@@ -940,7 +943,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                         w[hf * 8 + e] = pack2<T>(pv[hf * 16 + 2 * e], pv[hf * 16 + 2 * e + 1]);
                     // from here on minus p times the cap's factor 1 - tanh^2 (vjp_ds_scale
                     // has the sign)
-                    if (p.cap_out != 0.f) {
+                    if (kMod == 2 || p.cap_out != 0.f) {
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
                             const float2 t2 = make_float2(y[j], y[j + 1]);
@@ -1259,9 +1262,9 @@ __global__ void __launch_bounds__(256) vjp_join_groups(const __grid_constant__ V
     }
 }
 
-template <bool kMod>
+template <int kMod>
 using StatsFn = void (*)(VjpParamsOf<kMod>, CUtensorMap, CUtensorMap);
-template <bool kMod>
+template <int kMod>
 using MainFn = void (*)(VjpParamsOf<kMod>, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap);
 
 // [B * heads][rows][128] 16-bit as {64, 2, rows, B * heads}; box {64, 1, box_rows, 1}:
@@ -1282,7 +1285,7 @@ int encode_rows(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int 
                : PA_ERR_CUDA;
 }
 
-template <bool kMod>
+template <int kMod>
 int launch_tc(const VjpParamsOf<kMod>& p, int dtype, bool f32_out, cudaStream_t st, uint64_t* launches)
 {
     const CUtensorMapDataType dt =
@@ -1383,12 +1386,12 @@ bool vjp_tc_supported(int dtype, int D, int groups, int mask_kind)
 
 int launch_vjp_tc(const VjpParams& p, int dtype, bool f32_out, cudaStream_t st, uint64_t* launches)
 {
-    return launch_tc<false>(p, dtype, f32_out, st, launches);
+    return launch_tc<0>(p, dtype, f32_out, st, launches);
 }
 
 int launch_vjp_tc_scored(const VjpScoredParams& p, int dtype, bool f32_out, cudaStream_t st, uint64_t* launches)
 {
-    return launch_tc<true>(p, dtype, f32_out, st, launches);
+    return p.bounded ? launch_tc<2>(p, dtype, f32_out, st, launches) : launch_tc<1>(p, dtype, f32_out, st, launches);
 }
 
 }  // namespace pa
