@@ -542,7 +542,7 @@ static int vjp_impl(const void* q, const void* k, const void* v, const void* y, 
     else
         rc = tc ? launch_vjp_tc(p, o.dtype, odt == PA_F32, st, &launches)
                 : pick_simt<false>(o.dtype, odt == PA_F32)(p, st, &launches);
-    if (rc == PA_OK && p.dq_acc && SQ > 0) {
+    if (rc == PA_OK && p.dq_acc && SQ > 0 && !(score && tc)) {  // (those round dq with the rest)
         const int64_t n = qn;
         const int blocks = static_cast<int>(std::min<int64_t>((n + 255) / 256, 152 * 16));
         if (odt == PA_F16)

@@ -57,9 +57,13 @@
 //   * The backward computes P of the next step between dS^T of this one and
 //     the wait for its dQ^T: S^T of the next step is issued right after dV.
 //   * With few key tiles each query head of a group has a CTA of its own, and
-//     dk and dv are joined in group order (vjp_join_groups).
-// [4, 32/8, 2048, 128] bf16 causal with a cap: statistics 153 us, backward 421
-// (without a cap 94 and 385), rounding 37.  Bound by the softmax warps' own
+//     dk and dv are joined in group order, with the rounding of dq (vjp_finish).
+//   * The three launches follow one another programmatically: a CTA of the next
+//     kernel sets up, and loads its first tiles, while the last ones of the
+//     kernel before end ([2, 12/4, 1500, 128] with slopes, a window and a prefix:
+//     117 -> 104 us with the join and the rounding in one launch).
+// [4, 32/8, 2048, 128] bf16 causal with a cap: 609 us, of it statistics 153,
+// backward 421 (without a cap 94 and 385).  Bound by the softmax warps' own
 // instructions (issue slots 55% and 46% busy) and, in the backward, by the dq
 // reductions into L2 (1.1 GB a call, as without a cap).
 //
@@ -227,6 +231,8 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
             atomicOr(p.status, PA_STATUS_TIMEOUT);
         return;
     }
+    if constexpr (kMod)
+        grid_dependents_launch();  // the backward loads its first tiles as this grid's CTAs leave
     unsigned char* sQ = smem_raw;                  // buffer u at u * 2 * kHalf128
     unsigned char* sK = smem_raw + 4 * kHalf128;   // stage s at s * 2 * kHalf128
     StatsBars& bars = *reinterpret_cast<StatsBars*>(smem_raw + (4 + 2 * kKStages) * kHalf128);
@@ -620,6 +626,8 @@ __global__ void __launch_bounds__(kMainThreads, 1)
             atomicOr(p.status, PA_STATUS_TIMEOUT);
         return;
     }
+    if constexpr (kMod)
+        grid_dependents_launch();
     unsigned char* sK = smem_raw;                  // 2 halves of 16 KB
     unsigned char* sV = sK + 2 * kHalf128;         // 2 halves
     unsigned char* sQ = sV + 2 * kHalf128;         // 2 stages x 2 halves of 16 KB
@@ -739,6 +747,8 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                                 &bars.qd_full[st]);
                 }
                 const int64_t srow = (static_cast<int64_t>(b) * p.HQ + h) * p.sqp + i0;
+                if (kMod && it == 0)
+                    grid_dependency_wait();  // the statistics
                 bulk_load(sStat + st * 256, p.lse + srow, 512, &bars.qd_full[st]);
                 bulk_load(sStat + st * 256 + 128, p.delta + srow, 512, &bars.qd_full[st]);
                 issued = it + 1;
@@ -854,6 +864,8 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         const bool key_ok = key < p.SK;
         const bool keys_all = k0 + kKeys <= p.SK;  // every key of the tile is real
         bool fault = false;
+        if constexpr (kMod)
+            grid_dependency_wait();  // dq's accumulator is zero
         // the dQ^T reductions of a step are issued in two halves: rows 0-15 of
         // this thread's 32 as soon as they are read, rows 16-31 held in
         // registers and issued in the next step once its dS^T is handed over,
@@ -1239,26 +1251,41 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(bars.tmem), "r"(512) : "memory");
 }
 
-// dk and dv of split groups: the partial sums in group order.  grid.y: dk, dv.
 template <typename TO>
-__global__ void __launch_bounds__(256) vjp_join_groups(const __grid_constant__ VjpScoredParams p)
+__device__ __forceinline__ void store4(TO* out, float4 v)
 {
-    const int64_t n4 = static_cast<int64_t>(p.B) * p.HK * p.SK * (kD / 4);
-    const float4* part = reinterpret_cast<const float4*>(p.part[blockIdx.y]);
-    TO* out = static_cast<TO*>(blockIdx.y ? p.dv : p.dk);
-    for (int64_t e = blockIdx.x * 256ll + threadIdx.x; e < n4; e += gridDim.x * 256ll) {
-        float4 s = __ldcg(part + e);
+    if constexpr (std::is_same<TO, float>::value)
+        *reinterpret_cast<float4*>(out) = v;
+    else
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack2<TO>(v.x, v.y), pack2<TO>(v.z, v.w));
+}
+
+// The rest of a call with modified scores, four elements a thread: dq rounded from
+// its accumulator (16-bit outputs), then dk and dv of split groups, the partial
+// sums in group order.
+template <typename TO>
+__global__ void __launch_bounds__(256) vjp_finish(const __grid_constant__ VjpScoredParams p)
+{
+    grid_dependency_wait();
+    const int64_t first = blockIdx.x * 256ll + threadIdx.x, step = gridDim.x * 256ll;
+    const int64_t nq = p.dq_acc ? static_cast<int64_t>(p.B) * p.HQ * p.SQ * (kD / 4) : 0;
+    const int64_t nk = p.split ? static_cast<int64_t>(p.B) * p.HK * p.SK * (kD / 4) : 0;
+    const float4* acc = reinterpret_cast<const float4*>(p.dq_acc);
+#pragma unroll 4
+    for (int64_t e = first; e < nq; e += step)
+        store4(static_cast<TO*>(p.dq) + 4 * e, __ldcg(acc + e));
+    for (int64_t e = first; e < 2 * nk; e += step) {
+        const int64_t at = e < nk ? e : e - nk;
+        const float4* part = reinterpret_cast<const float4*>(p.part[e < nk ? 0 : 1]) + at;
+        float4 t = __ldcg(part);
         for (int g = 1; g < p.groups; ++g) {
-            const float4 x = __ldcg(part + g * n4 + e);
-            s.x += x.x;
-            s.y += x.y;
-            s.z += x.z;
-            s.w += x.w;
+            const float4 x = __ldcg(part + g * nk);
+            t.x += x.x;
+            t.y += x.y;
+            t.z += x.z;
+            t.w += x.w;
         }
-        if constexpr (std::is_same<TO, float>::value)
-            reinterpret_cast<float4*>(out)[e] = s;
-        else
-            reinterpret_cast<uint2*>(out)[e] = make_uint2(pack2<TO>(s.x, s.y), pack2<TO>(s.z, s.w));
+        store4(static_cast<TO*>(e < nk ? p.dk : p.dv) + 4 * at, t);
     }
 }
 
@@ -1283,6 +1310,21 @@ int encode_rows(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int 
                    CUDA_SUCCESS
                ? PA_OK
                : PA_ERR_CUDA;
+}
+
+// A launch that may start before the kernel ahead of it has ended.
+cudaLaunchConfig_t programmatic(cudaLaunchAttribute* attr, unsigned grid, int threads, size_t smem, cudaStream_t st)
+{
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
 }
 
 template <int kMod>
@@ -1346,24 +1388,26 @@ int launch_tc(const VjpParamsOf<kMod>& p, int dtype, bool f32_out, cudaStream_t 
         const long long grid = static_cast<long long>(p.B) * heads * ((p.SK + kKeys - 1) / kKeys);
         if (grid >= (1ll << 31))
             return PA_ERR_BAD_DIMS;
-        fn<<<static_cast<unsigned>(grid), kMainThreads, kMainSmem, st>>>(p, qmap, gmap, kmap, vmap);
-        if (cudaGetLastError() != cudaSuccess)
+        cudaLaunchAttribute pdl[1];
+        cudaLaunchConfig_t cfg = programmatic(pdl, static_cast<unsigned>(grid), kMainThreads, kMainSmem, st);
+        cfg.numAttrs = kMod && p.SQ > 0 ? 1 : 0;  // behind the statistics kernel
+        if (cudaLaunchKernelEx(&cfg, fn, p, qmap, gmap, kmap, vmap) != cudaSuccess)
             return PA_ERR_CUDA;
         ++*launches;
-        if constexpr (kMod)
-            if (p.split) {
-                const long long n4 = static_cast<long long>(p.B) * p.HK * p.SK * (kD / 4);
-                const dim3 jg(static_cast<unsigned>((n4 + 255) / 256 < 152 * 8 ? (n4 + 255) / 256 : 152 * 8), 2);
-                if (f32_out)
-                    vjp_join_groups<float><<<jg, 256, 0, st>>>(p);
-                else if (bf)
-                    vjp_join_groups<__nv_bfloat16><<<jg, 256, 0, st>>>(p);
-                else
-                    vjp_join_groups<__half><<<jg, 256, 0, st>>>(p);
-                if (cudaGetLastError() != cudaSuccess)
-                    return PA_ERR_CUDA;
-                ++*launches;
-            }
+    }
+    if constexpr (kMod) {
+        const long long nq = p.dq_acc ? static_cast<long long>(p.B) * p.HQ * p.SQ * (kD / 4) : 0;
+        const long long nk = p.split ? static_cast<long long>(p.B) * p.HK * p.SK * (kD / 4) : 0;
+        const long long n = nq > 2 * nk ? nq : 2 * nk;
+        if (n > 0) {
+            cudaLaunchAttribute pdl[1];
+            const cudaLaunchConfig_t cfg =
+                programmatic(pdl, static_cast<unsigned>((n + 255) / 256 < 152 * 8 ? (n + 255) / 256 : 152 * 8), 256, 0, st);
+            const auto fn = f32_out ? vjp_finish<float> : bf ? vjp_finish<__nv_bfloat16> : vjp_finish<__half>;
+            if (cudaLaunchKernelEx(&cfg, fn, static_cast<const VjpScoredParams&>(p)) != cudaSuccess)
+                return PA_ERR_CUDA;
+            ++*launches;
+        }
     }
     return PA_OK;
 }
