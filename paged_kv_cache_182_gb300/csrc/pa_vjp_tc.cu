@@ -47,13 +47,16 @@
 // Modified scores (kMod 1 and 2, pa_attention_vjp_scored): capped by a tanh,
 // biased by distance, limited to a window beside a prefix.
 //   * Key tiles (statistics) and row steps (backward) outside prefix and window
-//     are left out; masks are tested once per block of 32.
+//     are left out; masks are tested once per block of 32, and in it as intervals
+//     (of keys for a row, of rows for a key): two operations a score.  With the
+//     rule written out per score, statistics took 153 us, backward 421, the
+//     windowed call 104.
 //   * The cap's tanh is a polynomial without special-function operations
 //     (pa_tanh.cuh); its gradient's factor 1 - tanh^2 goes into p once P is
 //     packed, so it costs no register.
 //   * kMod 2 is for a cap of at most 69 without slopes: the row sums need no
 //     running maximum.  A kernel of its own because both are bound by the size
-//     of their code too (one kernel for all: statistics 162, backward 430).
+//     of their code too (one kernel for all: 162 for 153, 430 for 421).
 //   * The backward computes P of the next step between dS^T of this one and
 //     the wait for its dQ^T: S^T of the next step is issued right after dV.
 //   * With few key tiles each query head of a group has a CTA of its own, and
@@ -62,8 +65,8 @@
 //     kernel sets up, and loads its first tiles, while the last ones of the
 //     kernel before end ([2, 12/4, 1500, 128] with slopes, a window and a prefix:
 //     117 -> 104 us with the join and the rounding in one launch).
-// [4, 32/8, 2048, 128] bf16 causal with a cap: 609 us, of it statistics 153,
-// backward 421 (without a cap 94 and 385).  Bound by the softmax warps' own
+// [4, 32/8, 2048, 128] bf16 causal with a cap: 562 us, of it statistics 128,
+// backward 405 (without a cap 94 and 385).  Bound by the softmax warps' own
 // instructions (issue slots 55% and 46% busy) and, in the backward, by the dq
 // reductions into L2 (1.1 GB a call, as without a cap).
 //
@@ -160,6 +163,9 @@ __device__ __forceinline__ StatsItem stats_item_at(const VjpParamsOf<kMod>& p, i
 // The factor of dp - delta in ds: under a cap p is kept with the sign of
 // tanh^2 - 1.
 __device__ __forceinline__ float vjp_ds_scale(const VjpScoredParams& p) { return p.cap_out != 0.f ? -p.scale : p.scale; }
+
+// The largest distance inside the window.
+__device__ __forceinline__ int vjp_reach(const VjpScoredParams& p) { return min(p.window, 1 << 30) - 1; }
 
 struct MainBars {
     uint64_t kv_full, qd_full[2], qd_empty[2], s_full, dp_full, p_ready, ds_ready, dq_full, dq_free, mma_done;
@@ -446,9 +452,13 @@ __global__ void __launch_bounds__(kStatsThreads<kMod>, 1)
                                        (kbase + COLS <= p.SK && (!p.causal || kbase + COLS - 1 <= i_w) &&
                                         i_w + 31 - kbase < p.window && (p.causal || kbase + COLS - 1 - i_w < p.window));
                     if (!plain) {
+                        // keys below the prefix, and the interval of the rule
+                        const int pre = it.pl - kbase, at = kbase - (i - vjp_reach(p));
+                        const int last = min(p.SK - 1, p.causal ? i : i + vjp_reach(p));
+                        const unsigned span = static_cast<unsigned>(max(last - (i - vjp_reach(p)) + 1, 0));
 #pragma unroll
                         for (int j = 0; j < COLS; ++j)
-                            if (!(kbase + j < p.SK && vjp_seen(p, it.pl, i, kbase + j)))
+                            if (j >= pre && static_cast<unsigned>(at + j) >= span)
                                 sc[j] = -INFINITY;
                     }
                     if constexpr (kMod == 2) {
@@ -889,6 +899,11 @@ __global__ void __launch_bounds__(kMainThreads, 1)
             // and the wait for its dQ^T -- a third of the step's arithmetic, which
             // would otherwise stand between S^T and everything after it.
             float pv[32];        // p times the cap's factor, then ds
+            // the rows that see this thread's key: an interval, as the rule is the same
+            // seen from the key
+            const int row_lo = key < pl ? 0 : p.causal ? key : key - vjp_reach(p);
+            const unsigned row_span =
+                key_ok ? static_cast<unsigned>(max((key < pl ? p.SQ - 1 : min(p.SQ - 1, key + vjp_reach(p))) - row_lo + 1, 0)) : 0u;
             bool plain = false;  // of the step whose p is in pv: no mask on this thread's block
             auto make_p = [&](int it) {
                 const int st = it & 1;
@@ -944,11 +959,9 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                     }
                     if (!plain) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const int row = rb + hf * 16 + j;
-                            if (!(key_ok && row < p.SQ && vjp_seen(p, pl, row, key)))
+                        for (int j = 0; j < 16; ++j)
+                            if (static_cast<unsigned>(rb - row_lo + hf * 16 + j) >= row_span)
                                 pv[hf * 16 + j] = 0.f;
-                        }
                     }
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
