@@ -48,7 +48,8 @@ namespace {
 constexpr int kBins = 2048;
 constexpr int kKeys = 8;            // weights in flight per thread of the selection
 constexpr int kMoveThreads = 256;
-constexpr int kRun = 128;           // in place: rows of a run
+constexpr int kRunBytes = 16384;    // in place: a run of rows' slices
+constexpr int kRuns = 6;            // in flight
 constexpr int kMoveBytes = 16384;   // other blocks: rows of one item, at most (one row when longer)
 constexpr int kMoveRows = 256;
 constexpr int kMaxRowBytes = 65536;
@@ -365,21 +366,23 @@ __device__ __forceinline__ int slot_of(const EvictParams& p, int phys, int j, bo
     return -1;
 }
 
-// grid (slices * 2, B): a slice of VS 16-byte vectors of K or V of a sequence.
-// Thread t < kRun looks up the rows of a run, three steps ahead of their copy:
-// kept index, then table entries, then slots.
+// grid (slices * 2, B): a slice of VS 16-byte vectors of K or V of a sequence, S
+// runs in flight.  Each thread looks up LOOK rows of a run, three steps ahead of
+// their copy: kept index, then table entries, then slots.
 template <int VS, int S>
 __global__ void __launch_bounds__(kMoveThreads) pa_evict_shift(const __grid_constant__ EvictParams p)
 {
-    extern __shared__ __align__(16) unsigned char ring[];  // [S runs][kRun rows][VS vectors]
-    __shared__ int src[2][kRun], dst[S + 1][kRun];
+    constexpr int RUN = kRunBytes / (16 * VS), LOOK = (RUN + kMoveThreads - 1) / kMoveThreads;
+    static_assert(RUN % kMoveThreads == 0 || RUN < kMoveThreads, "rows looked up by the threads");
+    extern __shared__ __align__(16) unsigned char ring[];  // [S runs][RUN rows][VS vectors]
+    __shared__ int src[2][RUN], dst[S + 1][RUN];
     const int tid = threadIdx.x;
     const int kv = blockIdx.x & 1, slice = blockIdx.x >> 1, b = blockIdx.y;
     const int n = clamped_len(p, b, false);
     grid_dependency_wait();  // the kept list
     if (n <= p.budget)
         return;
-    const int runs = (p.budget + kRun - 1) / kRun;
+    const int runs = (p.budget + RUN - 1) / RUN;
     const int32_t* kept = p.kept + static_cast<int64_t>(b) * p.budget;
     const int32_t* table = p.table + static_cast<int64_t>(b) * p.maxb;
     const bool report = blockIdx.x == 0;
@@ -388,40 +391,50 @@ __global__ void __launch_bounds__(kMoveThreads) pa_evict_shift(const __grid_cons
     const int v = tid % VS, rr = tid / VS;
     constexpr int kStep = kMoveThreads / VS;  // rows the CTA copies at once
 
-    int j1 = -1, j2 = -1, ps = -1, pd = -1;  // the run three and two ahead: kept; its entries
+    int j1[LOOK], j2[LOOK], ps[LOOK], pd[LOOK];  // the run three and two ahead: kept; its entries
     auto fetch_kept = [&](int run) {
-        const int r = run * kRun + tid;
-        j1 = tid < kRun && r < p.budget ? kept[r] : -1;
+#pragma unroll
+        for (int k = 0; k < LOOK; ++k) {
+            const int at = tid + k * kMoveThreads, r = run * RUN + at;
+            j1[k] = at < RUN && r < p.budget ? kept[r] : -1;
+        }
     };
     auto fetch_entries = [&](int run) {
-        j2 = j1;
-        if (j2 >= 0) {
-            ps = __ldg(table + j2 / p.BLOCK);
-            pd = __ldg(table + (run * kRun + tid) / p.BLOCK);
+#pragma unroll
+        for (int k = 0; k < LOOK; ++k) {
+            j2[k] = j1[k];
+            if (j2[k] >= 0) {
+                ps[k] = __ldg(table + j2[k] / p.BLOCK);
+                pd[k] = __ldg(table + (run * RUN + tid + k * kMoveThreads) / p.BLOCK);
+            }
         }
     };
     auto put_slots = [&](int run) {
-        if (tid < kRun) {
-            const int r = run * kRun + tid;
-            int s = -1, d = -1;
-            if (j2 >= 0 && j2 != r) {
-                s = slot_of(p, ps, j2, report);
-                d = slot_of(p, pd, r, report);
+#pragma unroll
+        for (int k = 0; k < LOOK; ++k) {
+            const int at = tid + k * kMoveThreads;
+            if (at < RUN) {
+                const int r = run * RUN + at;
+                int f = -1, t = -1;
+                if (j2[k] >= 0 && j2[k] != r) {
+                    f = slot_of(p, ps[k], j2[k], report);
+                    t = slot_of(p, pd[k], r, report);
+                }
+                src[run & 1][at] = t < 0 ? -1 : f;
+                dst[run % (S + 1)][at] = f < 0 ? -1 : t;
             }
-            src[run & 1][tid] = d < 0 ? -1 : s;
-            dst[run % (S + 1)][tid] = s < 0 ? -1 : d;
         }
     };
     auto issue = [&](int run) {  // reads of a run
         if (v < nv) {
 #pragma unroll
-            for (int k = 0; k < kRun / kStep; ++k) {
+            for (int k = 0; k < RUN / kStep; ++k) {
                 const int row = rr + k * kStep;
-                const int s = src[run & 1][row];
-                if (s >= 0)
+                const int f = src[run & 1][row];
+                if (f >= 0)
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                     smem_u32(ring + (((run % S) * kRun + row) * VS + v) * 16)),
-                                 "l"(pool + static_cast<int64_t>(s) * p.row_bytes + v * 16)
+                                     smem_u32(ring + (((run % S) * RUN + row) * VS + v) * 16)),
+                                 "l"(pool + static_cast<int64_t>(f) * p.row_bytes + v * 16)
                                  : "memory");
             }
         }
@@ -446,12 +459,12 @@ __global__ void __launch_bounds__(kMoveThreads) pa_evict_shift(const __grid_cons
             __syncthreads();  // run `done` has been read by every thread, and all before it
             if (v < nv) {
 #pragma unroll
-                for (int k = 0; k < kRun / kStep; ++k) {
+                for (int k = 0; k < RUN / kStep; ++k) {
                     const int row = rr + k * kStep;
-                    const int d = dst[done % (S + 1)][row];
-                    if (d >= 0)
-                        *reinterpret_cast<uint4*>(pool + static_cast<int64_t>(d) * p.row_bytes + v * 16) =
-                            *reinterpret_cast<const uint4*>(ring + (((done % S) * kRun + row) * VS + v) * 16);
+                    const int t = dst[done % (S + 1)][row];
+                    if (t >= 0)
+                        *reinterpret_cast<uint4*>(pool + static_cast<int64_t>(t) * p.row_bytes + v * 16) =
+                            *reinterpret_cast<const uint4*>(ring + (((done % S) * RUN + row) * VS + v) * 16);
                 }
             }
         }
@@ -627,18 +640,26 @@ extern "C" int pa_cache_evict(void* k_cache, void* v_cache, const int32_t* block
     cfg.attrs = attr;
     cfg.numAttrs = C > 1 ? 1 : 0;
     void* args[1] = {&p};
-    // In place, about 96 KB of rows in flight per CTA: slices of 128 bytes, or of
-    // 64 where those would leave SMs idle (on the 64 ragged sequences 64-byte
-    // slices took 44.9 us against 33.5).
+    // In place, six runs of 16 KB in flight per CTA; slices of 128 bytes, or of 64
+    // or 32 (with two or four times the rows in a run) where wider ones would leave
+    // SMs idle.  Calls with 128-, 64- and 32-byte slices: one sequence, 8192 rows
+    // of 2 KB 73.9 / 47.2 / 39.0 us; one, 19569 of 512 bytes 153.8 / 88.2 / 69.6;
+    // four, 4096 of 2 KB 46.1 / 39.4 / 64.4; sixteen, 2048 of 2 KB 58.0 / 63.9 /
+    // 108.6; the 64 ragged ones 36.1 / 39.7 / 58.3.  (16-byte slices: 63.6 and
+    // 69.8 on the first two.)
     const void* move;
     size_t smem;
     dim3 grid;
     if (p.in_place) {
-        const bool narrow = 2ll * B * ((rb + 127) / 128) < 152;
-        p.slices = narrow ? (rb + 63) / 64 : (rb + 127) / 128;
+        int vs = 8;
+        while (vs > 2 && 2ll * B * ((rb + 16 * vs - 1) / (16 * vs)) < 152)
+            vs /= 2;
+        p.slices = (rb + 16 * vs - 1) / (16 * vs);
         grid = dim3(2u * p.slices, static_cast<unsigned>(B));
-        move = narrow ? reinterpret_cast<const void*>(pa_evict_shift<4, 12>) : reinterpret_cast<const void*>(pa_evict_shift<8, 6>);
-        smem = narrow ? 12 * kRun * 64 : 6 * kRun * 128;
+        move = vs == 8   ? reinterpret_cast<const void*>(pa_evict_shift<8, kRuns>)
+               : vs == 4 ? reinterpret_cast<const void*>(pa_evict_shift<4, kRuns>)
+                         : reinterpret_cast<const void*>(pa_evict_shift<2, kRuns>);
+        smem = kRuns * kRunBytes;
     } else {
         grid = dim3(2u * ((m + p.rows_item - 1) / p.rows_item), static_cast<unsigned>(B));
         move = reinterpret_cast<const void*>(pa_evict_gather);

@@ -142,6 +142,20 @@ def test_selects_and_moves(pa, fmt, lens, KV, D, BLOCK, budget, first, last, fre
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens,KV,D,BLOCK,budget,first,last", [
+    ([9000], 2, 128, 32, 7100, 0, 900),          # 32-byte slices, many runs of 512 rows
+    ([4000, 3900], 8, 128, 16, 3000, 5, 0),      # 64-byte ones or narrower
+    ([5000] * 10, 8, 128, 16, 1030, 16, 1),      # 128-byte ones
+    ([2500], 1, 8, 5, 2499, 0, 0),               # rows of one vector, nearly all kept
+    ([6000], 3, 8, 16, 1024, 3, 1021),           # three vectors: a slice that ends early
+])
+def test_moves_in_place_by_slices_of_every_width(pa, lens, KV, D, BLOCK, budget, first, last):
+    kc, vc, table, _, ln, w, _ = make(budget, "f16", lens, KV, D, BLOCK)
+    want = expect(kc, vc, table, lens, w, budget, first, last, None)
+    same(run(pa, kc, vc, table, None, ln, w, budget, first, last), want)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["zeros", "equal", "few", "infs", "nans", "signed", "close"])
 @pytest.mark.parametrize("n", [200, 3000, 9000, 40000])
 def test_ties_and_odd_weights(pa, n, kind):
