@@ -70,6 +70,7 @@ struct EvictParams {
     int row_bytes;           // KV * D * element bytes
     int rows_item;           // other blocks: rows per item
     int slices;              // in place: column slices of a row
+    int shift;               // log2 of BLOCK, or -1
 };
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -356,11 +357,15 @@ __global__ void __launch_bounds__(T) pa_evict_select(const __grid_constant__ Evi
         cluster_sync();  // the others have read this CTA's shared memory
 }
 
+// A token's block.  (The move looks up four a row, on its way to every copy: with
+// shifts in place of divisions a call of 19569 rows takes 55 us instead of 70.)
+__device__ __forceinline__ int block_of(const EvictParams& p, int j) { return p.shift >= 0 ? j >> p.shift : j / p.BLOCK; }
+
 // Slot of token j by a table row, or -1 (reported) when its block is outside the pool.
 __device__ __forceinline__ int slot_of(const EvictParams& p, int phys, int j, bool report)
 {
     if (phys >= 0 && phys < p.num_blocks)
-        return phys * p.BLOCK + j % p.BLOCK;
+        return phys * p.BLOCK + (j - block_of(p, j) * p.BLOCK);
     if (report && p.status)
         atomicOr(p.status, PA_STATUS_BAD_BLOCK);
     return -1;
@@ -404,8 +409,8 @@ __global__ void __launch_bounds__(kMoveThreads) pa_evict_shift(const __grid_cons
         for (int k = 0; k < LOOK; ++k) {
             j2[k] = j1[k];
             if (j2[k] >= 0) {
-                ps[k] = __ldg(table + j2[k] / p.BLOCK);
-                pd[k] = __ldg(table + (run * RUN + tid + k * kMoveThreads) / p.BLOCK);
+                ps[k] = __ldg(table + block_of(p, j2[k]));
+                pd[k] = __ldg(table + block_of(p, run * RUN + tid + k * kMoveThreads));
             }
         }
     };
@@ -489,8 +494,8 @@ __global__ void __launch_bounds__(kMoveThreads) pa_evict_gather(const __grid_con
     const int32_t* to = p.dst + static_cast<int64_t>(b) * p.dst_maxb;
     for (int i = tid; i < nr; i += kMoveThreads) {
         const int r = r0 + i;
-        const int pd = __ldg(to + r / p.BLOCK), j = kept[r];
-        const int s = slot_of(p, __ldg(table + j / p.BLOCK), j, kv == 0), d = slot_of(p, pd, r, kv == 0);
+        const int pd = __ldg(to + block_of(p, r)), j = kept[r];
+        const int s = slot_of(p, __ldg(table + block_of(p, j)), j, kv == 0), d = slot_of(p, pd, r, kv == 0);
         src[i] = d < 0 ? -1 : s;
         dst[i] = s < 0 ? -1 : d;
     }
@@ -615,6 +620,10 @@ extern "C" int pa_cache_evict(void* k_cache, void* v_cache, const int32_t* block
     p.cap = cap;
     p.row_bytes = rb;
     p.rows_item = rows_per_item(rb);
+    p.shift = -1;
+    for (int e = 0; e < 30; ++e)
+        if (1 << e == BLOCK)
+            p.shift = e;
 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // short sequences: a CTA of 256 threads holds 2048 weights in registers;
@@ -642,8 +651,9 @@ extern "C" int pa_cache_evict(void* k_cache, void* v_cache, const int32_t* block
     void* args[1] = {&p};
     // In place, six runs of 16 KB in flight per CTA; slices of 128 bytes, or of 64
     // or 32 (with two or four times the rows in a run) where wider ones would leave
-    // SMs idle.  Calls with 128-, 64- and 32-byte slices: one sequence, 8192 rows
-    // of 2 KB 73.9 / 47.2 / 39.0 us; one, 19569 of 512 bytes 153.8 / 88.2 / 69.6;
+    // SMs idle.  Calls with 128-, 64- and 32-byte slices (blocks found by division,
+    // which costs up to a fifth): one sequence, 8192 rows of 2 KB 73.9 / 47.2 /
+    // 39.0 us; one, 19569 of 512 bytes 153.8 / 88.2 / 69.6;
     // four, 4096 of 2 KB 46.1 / 39.4 / 64.4; sixteen, 2048 of 2 KB 58.0 / 63.9 /
     // 108.6; the 64 ragged ones 36.1 / 39.7 / 58.3.  (16-byte slices: 63.6 and
     // 69.8 on the first two.)
