@@ -148,7 +148,7 @@ SplitFn pick_split_f32(int D, int RG);
 SplitFn pick_split_f16(bool f32_out, int D, int MT);
 SplitFn pick_split_bf16(bool f32_out, int D, int MT);
 // The same kernels with modified scores (pa_scored_*.cu).
-ScoredFn pick_scored_f32(int D, int RG);
+ScoredFn pick_scored_f32(int D);
 ScoredFn pick_scored_f16(bool f32_out, int D, int MT);
 ScoredFn pick_scored_bf16(bool f32_out, int D, int MT);
 // The weight each key got (pa_scored.cu): after the partition kernel, on its stream.

@@ -573,9 +573,12 @@ static int decode_impl(const void* q, const void* k_cache, const void* v_cache,
 
     const int R = (H / KV) * NQ;
     const bool mma = dtype != PA_F32;
-    const int RG = rows_group(R);
+    // modified scores: 32 rows a pass also above 32 (eight rows a warp and their
+    // modifications spill: 8 sequences of 1000, 64 rows a KV head, D = 64, took 134 us,
+    // 57 in two passes; as many segments and bytes of workspace as 16-bit caches take)
+    const int RG = score ? 4 : rows_group(R);
     const int MT = mma_tiles(R);
-    const int rows_per_cta = rows_per_pass(dtype, R);
+    const int rows_per_cta = score && !mma ? kConsumerWarps * RG : rows_per_pass(dtype, R);
     const int NRS = (R + rows_per_cta - 1) / rows_per_cta;
     const int partitions = opts->partitions;
     const int row_stride = R < rows_per_cta ? R : rows_per_cta;
@@ -682,7 +685,7 @@ static int decode_impl(const void* q, const void* k_cache, const void* v_cache,
         return rc;
 
     const bool f32_out = out_dtype == PA_F32 && dtype != PA_F32;
-    const void* split = score ? (dtype == PA_F32   ? reinterpret_cast<const void*>(pick_scored_f32(D, RG))
+    const void* split = score ? (dtype == PA_F32   ? reinterpret_cast<const void*>(pick_scored_f32(D))
                                  : dtype == PA_F16 ? reinterpret_cast<const void*>(pick_scored_f16(f32_out, D, MT))
                                                    : reinterpret_cast<const void*>(pick_scored_bf16(f32_out, D, MT)))
                         : tc32 ? reinterpret_cast<const void*>(pick_split_tc(dtype, f32_out))

@@ -2732,11 +2732,9 @@ SplitFn pick_split_mma(int D, int MT)
 }
 
 template <typename T, typename TO>
-ScoredFn pick_scored_simt(int D, int RG)
+ScoredFn pick_scored_simt(int D)
 {
-    if (D == 64)
-        return RG == 4 ? pa_split_kernel<T, 64, 4, TO, true> : pa_split_kernel<T, 64, 8, TO, true>;
-    return RG == 4 ? pa_split_kernel<T, 128, 4, TO, true> : pa_split_kernel<T, 128, 8, TO, true>;
+    return D == 64 ? pa_split_kernel<T, 64, 4, TO, true> : pa_split_kernel<T, 128, 4, TO, true>;
 }
 
 template <typename T, typename TO>

@@ -3,6 +3,6 @@
 
 namespace pa {
 
-ScoredFn pick_scored_f32(int D, int RG) { return pick_scored_simt<float, float>(D, RG); }
+ScoredFn pick_scored_f32(int D) { return pick_scored_simt<float, float>(D); }
 
 }  // namespace pa

@@ -239,6 +239,15 @@ def test_many_rows(pa, H, KV, NQ, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,H,KV,NQ", [(64, 12, 3, 16), (128, 10, 2, 7), (64, 5, 1, 13), (128, 3, 1, 11), (64, 9, 1, 16)])
+def test_many_rows_of_float32(pa, D, H, KV, NQ):
+    # 64, 35, 65, 33 and 144 rows a KV head: passes of 32
+    x, _ = make(H + NQ, "f32", [300, 0, 97, 1200], H, KV, D, 16, NQ)
+    for mod in (dict(softcap=20.0), dict(slopes=True, window=150, prefix=40), dict(softcap=5.0, slopes=True)):
+        compare(pa, x, modified(mod, 4, H, 1 / math.sqrt(D), "f32", True))
+
+
+@pytest.mark.gpu
 def test_infinities_and_nans_in_hidden_keys_of_many_rows(pa):
     x, _ = make(14, "bf16", [700, 300], 16, 2, 128, 16, 4)
     kw = modified(dict(window=150, prefix=33), 2, 16, 0.09, "bf16", True)
