@@ -67,7 +67,7 @@
 //     117 -> 104 us with the join and the rounding in one launch).
 // [4, 32/8, 2048, 128] bf16 causal with a cap: 562 us, of it statistics 128,
 // backward 405 (without a cap 94 and 385).  Bound by the softmax warps' own
-// instructions (issue slots 55% and 46% busy) and, in the backward, by the dq
+// instructions (issue slots 60% and 43% busy) and, in the backward, by the dq
 // reductions into L2 (1.1 GB a call, as without a cap).
 //
 // Every wait is bounded (p.wait_ns); a wait that gives up ORs
