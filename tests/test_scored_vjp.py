@@ -333,3 +333,43 @@ def test_refused_arguments(pa):
             pa.attention_vjp_scored(q, k, v, q, g, scale=0.1, **bad)
     with pytest.raises(pa.PagedAttentionError):
         pa.attention_vjp_scored(q, k, v, q, g, scale=0.1, window=-1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("HK", [1, 4])
+@pytest.mark.parametrize("SQ,SK", [(0, 130), (130, 0), (0, 0)])
+def test_no_rows_or_no_keys(pa, SQ, SK, HK):
+    # native outputs: the launch that rounds dq and joins the groups comes behind
+    # the statistics alone, the backward alone, or nothing
+    q, k, v, g = (t.cuda() for t in make(90, "bf16", 2, 4, HK, SQ, SK, 128))
+    out = tuple(torch.full(t.shape, 3.0, dtype=torch.bfloat16, device="cuda") for t in (q, k, k))
+    pa.attention_vjp_scored(q, k, v, q, g, scale=0.1, softcap=20.0, window=40, out=out)
+    torch.cuda.synchronize()
+    assert all(not t.any() for t in out)
+
+
+@pytest.mark.gpu
+def test_calls_back_to_back_on_other_inputs(pa):
+    # launches that overlap their predecessor's end: calls of two shapes in turn, one
+    # of them split by heads, and one plan whose inputs change between its calls
+    kw = dict(scale=0.09, causal=True, softcap=30.0)
+    sets = [[t.cuda() for t in make(100 + i, "bf16", 2, 8, 2, s, s, 128)] for i, s in enumerate((900, 900, 300))]
+    plans = [pa.ScoredVjpPlan(q, k, v, q, g, **kw) for q, k, v, g in (sets[0], sets[2])]
+    want = []
+    for q, k, v, g in sets:
+        want.append([t.clone() for t in pa.attention_vjp_scored(q, k, v, q, g, **kw)])
+    torch.cuda.synchronize()
+    live = [t.clone() for t in sets[0]]
+    moving = pa.ScoredVjpPlan(live[0], live[1], live[2], live[0], live[3], **kw)
+    got = []
+    for n in range(12):
+        for a, b in zip(live, sets[n % 2]):
+            a.copy_(b)
+        for plan in (moving, *plans):
+            got.append((n, [t.clone() for t in plan.run()]))
+    torch.cuda.synchronize()
+    for i, (n, g) in enumerate(got):
+        w = want[(n % 2, 0, 2)[i % 3]]
+        assert torch.equal(g[1], w[1]) and torch.equal(g[2], w[2]), i
+        # dq: sums in another order, then one rounding to bfloat16
+        assert torch.allclose(g[0].float(), w[0].float(), rtol=2.0 ** -7, atol=1e-5), i
