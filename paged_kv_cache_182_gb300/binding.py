@@ -287,15 +287,27 @@ def _call(fn, args, device, stream):
         raise PagedAttentionError(rc)
 
 
+def _order(stream, device, *made):
+    """Orders a call on ``stream`` behind torch's current stream, where the call's
+    own tensors ``made`` are allocated, zero-filled or converted (their memory may
+    still be in use there); they stay allocated until ``stream`` has passed what
+    it holds by the time they are freed."""
+    if stream is None:
+        return
+    current = torch.cuda.current_stream(device)
+    if stream == current:
+        return
+    stream.wait_stream(current)
+    for t in made:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _run_once(plan, stream, *made):
-    """``plan.run(stream)`` of a plan that is dropped right after: the tensors it
-    made itself stay allocated until ``stream`` has passed the call."""
-    result = plan.run(stream)
-    if stream is not None:
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
-    return result
+    """``plan.run(stream)`` of a plan that was made for this call and is dropped
+    right after; ``made``: the tensors that it allocated."""
+    _order(stream, plan.device, *made)
+    return plan.run(stream)
 
 
 class Plan:
@@ -303,7 +315,10 @@ class Plan:
 
     Validates shapes once and packs the ctypes arguments, so that repeated
     calls (a decode loop, CUDA-graph capture, the bench) cost one foreign
-    call.  The workspace is allocated once, here, with torch.
+    call.  The workspace is allocated once, here, with torch, and zero-filled
+    on torch's current stream: a first ``run`` on another stream has to be
+    ordered behind that (``stream.wait_stream``).  The one-call functions do it
+    themselves.  The same holds for the other plans of this module.
     """
 
     def __init__(self, q, k_cache, v_cache, block_table, seq_lens, k_new, v_new, *,
@@ -402,7 +417,7 @@ def decode(q, k_cache, v_cache, block_table, seq_lens, k_new, v_new, *, scale: f
                 causal=causal, partitions=partitions, out=out, out_dtype=out_dtype,
                 workspace=workspace, status=status, checked=checked, merge_kernel=merge_kernel,
                 kernel=kernel)
-    return plan.run(stream)
+    return _run_once(plan, stream, plan.out, plan.workspace)
 
 
 def decode_positions(q, k_cache, v_cache, block_table, seq_lens, k_new, v_new, positions, *,
@@ -425,6 +440,7 @@ def decode_positions(q, k_cache, v_cache, block_table, seq_lens, k_new, v_new, p
     if not (positions.is_cuda and positions.is_contiguous()):
         raise ValueError("positions must be a contiguous CUDA tensor")
     args = plan._args[:7] + [_ptr(positions)] + plan._args[7:]
+    _order(stream, plan.device, plan.out, plan.workspace)
     with torch.cuda.device(plan.device):
         rc = LIB.pa_decode_positions(*args, _stream_handle(stream))
     if rc != 0:
@@ -494,9 +510,10 @@ def prefill(q, k_cache, v_cache, block_table, seq_lens, k_new, v_new, *, scale: 
     new rows are stored in ``k_cache`` / ``v_cache`` at the slots the block
     table gives their tokens (the table must hold blocks for them).  q
     [B, H, NQ, D], new rows [B, KV, NQ, D]; returns ``out``."""
-    return PrefillPlan(q, k_cache, v_cache, block_table, seq_lens, k_new, v_new, scale=scale,
+    plan = PrefillPlan(q, k_cache, v_cache, block_table, seq_lens, k_new, v_new, scale=scale,
                        partitions=partitions, out=out, out_dtype=out_dtype, status=status,
-                       checked=checked).run(stream)
+                       checked=checked)
+    return _run_once(plan, stream, plan.out, plan.workspace)
 
 
 class HostPlan:
@@ -635,6 +652,7 @@ def decode_host(q, block_table, seq_lens, k_new, v_new, *, k_cache, v_cache, sca
                         scale=scale, causal=causal, partitions=partitions, out_dtype=out_dtype)
         _host_plans.clear()  # one plan at a time: it owns a device workspace
         _host_plans[key] = plan
+        _order(stream, k_cache.device)  # the workspace is zero-filled on the current stream
     if stream is None:
         stream = torch.cuda.current_stream(k_cache.device)
     out = torch.empty(q.shape, dtype=odt, pin_memory=True)
@@ -739,7 +757,8 @@ class VjpPlan:
         o.kernel = int(kernel)
         o.wait_limit_ns = int(wait_limit_ns)
         self.opts = o
-        self._keep = (q, k, v, y, g, mask, status)
+        self.mask = mask  # as the kernels read it: a boolean mask is converted here
+        self._keep = (q, k, v, y, g, status)
         self.device = dev
         self._args = (_ptr(q), _ptr(k), _ptr(v), _ptr(y), _ptr(g), _ptr(mask), _ptr(self.dq),
                       _ptr(self.dk), _ptr(self.dv), ctypes.c_float(scale), B, HQ, HK, SQ, SK, D,
@@ -762,8 +781,9 @@ class VjpPlan:
 def attention_vjp(q, k, v, y, g, mask=None, *, scale: float, causal: bool = False,
                   out_dtype=None, kernel: int = 0, status=None, stream=None, out=None):
     """dq, dk, dv of attention (pa_attention_vjp): see ``VjpPlan``."""
-    return VjpPlan(q, k, v, y, g, mask, scale=scale, causal=causal, out_dtype=out_dtype,
-                   kernel=kernel, status=status, out=out).run(stream)
+    plan = VjpPlan(q, k, v, y, g, mask, scale=scale, causal=causal, out_dtype=out_dtype,
+                   kernel=kernel, status=status, out=out)
+    return _run_once(plan, stream, plan.workspace, plan.dq, plan.dk, plan.dv, plan.mask)
 
 
 # ------------------------------------------------------------------- modified scores
@@ -884,7 +904,7 @@ def attention_vjp_scored(q, k, v, y, g, mask=None, *, scale: float, causal: bool
     plan = ScoredVjpPlan(q, k, v, y, g, mask, scale=scale, causal=causal, softcap=softcap,
                          slopes=slopes, window=window, prefix=prefix, out_dtype=out_dtype,
                          kernel=kernel, status=status, out=out)
-    return _run_once(plan, stream, plan.workspace, plan.dq, plan.dk, plan.dv)
+    return _run_once(plan, stream, plan.workspace, plan.dq, plan.dk, plan.dv, plan.mask)
 
 
 # ------------------------------------------------------------------- rotary positions
