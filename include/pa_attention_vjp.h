@@ -38,7 +38,8 @@
  * The call only enqueues work on `stream` (a cudaStream_t, NULL = legacy
  * default stream) and returns; results are ready when the stream reaches
  * that point.  dq, dk and dv are fully overwritten (rows with no visible key
- * get dq = 0; keys no row sees get dk = dv = 0).
+ * get dq = 0; keys no row sees get dk = dv = 0, and their v may hold anything:
+ * everything else must be finite).
  *
  * Returns PA_OK or a PA_ERR_* code of pa_decode.h, checked before any launch:
  *   PA_ERR_NULL_POINTER  a tensor, opts, the mask (mask_kind != 0) or a needed

@@ -97,7 +97,8 @@ size_t pa_scored_scratch_bytes(int batch, int max_blocks, int BLOCK, int H, int 
  *   ds = p * (dp - delta) * (1 - tanh^2(scale q.k / softcap))   under a cap.
  *
  * A mask of opts (mask_kind != 0) adds its bias to the modified score and
- * hides what it hides, prefix or not.  Rows that see no key get dq = 0.
+ * hides what it hides, prefix or not.  Rows that see no key get dq = 0.  The v
+of a key that no row sees may hold anything; q, k, y and g must be finite.
  * 16-bit inputs with D = 128 and no mask run on the tensor cores; tiles
  * outside prefix and window are skipped.  opts->workspace holds
  * pa_attention_vjp_scored_workspace_bytes() for the current device (partial dk

@@ -83,7 +83,8 @@ __device__ __forceinline__ float warp_sum(float x)
 }
 
 // Score (i, j) in base-2 units of a dot product (already times `cap_in` under a
-// cap, else times scale_log2), and the cap's factor on its gradient.
+// cap, else times scale_log2), and the cap's factor on its gradient.  -inf for a
+// hidden pair whatever its dot product (which may not be finite).
 template <bool kMod>
 __device__ __forceinline__ float simt_score(const VjpParamsOf<kMod>& p, float x, int b, int h, int i, int j, int pl,
                                             float* slope)
@@ -98,9 +99,11 @@ __device__ __forceinline__ float simt_score(const VjpParamsOf<kMod>& p, float x,
             x = p.cap_out * th;
         }
         const float far = p.slopes ? __ldg(p.slopes + h) * static_cast<float>(abs(i - j)) : 0.f;
-        return x + (vjp_bias(p, b, h, i, j, false) - far) * kVjpLog2e;
+        const float bias = vjp_bias(p, b, h, i, j, false);
+        return bias == -INFINITY ? bias : x + (bias - far) * kVjpLog2e;
     } else {
-        return x + vjp_bias(p, b, h, i, j, p.causal) * kVjpLog2e;
+        const float bias = vjp_bias(p, b, h, i, j, p.causal);
+        return bias == -INFINITY ? bias : x + bias * kVjpLog2e;
     }
 }
 
@@ -258,7 +261,8 @@ __global__ void __launch_bounds__(256) vjp_main_simt(VjpParamsOf<kMod> p)
                     float slope;
                     const float s2 = simt_score<kMod>(p, s * factor, b, h, i, key, pl, &slope);
                     pv = exp2f(s2 - rl[pr]);
-                    dsv = pv * (dp - rd[pr]) * p.scale * slope;
+                    // a hidden pair's dp may not be finite: 0 times it is no 0
+                    dsv = s2 == -INFINITY ? 0.f : pv * (dp - rd[pr]) * p.scale * slope;
                 }
                 Ps[pj * 17 + pr] = pv;
                 Ss[pj * 17 + pr] = dsv;

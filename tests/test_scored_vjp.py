@@ -373,3 +373,54 @@ def test_calls_back_to_back_on_other_inputs(pa):
         assert torch.equal(g[1], w[1]) and torch.equal(g[2], w[2]), i
         # dq: sums in another order, then one rounding to bfloat16
         assert torch.allclose(g[0].float(), w[0].float(), rtol=2.0 ** -7, atol=1e-5), i
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,D,kernel", [("f32", 64, 0), ("f16", 64, 0), ("bf16", 128, 1), ("bf16", 128, 0), ("f16", 128, 0)])
+def test_values_of_hidden_keys_may_be_anything(pa, fmt, D, kernel):
+    # v of keys that no row sees holds infinities and NaN; both kernels give the gradient of finite ones
+    B, HQ, HK, SQ, SK = 1, 4, 2, 90, 300
+    q, k, v, g = make(120, fmt, B, HQ, HK, SQ, SK, D)
+    tc = D == 128 and kernel == 0
+    for kw, first in ((modified(dict(window=20), B, HQ, False, D), SQ + 19), (modified(dict(softcap=9.0, slopes=True), B, HQ, True, D), SQ)):
+        dead = torch.arange(SK) >= first
+        bad = v.clone()
+        bad[:, :, first::3], bad[:, :, first + 1::3], bad[:, :, first + 2::3] = math.nan, math.inf, -math.inf
+        f = [t.double().numpy() for t in (q, k, v, g)]
+        y = torch.from_numpy(forward(*f[:3], kw)).to(q.dtype)
+        want, err = gradient(*f[:3], y.double().numpy(), f[3], kw, U[fmt] if tc else 0.0, 2.0 ** -25 if tc and fmt == "f16" else 0.0)
+        dev = {n: (t.cuda() if isinstance(t, torch.Tensor) else t) for n, t in kw.items()}
+        got = pa.attention_vjp_scored(*(t.cuda() for t in (q, k, bad, y, g)), **dev, out_dtype=torch.float32, kernel=kernel)
+        torch.cuda.synchronize()
+        for name, a, w, e in zip(("dq", "dk", "dv"), got, want, err):
+            o = a.double().cpu().numpy()
+            assert np.all(np.abs(o - w) <= e + 2.0 ** -24 * (np.abs(w) + e) + 2.0 ** -140), name
+        assert not got[1][:, :, dead].any() and not got[2][:, :, dead].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kernel", [0, 1])
+@pytest.mark.parametrize("kind", ["causal", "bool", "add"])
+def test_values_hidden_from_the_plain_gradient_may_be_anything(pa, kind, kernel):
+    # the same of pa_attention_vjp: the causal rule, and masks (which run on the CUDA cores)
+    q, k, v, g = (t.cuda() for t in make(121, "f32" if kind != "causal" else "f16", 1, 4, 2, 60, 130, 128))
+    hidden, mask = torch.arange(130) >= 60, None
+    if kind != "causal":
+        mask = (~hidden).to(torch.uint8).view(1, 1, 1, 130).expand(1, 1, 60, 130).contiguous()
+        if kind == "add":
+            mask = torch.where(mask != 0, 0.0, -math.inf).float()
+        mask = mask.cuda()
+    y, bad = q.clone(), v.clone()
+    bad[:, :, 60::2], bad[:, :, 61::2] = math.nan, math.inf
+    call = lambda x: pa.attention_vjp(q, k, x, y, g, mask, scale=0.09, causal=kind == "causal", kernel=kernel,  # noqa: E731
+                                      out_dtype=torch.float32)
+    want, got = call(v), call(bad)
+    assert all(torch.isfinite(t).all() for t in got)
+    assert torch.equal(want[1], got[1]) and torch.equal(want[2], got[2])
+    # dq: the 60 visible keys are four tiles of 16 (CUDA cores) whose parts are added in any order: each
+    # order is off by at most 3 roundings of the sum of the parts' magnitudes, which is at most |ds| |k|
+    Q, K, V, G = (t.double().repeat_interleave(4 // t.shape[1], 1) for t in (q, k, v, g))
+    seen = ~hidden.cuda() & ((torch.arange(130) <= torch.arange(60)[:, None]).cuda() | (kind != "causal"))
+    p = torch.softmax((0.09 * Q @ K.mT).masked_fill(~seen, -math.inf), -1)
+    ds = 0.09 * p * (G @ V.mT - (Q * G).sum(-1, keepdim=True))
+    assert torch.all((want[0] - got[0]).abs() <= 2 * 3 * 2.0 ** -24 * 1.01 * (ds.abs() @ K.abs()))
