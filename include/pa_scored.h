@@ -38,9 +38,10 @@
  * PA_ERR_UNSUPPORTED; opts->partitions must be 0 or 1 and opts->merge_kernel 0
  * (PA_ERR_UNSUPPORTED); opts->inputs_unchanged and opts->kernel are ignored.
  * slopes [H] float32 and prefix [B] int32 are device pointers or NULL (a
- * negative prefix counts as 0).  PA_ERR_BAD_DIMS: a softcap that is negative
- * or not finite or so small that scale / softcap is not, a negative window, a
- * decay that is not finite, weights in and out that overlap without being one
+ * negative prefix counts as 0).  PA_ERR_BAD_DIMS: a softcap that is negative,
+ * not finite, or so small or so large that |scale| / softcap is outside 2^-100
+ * .. 2^100 (scale not 0) or softcap * log2(e) overflows -- a cap that is to
+ * change nothing is 0 --, a negative window, a decay that is not finite, weights in and out that overlap without being one
  * array, scores whose scratch passes 2^40 bytes.  PA_ERR_NULL_POINTER: weights without out.
  * PA_ERR_WORKSPACE / PA_ERR_ALIGNMENT: scratch below
  * pa_scored_scratch_bytes() or not 256-byte aligned.  Two calls that run at

@@ -805,7 +805,8 @@ class ScoredPlan(Plan):
     """One prepared decode call with modified scores (pa_decode_scored): as
     ``Plan``, with
 
-      softcap   scores t -> softcap * tanh(t / softcap) (0: none)
+      softcap   scores t -> softcap * tanh(t / softcap) (0: none; else
+                2^-100 <= |scale| / softcap <= 2^100)
       slopes    float32 [H]: slopes[h] * |row - key| subtracted (None: none)
       window    keys within ``window`` positions of the row only (0: all)
       prefix    int32 [B]: the first prefix[b] keys are visible to every row

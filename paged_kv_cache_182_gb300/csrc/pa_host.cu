@@ -894,10 +894,7 @@ int pa_decode_scored(const void* q, const void* k_cache, const void* v_cache, co
 {
     if (!score || !opts)
         return PA_ERR_NULL_POINTER;
-    if (!(score->softcap >= 0.f) || !std::isfinite(score->softcap) || score->window < 0 ||
-        (weights && !std::isfinite(weights->decay)))
-        return PA_ERR_BAD_DIMS;
-    if (score->softcap > 0.f && !std::isfinite(scale / score->softcap))
+    if (!softcap_ok(score->softcap, scale) || score->window < 0 || (weights && !std::isfinite(weights->decay)))
         return PA_ERR_BAD_DIMS;
     if ((opts->partitions != 0 && opts->partitions != 1) || opts->merge_kernel)
         return PA_ERR_UNSUPPORTED;

@@ -3,9 +3,25 @@
 
 #include <cuda_runtime.h>
 
+#include <cmath>
+
 #include "pa_ptx.cuh"
 
 namespace pa {
+
+// Whether scores scale * dot can be computed under this cap (0: none) as
+// cap * tanh(dot * (scale / cap)) in float32: both factors are normal numbers far
+// from either end of the range (a cap of 1e37 has a scale / cap that has lost
+// bits, one of 2.4e38 no finite cap * log2(e)).
+inline bool softcap_ok(float cap, float scale)
+{
+    if (cap == 0.f)
+        return true;
+    if (!(cap > 0.f) || !std::isfinite(cap * 1.4426950408889634f))
+        return false;
+    const float f = std::fabs(scale / cap);
+    return scale == 0.f || (f >= 0x1p-100f && f <= 0x1p100f);
+}
 
 // tanh of N scores (times 1 / cap), N even: an odd polynomial of degree 11
 // where every score of the warp is within 0.7 -- fitted here for the least

@@ -574,8 +574,7 @@ extern "C" int pa_attention_vjp_scored(const void* q, const void* k, const void*
 {
     if (!score)
         return PA_ERR_NULL_POINTER;
-    if (!(score->softcap >= 0.f) || !std::isfinite(score->softcap) || score->window < 0 ||
-        (score->softcap > 0.f && !std::isfinite(scale / score->softcap)))
+    if (!softcap_ok(score->softcap, scale) || score->window < 0)
         return PA_ERR_BAD_DIMS;
     if ((reinterpret_cast<uintptr_t>(score->slopes) & 3) || (reinterpret_cast<uintptr_t>(score->prefix) & 3))
         return PA_ERR_ALIGNMENT;

@@ -400,3 +400,26 @@ def test_refused_arguments(pa):
             pa.decode_scored(*x, scale=0.1, **bad)
     with pytest.raises(pa.PagedAttentionError):
         pa.decode_scored(*x, scale=0.1, softcap=-2.0)
+
+
+# ------------------------------------------------------------------ caps at the ends of float32's range
+# scale / softcap subnormal, softcap * log2(e) infinite, scale / softcap near the ends, each with a scale that leaves the other fine
+@pytest.mark.parametrize("softcap,scale", [(3e38, 0.125), (2.4e38, 1e10), (1e37, 0.125), (2e31, 0.125), (-3e38, 0.125), (1e-32, 0.125),
+                                           (3e-38, -0.125), (1e-45, 0.125), (1.0, 1e-31)])
+def test_refused_caps(pa, softcap, scale):
+    assert call(pa, softcap=softcap, scale=scale) == DIMS and call(pa, softcap=softcap, scale=scale, weights={}) == DIMS
+    assert call(pa, B=0, softcap=softcap, scale=scale) == DIMS
+
+
+@pytest.mark.parametrize("softcap,scale", [(1e29, 0.125), (2.3e38, 1e10), (1e-30, 0.125), (50.0, 0.0), (50.0, -0.125), (0.0, 1e-31)])
+def test_accepted_caps(pa, softcap, scale):
+    assert call(pa, B=0, softcap=softcap, scale=scale) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["f16", "f32"])
+@pytest.mark.parametrize("cap", [1e6, 1e20, 1e29])
+def test_caps_that_change_nothing(pa, fmt, cap):
+    x, _ = make(32, fmt, [300, 41], 8, 2, 64, 16, 2)
+    for mod in (dict(softcap=cap), dict(softcap=cap, slopes=True, window=90)):
+        compare(pa, x, modified(mod, 2, 8, 0.125, fmt, True))

@@ -424,3 +424,17 @@ def test_values_hidden_from_the_plain_gradient_may_be_anything(pa, kind, kernel)
     p = torch.softmax((0.09 * Q @ K.mT).masked_fill(~seen, -math.inf), -1)
     ds = 0.09 * p * (G @ V.mT - (Q * G).sum(-1, keepdim=True))
     assert torch.all((want[0] - got[0]).abs() <= 2 * 3 * 2.0 ** -24 * 1.01 * (ds.abs() @ K.abs()))
+
+
+@pytest.mark.parametrize("softcap,scale", [(3e38, 0.1), (2.4e38, 1e10), (1e37, 0.1), (2e31, 0.1), (1e-32, 0.1), (1e-45, 0.1), (1.0, 1e-31)])
+def test_refused_caps(pa, softcap, scale):
+    assert call(pa, softcap=softcap, scale=scale) == -2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,D", [("f16", 128), ("f32", 64)])
+@pytest.mark.parametrize("cap", [1e20, 1e29])
+def test_caps_that_change_nothing(pa, fmt, D, cap):
+    x = make(17, fmt, 1, 2, 1, 150, 200, D)
+    for mod in (dict(softcap=cap), dict(softcap=cap, slopes=True, window=90)):
+        compare(pa, x, modified(mod, 1, 2, False, D), fmt, torch.float32)
