@@ -261,6 +261,24 @@ def _ptr(t):
     return None if t is None or t.data_ptr() == 0 else ctypes.c_void_p(t.data_ptr())
 
 
+def _writable(device, **tensors):
+    """Refuses what kernels on ``device`` may not write: memory of another device,
+    or host memory that is not pinned."""
+    for name, t in tensors.items():
+        if t is not None and not (t.device == device if t.is_cuda else t.is_pinned()):
+            raise ValueError(f"{name} must be on the inputs' device")
+
+
+def _status_ptr(status, device):
+    """Address of the int32 status word of a call, or None."""
+    if status is None:
+        return None
+    _writable(device, status=status)
+    if status.dtype != torch.int32 or status.numel() < 1:
+        raise ValueError("status must be an int32 scalar")
+    return status.data_ptr()
+
+
 def _stream_handle(stream):
     # the raw handle of torch's current stream: building a Stream object costs
     # as much host time as the launch
@@ -352,6 +370,7 @@ class Plan:
             out = torch.empty((B, H, NQ, D), dtype=odt, device=q.device)
         elif tuple(out.shape) != (B, H, NQ, D) or not out.is_contiguous() or out.dtype != odt:
             raise ValueError("out must be a contiguous [B, H, NQ, D] tensor of the output dtype")
+        _writable(q.device, out=out, workspace=workspace)
         if workspace is None:
             workspace = new_workspace(B, H, KV, D, NQ, partitions, q.device)
         self.tensors = tensors
@@ -367,7 +386,7 @@ class Plan:
             out_dtype=_DT[odt], partitions=int(partitions), checked=int(bool(checked)),
             workspace=None if workspace is None else workspace.data_ptr(),
             workspace_bytes=0 if workspace is None else workspace.numel(),
-            status=None if status is None else status.data_ptr(),
+            status=_status_ptr(status, q.device),
             trace_begin=None if trace is None else trace[0].cuda_event,
             trace_split=None if trace is None else trace[1].cuda_event,
             merge_kernel=int(bool(merge_kernel)), inputs_unchanged=int(bool(inputs_unchanged)),
@@ -479,6 +498,7 @@ class PrefillPlan:
             out = torch.empty((B, H, NQ, D), dtype=odt, device=q.device)
         elif tuple(out.shape) != (B, H, NQ, D) or not out.is_contiguous() or out.dtype != odt:
             raise ValueError("out must be a contiguous [B, H, NQ, D] tensor of the output dtype")
+        _writable(q.device, out=out)
         need = int(LIB.pa_prefill_workspace_bytes(B, H, KV, D, NQ, int(partitions), _DT[dt],
                                                   _DT[odt]))
         if need == 0 and B > 0:
@@ -489,7 +509,7 @@ class PrefillPlan:
             batch=B, max_blocks=int(block_table.shape[1]), num_blocks=NB, dtype=_DT[dt],
             out_dtype=_DT[odt], partitions=int(partitions), checked=int(bool(checked)),
             workspace=self.workspace.data_ptr(), workspace_bytes=need,
-            status=None if status is None else status.data_ptr(), trace_begin=None,
+            status=_status_ptr(status, q.device), trace_begin=None,
             trace_split=None, merge_kernel=0)
         self._args = [_ptr(t) for t in tensors] + [_ptr(out), ctypes.c_float(scale), H, KV, D,
                                                    BLOCK, NQ, ctypes.byref(self.opts)]
@@ -683,7 +703,7 @@ def cache_append(k_cache, v_cache, k_new, v_new, slot_mapping, *, status=None, s
         if not (x.is_cuda and x.is_contiguous()):
             raise ValueError("all tensors must be contiguous CUDA tensors")
     args = (_ptr(k_cache), _ptr(v_cache), _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), B, KV, D,
-            NQ, BLOCK, NB, _DT[dt], _ptr(status))
+            NQ, BLOCK, NB, _DT[dt], _status_ptr(status, k_cache.device))
     if torch.cuda.current_device() == k_cache.device.index:
         rc = LIB.pa_cache_append(*args, _stream_handle(stream))
     else:
@@ -749,11 +769,12 @@ class VjpPlan:
         for t, ref in zip(out, (q, k, k)):
             if t.dtype != odt or tuple(t.shape) != tuple(ref.shape) or not t.is_contiguous():
                 raise ValueError("out: dq like q, dk and dv like k, of the output dtype")
+            _writable(dev, out=t)
         need = self._workspace_bytes(B, HQ, HK, SQ, SK, D, o.dtype, o.out_dtype, dev)
         self.workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
         o.workspace = _ptr(self.workspace)
         o.workspace_bytes = int(self.workspace.numel())
-        o.status = _ptr(status)
+        o.status = _status_ptr(status, dev)
         o.kernel = int(kernel)
         o.wait_limit_ns = int(wait_limit_ns)
         self.opts = o
@@ -1049,7 +1070,7 @@ class RotaryPlan:
             o.slot_mapping, o.v = slots.data_ptr(), v.data_ptr()
             o.k_cache, o.v_cache = caches[0].data_ptr(), caches[1].data_ptr()
             o.num_blocks, o.BLOCK = int(caches[0].shape[0]), int(caches[0].shape[1])
-            o.status = None if status is None else status.data_ptr()
+            o.status = _status_ptr(status, dev)
         self.opts, self.device = o, dev
         self._keep = (q, k, v, positions, table, slots, caches, status)
         self._args = _ready((_ptr(q), _ptr(k), _ptr(positions), _ptr(table.turns), _ptr(self.q_out),
@@ -1165,7 +1186,7 @@ class EvictPlan:
             keep_first=int(keep_first), keep_last=int(keep_last),
             dst_table=None if dst_table is None else dst_table.data_ptr(),
             dst_max_blocks=0 if dst_table is None else int(dst_table.shape[1]),
-            status=None if status is None else status.data_ptr())
+            status=_status_ptr(status, dev))
         self.device = dev
         self._keep = (tensors, dst_table, status)
         self._args = _ready((*(_ptr(t) for t in tensors), B, KV, D, BLOCK, ctypes.byref(self.opts)))
