@@ -1046,6 +1046,8 @@ class RotaryPlan:
             raise ValueError("positions must be contiguous")
         if table.rot > D:
             raise ValueError("the table turns more columns than a head has")
+        if table.turns.dtype != torch.int64 or table.turns.numel() != table.rot // 2 or not table.turns.is_contiguous():
+            raise ValueError("the table must hold rot / 2 int64 angles")
         for t in (*rows, positions, table.turns):
             if not t.is_cuda or t.device != dev:
                 raise ValueError("all tensors must be CUDA tensors on one device")

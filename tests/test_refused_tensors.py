@@ -1,5 +1,6 @@
 """Tensors that a plan must refuse before anything is launched: host memory
-where a kernel would write, status words of another type."""
+where a kernel would write, status words of another type, angles that are not
+the table's."""
 import pytest
 import torch
 
@@ -82,3 +83,15 @@ def test_outputs_and_workspaces_on_the_host(pa):
     q, k, v, g = (torch.randn(1, h, 20, 64).cuda() for h in (4, 2, 2, 4))
     with pytest.raises(ValueError, match="out"):
         pa.attention_vjp_scored(q, k, v, q, g, scale=0.1, out=(torch.zeros(q.shape), torch.zeros(k.shape), torch.zeros(k.shape)))
+
+
+@pytest.mark.gpu
+def test_tables_of_another_length(pa):
+    q, pos = torch.randn(1, 2, 3, 64, device="cuda"), torch.zeros(1, 3, dtype=torch.int32, device="cuda")
+    turns = pa.rotary_table(64).turns
+    for bad in (turns[:31], turns.int(), turns.repeat(2)[::2]):
+        with pytest.raises(ValueError, match="angles"):
+            pa.rotary(q, None, pos, pa.RotaryTable(bad, 1.0, 64))
+    got, _ = pa.rotary(q, None, pos, pa.RotaryTable(turns, 1.0, 64))
+    torch.cuda.synchronize()
+    assert torch.equal(got, q)  # position 0
