@@ -279,6 +279,13 @@ def _status_ptr(status, device):
     return status.data_ptr()
 
 
+def _int32(**values):
+    """Refuses sizes that the C ABI's int would take for others."""
+    for name, v in values.items():
+        if not -(2 ** 31) <= v < 2 ** 31:
+            raise ValueError(f"{name} is out of range")
+
+
 def _stream_handle(stream):
     # the raw handle of torch's current stream: building a Stream object costs
     # as much host time as the launch
@@ -810,6 +817,7 @@ def attention_vjp(q, k, v, y, g, mask=None, *, scale: float, causal: bool = Fals
 # ------------------------------------------------------------------- modified scores
 def _score(softcap, slopes, window, prefix, B, H, device):
     """The checked pa_score of a call (the tensors stay with the caller's plan)."""
+    _int32(window=int(window))
     if slopes is not None and (tuple(slopes.shape) != (H,) or slopes.dtype != torch.float32):
         raise ValueError("slopes must be a float32 [H] tensor")
     if prefix is not None and (tuple(prefix.shape) != (B,) or prefix.dtype != torch.int32):
@@ -1164,6 +1172,7 @@ class EvictPlan:
         budget = int(budget)
         if budget < 1:
             raise ValueError("budget must be at least 1")
+        _int32(budget=budget, keep_first=int(keep_first), keep_last=int(keep_last))
         dev = k_cache.device
 
         def output(t, shape, dtype, name):

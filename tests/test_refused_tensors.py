@@ -1,6 +1,8 @@
-"""Tensors that a plan must refuse before anything is launched: host memory
-where a kernel would write, status words of another type, angles that are not
-the table's."""
+"""Tensors and sizes that a plan must refuse before anything is launched:
+host memory where a kernel would write, status words of another type, angles
+that are not the table's, sizes that a C int would take for others."""
+import math
+
 import pytest
 import torch
 
@@ -29,6 +31,17 @@ def test_status_words(pa):
     assert pa._status_ptr(None, CUDA) is None
     with pytest.raises(ValueError, match="status"):
         pa._status_ptr(torch.zeros(1, dtype=torch.int32), CUDA)
+
+
+@pytest.mark.parametrize("window", [2 ** 31, 2 ** 32 + 5, -(2 ** 31) - 1])
+def test_windows_that_no_int_holds(pa, window):
+    with pytest.raises(ValueError, match="window"):
+        pa._score(0.0, None, window, None, 1, 1, CUDA)
+
+
+def test_every_other_window_is_passed_on(pa):
+    for window in (0, 5, 2 ** 31 - 1, -1):  # (a negative one is the library's to refuse)
+        assert pa._score(0.0, None, window, None, 1, 1, CUDA).window == window
 
 
 # ------------------------------------------------------------------ GPU
@@ -95,3 +108,13 @@ def test_tables_of_another_length(pa):
     got, _ = pa.rotary(q, None, pos, pa.RotaryTable(turns, 1.0, 64))
     torch.cuda.synchronize()
     assert torch.equal(got, q)  # position 0
+
+
+@pytest.mark.gpu
+def test_sizes_that_no_int_holds(pa):
+    x = paged()
+    with pytest.raises(ValueError, match="window"):
+        pa.decode_scored(*x, scale=1 / math.sqrt(64), window=2 ** 32 + 5)
+    for bad in (dict(keep_first=2 ** 32), dict(keep_last=2 ** 32 + 1)):
+        with pytest.raises(ValueError, match="keep"):
+            pa.cache_evict(*x[1:5], torch.rand(2, 48, device="cuda"), budget=12, **bad)
