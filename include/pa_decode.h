@@ -126,7 +126,9 @@ typedef struct pa_opts {
      * step of the same batch).  The partition kernel then reads them (the
      * lengths, the schedule, the table, the first stages of K and V) before
      * that kernel has completed; it still waits for it before writing out or
-     * the workspace.  0 (default): every input is read after it.  Ignored by
+     * the workspace.  Such a call may itself still be waiting when the next one
+     * starts: of several in a row, the guarantee of each covers the kernel ahead
+     * of the first of them too.  0 (default): every input is read after it.  Ignored by
      * pa_decode_positions, pa_decode_host and pa_prefill, which run their
      * own kernels just before the decode. */
     int inputs_unchanged;

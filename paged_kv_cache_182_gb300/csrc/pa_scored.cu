@@ -32,8 +32,10 @@ constexpr int kWThreads = 128;
 template <bool kVec, int L>
 __global__ void __launch_bounds__(kWThreads) pa_key_weights(const __grid_constant__ KeyWeightParams p)
 {
-    grid_dependents_launch();
+    // in this order: a kernel that is let off here may read its inputs before this one
+    // has ended (pa_opts.inputs_unchanged), and the partition kernel's out be among them
     grid_dependency_wait();
+    grid_dependents_launch();
     constexpr int W = kVec ? 4 : 1, U = 4, KEYS = kWThreads / L;
     const int b = blockIdx.y;
     const int n = min(max(__ldg(p.seq_lens + b), 0), p.cap);

@@ -423,3 +423,30 @@ def test_caps_that_change_nothing(pa, fmt, cap):
     x, _ = make(32, fmt, [300, 41], 8, 2, 64, 16, 2)
     for mod in (dict(softcap=cap), dict(softcap=cap, slopes=True, window=90)):
         compare(pa, x, modified(mod, 2, 8, 0.125, fmt, True))
+
+
+@pytest.mark.gpu
+def test_a_decode_that_reads_its_inputs_early_behind_key_weights(pa):
+    # the kernel ahead of the second call (the key weights') writes none of its inputs; the one before
+    # that writes its q
+    x, _ = make(41, "f16", [6000, 5000, 300], 16, 2, 128, 16, 1)
+    zero = torch.zeros(3, x[3].shape[1] * 16, device="cuda")
+    first = pa.ScoredPlan(*x, scale=0.09, causal=True, softcap=20.0, key_weights_out=zero)
+    second = pa.Plan(first.out, *x[1:], scale=1.0, causal=True, inputs_unchanged=True)
+    sets = [torch.randn_like(x[0]) for _ in range(2)]
+    want = []
+    for q in sets:
+        x[0].copy_(q)
+        first.run()
+        torch.cuda.synchronize()
+        want.append(second.run().clone())
+        torch.cuda.synchronize()
+    assert not torch.equal(*want)
+    got = []
+    for n in range(40):
+        x[0].copy_(sets[n % 2])
+        first.run()
+        got.append(second.run().clone())
+    torch.cuda.synchronize()
+    for n, t in enumerate(got):
+        assert torch.equal(t, want[n % 2]), n
