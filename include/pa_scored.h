@@ -29,8 +29,11 @@
  *
  * in and out are float32 [B][max_blocks * BLOCK] and may be the same array; in
  * may be NULL (zeros); keys at max_blocks * BLOCK and beyond are dropped and
- * entries behind the last new row are left as they were.  The sums are formed
- * in one order, whatever the split.
+ * entries behind the last new row are left as they were.  The sums over heads
+ * and rows are formed in one order, so equal calls give equal weights; a call
+ * that is split otherwise (opts->partitions, another batch) has the softmax
+ * denominators added in other groups, and weights that differ by their rounding
+ * (a few 1e-6 of a weight).
  *
  * Layouts, ownership, streams, opts and errors as pa_decode, with these
  * differences: the batch's lengths have to fit beside two pipeline stages in

@@ -6,7 +6,7 @@
 // 4 bytes beside the 4 D bytes or more of the key's K and V) and the rows'
 // softmax denominators; a second pass over K would cost half the decode.
 // Here every key's scores are read once, 2^(score - lse) summed in a fixed
-// order (no atomics: the sum's order does not depend on the split).  Bound by
+// order (no atomics; the denominators' own sums do go by the split).  Bound by
 // latency after the decode's last CTA: about 4 us of a call (B = 8, 512-4096
 // tokens, 32 heads: 25.3 us without the weights, 29 with; 32768 tokens: 34.8
 // and 39.7).

@@ -450,3 +450,18 @@ def test_a_decode_that_reads_its_inputs_early_behind_key_weights(pa):
     torch.cuda.synchronize()
     for n, t in enumerate(got):
         assert torch.equal(t, want[n % 2]), n
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["f32", "f16", "bf16"])
+def test_weights_of_two_schedules(pa, fmt):
+    # split or whole, the weights agree up to the rounding of the softmax denominators
+    x, _ = make(33, fmt, [9000, 700, 31], 4, 1, 128, 16, 1)
+    for mod in (dict(softcap=20.0), dict(slopes=True, window=3000, prefix=50)):
+        kw = modified(mod, 3, 4, 0.09, fmt, True)
+        _, bound, want, lim = reference(x, kw)
+        kw.pop("fmt")
+        got = [pa.decode_scored(*x, **kw, partitions=n, key_weights_out=torch.zeros(3, x[3].shape[1] * 16, device="cuda"))[1]
+               for n in (0, 1)]
+        a, b = (t.double().cpu().numpy() for t in got)
+        assert np.all(np.abs(a - b) <= 2 * (lim + 2.0 ** -23 * want))
