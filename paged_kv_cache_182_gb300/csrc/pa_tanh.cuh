@@ -31,7 +31,9 @@ inline bool softcap_ok(float cap, float scale)
 // whose relative error is about 2^-22.  The hardware's tanh is not used: its
 // relative error of 2^-11 would move a score of 10 under a cap of 50 by 0.005,
 // and every weight with it.
-// One block per warp (the branch is taken together).
+// One block per warp (the branch is taken together).  A score within 0.7 gets the
+// polynomial by the same operations on both sides: its result does not depend on
+// the block's other scores, hidden ones among them.
 template <int N>
 __device__ __forceinline__ void tanh_block(float (&y)[N])
 {

@@ -465,3 +465,25 @@ def test_weights_of_two_schedules(pa, fmt):
                for n in (0, 1)]
         a, b = (t.double().cpu().numpy() for t in got)
         assert np.all(np.abs(a - b) <= 2 * (lim + 2.0 ** -23 * want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,H,KV,D", [("f16", 4, 2, 64), ("f32", 4, 2, 64), ("bf16", 16, 2, 128), ("f16", 32, 2, 128), ("f32", 12, 1, 128)])
+def test_hidden_keys_under_a_cap_change_nothing(pa, fmt, H, KV, D):
+    # the way a block's tanh is computed goes by its largest score, hidden ones included: what hidden
+    # keys hold (large, infinite, NaN) must not move a visible score by a bit
+    lens = [500, 260, 113]
+    x, _ = make(31, fmt, lens, H, KV, D, 16, 2)
+    x[0] *= 0.02  # visible scores of every size below the cap
+    kw = modified(dict(softcap=1.5, window=100, prefix=33), 3, H, 1 / math.sqrt(D), fmt, True)
+    kw.pop("fmt")
+    width = x[3].shape[1] * 16
+    want, w = pa.decode_scored(*x, **kw, key_weights_out=torch.zeros(3, width, device="cuda"))
+    for large in (1.0, 300.0, math.inf):
+        for b, n in enumerate(lens):
+            for j in range(33 - b, n - 99):
+                phys = int(x[3][b, j // 16])
+                x[1][phys, j % 16] = math.nan if large == math.inf and j % 2 else large
+                x[2][phys, j % 16] = large if j % 3 else -large
+        got, u = pa.decode_scored(*x, **kw, key_weights_out=torch.zeros(3, width, device="cuda"))
+        assert torch.equal(got, want) and torch.equal(u, w)
