@@ -198,3 +198,40 @@ def test_training_step(pa):
     for name, a, x in (("dq", dq, leaf[0]), ("dk", dk, leaf[1]), ("dv", dv, leaf[2])):
         want = x.grad
         assert float((a.double().cpu() - want).abs().max()) <= 2e-5 * max(1.0, float(want.abs().max())), name
+
+
+def test_two_loops_and_a_gradient_on_streams_of_their_own(pa):
+    # every plan has its own workspace and scratch: what runs beside it changes nothing
+    def state():
+        loops = [Loop(pa, lens, 60, dtype=torch.float16, D=128) for lens in ([100, 75, 61, 20] * 6, [90, 118] * 4)]
+        g = torch.Generator().manual_seed(21)
+        x = [torch.randn(1, h, 700, 128, generator=g).half().cuda() for h in (4, 2, 2, 4)]
+        grad = pa.ScoredVjpPlan(x[0], x[1], x[2], x[0], x[3], scale=0.09, causal=True, softcap=20.0, window=300)
+        steps = [[torch.randn(t.shape, generator=g).half().cuda() for _ in range(12) for t in (loop.q, loop.k, loop.v)] for loop in loops]
+        return loops, grad, steps
+
+    def step(loop, rows, n):
+        for t, r in zip((loop.q, loop.k, loop.v), rows[3 * n:3 * n + 3]):
+            t.copy_(r)
+        return loop.step().clone()
+
+    loops, grad, rows = state()
+    want = [[step(loop, r, n) for n in range(12)] for loop, r in zip(loops, rows)]
+    want_end = [(loop.lens.clone(), loop.weights.clone(), loop.kc.clone()) for loop in loops]
+    _, dk, dv = (t.clone() for t in grad.run())
+    torch.cuda.synchronize()
+    loops, grad, rows = state()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got, parts = [[], []], []
+    for n in range(12):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(step(loops[i], rows[i], n))
+        with torch.cuda.stream(streams[2]):
+            parts.append([t.clone() for t in grad.run()[1:]])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(want[i], got[i]))
+        assert all(torch.equal(a, b) for a, b in zip(want_end[i], (loops[i].lens, loops[i].weights, loops[i].kc)))
+    assert all(torch.equal(a, dk) and torch.equal(b, dv) for a, b in parts)
