@@ -14,6 +14,13 @@
  *   token r of the shortened sequence gets the K and V rows of token
  *   kept[b][r], as they are (keys keep the positions they were rotated by).
  *
+ * The shortened sequence counts its tokens from 0 again: the distances of
+ * pa_decode_scored (slopes, window) and its prefix are then between places in
+ * the cache, r, no longer between the tokens' places in the text, kept[b][r].
+ * keep_first at least as large as the prefix leaves the prefix as it was, and
+ * keep_last at least as large as the window (or as the reach of the slopes)
+ * leaves the distances inside it exact; older kept tokens come nearer.
+ *
  * kept[b][m .. budget-1] is set to -1, weights_out[b][m .. width-1] to 0.
  *
  * The rows move inside the sequence's own blocks (dst_table NULL: token r goes

@@ -14,6 +14,9 @@
  *       (j <= i or not causal) and (|i - j| < window or window == 0)
  *   out[b][h][r] = sum_j softmax_j(t) * value_j over the visible keys
  *
+ * Positions are places in the cache: behind an eviction (pa_evict.h) the kept
+ * tokens stand closer together than they did in the text.
+ *
  * So prefix[b] is a prefix mask: those keys are visible to every row, also
  * across the causal rule and the window (a bidirectional prompt, or the first
  * tokens kept beside a sliding window).  Every row sees its own key.  Cache

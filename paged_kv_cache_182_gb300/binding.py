@@ -1150,7 +1150,10 @@ class EvictPlan:
     ``key_weights``): the shortened lengths, the kept tokens' old indices (-1
     behind them) and their weights (0 behind them).  ``seq_lens`` and
     ``key_weights`` are left as they are: the loop goes on with the returned
-    ones.  Blocks shared between sequences must not be moved in place."""
+    ones.  Rotary positions go on counting the text (cached keys keep theirs);
+    the window, slopes and prefix of ``decode_scored`` count places in the
+    shortened cache, so ``keep_first`` and ``keep_last`` should cover prefix
+    and window where their distances are to stay exact.  Blocks shared between sequences must not be moved in place."""
 
     def __init__(self, k_cache, v_cache, block_table, seq_lens, key_weights, *, budget: int,
                  keep_first: int = 0, keep_last: int = 0, dst_table=None, new_lens=None, kept=None,
