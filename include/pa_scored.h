@@ -87,8 +87,11 @@ int pa_decode_scored(const void *q, const void *k_cache, const void *v_cache,
                      int NQ, int causal, const pa_score *score, const pa_key_weights *weights,
                      const pa_opts *opts, void *stream);
 
-/* Scratch bytes of the key weights: every score of the call in float32, and
- * the rows' softmax denominators.  0 for invalid sizes. */
+/* Scratch bytes of the key weights: a float32 score for every row and every
+ * token that the table can hold (max_blocks * BLOCK + NQ, whatever the lengths
+ * and the window: 64 sequences, 32 heads, one new row and tables of 131072
+ * tokens take 1.07 GB), and the rows' softmax denominators.  0 for invalid
+ * sizes. */
 size_t pa_scored_scratch_bytes(int batch, int max_blocks, int BLOCK, int H, int KV, int NQ);
 
 /*

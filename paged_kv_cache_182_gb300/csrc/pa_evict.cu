@@ -628,8 +628,8 @@ extern "C" int pa_cache_evict(void* k_cache, void* v_cache, const int32_t* block
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // short sequences: a CTA of 256 threads holds 2048 weights in registers;
     // else 1024 threads and 8192, and a cluster of up to 8 of them (16 weights a
-    // thread and half the CTAs: 29.4 against 23.7 us for a call of 32768 tokens,
-    // 36.4 against 33.4 for 64 of up to 16384; twice the CTAs: 25.5)
+    // thread and half the CTAs: 28.9 against 26.6 us for a call of 32768 tokens,
+    // 37.2 against 36.0 for 64 of up to 16384; twice the CTAs: 28.7 and 39.1)
     const bool small = cap <= 2048;
     const int C = cap <= 8192 ? 1 : cap <= 16384 ? 2 : cap <= 32768 ? 4 : 8;
     const void* sel = small    ? reinterpret_cast<const void*>(pa_evict_select<256, 1>)
@@ -651,12 +651,10 @@ extern "C" int pa_cache_evict(void* k_cache, void* v_cache, const int32_t* block
     void* args[1] = {&p};
     // In place, six runs of 16 KB in flight per CTA; slices of 128 bytes, or of 64
     // or 32 (with two or four times the rows in a run) where wider ones would leave
-    // SMs idle.  Calls with 128-, 64- and 32-byte slices (blocks found by division,
-    // which costs up to a fifth): one sequence, 8192 rows of 2 KB 73.9 / 47.2 /
-    // 39.0 us; one, 19569 of 512 bytes 153.8 / 88.2 / 69.6;
-    // four, 4096 of 2 KB 46.1 / 39.4 / 64.4; sixteen, 2048 of 2 KB 58.0 / 63.9 /
-    // 108.6; the 64 ragged ones 36.1 / 39.7 / 58.3.  (16-byte slices: 63.6 and
-    // 69.8 on the first two.)
+    // SMs idle.  Calls with 128-, 64- and 32-byte slices: one sequence, 8192 rows
+    // of 2 KB 63.5 / 41.0 / 34.8 us; one, 19569 of 512 bytes 129.0 / 72.0 / 57.4;
+    // four, 4096 of 2 KB 43.8 / 38.4 / 56.1; sixteen, 2048 of 2 KB 57.7 / 62.9 /
+    // 97.4; 64 ragged ones 36.9 / 39.3 / 58.2.
     const void* move;
     size_t smem;
     dim3 grid;

@@ -766,7 +766,8 @@ static int decode_impl(const void* q, const void* k_cache, const void* v_cache,
     p.wait_ns = opts->wait_limit_ns ? opts->wait_limit_ns : kWaitLimitNs;
     p.withhold = opts->debug_withhold_stage > 0 ? opts->debug_withhold_stage : 0;
     // the slot-patched decode runs right after its own append kernel
-    // (with modified scores the consumers write scores before a piece ends)
+    // (modified scores do without: with key weights the consumers store scores
+    // before a piece ends, where the wait would have to come first)
     p.early = opts->inputs_unchanged && !positions && !score ? 1 : 0;
     if (score) {
         sp.slopes = score->slopes;

@@ -10,6 +10,14 @@
 // together into shared memory; then each keeps those of its own 16 bytes of a
 // row in registers and walks the heads with them.  The first heads' rows are in
 // flight while the table is computed.
+//
+// What is left: with one or two heads a position's sines are the time (1 + 1
+// heads, 4 x 16384 rows: 24.6 us for 10 of bytes); halves that are not whole
+// vectors read their partners one element at a time ([4, 32 + 8, 2048] bf16:
+// D = 72 halves 51.0 us, pairs 30.7; D = 80 with rot 36 50.8, rot 32 26.7); and
+// every CTA of a store looks through the rest of its sequence for a later row
+// with its slots, N^2 / 2 reads a head share (one sequence of 8192 rows, 32 + 8
+// heads: 71 us, 33 without the store; of 65536: 2.0 ms, 0.23 without).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -423,9 +431,11 @@ extern "C" int pa_rotary(const void* q, const void* k, const int32_t* positions,
     // unit's heads; with fewer than 20 heads a unit per thread, so that a
     // CTA still has enough to do; 32 KB of table at most; and as many heads as four rounds
     // of two take, fewer where the call would leave SMs idle.
-    // [4, 32 + 8, 2048, 128] bf16 (168 MB): 30.7 us, 5.5 TB/s (256 threads and
-    // 64 units 33.7); [31, 8 + 2, 1492, 64] f32 (237 MB): 61 us with 16 units,
-    // 49 with 64; [4, 1 + 1, 16384, 128] bf16: 43 us with 16, 23 with 64.
+    // us with 16 units / a unit per thread, bf16, D = 128, four sequences: 1 + 1
+    // heads (16384 rows) 45.1 / 24.6, 4 + 1 (8192) 28.7 / 22.5, 8 + 2 (4096)
+    // 22.1 / 21.4, 12 + 3 28.6 / 28.7, 16 + 4 (2048) 20.5 / 20.8, 24 + 6 27.8 /
+    // 28.7, 32 + 8 32.8 (5.1 TB/s) / 36.6; f32, D = 64: [31, 8 + 2, 1492] 41.0 /
+    // 42.6, [16, 16 + 4, 1492] 39.8 (6.1 TB/s) / 42.7.
     const int per_row = mode == kHalves ? (D - rot / 2) / V : D / V;
     const int threads = per_row > 128 ? 256 : per_row > 64 ? 128 : 64;
     int rows = p.heads >= 20 ? (15 + per_row) / per_row : threads / per_row;
