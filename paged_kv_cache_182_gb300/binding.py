@@ -319,6 +319,8 @@ def _order(stream, device, *made):
     it holds by the time they are freed."""
     if stream is None:
         return
+    if not hasattr(stream, "wait_stream"):  # another library's stream object: its handle is enough
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
     current = torch.cuda.current_stream(device)
     if stream == current:
         return

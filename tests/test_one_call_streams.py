@@ -244,3 +244,18 @@ def test_rotary_and_eviction_on_another_stream(pa):
         torch.cuda.synchronize()
         for a, b in zip(want, while_the_current_stream_is_busy(call, q.numel() * 4, k.numel() * 4, 256)):
             assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_a_stream_object_of_another_library(pa):
+    # anything with a cuda_stream handle
+    x = batch(torch.float16, [700, 40], 4, 2, 64, 16, 1)
+    want = pa.decode(*x, scale=0.1)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = pa.decode(*x, scale=0.1, stream=types.SimpleNamespace(cuda_stream=side.cuda_stream))
+    side.synchronize()
+    assert torch.equal(want, got)
+    got = pa.decode_scored(*x, scale=0.1, stream=types.SimpleNamespace(cuda_stream=side.cuda_stream))
+    side.synchronize()
+    assert torch.equal(want, got)
