@@ -76,6 +76,8 @@ extern "C" {
 #define PA_STATUS_TIMEOUT 4    /* an internal wait gave up (the output is undefined) */
 #define PA_STATUS_BAD_SLOT 8   /* a new row's slot < -1 or >= num_blocks * BLOCK, or (pa_prefill)
                                   its token beyond the table: the row is not stored */
+#define PA_STATUS_NO_BLOCKS 16 /* pa_plan_blocks: a sequence was refused for want of free blocks */
+#define PA_STATUS_NOT_FINITE 32 /* pa_q8_append: an infinity or a NaN among the rows */
 
 /* supported sizes */
 #define PA_MAX_NQ 16           /* new rows per sequence of one decode call */

@@ -13,7 +13,8 @@ from __future__ import annotations
 import importlib
 
 _CALLS = ("decode", "decode_host", "decode_scored", "attention_vjp_scored", "rotary_table", "rotary",
-          "rotary_append", "cache_evict", "workspace_bytes")
+          "rotary_append", "cache_evict", "plan_blocks", "cache_append_q8", "cache_read_q8",
+          "select_blocks_q8", "decode_q8", "workspace_bytes")
 
 __all__ = ["binding", "workloads", *_CALLS]
 

@@ -27,6 +27,14 @@ backward with scores that are capped, biased by distance or limited to a
 window beside a prefix; the decode also accumulates the weight of every key,
 ``include/pa_scored.h``) and ``cache_evict`` / ``EvictPlan`` (sequences
 shortened to their most attended keys, ``include/pa_evict.h``).
+
+Serving from a cache in 8 bits: ``plan_blocks`` / ``BlockPlan`` (block tables
+and slots of a step, blocks given back and taken, ``include/pa_blocks.h``) and,
+of ``include/pa_q8.h``, ``cache_append_q8`` / ``Q8AppendPlan`` (new rows with a
+scale for each block and head), ``cache_read_q8`` / ``Q8ReadPlan`` (rows back),
+``select_blocks_q8`` / ``Q8SelectPlan`` (the blocks that a step's queries look
+at most) and ``decode_q8`` / ``Q8Plan`` (attention over all blocks, or over
+selected ones).
 """
 from __future__ import annotations
 
@@ -40,6 +48,7 @@ from . import _build
 
 PA_F32, PA_F16, PA_BF16 = 0, 1, 2
 PA_STATUS_BAD_BLOCK, PA_STATUS_BAD_LENGTH, PA_STATUS_TIMEOUT, PA_STATUS_BAD_SLOT = 1, 2, 4, 8
+PA_STATUS_NO_BLOCKS, PA_STATUS_NOT_FINITE = 16, 32
 PA_MAX_NQ = 16
 PA_MAX_PREFILL = 65536
 _DT = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}
@@ -113,6 +122,68 @@ class EvictOpts(ctypes.Structure):
         ("keep_last", ctypes.c_int),
         ("dst_table", ctypes.c_void_p),
         ("dst_max_blocks", ctypes.c_int),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class BlocksOpts(ctypes.Structure):
+    _fields_ = [
+        ("max_blocks", ctypes.c_int),
+        ("num_blocks", ctypes.c_int),
+        ("add", ctypes.c_void_p),
+        ("keep", ctypes.c_void_p),
+        ("starts", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class Q8AppendOpts(ctypes.Structure):
+    _fields_ = [
+        ("max_blocks", ctypes.c_int),
+        ("num_blocks", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("k_strides", ctypes.c_longlong * 3),
+        ("v_strides", ctypes.c_longlong * 3),
+        ("counts", ctypes.c_void_p),
+        ("bounds", ctypes.c_void_p),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class Q8ReadOpts(ctypes.Structure):
+    _fields_ = [
+        ("max_blocks", ctypes.c_int),
+        ("num_blocks", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("counts", ctypes.c_void_p),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class Q8SelectOpts(ctypes.Structure):
+    _fields_ = [
+        ("max_blocks", ctypes.c_int),
+        ("num_blocks", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("budget", ctypes.c_int),
+        ("keep_first", ctypes.c_int),
+        ("keep_last", ctypes.c_int),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class Q8Opts(ctypes.Structure):
+    _fields_ = [
+        ("max_blocks", ctypes.c_int),
+        ("num_blocks", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("causal", ctypes.c_int),
+        ("selected", ctypes.c_void_p),
+        ("counts", ctypes.c_void_p),
+        ("budget", ctypes.c_int),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
         ("status", ctypes.c_void_p),
     ]
 
@@ -202,6 +273,20 @@ def load(path: Path = LIBRARY) -> ctypes.CDLL:
     lib.pa_rotary.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, ctypes.POINTER(RotaryOpts), P]
     lib.pa_cache_evict.restype = I
     lib.pa_cache_evict.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, ctypes.POINTER(EvictOpts), P]
+    lib.pa_plan_blocks.restype = I
+    lib.pa_plan_blocks.argtypes = [P, P, P, P, P, P, P, I, I, I, ctypes.POINTER(BlocksOpts), P]
+    lib.pa_q8_append.restype = I
+    lib.pa_q8_append.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, ctypes.POINTER(Q8AppendOpts), P]
+    lib.pa_q8_read.restype = I
+    lib.pa_q8_read.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, ctypes.POINTER(Q8ReadOpts), P]
+    lib.pa_q8_select.restype = I
+    lib.pa_q8_select.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, ctypes.POINTER(Q8SelectOpts), P]
+    lib.pa_q8_decode.restype = I
+    lib.pa_q8_decode.argtypes = [P, P, P, P, P, P, P, P, ctypes.c_float, I, I, I, I, I, I,
+                                 ctypes.POINTER(Q8Opts), P]
+    for name in ("pa_q8_workspace_bytes", "pa_q8_workspace_zero_bytes"):
+        getattr(lib, name).restype = ctypes.c_size_t
+        getattr(lib, name).argtypes = [I, I, I, I, I]
     lib.pa_cache_append.restype = I
     lib.pa_cache_append.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, P, P]
     return lib
@@ -1219,3 +1304,341 @@ def cache_evict(k_cache, v_cache, block_table, seq_lens, key_weights, *, budget:
     plan = EvictPlan(k_cache, v_cache, block_table, seq_lens, key_weights, budget=budget,
                      keep_first=keep_first, keep_last=keep_last, dst_table=dst_table, status=status)
     return _run_once(plan, stream, plan.new_lens, plan.kept, plan.weights_out)
+
+
+# ------------------------------------------------------------------- blocks of a step
+def _dev_ptr(t):
+    """Address of a tensor for an options structure, or None."""
+    return None if t is None else t.data_ptr()
+
+
+def _same_device(dev, **tensors):
+    """Refuses tensors that are not contiguous CUDA tensors on ``dev``."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda or t.device != dev:
+            raise ValueError(f"{name}: all tensors must be CUDA tensors on one device")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _int32_tensors(shape, **tensors):
+    """Refuses tensors that are not int32 of this shape."""
+    for name, t in tensors.items():
+        if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != torch.int32):
+            raise ValueError(f"{name} must be int32 {list(shape)}")
+
+
+def _made(t, shape, dtype, device, name):
+    """The caller's output tensor, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}")
+    return t
+
+
+class BlockPlan:
+    """One prepared block plan of a serving step (pa_plan_blocks): of every
+    sequence ``keep`` of its ``seq_lens`` tokens stay (None: all; 0: it is
+    done) and ``add`` new ones come (None: ``width``).  Blocks behind what it
+    needs go back on ``free_blocks`` (int32 [num_blocks], a stack of
+    ``free_count`` entries), blocks that it lacks come off it into
+    ``block_table``; both are changed in place.
+
+    ``run()`` returns (new_lens [B], new_free_count [1], slots [B, width],
+    positions [B, width]): slots as ``cache_append`` and ``rotary_append`` take
+    them, -1 behind a sequence's new rows, and the rows' positions in the cache,
+    or counted from ``starts`` (the text, after an eviction).  A sequence that
+    the free blocks do not suffice for keeps its length and gets no slots
+    (``PA_STATUS_NO_BLOCKS``)."""
+
+    def __init__(self, block_table, seq_lens, free_blocks, free_count, *, BLOCK: int, width: int, add=None,
+                 keep=None, starts=None, new_lens=None, new_free_count=None, slots=None, positions=None,
+                 status=None):
+        if block_table.dim() != 2 or block_table.dtype != torch.int32:
+            raise ValueError("block_table must be int32 [B, max_blocks]")
+        B, maxb = (int(x) for x in block_table.shape)
+        if free_blocks.dim() != 1 or free_blocks.dtype != torch.int32:
+            raise ValueError("free_blocks must be int32 [num_blocks]")
+        width = int(width)
+        if width < 0:
+            raise ValueError("width must not be negative")
+        _int32(BLOCK=int(BLOCK), width=width)
+        _int32_tensors((B,), seq_lens=seq_lens, add=add, keep=keep, starts=starts)
+        _int32_tensors((1,), free_count=free_count)
+        dev = block_table.device
+        self.new_lens = _made(new_lens, (B,), torch.int32, dev, "new_lens")
+        self.new_free_count = _made(new_free_count, (1,), torch.int32, dev, "new_free_count")
+        self.slots = _made(slots, (B, width), torch.int32, dev, "slots")
+        self.positions = _made(positions, (B, width), torch.int32, dev, "positions")
+        _same_device(dev, block_table=block_table, seq_lens=seq_lens, free_blocks=free_blocks,
+                     free_count=free_count, add=add, keep=keep, starts=starts, new_lens=self.new_lens,
+                     new_free_count=self.new_free_count, slots=self.slots, positions=self.positions)
+        self.opts = BlocksOpts(
+            max_blocks=maxb, num_blocks=int(free_blocks.shape[0]), add=_dev_ptr(add), keep=_dev_ptr(keep),
+            starts=_dev_ptr(starts), positions=_dev_ptr(self.positions), status=_status_ptr(status, dev))
+        self.device = dev
+        self._keep = (block_table, seq_lens, free_blocks, free_count, add, keep, starts, status)
+        self._args = _ready((_ptr(block_table), _ptr(seq_lens), _ptr(free_blocks), _ptr(free_count),
+                             _ptr(self.new_lens), _ptr(self.new_free_count), _ptr(self.slots), B, width,
+                             int(BLOCK), ctypes.byref(self.opts)))
+
+    def run(self, stream=None):
+        """Enqueue on ``stream`` (default: torch's current stream)."""
+        _call(LIB.pa_plan_blocks, self._args, self.device, stream)
+        return self.new_lens, self.new_free_count, self.slots, self.positions
+
+
+def plan_blocks(block_table, seq_lens, free_blocks, free_count, *, BLOCK: int, width: int, add=None,
+                keep=None, starts=None, status=None, stream=None):
+    """Block tables and slots of a step (pa_plan_blocks): see ``BlockPlan``."""
+    plan = BlockPlan(block_table, seq_lens, free_blocks, free_count, BLOCK=BLOCK, width=width, add=add,
+                     keep=keep, starts=starts, status=status)
+    return _run_once(plan, stream, plan.new_lens, plan.new_free_count, plan.slots, plan.positions)
+
+
+# ------------------------------------------------------------------- cache in 8 bits
+def _q8_cache(k_cache, v_cache, k_scale, v_scale, block_table):
+    """(num_blocks, BLOCK, KV, D, B, max_blocks) of a cache in 8 bits and its table, checked."""
+    if k_cache.dim() != 4 or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("shapes: caches [num_blocks, BLOCK, KV, D]")
+    if k_cache.dtype != torch.int8 or v_cache.dtype != torch.int8:
+        raise TypeError("k_cache and v_cache must be int8")
+    NB, BLOCK, KV, D = (int(x) for x in k_cache.shape)
+    for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if tuple(s.shape) != (NB, KV) or s.dtype != torch.float32:
+            raise ValueError(f"{name} must be float32 [num_blocks, KV]")
+    if block_table.dim() != 2 or block_table.dtype != torch.int32:
+        raise ValueError("block_table must be int32 [B, max_blocks]")
+    _same_device(k_cache.device, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale,
+                 block_table=block_table)
+    return NB, BLOCK, KV, D, int(block_table.shape[0]), int(block_table.shape[1])
+
+
+def _q8_bounds(bounds, NB, KV, D, device):
+    if tuple(bounds.shape) != (NB, KV, 2, D) or bounds.dtype != torch.int8:
+        raise ValueError("bounds must be int8 [num_blocks, KV, 2, D]")
+    _same_device(device, bounds=bounds)
+
+
+class Q8AppendPlan:
+    """One prepared store of new rows into a cache in 8 bits (pa_q8_append):
+    rows j < ``counts[b]`` (None: all N) of ``k_new`` / ``v_new`` [B, KV, N, D]
+    (float32, float16 or bfloat16, strided views with contiguous columns
+    allowed) become tokens ``seq_lens[b] + j`` of ``k_cache`` / ``v_cache``
+    (int8 [num_blocks, BLOCK, KV, D]), with ``k_scale`` / ``v_scale`` (float32
+    [num_blocks, KV]) and, if given, ``bounds`` (int8 [num_blocks, KV, 2, D],
+    the lowest and highest code of each channel).  A block whose scale grows has
+    its earlier codes rounded again.  ``run()`` returns (k_cache, v_cache,
+    k_scale, v_scale)."""
+
+    def __init__(self, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, *,
+                 counts=None, bounds=None, status=None):
+        NB, BLOCK, KV, D, B, maxb = _q8_cache(k_cache, v_cache, k_scale, v_scale, block_table)
+        if k_new.dim() != 4 or tuple(k_new.shape[:2]) != (B, KV) or k_new.shape[3] != D or \
+                tuple(v_new.shape) != tuple(k_new.shape):
+            raise ValueError("shapes: k_new and v_new [B, KV, N, D]")
+        if k_new.dtype not in _DT or v_new.dtype != k_new.dtype:
+            raise TypeError("k_new and v_new must share one supported dtype")
+        N, dev = int(k_new.shape[2]), k_cache.device
+        for t in (k_new, v_new):
+            if not t.is_cuda or t.device != dev:
+                raise ValueError("all tensors must be CUDA tensors on one device")
+        _int32_tensors((B,), seq_lens=seq_lens, counts=counts)
+        _same_device(dev, seq_lens=seq_lens, counts=counts)
+        if bounds is not None:
+            _q8_bounds(bounds, NB, KV, D, dev)
+        o = Q8AppendOpts(max_blocks=maxb, num_blocks=NB, dtype=_DT[k_new.dtype], counts=_dev_ptr(counts),
+                         bounds=_dev_ptr(bounds), status=_status_ptr(status, dev))
+        o.k_strides[:] = _row_strides(k_new)
+        o.v_strides[:] = _row_strides(v_new)
+        self.opts, self.device = o, dev
+        self.cache = (k_cache, v_cache, k_scale, v_scale)
+        self._keep = (k_new, v_new, block_table, seq_lens, counts, bounds, status)
+        self._args = _ready((*(_ptr(t) for t in self.cache), _ptr(k_new), _ptr(v_new), _ptr(block_table),
+                             _ptr(seq_lens), B, KV, D, N, BLOCK, ctypes.byref(o)))
+
+    def run(self, stream=None):
+        """Enqueue on ``stream`` (default: torch's current stream)."""
+        _call(LIB.pa_q8_append, self._args, self.device, stream)
+        return self.cache
+
+
+def cache_append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, *,
+                    counts=None, bounds=None, status=None, stream=None):
+    """New rows into a cache in 8 bits (pa_q8_append): see ``Q8AppendPlan``."""
+    plan = Q8AppendPlan(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                        counts=counts, bounds=bounds, status=status)
+    return _run_once(plan, stream)
+
+
+class Q8ReadPlan:
+    """One prepared read of a cache in 8 bits (pa_q8_read): tokens ``starts[b]``
+    .. ``starts[b] + counts[b] - 1`` of every sequence (counts None: ``width``)
+    as ``k_out`` / ``v_out`` [B, KV, width, D] of ``dtype``.  Rows behind the
+    counts are left as they were (zeros in tensors made here)."""
+
+    def __init__(self, k_cache, v_cache, k_scale, v_scale, block_table, starts, *, width: int | None = None,
+                 counts=None, dtype=None, k_out=None, v_out=None, status=None):
+        NB, BLOCK, KV, D, B, maxb = _q8_cache(k_cache, v_cache, k_scale, v_scale, block_table)
+        dev = k_cache.device
+        given = k_out if k_out is not None else v_out
+        if given is not None:
+            if given.dim() != 4:
+                raise ValueError("shapes: k_out and v_out [B, KV, width, D]")
+            width = int(given.shape[2]) if width is None else int(width)
+            dtype = given.dtype if dtype is None else dtype
+        if width is None:
+            raise ValueError("width is needed without k_out")
+        _int32(width=int(width))
+        dtype = torch.float16 if dtype is None else dtype
+        if dtype not in _DT:
+            raise TypeError(f"unsupported dtype {dtype}")
+        _int32_tensors((B,), starts=starts, counts=counts)
+        outs = []
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            if t is None:
+                t = torch.zeros((B, KV, int(width), D), dtype=dtype, device=dev)
+            outs.append(_made(t, (B, KV, int(width), D), dtype, dev, name))
+        self.k_out, self.v_out = outs
+        _same_device(dev, starts=starts, counts=counts, k_out=self.k_out, v_out=self.v_out)
+        self.opts = Q8ReadOpts(max_blocks=maxb, num_blocks=NB, dtype=_DT[dtype], counts=_dev_ptr(counts),
+                               status=_status_ptr(status, dev))
+        self.device = dev
+        self._keep = (k_cache, v_cache, k_scale, v_scale, block_table, starts, counts, status)
+        self._args = _ready((*(_ptr(t) for t in (k_cache, v_cache, k_scale, v_scale, block_table, starts,
+                                                  self.k_out, self.v_out)),
+                             B, KV, D, int(width), BLOCK, ctypes.byref(self.opts)))
+
+    def run(self, stream=None):
+        """Enqueue on ``stream`` (default: torch's current stream); returns (k_out, v_out)."""
+        _call(LIB.pa_q8_read, self._args, self.device, stream)
+        return self.k_out, self.v_out
+
+
+def cache_read_q8(k_cache, v_cache, k_scale, v_scale, block_table, starts, *, width: int, counts=None,
+                  dtype=None, status=None, stream=None):
+    """Rows of a cache in 8 bits (pa_q8_read): see ``Q8ReadPlan``."""
+    plan = Q8ReadPlan(k_cache, v_cache, k_scale, v_scale, block_table, starts, width=width, counts=counts,
+                      dtype=dtype, status=status)
+    return _run_once(plan, stream, plan.k_out, plan.v_out)
+
+
+class Q8SelectPlan:
+    """One prepared selection of blocks (pa_q8_select): for every sequence and KV
+    head the first ``keep_first`` blocks, the last ``keep_last`` and, of those
+    between, the ones whose keys the query rows q [B, H, NQ, D] may look at
+    most, ``budget`` in all, by a bound on their products from ``bounds`` and
+    ``k_scale``.  ``run()`` returns (selected int32 [B, KV, budget], ascending,
+    -1 behind them, and counts int32 [B, KV])."""
+
+    def __init__(self, q, bounds, k_scale, block_table, seq_lens, *, BLOCK: int, budget: int,
+                 keep_first: int = 0, keep_last: int = 1, selected=None, counts=None, status=None):
+        if q.dim() != 4 or q.dtype not in _DT:
+            raise ValueError("q must be [B, H, NQ, D] of a supported dtype")
+        if k_scale.dim() != 2 or k_scale.dtype != torch.float32:
+            raise ValueError("k_scale must be float32 [num_blocks, KV]")
+        B, H, NQ, D = (int(x) for x in q.shape)
+        NB, KV = (int(x) for x in k_scale.shape)
+        dev = q.device
+        _q8_bounds(bounds, NB, KV, D, dev)
+        if block_table.dim() != 2 or block_table.shape[0] != B or block_table.dtype != torch.int32:
+            raise ValueError("block_table must be int32 [B, max_blocks]")
+        _int32_tensors((B,), seq_lens=seq_lens)
+        budget = int(budget)
+        if budget < 1:
+            raise ValueError("budget must be at least 1")
+        _int32(BLOCK=int(BLOCK), budget=budget, keep_first=int(keep_first), keep_last=int(keep_last))
+        self.selected = _made(selected, (B, KV, budget), torch.int32, dev, "selected")
+        self.counts = _made(counts, (B, KV), torch.int32, dev, "counts")
+        _same_device(dev, q=q, k_scale=k_scale, block_table=block_table, seq_lens=seq_lens,
+                     selected=self.selected, counts=self.counts)
+        self.opts = Q8SelectOpts(
+            max_blocks=int(block_table.shape[1]), num_blocks=NB, dtype=_DT[q.dtype], budget=budget,
+            keep_first=int(keep_first), keep_last=int(keep_last), status=_status_ptr(status, dev))
+        self.device = dev
+        self._keep = (q, bounds, k_scale, block_table, seq_lens, status)
+        self._args = _ready((_ptr(q), _ptr(bounds), _ptr(k_scale), _ptr(block_table), _ptr(seq_lens),
+                             _ptr(self.selected), _ptr(self.counts), B, H, KV, D, NQ, int(BLOCK),
+                             ctypes.byref(self.opts)))
+
+    def run(self, stream=None):
+        """Enqueue on ``stream`` (default: torch's current stream)."""
+        _call(LIB.pa_q8_select, self._args, self.device, stream)
+        return self.selected, self.counts
+
+
+def select_blocks_q8(q, bounds, k_scale, block_table, seq_lens, *, BLOCK: int, budget: int,
+                     keep_first: int = 0, keep_last: int = 1, status=None, stream=None):
+    """The blocks that a step's queries look at most (pa_q8_select): see ``Q8SelectPlan``."""
+    plan = Q8SelectPlan(q, bounds, k_scale, block_table, seq_lens, BLOCK=BLOCK, budget=budget,
+                        keep_first=keep_first, keep_last=keep_last, status=status)
+    return _run_once(plan, stream, plan.selected, plan.counts)
+
+
+def q8_workspace_bytes(B: int, H: int, KV: int, D: int, NQ: int) -> int:
+    """Workspace of ``decode_q8``; the first ``q8_workspace_zero_bytes`` have to start as zeros."""
+    return int(LIB.pa_q8_workspace_bytes(B, H, KV, D, NQ))
+
+
+def q8_workspace_zero_bytes(B: int, H: int, KV: int, D: int, NQ: int) -> int:
+    return int(LIB.pa_q8_workspace_zero_bytes(B, H, KV, D, NQ))
+
+
+class Q8Plan:
+    """One prepared attention over a cache in 8 bits (pa_q8_decode): q [B, H, NQ,
+    D] of the last NQ of ``seq_lens`` tokens (``cache_append_q8`` has stored
+    them) against all cached keys, with ``causal`` up to the row's own, or, with
+    ``selected`` [B, KV, budget] and ``counts`` [B, KV], against those of the
+    selected blocks.  ``run()`` returns out, like q.  A workspace of one's own
+    (uint8, ``q8_workspace_bytes``, zeroed) may be shared by plans whose calls
+    do not overlap on the GPU."""
+
+    def __init__(self, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, *, scale: float,
+                 causal: bool = False, selected=None, counts=None, out=None, workspace=None, status=None):
+        NB, BLOCK, KV, D, B, maxb = _q8_cache(k_cache, v_cache, k_scale, v_scale, block_table)
+        if q.dim() != 4 or q.shape[0] != B or q.shape[3] != D:
+            raise ValueError("q must be [B, H, NQ, D]")
+        if q.dtype not in _DT:
+            raise TypeError(f"unsupported dtype {q.dtype}")
+        H, NQ, dev = int(q.shape[1]), int(q.shape[2]), k_cache.device
+        _int32_tensors((B,), seq_lens=seq_lens)
+        if (selected is None) != (counts is None):
+            raise ValueError("selected and counts come together")
+        if selected is not None:
+            if selected.dim() != 3:
+                raise ValueError("selected must be int32 [B, KV, budget]")
+            _int32_tensors((B, KV, int(selected.shape[2])), selected=selected)
+            _int32_tensors((B, KV), counts=counts)
+        self.out = _made(out, tuple(q.shape), q.dtype, dev, "out")
+        if workspace is None:
+            workspace = torch.zeros(q8_workspace_bytes(B, H, KV, D, NQ), dtype=torch.uint8, device=dev)
+        _same_device(dev, q=q, seq_lens=seq_lens, selected=selected, counts=counts, out=self.out,
+                     workspace=workspace)
+        self.workspace = workspace
+        self.opts = Q8Opts(
+            max_blocks=maxb, num_blocks=NB, dtype=_DT[q.dtype], causal=int(bool(causal)),
+            selected=_dev_ptr(selected), counts=_dev_ptr(counts),
+            budget=0 if selected is None else int(selected.shape[2]), workspace=workspace.data_ptr(),
+            workspace_bytes=workspace.numel() * workspace.element_size(), status=_status_ptr(status, dev))
+        self.device = dev
+        self._keep = (q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, selected, counts, status)
+        self._args = _ready((*(_ptr(t) for t in (q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                                                  self.out)),
+                             ctypes.c_float(scale), B, H, KV, D, NQ, BLOCK, ctypes.byref(self.opts)))
+
+    def run(self, stream=None):
+        """Enqueue on ``stream`` (default: torch's current stream); returns out."""
+        _call(LIB.pa_q8_decode, self._args, self.device, stream)
+        return self.out
+
+
+def decode_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, *, scale: float,
+              causal: bool = False, selected=None, counts=None, out=None, workspace=None, status=None,
+              stream=None):
+    """Attention over a cache in 8 bits (pa_q8_decode): see ``Q8Plan``."""
+    plan = Q8Plan(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale=scale, causal=causal,
+                  selected=selected, counts=counts, out=out, workspace=workspace, status=status)
+    return _run_once(plan, stream, plan.out, plan.workspace)

@@ -1,0 +1,401 @@
+// pa_q8_store.cu -- new rows into the cache in 8 bits, and rows back out of it
+// (include/pa_q8.h).
+//
+// pa_q8_append_kernel: a group of BLOCK * D / 32 threads owns one block of one
+// sequence and KV head, keys or values; a thread holds two runs of 16 elements
+// of it in registers, so the rows are read once for their largest magnitude and
+// their codes.  The largest magnitude, and for keys the lowest and highest
+// codes by channel, are joined by shuffles and through shared memory.  Earlier
+// codes are read only where the scale grew.
+//
+// pa_q8_read_kernel: a thread takes runs of 16 codes.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "pa_q8.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kStoreThreads = 256;
+
+struct AppendParams {
+    int8_t* cache[2];  // K, V
+    float* scale[2];
+    const void* rows[2];
+    long long stride[2][3];
+    int8_t* bounds;
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* counts;
+    int* status;
+    int KV, N, maxb, num_blocks, cap;
+};
+
+__device__ __forceinline__ int clamp_report(int x, int hi, int* status)
+{
+    if (x >= 0 && x <= hi)
+        return x;
+    q8_report(status, PA_STATUS_BAD_LENGTH);
+    return x < 0 ? 0 : hi;
+}
+
+// grid (blocks a sequence's new rows may touch, ceil(KV / heads of a CTA) * 2, B)
+template <typename T, int D, int BLOCK>
+__global__ void __launch_bounds__(kStoreThreads) pa_q8_append_kernel(const __grid_constant__ AppendParams p)
+{
+    constexpr int kGroup = BLOCK * D / 32;           // threads of a block and head
+    constexpr int kThreads = kGroup < 64 ? 64 : kGroup;
+    constexpr int kHeads = kThreads / kGroup;        // heads of a CTA
+    constexpr int kRuns = D / 16, kRows = kGroup / kRuns;  // a thread's rows: r, r + kRows (= BLOCK / 2)
+    __shared__ float part[kThreads / 32];
+    __shared__ uint32_t ends[2][kThreads / 32][kRuns * 4];  // lowest, highest codes by warp
+    grid_dependents_launch();
+    grid_dependency_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b = blockIdx.z, kv = blockIdx.y & 1;
+    const int h = (blockIdx.y >> 1) * kHeads + tid / kGroup;
+    const int me = tid % kGroup, run = me % kRuns, row0 = me / kRuns;
+    const bool report = blockIdx.x == 0 && blockIdx.y == 0 && tid == 0;
+    const int past = clamp_report(__ldg(p.lens + b), p.cap, report ? p.status : nullptr);
+    const int want = p.counts ? clamp_report(__ldg(p.counts + b), p.N, report ? p.status : nullptr) : p.N;
+    const int blk = past / BLOCK + blockIdx.x;  // of the sequence
+    const int first = blk * BLOCK;
+    if (first >= past + want)  // the same in every thread of the CTA
+        return;
+    int phys = -1;
+    if (blk < p.maxb)
+        phys = __ldg(p.table + static_cast<int64_t>(b) * p.maxb + blk);
+    if (phys < 0 || phys >= p.num_blocks) {
+        if (tid == 0)
+            q8_report(p.status, PA_STATUS_BAD_SLOT);
+        return;
+    }
+    const bool live = h < p.KV;
+    const bool earlier = first < past;
+    const int64_t at = static_cast<int64_t>(phys) * p.KV + h;
+    const float was = live && earlier ? p.scale[kv][at] : 0.f;
+
+    float x[2][16];
+    bool fresh[2];
+    float a = 0.f;
+    bool odd = false;  // something is not finite
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int token = first + row0 + k * kRows;
+        fresh[k] = live && token >= past && token < past + want;
+        if (fresh[k]) {
+            const T* src = static_cast<const T*>(p.rows[kv]) + b * p.stride[kv][0] + h * p.stride[kv][1] +
+                           (token - past) * p.stride[kv][2] + run * 16;
+            q8_load16(x[k], src);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                odd |= !(fabsf(x[k][i]) <= 3.402823466e38f);
+                a = q8_amax(a, x[k][i]);
+            }
+        }
+    }
+    if (odd)
+        q8_report(p.status, PA_STATUS_NOT_FINITE);
+#pragma unroll
+    for (int o = 1; o < (kGroup < 32 ? kGroup : 32); o <<= 1)
+        a = fmaxf(a, __shfl_xor_sync(kFullWarp, a, o));
+    if constexpr (kGroup > 32) {
+        if (lane == 0)
+            part[warp] = a;
+        __syncthreads();
+        constexpr int kWarps = kGroup / 32;
+        a = part[warp / kWarps * kWarps];
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i)
+            a = fmaxf(a, part[warp / kWarps * kWarps + i]);
+    }
+    const float scale = fmaxf(q8_scale_of(a), was), inv = 1.f / scale;
+    const bool grown = earlier && scale > was;
+    if (live && me == 0 && (!earlier || grown))
+        p.scale[kv][at] = scale;
+
+    uint32_t lo[4], hi[4];  // of this thread's new rows: lowest and highest code by channel, four a word
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        lo[i] = 0x7f7f7f7fu;
+        hi[i] = 0x81818181u;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int row = row0 + k * kRows, token = first + row;
+        int8_t* dst = p.cache[kv] + ((static_cast<int64_t>(phys) * BLOCK + row) * p.KV + h) * D + run * 16;
+        uint32_t w[4];
+        if (fresh[k]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[i] |= static_cast<uint32_t>(q8_code(x[k][4 * i + j], scale, inv) & 255) << (8 * j);
+                lo[i] = __vmins4(lo[i], w[i]);
+                hi[i] = __vmaxs4(hi[i], w[i]);
+            }
+            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else if (live && grown && token < past) {
+            const uint4 old = *reinterpret_cast<const uint4*>(dst);
+            const uint32_t o[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[i] |= static_cast<uint32_t>(q8_again(q8_byte(o[i], j), was, scale, inv) & 255) << (8 * j);
+            }
+            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+
+    if (kv == 0 && p.bounds) {  // (the same in every thread)
+        // lanes with the same columns, then warps
+#pragma unroll
+        for (int o = kRuns; o < (kGroup < 32 ? kGroup : 32); o <<= 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                lo[i] = __vmins4(lo[i], __shfl_xor_sync(kFullWarp, lo[i], o));
+                hi[i] = __vmaxs4(hi[i], __shfl_xor_sync(kFullWarp, hi[i], o));
+            }
+        if constexpr (kGroup > 32) {
+            if (lane < kRuns) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    ends[0][warp][lane * 4 + i] = lo[i];
+                    ends[1][warp][lane * 4 + i] = hi[i];
+                }
+            }
+            __syncthreads();
+        }
+        if (live && me < kRuns) {
+            if constexpr (kGroup > 32) {
+                constexpr int kWarps = kGroup / 32;
+                const int base = warp / kWarps * kWarps;
+#pragma unroll
+                for (int v = 0; v < kWarps; ++v)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        lo[i] = __vmins4(lo[i], ends[0][base + v][me * 4 + i]);
+                        hi[i] = __vmaxs4(hi[i], ends[1][base + v][me * 4 + i]);
+                    }
+            }
+            uint4* to = reinterpret_cast<uint4*>(p.bounds + at * 2 * D + me * 16);
+            if (earlier) {
+                const uint4 old[2] = {to[0], to[D / 16]};
+                const uint32_t o[2][4] = {{old[0].x, old[0].y, old[0].z, old[0].w}, {old[1].x, old[1].y, old[1].z, old[1].w}};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[2] = {o[0][i], o[1][i]};
+                    if (grown) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            w[e] = 0;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                w[e] |= static_cast<uint32_t>(q8_again(q8_byte(o[e][i], j), was, scale, inv) & 255) << (8 * j);
+                        }
+                    }
+                    lo[i] = __vmins4(lo[i], w[0]);
+                    hi[i] = __vmaxs4(hi[i], w[1]);
+                }
+            }
+            to[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            to[D / 16] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        }
+    }
+}
+
+struct ReadParams {
+    const int8_t* cache[2];
+    const float* scale[2];
+    void* out[2];
+    const int32_t* table;
+    const int32_t* starts;
+    const int32_t* counts;
+    int* status;
+    int KV, N, BLOCK, shift, maxb, num_blocks, cap;
+};
+
+// grid (ranges of a sequence's rows, 2, B): runs of 16 codes, heads and columns
+// innermost, as the cache has them.
+template <typename T, int D>
+__global__ void __launch_bounds__(kStoreThreads) pa_q8_read_kernel(const __grid_constant__ ReadParams p, int rows_cta)
+{
+    grid_dependents_launch();
+    grid_dependency_wait();
+    constexpr int kRuns = D / 16;
+    const int tid = threadIdx.x, b = blockIdx.z, kv = blockIdx.y;
+    const bool lead = tid == 0 && blockIdx.x == 0 && kv == 0;
+    const int start = clamp_report(__ldg(p.starts + b), p.cap, lead ? p.status : nullptr);
+    int rows = p.counts ? clamp_report(__ldg(p.counts + b), p.N, lead ? p.status : nullptr) : p.N;
+    rows = clamp_report(rows, p.cap - start, lead ? p.status : nullptr);
+    const int r0 = blockIdx.x * rows_cta, r1 = min(r0 + rows_cta, rows);
+    const int per = p.KV * kRuns;  // runs of a token
+    const int total = max(r1 - r0, 0) * per;
+    for (int i = tid; i < total; i += kStoreThreads) {
+        const int r = r0 + i / per, hr = i % per, h = hr / kRuns, run = hr % kRuns;
+        const int token = start + r, blk = token >> p.shift;
+        const int phys = __ldg(p.table + static_cast<int64_t>(b) * p.maxb + blk);
+        if (phys < 0 || phys >= p.num_blocks) {
+            q8_report(p.status, PA_STATUS_BAD_BLOCK);
+            continue;
+        }
+        const float scale = __ldg(p.scale[kv] + static_cast<int64_t>(phys) * p.KV + h);
+        const uint4 c = __ldg(reinterpret_cast<const uint4*>(
+            p.cache[kv] + ((static_cast<int64_t>(phys) * p.BLOCK + (token & (p.BLOCK - 1))) * p.KV + h) * D + run * 16));
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        float f[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            f[k] = static_cast<float>(q8_byte(w[k >> 2], k & 3)) * scale;
+        q8_store16(static_cast<T*>(p.out[kv]) + ((static_cast<int64_t>(b) * p.KV + h) * p.N + r) * D + run * 16, f);
+    }
+}
+
+template <typename T, int D>
+const void* append_kernel(int BLOCK)
+{
+    return BLOCK == 8    ? reinterpret_cast<const void*>(pa_q8_append_kernel<T, D, 8>)
+           : BLOCK == 16 ? reinterpret_cast<const void*>(pa_q8_append_kernel<T, D, 16>)
+           : BLOCK == 32 ? reinterpret_cast<const void*>(pa_q8_append_kernel<T, D, 32>)
+                         : reinterpret_cast<const void*>(pa_q8_append_kernel<T, D, 64>);
+}
+
+template <typename T>
+const void* append_kernel(int D, int BLOCK)
+{
+    return D == 64 ? append_kernel<T, 64>(BLOCK) : append_kernel<T, 128>(BLOCK);
+}
+
+template <typename T>
+const void* read_kernel(int D)
+{
+    return D == 64 ? reinterpret_cast<const void*>(pa_q8_read_kernel<T, 64>) : reinterpret_cast<const void*>(pa_q8_read_kernel<T, 128>);
+}
+
+// Elements from the first to behind the last of rows with these strides.
+size_t span_of(int B, int KV, int N, int D, const long long* s)
+{
+    return static_cast<size_t>((B - 1) * s[0] + (KV - 1) * s[1] + (N - 1) * s[2] + D);
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" int pa_q8_append(int8_t* k_cache, int8_t* v_cache, float* k_scale, float* v_scale, const void* k_new,
+                            const void* v_new, const int32_t* block_table, const int32_t* seq_lens, int B, int KV, int D, int N,
+                            int BLOCK, const pa_q8_append_opts* opts, void* stream)
+{
+    if (!opts)
+        return PA_ERR_NULL_POINTER;
+    const pa_q8_append_opts& o = *opts;
+    const int rc = q8_sizes(B, KV, D, BLOCK, o.max_blocks, o.num_blocks, o.dtype);
+    if (rc != PA_OK)
+        return rc;
+    if (N < 0)
+        return PA_ERR_BAD_DIMS;
+    if (N > PA_MAX_PREFILL)
+        return PA_ERR_UNSUPPORTED;
+    if (B == 0 || N == 0)
+        return PA_OK;
+    if (!k_cache || !v_cache || !k_scale || !v_scale || !k_new || !v_new || !block_table || !seq_lens)
+        return PA_ERR_NULL_POINTER;
+    const int e = o.dtype == PA_F32 ? 4 : 2;
+    if (!q8_a16(k_cache) || !q8_a16(v_cache) || !q8_a16(k_new) || !q8_a16(v_new) || !q8_a16(o.bounds) || !q8_a4(k_scale) ||
+        !q8_a4(v_scale) || !q8_a4(block_table) || !q8_a4(seq_lens) || !q8_a4(o.counts) || !q8_a4(o.status))
+        return PA_ERR_ALIGNMENT;
+    for (int i = 0; i < 3; ++i) {
+        if (o.k_strides[i] < 0 || o.v_strides[i] < 0 || (o.k_strides[i] * e) % 16 != 0 || (o.v_strides[i] * e) % 16 != 0)
+            return PA_ERR_ALIGNMENT;
+        if (o.k_strides[i] >= (1ll << 40) || o.v_strides[i] >= (1ll << 40))
+            return PA_ERR_BAD_DIMS;
+    }
+    const size_t blocks = static_cast<size_t>(o.num_blocks) * KV, pool = blocks * BLOCK * D, b4 = static_cast<size_t>(B) * 4;
+    const Q8Range r[] = {{k_cache, pool, true},        {v_cache, pool, true},
+                         {k_scale, blocks * 4, true},  {v_scale, blocks * 4, true},
+                         {o.bounds, blocks * 2 * D, true}, {o.status, 4, true},
+                         {k_new, span_of(B, KV, N, D, o.k_strides) * e, false}, {v_new, span_of(B, KV, N, D, o.v_strides) * e, false},
+                         {block_table, b4 * o.max_blocks, false}, {seq_lens, b4, false}, {o.counts, b4, false}};
+    if (q8_overlap(r, 11))
+        return PA_ERR_BAD_DIMS;
+    AppendParams p{};
+    p.cache[0] = k_cache, p.cache[1] = v_cache;
+    p.scale[0] = k_scale, p.scale[1] = v_scale;
+    p.rows[0] = k_new, p.rows[1] = v_new;
+    for (int i = 0; i < 3; ++i)
+        p.stride[0][i] = o.k_strides[i], p.stride[1][i] = o.v_strides[i];
+    p.bounds = o.bounds;
+    p.table = block_table;
+    p.lens = seq_lens;
+    p.counts = o.counts;
+    p.status = o.status;
+    p.KV = KV;
+    p.N = N;
+    p.maxb = o.max_blocks;
+    p.num_blocks = o.num_blocks;
+    p.cap = o.max_blocks * BLOCK;
+    const int group = BLOCK * D / 32, threads = group < 64 ? 64 : group, heads = threads / group;
+    const void* fn = o.dtype == PA_F32   ? append_kernel<float>(D, BLOCK)
+                     : o.dtype == PA_F16 ? append_kernel<__half>(D, BLOCK)
+                                         : append_kernel<__nv_bfloat16>(D, BLOCK);
+    void* args[] = {&p};
+    return q8_launch(fn, dim3((N + BLOCK - 2) / BLOCK + 1, (KV + heads - 1) / heads * 2, B), threads, 0,
+                     static_cast<cudaStream_t>(stream), args);
+}
+
+extern "C" int pa_q8_read(const int8_t* k_cache, const int8_t* v_cache, const float* k_scale, const float* v_scale,
+                          const int32_t* block_table, const int32_t* starts, void* k_out, void* v_out, int B, int KV, int D, int N,
+                          int BLOCK, const pa_q8_read_opts* opts, void* stream)
+{
+    if (!opts)
+        return PA_ERR_NULL_POINTER;
+    const pa_q8_read_opts& o = *opts;
+    const int rc = q8_sizes(B, KV, D, BLOCK, o.max_blocks, o.num_blocks, o.dtype);
+    if (rc != PA_OK)
+        return rc;
+    if (N < 0 || N >= (1 << 30))
+        return PA_ERR_BAD_DIMS;
+    if (B == 0 || N == 0)
+        return PA_OK;
+    if (!k_cache || !v_cache || !k_scale || !v_scale || !k_out || !v_out || !block_table || !starts)
+        return PA_ERR_NULL_POINTER;
+    if (!q8_a16(k_cache) || !q8_a16(v_cache) || !q8_a16(k_out) || !q8_a16(v_out) || !q8_a4(k_scale) || !q8_a4(v_scale) ||
+        !q8_a4(block_table) || !q8_a4(starts) || !q8_a4(o.counts) || !q8_a4(o.status))
+        return PA_ERR_ALIGNMENT;
+    const size_t blocks = static_cast<size_t>(o.num_blocks) * KV, pool = blocks * BLOCK * D, b4 = static_cast<size_t>(B) * 4;
+    const size_t out = static_cast<size_t>(B) * KV * N * D * (o.dtype == PA_F32 ? 4 : 2);
+    const Q8Range r[] = {{k_out, out, true},           {v_out, out, true},
+                         {o.status, 4, true},          {k_cache, pool, false},
+                         {v_cache, pool, false},       {k_scale, blocks * 4, false},
+                         {v_scale, blocks * 4, false}, {block_table, b4 * o.max_blocks, false},
+                         {starts, b4, false},          {o.counts, b4, false}};
+    if (q8_overlap(r, 10))
+        return PA_ERR_BAD_DIMS;
+    ReadParams p{};
+    p.cache[0] = k_cache, p.cache[1] = v_cache;
+    p.scale[0] = k_scale, p.scale[1] = v_scale;
+    p.out[0] = k_out, p.out[1] = v_out;
+    p.table = block_table;
+    p.starts = starts;
+    p.counts = o.counts;
+    p.status = o.status;
+    p.KV = KV;
+    p.N = N;
+    p.BLOCK = BLOCK;
+    p.shift = BLOCK == 8 ? 3 : BLOCK == 16 ? 4 : BLOCK == 32 ? 5 : 6;
+    p.maxb = o.max_blocks;
+    p.num_blocks = o.num_blocks;
+    p.cap = o.max_blocks * BLOCK;
+    const void* fn = o.dtype == PA_F32 ? read_kernel<float>(D) : o.dtype == PA_F16 ? read_kernel<__half>(D) : read_kernel<__nv_bfloat16>(D);
+    // about four runs a thread
+    int rows = 4 * kStoreThreads / (KV * (D / 16));
+    rows = rows < 1 ? 1 : rows;
+    void* args[] = {&p, &rows};
+    return q8_launch(fn, dim3((N + rows - 1) / rows, 2, B), kStoreThreads, 0, static_cast<cudaStream_t>(stream), args);
+}
