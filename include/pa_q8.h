@@ -62,8 +62,8 @@ extern "C" {
  *           [-127, 127]; an infinity is +-127, a NaN 0
  *   codes of the earlier rows, where the scale grew: the integer nearest to
  *           code * earlier scale / scale (ties to even)
- *   bounds (if given): the earlier ones, rounded again in the same way (none
- *           where the block holds no earlier tokens), widened by the new rows
+ *   bounds (if given): lowest and highest code by channel of the block's keys,
+ *           the earlier rows' and the new ones'
  *
  * a / 127 is rounded to float32, the quotients are not: the codes are exact.
  * A value is off by at most half its block's scale at the time it is stored,

@@ -59,7 +59,7 @@ struct DecodeParams {
     float* part_o;     // [CTA][2][8 NT][D]
     int* status;
     float scale;       // scale * log2(e)
-    int B, H, KV, R, NQ, groups, shift, maxb, num_blocks, cap, budget, causal, dtype, entries, stages;
+    int B, H, KV, R, NQ, groups, shift, maxb, num_blocks, cap, budget, causal, dtype, entries;
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src)
@@ -105,7 +105,7 @@ __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, ui
 
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
-// log2 and exp2 in float32 of the hardware (2 units in the last place or so).
+// log2 and 1 / x of the hardware (a unit in the last place or two).
 __device__ __forceinline__ float fast_log2(float x)
 {
     float y;
@@ -113,24 +113,80 @@ __device__ __forceinline__ float fast_log2(float x)
     return y;
 }
 
-// QP: fp16 parts of a query row and of a weight (2: float32).
-template <int D, int NT, int QP>
-__global__ void __launch_bounds__(kDecodeThreads, NT == 1 && QP == 1 ? 2 : 1) pa_q8_decode_kernel(const __grid_constant__ DecodeParams p)
+__device__ __forceinline__ float fast_rcp(float x)
 {
-    constexpr int kRows = 8 * NT, kSteps = D / 16, kTileBytes = 2 * kTile * D, kStage = kTileBytes + kMeta;
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// QP: fp16 parts of a query row and of a weight (2: float32).  HB: blocks a
+// tile may touch (2: BLOCK is 8).  Query fragments stay in registers, or in
+// shared memory where the accumulators of four groups of rows leave no room.
+template <int D, int NT, int QP>
+struct Shape {
+    static constexpr int kRows = 8 * NT, kSteps = D / 16;
+    static constexpr int kTileBytes = 2 * kTile * D, kStage = kTileBytes + kMeta;
+    static constexpr int kCtas = NT == 1 && QP == 1 ? 2 : 1;
+    static constexpr bool kQueryShared = NT == 4;
+    static constexpr int kQueryBytes = kQueryShared ? QP * kSteps * NT * 32 * 8 : 0;
+    static constexpr int kStages = kCtas == 2 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+    static constexpr int kRing = kWarps * kStages * kStage;
+    static constexpr int kMerge = kWarps * kRows * D * 4, kPieces = kMaxCtas * kRows * 8;
+    static constexpr int kBody = kRing > kMerge ? (kRing > kPieces ? kRing : kPieces) : (kMerge > kPieces ? kMerge : kPieces);
+};
+
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float4 v)
+{
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(p) = v;
+    } else if constexpr (std::is_same_v<T, __half>) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(half2_bits(__floats2half2_rn(v.x, v.y)), half2_bits(__floats2half2_rn(v.z, v.w)));
+    } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
+}
+
+__device__ __forceinline__ void store_out(const DecodeParams& p, int64_t at, float4 v)
+{
+    if (p.dtype == PA_F32)
+        store4(static_cast<float*>(p.out) + at, v);
+    else if (p.dtype == PA_F16)
+        store4(static_cast<__half*>(p.out) + at, v);
+    else
+        store4(static_cast<__nv_bfloat16*>(p.out) + at, v);
+}
+
+__device__ __forceinline__ void fma4(float4& a, float f, float4 v)
+{
+    a.x = fmaf(f, v.x, a.x);
+    a.y = fmaf(f, v.y, a.y);
+    a.z = fmaf(f, v.z, a.z);
+    a.w = fmaf(f, v.w, a.w);
+}
+
+template <int D, int NT, int QP, int HB>
+__global__ void __launch_bounds__(kDecodeThreads, Shape<D, NT, QP>::kCtas) pa_q8_decode_kernel(const __grid_constant__ DecodeParams p)
+{
+    using Sh = Shape<D, NT, QP>;
+    constexpr int kRows = Sh::kRows, kSteps = Sh::kSteps, kTileBytes = Sh::kTileBytes, kStage = Sh::kStage, S = Sh::kStages;
     constexpr int kChunks = D / 64;  // 16-byte runs of a key row per lane
-    extern __shared__ __align__(16) unsigned char smem[];
+    constexpr bool kQs = Sh::kQueryShared;
+    extern __shared__ __align__(16) unsigned char smem[];  // states or ring | query fragments | prefix sums
     __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
     __shared__ int sm_last;
     grid_dependents_launch();
     grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * S * kStage);
+    float* merge = reinterpret_cast<float*>(smem);
+    uint2* sm_q = reinterpret_cast<uint2*>(smem + Sh::kBody);  // [QP][step][group of rows][lane]
+    int* prefix = reinterpret_cast<int*>(smem + Sh::kBody + Sh::kQueryBytes);
 
     // prefix sums of the units of the entries (sequences, or sequences and KV
     // heads where each has its own blocks); `copies` segments share an entry's length
-    int* prefix = reinterpret_cast<int*>(smem);
-    const uint32_t ring0 = smem_u32(smem) + static_cast<uint32_t>((p.entries + 1) * 4 + 15) / 16 * 16;
-    float* merge = reinterpret_cast<float*>(smem + ((p.entries + 1) * 4 + 15) / 16 * 16);
     const int copies = p.selected ? p.groups : p.KV * p.groups;
     {
         int* sums = reinterpret_cast<int*>(&sm_m[0][0]);
@@ -182,7 +238,6 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 && QP == 1 ? 2 : 1) pa
         return;
     const int64_t u_end = (static_cast<int64_t>(blockIdx.x) + 1) * U / G;
     const int64_t u_begin = static_cast<int64_t>(blockIdx.x) * U / G;
-    const uint32_t ring = ring0 + static_cast<uint32_t>(warp * p.stages * kStage);
 
     for (int64_t u = u_begin; u < u_end;) {
         // the segment of unit u: entry e, copy c of it
@@ -216,8 +271,89 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 && QP == 1 ? 2 : 1) pa
         const int last = min(static_cast<int>(stop - s_begin) * kUnit, (tokens + kTile - 1) / kTile);
         const int row_base = grp * kRows;
 
+        // ---- copies: block numbers are looked up one tile ahead, selected ones two
+        const uint32_t step = static_cast<uint32_t>(p.KV) * D;
+        const int8_t* pk = p.k + static_cast<int64_t>(kh) * D + g * step + t * 16;
+        const int8_t* pv = p.v + static_cast<int64_t>(kh) * D + 2 * t * step + g * (D / 8);
+        const float* psc = (lane ? p.vs : p.ks) + kh;
+        int blk[HB], blk_next[HB], phys[HB];
+        auto look_selected = [&](int tile) {  // logical blocks of a tile (-1: none)
+#pragma unroll
+            for (int x = 0; x < HB; ++x) {
+                const int place = tile * kTile + 8 * x;
+                int j = -1;
+                if (tile < last && place < tokens) {
+                    j = place >> p.shift;
+                    if (sel)
+                        j = __ldg(sel + j);
+                }
+                blk_next[x] = j;
+            }
+        };
+        auto look_table = [&]() {
+#pragma unroll
+            for (int x = 0; x < HB; ++x) {
+                blk[x] = blk_next[x];
+                if (sel && (blk[x] < 0 || blk[x] >= nb)) {
+                    if (blk[x] != -1)
+                        q8_report(p.status, PA_STATUS_BAD_BLOCK);
+                    blk[x] = -1;
+                }
+                phys[x] = blk[x] >= 0 ? __ldg(table + blk[x]) : -1;
+            }
+        };
+        auto issue = [&](int tile, uint32_t st) {
+            if (tile < last) {
+                const int in_block = HB == 2 ? 0 : (tile * kTile) & ((1 << p.shift) - 1);
+                uint32_t row[HB];
+                int place[HB];
+#pragma unroll
+                for (int x = 0; x < HB; ++x) {
+                    const bool there = static_cast<uint32_t>(phys[x]) < static_cast<uint32_t>(p.num_blocks);
+                    if (!there && blk[x] >= 0)
+                        q8_report(p.status, PA_STATUS_BAD_BLOCK);
+                    // (without a block: the first rows of the pool are read in its place, and hidden)
+                    const uint32_t ph = there ? static_cast<uint32_t>(phys[x]) : 0u;
+                    place[x] = there ? (blk[x] << p.shift) + in_block : INT_MAX - 64;
+                    row[x] = (ph << p.shift) + static_cast<uint32_t>(in_block);
+                    if (lane < 2)
+                        copy4(st + kTileBytes + x * 8 + lane * 4, psc + static_cast<uint64_t>(ph) * p.KV);
+                    if (lane == 2)
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + kTileBytes + 16 + 4 * x), "r"(place[x]) : "memory");
+                }
+                const uint32_t sv = st + kTile * D;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t r = HB == 2 ? row[x & (HB - 1)] : row[0] + 8 * x;
+                    const uint64_t at = static_cast<uint64_t>(r) * step;
+                    const int8_t* k = pk + at;
+                    const int8_t* v = pv + at;
+#pragma unroll
+                    for (int ch = 0; ch < kChunks; ++ch)
+                        copy16(st + ((x * kChunks + ch) * 32 + lane) * 16, k + ch * 64);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if constexpr (D == 128)
+                            copy16(sv + ((x * 2 + i) * 32 + lane) * 16, v + i * step);
+                        else
+                            copy8(sv + ((x * 2 + i) * 32 + lane) * 8, v + i * step);
+                    }
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        look_selected(first);
+        look_table();
+        look_selected(first + kUnit);
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i) {
+            issue(first + i * kUnit, ring + i * kStage);
+            look_table();
+            look_selected(first + (i + 2) * kUnit);
+        }
+
         // ---- query rows: fragments of B, scaled by a power of two
-        uint32_t qf[QP][NT][kSteps][2];
+        uint32_t qf[kQs ? 1 : QP][kQs ? 1 : NT][kQs ? 1 : kSteps][2];
         float rowf[NT][2];   // of this lane's two score columns: scale * log2(e) / the power of two
         int lim[NT][2];      // keys that the column's row sees
 #pragma unroll
@@ -258,17 +394,25 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 && QP == 1 ? 2 : 1) pa
             const float factor = p.scale * d1 * d2;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
-                float z[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    z[i] = x[4 * s + i] * f1 * f2;
+                uint32_t w[QP][2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const __half2 hi = __floats2half2_rn(z[2 * i], z[2 * i + 1]);
-                    qf[0][nt][s][i] = half2_bits(hi);
+                    const float z0 = x[4 * s + 2 * i] * f1 * f2, z1 = x[4 * s + 2 * i + 1] * f1 * f2;
+                    const __half2 hi = __floats2half2_rn(z0, z1);
+                    w[0][i] = half2_bits(hi);
                     if constexpr (QP == 2) {
                         const float2 back = __half22float2(hi);
-                        qf[1][nt][s][i] = half2_bits(__floats2half2_rn(z[2 * i] - back.x, z[2 * i + 1] - back.y));
+                        w[QP - 1][i] = half2_bits(__floats2half2_rn(z0 - back.x, z1 - back.y));
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < QP; ++q) {
+                    if constexpr (kQs) {
+                        if (warp == nt)  // one warp a group of rows
+                            sm_q[((q * kSteps + s) * NT + nt) * 32 + lane] = make_uint2(w[q][0], w[q][1]);
+                    } else {
+                        qf[q][nt][s][0] = w[q][0];
+                        qf[q][nt][s][1] = w[q][1];
                     }
                 }
             }
@@ -279,7 +423,10 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 && QP == 1 ? 2 : 1) pa
                 lim[nt][i] = r >= p.R ? 0 : p.causal ? min(n, n - p.NQ + r % p.NQ + 1) : n;
             }
         }
-        const int all_see = p.causal ? n - p.NQ + 1 : n;  // every row sees the keys below
+        if constexpr (kQs)
+            __syncthreads();
+        // every row sees the keys below
+        const int all_see = row_base + kRows > p.R ? INT_MIN : (p.causal ? n - p.NQ + 1 : n) - 8 * (3 - HB);
 
         float o[kSteps][NT][4];
         float mx[NT][2], l[NT][2];
@@ -297,98 +444,9 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 && QP == 1 ? 2 : 1) pa
                     o[s][nt][i] = 0.f;
         }
 
-        // ---- copies: block numbers are looked up one tile ahead, selected ones two
-        int blk[2], blk_next[2], phys[2];
-        auto look_selected = [&](int tile) {  // logical blocks of a tile's halves (-1: none)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int place = tile * kTile + 8 * x;
-                int j = -1;
-                if (tile < last && place < tokens) {
-                    j = place >> p.shift;
-                    if (sel)
-                        j = __ldg(sel + j);
-                }
-                blk_next[x] = j;
-            }
-        };
-        auto look_table = [&]() {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                blk[x] = blk_next[x];
-                if (sel && (blk[x] < 0 || blk[x] >= nb)) {
-                    if (blk[x] != -1)
-                        q8_report(p.status, PA_STATUS_BAD_BLOCK);
-                    blk[x] = -1;
-                }
-                phys[x] = blk[x] >= 0 ? __ldg(table + blk[x]) : -1;
-            }
-        };
-        auto issue = [&](int tile, int stage) {
-            if (tile < last) {
-                const uint32_t st = ring + static_cast<uint32_t>(stage * kStage);
-                const int in_block = (tile * kTile) & ((1 << p.shift) - 1);
-                int64_t at[2];
-                int place[2];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (phys[x] >= p.num_blocks || (blk[x] >= 0 && phys[x] < 0)) {
-                        q8_report(p.status, PA_STATUS_BAD_BLOCK);
-                        phys[x] = -1;
-                    }
-                    const int r = p.shift == 3 ? 0 : in_block + 8 * x;
-                    place[x] = phys[x] >= 0 ? (blk[x] << p.shift) + r : INT_MAX - 64;
-                    const int ph = max(phys[x], 0);
-                    at[x] = (((static_cast<int64_t>(ph) << p.shift) + r) * p.KV + kh) * D;
-                    if (lane < 2 && phys[x] >= 0) {
-                        const float* src = (lane ? p.vs : p.ks) + static_cast<int64_t>(ph) * p.KV + kh;
-                        copy4(st + kTileBytes + x * 8 + lane * 4, src);
-                    }
-                }
-                if (lane == 2) {
-                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(st + kTileBytes + 16), "r"(place[0]), "r"(place[1]) : "memory");
-                }
-                const int64_t step = static_cast<int64_t>(p.KV) * D;
-                // (a half without a block repeats row 0 of the pool: in bounds, weighed with zero)
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int ch = 0; ch < kChunks; ++ch)
-                        copy16(st + ((x * kChunks + ch) * 32 + lane) * 16, p.k + at[x] + g * step + ch * 64 + t * 16);
-                const uint32_t sv = st + kTile * D;
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int8_t* src = p.v + at[x] + (2 * t + i) * step + g * (D / 8);
-                        if constexpr (D == 128)
-                            copy16(sv + ((x * 2 + i) * 32 + lane) * 16, src);
-                        else
-                            copy8(sv + ((x * 2 + i) * 32 + lane) * 8, src);
-                    }
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        const int S = p.stages;
-        look_selected(first);
-        look_table();
-        look_selected(first + kUnit);
-        for (int i = 0; i < S - 1; ++i) {
-            issue(first + i * kUnit, i);
-            look_table();
-            look_selected(first + (i + 2) * kUnit);
-        }
-        int stage = 0, fill = S - 1;
+        uint32_t st = ring, fill = ring + (S - 1) * kStage;
         for (int tile = first; tile < last; tile += kUnit) {
-            // the oldest group is this tile's (S is 3, 4, 6 or 8)
-            if (S == 3)
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
-            else if (S == 4)
-                asm volatile("cp.async.wait_group 2;" ::: "memory");
-            else if (S == 6)
-                asm volatile("cp.async.wait_group 4;" ::: "memory");
-            else
-                asm volatile("cp.async.wait_group 6;" ::: "memory");
+            asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");  // this tile's
             __syncwarp();  // scales and places come from other lanes; the stage filled next has been read
             {
                 const int ahead = tile + (S - 1) * kUnit;
@@ -396,17 +454,25 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 && QP == 1 ? 2 : 1) pa
                 look_table();
                 look_selected(ahead + 2 * kUnit);
             }
-            const uint32_t st = ring + static_cast<uint32_t>(stage * kStage);
-            const uint4 sc = lds16(st + kTileBytes);
-            const uint2 pl = lds8(st + kTileBytes + 16);
-            const int place[2] = {static_cast<int>(pl.x), static_cast<int>(pl.y)};
-            const float ks[2] = {__uint_as_float(sc.x), __uint_as_float(sc.z)};
-            float lv[2], iv[2];
+            float ks[HB], lv[HB], iv[HB];
+            int place[2];
+            if constexpr (HB == 2) {
+                const uint4 sc = lds16(st + kTileBytes);
+                const uint2 pl = lds8(st + kTileBytes + 16);
+                ks[0] = __uint_as_float(sc.x), ks[HB - 1] = __uint_as_float(sc.z);
+                lv[0] = __uint_as_float(sc.y), lv[HB - 1] = __uint_as_float(sc.w);
+                place[0] = static_cast<int>(pl.x), place[1] = static_cast<int>(pl.y);
+            } else {
+                const uint2 sc = lds8(st + kTileBytes);
+                const uint2 pl = lds8(st + kTileBytes + 16);
+                ks[0] = __uint_as_float(sc.x), lv[0] = __uint_as_float(sc.y);
+                place[0] = static_cast<int>(pl.x), place[1] = place[0] + 8;
+            }
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const float vs = fmaxf(__uint_as_float(x ? sc.w : sc.y), kMinScale);
+            for (int x = 0; x < HB; ++x) {
+                const float vs = fmaxf(lv[x], kMinScale);
                 lv[x] = fast_log2(vs);
-                iv[x] = __frcp_rn(vs);
+                iv[x] = fast_rcp(vs);
             }
             // ---- S^T = K Q^T
             float sacc[NT][4];
@@ -426,18 +492,23 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 && QP == 1 ? 2 : 1) pa
 #pragma unroll
                     for (int q = 0; q < QP; ++q)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma(sacc[nt], a, qf[q][nt][ch * 4 + i][0], qf[q][nt][ch * 4 + i][1]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if constexpr (kQs) {
+                                const uint2 w = sm_q[((q * kSteps + ch * 4 + i) * NT + nt) * 32 + lane];
+                                mma(sacc[nt], a, w.x, w.y);
+                            } else {
+                                mma(sacc[nt], a, qf[q][nt][ch * 4 + i][0], qf[q][nt][ch * 4 + i][1]);
+                            }
+                        }
                 }
             }
             // ---- scores in base 2 plus log2 of the value scale; hidden ones -inf
-            bool raise = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    sacc[nt][i] = fmaf(sacc[nt][i], rowf[nt][i & 1] * ks[i >> 1], lv[i >> 1]);
-            if (max(place[0], place[1]) + 8 > all_see || row_base + kRows > p.R) {
+                    sacc[nt][i] = fmaf(sacc[nt][i], rowf[nt][i & 1] * ks[(i >> 1) & (HB - 1)], lv[(i >> 1) & (HB - 1)]);
+            if (HB == 1 ? place[0] > all_see : max(place[0], place[1]) > all_see) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -445,11 +516,12 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 && QP == 1 ? 2 : 1) pa
                         if (place[i >> 1] + g >= lim[nt][i & 1])
                             sacc[nt][i] = -INFINITY;
             }
+            bool raise = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    raise |= sacc[nt][i] > mx[nt][i & 1] + kSlack;
+                for (int i = 0; i < 2; ++i)
+                    raise |= fmaxf(sacc[nt][i], sacc[nt][i + 2]) > mx[nt][i] + kSlack;
             if (__any_sync(kFullWarp, raise)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -477,9 +549,16 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 && QP == 1 ? 2 : 1) pa
                 float w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float base = mx[nt][i & 1] == -INFINITY ? 0.f : mx[nt][i & 1] - kLift;
+                    // (a row that has seen nothing: its scores are -inf, and so is what is left of them)
+                    const float base = fmaxf(mx[nt][i & 1], -3.402823466e38f) - kLift;
                     w[i] = fast_exp2(sacc[nt][i] - base);
-                    l[nt][i & 1] = sacc[nt][i] == -INFINITY ? l[nt][i & 1] : fmaf(w[i], iv[i >> 1], l[nt][i & 1]);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if constexpr (HB == 1)
+                        l[nt][i] = fmaf(w[i] + w[i + 2], iv[0], l[nt][i]);
+                    else
+                        l[nt][i] = fmaf(w[i], iv[0], fmaf(w[i + 2], iv[HB - 1], l[nt][i]));
                 }
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
@@ -487,7 +566,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 && QP == 1 ? 2 : 1) pa
                     pf[0][nt][x] = movm_trans(half2_bits(hi));
                     if constexpr (QP == 2) {
                         const float2 back = __half22float2(hi);
-                        pf[1][nt][x] = movm_trans(half2_bits(__floats2half2_rn(w[2 * x] - back.x, w[2 * x + 1] - back.y)));
+                        pf[QP - 1][nt][x] = movm_trans(half2_bits(__floats2half2_rn(w[2 * x] - back.x, w[2 * x + 1] - back.y)));
                     }
                 }
             }
@@ -533,8 +612,8 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 && QP == 1 ? 2 : 1) pa
                     }
                 }
             }
-            stage = stage + 1 == S ? 0 : stage + 1;
-            fill = fill + 1 == S ? 0 : fill + 1;
+            st = st + kStage == ring + S * kStage ? ring : st + kStage;
+            fill = fill + kStage == ring + S * kStage ? ring : fill + kStage;
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();  // the rings are free
@@ -563,38 +642,35 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 && QP == 1 ? 2 : 1) pa
         const bool whole = u == s_begin && stop == s_end;
         const int slot = u == u_begin && u != s_begin ? 0 : 1;  // a piece of a segment begun earlier, or one that goes on
         const int64_t record = static_cast<int64_t>(blockIdx.x) * 2 + slot;
-        for (int x = tid; x < kRows * D; x += kDecodeThreads) {
-            const int row = x / D, d = x % D;
+        const int64_t out0 = ((static_cast<int64_t>(b) * p.KV + kh) * p.R + row_base) * D;
+        constexpr int kItems = kRows * D / 4;
+        for (int x = tid; x < kItems; x += kDecodeThreads) {
+            const int row = x / (D / 4), d = x % (D / 4) * 4;
             if (row_base + row >= p.R)
                 break;
             float m = -INFINITY;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w)
                 m = fmaxf(m, sm_m[w][row]);
-            float sum = 0.f, val = 0.f;
+            float sum = 0.f;
+            float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float f = sm_m[w][row] == -INFINITY ? 0.f : fast_exp2(sm_m[w][row] - m);
                 sum = fmaf(sm_l[w][row], f, sum);
-                val = fmaf(merge[(static_cast<size_t>(w) * kRows + row) * D + d], f, val);
+                fma4(val, f, *reinterpret_cast<const float4*>(merge + (static_cast<size_t>(w) * kRows + row) * D + d));
             }
             if (whole) {
-                const float y = sum == 0.f ? 0.f : val / sum;
-                const int64_t at = ((static_cast<int64_t>(b) * p.KV + kh) * p.R + row_base + row) * D + d;
-                if (p.dtype == PA_F32)
-                    static_cast<float*>(p.out)[at] = y;
-                else if (p.dtype == PA_F16)
-                    static_cast<__half*>(p.out)[at] = __float2half_rn(y);
-                else
-                    static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
+                const float r = sum == 0.f ? 0.f : 1.f / sum;
+                store_out(p, out0 + static_cast<int64_t>(row) * D + d, make_float4(val.x * r, val.y * r, val.z * r, val.w * r));
             } else {
-                p.part_o[(record * kRows + row) * D + d] = val;
+                *reinterpret_cast<float4*>(p.part_o + (record * kRows + row) * D + d) = val;
                 if (d == 0)
                     p.part_ml[record * kRows + row] = make_float2(m, sum);
             }
         }
         if (!whole) {
-            // pieces of the segment: CTAs c0 .. c1
+            // pieces of the segment: those of CTAs c0 .. c1
             const int c0 = static_cast<int>(((s_begin + 1) * G - 1) / U), c1 = static_cast<int>((s_end * G - 1) / U);
             __threadfence();
             __syncthreads();
@@ -607,31 +683,47 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 && QP == 1 ? 2 : 1) pa
             __syncthreads();
             if (sm_last) {
                 __threadfence();
-                for (int x = tid; x < kRows * D; x += kDecodeThreads) {
-                    const int row = x / D, d = x % D;
+                const int pieces = c1 - c0 + 1;
+                // the first CTA's range begins with this segment or earlier, the others' inside it
+                const bool late = static_cast<int64_t>(c0) * U / G > s_begin;
+                auto record_of = [&](int i) { return static_cast<int64_t>(c0 + i) * 2 + (i > 0 || late ? 0 : 1); };
+                float2* ml = reinterpret_cast<float2*>(smem);  // [piece][row]: maximum, sum; then factor
+                for (int x = tid; x < pieces * kRows; x += kDecodeThreads)
+                    ml[x] = __ldcg(p.part_ml + record_of(x / kRows) * kRows + x % kRows);
+                __syncthreads();
+                for (int row = warp; row < kRows; row += kWarps) {
                     if (row_base + row >= p.R)
                         break;
-                    float m = -INFINITY, sum = 0.f, val = 0.f;
-                    for (int i = c0; i <= c1; ++i) {
-                        // the first CTA's range may begin with this segment or earlier
-                        const int64_t begin = static_cast<int64_t>(i) * U / G;
-                        const int64_t rec = static_cast<int64_t>(i) * 2 + (begin > s_begin ? 0 : 1);
-                        const float2 ml = __ldcg(p.part_ml + rec * kRows + row);
-                        const float v = __ldcg(p.part_o + (rec * kRows + row) * D + d);
-                        const float now = fmaxf(m, ml.x);
-                        const float fa = m == -INFINITY ? 0.f : fast_exp2(m - now), fb = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - now);
-                        sum = sum * fa + ml.y * fb;
-                        val = val * fa + v * fb;
-                        m = now;
+                    float m = -INFINITY, sum = 0.f;
+                    for (int i = lane; i < pieces; i += 32)
+                        m = fmaxf(m, ml[i * kRows + row].x);
+#pragma unroll
+                    for (int k = 1; k < 32; k <<= 1)
+                        m = fmaxf(m, __shfl_xor_sync(kFullWarp, m, k));
+                    for (int i = lane; i < pieces; i += 32) {
+                        const float2 v = ml[i * kRows + row];
+                        const float f = v.x == -INFINITY ? 0.f : fast_exp2(v.x - m);
+                        ml[i * kRows + row].x = f;
+                        sum = fmaf(v.y, f, sum);
                     }
-                    const float y = sum == 0.f ? 0.f : val / sum;
-                    const int64_t at = ((static_cast<int64_t>(b) * p.KV + kh) * p.R + row_base + row) * D + d;
-                    if (p.dtype == PA_F32)
-                        static_cast<float*>(p.out)[at] = y;
-                    else if (p.dtype == PA_F16)
-                        static_cast<__half*>(p.out)[at] = __float2half_rn(y);
-                    else
-                        static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
+#pragma unroll
+                    for (int k = 1; k < 32; k <<= 1)
+                        sum += __shfl_xor_sync(kFullWarp, sum, k);
+                    if (lane == 0)
+                        sm_l[0][row] = sum == 0.f ? 0.f : 1.f / sum;
+                }
+                __syncthreads();
+                for (int x = tid; x < kItems; x += kDecodeThreads) {
+                    const int row = x / (D / 4), d = x % (D / 4) * 4;
+                    if (row_base + row >= p.R)
+                        break;
+                    float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
+                    const float* from = p.part_o + static_cast<int64_t>(row) * D + d;
+#pragma unroll 8
+                    for (int i = 0; i < pieces; ++i)
+                        fma4(val, ml[i * kRows + row].x, __ldcg(reinterpret_cast<const float4*>(from + record_of(i) * kRows * D)));
+                    const float r = sm_l[0][row];
+                    store_out(p, out0 + static_cast<int64_t>(row) * D + d, make_float4(val.x * r, val.y * r, val.z * r, val.w * r));
                 }
             }
         }
@@ -642,29 +734,26 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 && QP == 1 ? 2 : 1) pa
 
 struct Variant {
     const void* fn;
-    int rows, ctas, stages;
-    size_t tile;
+    int rows, ctas;
+    size_t body;  // shared memory apart from the prefix sums
 };
 
-template <int D>
-Variant variant(int dtype, int R)
+template <int D, int NT, int QP>
+Variant variant(int BLOCK)
 {
-    Variant v;
-    v.tile = static_cast<size_t>(2) * kTile * D + kMeta;
-    if (dtype == PA_F32) {
-        v.rows = R > 8 ? 16 : 8;
-        v.fn = R > 8 ? reinterpret_cast<const void*>(pa_q8_decode_kernel<D, 2, 2>) : reinterpret_cast<const void*>(pa_q8_decode_kernel<D, 1, 2>);
-    } else {
-        v.rows = R > 16 ? 32 : R > 8 ? 16 : 8;
-        v.fn = R > 16  ? reinterpret_cast<const void*>(pa_q8_decode_kernel<D, 4, 1>)
-               : R > 8 ? reinterpret_cast<const void*>(pa_q8_decode_kernel<D, 2, 1>)
-                       : reinterpret_cast<const void*>(pa_q8_decode_kernel<D, 1, 1>);
-    }
-    v.ctas = dtype != PA_F32 && R <= 8 ? 2 : 1;
-    return v;
+    using Sh = Shape<D, NT, QP>;
+    return {BLOCK == 8 ? reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 2>)
+                       : reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 1>),
+            Sh::kRows, Sh::kCtas, static_cast<size_t>(Sh::kBody) + Sh::kQueryBytes};
 }
 
-Variant variant_of(int D, int dtype, int R) { return D == 64 ? variant<64>(dtype, R) : variant<128>(dtype, R); }
+template <int D>
+Variant variant(int BLOCK, int dtype, int R)
+{
+    if (dtype == PA_F32)
+        return R > 8 ? variant<D, 2, 2>(BLOCK) : variant<D, 1, 2>(BLOCK);
+    return R > 16 ? variant<D, 4, 1>(BLOCK) : R > 8 ? variant<D, 2, 1>(BLOCK) : variant<D, 1, 1>(BLOCK);
+}
 
 // Sizes that pa_q8_decode refuses, apart from those of the cache.
 int decode_sizes(int B, int H, int KV, int NQ)
@@ -756,7 +845,7 @@ extern "C" int pa_q8_decode(const void* q, const int8_t* k_cache, const int8_t* 
                          {o.counts, b4 * KV, false}};
     if (q8_overlap(r, 12))
         return PA_ERR_BAD_DIMS;
-    const Variant v = variant_of(D, o.dtype, R);
+    const Variant v = D == 64 ? variant<64>(BLOCK, o.dtype, R) : variant<128>(BLOCK, o.dtype, R);
     DecodeParams p{};
     p.groups = (R + v.rows - 1) / v.rows;
     p.entries = o.selected ? B * KV : B;
@@ -793,20 +882,11 @@ extern "C" int pa_q8_decode(const void* q, const int8_t* k_cache, const int8_t* 
     p.budget = o.budget;
     p.causal = o.causal ? 1 : 0;
     p.dtype = o.dtype;
-    // ring depth: what fits beside the prefix sums, and the states merged in the same memory
-    const size_t head = ((static_cast<size_t>(p.entries) + 1) * 4 + 15) / 16 * 16;
-    const size_t room = static_cast<size_t>(v.ctas == 2 ? 108 : 220) * 1024 - head;
-    const int fit = static_cast<int>(room / (kWarps * v.tile));
-    p.stages = fit >= 8 ? 8 : fit >= 6 ? 6 : fit >= 4 ? 4 : 3;
-    size_t body = kWarps * v.tile * p.stages;
-    const size_t merge = static_cast<size_t>(kWarps) * v.rows * D * 4;
-    if (body < merge)
-        body = merge;
     int sms = 0, dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return PA_ERR_CUDA;
     int grid = sms * v.ctas;
     grid = grid > kMaxCtas ? kMaxCtas : grid;
     void* args[] = {&p};
-    return q8_launch(v.fn, dim3(grid), kDecodeThreads, head + body, static_cast<cudaStream_t>(stream), args);
+    return q8_launch(v.fn, dim3(grid), kDecodeThreads, v.body + (static_cast<size_t>(p.entries) + 1) * 4, static_cast<cudaStream_t>(stream), args);
 }

@@ -6,7 +6,7 @@
 // of it in registers, so the rows are read once for their largest magnitude and
 // their codes.  The largest magnitude, and for keys the lowest and highest
 // codes by channel, are joined by shuffles and through shared memory.  Earlier
-// codes are read only where the scale grew.
+// codes are read only where the scale grew, and for the bounds.
 //
 // pa_q8_read_kernel: a thread takes runs of 16 codes.
 #include <cuda_runtime.h>
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kStoreThreads) pa_q8_append_kernel(const __gri
     const int want = p.counts ? clamp_report(__ldg(p.counts + b), p.N, report ? p.status : nullptr) : p.N;
     const int blk = past / BLOCK + blockIdx.x;  // of the sequence
     const int first = blk * BLOCK;
-    if (first >= past + want)  // the same in every thread of the CTA
+    if (want == 0 || first >= past + want)  // no new row; the same in every thread of the CTA
         return;
     int phys = -1;
     if (blk < p.maxb)
@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(kStoreThreads) pa_q8_append_kernel(const __gri
     if (live && me == 0 && (!earlier || grown))
         p.scale[kv][at] = scale;
 
-    uint32_t lo[4], hi[4];  // of this thread's new rows: lowest and highest code by channel, four a word
+    const bool ranged = kv == 0 && p.bounds;  // (the same in every thread)
+    uint32_t lo[4], hi[4];  // of this thread's rows: lowest and highest code by channel, four a word
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         lo[i] = 0x7f7f7f7fu;
@@ -138,21 +139,27 @@ __global__ void __launch_bounds__(kStoreThreads) pa_q8_append_kernel(const __gri
                 hi[i] = __vmaxs4(hi[i], w[i]);
             }
             *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else if (live && grown && token < past) {
+        } else if (live && token < past && (grown || ranged)) {
             const uint4 old = *reinterpret_cast<const uint4*>(dst);
             const uint32_t o[4] = {old.x, old.y, old.z, old.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                w[i] = 0;
+                w[i] = o[i];
+                if (grown) {
+                    w[i] = 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[i] |= static_cast<uint32_t>(q8_again(q8_byte(o[i], j), was, scale, inv) & 255) << (8 * j);
+                    for (int j = 0; j < 4; ++j)
+                        w[i] |= static_cast<uint32_t>(q8_again(q8_byte(o[i], j), was, scale, inv) & 255) << (8 * j);
+                }
+                lo[i] = __vmins4(lo[i], w[i]);
+                hi[i] = __vmaxs4(hi[i], w[i]);
             }
-            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (grown)
+                *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
 
-    if (kv == 0 && p.bounds) {  // (the same in every thread)
+    if (ranged) {
         // lanes with the same columns, then warps
 #pragma unroll
         for (int o = kRuns; o < (kGroup < 32 ? kGroup : 32); o <<= 1)
@@ -184,25 +191,6 @@ __global__ void __launch_bounds__(kStoreThreads) pa_q8_append_kernel(const __gri
                     }
             }
             uint4* to = reinterpret_cast<uint4*>(p.bounds + at * 2 * D + me * 16);
-            if (earlier) {
-                const uint4 old[2] = {to[0], to[D / 16]};
-                const uint32_t o[2][4] = {{old[0].x, old[0].y, old[0].z, old[0].w}, {old[1].x, old[1].y, old[1].z, old[1].w}};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t w[2] = {o[0][i], o[1][i]};
-                    if (grown) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            w[e] = 0;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                w[e] |= static_cast<uint32_t>(q8_again(q8_byte(o[e][i], j), was, scale, inv) & 255) << (8 * j);
-                        }
-                    }
-                    lo[i] = __vmins4(lo[i], w[0]);
-                    hi[i] = __vmaxs4(hi[i], w[1]);
-                }
-            }
             to[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             to[D / 16] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         }

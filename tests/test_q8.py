@@ -176,17 +176,13 @@ class Cache:
                         was = scale[p, h] if old else np.float32(0)
                         now = max(scale_of(rows), was)
                         c = codes_of(rows, now)
-                        ends = None if old else (np.full(self.D, 127), np.full(self.D, -127))
                         if now > was and old:
                             cache[p, :old, h] = codes_of(cache[p, :old, h].astype(np.float64) * np.float64(was), now)
-                        if cache is self.kc and bounds:
-                            if old:
-                                ends = self.bounds[p, h]
-                                if now > was:
-                                    ends = codes_of(ends.astype(np.float64) * np.float64(was), now)
-                            self.bounds[p, h] = np.minimum(ends[0], c.min(0)), np.maximum(ends[1], c.max(0))
                         cache[p, old: old + len(c), h] = c
                         scale[p, h] = now
+                        if cache is self.kc and bounds:
+                            every = cache[p, : old + len(c), h]
+                            self.bounds[p, h] = every.min(0), every.max(0)
 
     def rows(self, b, ids, h):
         p, r = self.table[b, ids // self.BLOCK], ids % self.BLOCK
