@@ -7,9 +7,9 @@
 // sum, values) in the workspace, and the last CTA to finish one joins them.
 //
 // Tiles: a warp streams its own tiles through a ring of shared memory with
-// 8- and 16-byte asynchronous copies.  Each lane copies exactly the bytes that it
-// will use as matrix fragments and reads back only its own, so that the ring
-// needs no barrier and no bank is hit twice:
+// 16-byte asynchronous copies, whole lines of 128 bytes together (copies in the
+// order of the fragments, four lines of 32 bytes at once, took up the L1's tags:
+// @), swizzled so that the reads meet no bank twice:
 //   S^T = K Q^T:   lane (g, t) has rows g and g + 8 of K, D / 4 channels in runs
 //                  of 16; the channels' order is the same in Q's fragments;
 //   O^T += V^T P^T: lane (g, t) has tokens 2t, 2t + 1, 2t + 8, 2t + 9 of V,
@@ -65,11 +65,6 @@ struct DecodeParams {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src)
@@ -181,6 +176,24 @@ __global__ void __launch_bounds__(kDecodeThreads, Shape<D, NT, QP>::kCtas) pa_q8
     grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * S * kStage);
+    // a copy takes kRowsCopy rows of D bytes, 16 bytes a lane, whole lines together;
+    // the places of the 16-byte runs (and, at D = 64, the order of V's rows) are such
+    // that the reads below meet no bank twice
+    constexpr int kRuns = D / 16, kRowsCopy = 32 / kRuns, kCopies = kTile / kRowsCopy;
+    const int copy_run = lane % kRuns;
+    const int copy_row = D == 128 ? lane / kRuns : (lane >> 2 & 3) * 2 + (lane >> 4);
+    uint32_t copy_k, copy_v, read_k, read_v;
+    if constexpr (D == 128) {
+        copy_k = copy_row * 128 + (copy_run ^ (copy_row & 1) << 2) * 16;
+        copy_v = copy_row * 128 + (copy_run ^ (copy_row >> 1 & 1) << 1) * 16;  // rows 4, 5 (mod 8) and on: ^ 64, see issue()
+        read_k = g * 128 + (t ^ (g & 1) << 2) * 16;
+        read_v = 2 * t * 128 + (g ^ t << 1) * 16;
+    } else {
+        copy_k = copy_row * 64 + copy_run * 16;
+        copy_v = (lane >> 2) * 64 + (copy_run ^ (lane >> 3 & 1) << 1) * 16;
+        read_k = g * 64 + t * 16;
+        read_v = t * 64 + (g ^ (t >> 1) << 2) * 8;
+    }
     float* merge = reinterpret_cast<float*>(smem);
     uint2* sm_q = reinterpret_cast<uint2*>(smem + Sh::kBody);  // [QP][step][group of rows][lane]
     int* prefix = reinterpret_cast<int*>(smem + Sh::kBody + Sh::kQueryBytes);
@@ -273,8 +286,8 @@ __global__ void __launch_bounds__(kDecodeThreads, Shape<D, NT, QP>::kCtas) pa_q8
 
         // ---- copies: block numbers are looked up one tile ahead, selected ones two
         const uint32_t step = static_cast<uint32_t>(p.KV) * D;
-        const int8_t* pk = p.k + static_cast<int64_t>(kh) * D + g * step + t * 16;
-        const int8_t* pv = p.v + static_cast<int64_t>(kh) * D + 2 * t * step + g * (D / 8);
+        const int8_t* pk = p.k + static_cast<int64_t>(kh) * D + copy_row * step + copy_run * 16;
+        const int8_t* pv = p.v + static_cast<int64_t>(kh) * D + copy_row * step + copy_run * 16;
         const float* psc = (lane ? p.vs : p.ks) + kh;
         int blk[HB], blk_next[HB], phys[HB];
         auto look_selected = [&](int tile) {  // logical blocks of a tile (-1: none)
@@ -321,23 +334,13 @@ __global__ void __launch_bounds__(kDecodeThreads, Shape<D, NT, QP>::kCtas) pa_q8
                     if (lane == 2)
                         asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + kTileBytes + 16 + 4 * x), "r"(place[x]) : "memory");
                 }
-                const uint32_t sv = st + kTile * D;
+                const uint64_t at = static_cast<uint64_t>(row[0]) * step;
+                const uint64_t second = HB == 2 ? static_cast<uint64_t>(row[HB - 1]) * step - kRowsCopy * (kCopies / 2) * step : at;
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint32_t r = HB == 2 ? row[x & (HB - 1)] : row[0] + 8 * x;
-                    const uint64_t at = static_cast<uint64_t>(r) * step;
-                    const int8_t* k = pk + at;
-                    const int8_t* v = pv + at;
-#pragma unroll
-                    for (int ch = 0; ch < kChunks; ++ch)
-                        copy16(st + ((x * kChunks + ch) * 32 + lane) * 16, k + ch * 64);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if constexpr (D == 128)
-                            copy16(sv + ((x * 2 + i) * 32 + lane) * 16, v + i * step);
-                        else
-                            copy8(sv + ((x * 2 + i) * 32 + lane) * 8, v + i * step);
-                    }
+                for (int i = 0; i < kCopies; ++i) {
+                    const uint64_t from = (HB == 2 && i >= kCopies / 2 ? second : at) + static_cast<uint64_t>(i * kRowsCopy) * step;
+                    copy16(st + i * 512 + copy_k, pk + from);
+                    copy16(st + kTile * D + i * 512 + (D == 128 && i & 1 ? copy_v ^ 64 : copy_v), pv + from);
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -483,7 +486,7 @@ __global__ void __launch_bounds__(kDecodeThreads, Shape<D, NT, QP>::kCtas) pa_q8
                     sacc[nt][i] = 0.f;
 #pragma unroll
             for (int ch = 0; ch < kChunks; ++ch) {
-                const uint4 ka = lds16(st + (ch * 32 + lane) * 16), kb = lds16(st + ((kChunks + ch) * 32 + lane) * 16);
+                const uint4 ka = lds16(st + (read_k ^ ch * 64)), kb = lds16(st + 8 * D + (read_k ^ ch * 64));
                 const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -576,10 +579,10 @@ __global__ void __launch_bounds__(kDecodeThreads, Shape<D, NT, QP>::kCtas) pa_q8
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if constexpr (D == 128) {
-                    const uint4 v = lds16(sv + (i * 32 + lane) * 16);
+                    const uint4 v = lds16(sv + (i >> 1) * 8 * D + (i & 1) * 128 + read_v);
                     vw[i][0] = v.x, vw[i][1] = v.y, vw[i][2] = v.z, vw[i][3] = v.w;
                 } else {
-                    const uint2 v = lds8(sv + (i * 32 + lane) * 8);
+                    const uint2 v = lds8(sv + (i >> 1) * 8 * D + (i & 1) * 256 + read_v);
                     vw[i][0] = v.x, vw[i][1] = v.y;
                 }
             }
