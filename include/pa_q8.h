@@ -162,7 +162,7 @@ int pa_q8_select(const void *q, const int8_t *bounds, const float *k_scale,
  * pa_q8_workspace_zero_bytes() bytes zero before the first use, and every
  * call that completes leaves them zero.  Calls that may overlap on the GPU
  * need workspaces of their own.  Limits: NQ <= PA_MAX_NQ, H / KV * NQ <= 1024;
- * with `selected` B * KV <= 8192.
+ * with `selected` B * KV <= 4096.
  */
 typedef struct pa_q8_opts {
     int max_blocks, num_blocks, dtype;

@@ -34,12 +34,10 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kDecodeThreads = kWarps * 32;
 constexpr int kTile = 16;                 // tokens of a tile
-constexpr int kUnit = kWarps;             // tiles of a unit
-constexpr int kMaxEntries = 8192;         // prefix sums in shared memory
-constexpr int kMaxCtas = 304;             // two per SM
+constexpr int kMaxEntries = 4096;         // prefix sums in shared memory
+constexpr int kMaxCtas = 160;             // one per SM
+constexpr int kCharge = 12;               // tiles that a piece's start and end count for
 constexpr int kMeta = 32;                 // bytes of a tile's scales and places
 constexpr float kLift = 6.f, kSlack = 8.f;  // weights are 2^(t - m + 6), t - m <= 8
 
@@ -59,7 +57,7 @@ struct DecodeParams {
     float* part_o;     // [CTA][2][8 NT][D]
     int* status;
     float scale;       // scale * log2(e)
-    int B, H, KV, R, NQ, groups, shift, maxb, num_blocks, cap, budget, causal, dtype, entries;
+    int B, H, KV, R, NQ, groups, shift, maxb, num_blocks, cap, budget, causal, dtype, entries, team;
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src)
@@ -121,14 +119,17 @@ __device__ __forceinline__ float fast_rcp(float x)
 template <int D, int NT, int QP>
 struct Shape {
     static constexpr int kRows = 8 * NT, kSteps = D / 16;
+    static constexpr int kWarps = NT == 1 && QP == 1 ? 12 : 8, kThreads = kWarps * 32;
     static constexpr int kTileBytes = 2 * kTile * D, kStage = kTileBytes + kMeta;
-    static constexpr int kCtas = NT == 1 && QP == 1 ? 2 : 1;
-    static constexpr bool kQueryShared = NT == 4;
-    static constexpr int kQueryBytes = kQueryShared ? QP * kSteps * NT * 32 * 8 : 0;
-    static constexpr int kStages = kCtas == 2 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+    static constexpr int kStages = (kWarps == 12 ? 4 : 5) * (D == 128 ? 1 : 2);
     static constexpr int kRing = kWarps * kStages * kStage;
-    static constexpr int kMerge = kWarps * kRows * D * 4, kPieces = kMaxCtas * kRows * 8;
-    static constexpr int kBody = kRing > kMerge ? (kRing > kPieces ? kRing : kPieces) : (kMerge > kPieces ? kMerge : kPieces);
+    // a warp's state in shared memory: steps of 16 + 4 floats, rows 4 (mod 32) floats
+    // apart, so that neither its writes nor its reads meet a bank twice
+    static constexpr int kStateStep = 20, kStateRow = kSteps * kStateStep + 4;
+    static constexpr int kMerge = kWarps * kRows * kStateRow * 4;
+    static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
+    static constexpr bool kQueryShared = NT == 4;
+    static constexpr int kQueryBytes = QP * kSteps * NT * 32 * 8;
 };
 
 template <typename T>
@@ -163,14 +164,17 @@ __device__ __forceinline__ void fma4(float4& a, float f, float4 v)
 }
 
 template <int D, int NT, int QP, int HB>
-__global__ void __launch_bounds__(kDecodeThreads, Shape<D, NT, QP>::kCtas) pa_q8_decode_kernel(const __grid_constant__ DecodeParams p)
+__global__ void __launch_bounds__(Shape<D, NT, QP>::kThreads, 1) pa_q8_decode_kernel(const __grid_constant__ DecodeParams p)
 {
     using Sh = Shape<D, NT, QP>;
     constexpr int kRows = Sh::kRows, kSteps = Sh::kSteps, kTileBytes = Sh::kTileBytes, kStage = Sh::kStage, S = Sh::kStages;
+    constexpr int kWarps = Sh::kWarps, kThreads = Sh::kThreads;
     constexpr int kChunks = D / 64;  // 16-byte runs of a key row per lane
     constexpr bool kQs = Sh::kQueryShared;
-    extern __shared__ __align__(16) unsigned char smem[];  // states or ring | query fragments | prefix sums
+    extern __shared__ __align__(16) unsigned char smem[];  // ring, then states | query fragments | prefix sums
     __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
+    __shared__ float sm_f[kRows];  // of a row's scores: scale * log2(e) / the power of two
+    __shared__ int sm_lim[kRows];  // keys that the row sees
     __shared__ int sm_last;
     grid_dependents_launch();
     grid_dependency_wait();
@@ -185,7 +189,7 @@ __global__ void __launch_bounds__(kDecodeThreads, Shape<D, NT, QP>::kCtas) pa_q8
     uint32_t copy_k, copy_v, read_k, read_v;
     if constexpr (D == 128) {
         copy_k = copy_row * 128 + (copy_run ^ (copy_row & 1) << 2) * 16;
-        copy_v = copy_row * 128 + (copy_run ^ (copy_row >> 1 & 1) << 1) * 16;  // rows 4, 5 (mod 8) and on: ^ 64, see issue()
+        copy_v = copy_row * 128 + (copy_run ^ (copy_row >> 1 & 1) << 1) * 16;  // (rows 4 to 7 of 8: ^ 64)
         read_k = g * 128 + (t ^ (g & 1) << 2) * 16;
         read_v = 2 * t * 128 + (g ^ t << 1) * 16;
     } else {
@@ -194,16 +198,15 @@ __global__ void __launch_bounds__(kDecodeThreads, Shape<D, NT, QP>::kCtas) pa_q8
         read_k = g * 64 + t * 16;
         read_v = t * 64 + (g ^ (t >> 1) << 2) * 8;
     }
-    float* merge = reinterpret_cast<float*>(smem);
+    float* state = reinterpret_cast<float*>(smem);             // [warp][row] in steps
     uint2* sm_q = reinterpret_cast<uint2*>(smem + Sh::kBody);  // [QP][step][group of rows][lane]
     int* prefix = reinterpret_cast<int*>(smem + Sh::kBody + Sh::kQueryBytes);
 
-    // prefix sums of the units of the entries (sequences, or sequences and KV
-    // heads where each has its own blocks); `copies` segments share an entry's length
-    const int copies = p.selected ? p.groups : p.KV * p.groups;
+    // prefix sums of the tiles of the entries (sequences, or sequences and KV
+    // heads where each has its own blocks), each with the charge of a piece
     {
         int* sums = reinterpret_cast<int*>(&sm_m[0][0]);
-        const int per = (p.entries + kDecodeThreads - 1) / kDecodeThreads;
+        const int per = (p.entries + kThreads - 1) / kThreads;
         const int e0 = min(tid * per, p.entries), e1 = min(e0 + per, p.entries);
         int sum = 0;
         for (int e = e0; e < e1; ++e) {
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(kDecodeThreads, Shape<D, NT, QP>::kCtas) pa_q8
                     q8_report(p.status, PA_STATUS_BAD_LENGTH);
                 tokens = min(max(n, 0), p.cap);
             }
-            const int u = max(1, (tokens + kTile * kUnit - 1) / (kTile * kUnit));
+            const int u = kCharge + max(1, (tokens + kTile - 1) / kTile);
             prefix[e] = u;
             sum += u;
         }
@@ -241,19 +244,23 @@ __global__ void __launch_bounds__(kDecodeThreads, Shape<D, NT, QP>::kCtas) pa_q8
             prefix[e] = at;
             at += u;
         }
-        if (tid == kDecodeThreads - 1)
+        if (tid == kThreads - 1)
             prefix[p.entries] = at;
         __syncthreads();
     }
+    // Teams of p.team CTAs walk the same tokens of neighbouring KV heads (or of
+    // groups of rows of one head); `copies` segments of a team share an entry's length.
+    const int copies = (p.selected ? p.groups : p.KV * p.groups) / p.team;
+    const int team = blockIdx.x / p.team, member = blockIdx.x % p.team;
     const int64_t U = static_cast<int64_t>(prefix[p.entries]) * copies;
-    const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x), U));
-    if (static_cast<int>(blockIdx.x) >= G)
+    const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x / p.team), (U + kCharge + kWarps - 1) / (kCharge + kWarps)));
+    if (team >= G)
         return;
-    const int64_t u_end = (static_cast<int64_t>(blockIdx.x) + 1) * U / G;
-    const int64_t u_begin = static_cast<int64_t>(blockIdx.x) * U / G;
+    const int64_t u_end = (static_cast<int64_t>(team) + 1) * U / G;
+    const int64_t u_begin = static_cast<int64_t>(team) * U / G;
 
     for (int64_t u = u_begin; u < u_end;) {
-        // the segment of unit u: entry e, copy c of it
+        // the segment of tile u: entry e, copy c of it
         int e = 0;
         {
             int hi = p.entries;
@@ -265,127 +272,124 @@ __global__ void __launch_bounds__(kDecodeThreads, Shape<D, NT, QP>::kCtas) pa_q8
                     hi = mid;
             }
         }
-        const int units = prefix[e + 1] - prefix[e];
-        const int c = static_cast<int>((u - static_cast<int64_t>(prefix[e]) * copies) / units);
-        const int64_t s_begin = static_cast<int64_t>(prefix[e]) * copies + static_cast<int64_t>(c) * units, s_end = s_begin + units;
-        const int64_t stop = min(s_end, u_end);
+        const int length = prefix[e + 1] - prefix[e];
+        const int cc = static_cast<int>((u - static_cast<int64_t>(prefix[e]) * copies) / length);
+        const int64_t s_end = static_cast<int64_t>(prefix[e]) * copies + static_cast<int64_t>(cc + 1) * length;
+        const int64_t s_begin = s_end - length + kCharge;  // its first tile, behind the charge
+        const int64_t from = max(u, s_begin), stop = min(s_end, u_end);
+        if (stop <= s_begin)
+            break;  // only of the charge: the next CTAs have the tiles
+        const int c = cc * p.team + member;
         const int b = p.selected ? e / p.KV : e;
         const int kh = p.selected ? e % p.KV : c / p.groups;
         const int grp = p.selected ? c : c % p.groups;
-        const int64_t segment = (static_cast<int64_t>(b) * p.KV + kh) * p.groups + grp;
+        const int row_base = grp * kRows;
+
+        // ---- query rows: one warp a group of eight
+        float x[kSteps * 4];
+        if (warp < NT) {
+            const int row = row_base + warp * 8 + g;
+#pragma unroll
+            for (int ch = 0; ch < kChunks; ++ch) {
+                const int64_t at = ((static_cast<int64_t>(b) * p.KV + kh) * p.R + row) * D + ch * 64 + t * 16;
+                if (row >= p.R) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        x[ch * 16 + i] = 0.f;
+                } else if (p.dtype == PA_F32) {
+                    q8_load16(x + ch * 16, static_cast<const float*>(p.q) + at);
+                } else if (p.dtype == PA_F16) {
+                    q8_load16(x + ch * 16, static_cast<const __half*>(p.q) + at);
+                } else {
+                    q8_load16(x + ch * 16, static_cast<const __nv_bfloat16*>(p.q) + at);
+                }
+            }
+        }
         const int n = min(max(__ldg(p.lens + b), 0), p.cap);
         const int32_t* sel = p.selected ? p.selected + static_cast<int64_t>(e) * p.budget : nullptr;
         const int nsel = p.selected ? min(max(__ldg(p.counts + e), 0), p.budget) : 0;
         const int tokens = p.selected ? nsel << p.shift : n;  // places in the list of blocks
         const int nb = (n + (1 << p.shift) - 1) >> p.shift;
         const int32_t* table = p.table + static_cast<int64_t>(b) * p.maxb;
-        // this warp's tiles: first, first + 8, ... below last
-        const int first = static_cast<int>(u - s_begin) * kUnit + warp;
-        const int last = min(static_cast<int>(stop - s_begin) * kUnit, (tokens + kTile - 1) / kTile);
-        const int row_base = grp * kRows;
+        // this warp's tiles: first, first + kWarps, ... below last
+        const int first = static_cast<int>(from - s_begin) + warp;
+        const int last = min(static_cast<int>(stop - s_begin), (tokens + kTile - 1) / kTile);
 
-        // ---- copies: block numbers are looked up one tile ahead, selected ones two
+        // ---- copies.  The lanes look up the blocks of the warp's next 32 tiles (16
+        // where a tile touches two) together.
+        constexpr int kWindow = 32 / HB;
         const uint32_t step = static_cast<uint32_t>(p.KV) * D;
         const int8_t* pk = p.k + static_cast<int64_t>(kh) * D + copy_row * step + copy_run * 16;
         const int8_t* pv = p.v + static_cast<int64_t>(kh) * D + copy_row * step + copy_run * 16;
         const float* psc = (lane ? p.vs : p.ks) + kh;
-        int blk[HB], blk_next[HB], phys[HB];
-        auto look_selected = [&](int tile) {  // logical blocks of a tile (-1: none)
-#pragma unroll
-            for (int x = 0; x < HB; ++x) {
-                const int place = tile * kTile + 8 * x;
-                int j = -1;
-                if (tile < last && place < tokens) {
-                    j = place >> p.shift;
-                    if (sel)
-                        j = __ldg(sel + j);
+        int blk, phys, blk_next = -1, phys_next = -1;
+        auto look_up = [&](int window, int& bl, int& ph) {
+            const int tile = first + (window * kWindow + lane / HB) * kWarps;
+            const int place = tile * kTile + 8 * (lane % HB);
+            int j = -1;
+            if (tile < last && place < tokens) {
+                j = place >> p.shift;
+                if (sel) {
+                    j = __ldg(sel + j);
+                    if (j < 0 || j >= nb) {
+                        if (j != -1)
+                            q8_report(p.status, PA_STATUS_BAD_BLOCK);
+                        j = -1;
+                    }
                 }
-                blk_next[x] = j;
             }
+            bl = j;
+            ph = j >= 0 ? __ldg(table + j) : -1;
         };
-        auto look_table = [&]() {
-#pragma unroll
-            for (int x = 0; x < HB; ++x) {
-                blk[x] = blk_next[x];
-                if (sel && (blk[x] < 0 || blk[x] >= nb)) {
-                    if (blk[x] != -1)
-                        q8_report(p.status, PA_STATUS_BAD_BLOCK);
-                    blk[x] = -1;
-                }
-                phys[x] = blk[x] >= 0 ? __ldg(table + blk[x]) : -1;
-            }
-        };
-        auto issue = [&](int tile, uint32_t st) {
+        auto issue = [&](int k, uint32_t st) {  // the warp's k-th tile
+            const int tile = first + k * kWarps;
             if (tile < last) {
+                const int at_window = k & (kWindow - 1);
+                if (at_window == 0 && k > 0) {
+                    blk = blk_next;
+                    phys = phys_next;
+                }
+                if (at_window == kWindow / 2)
+                    look_up(k / kWindow + 1, blk_next, phys_next);
                 const int in_block = HB == 2 ? 0 : (tile * kTile) & ((1 << p.shift) - 1);
                 uint32_t row[HB];
-                int place[HB];
 #pragma unroll
                 for (int x = 0; x < HB; ++x) {
-                    const bool there = static_cast<uint32_t>(phys[x]) < static_cast<uint32_t>(p.num_blocks);
-                    if (!there && blk[x] >= 0)
+                    const int bl = __shfl_sync(kFullWarp, blk, at_window * HB + x), phy = __shfl_sync(kFullWarp, phys, at_window * HB + x);
+                    const bool there = static_cast<uint32_t>(phy) < static_cast<uint32_t>(p.num_blocks);
+                    if (!there && bl >= 0)
                         q8_report(p.status, PA_STATUS_BAD_BLOCK);
                     // (without a block: the first rows of the pool are read in its place, and hidden)
-                    const uint32_t ph = there ? static_cast<uint32_t>(phys[x]) : 0u;
-                    place[x] = there ? (blk[x] << p.shift) + in_block : INT_MAX - 64;
+                    const uint32_t ph = there ? static_cast<uint32_t>(phy) : 0u;
+                    const int place = there ? (bl << p.shift) + in_block : INT_MAX - 64;
                     row[x] = (ph << p.shift) + static_cast<uint32_t>(in_block);
                     if (lane < 2)
                         copy4(st + kTileBytes + x * 8 + lane * 4, psc + static_cast<uint64_t>(ph) * p.KV);
                     if (lane == 2)
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + kTileBytes + 16 + 4 * x), "r"(place[x]) : "memory");
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + kTileBytes + 16 + 4 * x), "r"(place) : "memory");
                 }
                 const uint64_t at = static_cast<uint64_t>(row[0]) * step;
                 const uint64_t second = HB == 2 ? static_cast<uint64_t>(row[HB - 1]) * step - kRowsCopy * (kCopies / 2) * step : at;
 #pragma unroll
                 for (int i = 0; i < kCopies; ++i) {
-                    const uint64_t from = (HB == 2 && i >= kCopies / 2 ? second : at) + static_cast<uint64_t>(i * kRowsCopy) * step;
-                    copy16(st + i * 512 + copy_k, pk + from);
-                    copy16(st + kTile * D + i * 512 + (D == 128 && i & 1 ? copy_v ^ 64 : copy_v), pv + from);
+                    const uint64_t off = (HB == 2 && i >= kCopies / 2 ? second : at) + static_cast<uint64_t>(i * kRowsCopy) * step;
+                    copy16(st + i * 512 + copy_k, pk + off);
+                    copy16(st + kTile * D + i * 512 + (D == 128 && i & 1 ? copy_v ^ 64 : copy_v), pv + off);
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        look_selected(first);
-        look_table();
-        look_selected(first + kUnit);
+        look_up(0, blk, phys);
 #pragma unroll
-        for (int i = 0; i < S - 1; ++i) {
-            issue(first + i * kUnit, ring + i * kStage);
-            look_table();
-            look_selected(first + (i + 2) * kUnit);
-        }
+        for (int i = 0; i < S - 1; ++i)
+            issue(i, ring + i * kStage);
 
-        // ---- query rows: fragments of B, scaled by a power of two
-        uint32_t qf[kQs ? 1 : QP][kQs ? 1 : NT][kQs ? 1 : kSteps][2];
-        float rowf[NT][2];   // of this lane's two score columns: scale * log2(e) / the power of two
-        int lim[NT][2];      // keys that the column's row sees
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int row = row_base + nt * 8 + g;
-            float x[kSteps * 4];
+        // ---- query rows as fragments of B, scaled by a power of two
+        if (warp < NT) {
             float a = 0.f;
 #pragma unroll
-            for (int ch = 0; ch < kChunks; ++ch) {
-                float y[16];
-                if (row < p.R) {
-                    const int64_t at = (static_cast<int64_t>(b) * p.KV + kh) * p.R * D + static_cast<int64_t>(row) * D + ch * 64 + t * 16;
-                    if (p.dtype == PA_F32)
-                        q8_load16(y, static_cast<const float*>(p.q) + at);
-                    else if (p.dtype == PA_F16)
-                        q8_load16(y, static_cast<const __half*>(p.q) + at);
-                    else
-                        q8_load16(y, static_cast<const __nv_bfloat16*>(p.q) + at);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        y[i] = 0.f;
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    x[ch * 16 + i] = y[i];
-                    a = q8_amax(a, y[i]);
-                }
-            }
+            for (int i = 0; i < kSteps * 4; ++i)
+                a = q8_amax(a, x[i]);
             a = fmaxf(a, __shfl_xor_sync(kFullWarp, a, 1));
             a = fmaxf(a, __shfl_xor_sync(kFullWarp, a, 2));
             // 2^up brings the largest magnitude into [2^11, 2^12)
@@ -394,7 +398,11 @@ __global__ void __launch_bounds__(kDecodeThreads, Shape<D, NT, QP>::kCtas) pa_q8
             const float f2 = __uint_as_float(static_cast<uint32_t>(127 + up - up / 2) << 23);
             const float d1 = __uint_as_float(static_cast<uint32_t>(127 - up / 2) << 23);
             const float d2 = __uint_as_float(static_cast<uint32_t>(127 - (up - up / 2)) << 23);
-            const float factor = p.scale * d1 * d2;
+            if (t == 0) {
+                const int r = row_base + warp * 8 + g;
+                sm_f[warp * 8 + g] = p.scale * d1 * d2;
+                sm_lim[warp * 8 + g] = r >= p.R ? 0 : p.causal ? min(n, n - p.NQ + r % p.NQ + 1) : n;
+            }
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 uint32_t w[QP][2];
@@ -409,25 +417,30 @@ __global__ void __launch_bounds__(kDecodeThreads, Shape<D, NT, QP>::kCtas) pa_q8
                     }
                 }
 #pragma unroll
-                for (int q = 0; q < QP; ++q) {
-                    if constexpr (kQs) {
-                        if (warp == nt)  // one warp a group of rows
-                            sm_q[((q * kSteps + s) * NT + nt) * 32 + lane] = make_uint2(w[q][0], w[q][1]);
-                    } else {
-                        qf[q][nt][s][0] = w[q][0];
-                        qf[q][nt][s][1] = w[q][1];
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                rowf[nt][i] = __shfl_sync(kFullWarp, factor, (2 * t + i) * 4);
-                const int r = row_base + nt * 8 + 2 * t + i;
-                lim[nt][i] = r >= p.R ? 0 : p.causal ? min(n, n - p.NQ + r % p.NQ + 1) : n;
+                for (int q = 0; q < QP; ++q)
+                    sm_q[((q * kSteps + s) * NT + warp) * 32 + lane] = make_uint2(w[q][0], w[q][1]);
             }
         }
-        if constexpr (kQs)
-            __syncthreads();
+        __syncthreads();
+        uint32_t qf[kQs ? 1 : QP][kQs ? 1 : NT][kQs ? 1 : kSteps][2];
+        if constexpr (!kQs) {
+#pragma unroll
+            for (int q = 0; q < QP; ++q)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) {
+                        const uint2 w = sm_q[((q * kSteps + s) * NT + nt) * 32 + lane];
+                        qf[q][nt][s][0] = w.x;
+                        qf[q][nt][s][1] = w.y;
+                    }
+        }
+        float rowf[NT][2];  // of this lane's two score columns
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                rowf[nt][i] = sm_f[nt * 8 + 2 * t + i];
         // every row sees the keys below
         const int all_see = row_base + kRows > p.R ? INT_MIN : (p.causal ? n - p.NQ + 1 : n) - 8 * (3 - HB);
 
@@ -448,15 +461,11 @@ __global__ void __launch_bounds__(kDecodeThreads, Shape<D, NT, QP>::kCtas) pa_q8
         }
 
         uint32_t st = ring, fill = ring + (S - 1) * kStage;
-        for (int tile = first; tile < last; tile += kUnit) {
+        int ahead = S - 1;
+        for (int tile = first; tile < last; tile += kWarps) {
             asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");  // this tile's
-            __syncwarp();  // scales and places come from other lanes; the stage filled next has been read
-            {
-                const int ahead = tile + (S - 1) * kUnit;
-                issue(ahead, fill);
-                look_table();
-                look_selected(ahead + 2 * kUnit);
-            }
+            __syncwarp();  // the copies of the other lanes; the stage filled next has been read
+            issue(ahead++, fill);
             float ks[HB], lv[HB], iv[HB];
             int place[2];
             if constexpr (HB == 2) {
@@ -516,7 +525,7 @@ __global__ void __launch_bounds__(kDecodeThreads, Shape<D, NT, QP>::kCtas) pa_q8
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (place[i >> 1] + g >= lim[nt][i & 1])
+                        if (place[i >> 1] + g >= sm_lim[nt * 8 + 2 * t + (i & 1)])
                             sacc[nt][i] = -INFINITY;
             }
             bool raise = false;
@@ -626,29 +635,28 @@ __global__ void __launch_bounds__(kDecodeThreads, Shape<D, NT, QP>::kCtas) pa_q8
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
+                const int row = nt * 8 + 2 * t + i;
                 float s = l[nt][i];
                 s += __shfl_xor_sync(kFullWarp, s, 4);
                 s += __shfl_xor_sync(kFullWarp, s, 8);
                 s += __shfl_xor_sync(kFullWarp, s, 16);
                 if (g == 0) {
-                    sm_m[warp][nt * 8 + 2 * t + i] = mx[nt][i];
-                    sm_l[warp][nt * 8 + 2 * t + i] = s;
+                    sm_m[warp][row] = mx[nt][i];
+                    sm_l[warp][row] = s;
                 }
+                float* to = state + (warp * kRows + row) * Sh::kStateRow + 2 * g;
 #pragma unroll
-                for (int s2 = 0; s2 < kSteps; ++s2) {
-                    // step s2 = 2 w + x: channels D / 8 g + 4 w + 2 x, + 1
-                    float2 two = make_float2(o[s2][nt][i], o[s2][nt][i + 2]);
-                    *reinterpret_cast<float2*>(merge + (static_cast<size_t>(warp) * kRows + nt * 8 + 2 * t + i) * D + g * (D / 8) + 2 * s2) = two;
-                }
+                for (int s2 = 0; s2 < kSteps; ++s2)  // channels D / 8 g + 2 s2, + 1
+                    *reinterpret_cast<float2*>(to + s2 * Sh::kStateStep) = make_float2(o[s2][nt][i], o[s2][nt][i + 2]);
             }
         __syncthreads();
-        const bool whole = u == s_begin && stop == s_end;
-        const int slot = u == u_begin && u != s_begin ? 0 : 1;  // a piece of a segment begun earlier, or one that goes on
-        const int64_t record = static_cast<int64_t>(blockIdx.x) * 2 + slot;
+        const bool whole = from == s_begin && stop == s_end;
+        // a piece of a segment begun by an earlier CTA, or one that goes on
+        const int64_t record = static_cast<int64_t>(blockIdx.x) * 2 + (u_begin > s_begin ? 0 : 1);
         const int64_t out0 = ((static_cast<int64_t>(b) * p.KV + kh) * p.R + row_base) * D;
-        constexpr int kItems = kRows * D / 4;
-        for (int x = tid; x < kItems; x += kDecodeThreads) {
-            const int row = x / (D / 4), d = x % (D / 4) * 4;
+        constexpr int kQuads = D / 4, kItems = kRows * kQuads;  // four channels each
+        for (int x = tid; x < kItems; x += kThreads) {
+            const int row = x / kQuads, quad = x % kQuads;
             if (row_base + row >= p.R)
                 break;
             float m = -INFINITY;
@@ -657,76 +665,81 @@ __global__ void __launch_bounds__(kDecodeThreads, Shape<D, NT, QP>::kCtas) pa_q8
                 m = fmaxf(m, sm_m[w][row]);
             float sum = 0.f;
             float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float* at = state + row * Sh::kStateRow + quad / (D / 32) * 2 + quad % (D / 32) * 2 * Sh::kStateStep;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float f = sm_m[w][row] == -INFINITY ? 0.f : fast_exp2(sm_m[w][row] - m);
                 sum = fmaf(sm_l[w][row], f, sum);
-                fma4(val, f, *reinterpret_cast<const float4*>(merge + (static_cast<size_t>(w) * kRows + row) * D + d));
+                const float2 v0 = *reinterpret_cast<const float2*>(at + w * kRows * Sh::kStateRow);
+                const float2 v1 = *reinterpret_cast<const float2*>(at + w * kRows * Sh::kStateRow + Sh::kStateStep);
+                fma4(val, f, make_float4(v0.x, v0.y, v1.x, v1.y));
             }
             if (whole) {
                 const float r = sum == 0.f ? 0.f : 1.f / sum;
-                store_out(p, out0 + static_cast<int64_t>(row) * D + d, make_float4(val.x * r, val.y * r, val.z * r, val.w * r));
+                store_out(p, out0 + static_cast<int64_t>(x) * 4, make_float4(val.x * r, val.y * r, val.z * r, val.w * r));
             } else {
-                *reinterpret_cast<float4*>(p.part_o + (record * kRows + row) * D + d) = val;
-                if (d == 0)
+                *reinterpret_cast<float4*>(p.part_o + record * kRows * D + x * 4) = val;
+                if (quad == 0)
                     p.part_ml[record * kRows + row] = make_float2(m, sum);
             }
         }
         if (!whole) {
-            // pieces of the segment: those of CTAs c0 .. c1
+            // pieces of the segment: those of teams c0 .. c1
             const int c0 = static_cast<int>(((s_begin + 1) * G - 1) / U), c1 = static_cast<int>((s_end * G - 1) / U);
-            __threadfence();
             __syncthreads();
             if (tid == 0) {
-                const int before = atomicAdd(p.counters + segment, 1);
+                int* counter = p.counters + (static_cast<int64_t>(b) * p.KV + kh) * p.groups + grp;
+                __threadfence();
+                const int before = atomicAdd(counter, 1);
                 sm_last = before == c1 - c0;
                 if (before == c1 - c0)
-                    p.counters[segment] = 0;
+                    *counter = 0;
+                __threadfence();
             }
             __syncthreads();
             if (sm_last) {
-                __threadfence();
+                // a row to each set of D / 4 lanes; their lanes hold the pieces' factors
                 const int pieces = c1 - c0 + 1;
-                // the first CTA's range begins with this segment or earlier, the others' inside it
-                const bool late = static_cast<int64_t>(c0) * U / G > s_begin;
-                auto record_of = [&](int i) { return static_cast<int64_t>(c0 + i) * 2 + (i > 0 || late ? 0 : 1); };
-                float2* ml = reinterpret_cast<float2*>(smem);  // [piece][row]: maximum, sum; then factor
-                for (int x = tid; x < pieces * kRows; x += kDecodeThreads)
-                    ml[x] = __ldcg(p.part_ml + record_of(x / kRows) * kRows + x % kRows);
-                __syncthreads();
-                for (int row = warp; row < kRows; row += kWarps) {
-                    if (row_base + row >= p.R)
-                        break;
+                // (the first team's range begins with the segment or earlier, the others' inside it)
+                auto record_of = [&](int i) { return (static_cast<int64_t>(c0 + i) * p.team + member) * 2 + (i > 0 ? 0 : 1); };
+                for (int x0 = warp * 32; x0 < kItems; x0 += kThreads) {
+                    const int x = x0 + lane, row = x / kQuads, in_row = lane % kQuads;
+                    const bool live = row_base + row < p.R;
                     float m = -INFINITY, sum = 0.f;
-                    for (int i = lane; i < pieces; i += 32)
-                        m = fmaxf(m, ml[i * kRows + row].x);
-#pragma unroll
-                    for (int k = 1; k < 32; k <<= 1)
-                        m = fmaxf(m, __shfl_xor_sync(kFullWarp, m, k));
-                    for (int i = lane; i < pieces; i += 32) {
-                        const float2 v = ml[i * kRows + row];
-                        const float f = v.x == -INFINITY ? 0.f : fast_exp2(v.x - m);
-                        ml[i * kRows + row].x = f;
-                        sum = fmaf(v.y, f, sum);
-                    }
-#pragma unroll
-                    for (int k = 1; k < 32; k <<= 1)
-                        sum += __shfl_xor_sync(kFullWarp, sum, k);
-                    if (lane == 0)
-                        sm_l[0][row] = sum == 0.f ? 0.f : 1.f / sum;
-                }
-                __syncthreads();
-                for (int x = tid; x < kItems; x += kDecodeThreads) {
-                    const int row = x / (D / 4), d = x % (D / 4) * 4;
-                    if (row_base + row >= p.R)
-                        break;
                     float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
-                    const float* from = p.part_o + static_cast<int64_t>(row) * D + d;
-#pragma unroll 8
-                    for (int i = 0; i < pieces; ++i)
-                        fma4(val, ml[i * kRows + row].x, __ldcg(reinterpret_cast<const float4*>(from + record_of(i) * kRows * D)));
-                    const float r = sm_l[0][row];
-                    store_out(p, out0 + static_cast<int64_t>(row) * D + d, make_float4(val.x * r, val.y * r, val.z * r, val.w * r));
+                    for (int i0 = 0; i0 < pieces; i0 += kQuads) {  // (one turn, mostly)
+                        const int many = min(kQuads, pieces - i0);
+                        float2 ml = make_float2(-INFINITY, 0.f);
+                        if (live && in_row < many)
+                            ml = __ldcg(p.part_ml + record_of(i0 + in_row) * kRows + row);
+                        float top = ml.x;
+#pragma unroll
+                        for (int k = 1; k < kQuads; k <<= 1)
+                            top = fmaxf(top, __shfl_xor_sync(kFullWarp, top, k));
+                        top = fmaxf(top, m);
+                        const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top), old = m == -INFINITY ? 0.f : fast_exp2(m - top);
+                        float part = ml.y * f;
+#pragma unroll
+                        for (int k = 1; k < kQuads; k <<= 1)
+                            part += __shfl_xor_sync(kFullWarp, part, k);
+                        sum = fmaf(sum, old, part);
+                        val.x *= old, val.y *= old, val.z *= old, val.w *= old;
+                        m = top;
+                        const float* src = p.part_o + x * 4;
+                        for (int i = 0; i < many; i += 8) {
+                            float4 v[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                v[k] = live && i + k < many ? __ldcg(reinterpret_cast<const float4*>(src + record_of(i0 + i + k) * kRows * D))
+                                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                fma4(val, __shfl_sync(kFullWarp, f, (lane & ~(kQuads - 1)) + ((i + k) & (kQuads - 1))), v[k]);
+                        }
+                    }
+                    const float r = sum == 0.f ? 0.f : 1.f / sum;
+                    if (live)
+                        store_out(p, out0 + static_cast<int64_t>(x) * 4, make_float4(val.x * r, val.y * r, val.z * r, val.w * r));
                 }
             }
         }
@@ -737,7 +750,7 @@ __global__ void __launch_bounds__(kDecodeThreads, Shape<D, NT, QP>::kCtas) pa_q8
 
 struct Variant {
     const void* fn;
-    int rows, ctas;
+    int rows, threads;
     size_t body;  // shared memory apart from the prefix sums
 };
 
@@ -747,7 +760,7 @@ Variant variant(int BLOCK)
     using Sh = Shape<D, NT, QP>;
     return {BLOCK == 8 ? reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 2>)
                        : reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 1>),
-            Sh::kRows, Sh::kCtas, static_cast<size_t>(Sh::kBody) + Sh::kQueryBytes};
+            Sh::kRows, Sh::kThreads, static_cast<size_t>(Sh::kBody) + Sh::kQueryBytes};
 }
 
 template <int D>
@@ -854,8 +867,8 @@ extern "C" int pa_q8_decode(const void* q, const int8_t* k_cache, const int8_t* 
     p.entries = o.selected ? B * KV : B;
     const long long copies = o.selected ? p.groups : static_cast<long long>(KV) * p.groups;
     const long long most = o.selected ? static_cast<long long>(o.budget) * BLOCK : static_cast<long long>(o.max_blocks) * BLOCK;
-    if (p.entries * ((most + kTile * kUnit - 1) / (kTile * kUnit)) * copies >= (1ll << 50) ||
-        p.entries * ((most + kTile * kUnit - 1) / (kTile * kUnit)) >= (1ll << 31))
+    const long long tiles = (most + kTile - 1) / kTile + kCharge;
+    if (p.entries * tiles >= (1ll << 31) || p.entries * tiles * copies >= (1ll << 50))
         return PA_ERR_BAD_DIMS;
     p.q = q;
     p.k = k_cache;
@@ -888,8 +901,12 @@ extern "C" int pa_q8_decode(const void* q, const int8_t* k_cache, const int8_t* 
     int sms = 0, dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return PA_ERR_CUDA;
-    int grid = sms * v.ctas;
-    grid = grid > kMaxCtas ? kMaxCtas : grid;
+    const int grid = sms > kMaxCtas ? kMaxCtas : sms;
+    // Teams: the copies of one length that run side by side (rows of the same or of
+    // neighbouring heads, whose cache lines lie together)
+    p.team = copies % 4 == 0 ? 4 : copies % 2 == 0 ? 2 : 1;
+    if (grid % p.team != 0)
+        p.team = 1;
     void* args[] = {&p};
-    return q8_launch(v.fn, dim3(grid), kDecodeThreads, v.body + (static_cast<size_t>(p.entries) + 1) * 4, static_cast<cudaStream_t>(stream), args);
+    return q8_launch(v.fn, dim3(grid), v.threads, v.body + (static_cast<size_t>(p.entries) + 1) * 4, static_cast<cudaStream_t>(stream), args);
 }
