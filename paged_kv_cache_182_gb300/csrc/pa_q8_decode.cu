@@ -34,11 +34,11 @@
 namespace pa {
 namespace {
 
-constexpr int kTile = 16;                 // tokens of a tile
+constexpr int kTile = 32;                 // tokens of a tile: two MMA groups of 16
 constexpr int kMaxEntries = 4096;         // prefix sums in shared memory
-constexpr int kMaxCtas = 160;             // one per SM
-constexpr int kCharge = 12;               // tiles that a piece's start and end count for
-constexpr int kMeta = 32;                 // bytes of a tile's scales and places
+constexpr int kMaxCtas = 304;             // two per SM
+constexpr int kCharge = 6;                // tiles that a piece's start and end count for
+constexpr int kMeta = 64;                 // bytes of a tile's scales and places
 constexpr float kLift = 6.f, kSlack = 8.f;  // weights are 2^(t - m + 6), t - m <= 8
 
 struct DecodeParams {
@@ -74,6 +74,13 @@ __device__ __forceinline__ uint4 lds16(uint32_t a)
 {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds4(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
 }
 
@@ -114,14 +121,15 @@ __device__ __forceinline__ float fast_rcp(float x)
 }
 
 // QP: fp16 parts of a query row and of a weight (2: float32).  HB: blocks a
-// tile may touch (2: BLOCK is 8).  Query fragments stay in registers, or in
+// tile may touch (2; 4 where BLOCK is 8).  Query fragments stay in registers, or in
 // shared memory where the accumulators of four groups of rows leave no room.
-template <int D, int NT, int QP>
+template <int D, int NT, int QP, int C>
 struct Shape {
     static constexpr int kRows = 8 * NT, kSteps = D / 16;
-    static constexpr int kWarps = NT == 1 && QP == 1 ? 12 : 8, kThreads = kWarps * 32;
+    static constexpr int kWarps = NT == 1 && QP == 1 ? 12 / C : 8, kThreads = kWarps * 32;
+    static constexpr int kJoint = NT * QP == 4 ? 1 : 2;  // MMA groups of a tile taken together
     static constexpr int kTileBytes = 2 * kTile * D, kStage = kTileBytes + kMeta;
-    static constexpr int kStages = (kWarps == 12 ? 4 : 5) * (D == 128 ? 1 : 2);
+    static constexpr int kStages = (NT == 1 && QP == 1 ? 2 : 3) * (D == 128 ? 1 : 2);
     static constexpr int kRing = kWarps * kStages * kStage;
     // a warp's state in shared memory: steps of 16 + 4 floats, rows 4 (mod 32) floats
     // apart, so that neither its writes nor its reads meet a bank twice
@@ -163,17 +171,23 @@ __device__ __forceinline__ void fma4(float4& a, float f, float4 v)
     a.w = fmaf(f, v.w, a.w);
 }
 
-template <int D, int NT, int QP, int HB>
-__global__ void __launch_bounds__(Shape<D, NT, QP>::kThreads, 1) pa_q8_decode_kernel(const __grid_constant__ DecodeParams p)
+template <int D, int NT, int QP, int HB, int C>
+__global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode_kernel(const __grid_constant__ DecodeParams p)
 {
-    using Sh = Shape<D, NT, QP>;
+    using Sh = Shape<D, NT, QP, C>;
     constexpr int kRows = Sh::kRows, kSteps = Sh::kSteps, kTileBytes = Sh::kTileBytes, kStage = Sh::kStage, S = Sh::kStages;
     constexpr int kWarps = Sh::kWarps, kThreads = Sh::kThreads;
     constexpr int kChunks = D / 64;  // 16-byte runs of a key row per lane
     constexpr bool kQs = Sh::kQueryShared;
+    // float16 has a code + 128 as a subnormal number, with no arithmetic: the sum of
+    // the row's 128 is taken off the score beforehand.  (Keys only: the values'
+    // weights have one sign, and their sum would swamp the output.)
+    constexpr bool kSmall = QP == 1;
+    constexpr int J = Sh::kJoint;
     extern __shared__ __align__(16) unsigned char smem[];  // ring, then states | query fragments | prefix sums
     __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
     __shared__ float sm_f[kRows];  // of a row's scores: scale * log2(e) / the power of two
+    __shared__ float sm_off[kRows];  // what a row's scores begin with (kSmall)
     __shared__ int sm_lim[kRows];  // keys that the row sees
     __shared__ int sm_last;
     grid_dependents_launch();
@@ -183,7 +197,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP>::kThreads, 1) pa_q8_decode_ke
     // a copy takes kRowsCopy rows of D bytes, 16 bytes a lane, whole lines together;
     // the places of the 16-byte runs (and, at D = 64, the order of V's rows) are such
     // that the reads below meet no bank twice
-    constexpr int kRuns = D / 16, kRowsCopy = 32 / kRuns, kCopies = kTile / kRowsCopy;
+    constexpr int kRuns = D / 16, kRowsCopy = 32 / kRuns;
     const int copy_run = lane % kRuns;
     const int copy_row = D == 128 ? lane / kRuns : (lane >> 2 & 3) * 2 + (lane >> 4);
     uint32_t copy_k, copy_v, read_k, read_v;
@@ -252,31 +266,34 @@ __global__ void __launch_bounds__(Shape<D, NT, QP>::kThreads, 1) pa_q8_decode_ke
     // groups of rows of one head); `copies` segments of a team share an entry's length.
     const int copies = (p.selected ? p.groups : p.KV * p.groups) / p.team;
     const int team = blockIdx.x / p.team, member = blockIdx.x % p.team;
-    const int64_t U = static_cast<int64_t>(prefix[p.entries]) * copies;
-    const int G = static_cast<int>(min(static_cast<int64_t>(gridDim.x / p.team), (U + kCharge + kWarps - 1) / (kCharge + kWarps)));
+    const int U = prefix[p.entries] * copies;  // (below 2^31: the host has seen to it)
+    const int G = min(static_cast<int>(gridDim.x) / p.team, (U + kCharge + kWarps - 1) / (kCharge + kWarps));
     if (team >= G)
         return;
-    const int64_t u_end = (static_cast<int64_t>(team) + 1) * U / G;
-    const int64_t u_begin = static_cast<int64_t>(team) * U / G;
+    // U = G share + extra: the first `extra` teams take one tile more
+    const int share = U / G, extra = U - G * share;
+    auto begin_of = [&](int i) { return i * share + min(i, extra); };
+    auto owner_of = [&](int x) { return x < extra * (share + 1) ? x / (share + 1) : extra + (x - extra * (share + 1)) / share; };
+    const int u_begin = begin_of(team), u_end = begin_of(team + 1);
 
-    for (int64_t u = u_begin; u < u_end;) {
+    for (int u = u_begin; u < u_end;) {
         // the segment of tile u: entry e, copy c of it
         int e = 0;
         {
             int hi = p.entries;
             while (hi - e > 1) {
                 const int mid = (e + hi) >> 1;
-                if (static_cast<int64_t>(prefix[mid]) * copies <= u)
+                if (prefix[mid] * copies <= u)
                     e = mid;
                 else
                     hi = mid;
             }
         }
         const int length = prefix[e + 1] - prefix[e];
-        const int cc = static_cast<int>((u - static_cast<int64_t>(prefix[e]) * copies) / length);
-        const int64_t s_end = static_cast<int64_t>(prefix[e]) * copies + static_cast<int64_t>(cc + 1) * length;
-        const int64_t s_begin = s_end - length + kCharge;  // its first tile, behind the charge
-        const int64_t from = max(u, s_begin), stop = min(s_end, u_end);
+        const int cc = (u - prefix[e] * copies) / length;
+        const int s_end = prefix[e] * copies + (cc + 1) * length;
+        const int s_begin = s_end - length + kCharge;  // its first tile, behind the charge
+        const int from = max(u, s_begin), stop = min(s_end, u_end);
         if (stop <= s_begin)
             break;  // only of the charge: the next CTAs have the tiles
         const int c = cc * p.team + member;
@@ -286,23 +303,16 @@ __global__ void __launch_bounds__(Shape<D, NT, QP>::kThreads, 1) pa_q8_decode_ke
         const int row_base = grp * kRows;
 
         // ---- query rows: one warp a group of eight
-        float x[kSteps * 4];
+        uint4 raw[kChunks][QP * 2];  // 16 elements a chunk, converted behind the first copies
         if (warp < NT) {
             const int row = row_base + warp * 8 + g;
 #pragma unroll
             for (int ch = 0; ch < kChunks; ++ch) {
                 const int64_t at = ((static_cast<int64_t>(b) * p.KV + kh) * p.R + row) * D + ch * 64 + t * 16;
-                if (row >= p.R) {
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p.q) + at * (QP * 2));
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        x[ch * 16 + i] = 0.f;
-                } else if (p.dtype == PA_F32) {
-                    q8_load16(x + ch * 16, static_cast<const float*>(p.q) + at);
-                } else if (p.dtype == PA_F16) {
-                    q8_load16(x + ch * 16, static_cast<const __half*>(p.q) + at);
-                } else {
-                    q8_load16(x + ch * 16, static_cast<const __nv_bfloat16*>(p.q) + at);
-                }
+                for (int i = 0; i < QP * 2; ++i)
+                    raw[ch][i] = row < p.R ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
             }
         }
         const int n = min(max(__ldg(p.lens + b), 0), p.cap);
@@ -312,20 +322,21 @@ __global__ void __launch_bounds__(Shape<D, NT, QP>::kThreads, 1) pa_q8_decode_ke
         const int nb = (n + (1 << p.shift) - 1) >> p.shift;
         const int32_t* table = p.table + static_cast<int64_t>(b) * p.maxb;
         // this warp's tiles: first, first + kWarps, ... below last
-        const int first = static_cast<int>(from - s_begin) + warp;
-        const int last = min(static_cast<int>(stop - s_begin), (tokens + kTile - 1) / kTile);
+        const int first = from - s_begin + warp;
+        const int last = min(stop - s_begin, (tokens + kTile - 1) / kTile);
 
-        // ---- copies.  The lanes look up the blocks of the warp's next 32 tiles (16
-        // where a tile touches two) together.
-        constexpr int kWindow = 32 / HB;
+        // ---- copies.  The lanes look up the blocks of the warp's next kWindow tiles together.
+        constexpr int kWindow = 32 / HB, kPart = kTile / HB;  // tokens of a block within a tile, at most
         const uint32_t step = static_cast<uint32_t>(p.KV) * D;
         const int8_t* pk = p.k + static_cast<int64_t>(kh) * D + copy_row * step + copy_run * 16;
         const int8_t* pv = p.v + static_cast<int64_t>(kh) * D + copy_row * step + copy_run * 16;
-        const float* psc = (lane ? p.vs : p.ks) + kh;
-        int blk, phys, blk_next = -1, phys_next = -1;
-        auto look_up = [&](int window, int& bl, int& ph) {
+        const float* psc = (lane & 1 ? p.vs : p.ks) + kh;
+        const int own = lane >> 1 & (HB - 1);     // the part whose scale and place this lane stores
+        uint32_t w_row = 0;                       // of this lane's part of the window: its first row of the pool
+        int w_place = 0, blk_next = -1, phys_next = -1;
+        auto look_up = [&](int window) {
             const int tile = first + (window * kWindow + lane / HB) * kWarps;
-            const int place = tile * kTile + 8 * (lane % HB);
+            const int place = tile * kTile + kPart * (lane % HB);
             int j = -1;
             if (tile < last && place < tokens) {
                 j = place >> p.shift;
@@ -338,87 +349,105 @@ __global__ void __launch_bounds__(Shape<D, NT, QP>::kThreads, 1) pa_q8_decode_ke
                     }
                 }
             }
-            bl = j;
-            ph = j >= 0 ? __ldg(table + j) : -1;
+            blk_next = j;
+            phys_next = j >= 0 ? __ldg(table + j) : -1;
+        };
+        auto take_up = [&](int window) {
+            const int tile = first + (window * kWindow + lane / HB) * kWarps;
+            const int in_block = (tile * kTile + kPart * (lane % HB)) & ((1 << p.shift) - 1);
+            const bool there = static_cast<uint32_t>(phys_next) < static_cast<uint32_t>(p.num_blocks);
+            if (!there && blk_next >= 0)
+                q8_report(p.status, PA_STATUS_BAD_BLOCK);
+            // (without a block: the first rows of the pool are read in its place, and hidden)
+            w_row = there ? (static_cast<uint32_t>(phys_next) << p.shift) + in_block : 0u;
+            w_place = there ? (blk_next << p.shift) + in_block : INT_MAX - 64;
         };
         auto issue = [&](int k, uint32_t st) {  // the warp's k-th tile
-            const int tile = first + k * kWarps;
-            if (tile < last) {
+            if (first + k * kWarps < last) {
                 const int at_window = k & (kWindow - 1);
-                if (at_window == 0 && k > 0) {
-                    blk = blk_next;
-                    phys = phys_next;
-                }
+                if (at_window == 0 && k > 0)
+                    take_up(k / kWindow);
                 if (at_window == kWindow / 2)
-                    look_up(k / kWindow + 1, blk_next, phys_next);
-                const int in_block = HB == 2 ? 0 : (tile * kTile) & ((1 << p.shift) - 1);
-                uint32_t row[HB];
+                    look_up(k / kWindow + 1);
+                const uint32_t own_row = __shfl_sync(kFullWarp, w_row, at_window * HB + own);
+                const int own_place = __shfl_sync(kFullWarp, w_place, at_window * HB + own);
+                if (lane < 2 * HB) {
+                    copy4(st + kTileBytes + lane * 4, psc + static_cast<uint64_t>(own_row >> p.shift) * p.KV);
+                    if ((lane & 1) == 0)
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + kTileBytes + 32 + 2 * lane), "r"(own_place) : "memory");
+                }
 #pragma unroll
                 for (int x = 0; x < HB; ++x) {
-                    const int bl = __shfl_sync(kFullWarp, blk, at_window * HB + x), phy = __shfl_sync(kFullWarp, phys, at_window * HB + x);
-                    const bool there = static_cast<uint32_t>(phy) < static_cast<uint32_t>(p.num_blocks);
-                    if (!there && bl >= 0)
-                        q8_report(p.status, PA_STATUS_BAD_BLOCK);
-                    // (without a block: the first rows of the pool are read in its place, and hidden)
-                    const uint32_t ph = there ? static_cast<uint32_t>(phy) : 0u;
-                    const int place = there ? (bl << p.shift) + in_block : INT_MAX - 64;
-                    row[x] = (ph << p.shift) + static_cast<uint32_t>(in_block);
-                    if (lane < 2)
-                        copy4(st + kTileBytes + x * 8 + lane * 4, psc + static_cast<uint64_t>(ph) * p.KV);
-                    if (lane == 2)
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + kTileBytes + 16 + 4 * x), "r"(place) : "memory");
-                }
-                const uint64_t at = static_cast<uint64_t>(row[0]) * step;
-                const uint64_t second = HB == 2 ? static_cast<uint64_t>(row[HB - 1]) * step - kRowsCopy * (kCopies / 2) * step : at;
+                    const uint64_t at = static_cast<uint64_t>(__shfl_sync(kFullWarp, w_row, at_window * HB + x)) * step;
+                    const int8_t* k0 = pk + at;
+                    const int8_t* v0 = pv + at;
 #pragma unroll
-                for (int i = 0; i < kCopies; ++i) {
-                    const uint64_t off = (HB == 2 && i >= kCopies / 2 ? second : at) + static_cast<uint64_t>(i * kRowsCopy) * step;
-                    copy16(st + i * 512 + copy_k, pk + off);
-                    copy16(st + kTile * D + i * 512 + (D == 128 && i & 1 ? copy_v ^ 64 : copy_v), pv + off);
+                    for (int i = 0; i < kPart / kRowsCopy; ++i) {
+                        const uint32_t to = st + (x * (kPart / kRowsCopy) + i) * 512;
+                        copy16(to + copy_k, k0 + i * kRowsCopy * step);
+                        copy16(to + kTile * D + (D == 128 && i & 1 ? copy_v ^ 64 : copy_v), v0 + i * kRowsCopy * step);
+                    }
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        look_up(0, blk, phys);
+        look_up(0);
+        take_up(0);
 #pragma unroll
         for (int i = 0; i < S - 1; ++i)
             issue(i, ring + i * kStage);
 
         // ---- query rows as fragments of B, scaled by a power of two
         if (warp < NT) {
-            float a = 0.f;
+            float x[kSteps * 4], a = 0.f;
+#pragma unroll
+            for (int i = 0; i < kSteps * 4; i += QP == 2 ? 1 : 2) {
+                const uint4 v = raw[i / 16][i % 16 / (QP == 2 ? 4 : 8)];
+                const int word = QP == 2 ? i % 4 : i % 8 / 2;
+                const uint32_t w = word == 0 ? v.x : word == 1 ? v.y : word == 2 ? v.z : v.w;
+                if constexpr (QP == 2) {
+                    x[i] = __uint_as_float(w);
+                } else {
+                    const float2 two = p.dtype == PA_F16 ? __half22float2(*reinterpret_cast<const __half2*>(&w))
+                                                         : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+                    x[i] = two.x;
+                    x[i + 1] = two.y;
+                }
+            }
 #pragma unroll
             for (int i = 0; i < kSteps * 4; ++i)
-                a = q8_amax(a, x[i]);
+                a = fmaxf(a, fabsf(x[i]));
             a = fmaxf(a, __shfl_xor_sync(kFullWarp, a, 1));
             a = fmaxf(a, __shfl_xor_sync(kFullWarp, a, 2));
             // 2^up brings the largest magnitude into [2^11, 2^12)
-            const int ex = max(static_cast<int>(__float_as_uint(a) >> 23) - 127, -100), up = 11 - ex;
-            const float f1 = __uint_as_float(static_cast<uint32_t>(127 + up / 2) << 23);
-            const float f2 = __uint_as_float(static_cast<uint32_t>(127 + up - up / 2) << 23);
-            const float d1 = __uint_as_float(static_cast<uint32_t>(127 - up / 2) << 23);
-            const float d2 = __uint_as_float(static_cast<uint32_t>(127 - (up - up / 2)) << 23);
-            if (t == 0) {
-                const int r = row_base + warp * 8 + g;
-                sm_f[warp * 8 + g] = p.scale * d1 * d2;
-                sm_lim[warp * 8 + g] = r >= p.R ? 0 : p.causal ? min(n, n - p.NQ + r % p.NQ + 1) : n;
-            }
+            const int up = 11 - max(static_cast<int>(__float_as_uint(a) >> 23) - 127, -100);
+            const float lift = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+            float total = 0.f;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 uint32_t w[QP][2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float z0 = x[4 * s + 2 * i] * f1 * f2, z1 = x[4 * s + 2 * i + 1] * f1 * f2;
+                    const float z0 = x[4 * s + 2 * i] * lift, z1 = x[4 * s + 2 * i + 1] * lift;
                     const __half2 hi = __floats2half2_rn(z0, z1);
+                    const float2 back = __half22float2(hi);
                     w[0][i] = half2_bits(hi);
-                    if constexpr (QP == 2) {
-                        const float2 back = __half22float2(hi);
+                    if constexpr (QP == 2)
                         w[QP - 1][i] = half2_bits(__floats2half2_rn(z0 - back.x, z1 - back.y));
-                    }
+                    total += back.x + back.y;
                 }
 #pragma unroll
                 for (int q = 0; q < QP; ++q)
                     sm_q[((q * kSteps + s) * NT + warp) * 32 + lane] = make_uint2(w[q][0], w[q][1]);
+            }
+            total += __shfl_xor_sync(kFullWarp, total, 1);
+            total += __shfl_xor_sync(kFullWarp, total, 2);
+            if (t == 0) {
+                const int r = row_base + warp * 8 + g;
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+                sm_f[warp * 8 + g] = p.scale * down * (kSmall ? 16777216.f : 1.f);
+                sm_off[warp * 8 + g] = kSmall ? total * (-128.f / 16777216.f) : 0.f;
+                sm_lim[warp * 8 + g] = r >= p.R ? 0 : p.causal ? min(n, n - p.NQ + r % p.NQ + 1) : n;
             }
         }
         __syncthreads();
@@ -435,14 +464,20 @@ __global__ void __launch_bounds__(Shape<D, NT, QP>::kThreads, 1) pa_q8_decode_ke
                         qf[q][nt][s][1] = w.y;
                     }
         }
-        float rowf[NT][2];  // of this lane's two score columns
+        float rowf[NT][2], off[NT][2];  // of this lane's two score columns
+        auto row_factors = [&]() {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                rowf[nt][i] = sm_f[nt * 8 + 2 * t + i];
-        // every row sees the keys below
-        const int all_see = row_base + kRows > p.R ? INT_MIN : (p.causal ? n - p.NQ + 1 : n) - 8 * (3 - HB);
+                for (int i = 0; i < 2; ++i) {
+                    rowf[nt][i] = sm_f[nt * 8 + 2 * t + i];
+                    off[nt][i] = sm_off[nt * 8 + 2 * t + i];
+                }
+        };
+        if constexpr (!kQs)
+            row_factors();
+        // parts that begin here or before are seen by every row
+        const int all_see = row_base + kRows > p.R ? INT_MIN : (p.causal ? n - p.NQ + 1 : n) - kPart;
 
         float o[kSteps][NT][4];
         float mx[NT][2], l[NT][2];
@@ -466,160 +501,192 @@ __global__ void __launch_bounds__(Shape<D, NT, QP>::kThreads, 1) pa_q8_decode_ke
             asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");  // this tile's
             __syncwarp();  // the copies of the other lanes; the stage filled next has been read
             issue(ahead++, fill);
-            float ks[HB], lv[HB], iv[HB];
-            int place[2];
-            if constexpr (HB == 2) {
-                const uint4 sc = lds16(st + kTileBytes);
-                const uint2 pl = lds8(st + kTileBytes + 16);
-                ks[0] = __uint_as_float(sc.x), ks[HB - 1] = __uint_as_float(sc.z);
-                lv[0] = __uint_as_float(sc.y), lv[HB - 1] = __uint_as_float(sc.w);
-                place[0] = static_cast<int>(pl.x), place[1] = static_cast<int>(pl.y);
-            } else {
-                const uint2 sc = lds8(st + kTileBytes);
-                const uint2 pl = lds8(st + kTileBytes + 16);
-                ks[0] = __uint_as_float(sc.x), lv[0] = __uint_as_float(sc.y);
-                place[0] = static_cast<int>(pl.x), place[1] = place[0] + 8;
-            }
+#pragma unroll 1
+            for (int j0 = 0; j0 < 2; j0 += J) {
+                constexpr int B2 = HB / 2;  // blocks of a group of 16
+                if constexpr (kQs)  // (registers are short: from shared memory each time)
+                    row_factors();
+                float ks[J][B2], lv[J][B2], iv[J][B2];
+                int place[J][2];
 #pragma unroll
-            for (int x = 0; x < HB; ++x) {
-                const float vs = fmaxf(lv[x], kMinScale);
-                lv[x] = fast_log2(vs);
-                iv[x] = fast_rcp(vs);
-            }
-            // ---- S^T = K Q^T
-            float sacc[NT][4];
+                for (int j = 0; j < J; ++j)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                    for (int x = 0; x < B2; ++x) {
+                        const int part = (j0 + j) * B2 + x;
+                        const uint2 sc = lds8(st + kTileBytes + part * 8);
+                        ks[j][x] = __uint_as_float(sc.x);
+                        const float vs = fmaxf(__uint_as_float(sc.y), kMinScale);
+                        lv[j][x] = fast_log2(vs);
+                        iv[j][x] = fast_rcp(vs);
+                        place[j][x] = static_cast<int>(lds4(st + kTileBytes + 32 + part * 4));
+                        if constexpr (B2 == 1)
+                            place[j][1] = place[j][0] + 8;
+                    }
+                // ---- S^T = K Q^T
+                float sacc[J][NT][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sacc[nt][i] = 0.f;
+                for (int j = 0; j < J; ++j)
 #pragma unroll
-            for (int ch = 0; ch < kChunks; ++ch) {
-                const uint4 ka = lds16(st + (read_k ^ ch * 64)), kb = lds16(st + 8 * D + (read_k ^ ch * 64));
-                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t ua = wa[i] ^ 0x80808080u, ub = wb[i] ^ 0x80808080u;
-                    const uint32_t a[4] = {codes2(ua, 0x4140), codes2(ub, 0x4140), codes2(ua, 0x4342), codes2(ub, 0x4342)};
+                        for (int i = 0; i < 4; ++i)
+                            sacc[j][nt][i] = off[nt][i & 1];
 #pragma unroll
-                    for (int q = 0; q < QP; ++q)
+                for (int ch = 0; ch < kChunks; ++ch) {
+                    uint32_t wa[J][4], wb[J][4];
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            if constexpr (kQs) {
-                                const uint2 w = sm_q[((q * kSteps + ch * 4 + i) * NT + nt) * 32 + lane];
-                                mma(sacc[nt], a, w.x, w.y);
-                            } else {
-                                mma(sacc[nt], a, qf[q][nt][ch * 4 + i][0], qf[q][nt][ch * 4 + i][1]);
-                            }
+                    for (int j = 0; j < J; ++j) {
+                        const uint32_t at = st + (j0 + j) * 16 * D + (read_k ^ ch * 64);
+                        const uint4 ka = lds16(at), kb = lds16(at + 8 * D);
+                        wa[j][0] = ka.x, wa[j][1] = ka.y, wa[j][2] = ka.z, wa[j][3] = ka.w;
+                        wb[j][0] = kb.x, wb[j][1] = kb.y, wb[j][2] = kb.z, wb[j][3] = kb.w;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                        for (int j = 0; j < J; ++j) {
+                            const uint32_t ua = wa[j][i] ^ 0x80808080u, ub = wb[j][i] ^ 0x80808080u;
+                            const uint32_t a[4] = {kSmall ? __byte_perm(ua, 0, 0x4140) : codes2(ua, 0x4140),
+                                                   kSmall ? __byte_perm(ub, 0, 0x4140) : codes2(ub, 0x4140),
+                                                   kSmall ? __byte_perm(ua, 0, 0x4342) : codes2(ua, 0x4342),
+                                                   kSmall ? __byte_perm(ub, 0, 0x4342) : codes2(ub, 0x4342)};
+#pragma unroll
+                            for (int q = 0; q < QP; ++q)
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    if constexpr (kQs) {
+                                        const uint2 w = sm_q[((q * kSteps + ch * 4 + i) * NT + nt) * 32 + lane];
+                                        mma(sacc[j][nt], a, w.x, w.y);
+                                    } else {
+                                        mma(sacc[j][nt], a, qf[q][nt][ch * 4 + i][0], qf[q][nt][ch * 4 + i][1]);
+                                    }
+                                }
                         }
+                    }
                 }
-            }
-            // ---- scores in base 2 plus log2 of the value scale; hidden ones -inf
+                // ---- scores in base 2 plus log2 of the value scale; hidden ones -inf
+                bool hide = false, raise = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                for (int j = 0; j < J; ++j) {
+                    hide |= (B2 == 1 ? place[j][0] : max(place[j][0], place[j][1])) > all_see;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sacc[nt][i] = fmaf(sacc[nt][i], rowf[nt][i & 1] * ks[(i >> 1) & (HB - 1)], lv[(i >> 1) & (HB - 1)]);
-            if (HB == 1 ? place[0] > all_see : max(place[0], place[1]) > all_see) {
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                        for (int i = 0; i < 4; ++i)
+                            sacc[j][nt][i] = fmaf(sacc[j][nt][i], rowf[nt][i & 1] * ks[j][i >> 1 & (B2 - 1)], lv[j][i >> 1 & (B2 - 1)]);
+                }
+                if (hide) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (place[i >> 1] + g >= sm_lim[nt * 8 + 2 * t + (i & 1)])
-                            sacc[nt][i] = -INFINITY;
-            }
-            bool raise = false;
+                    for (int j = 0; j < J; ++j)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    raise |= fmaxf(sacc[nt][i], sacc[nt][i + 2]) > mx[nt][i] + kSlack;
-            if (__any_sync(kFullWarp, raise)) {
+                            for (int i = 0; i < 4; ++i)
+                                if (place[j][i >> 1] + g >= sm_lim[nt * 8 + 2 * t + (i & 1)])
+                                    sacc[j][nt][i] = -INFINITY;
+                }
+                float top[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float m = fmaxf(sacc[nt][i], sacc[nt][i + 2]);
-                        m = fmaxf(m, __shfl_xor_sync(kFullWarp, m, 4));
-                        m = fmaxf(m, __shfl_xor_sync(kFullWarp, m, 8));
-                        m = fmaxf(m, __shfl_xor_sync(kFullWarp, m, 16));
-                        m = fmaxf(m, mx[nt][i]);
-                        const float down = m == -INFINITY ? 1.f : fast_exp2(mx[nt][i] - m);
-                        mx[nt][i] = m;
-                        l[nt][i] *= down;
+                        top[nt][i] = fmaxf(sacc[0][nt][i], sacc[0][nt][i + 2]);
+                        if constexpr (J == 2)
+                            top[nt][i] = fmaxf(top[nt][i], fmaxf(sacc[J - 1][nt][i], sacc[J - 1][nt][i + 2]));
+                        raise |= top[nt][i] > mx[nt][i] + kSlack;
+                    }
+                if (__any_sync(kFullWarp, raise)) {
 #pragma unroll
-                        for (int s = 0; s < kSteps; ++s) {
-                            o[s][nt][i] *= down;
-                            o[s][nt][i + 2] *= down;
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float m = top[nt][i];
+                            m = fmaxf(m, __shfl_xor_sync(kFullWarp, m, 4));
+                            m = fmaxf(m, __shfl_xor_sync(kFullWarp, m, 8));
+                            m = fmaxf(m, __shfl_xor_sync(kFullWarp, m, 16));
+                            m = fmaxf(m, mx[nt][i]);
+                            const float down = m == -INFINITY ? 1.f : fast_exp2(mx[nt][i] - m);
+                            mx[nt][i] = m;
+                            l[nt][i] *= down;
+#pragma unroll
+                            for (int s = 0; s < kSteps; ++s) {
+                                o[s][nt][i] *= down;
+                                o[s][nt][i + 2] *= down;
+                            }
+                        }
+                }
+                // ---- weights, and as fragments of P^T
+                uint32_t pf[J][QP][NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    // (a row that has seen nothing: its scores are -inf, and so is what is left of them)
+                    const float base[2] = {fmaxf(mx[nt][0], -3.402823466e38f) - kLift, fmaxf(mx[nt][1], -3.402823466e38f) - kLift};
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        float w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            w[i] = fast_exp2(sacc[j][nt][i] - base[i & 1]);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if constexpr (B2 == 1)
+                                l[nt][i] = fmaf(w[i] + w[i + 2], iv[j][0], l[nt][i]);
+                            else
+                                l[nt][i] = fmaf(w[i], iv[j][0], fmaf(w[i + 2], iv[j][B2 - 1], l[nt][i]));
+                        }
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const __half2 hi = __floats2half2_rn(w[2 * x], w[2 * x + 1]);
+                            pf[j][0][nt][x] = movm_trans(half2_bits(hi));
+                            if constexpr (QP == 2) {
+                                const float2 back = __half22float2(hi);
+                                pf[j][QP - 1][nt][x] = movm_trans(half2_bits(__floats2half2_rn(w[2 * x] - back.x, w[2 * x + 1] - back.y)));
+                            }
                         }
                     }
-            }
-            // ---- weights, and as fragments of P^T
-            uint32_t pf[QP][NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // (a row that has seen nothing: its scores are -inf, and so is what is left of them)
-                    const float base = fmaxf(mx[nt][i & 1], -3.402823466e38f) - kLift;
-                    w[i] = fast_exp2(sacc[nt][i] - base);
                 }
+                // ---- O^T += V^T P^T
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if constexpr (HB == 1)
-                        l[nt][i] = fmaf(w[i] + w[i + 2], iv[0], l[nt][i]);
-                    else
-                        l[nt][i] = fmaf(w[i], iv[0], fmaf(w[i + 2], iv[HB - 1], l[nt][i]));
-                }
+                for (int j = 0; j < J; ++j) {
+                    const uint32_t sv = st + kTile * D + (j0 + j) * 16 * D;
+                    uint32_t vw[4][D / 32];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const __half2 hi = __floats2half2_rn(w[2 * x], w[2 * x + 1]);
-                    pf[0][nt][x] = movm_trans(half2_bits(hi));
-                    if constexpr (QP == 2) {
-                        const float2 back = __half22float2(hi);
-                        pf[QP - 1][nt][x] = movm_trans(half2_bits(__floats2half2_rn(w[2 * x] - back.x, w[2 * x + 1] - back.y)));
-                    }
-                }
-            }
-            // ---- O^T += V^T P^T
-            const uint32_t sv = st + kTile * D;
-            uint32_t vw[4][D / 32];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (D == 128) {
-                    const uint4 v = lds16(sv + (i >> 1) * 8 * D + (i & 1) * 128 + read_v);
-                    vw[i][0] = v.x, vw[i][1] = v.y, vw[i][2] = v.z, vw[i][3] = v.w;
-                } else {
-                    const uint2 v = lds8(sv + (i >> 1) * 8 * D + (i & 1) * 256 + read_v);
-                    vw[i][0] = v.x, vw[i][1] = v.y;
-                }
-            }
-#pragma unroll
-            for (int w = 0; w < D / 32; ++w) {
-                uint32_t mixed[2][2];  // [half of the tokens][channels 0 1 | 2 3]
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    mixed[x][0] = __byte_perm(vw[2 * x][w], vw[2 * x + 1][w], 0x5140) ^ 0x80808080u;
-                    mixed[x][1] = __byte_perm(vw[2 * x][w], vw[2 * x + 1][w], 0x7362) ^ 0x80808080u;
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t a[4] = {codes2(mixed[0][i], 0x4140), codes2(mixed[0][i], 0x4342), codes2(mixed[1][i], 0x4140),
-                                           codes2(mixed[1][i], 0x4342)};
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if constexpr (QP == 1) {
-                            mma(o[2 * w + i][nt], a, pf[0][nt][0], pf[0][nt][1]);
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (D == 128) {
+                            const uint4 v = lds16(sv + (i >> 1) * 8 * D + (i & 1) * 128 + read_v);
+                            vw[i][0] = v.x, vw[i][1] = v.y, vw[i][2] = v.z, vw[i][3] = v.w;
                         } else {
-                            // a tile's products by themselves: added to the sums by rounded
-                            // additions (the tensor core's own cut off what does not fit)
-                            float d[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma(d, a, pf[QP - 1][nt][0], pf[QP - 1][nt][1]);
-                            mma(d, a, pf[0][nt][0], pf[0][nt][1]);
+                            const uint2 v = lds8(sv + (i >> 1) * 8 * D + (i & 1) * 256 + read_v);
+                            vw[i][0] = v.x, vw[i][1] = v.y;
+                        }
+                    }
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                o[2 * w + i][nt][j] += d[j];
+                    for (int w = 0; w < D / 32; ++w) {
+                        uint32_t mixed[2][2];  // [half of the tokens][channels 0 1 | 2 3]
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            mixed[x][0] = __byte_perm(vw[2 * x][w], vw[2 * x + 1][w], 0x5140) ^ 0x80808080u;
+                            mixed[x][1] = __byte_perm(vw[2 * x][w], vw[2 * x + 1][w], 0x7362) ^ 0x80808080u;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t a[4] = {codes2(mixed[0][i], 0x4140), codes2(mixed[0][i], 0x4342), codes2(mixed[1][i], 0x4140),
+                                                   codes2(mixed[1][i], 0x4342)};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                if constexpr (QP == 1) {
+                                    mma(o[2 * w + i][nt], a, pf[j][0][nt][0], pf[j][0][nt][1]);
+                                } else {
+                                    // a group's products by themselves: added to the sums by rounded
+                                    // additions (the tensor core's own cut off what does not fit)
+                                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+                                    mma(d, a, pf[j][QP - 1][nt][0], pf[j][QP - 1][nt][1]);
+                                    mma(d, a, pf[j][0][nt][0], pf[j][0][nt][1]);
+#pragma unroll
+                                    for (int y = 0; y < 4; ++y)
+                                        o[2 * w + i][nt][y] += d[y];
+                                }
+                            }
                         }
                     }
                 }
@@ -655,6 +722,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP>::kThreads, 1) pa_q8_decode_ke
         const int64_t record = static_cast<int64_t>(blockIdx.x) * 2 + (u_begin > s_begin ? 0 : 1);
         const int64_t out0 = ((static_cast<int64_t>(b) * p.KV + kh) * p.R + row_base) * D;
         constexpr int kQuads = D / 4, kItems = kRows * kQuads;  // four channels each
+        constexpr int kBatch = 20;  // pieces loaded together
         for (int x = tid; x < kItems; x += kThreads) {
             const int row = x / kQuads, quad = x % kQuads;
             if (row_base + row >= p.R)
@@ -685,7 +753,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP>::kThreads, 1) pa_q8_decode_ke
         }
         if (!whole) {
             // pieces of the segment: those of teams c0 .. c1
-            const int c0 = static_cast<int>(((s_begin + 1) * G - 1) / U), c1 = static_cast<int>((s_end * G - 1) / U);
+            const int c0 = owner_of(s_begin), c1 = owner_of(s_end - 1);
             __syncthreads();
             if (tid == 0) {
                 int* counter = p.counters + (static_cast<int64_t>(b) * p.KV + kh) * p.groups + grp;
@@ -709,6 +777,15 @@ __global__ void __launch_bounds__(Shape<D, NT, QP>::kThreads, 1) pa_q8_decode_ke
                     float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
                     for (int i0 = 0; i0 < pieces; i0 += kQuads) {  // (one turn, mostly)
                         const int many = min(kQuads, pieces - i0);
+                        const float* src = p.part_o + x * 4;
+                        float4 v[kBatch];
+                        auto load = [&](int i) {
+#pragma unroll
+                            for (int k = 0; k < kBatch; ++k)
+                                v[k] = live && i + k < many ? __ldcg(reinterpret_cast<const float4*>(src + record_of(i0 + i + k) * kRows * D))
+                                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                        };
+                        load(0);
                         float2 ml = make_float2(-INFINITY, 0.f);
                         if (live && in_row < many)
                             ml = __ldcg(p.part_ml + record_of(i0 + in_row) * kRows + row);
@@ -725,15 +802,11 @@ __global__ void __launch_bounds__(Shape<D, NT, QP>::kThreads, 1) pa_q8_decode_ke
                         sum = fmaf(sum, old, part);
                         val.x *= old, val.y *= old, val.z *= old, val.w *= old;
                         m = top;
-                        const float* src = p.part_o + x * 4;
-                        for (int i = 0; i < many; i += 8) {
-                            float4 v[8];
+                        for (int i = 0; i < many; i += kBatch) {
+                            if (i > 0)
+                                load(i);
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                v[k] = live && i + k < many ? __ldcg(reinterpret_cast<const float4*>(src + record_of(i0 + i + k) * kRows * D))
-                                                            : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
+                            for (int k = 0; k < kBatch; ++k)
                                 fma4(val, __shfl_sync(kFullWarp, f, (lane & ~(kQuads - 1)) + ((i + k) & (kQuads - 1))), v[k]);
                         }
                     }
@@ -750,25 +823,28 @@ __global__ void __launch_bounds__(Shape<D, NT, QP>::kThreads, 1) pa_q8_decode_ke
 
 struct Variant {
     const void* fn;
-    int rows, threads;
+    int rows, threads, ctas;
     size_t body;  // shared memory apart from the prefix sums
 };
 
-template <int D, int NT, int QP>
+template <int D, int NT, int QP, int C>
 Variant variant(int BLOCK)
 {
-    using Sh = Shape<D, NT, QP>;
-    return {BLOCK == 8 ? reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 2>)
-                       : reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 1>),
-            Sh::kRows, Sh::kThreads, static_cast<size_t>(Sh::kBody) + Sh::kQueryBytes};
+    using Sh = Shape<D, NT, QP, C>;
+    return {BLOCK == 8 ? reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 4, C>)
+                       : reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 2, C>),
+            Sh::kRows, Sh::kThreads, C, static_cast<size_t>(Sh::kBody) + Sh::kQueryBytes};
 }
 
+// `segments`: of 8 query rows.
 template <int D>
-Variant variant(int BLOCK, int dtype, int R)
+Variant variant(int BLOCK, int dtype, int R, long long segments, int sms)
 {
     if (dtype == PA_F32)
-        return R > 8 ? variant<D, 2, 2>(BLOCK) : variant<D, 1, 2>(BLOCK);
-    return R > 16 ? variant<D, 4, 1>(BLOCK) : R > 8 ? variant<D, 2, 1>(BLOCK) : variant<D, 1, 1>(BLOCK);
+        return R > 8 ? variant<D, 2, 2, 1>(BLOCK) : variant<D, 1, 2, 1>(BLOCK);
+    if (R > 8)
+        return R > 16 ? variant<D, 4, 1, 1>(BLOCK) : variant<D, 2, 1, 1>(BLOCK);
+    return segments > sms / 2 ? variant<D, 1, 1, 2>(BLOCK) : variant<D, 1, 1, 1>(BLOCK);
 }
 
 // Sizes that pa_q8_decode refuses, apart from those of the cache.
@@ -861,14 +937,18 @@ extern "C" int pa_q8_decode(const void* q, const int8_t* k_cache, const int8_t* 
                          {o.counts, b4 * KV, false}};
     if (q8_overlap(r, 12))
         return PA_ERR_BAD_DIMS;
-    const Variant v = D == 64 ? variant<64>(BLOCK, o.dtype, R) : variant<128>(BLOCK, o.dtype, R);
+    int sms = 0, dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return PA_ERR_CUDA;
+    const long long segments = static_cast<long long>(B) * KV;
+    const Variant v = D == 64 ? variant<64>(BLOCK, o.dtype, R, segments, sms) : variant<128>(BLOCK, o.dtype, R, segments, sms);
     DecodeParams p{};
     p.groups = (R + v.rows - 1) / v.rows;
     p.entries = o.selected ? B * KV : B;
     const long long copies = o.selected ? p.groups : static_cast<long long>(KV) * p.groups;
     const long long most = o.selected ? static_cast<long long>(o.budget) * BLOCK : static_cast<long long>(o.max_blocks) * BLOCK;
     const long long tiles = (most + kTile - 1) / kTile + kCharge;
-    if (p.entries * tiles >= (1ll << 31) || p.entries * tiles * copies >= (1ll << 50))
+    if (p.entries * tiles * copies >= (1ll << 31))
         return PA_ERR_BAD_DIMS;
     p.q = q;
     p.k = k_cache;
@@ -898,10 +978,7 @@ extern "C" int pa_q8_decode(const void* q, const int8_t* k_cache, const int8_t* 
     p.budget = o.budget;
     p.causal = o.causal ? 1 : 0;
     p.dtype = o.dtype;
-    int sms = 0, dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return PA_ERR_CUDA;
-    const int grid = sms > kMaxCtas ? kMaxCtas : sms;
+    const int grid = sms * v.ctas > kMaxCtas ? kMaxCtas : sms * v.ctas;
     // Teams: the copies of one length that run side by side (rows of the same or of
     // neighbouring heads, whose cache lines lie together)
     p.team = copies % 4 == 0 ? 4 : copies % 2 == 0 ? 2 : 1;
