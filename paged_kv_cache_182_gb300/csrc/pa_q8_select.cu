@@ -5,9 +5,13 @@
 // rows become whole numbers in shared memory, positive and negative parts apart,
 // so that sum_d max(c min, c max) = c+ . max + c- . min is a product of whole
 // numbers (dp4a): exact, in any order.  Four lanes share a block, a quarter of
-// the channels each; four rows are summed over those lanes together.  The scores
-// go to the first CTA of the cluster, which finds the score of the last block
-// taken two bits at a time and writes the indices in order.
+// the channels each; four rows are summed over those lanes together.  Table
+// entries are read before the length is known, and the next blocks' bounds
+// while this step's are used.
+//
+// The scores go to the first CTA of the cluster, which finds the score of the
+// last block taken by counting them in 256 bins over their range, then over the
+// bin that it falls into, until that bin is taken whole: mostly two rounds.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -18,11 +22,9 @@
 namespace pa {
 namespace {
 
-constexpr int kSelectThreads = 512;
-constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kSelectRows = 128;        // query rows in shared memory at once
 constexpr int kSelectBlocks = 32768;    // blocks of a table row at most
-constexpr int kStepBlocks = kSelectWarps * 8;
+constexpr int kBins = 256;
 
 struct SelectParams {
     const void* q;
@@ -54,27 +56,37 @@ __device__ __forceinline__ float q8_element(const void* q, int dtype, int64_t i)
     return __bfloat162float(static_cast<const __nv_bfloat16*>(q)[i]);
 }
 
-// grid (C, B * KV), clusters of C along x.
-template <int D, int C>
-__global__ void __launch_bounds__(kSelectThreads) pa_q8_select_kernel(const __grid_constant__ SelectParams p)
+// grid (C, B * KV), clusters of C along x; T threads.
+template <int D, int C, int T>
+__global__ void __launch_bounds__(T, 768 / T) pa_q8_select_kernel(const __grid_constant__ SelectParams p)
 {
+    constexpr int kWarps = T / 32, kStep = kWarps * C * 8;  // blocks that the cluster takes together
     constexpr int kWords = D / 16;                 // words of a lane's quarter of a row
     extern __shared__ __align__(16) uint32_t smem[];
     uint32_t* keys = smem;                         // [maxb] scores in order (the first CTA's)
-    const int per = ((p.maxb + C - 1) / C + 7) & ~7;
-    float* own = reinterpret_cast<float*>(C == 1 ? smem : smem + ((p.maxb + 3) & ~3));  // [per] this CTA's scores
-    uint32_t* codes = smem + ((p.maxb + 3) & ~3) + (C == 1 ? 0 : per);  // [rows][4 quarters][positive words | negative words]
+    const int most = (p.maxb + kStep - 1) / kStep * kWarps * 8;  // blocks of a CTA
+    float* own = reinterpret_cast<float*>(smem + ((p.maxb + 3) & ~3));  // [most] this CTA's scores
+    uint32_t* codes = smem + ((p.maxb + 3) & ~3) + most;  // [rows][4 quarters][positive words | negative words]
+    constexpr int kQuarter = D / 8 + 4, kRow = 4 * kQuarter;  // words; the four quarters in banks of their own
     __shared__ float steps[kSelectRows];
-    __shared__ int2 sums[2][kSelectWarps];
-    __shared__ int cnt[kSelectWarps][2];
+    __shared__ __align__(16) uint32_t hist[kBins];
+    __shared__ uint32_t wide[kWarps][2];
+    __shared__ uint32_t pick[3];                   // bin, still wanted in it, its count
+    __shared__ int cnt[kWarps][2];
     grid_dependents_launch();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int seg = blockIdx.y, b = seg / p.KV, h = seg % p.KV;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int seg = blockIdx.y, b = seg / p.KV, h = seg - b * p.KV;
     const int rank = C == 1 ? 0 : static_cast<int>(blockIdx.x);
     if (C > 1)  // the first CTA's shared memory may be written once it runs
         asm volatile("barrier.cluster.arrive;" ::: "memory");
     grid_dependency_wait();
     int n = __ldg(p.lens + b);
+    const int32_t* table = p.table + static_cast<int64_t>(b) * p.maxb;
+    // the cluster's warps take eight blocks each in turn
+    const int j0 = (warp * C + rank) * 8 + g;
+    int phys = j0 < p.maxb ? __ldg(table + j0) : -1;
+    int phys1 = j0 + kStep < p.maxb ? __ldg(table + j0 + kStep) : -1;
+    const int64_t q0 = static_cast<int64_t>(seg) * p.R * D;
     if (n < 0 || n > p.cap) {
         if (h == 0 && rank == 0 && tid == 0)
             q8_report(p.status, PA_STATUS_BAD_LENGTH);
@@ -83,113 +95,109 @@ __global__ void __launch_bounds__(kSelectThreads) pa_q8_select_kernel(const __gr
     const int nb = (n + (1 << p.shift) - 1) >> p.shift;
     const int m = min(nb, p.budget);
     int32_t* sel = p.selected + static_cast<int64_t>(seg) * p.budget;
-    if (rank == 0) {
-        for (int i = m + tid; i < p.budget; i += kSelectThreads)
-            sel[i] = -1;
-        if (tid == 0)
-            p.counts[seg] = m;
-    }
-    if (nb <= p.budget) {  // the same in every CTA of the cluster
-        if (rank == 0)
-            for (int i = tid; i < nb; i += kSelectThreads)
-                sel[i] = i;
-        if (C > 1)
-            asm volatile("barrier.cluster.wait;" ::: "memory");
-        return;
-    }
     const int lo = p.first, hi = nb - p.last;
     const int need = p.budget - p.first - p.last;
     if (rank == 0) {
-        for (int i = tid; i < p.first; i += kSelectThreads)
-            sel[i] = i;
-        for (int i = tid; i < p.last; i += kSelectThreads)
-            sel[p.first + need + i] = hi + i;
+        for (int i = m + tid; i < p.budget; i += T)
+            sel[i] = -1;
+        if (tid == 0)
+            p.counts[seg] = m;
+        if (nb <= p.budget) {
+            for (int i = tid; i < nb; i += T)
+                sel[i] = i;
+        } else {
+            for (int i = tid; i < p.first; i += T)
+                sel[i] = i;
+            for (int i = tid; i < p.last; i += T)
+                sel[p.first + need + i] = hi + i;
+        }
     }
-    if (need == 0) {
+    if (nb <= p.budget || need == 0) {  // the same in every CTA of the cluster
         if (C > 1)
             asm volatile("barrier.cluster.wait;" ::: "memory");
         return;
     }
 
-    // scores of this CTA's blocks [j0, j1)
-    const int j0 = min(rank * per, nb), j1 = min(j0 + per, nb);
-    const int g = lane >> 2, t = lane & 3;
-    const int64_t q0 = static_cast<int64_t>(seg) * p.R * D;
+    // scores
+    struct Bounds {
+        uint32_t mn[kWords], mx[kWords];
+        float ks;
+        bool there;
+    };
+    auto fetch = [&](Bounds& x, int j, int ph) {
+        x.there = j < nb && static_cast<uint32_t>(ph) < static_cast<uint32_t>(p.num_blocks);
+        if (!x.there && j < nb)
+            q8_report(p.status, PA_STATUS_BAD_BLOCK);
+        const int64_t at = static_cast<int64_t>(x.there ? ph : 0) * p.KV + h;
+        const uint4* src = reinterpret_cast<const uint4*>(p.bounds + at * 2 * D + t * (D / 4));
+        if (x.there) {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 v = __ldg(src + i), w = __ldg(src + i + D / 16);
+                x.mn[4 * i] = v.x, x.mn[4 * i + 1] = v.y, x.mn[4 * i + 2] = v.z, x.mn[4 * i + 3] = v.w;
+                x.mx[4 * i] = w.x, x.mx[4 * i + 1] = w.y, x.mx[4 * i + 2] = w.z, x.mx[4 * i + 3] = w.w;
+            }
+            x.ks = __ldg(p.k_scale + at);
+        }
+    };
     for (int r0 = 0; r0 < p.R; r0 += kSelectRows) {
         const int rows = min(kSelectRows, p.R - r0), rows4 = (rows + 3) & ~3;
-        if (r0 > 0)
+        // two steps of blocks are on their way, the entries of the third
+        Bounds x, next;
+        if (r0 > 0) {
+            phys = j0 < nb ? __ldg(table + j0) : -1;
+            phys1 = j0 + kStep < nb ? __ldg(table + j0 + kStep) : -1;
             __syncthreads();
-        for (int r = warp; r < rows4; r += kSelectWarps) {
-            float x[D / 32];
+        }
+        fetch(x, j0, phys);
+        fetch(next, j0 + kStep, phys1);
+        int phys2 = j0 + 2 * kStep < nb ? __ldg(table + j0 + 2 * kStep) : -1;
+        for (int r = warp; r < rows4; r += kWarps) {
+            float v[D / 32];
             float a = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
-                x[i] = r < rows ? q8_element(p.q, p.dtype, q0 + static_cast<int64_t>(r0 + r) * D + lane * (D / 32) + i) : 0.f;
-                a = q8_amax(a, x[i]);
+                v[i] = r < rows ? q8_element(p.q, p.dtype, q0 + static_cast<int64_t>(r0 + r) * D + lane * (D / 32) + i) : 0.f;
+                a = q8_amax(a, v[i]);
             }
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1)
                 a = fmaxf(a, __shfl_xor_sync(kFullWarp, a, o));
             const float scale = q8_scale_of(a), inv = 1.f / scale;
-            // (rows behind the last repeat step 0: they give 0, replaced below)
             if (lane == 0)
                 steps[r] = scale;
-            int8_t* row = reinterpret_cast<int8_t*>(codes + r * (D / 2));
+            int8_t* row = reinterpret_cast<int8_t*>(codes + r * kRow);
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
-                const int d = lane * (D / 32) + i, c = q8_code(x[i], scale, inv);
-                int8_t* at = row + (d / (D / 4)) * (D / 2) + d % (D / 4);
+                const int d = lane * (D / 32) + i, c = q8_code(v[i], scale, inv);
+                int8_t* at = row + (d / (D / 4)) * (kQuarter * 4) + d % (D / 4);
                 at[0] = static_cast<int8_t>(max(c, 0));
                 at[D / 4] = static_cast<int8_t>(min(c, 0));
             }
         }
         __syncthreads();
-        for (int base = j0 + warp * 8; base < j1; base += kStepBlocks) {
+        int slot = warp * 8 + g;
+        for (int base = j0 - g; base < nb; base += kStep, slot += kWarps * 8) {
             const int j = base + g;
-            int phys = -1;
-            if (j < j1) {
-                phys = __ldg(p.table + static_cast<int64_t>(b) * p.maxb + j);
-                if (phys < 0 || phys >= p.num_blocks) {
-                    phys = -1;
-                    q8_report(p.status, PA_STATUS_BAD_BLOCK);
-                }
-            }
-            uint32_t mn[kWords], mx[kWords];
-            float ks = 0.f;
-            if (phys >= 0) {
-                const int64_t at = static_cast<int64_t>(phys) * p.KV + h;
-                const uint4* src = reinterpret_cast<const uint4*>(p.bounds + at * 2 * D + t * (D / 4));
-#pragma unroll
-                for (int i = 0; i < kWords / 4; ++i) {
-                    const uint4 v = __ldg(src + i), w = __ldg(src + i + D / 16);
-                    mn[4 * i] = v.x, mn[4 * i + 1] = v.y, mn[4 * i + 2] = v.z, mn[4 * i + 3] = v.w;
-                    mx[4 * i] = w.x, mx[4 * i + 1] = w.y, mx[4 * i + 2] = w.z, mx[4 * i + 3] = w.w;
-                }
-                ks = __ldg(p.k_scale + at);
-            } else {
-#pragma unroll
-                for (int i = 0; i < kWords; ++i)
-                    mn[i] = mx[i] = 0;
-            }
             float best = -INFINITY;
             bool any = false;
             for (int r = 0; r < rows; r += 4) {
                 int sum[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint4* c = reinterpret_cast<const uint4*>(codes + (r + k) * (D / 2) + t * (D / 8));
+                    const uint4* c = reinterpret_cast<const uint4*>(codes + (r + k) * kRow + t * kQuarter);
                     int s = 0;
 #pragma unroll
                     for (int i = 0; i < kWords / 4; ++i) {
                         const uint4 up = c[i], dn = c[i + D / 64];
-                        s = __dp4a(static_cast<int>(up.x), static_cast<int>(mx[4 * i]), s);
-                        s = __dp4a(static_cast<int>(up.y), static_cast<int>(mx[4 * i + 1]), s);
-                        s = __dp4a(static_cast<int>(up.z), static_cast<int>(mx[4 * i + 2]), s);
-                        s = __dp4a(static_cast<int>(up.w), static_cast<int>(mx[4 * i + 3]), s);
-                        s = __dp4a(static_cast<int>(dn.x), static_cast<int>(mn[4 * i]), s);
-                        s = __dp4a(static_cast<int>(dn.y), static_cast<int>(mn[4 * i + 1]), s);
-                        s = __dp4a(static_cast<int>(dn.z), static_cast<int>(mn[4 * i + 2]), s);
-                        s = __dp4a(static_cast<int>(dn.w), static_cast<int>(mn[4 * i + 3]), s);
+                        s = __dp4a(static_cast<int>(up.x), static_cast<int>(x.mx[4 * i]), s);
+                        s = __dp4a(static_cast<int>(up.y), static_cast<int>(x.mx[4 * i + 1]), s);
+                        s = __dp4a(static_cast<int>(up.z), static_cast<int>(x.mx[4 * i + 2]), s);
+                        s = __dp4a(static_cast<int>(up.w), static_cast<int>(x.mx[4 * i + 3]), s);
+                        s = __dp4a(static_cast<int>(dn.x), static_cast<int>(x.mn[4 * i]), s);
+                        s = __dp4a(static_cast<int>(dn.y), static_cast<int>(x.mn[4 * i + 1]), s);
+                        s = __dp4a(static_cast<int>(dn.z), static_cast<int>(x.mn[4 * i + 2]), s);
+                        s = __dp4a(static_cast<int>(dn.w), static_cast<int>(x.mn[4 * i + 3]), s);
                     }
                     sum[k] = s;
                 }
@@ -200,7 +208,7 @@ __global__ void __launch_bounds__(kSelectThreads) pa_q8_select_kernel(const __gr
                 const int o2 = __shfl_xor_sync(kFullWarp, t & 2 ? a0 : a1, 2);
                 const int total = (t & 2 ? a1 : a0) + o2;
                 if (r + t < rows) {
-                    const float score = __fmul_rn(__fmul_rn(steps[r + t], ks), static_cast<float>(total));
+                    const float score = __fmul_rn(__fmul_rn(steps[r + t], x.ks), static_cast<float>(total));
                     any |= score == score;
                     best = fmaxf(best, score);  // (a NaN leaves the other)
                 }
@@ -210,83 +218,122 @@ __global__ void __launch_bounds__(kSelectThreads) pa_q8_select_kernel(const __gr
                 best = fmaxf(best, __shfl_xor_sync(kFullWarp, best, o));
                 any |= __shfl_xor_sync(kFullWarp, static_cast<int>(any), o) != 0;
             }
-            if (j < j1 && t == 0) {
-                float s = phys >= 0 && any ? best : __int_as_float(0x7fc00000);
+            if (j < nb && t == 0) {
+                float s = x.there && any ? best : __int_as_float(0x7fc00000);
                 if (r0 > 0) {
-                    const float before = own[j - j0];
+                    const float before = own[slot];
                     s = before != before ? s : s != s ? before : fmaxf(s, before);
                 }
-                own[j - j0] = s;
+                own[slot] = s;
+            }
+            x = next;
+            if (base + kStep < nb) {
+                fetch(next, j + 2 * kStep, phys2);
+                phys2 = j + 3 * kStep < nb ? __ldg(table + j + 3 * kStep) : -1;
             }
         }
     }
-    __syncthreads();
-    // to the first CTA
-    if (C == 1) {
-        for (int j = tid; j < nb; j += kSelectThreads)
-            keys[j] = score_order(own[j]);
-        __syncthreads();
-    } else {
+    // to the first CTA; a warp moves its own
+    __syncwarp();
+    uint32_t to = smem_u32(keys);
+    if (C > 1) {
         asm volatile("barrier.cluster.wait;" ::: "memory");
-        uint32_t to;
         asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(smem_u32(keys)));
-        for (int j = j0 + tid; j < j1; j += kSelectThreads)
-            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + static_cast<uint32_t>(j) * 4),
-                         "r"(score_order(own[j - j0]))
-                         : "memory");
+    }
+    for (int base = (warp * C + rank) * 8 + lane % 8 + lane / 8 * kStep, slot = warp * 8 + lane % 8 + lane / 8 * kWarps * 8; base < nb;
+         base += 4 * kStep, slot += 4 * kWarps * 8)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + static_cast<uint32_t>(base) * 4), "r"(score_order(own[slot])) : "memory");
+    if (C > 1) {
         asm volatile("barrier.cluster.arrive;" ::: "memory");
-        asm volatile("barrier.cluster.wait;" ::: "memory");
         if (rank != 0)
-            return;
+            return;  // (the first CTA alone waits: only its shared memory was written)
+        asm volatile("barrier.cluster.wait;" ::: "memory");
+    } else {
+        __syncthreads();
     }
 
-    // the score of the last block taken: the largest T that `need` candidates reach
-    uint32_t T = 0, t_ge = 0, t_eq = 0;
-    int n_eq = 0;
-    bool whole = false;
-    for (int s = 30; s >= 0 && !whole; s -= 2) {
-        const uint32_t c1 = T | 1u << s, c2 = T | 2u << s, c3 = T | 3u << s;
-        int x = 0, y = 0;
-        for (int j = lo + tid; j < hi; j += kSelectThreads) {
-            const uint32_t k = keys[j];
-            x += (k >= c1 ? 1 : 0) + (k >= c2 ? 1 << 16 : 0);
-            y += k >= c3 ? 1 : 0;
-        }
-        x = static_cast<int>(__reduce_add_sync(kFullWarp, static_cast<uint32_t>(x)));
-        y = __reduce_add_sync(kFullWarp, y);
-        int2* sum = sums[(s >> 1) & 1];
-        if (lane == 0)
-            sum[warp] = make_int2(x, y);
-        __syncthreads();
-        const int2 v = lane < kSelectWarps ? sum[lane] : make_int2(0, 0);
-        const uint32_t xx = __reduce_add_sync(kFullWarp, static_cast<uint32_t>(v.x));
-        const int n1 = static_cast<int>(xx & 0xffffu), n2 = static_cast<int>(xx >> 16), n3 = __reduce_add_sync(kFullWarp, v.y);
-        int got = 0;
-        if (n3 >= need) {
-            T = c3;
-            got = n3;
-        } else if (n2 >= need) {
-            T = c2;
-            got = n2;
-        } else if (n1 >= need) {
-            T = c1;
-            got = n1;
-        }
-        whole = got == need;  // all that reach T are taken
+    // the range of the candidates' scores
+    uint32_t least = 0xffffffffu, largest = 0;
+    for (int i = tid; i < kBins; i += T)
+        hist[i] = 0;
+    for (int j = lo + tid; j < hi; j += T) {
+        least = min(least, keys[j]);
+        largest = max(largest, keys[j]);
     }
-    if (whole) {
-        t_ge = T;
-    } else {  // more than are wanted have the score T: the first of them
-        t_eq = T;
-        t_ge = T + 1;
+    least = __reduce_min_sync(kFullWarp, least);
+    largest = __reduce_max_sync(kFullWarp, largest);
+    if (lane == 0) {
+        wide[warp][0] = least;
+        wide[warp][1] = largest;
+    }
+    __syncthreads();
+    least = __reduce_min_sync(kFullWarp, lane < kWarps ? wide[lane][0] : 0xffffffffu);
+    largest = __reduce_max_sync(kFullWarp, lane < kWarps ? wide[lane][1] : 0u);
+    // taken: scores >= t_ge, and of those equal to t_eq the first n_eq
+    uint32_t t_ge = 0, t_eq = 0, from = least, width = largest - least;  // candidates in [from, from + width]
+    int n_eq = 0, want = need;
+    for (;;) {
+        const int shift = max(0, 32 - __clz(width) - 8);  // 256 bins over the range
+        for (int j = lo + tid; j < hi; j += T) {
+            const uint32_t d = keys[j] - from;
+            if (keys[j] >= from && d <= width)
+                atomicAdd(&hist[d >> shift], 1u);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            // eight bins a lane, from the top
+            constexpr int kOwn = kBins / 32;
+            const uint4 v0 = *reinterpret_cast<const uint4*>(hist + kBins - kOwn * (lane + 1)), v1 = *reinterpret_cast<const uint4*>(hist + kBins - kOwn * (lane + 1) + 4);
+            const uint32_t v[kOwn] = {v1.w, v1.z, v1.y, v1.x, v0.w, v0.z, v0.y, v0.x};
+            uint32_t sum = 0;
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i)
+                sum += v[i];
+            uint32_t incl = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(kFullWarp, incl, o);
+                if (lane >= o)
+                    incl += y;
+            }
+            uint32_t at = incl - sum;
+            if (at < static_cast<uint32_t>(want) && static_cast<uint32_t>(want) <= incl) {
+#pragma unroll
+                for (int i = 0; i < kOwn; ++i) {
+                    if (at < static_cast<uint32_t>(want) && static_cast<uint32_t>(want) <= at + v[i]) {
+                        pick[0] = static_cast<uint32_t>(kBins - 1 - lane * kOwn - i);
+                        pick[1] = static_cast<uint32_t>(want) - at;
+                        pick[2] = v[i];
+                    }
+                    at += v[i];
+                }
+            }
+        }
+        __syncthreads();
+        from += pick[0] << shift;
+        want = static_cast<int>(pick[1]);
+        if (pick[1] == pick[2]) {  // the bin is taken whole
+            t_ge = from;
+            break;
+        }
+        if (shift == 0) {  // its scores are equal: the first of them
+            t_eq = from;
+            t_ge = from + 1;
+            n_eq = want;
+            break;
+        }
+        width = (1u << shift) - 1;
+        for (int i = tid; i < kBins; i += T)
+            hist[i] = 0;
+        __syncthreads();
     }
     // counts of the warps' ranges, then the places
-    const int chunk = ((hi - lo + kSelectWarps - 1) / kSelectWarps + 31) & ~31;
+    const int chunk = ((hi - lo + kWarps - 1) / kWarps + 31) & ~31;
     const int w0 = min(lo + warp * chunk, hi), w1 = min(w0 + chunk, hi);
     int ge = 0, eq = 0;
     for (int j = w0 + lane; j < w1; j += 32) {
         ge += keys[j] >= t_ge;
-        eq += !whole && keys[j] == t_eq;
+        eq += n_eq > 0 && keys[j] == t_eq;
     }
     ge = __reduce_add_sync(kFullWarp, ge);
     eq = __reduce_add_sync(kFullWarp, eq);
@@ -295,14 +342,12 @@ __global__ void __launch_bounds__(kSelectThreads) pa_q8_select_kernel(const __gr
         cnt[warp][1] = eq;
     }
     __syncthreads();
-    const int cg = lane < kSelectWarps ? cnt[lane][0] : 0, ce = lane < kSelectWarps ? cnt[lane][1] : 0;
-    n_eq = whole ? 0 : need - __reduce_add_sync(kFullWarp, cg);
-    int bge = __reduce_add_sync(kFullWarp, lane < warp ? cg : 0), beq = __reduce_add_sync(kFullWarp, lane < warp ? ce : 0);
+    int bge = __reduce_add_sync(kFullWarp, lane < warp ? cnt[lane][0] : 0), beq = __reduce_add_sync(kFullWarp, lane < warp ? cnt[lane][1] : 0);
     const uint32_t below = (1u << lane) - 1;
     for (int base = w0; base < w1; base += 32) {
         const int j = base + lane;
         const uint32_t key = j < w1 ? keys[j] : 0;
-        const bool is_ge = j < w1 && key >= t_ge, is_eq = j < w1 && !whole && key == t_eq;
+        const bool is_ge = j < w1 && key >= t_ge, is_eq = j < w1 && n_eq > 0 && key == t_eq;
         const uint32_t mg = __ballot_sync(kFullWarp, is_ge), me = __ballot_sync(kFullWarp, is_eq);
         const int a = bge + __popc(mg & below), e = beq + __popc(me & below);
         if (is_ge || (is_eq && e < n_eq))
@@ -315,10 +360,10 @@ __global__ void __launch_bounds__(kSelectThreads) pa_q8_select_kernel(const __gr
 template <int D>
 const void* select_kernel(int C)
 {
-    return C == 1   ? reinterpret_cast<const void*>(pa_q8_select_kernel<D, 1>)
-           : C == 2 ? reinterpret_cast<const void*>(pa_q8_select_kernel<D, 2>)
-           : C == 4 ? reinterpret_cast<const void*>(pa_q8_select_kernel<D, 4>)
-                    : reinterpret_cast<const void*>(pa_q8_select_kernel<D, 8>);
+    return C == 1   ? reinterpret_cast<const void*>(pa_q8_select_kernel<D, 1, 256>)
+           : C == 2 ? reinterpret_cast<const void*>(pa_q8_select_kernel<D, 2, 256>)
+           : C == 4 ? reinterpret_cast<const void*>(pa_q8_select_kernel<D, 4, 256>)
+                    : reinterpret_cast<const void*>(pa_q8_select_kernel<D, 8, 256>);
 }
 
 }  // namespace
@@ -379,14 +424,16 @@ extern "C" int pa_q8_select(const void* q, const int8_t* bounds, const float* k_
     p.shift = BLOCK == 8 ? 3 : BLOCK == 16 ? 4 : BLOCK == 32 ? 5 : 6;
     p.cap = o.max_blocks * BLOCK;
     p.dtype = o.dtype;
-    // CTAs per segment: as many as the SMs hold at once, with a step of blocks each
+    // CTAs per segment: as many as have a step of blocks each, up to a cluster of 8,
+    // while the SMs hold them all at once (three each)
     int C = 8;
-    while (C > 1 && (static_cast<long long>(B) * KV * C > 304 || kStepBlocks * (C / 2) >= o.max_blocks))
+    while (C > 1 && (static_cast<long long>(B) * KV * C > 456 || 64 * (C / 2) >= o.max_blocks))
         C /= 2;
-    const int per = ((o.max_blocks + C - 1) / C + 7) & ~7;
+    const int T = 256;
+    const int most = (o.max_blocks + T / 4 * C - 1) / (T / 4 * C) * (T / 4);
     const int rows = p.R < kSelectRows ? (p.R + 3) & ~3 : kSelectRows;
-    const size_t smem = 4 * (static_cast<size_t>((o.max_blocks + 3) & ~3) + (C == 1 ? 0 : per) + static_cast<size_t>(rows) * (D / 2));
+    const size_t smem = 4 * (static_cast<size_t>((o.max_blocks + 3) & ~3) + most + static_cast<size_t>(rows) * (D / 2 + 16));
     void* args[] = {&p};
-    return q8_launch(D == 64 ? select_kernel<64>(C) : select_kernel<128>(C), dim3(C, B * KV), kSelectThreads, smem,
+    return q8_launch(D == 64 ? select_kernel<64>(C) : select_kernel<128>(C), dim3(C, B * KV), T, smem,
                      static_cast<cudaStream_t>(stream), args, C);
 }

@@ -2,10 +2,10 @@
 // (include/pa_q8.h).
 //
 // pa_q8_append_kernel: a group of BLOCK * D / 32 threads owns one block of one
-// sequence and KV head, keys or values; a thread holds two runs of 16 elements
-// of it in registers, so the rows are read once for their largest magnitude and
-// their codes.  The largest magnitude, and for keys the lowest and highest
-// codes by channel, are joined by shuffles and through shared memory.  Earlier
+// sequence and KV head, its keys and its values; a thread holds two runs of 16
+// elements of each in registers, so the rows are read once for their largest
+// magnitude and their codes.  The largest magnitudes, and for keys the lowest and
+// highest codes by channel, are joined by shuffles and through shared memory.  Earlier
 // codes are read only where the scale grew, and for the bounds.
 //
 // pa_q8_read_kernel: a thread takes runs of 16 codes.
@@ -41,7 +41,128 @@ __device__ __forceinline__ int clamp_report(int x, int hi, int* status)
     return x < 0 ? 0 : hi;
 }
 
-// grid (blocks a sequence's new rows may touch, ceil(KV / heads of a CTA) * 2, B)
+// 16 elements of a row as they are in memory.
+template <typename T>
+struct Run {
+    static constexpr int kVectors = sizeof(T);
+    uint4 v[kVectors];
+
+    __device__ __forceinline__ uint32_t word(int i) const
+    {
+        const uint4 x = v[i >> 2];
+        return (i & 3) == 0 ? x.x : (i & 3) == 1 ? x.y : (i & 3) == 2 ? x.z : x.w;
+    }
+    __device__ __forceinline__ float get(int i) const
+    {
+        if constexpr (sizeof(T) == 4) {
+            return __uint_as_float(word(i));
+        } else {
+            const uint32_t w = word(i >> 1);
+            if constexpr (std::is_same_v<T, __half>) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+                return i & 1 ? f.y : f.x;
+            } else {
+                return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+            }
+        }
+    }
+    // Largest magnitude, as an integer of the type's width in the order of the
+    // magnitudes (two 16-bit ones side by side).
+    __device__ __forceinline__ uint32_t largest(uint32_t m) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4 * kVectors; ++i) {
+            if constexpr (sizeof(T) == 4)
+                m = max(m, word(i) & 0x7fffffffu);
+            else
+                asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(word(i) & 0x7fff7fffu));
+        }
+        return m;
+    }
+};
+
+// The magnitude of largest()'s integer; infinite or NaN where an element is.
+template <typename T>
+__device__ __forceinline__ float magnitude(uint32_t m)
+{
+    if constexpr (sizeof(T) == 4)
+        return __uint_as_float(m);
+    const uint32_t x = max(m & 0xffffu, m >> 16);
+    if constexpr (std::is_same_v<T, __half>)
+        return __half2float(__ushort_as_half(static_cast<unsigned short>(x)));
+    else
+        return __uint_as_float(x << 16);
+}
+
+__device__ __forceinline__ float element(const float* p) { return *p; }
+__device__ __forceinline__ float element(const __half* p) { return __half2float(*p); }
+__device__ __forceinline__ float element(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+// Stores the codes of 16 elements (also at `src`) and returns them.  x / scale is
+// rounded to a whole number by adding 1.5 2^23; the product with 1 / scale is
+// within 2^-17 of the quotient, so that only one nearer than that to a half has to
+// be looked at again (one run in 1500), as has what is not finite: in a loop, to
+// keep the code short.
+template <typename T>
+__device__ __forceinline__ uint4 run_codes(int8_t* dst, const Run<T>& r, const T* src, float scale, float inv, bool odd)
+{
+    constexpr float kWhole = 12582912.f;
+    float worst = 0.f;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+        uint32_t c[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float x = r.get(i + k), t = __fmaf_rn(x, inv, kWhole);
+            worst = fmaxf(worst, fabsf(__fmaf_rn(x, inv, -(t - kWhole))));
+            c[k] = __float_as_uint(t);
+        }
+        w[i >> 2] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    }
+    uint4 codes = make_uint4(w[0], w[1], w[2], w[3]);
+    if (odd || worst > 0.49998f) {
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i)
+            dst[i] = static_cast<int8_t>(q8_code(element(src + i), scale, inv));
+        codes = *reinterpret_cast<const uint4*>(dst);
+    } else {
+        *reinterpret_cast<uint4*>(dst) = codes;
+    }
+    return codes;
+}
+
+// Lowest and highest of two 16-bit integers each.
+__device__ __forceinline__ uint32_t lowest2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("min.s16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t highest2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.s16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Bytes 0 and 1 (2 and 3: upper) of a word as 16-bit integers.
+__device__ __forceinline__ uint32_t widen(uint32_t w, bool upper)
+{
+    uint32_t r;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(w), "r"(upper ? 0xb3a2u : 0x9180u));
+    return r;
+}
+
+// Low bytes of 16-bit integers.
+__device__ __forceinline__ uint4 pack_codes(const uint32_t* two)
+{
+    return make_uint4(__byte_perm(two[0], two[1], 0x6420), __byte_perm(two[2], two[3], 0x6420),
+                      __byte_perm(two[4], two[5], 0x6420), __byte_perm(two[6], two[7], 0x6420));
+}
+
+// grid (blocks a sequence's new rows may touch, ceil(KV / heads of a CTA), B)
 template <typename T, int D, int BLOCK>
 __global__ void __launch_bounds__(kStoreThreads) pa_q8_append_kernel(const __grid_constant__ AppendParams p)
 {
@@ -49,13 +170,13 @@ __global__ void __launch_bounds__(kStoreThreads) pa_q8_append_kernel(const __gri
     constexpr int kThreads = kGroup < 64 ? 64 : kGroup;
     constexpr int kHeads = kThreads / kGroup;        // heads of a CTA
     constexpr int kRuns = D / 16, kRows = kGroup / kRuns;  // a thread's rows: r, r + kRows (= BLOCK / 2)
-    __shared__ float part[kThreads / 32];
-    __shared__ uint32_t ends[2][kThreads / 32][kRuns * 4];  // lowest, highest codes by warp
+    __shared__ float part[2][kThreads / 32];
+    __shared__ uint32_t ends[2][kThreads / 32][kRuns * 8];  // lowest, highest codes by warp
     grid_dependents_launch();
     grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = blockIdx.z, kv = blockIdx.y & 1;
-    const int h = (blockIdx.y >> 1) * kHeads + tid / kGroup;
+    const int b = blockIdx.z;
+    const int h = blockIdx.y * kHeads + tid / kGroup;
     const int me = tid % kGroup, run = me % kRuns, row0 = me / kRuns;
     const bool report = blockIdx.x == 0 && blockIdx.y == 0 && tid == 0;
     const int past = clamp_report(__ldg(p.lens + b), p.cap, report ? p.status : nullptr);
@@ -67,132 +188,150 @@ __global__ void __launch_bounds__(kStoreThreads) pa_q8_append_kernel(const __gri
     int phys = -1;
     if (blk < p.maxb)
         phys = __ldg(p.table + static_cast<int64_t>(b) * p.maxb + blk);
+    // the new rows are on their way while the block is looked up
+    const bool head = h < p.KV;
+    Run<T> x[2][2];  // keys, values
+    bool fresh[2];
+    uint32_t most[2] = {0, 0};
+    auto src_of = [&](int kv, int k) {
+        return static_cast<const T*>(p.rows[kv]) + b * p.stride[kv][0] + h * p.stride[kv][1] +
+               (first + row0 + k * kRows - past) * p.stride[kv][2] + run * 16;
+    };
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int token = first + row0 + k * kRows;
+        fresh[k] = head && token >= past && token < past + want;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv)
+            if (fresh[k]) {
+                const T* src = src_of(kv, k);
+#pragma unroll
+                for (int i = 0; i < Run<T>::kVectors; ++i)
+                    x[kv][k].v[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+            }
+    }
     if (phys < 0 || phys >= p.num_blocks) {
         if (tid == 0)
             q8_report(p.status, PA_STATUS_BAD_SLOT);
         return;
     }
-    const bool live = h < p.KV;
     const bool earlier = first < past;
     const int64_t at = static_cast<int64_t>(phys) * p.KV + h;
-    const float was = live && earlier ? p.scale[kv][at] : 0.f;
-
-    float x[2][16];
-    bool fresh[2];
-    float a = 0.f;
+    float was[2] = {0.f, 0.f}, a[2];
     bool odd = false;  // something is not finite
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int token = first + row0 + k * kRows;
-        fresh[k] = live && token >= past && token < past + want;
-        if (fresh[k]) {
-            const T* src = static_cast<const T*>(p.rows[kv]) + b * p.stride[kv][0] + h * p.stride[kv][1] +
-                           (token - past) * p.stride[kv][2] + run * 16;
-            q8_load16(x[k], src);
+    for (int kv = 0; kv < 2; ++kv) {
+        if (head && earlier)
+            was[kv] = p.scale[kv][at];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                odd |= !(fabsf(x[k][i]) <= 3.402823466e38f);
-                a = q8_amax(a, x[k][i]);
-            }
+        for (int k = 0; k < 2; ++k)
+            if (fresh[k])
+                most[kv] = x[kv][k].largest(most[kv]);
+        a[kv] = magnitude<T>(most[kv]);
+        if (!(a[kv] <= 3.402823466e38f)) {
+            odd = true;
+            a[kv] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (fresh[k])
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        a[kv] = q8_amax(a[kv], x[kv][k].get(i));
         }
+#pragma unroll
+        for (int o = 1; o < (kGroup < 32 ? kGroup : 32); o <<= 1)
+            a[kv] = fmaxf(a[kv], __shfl_xor_sync(kFullWarp, a[kv], o));
     }
     if (odd)
         q8_report(p.status, PA_STATUS_NOT_FINITE);
-#pragma unroll
-    for (int o = 1; o < (kGroup < 32 ? kGroup : 32); o <<= 1)
-        a = fmaxf(a, __shfl_xor_sync(kFullWarp, a, o));
     if constexpr (kGroup > 32) {
-        if (lane == 0)
-            part[warp] = a;
+        if (lane == 0) {
+            part[0][warp] = a[0];
+            part[1][warp] = a[1];
+        }
         __syncthreads();
         constexpr int kWarps = kGroup / 32;
-        a = part[warp / kWarps * kWarps];
 #pragma unroll
-        for (int i = 1; i < kWarps; ++i)
-            a = fmaxf(a, part[warp / kWarps * kWarps + i]);
+        for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i)
+                a[kv] = fmaxf(a[kv], part[kv][warp / kWarps * kWarps + i]);
     }
-    const float scale = fmaxf(q8_scale_of(a), was), inv = 1.f / scale;
-    const bool grown = earlier && scale > was;
-    if (live && me == 0 && (!earlier || grown))
-        p.scale[kv][at] = scale;
 
-    const bool ranged = kv == 0 && p.bounds;  // (the same in every thread)
-    uint32_t lo[4], hi[4];  // of this thread's rows: lowest and highest code by channel, four a word
+    uint32_t lo[8], hi[8];  // of this thread's keys: lowest and highest code by channel, two a word
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        lo[i] = 0x7f7f7f7fu;
-        hi[i] = 0x81818181u;
+    for (int i = 0; i < 8; ++i) {
+        lo[i] = 0x007f007fu;
+        hi[i] = 0xff81ff81u;
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int row = row0 + k * kRows, token = first + row;
-        int8_t* dst = p.cache[kv] + ((static_cast<int64_t>(phys) * BLOCK + row) * p.KV + h) * D + run * 16;
-        uint32_t w[4];
-        if (fresh[k]) {
+    for (int kv = 0; kv < 2; ++kv) {
+        const float scale = fmaxf(q8_scale_of(a[kv]), was[kv]), inv = 1.f / scale;
+        const bool grown = earlier && scale > was[kv], ranged = kv == 0 && p.bounds;
+        if (head && me == 0 && (!earlier || grown))
+            p.scale[kv][at] = scale;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[i] = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[i] |= static_cast<uint32_t>(q8_code(x[k][4 * i + j], scale, inv) & 255) << (8 * j);
-                lo[i] = __vmins4(lo[i], w[i]);
-                hi[i] = __vmaxs4(hi[i], w[i]);
-            }
-            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else if (live && token < past && (grown || ranged)) {
-            const uint4 old = *reinterpret_cast<const uint4*>(dst);
-            const uint32_t o[4] = {old.x, old.y, old.z, old.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[i] = o[i];
+        for (int k = 0; k < 2; ++k) {
+            const int row = row0 + k * kRows;
+            int8_t* dst = p.cache[kv] + ((static_cast<int64_t>(phys) * BLOCK + row) * p.KV + h) * D + run * 16;
+            const bool old = head && first + row < past && (grown || ranged);
+            uint4 c = make_uint4(0u, 0u, 0u, 0u);
+            if (fresh[k]) {
+                c = run_codes(dst, x[kv][k], src_of(kv, k), scale, inv, odd);
+            } else if (old) {
                 if (grown) {
-                    w[i] = 0;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        w[i] |= static_cast<uint32_t>(q8_again(q8_byte(o[i], j), was, scale, inv) & 255) << (8 * j);
+#pragma unroll 1
+                    for (int i = 0; i < 16; ++i)
+                        dst[i] = static_cast<int8_t>(q8_again(dst[i], was[kv], scale, inv));
                 }
-                lo[i] = __vmins4(lo[i], w[i]);
-                hi[i] = __vmaxs4(hi[i], w[i]);
+                c = *reinterpret_cast<const uint4*>(dst);
             }
-            if (grown)
-                *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (ranged && (fresh[k] || old)) {
+                const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t two = widen(w[i >> 1], i & 1);
+                    lo[i] = lowest2(lo[i], two);
+                    hi[i] = highest2(hi[i], two);
+                }
+            }
         }
     }
 
-    if (ranged) {
+    if (p.bounds) {  // (the same in every thread)
         // lanes with the same columns, then warps
 #pragma unroll
         for (int o = kRuns; o < (kGroup < 32 ? kGroup : 32); o <<= 1)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                lo[i] = __vmins4(lo[i], __shfl_xor_sync(kFullWarp, lo[i], o));
-                hi[i] = __vmaxs4(hi[i], __shfl_xor_sync(kFullWarp, hi[i], o));
+            for (int i = 0; i < 8; ++i) {
+                lo[i] = lowest2(lo[i], __shfl_xor_sync(kFullWarp, lo[i], o));
+                hi[i] = highest2(hi[i], __shfl_xor_sync(kFullWarp, hi[i], o));
             }
         if constexpr (kGroup > 32) {
             if (lane < kRuns) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    ends[0][warp][lane * 4 + i] = lo[i];
-                    ends[1][warp][lane * 4 + i] = hi[i];
+                for (int i = 0; i < 8; ++i) {
+                    ends[0][warp][lane * 8 + i] = lo[i];
+                    ends[1][warp][lane * 8 + i] = hi[i];
                 }
             }
             __syncthreads();
         }
-        if (live && me < kRuns) {
+        if (head && me < kRuns) {
             if constexpr (kGroup > 32) {
                 constexpr int kWarps = kGroup / 32;
                 const int base = warp / kWarps * kWarps;
 #pragma unroll
-                for (int v = 0; v < kWarps; ++v)
+                for (int v = 1; v < kWarps; ++v)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        lo[i] = __vmins4(lo[i], ends[0][base + v][me * 4 + i]);
-                        hi[i] = __vmaxs4(hi[i], ends[1][base + v][me * 4 + i]);
+                    for (int i = 0; i < 8; ++i) {
+                        lo[i] = lowest2(lo[i], ends[0][base + v][me * 8 + i]);
+                        hi[i] = highest2(hi[i], ends[1][base + v][me * 8 + i]);
                     }
             }
             uint4* to = reinterpret_cast<uint4*>(p.bounds + at * 2 * D + me * 16);
-            to[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            to[D / 16] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            to[0] = pack_codes(lo);
+            to[D / 16] = pack_codes(hi);
         }
     }
 }
@@ -333,7 +472,7 @@ extern "C" int pa_q8_append(int8_t* k_cache, int8_t* v_cache, float* k_scale, fl
                      : o.dtype == PA_F16 ? append_kernel<__half>(D, BLOCK)
                                          : append_kernel<__nv_bfloat16>(D, BLOCK);
     void* args[] = {&p};
-    return q8_launch(fn, dim3((N + BLOCK - 2) / BLOCK + 1, (KV + heads - 1) / heads * 2, B), threads, 0,
+    return q8_launch(fn, dim3((N + BLOCK - 2) / BLOCK + 1, (KV + heads - 1) / heads, B), threads, 0,
                      static_cast<cudaStream_t>(stream), args);
 }
 
