@@ -124,6 +124,16 @@ __device__ __forceinline__ void q8_store16(T* p, const float* f)
     }
 }
 
+// Bytes at `pick` (two of code + 128) as two fp16 codes.
+__device__ __forceinline__ uint32_t codes2(uint32_t biased, uint32_t pick)
+{
+    const uint32_t w = __byte_perm(biased, 0x64646464u, pick);
+    const uint32_t off = 0x64806480u;  // 1152
+    uint32_t r;
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(off));
+    return r;
+}
+
 // Byte j of a word as a signed integer.
 __device__ __forceinline__ int q8_byte(uint32_t w, int j) { return static_cast<int>(static_cast<int8_t>(w >> (8 * j))); }
 

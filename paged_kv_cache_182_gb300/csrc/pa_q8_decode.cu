@@ -37,6 +37,7 @@ namespace {
 constexpr int kTile = 32;                 // tokens of a tile: two MMA groups of 16
 constexpr int kMaxEntries = 4096;         // prefix sums in shared memory
 constexpr int kMaxCtas = 304;             // two per SM
+constexpr int kJoinTiles = 14;            // tiles that joining the pieces of a segment counts for
 constexpr int kCharge = 6;                // tiles that a piece's start and end count for
 constexpr int kMeta = 64;                 // bytes of a tile's scales and places
 constexpr float kLift = 6.f, kSlack = 8.f;  // weights are 2^(t - m + 6), t - m <= 8
@@ -57,7 +58,7 @@ struct DecodeParams {
     float* part_o;     // [CTA][2][8 NT][D]
     int* status;
     float scale;       // scale * log2(e)
-    int B, H, KV, R, NQ, groups, shift, maxb, num_blocks, cap, budget, causal, dtype, entries, team;
+    int B, H, KV, R, NQ, groups, shift, maxb, num_blocks, cap, budget, causal, dtype, entries, copies, lg_team;
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src)
@@ -91,16 +92,6 @@ __device__ __forceinline__ uint2 lds8(uint32_t a)
     return v;
 }
 
-// Bytes at `pick` (two of code + 128) as two fp16 codes.
-__device__ __forceinline__ uint32_t codes2(uint32_t biased, uint32_t pick)
-{
-    const uint32_t w = __byte_perm(biased, 0x64646464u, pick);
-    const uint32_t off = 0x64806480u;  // 1152
-    uint32_t r;
-    asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(off));
-    return r;
-}
-
 __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) { mma_16816<false>(d, a, b0, b1); }
 
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
@@ -129,13 +120,14 @@ struct Shape {
     static constexpr int kWarps = NT == 1 && QP == 1 ? 12 / C : 8, kThreads = kWarps * 32;
     static constexpr int kJoint = NT * QP == 4 ? 1 : 2;  // MMA groups of a tile taken together
     static constexpr int kTileBytes = 2 * kTile * D, kStage = kTileBytes + kMeta;
-    static constexpr int kStages = (NT == 1 && QP == 1 ? 2 : 3) * (D == 128 ? 1 : 2);
+    static constexpr int kStages = 2 * (D == 128 ? 1 : 2);
     static constexpr int kRing = kWarps * kStages * kStage;
     // a warp's state in shared memory: steps of 16 + 4 floats, rows 4 (mod 32) floats
     // apart, so that neither its writes nor its reads meet a bank twice
-    static constexpr int kStateStep = 20, kStateRow = kSteps * kStateStep + 4;
-    static constexpr int kMerge = kWarps * kRows * kStateRow * 4;
-    static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
+    static constexpr int kStateStep = 20, kStateRow = kSteps * kStateStep + 4, kState = kRows * kStateRow * 4;
+    static constexpr int kGroup = 2;  // warps' states joined at once beside a ring in use
+    static constexpr int kLastGroup = kRing >= kWarps * kState ? kWarps : kWarps / 2;  // ... and in the place of the ring
+    static_assert(kRing >= kLastGroup * kState, "states fit");
     static constexpr bool kQueryShared = NT == 4;
     static constexpr int kQueryBytes = QP * kSteps * NT * 32 * 8;
 };
@@ -184,7 +176,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
     // weights have one sign, and their sum would swamp the output.)
     constexpr bool kSmall = QP == 1;
     constexpr int J = Sh::kJoint;
-    extern __shared__ __align__(16) unsigned char smem[];  // ring, then states | query fragments | prefix sums
+    extern __shared__ __align__(16) unsigned char smem[];  // ring | query fragments | states | prefix sums
     __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
     __shared__ float sm_f[kRows];  // of a row's scores: scale * log2(e) / the power of two
     __shared__ float sm_off[kRows];  // what a row's scores begin with (kSmall)
@@ -212,17 +204,18 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
         read_k = g * 64 + t * 16;
         read_v = t * 64 + (g ^ (t >> 1) << 2) * 8;
     }
-    float* state = reinterpret_cast<float*>(smem);             // [warp][row] in steps
-    uint2* sm_q = reinterpret_cast<uint2*>(smem + Sh::kBody);  // [QP][step][group of rows][lane]
-    int* prefix = reinterpret_cast<int*>(smem + Sh::kBody + Sh::kQueryBytes);
+    uint2* sm_q = reinterpret_cast<uint2*>(smem + Sh::kRing);  // [QP][step][group of rows][lane]
+    int* prefix = reinterpret_cast<int*>(smem + Sh::kRing + Sh::kQueryBytes + Sh::kGroup * Sh::kState);
 
     // prefix sums of the tiles of the entries (sequences, or sequences and KV
     // heads where each has its own blocks), each with the charge of a piece
+    int longest;
     {
         int* sums = reinterpret_cast<int*>(&sm_m[0][0]);
         const int per = (p.entries + kThreads - 1) / kThreads;
         const int e0 = min(tid * per, p.entries), e1 = min(e0 + per, p.entries);
         int sum = 0;
+        longest = 0;
         for (int e = e0; e < e1; ++e) {
             int tokens;
             if (p.selected) {
@@ -239,7 +232,9 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
             const int u = kCharge + max(1, (tokens + kTile - 1) / kTile);
             prefix[e] = u;
             sum += u;
+            longest = max(longest, u);
         }
+        longest = __reduce_max_sync(kFullWarp, longest);
         int incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -247,12 +242,16 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
             if (lane >= o)
                 incl += y;
         }
-        if (lane == 31)
+        if (lane == 31) {
             sums[warp] = incl;
+            sums[kWarps + warp] = longest;
+        }
         __syncthreads();
         int at = incl - sum;
-        for (int w = 0; w < warp; ++w)
-            at += sums[w];
+        for (int w = 0; w < kWarps; ++w) {
+            at += w < warp ? sums[w] : 0;
+            longest = max(longest, sums[kWarps + w]);
+        }
         for (int e = e0; e < e1; ++e) {
             const int u = prefix[e];
             prefix[e] = at;
@@ -264,20 +263,102 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
     }
     // Teams of p.team CTAs walk the same tokens of neighbouring KV heads (or of
     // groups of rows of one head); `copies` segments of a team share an entry's length.
-    const int copies = (p.selected ? p.groups : p.KV * p.groups) / p.team;
-    const int team = blockIdx.x / p.team, member = blockIdx.x % p.team;
+    const int copies = p.copies, team = blockIdx.x >> p.lg_team, member = blockIdx.x & ((1 << p.lg_team) - 1);
+    const int teams = gridDim.x >> p.lg_team;
     const int U = prefix[p.entries] * copies;  // (below 2^31: the host has seen to it)
-    const int G = min(static_cast<int>(gridDim.x) / p.team, (U + kCharge + kWarps - 1) / (kCharge + kWarps));
-    if (team >= G)
-        return;
+    const int G = min(teams, (U + kCharge + kWarps - 1) / (kCharge + kWarps));
     // U = G share + extra: the first `extra` teams take one tile more
     const int share = U / G, extra = U - G * share;
-    auto begin_of = [&](int i) { return i * share + min(i, extra); };
     auto owner_of = [&](int x) { return x < extra * (share + 1) ? x / (share + 1) : extra + (x - extra * (share + 1)) / share; };
-    const int u_begin = begin_of(team), u_end = begin_of(team + 1);
+    int u_begin, u_end;
+    if (p.entries * copies <= teams && longest <= share + kJoinTiles) {
+        // a segment to each team: the longest takes no more than a share and a join
+        if (team >= p.entries * copies)
+            return;
+        const int e = team / copies, length = prefix[e + 1] - prefix[e];
+        u_begin = prefix[e] * copies + (team - e * copies) * length;
+        u_end = u_begin + length;
+    } else {
+        if (team >= G)
+            return;
+        u_begin = team * share + min(team, extra);
+        u_end = u_begin + share + (team < extra ? 1 : 0);
+    }
 
-    for (int u = u_begin; u < u_end;) {
-        // the segment of tile u: entry e, copy c of it
+    // ---- a piece: tiles from .. stop - 1 of a segment (tiles s_begin .. s_end - 1)
+    int u = u_begin, s_begin, s_end, from, stop;
+    int b, kh, grp, row_base, n, tokens, nb, first, last;
+    const int32_t* sel;
+    const int32_t* table;
+    uint4 raw[kChunks][QP * 2];  // query rows: one warp a group of eight; 16 elements a chunk
+
+    // ---- copies.  The lanes look up the blocks of the warp's next kWindow tiles together.
+    constexpr int kWindow = 32 / HB, kPart = kTile / HB;  // tokens of a block within a tile, at most
+    const uint32_t step = static_cast<uint32_t>(p.KV) * D;
+    const uint32_t copy_at = copy_row * step + copy_run * 16;
+    const int own = lane >> 1 & (HB - 1);     // the part whose scale and place this lane stores
+    uint32_t w_row = 0;                       // of this lane's part of the window: its first row of the pool
+    int w_place = 0, blk_next = -1, phys_next = -1;
+    auto look_up = [&](int window) {
+        const int tile = first + (window * kWindow + lane / HB) * kWarps;
+        const int place = tile * kTile + kPart * (lane % HB);
+        int j = -1;
+        if (tile < last && place < tokens) {
+            j = place >> p.shift;
+            if (sel) {
+                j = __ldg(sel + j);
+                if (j < 0 || j >= nb) {
+                    if (j != -1)
+                        q8_report(p.status, PA_STATUS_BAD_BLOCK);
+                    j = -1;
+                }
+            }
+        }
+        blk_next = j;
+        phys_next = j >= 0 ? __ldg(table + j) : -1;
+    };
+    auto take_up = [&](int window) {
+        const int tile = first + (window * kWindow + lane / HB) * kWarps;
+        const int in_block = (tile * kTile + kPart * (lane % HB)) & ((1 << p.shift) - 1);
+        const bool there = static_cast<uint32_t>(phys_next) < static_cast<uint32_t>(p.num_blocks);
+        if (!there && blk_next >= 0)
+            q8_report(p.status, PA_STATUS_BAD_BLOCK);
+        // (without a block: the first rows of the pool are read in its place, and hidden)
+        w_row = there ? (static_cast<uint32_t>(phys_next) << p.shift) + in_block : 0u;
+        w_place = there ? (blk_next << p.shift) + in_block : INT_MAX - 64;
+    };
+    auto issue = [&](int k, uint32_t st) {  // the warp's k-th tile
+        if (first + k * kWarps < last) {
+            const int at_window = k & (kWindow - 1);
+            if (at_window == 0 && k > 0)
+                take_up(k / kWindow);
+            if (at_window == kWindow / 2)
+                look_up(k / kWindow + 1);
+            const uint32_t own_row = __shfl_sync(kFullWarp, w_row, at_window * HB + own);
+            const int own_place = __shfl_sync(kFullWarp, w_place, at_window * HB + own);
+            if (lane < 2 * HB) {
+                copy4(st + kTileBytes + lane * 4, (lane & 1 ? p.vs : p.ks) + static_cast<uint64_t>(own_row >> p.shift) * p.KV + kh);
+                if ((lane & 1) == 0)
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + kTileBytes + 32 + 2 * lane), "r"(own_place) : "memory");
+            }
+#pragma unroll
+            for (int x = 0; x < HB; ++x) {
+                const uint64_t at = static_cast<uint64_t>(__shfl_sync(kFullWarp, w_row, at_window * HB + x)) * step + (kh * D + copy_at);
+                const int8_t* k0 = p.k + at;
+                const int8_t* v0 = p.v + at;
+#pragma unroll
+                for (int i = 0; i < kPart / kRowsCopy; ++i) {
+                    const uint32_t to = st + (x * (kPart / kRowsCopy) + i) * 512;
+                    copy16(to + copy_k, k0 + i * kRowsCopy * step);
+                    copy16(to + kTile * D + (D == 128 && i & 1 ? copy_v ^ 64 : copy_v), v0 + i * kRowsCopy * step);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // Takes up the piece at tile u and starts its first copies; false when only a
+    // charge is left of this CTA's range (the next one has the tiles).
+    auto begin = [&]() -> bool {
         int e = 0;
         {
             int hi = p.entries;
@@ -290,20 +371,27 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
             }
         }
         const int length = prefix[e + 1] - prefix[e];
-        const int cc = (u - prefix[e] * copies) / length;
-        const int s_end = prefix[e] * copies + (cc + 1) * length;
-        const int s_begin = s_end - length + kCharge;  // its first tile, behind the charge
-        const int from = max(u, s_begin), stop = min(s_end, u_end);
+        const int cc = copies == 1 ? 0 : (u - prefix[e] * copies) / length;
+        s_end = prefix[e] * copies + (cc + 1) * length;
+        s_begin = s_end - length + kCharge;  // its first tile, behind the charge
+        from = max(u, s_begin);
+        stop = min(s_end, u_end);
         if (stop <= s_begin)
-            break;  // only of the charge: the next CTAs have the tiles
-        const int c = cc * p.team + member;
-        const int b = p.selected ? e / p.KV : e;
-        const int kh = p.selected ? e % p.KV : c / p.groups;
-        const int grp = p.selected ? c : c % p.groups;
-        const int row_base = grp * kRows;
-
-        // ---- query rows: one warp a group of eight
-        uint4 raw[kChunks][QP * 2];  // 16 elements a chunk, converted behind the first copies
+            return false;
+        const int c = (cc << p.lg_team) + member;
+        b = p.selected ? e / p.KV : e;
+        kh = p.selected ? e - b * p.KV : p.groups == 1 ? c : c / p.groups;
+        grp = p.selected ? c : p.groups == 1 ? 0 : c - kh * p.groups;
+        row_base = grp * kRows;
+        n = min(max(__ldg(p.lens + b), 0), p.cap);
+        sel = p.selected ? p.selected + static_cast<int64_t>(e) * p.budget : nullptr;
+        tokens = p.selected ? min(max(__ldg(p.counts + e), 0), p.budget) << p.shift : n;  // places in the list of blocks
+        nb = (n + (1 << p.shift) - 1) >> p.shift;
+        table = p.table + static_cast<int64_t>(b) * p.maxb;
+        // this warp's tiles: first, first + kWarps, ... below last
+        first = from - s_begin + warp;
+        last = min(stop - s_begin, (tokens + kTile - 1) / kTile);
+        look_up(0);
         if (warp < NT) {
             const int row = row_base + warp * 8 + g;
 #pragma unroll
@@ -315,88 +403,17 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                     raw[ch][i] = row < p.R ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
             }
         }
-        const int n = min(max(__ldg(p.lens + b), 0), p.cap);
-        const int32_t* sel = p.selected ? p.selected + static_cast<int64_t>(e) * p.budget : nullptr;
-        const int nsel = p.selected ? min(max(__ldg(p.counts + e), 0), p.budget) : 0;
-        const int tokens = p.selected ? nsel << p.shift : n;  // places in the list of blocks
-        const int nb = (n + (1 << p.shift) - 1) >> p.shift;
-        const int32_t* table = p.table + static_cast<int64_t>(b) * p.maxb;
-        // this warp's tiles: first, first + kWarps, ... below last
-        const int first = from - s_begin + warp;
-        const int last = min(stop - s_begin, (tokens + kTile - 1) / kTile);
-
-        // ---- copies.  The lanes look up the blocks of the warp's next kWindow tiles together.
-        constexpr int kWindow = 32 / HB, kPart = kTile / HB;  // tokens of a block within a tile, at most
-        const uint32_t step = static_cast<uint32_t>(p.KV) * D;
-        const int8_t* pk = p.k + static_cast<int64_t>(kh) * D + copy_row * step + copy_run * 16;
-        const int8_t* pv = p.v + static_cast<int64_t>(kh) * D + copy_row * step + copy_run * 16;
-        const float* psc = (lane & 1 ? p.vs : p.ks) + kh;
-        const int own = lane >> 1 & (HB - 1);     // the part whose scale and place this lane stores
-        uint32_t w_row = 0;                       // of this lane's part of the window: its first row of the pool
-        int w_place = 0, blk_next = -1, phys_next = -1;
-        auto look_up = [&](int window) {
-            const int tile = first + (window * kWindow + lane / HB) * kWarps;
-            const int place = tile * kTile + kPart * (lane % HB);
-            int j = -1;
-            if (tile < last && place < tokens) {
-                j = place >> p.shift;
-                if (sel) {
-                    j = __ldg(sel + j);
-                    if (j < 0 || j >= nb) {
-                        if (j != -1)
-                            q8_report(p.status, PA_STATUS_BAD_BLOCK);
-                        j = -1;
-                    }
-                }
-            }
-            blk_next = j;
-            phys_next = j >= 0 ? __ldg(table + j) : -1;
-        };
-        auto take_up = [&](int window) {
-            const int tile = first + (window * kWindow + lane / HB) * kWarps;
-            const int in_block = (tile * kTile + kPart * (lane % HB)) & ((1 << p.shift) - 1);
-            const bool there = static_cast<uint32_t>(phys_next) < static_cast<uint32_t>(p.num_blocks);
-            if (!there && blk_next >= 0)
-                q8_report(p.status, PA_STATUS_BAD_BLOCK);
-            // (without a block: the first rows of the pool are read in its place, and hidden)
-            w_row = there ? (static_cast<uint32_t>(phys_next) << p.shift) + in_block : 0u;
-            w_place = there ? (blk_next << p.shift) + in_block : INT_MAX - 64;
-        };
-        auto issue = [&](int k, uint32_t st) {  // the warp's k-th tile
-            if (first + k * kWarps < last) {
-                const int at_window = k & (kWindow - 1);
-                if (at_window == 0 && k > 0)
-                    take_up(k / kWindow);
-                if (at_window == kWindow / 2)
-                    look_up(k / kWindow + 1);
-                const uint32_t own_row = __shfl_sync(kFullWarp, w_row, at_window * HB + own);
-                const int own_place = __shfl_sync(kFullWarp, w_place, at_window * HB + own);
-                if (lane < 2 * HB) {
-                    copy4(st + kTileBytes + lane * 4, psc + static_cast<uint64_t>(own_row >> p.shift) * p.KV);
-                    if ((lane & 1) == 0)
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + kTileBytes + 32 + 2 * lane), "r"(own_place) : "memory");
-                }
-#pragma unroll
-                for (int x = 0; x < HB; ++x) {
-                    const uint64_t at = static_cast<uint64_t>(__shfl_sync(kFullWarp, w_row, at_window * HB + x)) * step;
-                    const int8_t* k0 = pk + at;
-                    const int8_t* v0 = pv + at;
-#pragma unroll
-                    for (int i = 0; i < kPart / kRowsCopy; ++i) {
-                        const uint32_t to = st + (x * (kPart / kRowsCopy) + i) * 512;
-                        copy16(to + copy_k, k0 + i * kRowsCopy * step);
-                        copy16(to + kTile * D + (D == 128 && i & 1 ? copy_v ^ 64 : copy_v), v0 + i * kRowsCopy * step);
-                    }
-                }
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        look_up(0);
+        __syncwarp();  // the ring's last tiles have been read
         take_up(0);
 #pragma unroll
         for (int i = 0; i < S - 1; ++i)
             issue(i, ring + i * kStage);
+        return true;
+    };
+    if (!begin())
+        return;
 
+    for (;;) {
         // ---- query rows as fragments of B, scaled by a power of two
         if (warp < NT) {
             float x[kSteps * 4], a = 0.f;
@@ -694,8 +711,15 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
             st = st + kStage == ring + S * kStage ? ring : st + kStage;
             fill = fill + kStage == ring + S * kStage ? ring : fill + kStage;
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncthreads();  // the rings are free
+        // ---- what the end of this piece needs, and the start of the next
+        const bool whole = from == s_begin && stop == s_end;
+        // a piece of a segment begun by an earlier CTA, or one that goes on
+        const int64_t record = static_cast<int64_t>(blockIdx.x) * 2 + (u_begin > s_begin ? 0 : 1);
+        const int64_t out0 = ((static_cast<int64_t>(b) * p.KV + kh) * p.R + row_base) * D;
+        const int rows_left = p.R - row_base, seg_begin = s_begin, seg_end = s_end;
+        int* counter = p.counters + (static_cast<int64_t>(b) * p.KV + kh) * p.groups + grp;
+        u = stop;
+        const bool more = u < u_end && begin();
 
         // ---- the warps' states together
 #pragma unroll
@@ -711,52 +735,77 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                     sm_m[warp][row] = mx[nt][i];
                     sm_l[warp][row] = s;
                 }
-                float* to = state + (warp * kRows + row) * Sh::kStateRow + 2 * g;
-#pragma unroll
-                for (int s2 = 0; s2 < kSteps; ++s2)  // channels D / 8 g + 2 s2, + 1
-                    *reinterpret_cast<float2*>(to + s2 * Sh::kStateStep) = make_float2(o[s2][nt][i], o[s2][nt][i + 2]);
             }
-        __syncthreads();
-        const bool whole = from == s_begin && stop == s_end;
-        // a piece of a segment begun by an earlier CTA, or one that goes on
-        const int64_t record = static_cast<int64_t>(blockIdx.x) * 2 + (u_begin > s_begin ? 0 : 1);
-        const int64_t out0 = ((static_cast<int64_t>(b) * p.KV + kh) * p.R + row_base) * D;
+        __syncthreads();  // (and the rings of all warps are free, when there is no next piece)
         constexpr int kQuads = D / 4, kItems = kRows * kQuads;  // four channels each
+        constexpr int kPer = (kItems + kThreads - 1) / kThreads;
         constexpr int kBatch = 20;  // pieces loaded together
-        for (int x = tid; x < kItems; x += kThreads) {
-            const int row = x / kQuads, quad = x % kQuads;
-            if (row_base + row >= p.R)
+        float4 val[kPer];
+#pragma unroll
+        for (int x = 0; x < kPer; ++x)
+            val[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float* state = reinterpret_cast<float*>(more ? smem + Sh::kRing + Sh::kQueryBytes : smem);  // [warp][row] in steps
+        const int group = more ? Sh::kGroup : Sh::kLastGroup;
+        for (int w0 = 0; w0 < kWarps; w0 += group) {
+            if (w0 > 0)
+                __syncthreads();
+            if (warp >= w0 && warp < w0 + group) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int row = nt * 8 + 2 * t + i;
+                        float m = -INFINITY;
+#pragma unroll
+                        for (int w = 0; w < kWarps; ++w)
+                            m = fmaxf(m, sm_m[w][row]);
+                        const float f = mx[nt][i] == -INFINITY ? 0.f : fast_exp2(mx[nt][i] - m);
+                        float* to = state + ((warp - w0) * kRows + row) * Sh::kStateRow + 2 * g;
+#pragma unroll
+                        for (int s2 = 0; s2 < kSteps; ++s2)  // channels D / 8 g + 2 s2, + 1
+                            *reinterpret_cast<float2*>(to + s2 * Sh::kStateStep) = make_float2(o[s2][nt][i] * f, o[s2][nt][i + 2] * f);
+                    }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                const int x = tid + k * kThreads, row = x / kQuads, quad = x % kQuads;
+                if (x < kItems) {
+                    const float* at = state + row * Sh::kStateRow + quad / (D / 32) * 2 + quad % (D / 32) * 2 * Sh::kStateStep;
+                    for (int w = 0; w < group; ++w) {
+                        const float2 v0 = *reinterpret_cast<const float2*>(at + w * kRows * Sh::kStateRow);
+                        const float2 v1 = *reinterpret_cast<const float2*>(at + w * kRows * Sh::kStateRow + Sh::kStateStep);
+                        val[k].x += v0.x, val[k].y += v0.y, val[k].z += v1.x, val[k].w += v1.y;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int x = tid + k * kThreads, row = x / kQuads, quad = x % kQuads;
+            if (x >= kItems || row >= rows_left)
                 break;
-            float m = -INFINITY;
+            float m = -INFINITY, sum = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w)
                 m = fmaxf(m, sm_m[w][row]);
-            float sum = 0.f;
-            float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
-            const float* at = state + row * Sh::kStateRow + quad / (D / 32) * 2 + quad % (D / 32) * 2 * Sh::kStateStep;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = sm_m[w][row] == -INFINITY ? 0.f : fast_exp2(sm_m[w][row] - m);
-                sum = fmaf(sm_l[w][row], f, sum);
-                const float2 v0 = *reinterpret_cast<const float2*>(at + w * kRows * Sh::kStateRow);
-                const float2 v1 = *reinterpret_cast<const float2*>(at + w * kRows * Sh::kStateRow + Sh::kStateStep);
-                fma4(val, f, make_float4(v0.x, v0.y, v1.x, v1.y));
-            }
+            for (int w = 0; w < kWarps; ++w)
+                sum = fmaf(sm_l[w][row], sm_m[w][row] == -INFINITY ? 0.f : fast_exp2(sm_m[w][row] - m), sum);
             if (whole) {
                 const float r = sum == 0.f ? 0.f : 1.f / sum;
-                store_out(p, out0 + static_cast<int64_t>(x) * 4, make_float4(val.x * r, val.y * r, val.z * r, val.w * r));
+                store_out(p, out0 + static_cast<int64_t>(x) * 4, make_float4(val[k].x * r, val[k].y * r, val[k].z * r, val[k].w * r));
             } else {
-                *reinterpret_cast<float4*>(p.part_o + record * kRows * D + x * 4) = val;
+                *reinterpret_cast<float4*>(p.part_o + record * kRows * D + x * 4) = val[k];
                 if (quad == 0)
                     p.part_ml[record * kRows + row] = make_float2(m, sum);
             }
         }
         if (!whole) {
             // pieces of the segment: those of teams c0 .. c1
-            const int c0 = owner_of(s_begin), c1 = owner_of(s_end - 1);
+            const int c0 = owner_of(seg_begin), c1 = owner_of(seg_end - 1);
             __syncthreads();
             if (tid == 0) {
-                int* counter = p.counters + (static_cast<int64_t>(b) * p.KV + kh) * p.groups + grp;
                 __threadfence();
                 const int before = atomicAdd(counter, 1);
                 sm_last = before == c1 - c0;
@@ -769,12 +818,12 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                 // a row to each set of D / 4 lanes; their lanes hold the pieces' factors
                 const int pieces = c1 - c0 + 1;
                 // (the first team's range begins with the segment or earlier, the others' inside it)
-                auto record_of = [&](int i) { return (static_cast<int64_t>(c0 + i) * p.team + member) * 2 + (i > 0 ? 0 : 1); };
+                auto record_of = [&](int i) { return ((static_cast<int64_t>(c0 + i) << p.lg_team) + member) * 2 + (i > 0 ? 0 : 1); };
                 for (int x0 = warp * 32; x0 < kItems; x0 += kThreads) {
                     const int x = x0 + lane, row = x / kQuads, in_row = lane % kQuads;
-                    const bool live = row_base + row < p.R;
+                    const bool live = row < rows_left;
                     float m = -INFINITY, sum = 0.f;
-                    float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
+                    float4 all = make_float4(0.f, 0.f, 0.f, 0.f);
                     for (int i0 = 0; i0 < pieces; i0 += kQuads) {  // (one turn, mostly)
                         const int many = min(kQuads, pieces - i0);
                         const float* src = p.part_o + x * 4;
@@ -800,24 +849,24 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                         for (int k = 1; k < kQuads; k <<= 1)
                             part += __shfl_xor_sync(kFullWarp, part, k);
                         sum = fmaf(sum, old, part);
-                        val.x *= old, val.y *= old, val.z *= old, val.w *= old;
+                        all.x *= old, all.y *= old, all.z *= old, all.w *= old;
                         m = top;
                         for (int i = 0; i < many; i += kBatch) {
                             if (i > 0)
                                 load(i);
 #pragma unroll
                             for (int k = 0; k < kBatch; ++k)
-                                fma4(val, __shfl_sync(kFullWarp, f, (lane & ~(kQuads - 1)) + ((i + k) & (kQuads - 1))), v[k]);
+                                fma4(all, __shfl_sync(kFullWarp, f, (lane & ~(kQuads - 1)) + ((i + k) & (kQuads - 1))), v[k]);
                         }
                     }
                     const float r = sum == 0.f ? 0.f : 1.f / sum;
                     if (live)
-                        store_out(p, out0 + static_cast<int64_t>(x) * 4, make_float4(val.x * r, val.y * r, val.z * r, val.w * r));
+                        store_out(p, out0 + static_cast<int64_t>(x) * 4, make_float4(all.x * r, all.y * r, all.z * r, all.w * r));
                 }
             }
         }
-        __syncthreads();  // the next segment's copies overwrite the merged states
-        u = stop;
+        if (!more)
+            break;
     }
 }
 
@@ -833,18 +882,19 @@ Variant variant(int BLOCK)
     using Sh = Shape<D, NT, QP, C>;
     return {BLOCK == 8 ? reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 4, C>)
                        : reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 2, C>),
-            Sh::kRows, Sh::kThreads, C, static_cast<size_t>(Sh::kBody) + Sh::kQueryBytes};
+            Sh::kRows, Sh::kThreads, C, static_cast<size_t>(Sh::kRing) + Sh::kQueryBytes + Sh::kGroup * Sh::kState};
 }
 
 // `segments`: of 8 query rows.
 template <int D>
-Variant variant(int BLOCK, int dtype, int R, long long segments, int sms)
+Variant variant(int BLOCK, int dtype, int R, long long segments, int sms, int entries)
 {
     if (dtype == PA_F32)
         return R > 8 ? variant<D, 2, 2, 1>(BLOCK) : variant<D, 1, 2, 1>(BLOCK);
     if (R > 8)
         return R > 16 ? variant<D, 4, 1, 1>(BLOCK) : variant<D, 2, 1, 1>(BLOCK);
-    return segments > sms / 2 ? variant<D, 1, 1, 2>(BLOCK) : variant<D, 1, 1, 1>(BLOCK);
+    const Variant two = variant<D, 1, 1, 2>(BLOCK);
+    return segments > sms / 2 && two.body + 4 * static_cast<size_t>(entries) <= 114000 ? two : variant<D, 1, 1, 1>(BLOCK);
 }
 
 // Sizes that pa_q8_decode refuses, apart from those of the cache.
@@ -941,10 +991,11 @@ extern "C" int pa_q8_decode(const void* q, const int8_t* k_cache, const int8_t* 
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return PA_ERR_CUDA;
     const long long segments = static_cast<long long>(B) * KV;
-    const Variant v = D == 64 ? variant<64>(BLOCK, o.dtype, R, segments, sms) : variant<128>(BLOCK, o.dtype, R, segments, sms);
+    const int entries = o.selected ? B * KV : B;
+    const Variant v = D == 64 ? variant<64>(BLOCK, o.dtype, R, segments, sms, entries) : variant<128>(BLOCK, o.dtype, R, segments, sms, entries);
     DecodeParams p{};
     p.groups = (R + v.rows - 1) / v.rows;
-    p.entries = o.selected ? B * KV : B;
+    p.entries = entries;
     const long long copies = o.selected ? p.groups : static_cast<long long>(KV) * p.groups;
     const long long most = o.selected ? static_cast<long long>(o.budget) * BLOCK : static_cast<long long>(o.max_blocks) * BLOCK;
     const long long tiles = (most + kTile - 1) / kTile + kCharge;
@@ -981,9 +1032,10 @@ extern "C" int pa_q8_decode(const void* q, const int8_t* k_cache, const int8_t* 
     const int grid = sms * v.ctas > kMaxCtas ? kMaxCtas : sms * v.ctas;
     // Teams: the copies of one length that run side by side (rows of the same or of
     // neighbouring heads, whose cache lines lie together)
-    p.team = copies % 4 == 0 ? 4 : copies % 2 == 0 ? 2 : 1;
-    if (grid % p.team != 0)
-        p.team = 1;
+    p.lg_team = copies % 4 == 0 ? 2 : copies % 2 == 0 ? 1 : 0;
+    if (grid % (1 << p.lg_team) != 0)
+        p.lg_team = 0;
+    p.copies = static_cast<int>(copies >> p.lg_team);
     void* args[] = {&p};
     return q8_launch(v.fn, dim3(grid), v.threads, v.body + (static_cast<size_t>(p.entries) + 1) * 4, static_cast<cudaStream_t>(stream), args);
 }

@@ -66,32 +66,34 @@ struct Run {
             }
         }
     }
-    // Largest magnitude, as an integer of the type's width in the order of the
-    // magnitudes (two 16-bit ones side by side).
+    // Largest magnitude, NaN where an element is none (16-bit: two side by side).
     __device__ __forceinline__ uint32_t largest(uint32_t m) const
     {
 #pragma unroll
         for (int i = 0; i < 4 * kVectors; ++i) {
             if constexpr (sizeof(T) == 4)
-                m = max(m, word(i) & 0x7fffffffu);
+                asm("max.NaN.f32 %0, %0, %1;" : "+r"(m) : "r"(word(i) & 0x7fffffffu));
+            else if constexpr (std::is_same_v<T, __half>)
+                asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(m) : "r"(word(i) & 0x7fff7fffu));
             else
-                asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(word(i) & 0x7fff7fffu));
+                asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(word(i) & 0x7fff7fffu));
         }
         return m;
     }
 };
 
-// The magnitude of largest()'s integer; infinite or NaN where an element is.
+// The magnitude of largest()'s word.
 template <typename T>
 __device__ __forceinline__ float magnitude(uint32_t m)
 {
     if constexpr (sizeof(T) == 4)
         return __uint_as_float(m);
-    const uint32_t x = max(m & 0xffffu, m >> 16);
+    float2 f;
     if constexpr (std::is_same_v<T, __half>)
-        return __half2float(__ushort_as_half(static_cast<unsigned short>(x)));
+        f = __half22float2(*reinterpret_cast<const __half2*>(&m));
     else
-        return __uint_as_float(x << 16);
+        f = make_float2(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    return f.x + f.y == f.x + f.y ? fmaxf(f.x, f.y) : f.x + f.y;
 }
 
 __device__ __forceinline__ float element(const float* p) { return *p; }
@@ -132,34 +134,30 @@ __device__ __forceinline__ uint4 run_codes(int8_t* dst, const Run<T>& r, const T
     return codes;
 }
 
-// Lowest and highest of two 16-bit integers each.
+// Lowest and highest of two fp16 codes each.
 __device__ __forceinline__ uint32_t lowest2(uint32_t a, uint32_t b)
 {
     uint32_t r;
-    asm("min.s16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
 __device__ __forceinline__ uint32_t highest2(uint32_t a, uint32_t b)
 {
     uint32_t r;
-    asm("max.s16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
-// Bytes 0 and 1 (2 and 3: upper) of a word as 16-bit integers.
-__device__ __forceinline__ uint32_t widen(uint32_t w, bool upper)
-{
-    uint32_t r;
-    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(w), "r"(upper ? 0xb3a2u : 0x9180u));
-    return r;
-}
-
-// Low bytes of 16-bit integers.
+// Eight words of two fp16 codes as bytes: code + 1152 has code + 128 in its low byte.
 __device__ __forceinline__ uint4 pack_codes(const uint32_t* two)
 {
-    return make_uint4(__byte_perm(two[0], two[1], 0x6420), __byte_perm(two[2], two[3], 0x6420),
-                      __byte_perm(two[4], two[5], 0x6420), __byte_perm(two[6], two[7], 0x6420));
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        asm("add.f16x2 %0, %1, %2;" : "=r"(w[i]) : "r"(two[i]), "r"(0x64806480u));
+    return make_uint4(__byte_perm(w[0], w[1], 0x6420) ^ 0x80808080u, __byte_perm(w[2], w[3], 0x6420) ^ 0x80808080u,
+                      __byte_perm(w[4], w[5], 0x6420) ^ 0x80808080u, __byte_perm(w[6], w[7], 0x6420) ^ 0x80808080u);
 }
 
 // grid (blocks a sequence's new rows may touch, ceil(KV / heads of a CTA), B)
@@ -261,8 +259,8 @@ __global__ void __launch_bounds__(kStoreThreads) pa_q8_append_kernel(const __gri
     uint32_t lo[8], hi[8];  // of this thread's keys: lowest and highest code by channel, two a word
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        lo[i] = 0x007f007fu;
-        hi[i] = 0xff81ff81u;
+        lo[i] = 0x57f057f0u;  // 127
+        hi[i] = 0xd7f0d7f0u;  // -127
     }
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
@@ -290,7 +288,7 @@ __global__ void __launch_bounds__(kStoreThreads) pa_q8_append_kernel(const __gri
                 const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const uint32_t two = widen(w[i >> 1], i & 1);
+                    const uint32_t two = codes2(w[i >> 1] ^ 0x80808080u, i & 1 ? 0x4342 : 0x4140);
                     lo[i] = lowest2(lo[i], two);
                     hi[i] = highest2(hi[i], two);
                 }
