@@ -37,8 +37,8 @@ namespace {
 constexpr int kTile = 32;                 // tokens of a tile: two MMA groups of 16
 constexpr int kMaxEntries = 4096;         // prefix sums in shared memory
 constexpr int kMaxCtas = 304;             // two per SM
-constexpr int kJoinTiles = 14;            // tiles that joining the pieces of a segment counts for
-constexpr int kCharge = 6;                // tiles that a piece's start and end count for
+constexpr int kChargeBytes = 14 << 13;    // a piece's start and end count for so many bytes of tiles
+constexpr int kJoinBytes = 8 << 13;       // joining the pieces of a segment, besides
 constexpr int kMeta = 64;                 // bytes of a tile's scales and places
 constexpr float kLift = 6.f, kSlack = 8.f;  // weights are 2^(t - m + 6), t - m <= 8
 
@@ -122,6 +122,7 @@ struct Shape {
     static constexpr int kTileBytes = 2 * kTile * D, kStage = kTileBytes + kMeta;
     static constexpr int kStages = 2 * (D == 128 ? 1 : 2);
     static constexpr int kRing = kWarps * kStages * kStage;
+    static constexpr int kCharge = kChargeBytes / kTileBytes, kJoin = kJoinBytes / kTileBytes;  // in tiles
     // a warp's state in shared memory: steps of 16 + 4 floats, rows 4 (mod 32) floats
     // apart, so that neither its writes nor its reads meet a bank twice
     static constexpr int kStateStep = 20, kStateRow = kSteps * kStateStep + 4, kState = kRows * kStateRow * 4;
@@ -163,6 +164,15 @@ __device__ __forceinline__ void fma4(float4& a, float f, float4 v)
     a.w = fmaf(f, v.w, a.w);
 }
 
+// A segment of which this CTA has left a record: its first team, its pieces (0:
+// another CTA joins them), where its rows go.
+struct OpenPiece {
+    int first, pieces;
+    int* counter;
+    int64_t out;
+    int rows;
+};
+
 template <int D, int NT, int QP, int HB, int C>
 __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode_kernel(const __grid_constant__ DecodeParams p)
 {
@@ -175,13 +185,13 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
     // the row's 128 is taken off the score beforehand.  (Keys only: the values'
     // weights have one sign, and their sum would swamp the output.)
     constexpr bool kSmall = QP == 1;
-    constexpr int J = Sh::kJoint;
+    constexpr int J = Sh::kJoint, kCharge = Sh::kCharge;
     extern __shared__ __align__(16) unsigned char smem[];  // ring | query fragments | states | prefix sums
     __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
     __shared__ float sm_f[kRows];  // of a row's scores: scale * log2(e) / the power of two
     __shared__ float sm_off[kRows];  // what a row's scores begin with (kSmall)
     __shared__ int sm_lim[kRows];  // keys that the row sees
-    __shared__ int sm_last;
+    __shared__ OpenPiece sm_open[2];
     grid_dependents_launch();
     grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -266,13 +276,14 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
     const int copies = p.copies, team = blockIdx.x >> p.lg_team, member = blockIdx.x & ((1 << p.lg_team) - 1);
     const int teams = gridDim.x >> p.lg_team;
     const int U = prefix[p.entries] * copies;  // (below 2^31: the host has seen to it)
-    const int G = min(teams, (U + kCharge + kWarps - 1) / (kCharge + kWarps));
+    const int G = min(teams, (U + kCharge + 3) / (kCharge + 4));
     // U = G share + extra: the first `extra` teams take one tile more
     const int share = U / G, extra = U - G * share;
     auto owner_of = [&](int x) { return x < extra * (share + 1) ? x / (share + 1) : extra + (x - extra * (share + 1)) / share; };
     int u_begin, u_end;
-    if (p.entries * copies <= teams && longest <= share + kJoinTiles) {
-        // a segment to each team: the longest takes no more than a share and a join
+    if (p.entries * copies <= teams && longest <= share + kCharge + Sh::kJoin) {
+        // a segment to each team: the longest takes no more than a share, the start and
+        // end of the second piece that a cut leaves most CTAs, and the join
         if (team >= p.entries * copies)
             return;
         const int e = team / copies, length = prefix[e + 1] - prefix[e];
@@ -286,8 +297,8 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
     }
 
     // ---- a piece: tiles from .. stop - 1 of a segment (tiles s_begin .. s_end - 1)
-    int u = u_begin, s_begin, s_end, from, stop;
-    int b, kh, grp, row_base, n, tokens, nb, first, last;
+    int u = u_begin, s_begin = 0, s_end = 0, from = 0, stop = 0;
+    int b = 0, kh = 0, grp = 0, row_base = 0, n = 0, tokens = 0, nb = 0, first = 0, last = 0;
     const int32_t* sel;
     const int32_t* table;
     uint4 raw[kChunks][QP * 2];  // query rows: one warp a group of eight; 16 elements a chunk
@@ -410,10 +421,110 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
             issue(i, ring + i * kStage);
         return true;
     };
-    if (!begin())
-        return;
-
+    float o[kSteps][NT][4];
+    float mx[NT][2], l[NT][2];
+    int open = 0;  // pieces of this CTA that leave a record: at most the first and the last
+    bool have = false;
     for (;;) {
+        // ---- what the end of the piece in hand needs, and the start of the next
+        const bool whole = from == s_begin && stop == s_end;
+        // a piece of a segment begun by an earlier CTA, or one that goes on
+        const int slot = u_begin > s_begin ? 0 : 1;
+        const int64_t out0 = ((static_cast<int64_t>(b) * p.KV + kh) * p.R + row_base) * D;
+        const int rows_left = p.R - row_base;
+        if (have && !whole && tid == 0) {
+            const int c0 = owner_of(s_begin), c1 = owner_of(s_end - 1);
+            sm_open[open] = {c0, c1 - c0 + 1, p.counters + (static_cast<int64_t>(b) * p.KV + kh) * p.groups + grp, out0, rows_left};
+        }
+        if (have)
+            u = stop;
+        const bool more = u < u_end && begin();
+        if (have) {
+            // ---- the warps' states together
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int row = nt * 8 + 2 * t + i;
+                    float s = l[nt][i];
+                    s += __shfl_xor_sync(kFullWarp, s, 4);
+                    s += __shfl_xor_sync(kFullWarp, s, 8);
+                    s += __shfl_xor_sync(kFullWarp, s, 16);
+                    if (g == 0) {
+                        sm_m[warp][row] = mx[nt][i];
+                        sm_l[warp][row] = s;
+                    }
+                }
+            __syncthreads();  // (without a next piece, the rings of all warps are free then)
+            constexpr int kQuads = D / 4, kItems = kRows * kQuads;  // four channels each
+            constexpr int kPer = (kItems + kThreads - 1) / kThreads;
+            float4 val[kPer];
+#pragma unroll
+            for (int x = 0; x < kPer; ++x)
+                val[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            float* state = reinterpret_cast<float*>(more ? smem + Sh::kRing + Sh::kQueryBytes : smem);  // [warp][row] in steps
+            const int group = more ? Sh::kGroup : Sh::kLastGroup;
+            for (int w0 = 0; w0 < kWarps; w0 += group) {
+                if (w0 > 0)
+                    __syncthreads();
+                if (warp >= w0 && warp < w0 + group) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int row = nt * 8 + 2 * t + i;
+                            float m = -INFINITY;
+#pragma unroll
+                            for (int w = 0; w < kWarps; ++w)
+                                m = fmaxf(m, sm_m[w][row]);
+                            const float f = mx[nt][i] == -INFINITY ? 0.f : fast_exp2(mx[nt][i] - m);
+                            float* to = state + ((warp - w0) * kRows + row) * Sh::kStateRow + 2 * g;
+#pragma unroll
+                            for (int s2 = 0; s2 < kSteps; ++s2)  // channels D / 8 g + 2 s2, + 1
+                                *reinterpret_cast<float2*>(to + s2 * Sh::kStateStep) = make_float2(o[s2][nt][i] * f, o[s2][nt][i + 2] * f);
+                        }
+                }
+                __syncthreads();
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) {
+                    const int x = tid + k * kThreads, row = x / kQuads, quad = x % kQuads;
+                    if (x < kItems) {
+                        const float* at = state + row * Sh::kStateRow + quad / (D / 32) * 2 + quad % (D / 32) * 2 * Sh::kStateStep;
+                        for (int w = 0; w < group; ++w) {
+                            const float2 v0 = *reinterpret_cast<const float2*>(at + w * kRows * Sh::kStateRow);
+                            const float2 v1 = *reinterpret_cast<const float2*>(at + w * kRows * Sh::kStateRow + Sh::kStateStep);
+                            val[k].x += v0.x, val[k].y += v0.y, val[k].z += v1.x, val[k].w += v1.y;
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                const int x = tid + k * kThreads, row = x / kQuads, quad = x % kQuads;
+                if (x >= kItems || row >= rows_left)
+                    break;
+                float m = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    m = fmaxf(m, sm_m[w][row]);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    sum = fmaf(sm_l[w][row], sm_m[w][row] == -INFINITY ? 0.f : fast_exp2(sm_m[w][row] - m), sum);
+                if (whole) {
+                    const float r = sum == 0.f ? 0.f : 1.f / sum;
+                    store_out(p, out0 + static_cast<int64_t>(x) * 4, make_float4(val[k].x * r, val[k].y * r, val[k].z * r, val[k].w * r));
+                } else {
+                    *reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * kRows * D + x * 4) = val[k];
+                    if (quad == 0)
+                        p.part_ml[(static_cast<int64_t>(blockIdx.x) * 2 + slot) * kRows + row] = make_float2(m, sum);
+                }
+            }
+            open += whole ? 0 : 1;
+        }
+        if (!more)
+            break;
+        have = true;
+
         // ---- query rows as fragments of B, scaled by a power of two
         if (warp < NT) {
             float x[kSteps * 4], a = 0.f;
@@ -496,8 +607,6 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
         // parts that begin here or before are seen by every row
         const int all_see = row_base + kRows > p.R ? INT_MIN : (p.causal ? n - p.NQ + 1 : n) - kPart;
 
-        float o[kSteps][NT][4];
-        float mx[NT][2], l[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -711,168 +820,84 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
             st = st + kStage == ring + S * kStage ? ring : st + kStage;
             fill = fill + kStage == ring + S * kStage ? ring : fill + kStage;
         }
-        // ---- what the end of this piece needs, and the start of the next
-        const bool whole = from == s_begin && stop == s_end;
-        // a piece of a segment begun by an earlier CTA, or one that goes on
-        const int64_t record = static_cast<int64_t>(blockIdx.x) * 2 + (u_begin > s_begin ? 0 : 1);
-        const int64_t out0 = ((static_cast<int64_t>(b) * p.KV + kh) * p.R + row_base) * D;
-        const int rows_left = p.R - row_base, seg_begin = s_begin, seg_end = s_end;
-        int* counter = p.counters + (static_cast<int64_t>(b) * p.KV + kh) * p.groups + grp;
-        u = stop;
-        const bool more = u < u_end && begin();
+    }
 
-        // ---- the warps' states together
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int row = nt * 8 + 2 * t + i;
-                float s = l[nt][i];
-                s += __shfl_xor_sync(kFullWarp, s, 4);
-                s += __shfl_xor_sync(kFullWarp, s, 8);
-                s += __shfl_xor_sync(kFullWarp, s, 16);
-                if (g == 0) {
-                    sm_m[warp][row] = mx[nt][i];
-                    sm_l[warp][row] = s;
-                }
+    // ---- the pieces that left a record: the last CTA to finish one of a segment joins them all
+    if (open > 0) {
+        __syncthreads();
+        if (tid == 0) {
+            __threadfence();
+            for (int i = 0; i < open; ++i) {
+                const int before = atomicAdd(sm_open[i].counter, 1);
+                if (before == sm_open[i].pieces - 1)
+                    *sm_open[i].counter = 0;
+                else
+                    sm_open[i].pieces = 0;
             }
-        __syncthreads();  // (and the rings of all warps are free, when there is no next piece)
-        constexpr int kQuads = D / 4, kItems = kRows * kQuads;  // four channels each
-        constexpr int kPer = (kItems + kThreads - 1) / kThreads;
-        constexpr int kBatch = 20;  // pieces loaded together
-        float4 val[kPer];
-#pragma unroll
-        for (int x = 0; x < kPer; ++x)
-            val[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-        float* state = reinterpret_cast<float*>(more ? smem + Sh::kRing + Sh::kQueryBytes : smem);  // [warp][row] in steps
-        const int group = more ? Sh::kGroup : Sh::kLastGroup;
-        for (int w0 = 0; w0 < kWarps; w0 += group) {
-            if (w0 > 0)
-                __syncthreads();
-            if (warp >= w0 && warp < w0 + group) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int row = nt * 8 + 2 * t + i;
-                        float m = -INFINITY;
-#pragma unroll
-                        for (int w = 0; w < kWarps; ++w)
-                            m = fmaxf(m, sm_m[w][row]);
-                        const float f = mx[nt][i] == -INFINITY ? 0.f : fast_exp2(mx[nt][i] - m);
-                        float* to = state + ((warp - w0) * kRows + row) * Sh::kStateRow + 2 * g;
-#pragma unroll
-                        for (int s2 = 0; s2 < kSteps; ++s2)  // channels D / 8 g + 2 s2, + 1
-                            *reinterpret_cast<float2*>(to + s2 * Sh::kStateStep) = make_float2(o[s2][nt][i] * f, o[s2][nt][i + 2] * f);
-                    }
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                const int x = tid + k * kThreads, row = x / kQuads, quad = x % kQuads;
-                if (x < kItems) {
-                    const float* at = state + row * Sh::kStateRow + quad / (D / 32) * 2 + quad % (D / 32) * 2 * Sh::kStateStep;
-                    for (int w = 0; w < group; ++w) {
-                        const float2 v0 = *reinterpret_cast<const float2*>(at + w * kRows * Sh::kStateRow);
-                        const float2 v1 = *reinterpret_cast<const float2*>(at + w * kRows * Sh::kStateRow + Sh::kStateStep);
-                        val[k].x += v0.x, val[k].y += v0.y, val[k].z += v1.x, val[k].w += v1.y;
-                    }
-                }
-            }
+            __threadfence();
         }
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const int x = tid + k * kThreads, row = x / kQuads, quad = x % kQuads;
-            if (x >= kItems || row >= rows_left)
-                break;
+        __syncthreads();
+    }
+    constexpr int kQuads = D / 4, kItems = kRows * kQuads;
+    constexpr int kBatch = 20;  // pieces loaded together
+    for (int which = 0; which < open; ++which) {
+        // a row to each set of D / 4 lanes; their lanes hold the pieces' factors
+        const int c0 = sm_open[which].first, pieces = sm_open[which].pieces, rows_left = sm_open[which].rows;
+        const int64_t out0 = sm_open[which].out;
+        if (pieces == 0)
+            continue;
+        // (the first team's range begins with the segment or earlier, the others' inside it)
+        auto record_of = [&](int i) { return ((static_cast<int64_t>(c0 + i) << p.lg_team) + member) * 2 + (i > 0 ? 0 : 1); };
+        for (int x0 = warp * 32; x0 < kItems; x0 += kThreads) {
+            const int x = x0 + lane, row = x / kQuads, in_row = lane % kQuads;
+            const bool live = row < rows_left;
             float m = -INFINITY, sum = 0.f;
+            float4 all = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i0 = 0; i0 < pieces; i0 += kQuads) {  // (one turn, mostly)
+                const int many = min(kQuads, pieces - i0);
+                const float* src = p.part_o + x * 4;
+                float4 v[kBatch];
+                auto load = [&](int i) {
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-                m = fmaxf(m, sm_m[w][row]);
+                    for (int k = 0; k < kBatch; ++k)
+                        v[k] = live && i + k < many ? __ldcg(reinterpret_cast<const float4*>(src + record_of(i0 + i + k) * kRows * D))
+                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+                };
+                load(0);
+                float2 ml = make_float2(-INFINITY, 0.f);
+                if (live && in_row < many)
+                    ml = __ldcg(p.part_ml + record_of(i0 + in_row) * kRows + row);
+                float top = ml.x;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-                sum = fmaf(sm_l[w][row], sm_m[w][row] == -INFINITY ? 0.f : fast_exp2(sm_m[w][row] - m), sum);
-            if (whole) {
-                const float r = sum == 0.f ? 0.f : 1.f / sum;
-                store_out(p, out0 + static_cast<int64_t>(x) * 4, make_float4(val[k].x * r, val[k].y * r, val[k].z * r, val[k].w * r));
-            } else {
-                *reinterpret_cast<float4*>(p.part_o + record * kRows * D + x * 4) = val[k];
-                if (quad == 0)
-                    p.part_ml[record * kRows + row] = make_float2(m, sum);
-            }
-        }
-        if (!whole) {
-            // pieces of the segment: those of teams c0 .. c1
-            const int c0 = owner_of(seg_begin), c1 = owner_of(seg_end - 1);
-            __syncthreads();
-            if (tid == 0) {
-                __threadfence();
-                const int before = atomicAdd(counter, 1);
-                sm_last = before == c1 - c0;
-                if (before == c1 - c0)
-                    *counter = 0;
-                __threadfence();
-            }
-            __syncthreads();
-            if (sm_last) {
-                // a row to each set of D / 4 lanes; their lanes hold the pieces' factors
-                const int pieces = c1 - c0 + 1;
-                // (the first team's range begins with the segment or earlier, the others' inside it)
-                auto record_of = [&](int i) { return ((static_cast<int64_t>(c0 + i) << p.lg_team) + member) * 2 + (i > 0 ? 0 : 1); };
-                for (int x0 = warp * 32; x0 < kItems; x0 += kThreads) {
-                    const int x = x0 + lane, row = x / kQuads, in_row = lane % kQuads;
-                    const bool live = row < rows_left;
-                    float m = -INFINITY, sum = 0.f;
-                    float4 all = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int i0 = 0; i0 < pieces; i0 += kQuads) {  // (one turn, mostly)
-                        const int many = min(kQuads, pieces - i0);
-                        const float* src = p.part_o + x * 4;
-                        float4 v[kBatch];
-                        auto load = [&](int i) {
+                for (int k = 1; k < kQuads; k <<= 1)
+                    top = fmaxf(top, __shfl_xor_sync(kFullWarp, top, k));
+                top = fmaxf(top, m);
+                const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top), old = m == -INFINITY ? 0.f : fast_exp2(m - top);
+                float part = ml.y * f;
 #pragma unroll
-                            for (int k = 0; k < kBatch; ++k)
-                                v[k] = live && i + k < many ? __ldcg(reinterpret_cast<const float4*>(src + record_of(i0 + i + k) * kRows * D))
-                                                            : make_float4(0.f, 0.f, 0.f, 0.f);
-                        };
-                        load(0);
-                        float2 ml = make_float2(-INFINITY, 0.f);
-                        if (live && in_row < many)
-                            ml = __ldcg(p.part_ml + record_of(i0 + in_row) * kRows + row);
-                        float top = ml.x;
+                for (int k = 1; k < kQuads; k <<= 1)
+                    part += __shfl_xor_sync(kFullWarp, part, k);
+                sum = fmaf(sum, old, part);
+                all.x *= old, all.y *= old, all.z *= old, all.w *= old;
+                m = top;
+                for (int i = 0; i < many; i += kBatch) {
+                    if (i > 0)
+                        load(i);
 #pragma unroll
-                        for (int k = 1; k < kQuads; k <<= 1)
-                            top = fmaxf(top, __shfl_xor_sync(kFullWarp, top, k));
-                        top = fmaxf(top, m);
-                        const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top), old = m == -INFINITY ? 0.f : fast_exp2(m - top);
-                        float part = ml.y * f;
-#pragma unroll
-                        for (int k = 1; k < kQuads; k <<= 1)
-                            part += __shfl_xor_sync(kFullWarp, part, k);
-                        sum = fmaf(sum, old, part);
-                        all.x *= old, all.y *= old, all.z *= old, all.w *= old;
-                        m = top;
-                        for (int i = 0; i < many; i += kBatch) {
-                            if (i > 0)
-                                load(i);
-#pragma unroll
-                            for (int k = 0; k < kBatch; ++k)
-                                fma4(all, __shfl_sync(kFullWarp, f, (lane & ~(kQuads - 1)) + ((i + k) & (kQuads - 1))), v[k]);
-                        }
-                    }
-                    const float r = sum == 0.f ? 0.f : 1.f / sum;
-                    if (live)
-                        store_out(p, out0 + static_cast<int64_t>(x) * 4, make_float4(all.x * r, all.y * r, all.z * r, all.w * r));
+                    for (int k = 0; k < kBatch; ++k)
+                        fma4(all, __shfl_sync(kFullWarp, f, (lane & ~(kQuads - 1)) + ((i + k) & (kQuads - 1))), v[k]);
                 }
             }
+            const float r = sum == 0.f ? 0.f : 1.f / sum;
+            if (live)
+                store_out(p, out0 + static_cast<int64_t>(x) * 4, make_float4(all.x * r, all.y * r, all.z * r, all.w * r));
         }
-        if (!more)
-            break;
     }
 }
 
 struct Variant {
     const void* fn;
-    int rows, threads, ctas;
+    int rows, threads, ctas, charge;
     size_t body;  // shared memory apart from the prefix sums
 };
 
@@ -882,7 +907,7 @@ Variant variant(int BLOCK)
     using Sh = Shape<D, NT, QP, C>;
     return {BLOCK == 8 ? reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 4, C>)
                        : reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 2, C>),
-            Sh::kRows, Sh::kThreads, C, static_cast<size_t>(Sh::kRing) + Sh::kQueryBytes + Sh::kGroup * Sh::kState};
+            Sh::kRows, Sh::kThreads, C, Sh::kCharge, static_cast<size_t>(Sh::kRing) + Sh::kQueryBytes + Sh::kGroup * Sh::kState};
 }
 
 // `segments`: of 8 query rows.
@@ -998,7 +1023,7 @@ extern "C" int pa_q8_decode(const void* q, const int8_t* k_cache, const int8_t* 
     p.entries = entries;
     const long long copies = o.selected ? p.groups : static_cast<long long>(KV) * p.groups;
     const long long most = o.selected ? static_cast<long long>(o.budget) * BLOCK : static_cast<long long>(o.max_blocks) * BLOCK;
-    const long long tiles = (most + kTile - 1) / kTile + kCharge;
+    const long long tiles = (most + kTile - 1) / kTile + v.charge;
     if (p.entries * tiles * copies >= (1ll << 31))
         return PA_ERR_BAD_DIMS;
     p.q = q;
