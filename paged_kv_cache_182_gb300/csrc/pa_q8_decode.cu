@@ -37,7 +37,7 @@ namespace {
 constexpr int kTile = 32;                 // tokens of a tile: two MMA groups of 16
 constexpr int kMaxEntries = 4096;         // prefix sums in shared memory
 constexpr int kMaxCtas = 304;             // two per SM
-constexpr int kChargeBytes = 14 << 13;    // a piece's start and end count for so many bytes of tiles
+constexpr int kChargeBytes = 32 << 13;    // a piece's start and end count for so many bytes of tiles on an SM
 constexpr int kJoinBytes = 8 << 13;       // joining the pieces of a segment, besides
 constexpr int kMeta = 64;                 // bytes of a tile's scales and places
 constexpr float kLift = 6.f, kSlack = 8.f;  // weights are 2^(t - m + 6), t - m <= 8
@@ -122,7 +122,7 @@ struct Shape {
     static constexpr int kTileBytes = 2 * kTile * D, kStage = kTileBytes + kMeta;
     static constexpr int kStages = 2 * (D == 128 ? 1 : 2);
     static constexpr int kRing = kWarps * kStages * kStage;
-    static constexpr int kCharge = kChargeBytes / kTileBytes, kJoin = kJoinBytes / kTileBytes;  // in tiles
+    static constexpr int kCharge = kChargeBytes / C / kTileBytes, kJoin = kJoinBytes / kTileBytes;  // in tiles
     // a warp's state in shared memory: steps of 16 + 4 floats, rows 4 (mod 32) floats
     // apart, so that neither its writes nor its reads meet a bank twice
     static constexpr int kStateStep = 20, kStateRow = kSteps * kStateStep + 4, kState = kRows * kStateRow * 4;
@@ -219,32 +219,34 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
 
     // prefix sums of the tiles of the entries (sequences, or sequences and KV
     // heads where each has its own blocks), each with the charge of a piece
-    int longest;
+    int longest = 0;
+    auto tiles_of = [&](int e) -> int {
+        int tokens;
+        if (p.selected) {
+            const int c = __ldg(p.counts + e);
+            if ((c < 0 || c > p.budget) && blockIdx.x == 0)
+                q8_report(p.status, PA_STATUS_BAD_LENGTH);
+            tokens = min(max(c, 0), p.budget) << p.shift;
+        } else {
+            const int n = __ldg(p.lens + e);
+            if ((n < 0 || n > p.cap) && blockIdx.x == 0)
+                q8_report(p.status, PA_STATUS_BAD_LENGTH);
+            tokens = min(max(n, 0), p.cap);
+        }
+        const int u = max(1, (tokens + kTile - 1) / kTile);
+        longest = max(longest, u);
+        return kCharge + u;
+    };
     {
         int* sums = reinterpret_cast<int*>(&sm_m[0][0]);
         const int per = (p.entries + kThreads - 1) / kThreads;
         const int e0 = min(tid * per, p.entries), e1 = min(e0 + per, p.entries);
         int sum = 0;
-        longest = 0;
         for (int e = e0; e < e1; ++e) {
-            int tokens;
-            if (p.selected) {
-                const int c = __ldg(p.counts + e);
-                if ((c < 0 || c > p.budget) && blockIdx.x == 0)
-                    q8_report(p.status, PA_STATUS_BAD_LENGTH);
-                tokens = min(max(c, 0), p.budget) << p.shift;
-            } else {
-                const int n = __ldg(p.lens + e);
-                if ((n < 0 || n > p.cap) && blockIdx.x == 0)
-                    q8_report(p.status, PA_STATUS_BAD_LENGTH);
-                tokens = min(max(n, 0), p.cap);
-            }
-            const int u = kCharge + max(1, (tokens + kTile - 1) / kTile);
-            prefix[e] = u;
-            sum += u;
-            longest = max(longest, u);
+            const int v = tiles_of(e);
+            prefix[e] = v;
+            sum += v;
         }
-        longest = __reduce_max_sync(kFullWarp, longest);
         int incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -252,9 +254,10 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
             if (lane >= o)
                 incl += y;
         }
+        const int most = __reduce_max_sync(kFullWarp, longest);
         if (lane == 31) {
             sums[warp] = incl;
-            sums[kWarps + warp] = longest;
+            sums[kWarps + warp] = most;
         }
         __syncthreads();
         int at = incl - sum;
@@ -263,32 +266,76 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
             longest = max(longest, sums[kWarps + w]);
         }
         for (int e = e0; e < e1; ++e) {
-            const int u = prefix[e];
+            const int v = prefix[e];
             prefix[e] = at;
-            at += u;
+            at += v;
         }
         if (tid == kThreads - 1)
             prefix[p.entries] = at;
         __syncthreads();
     }
-    // Teams of p.team CTAs walk the same tokens of neighbouring KV heads (or of
-    // groups of rows of one head); `copies` segments of a team share an entry's length.
+    // Teams of CTAs walk the same tokens of neighbouring KV heads (or of groups of
+    // rows of one head); `copies` segments of a team share an entry's length.
     const int copies = p.copies, team = blockIdx.x >> p.lg_team, member = blockIdx.x & ((1 << p.lg_team) - 1);
-    const int teams = gridDim.x >> p.lg_team;
+    const int teams = gridDim.x >> p.lg_team, segments = p.entries * copies;
     const int U = prefix[p.entries] * copies;  // (below 2^31: the host has seen to it)
     const int G = min(teams, (U + kCharge + 3) / (kCharge + 4));
     // U = G share + extra: the first `extra` teams take one tile more
     const int share = U / G, extra = U - G * share;
     auto owner_of = [&](int x) { return x < extra * (share + 1) ? x / (share + 1) : extra + (x - extra * (share + 1)) / share; };
-    int u_begin, u_end;
-    if (p.entries * copies <= teams && longest <= share + kCharge + Sh::kJoin) {
-        // a segment to each team: the longest takes no more than a share, the start and
-        // end of the second piece that a cut leaves most CTAs, and the join
-        if (team >= p.entries * copies)
+    // Segments whole, or in equal pieces of at most `piece` tiles, one a team, where
+    // the largest is no more than a share: a share starts a second segment on most
+    // teams, which costs them another start and end.
+    int piece = 0;
+    if (segments <= teams) {
+        piece = longest;
+        if (segments < teams) {
+            const int cut = max(4, (U - segments * kCharge + teams - segments - 1) / (teams - segments));
+            if (cut + Sh::kJoin < longest)
+                piece = cut;
+        }
+        if ((piece < longest ? piece : piece - Sh::kJoin) > share)
+            piece = 0;
+    }
+    int u_begin, u_end, first_team = 0, own_pieces = 1;
+    if (piece > 0) {
+        int e = copies == 1 ? team : team / copies;
+        first_team = e * copies;
+        if (piece < longest) {
+            // every warp for itself: the entry whose pieces hold this team
+            int before = 0;
+            bool found = false;
+            for (int e0 = 0; e0 < p.entries && !found; e0 += 32) {
+                const int v = e0 + lane < p.entries ? (prefix[e0 + lane + 1] - prefix[e0 + lane] - kCharge + piece - 1) / piece : 0;
+                int incl = v;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(kFullWarp, incl, o);
+                    if (lane >= o)
+                        incl += y;
+                }
+                const uint32_t here = __ballot_sync(kFullWarp, (before + incl) * copies > team);
+                if (here != 0) {
+                    const int at = __ffs(here) - 1;
+                    e = e0 + at;
+                    own_pieces = __shfl_sync(kFullWarp, v, at);
+                    first_team = (before + __shfl_sync(kFullWarp, incl, at) - own_pieces) * copies;
+                    found = true;
+                }
+                before += __shfl_sync(kFullWarp, incl, 31);
+            }
+            if (!found)
+                return;
+        } else if (team >= segments) {
             return;
-        const int e = team / copies, length = prefix[e + 1] - prefix[e];
-        u_begin = prefix[e] * copies + (team - e * copies) * length;
-        u_end = u_begin + length;
+        }
+        const int length = prefix[e + 1] - prefix[e];
+        const int cc = copies == 1 ? 0 : (team - first_team) / own_pieces, i = team - first_team - cc * own_pieces;
+        first_team += cc * own_pieces;
+        const int tiles = length - kCharge, each = tiles / own_pieces, over = tiles - each * own_pieces;
+        const int base = prefix[e] * copies + cc * length + kCharge;
+        u_begin = i == 0 ? base - kCharge : base + i * each + min(i, over);
+        u_end = base + (i + 1) * each + min(i + 1, over);
     } else {
         if (team >= G)
             return;
@@ -433,8 +480,8 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
         const int64_t out0 = ((static_cast<int64_t>(b) * p.KV + kh) * p.R + row_base) * D;
         const int rows_left = p.R - row_base;
         if (have && !whole && tid == 0) {
-            const int c0 = owner_of(s_begin), c1 = owner_of(s_end - 1);
-            sm_open[open] = {c0, c1 - c0 + 1, p.counters + (static_cast<int64_t>(b) * p.KV + kh) * p.groups + grp, out0, rows_left};
+            const int c0 = piece > 0 ? first_team : owner_of(s_begin), count = piece > 0 ? own_pieces : owner_of(s_end - 1) - c0 + 1;
+            sm_open[open] = {c0, count, p.counters + (static_cast<int64_t>(b) * p.KV + kh) * p.groups + grp, out0, rows_left};
         }
         if (have)
             u = stop;
@@ -1062,5 +1109,5 @@ extern "C" int pa_q8_decode(const void* q, const int8_t* k_cache, const int8_t* 
         p.lg_team = 0;
     p.copies = static_cast<int>(copies >> p.lg_team);
     void* args[] = {&p};
-    return q8_launch(v.fn, dim3(grid), v.threads, v.body + (static_cast<size_t>(p.entries) + 1) * 4, static_cast<cudaStream_t>(stream), args);
+    return q8_launch(v.fn, dim3(grid), v.threads, v.body + (static_cast<size_t>(entries) + 1) * 4, static_cast<cudaStream_t>(stream), args);
 }
