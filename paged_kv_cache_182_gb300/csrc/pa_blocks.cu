@@ -40,6 +40,7 @@ struct PlanParams {
     const int32_t* starts;
     int* status;
     int B, N, BLOCK, maxb, num_blocks, cap, shift;
+    int vectors;  // rows of slots and positions are whole 16-byte vectors
 };
 
 struct Sequence {
@@ -183,22 +184,44 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(const __grid_cons
     }
     for (int at = count + me; at < left; at += step)
         p.stack[at] = entry(at);
-    // slots: equal ranges of the rows of all sequences
-    const int64_t rows = static_cast<int64_t>(B) * p.N;
-    for (int64_t x = me; x < rows; x += step) {
-        const int b = static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(p.N)), j = static_cast<int>(x - static_cast<int64_t>(b) * p.N);
+    // slots, four rows of a sequence at a time
+    const uint32_t quads = (static_cast<uint32_t>(p.N) + 3) / 4, total = static_cast<uint32_t>(B) * quads;
+    for (uint32_t x = me; x < total; x += step) {
+        const uint32_t b = x / quads;
+        const int j0 = static_cast<int>(x - b * quads) * 4;
         const int2 s = span[b];
-        int slot = -1, pos = -1;
-        if (j < s.y) {
-            const int t = s.x + j, blk = div_block(p, t);
-            const int phys = blk < held[b] ? p.table[static_cast<int64_t>(b) * p.maxb + blk]
-                                           : entry(there - 1 - (taken[b] + blk - held[b]));
-            slot = phys < 0 || phys >= p.num_blocks ? -1 : phys * p.BLOCK + (t - blk * p.BLOCK);
-            pos = p.starts ? __ldg(p.starts + b) + j : t;
+        int slot[4] = {-1, -1, -1, -1}, pos[4] = {-1, -1, -1, -1};
+        if (j0 < s.y) {
+            const int had = held[b], start = p.starts ? __ldg(p.starts + b) : s.x;
+            int blk = -1, base = -1;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int t = s.x + j0 + k;
+                if (j0 + k >= s.y)
+                    break;
+                if (div_block(p, t) != blk) {
+                    blk = div_block(p, t);
+                    const int phys = blk < had ? p.table[static_cast<int64_t>(b) * p.maxb + blk] : entry(there - 1 - (taken[b] + blk - had));
+                    base = phys < 0 || phys >= p.num_blocks ? INT_MIN : (phys - blk) * p.BLOCK;
+                }
+                slot[k] = base == INT_MIN ? -1 : base + t;
+                pos[k] = start + j0 + k;
+            }
         }
-        p.slots[x] = slot;
-        if (p.positions)
-            p.positions[x] = pos;
+        const int64_t at = static_cast<int64_t>(b) * p.N + j0;
+        if (p.vectors) {
+            *reinterpret_cast<int4*>(p.slots + at) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            if (p.positions)
+                *reinterpret_cast<int4*>(p.positions + at) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (j0 + k < p.N) {
+                    p.slots[at + k] = slot[k];
+                    if (p.positions)
+                        p.positions[at + k] = pos[k];
+                }
+        }
     }
 }
 
@@ -260,9 +283,10 @@ extern "C" int pa_plan_blocks(int32_t* block_table, const int32_t* seq_lens, int
     for (int e = 0; e < 30; ++e)
         if (1 << e == BLOCK)
             p.shift = e;
-    long long work = static_cast<long long>(B) * (N > 0 ? N : 1);
-    long long grid = (work + 2 * kPlanThreads - 1) / (2 * kPlanThreads);
-    grid = grid < 1 ? 1 : grid > 152 ? 152 : grid;
+    p.vectors = N % 4 == 0 && q8_a16(slots) && q8_a16(p.positions) ? 1 : 0;
+    // a CTA for about 512 groups of four rows, and two per SM at most
+    long long grid = (static_cast<long long>(B) * ((N + 3) / 4) + 511) / 512;
+    grid = grid < 1 ? 1 : grid > 304 ? 304 : grid;
     const size_t smem = static_cast<size_t>(B) * 20;
     void* args[] = {&p};
     return q8_launch(reinterpret_cast<const void*>(pa_plan_kernel), dim3(static_cast<unsigned>(grid)), kPlanThreads, smem,

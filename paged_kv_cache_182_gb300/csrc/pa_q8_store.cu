@@ -101,29 +101,42 @@ __device__ __forceinline__ float element(const __half* p) { return __half2float(
 __device__ __forceinline__ float element(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
 // Stores the codes of 16 elements (also at `src`) and returns them.  x / scale is
-// rounded to a whole number by adding 1.5 2^23; the product with 1 / scale is
-// within 2^-17 of the quotient, so that only one nearer than that to a half has to
-// be looked at again (one run in 1500), as has what is not finite: in a loop, to
-// keep the code short.
+// rounded to a whole number by adding 1.5 2^23.  The product with 1 / scale is
+// within 2^-17 of the quotient: only where that leaves the side of a half open is
+// the remainder x - r scale (exact in an fma) compared with half a step.  Ties are
+// no rarity: half of a block's largest magnitude is one (63.5 steps), and every
+// eighth run of bf16 rows has it.  What is not finite goes through a loop, to keep
+// the code short.
 template <typename T>
 __device__ __forceinline__ uint4 run_codes(int8_t* dst, const Run<T>& r, const T* src, float scale, float inv, bool odd)
 {
     constexpr float kWhole = 12582912.f;
-    float worst = 0.f;
+    float worst = 0.f, t[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float x = r.get(i);
+        t[i] = __fmaf_rn(x, inv, kWhole);
+        worst = fmaxf(worst, fabsf(__fmaf_rn(x, inv, -(t[i] - kWhole))));
+    }
+    if (worst > 0.49998f) {
+        const float half = 0.5f * scale;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float d = __fmaf_rn(-(t[i] - kWhole), scale, r.get(i));
+            const bool uneven = __float_as_uint(t[i]) & 1u;
+            if (d > half || (uneven && d == half))
+                t[i] += 1.f;
+            else if (d < -half || (uneven && d == -half))
+                t[i] -= 1.f;
+        }
+    }
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-        uint32_t c[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float x = r.get(i + k), t = __fmaf_rn(x, inv, kWhole);
-            worst = fmaxf(worst, fabsf(__fmaf_rn(x, inv, -(t - kWhole))));
-            c[k] = __float_as_uint(t);
-        }
-        w[i >> 2] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
-    }
+    for (int i = 0; i < 4; ++i)
+        w[i] = __byte_perm(__byte_perm(__float_as_uint(t[4 * i]), __float_as_uint(t[4 * i + 1]), 0x0040),
+                           __byte_perm(__float_as_uint(t[4 * i + 2]), __float_as_uint(t[4 * i + 3]), 0x0040), 0x5410);
     uint4 codes = make_uint4(w[0], w[1], w[2], w[3]);
-    if (odd || worst > 0.49998f) {
+    if (odd) {
 #pragma unroll 1
         for (int i = 0; i < 16; ++i)
             dst[i] = static_cast<int8_t>(q8_code(element(src + i), scale, inv));
