@@ -26,8 +26,22 @@ __device__ __forceinline__ void q8_report(int* status, int bit)
         atomicOr(status, bit);
 }
 
-// A block's scale for a largest magnitude: a / 127 rounded once.
-__device__ __forceinline__ float q8_scale_of(float a) { return fmaxf(__fdiv_rn(a, 127.f), kMinScale); }
+// A block's scale for a largest magnitude: a / 127 rounded once (the remainder of
+// a first quotient corrects it; compared with the division for every significand).
+__device__ __forceinline__ float q8_scale_of(float a)
+{
+    constexpr float r = 1.f / 127.f;
+    const float q = __fmul_rn(a, r);
+    return fmaxf(__fmaf_rn(__fmaf_rn(-127.f, q, a), r, q), kMinScale);
+}
+
+// 1 / x of the hardware (a unit in the last place).
+__device__ __forceinline__ float fast_rcp(float x)
+{
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // Largest of m and |x|, leaving out what is not finite.
 __device__ __forceinline__ float q8_amax(float m, float x)

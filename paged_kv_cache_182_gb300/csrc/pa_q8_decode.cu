@@ -96,18 +96,11 @@ __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, ui
 
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
-// log2 and 1 / x of the hardware (a unit in the last place or two).
+// log2 of the hardware.
 __device__ __forceinline__ float fast_log2(float x)
 {
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ float fast_rcp(float x)
-{
-    float y;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 

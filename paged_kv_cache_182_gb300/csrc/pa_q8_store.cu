@@ -20,6 +20,9 @@ namespace {
 
 constexpr int kStoreThreads = 256;
 
+// Threads of an append CTA for a block's rows of so many elements.
+__host__ __device__ constexpr int append_threads(int elements) { return elements / 32 < 64 ? 64 : elements / 32; }
+
 struct AppendParams {
     int8_t* cache[2];  // K, V
     float* scale[2];
@@ -100,34 +103,65 @@ __device__ __forceinline__ float element(const float* p) { return *p; }
 __device__ __forceinline__ float element(const __half* p) { return __half2float(*p); }
 __device__ __forceinline__ float element(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-// Stores the codes of 16 elements (also at `src`) and returns them.  x / scale is
-// rounded to a whole number by adding 1.5 2^23.  The product with 1 / scale is
-// within 2^-17 of the quotient: only where that leaves the side of a half open is
-// the remainder x - r scale (exact in an fma) compared with half a step.  Ties are
-// no rarity: half of a block's largest magnitude is one (63.5 steps), and every
-// eighth run of bf16 rows has it.  What is not finite goes through a loop, to keep
-// the code short.
+// How a block's values become whole numbers: by one product with `inv` and one
+// rounding (adding 1.5 2^23) where `sure`, else with a look at the remainder.
+//
+// 16-bit values under a scale made of their own largest magnitude a are sure.
+// Values and a are whole multiples of a unit u, so that x / (a / 127) is a half or
+// at least u / (254 x) >= 2^-19 of itself away from one; the scale is a / 127
+// (1 - e) with |e| <= 2^-24, and all halves go the way of e.  So `inv` is 1 / scale
+// times 1 +- 1.5 2^-22 in the direction of e (with the error of the reciprocal
+// between 2^-23 and 2^-21): halves fall on their side, nothing else crosses.  With
+// e = 0 the halves are ties, and with an earlier block's scale anything may lie next
+// to a half: then the checked way.
+struct Rounding {
+    float scale, inv;
+    bool sure;
+};
+
 template <typename T>
-__device__ __forceinline__ uint4 run_codes(int8_t* dst, const Run<T>& r, const T* src, float scale, float inv, bool odd)
+__device__ __forceinline__ Rounding rounding_of(float a, float scale)
+{
+    Rounding r{scale, fast_rcp(scale), false};
+    if constexpr (sizeof(T) == 2) {
+        const float e = __fmaf_rn(-127.f, scale, a);  // a - 127 scale: its sign is exact
+        if (e != 0.f && scale == q8_scale_of(a) && scale > kMinScale) {
+            r.inv = __fmaf_rn(r.inv, copysignf(1.5f / 4194304.f, e), r.inv);
+            r.sure = true;
+        }
+    }
+    return r;
+}
+
+// Stores the codes of 16 elements (also at `src`) and returns them.  The checked
+// way: the product with 1 / scale is within 2^-16 of the quotient; only where that
+// leaves the side of a half open is the remainder x - r scale (exact in an fma)
+// compared with half a step.  What is not finite goes through a loop, to keep the
+// code short.
+template <typename T>
+__device__ __forceinline__ uint4 run_codes(int8_t* dst, const Run<T>& r, const T* src, const Rounding& by, bool odd)
 {
     constexpr float kWhole = 12582912.f;
-    float worst = 0.f, t[16];
+    float t[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float x = r.get(i);
-        t[i] = __fmaf_rn(x, inv, kWhole);
-        worst = fmaxf(worst, fabsf(__fmaf_rn(x, inv, -(t[i] - kWhole))));
-    }
-    if (worst > 0.49998f) {
-        const float half = 0.5f * scale;
+    for (int i = 0; i < 16; ++i)
+        t[i] = __fmaf_rn(r.get(i), by.inv, kWhole);
+    if (!by.sure) {
+        float worst = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float d = __fmaf_rn(-(t[i] - kWhole), scale, r.get(i));
-            const bool uneven = __float_as_uint(t[i]) & 1u;
-            if (d > half || (uneven && d == half))
-                t[i] += 1.f;
-            else if (d < -half || (uneven && d == -half))
-                t[i] -= 1.f;
+        for (int i = 0; i < 16; ++i)
+            worst = fmaxf(worst, fabsf(__fmaf_rn(r.get(i), by.inv, -(t[i] - kWhole))));
+        if (worst > 0.49995f) {
+            const float half = 0.5f * by.scale;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float d = __fmaf_rn(-(t[i] - kWhole), by.scale, r.get(i));
+                const bool uneven = __float_as_uint(t[i]) & 1u;
+                if (d > half || (uneven && d == half))
+                    t[i] += 1.f;
+                else if (d < -half || (uneven && d == -half))
+                    t[i] -= 1.f;
+            }
         }
     }
     uint32_t w[4];
@@ -139,7 +173,7 @@ __device__ __forceinline__ uint4 run_codes(int8_t* dst, const Run<T>& r, const T
     if (odd) {
 #pragma unroll 1
         for (int i = 0; i < 16; ++i)
-            dst[i] = static_cast<int8_t>(q8_code(element(src + i), scale, inv));
+            dst[i] = static_cast<int8_t>(q8_code(element(src + i), by.scale, by.inv));
         codes = *reinterpret_cast<const uint4*>(dst);
     } else {
         *reinterpret_cast<uint4*>(dst) = codes;
@@ -174,15 +208,17 @@ __device__ __forceinline__ uint4 pack_codes(const uint32_t* two)
 }
 
 // grid (blocks a sequence's new rows may touch, ceil(KV / heads of a CTA), B)
+// (16-bit rows in 96 registers: 21.0 us for 12,300 rows of 8 heads; 124 by
+// themselves 22.5, 64 27.3)
 template <typename T, int D, int BLOCK>
-__global__ void __launch_bounds__(kStoreThreads) pa_q8_append_kernel(const __grid_constant__ AppendParams p)
+__global__ void __launch_bounds__(append_threads(BLOCK * D), sizeof(T) == 2 ? 672 / append_threads(BLOCK * D) : 1) pa_q8_append_kernel(const __grid_constant__ AppendParams p)
 {
     constexpr int kGroup = BLOCK * D / 32;           // threads of a block and head
-    constexpr int kThreads = kGroup < 64 ? 64 : kGroup;
+    constexpr int kThreads = append_threads(BLOCK * D);
     constexpr int kHeads = kThreads / kGroup;        // heads of a CTA
     constexpr int kRuns = D / 16, kRows = kGroup / kRuns;  // a thread's rows: r, r + kRows (= BLOCK / 2)
     __shared__ float part[2][kThreads / 32];
-    __shared__ uint32_t ends[2][kThreads / 32][kRuns * 8];  // lowest, highest codes by warp
+    __shared__ __align__(16) uint32_t ends[kThreads / 32][2][kRuns * 8];  // lowest, highest codes by warp
     grid_dependents_launch();
     grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -204,10 +240,12 @@ __global__ void __launch_bounds__(kStoreThreads) pa_q8_append_kernel(const __gri
     Run<T> x[2][2];  // keys, values
     bool fresh[2];
     uint32_t most[2] = {0, 0};
-    auto src_of = [&](int kv, int k) {
-        return static_cast<const T*>(p.rows[kv]) + b * p.stride[kv][0] + h * p.stride[kv][1] +
-               (first + row0 + k * kRows - past) * p.stride[kv][2] + run * 16;
-    };
+    const T* rows[2];
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+        rows[kv] = static_cast<const T*>(p.rows[kv]) + b * p.stride[kv][0] + h * p.stride[kv][1] +
+                   (first + row0 - past) * p.stride[kv][2] + run * 16;
+    auto src_of = [&](int kv, int k) { return rows[kv] + (k ? kRows * p.stride[kv][2] : 0ll); };
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int token = first + row0 + k * kRows;
@@ -228,6 +266,7 @@ __global__ void __launch_bounds__(kStoreThreads) pa_q8_append_kernel(const __gri
     }
     const bool earlier = first < past;
     const int64_t at = static_cast<int64_t>(phys) * p.KV + h;
+    const int64_t place = ((static_cast<int64_t>(phys) * BLOCK + row0) * p.KV + h) * D + run * 16;
     float was[2] = {0.f, 0.f}, a[2];
     bool odd = false;  // something is not finite
 #pragma unroll
@@ -277,23 +316,24 @@ __global__ void __launch_bounds__(kStoreThreads) pa_q8_append_kernel(const __gri
     }
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-        const float scale = fmaxf(q8_scale_of(a[kv]), was[kv]), inv = 1.f / scale;
+        const float scale = fmaxf(q8_scale_of(a[kv]), was[kv]);
+        const Rounding by = rounding_of<T>(a[kv], scale);
         const bool grown = earlier && scale > was[kv], ranged = kv == 0 && p.bounds;
         if (head && me == 0 && (!earlier || grown))
             p.scale[kv][at] = scale;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int row = row0 + k * kRows;
-            int8_t* dst = p.cache[kv] + ((static_cast<int64_t>(phys) * BLOCK + row) * p.KV + h) * D + run * 16;
+            int8_t* dst = p.cache[kv] + place + (k ? kRows * p.KV * D : 0);
             const bool old = head && first + row < past && (grown || ranged);
             uint4 c = make_uint4(0u, 0u, 0u, 0u);
             if (fresh[k]) {
-                c = run_codes(dst, x[kv][k], src_of(kv, k), scale, inv, odd);
+                c = run_codes(dst, x[kv][k], src_of(kv, k), by, odd);
             } else if (old) {
                 if (grown) {
 #pragma unroll 1
                     for (int i = 0; i < 16; ++i)
-                        dst[i] = static_cast<int8_t>(q8_again(dst[i], was[kv], scale, inv));
+                        dst[i] = static_cast<int8_t>(q8_again(dst[i], was[kv], scale, by.inv));
                 }
                 c = *reinterpret_cast<const uint4*>(dst);
             }
@@ -319,12 +359,12 @@ __global__ void __launch_bounds__(kStoreThreads) pa_q8_append_kernel(const __gri
                 hi[i] = highest2(hi[i], __shfl_xor_sync(kFullWarp, hi[i], o));
             }
         if constexpr (kGroup > 32) {
-            if (lane < kRuns) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    ends[0][warp][lane * 8 + i] = lo[i];
-                    ends[1][warp][lane * 8 + i] = hi[i];
-                }
+            if (lane < kRuns && me >= 32) {
+                uint4* to = reinterpret_cast<uint4*>(&ends[warp][0][lane * 8]);
+                to[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                to[1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+                to[kRuns * 2] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                to[kRuns * 2 + 1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
             }
             __syncthreads();
         }
@@ -333,12 +373,17 @@ __global__ void __launch_bounds__(kStoreThreads) pa_q8_append_kernel(const __gri
                 constexpr int kWarps = kGroup / 32;
                 const int base = warp / kWarps * kWarps;
 #pragma unroll
-                for (int v = 1; v < kWarps; ++v)
+                for (int v = 1; v < kWarps; ++v) {
+                    const uint4* at = reinterpret_cast<const uint4*>(&ends[base + v][0][me * 8]);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        lo[i] = lowest2(lo[i], ends[0][base + v][me * 8 + i]);
-                        hi[i] = highest2(hi[i], ends[1][base + v][me * 8 + i]);
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 x = at[i], y = at[kRuns * 2 + i];
+                        lo[4 * i] = lowest2(lo[4 * i], x.x), lo[4 * i + 1] = lowest2(lo[4 * i + 1], x.y);
+                        lo[4 * i + 2] = lowest2(lo[4 * i + 2], x.z), lo[4 * i + 3] = lowest2(lo[4 * i + 3], x.w);
+                        hi[4 * i] = highest2(hi[4 * i], y.x), hi[4 * i + 1] = highest2(hi[4 * i + 1], y.y);
+                        hi[4 * i + 2] = highest2(hi[4 * i + 2], y.z), hi[4 * i + 3] = highest2(hi[4 * i + 3], y.w);
                     }
+                }
             }
             uint4* to = reinterpret_cast<uint4*>(p.bounds + at * 2 * D + me * 16);
             to[0] = pack_codes(lo);
@@ -478,7 +523,7 @@ extern "C" int pa_q8_append(int8_t* k_cache, int8_t* v_cache, float* k_scale, fl
     p.maxb = o.max_blocks;
     p.num_blocks = o.num_blocks;
     p.cap = o.max_blocks * BLOCK;
-    const int group = BLOCK * D / 32, threads = group < 64 ? 64 : group, heads = threads / group;
+    const int group = BLOCK * D / 32, threads = append_threads(BLOCK * D), heads = threads / group;
     const void* fn = o.dtype == PA_F32   ? append_kernel<float>(D, BLOCK)
                      : o.dtype == PA_F16 ? append_kernel<__half>(D, BLOCK)
                                          : append_kernel<__nv_bfloat16>(D, BLOCK);
