@@ -69,9 +69,8 @@ __global__ void __launch_bounds__(T, 768 / T) pa_q8_select_kernel(const __grid_c
     uint32_t* codes = smem + ((p.maxb + 3) & ~3) + most;  // [rows][4 quarters][positive words | negative words]
     constexpr int kQuarter = D / 8 + 4, kRow = 4 * kQuarter;  // words; the four quarters in banks of their own
     __shared__ float steps[kSelectRows];
-    __shared__ __align__(16) uint32_t hist[kBins];
+    __shared__ __align__(16) uint32_t hist[2][kBins];
     __shared__ uint32_t wide[kWarps][2];
-    __shared__ uint32_t pick[3];                   // bin, still wanted in it, its count
     __shared__ int cnt[kWarps][2];
     grid_dependents_launch();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -254,8 +253,8 @@ __global__ void __launch_bounds__(T, 768 / T) pa_q8_select_kernel(const __grid_c
 
     // the range of the candidates' scores
     uint32_t least = 0xffffffffu, largest = 0;
-    for (int i = tid; i < kBins; i += T)
-        hist[i] = 0;
+    for (int i = tid; i < 2 * kBins; i += T)
+        hist[0][i] = 0;
     for (int j = lo + tid; j < hi; j += T) {
         least = min(least, keys[j]);
         largest = max(largest, keys[j]);
@@ -272,47 +271,47 @@ __global__ void __launch_bounds__(T, 768 / T) pa_q8_select_kernel(const __grid_c
     // taken: scores >= t_ge, and of those equal to t_eq the first n_eq
     uint32_t t_ge = 0, t_eq = 0, from = least, width = largest - least;  // candidates in [from, from + width]
     int n_eq = 0, want = need;
-    for (;;) {
+    for (int round = 0;; ++round) {
         const int shift = max(0, 32 - __clz(width) - 8);  // 256 bins over the range
+        uint32_t* bins = hist[round & 1];
         for (int j = lo + tid; j < hi; j += T) {
-            const uint32_t d = keys[j] - from;
-            if (keys[j] >= from && d <= width)
-                atomicAdd(&hist[d >> shift], 1u);
+            const uint32_t key = keys[j], d = key - from;
+            if (key >= from && d <= width)
+                atomicAdd(&bins[d >> shift], 1u);
         }
         __syncthreads();
-        if (warp == 0) {
-            // eight bins a lane, from the top
-            constexpr int kOwn = kBins / 32;
-            const uint4 v0 = *reinterpret_cast<const uint4*>(hist + kBins - kOwn * (lane + 1)), v1 = *reinterpret_cast<const uint4*>(hist + kBins - kOwn * (lane + 1) + 4);
-            const uint32_t v[kOwn] = {v1.w, v1.z, v1.y, v1.x, v0.w, v0.z, v0.y, v0.x};
-            uint32_t sum = 0;
+        // every warp for itself: eight bins a lane, from the top
+        constexpr int kOwn = kBins / 32;
+        const uint4 v0 = *reinterpret_cast<const uint4*>(bins + kBins - kOwn * (lane + 1)), v1 = *reinterpret_cast<const uint4*>(bins + kBins - kOwn * (lane + 1) + 4);
+        const uint32_t v[kOwn] = {v1.w, v1.z, v1.y, v1.x, v0.w, v0.z, v0.y, v0.x};
+        uint32_t sum = 0;
 #pragma unroll
-            for (int i = 0; i < kOwn; ++i)
-                sum += v[i];
-            uint32_t incl = sum;
+        for (int i = 0; i < kOwn; ++i)
+            sum += v[i];
+        uint32_t incl = sum;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t y = __shfl_up_sync(kFullWarp, incl, o);
-                if (lane >= o)
-                    incl += y;
-            }
-            uint32_t at = incl - sum;
-            if (at < static_cast<uint32_t>(want) && static_cast<uint32_t>(want) <= incl) {
-#pragma unroll
-                for (int i = 0; i < kOwn; ++i) {
-                    if (at < static_cast<uint32_t>(want) && static_cast<uint32_t>(want) <= at + v[i]) {
-                        pick[0] = static_cast<uint32_t>(kBins - 1 - lane * kOwn - i);
-                        pick[1] = static_cast<uint32_t>(want) - at;
-                        pick[2] = v[i];
-                    }
-                    at += v[i];
-                }
-            }
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(kFullWarp, incl, o);
+            if (lane >= o)
+                incl += y;
         }
-        __syncthreads();
-        from += pick[0] << shift;
-        want = static_cast<int>(pick[1]);
-        if (pick[1] == pick[2]) {  // the bin is taken whole
+        const int at_lane = __ffs(__ballot_sync(kFullWarp, incl >= static_cast<uint32_t>(want))) - 1;
+        uint32_t at = incl - sum, bin = 0, left = 0, count = 0;
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            if (at < static_cast<uint32_t>(want)) {
+                bin = static_cast<uint32_t>(kBins - 1 - lane * kOwn - i);
+                left = static_cast<uint32_t>(want) - at;
+                count = v[i];
+            }
+            at += v[i];
+        }
+        bin = __shfl_sync(kFullWarp, bin, at_lane);
+        left = __shfl_sync(kFullWarp, left, at_lane);
+        count = __shfl_sync(kFullWarp, count, at_lane);
+        from += bin << shift;
+        want = static_cast<int>(left);
+        if (left == count) {  // the bin is taken whole
             t_ge = from;
             break;
         }
@@ -323,9 +322,11 @@ __global__ void __launch_bounds__(T, 768 / T) pa_q8_select_kernel(const __grid_c
             break;
         }
         width = (1u << shift) - 1;
-        for (int i = tid; i < kBins; i += T)
-            hist[i] = 0;
-        __syncthreads();
+        if (round > 0) {  // (the bins of the round before this one: all have read them)
+            for (int i = tid; i < kBins; i += T)
+                hist[(round + 1) & 1][i] = 0;
+            __syncthreads();
+        }
     }
     // counts of the warps' ranges, then the places
     const int chunk = ((hi - lo + kWarps - 1) / kWarps + 31) & ~31;
@@ -363,7 +364,8 @@ const void* select_kernel(int C)
     return C == 1   ? reinterpret_cast<const void*>(pa_q8_select_kernel<D, 1, 256>)
            : C == 2 ? reinterpret_cast<const void*>(pa_q8_select_kernel<D, 2, 256>)
            : C == 4 ? reinterpret_cast<const void*>(pa_q8_select_kernel<D, 4, 256>)
-                    : reinterpret_cast<const void*>(pa_q8_select_kernel<D, 8, 256>);
+           : C == 8 ? reinterpret_cast<const void*>(pa_q8_select_kernel<D, 8, 256>)
+                    : reinterpret_cast<const void*>(pa_q8_select_kernel<D, 16, 256>);
 }
 
 }  // namespace
@@ -424,10 +426,10 @@ extern "C" int pa_q8_select(const void* q, const int8_t* bounds, const float* k_
     p.shift = BLOCK == 8 ? 3 : BLOCK == 16 ? 4 : BLOCK == 32 ? 5 : 6;
     p.cap = o.max_blocks * BLOCK;
     p.dtype = o.dtype;
-    // CTAs per segment: as many as have a step of blocks each, up to a cluster of 8,
-    // while the SMs hold them all at once (three each)
-    int C = 8;
-    while (C > 1 && (static_cast<long long>(B) * KV * C > 456 || 64 * (C / 2) >= o.max_blocks))
+    // CTAs per segment: as many as have a step of blocks each, up to a cluster of 16,
+    // while the SMs hold them all at once (one each, or three in clusters up to 8)
+    int C = 16;
+    while (C > 1 && (static_cast<long long>(B) * KV * C > (C == 16 ? 152 : 456) || 64 * (C / 2) >= o.max_blocks))
         C /= 2;
     const int T = 256;
     const int most = (o.max_blocks + T / 4 * C - 1) / (T / 4 * C) * (T / 4);
