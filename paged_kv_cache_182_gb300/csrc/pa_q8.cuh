@@ -138,6 +138,16 @@ __device__ __forceinline__ void q8_store16(T* p, const float* f)
     }
 }
 
+__device__ __forceinline__ void q8_copy16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void q8_copy4(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // Bytes at `pick` (two of code + 128) as two fp16 codes.
 __device__ __forceinline__ uint32_t codes2(uint32_t biased, uint32_t pick)
 {
@@ -190,7 +200,7 @@ inline int q8_sizes(int B, int KV, int D, int BLOCK, int max_blocks, int num_blo
 // the kernel waits for that one before it reads anything (grid_dependency_wait).
 inline int q8_launch(const void* fn, dim3 grid, int threads, size_t smem, cudaStream_t st, void** args, int cluster = 1)
 {
-    if (smem > 48 * 1024 &&
+    if (smem > 40 * 1024 &&  // (48 KB with what a kernel has statically)
         cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return PA_ERR_CUDA;
     if (cluster > 8 && cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)

@@ -61,16 +61,6 @@ struct DecodeParams {
     int B, H, KV, R, NQ, groups, shift, maxb, num_blocks, cap, budget, causal, dtype, entries, copies, lg_team;
 };
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-
 __device__ __forceinline__ uint4 lds16(uint32_t a)
 {
     uint4 v;
@@ -388,7 +378,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
             const uint32_t own_row = __shfl_sync(kFullWarp, w_row, at_window * HB + own);
             const int own_place = __shfl_sync(kFullWarp, w_place, at_window * HB + own);
             if (lane < 2 * HB) {
-                copy4(st + kTileBytes + lane * 4, (lane & 1 ? p.vs : p.ks) + static_cast<uint64_t>(own_row >> p.shift) * p.KV + kh);
+                q8_copy4(st + kTileBytes + lane * 4, (lane & 1 ? p.vs : p.ks) + static_cast<uint64_t>(own_row >> p.shift) * p.KV + kh);
                 if ((lane & 1) == 0)
                     asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + kTileBytes + 32 + 2 * lane), "r"(own_place) : "memory");
             }
@@ -400,8 +390,8 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
 #pragma unroll
                 for (int i = 0; i < kPart / kRowsCopy; ++i) {
                     const uint32_t to = st + (x * (kPart / kRowsCopy) + i) * 512;
-                    copy16(to + copy_k, k0 + i * kRowsCopy * step);
-                    copy16(to + kTile * D + (D == 128 && i & 1 ? copy_v ^ 64 : copy_v), v0 + i * kRowsCopy * step);
+                    q8_copy16(to + copy_k, k0 + i * kRowsCopy * step);
+                    q8_copy16(to + kTile * D + (D == 128 && i & 1 ? copy_v ^ 64 : copy_v), v0 + i * kRowsCopy * step);
                 }
             }
         }

@@ -2,12 +2,15 @@
 // most (include/pa_q8.h).
 //
 // One kernel, a CTA or a cluster of them per sequence and KV head.  The query
-// rows become whole numbers in shared memory, positive and negative parts apart,
-// so that sum_d max(c min, c max) = c+ . max + c- . min is a product of whole
-// numbers (dp4a): exact, in any order.  Four lanes share a block, a quarter of
-// the channels each; four rows are summed over those lanes together.  Table
-// entries are read before the length is known, and the next blocks' bounds
-// while this step's are used.
+// rows become whole numbers, positive and negative parts apart, so that
+// sum_d max(c min, c max) = c- . min + c+ . max is a product of whole numbers of
+// length 2 D.  The tensor cores take it in fp16 with float32 sums: a bound + 128 is
+// a subnormal fp16 number as it stands (the row's 128 sum c is taken off
+// beforehand), a code is exact, and all sums are below 2^24 of the unit 2^-24:
+// nothing is rounded, in any order.  (Integer products, dp4a, run at a tenth of
+// the rate here: 42 us for 8 x 8 x 4096 blocks and 4 rows, 40 for 4 x 8 x 2048 and
+// 32 rows.)  A warp has 16 blocks in hand and 16 on their way; table entries are
+// read before the length is known.
 //
 // The scores go to the first CTA of the cluster, which finds the score of the
 // last block taken by counting them in 256 bins over their range, then over the
@@ -25,6 +28,8 @@ namespace {
 constexpr int kSelectRows = 128;        // query rows in shared memory at once
 constexpr int kSelectBlocks = 32768;    // blocks of a table row at most
 constexpr int kBins = 256;
+constexpr int kRing = 2;                // steps of a warp's blocks in shared memory
+__host__ __device__ constexpr int kStepBytes(int D) { return 16 * 2 * D + 64; }  // bounds of 16 blocks, their scales
 
 struct SelectParams {
     const void* q;
@@ -35,7 +40,7 @@ struct SelectParams {
     int32_t* selected;
     int32_t* counts;
     int* status;
-    int KV, R, maxb, num_blocks, budget, first, last, shift, cap, dtype;
+    int KV, R, chunk, maxb, num_blocks, budget, first, last, shift, cap, dtype;
 };
 
 // Unsigned integers in the order of the scores: NaN lowest, -0 equal to 0.
@@ -58,16 +63,21 @@ __device__ __forceinline__ float q8_element(const void* q, int dtype, int64_t i)
 
 // grid (C, B * KV), clusters of C along x; T threads.
 template <int D, int C, int T>
-__global__ void __launch_bounds__(T, 768 / T) pa_q8_select_kernel(const __grid_constant__ SelectParams p)
+__global__ void __launch_bounds__(T, 512 / T) pa_q8_select_kernel(const __grid_constant__ SelectParams p)
 {
-    constexpr int kWarps = T / 32, kStep = kWarps * C * 8;  // blocks that the cluster takes together
-    constexpr int kWords = D / 16;                 // words of a lane's quarter of a row
+    constexpr int kWarps = T / 32, kStep = kWarps * C * 16;  // blocks that the cluster takes together
+    constexpr int kChunks = D / 32, kSteps = D / 8;          // 64 bytes of a block's bounds; MMA steps
     extern __shared__ __align__(16) uint32_t smem[];
     uint32_t* keys = smem;                         // [maxb] scores in order (the first CTA's)
-    const int most = (p.maxb + kStep - 1) / kStep * kWarps * 8;  // blocks of a CTA
-    float* own = reinterpret_cast<float*>(smem + ((p.maxb + 3) & ~3));  // [most] this CTA's scores
-    uint32_t* codes = smem + ((p.maxb + 3) & ~3) + most;  // [rows][4 quarters][positive words | negative words]
-    constexpr int kQuarter = D / 8 + 4, kRow = 4 * kQuarter;  // words; the four quarters in banks of their own
+    // [most] this CTA's scores, one CTA's in the keys' place; the warps' rings;
+    // fragments of the rows [8 rows][step][lane]
+    const int most = C == 1 ? 0 : (p.maxb + kStep - 1) / kStep * kWarps * 16;
+    uint32_t* const behind = smem + (p.maxb + 15) / 16 * 16;
+    float* own = reinterpret_cast<float*>(C == 1 ? smem : behind);
+    unsigned char* rings = reinterpret_cast<unsigned char*>(behind + most);
+    unsigned char* ring = rings + (threadIdx.x >> 5) * kRing * kStepBytes(D);
+    uint2* codes = reinterpret_cast<uint2*>(rings + kWarps * kRing * kStepBytes(D));
+    __shared__ float offs[kSelectRows];            // what a row's sums begin with
     __shared__ float steps[kSelectRows];
     __shared__ __align__(16) uint32_t hist[2][kBins];
     __shared__ uint32_t wide[kWarps][2];
@@ -81,10 +91,15 @@ __global__ void __launch_bounds__(T, 768 / T) pa_q8_select_kernel(const __grid_c
     grid_dependency_wait();
     int n = __ldg(p.lens + b);
     const int32_t* table = p.table + static_cast<int64_t>(b) * p.maxb;
-    // the cluster's warps take eight blocks each in turn
-    const int j0 = (warp * C + rank) * 8 + g;
-    int phys = j0 < p.maxb ? __ldg(table + j0) : -1;
-    int phys1 = j0 + kStep < p.maxb ? __ldg(table + j0 + kStep) : -1;
+    // the cluster's warps take 16 blocks each in turn, a lane those of rows g and g + 8
+    const int j0 = (warp * C + rank) * 16 + g;
+    auto entry = [&](int j, int end) { return j < end ? __ldg(table + j) : -1; };
+    int phys[kRing][2];
+#pragma unroll
+    for (int s = 0; s < kRing; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            phys[s][i] = entry(j0 + s * kStep + 8 * i, p.maxb);
     const int64_t q0 = static_cast<int64_t>(seg) * p.R * D;
     if (n < 0 || n > p.cap) {
         if (h == 0 && rank == 0 && tid == 0)
@@ -117,120 +132,144 @@ __global__ void __launch_bounds__(T, 768 / T) pa_q8_select_kernel(const __grid_c
         return;
     }
 
-    // scores
-    struct Bounds {
-        uint32_t mn[kWords], mx[kWords];
-        float ks;
-        bool there;
-    };
-    auto fetch = [&](Bounds& x, int j, int ph) {
-        x.there = j < nb && static_cast<uint32_t>(ph) < static_cast<uint32_t>(p.num_blocks);
-        if (!x.there && j < nb)
-            q8_report(p.status, PA_STATUS_BAD_BLOCK);
-        const int64_t at = static_cast<int64_t>(x.there ? ph : 0) * p.KV + h;
-        const uint4* src = reinterpret_cast<const uint4*>(p.bounds + at * 2 * D + t * (D / 4));
-        if (x.there) {
+    // scores.  A lane copies the bytes that it will use itself (and one scale of two).
+    const uint32_t ring0 = smem_u32(ring);
+    uint32_t there = 0;  // of the steps on their way, two bits each: the lane's blocks are in the pool
+    auto issue = [&](int j, const int* ph, int stage) {
+        const uint32_t to = ring0 + stage * kStepBytes(D);
 #pragma unroll
-            for (int i = 0; i < kWords / 4; ++i) {
-                const uint4 v = __ldg(src + i), w = __ldg(src + i + D / 16);
-                x.mn[4 * i] = v.x, x.mn[4 * i + 1] = v.y, x.mn[4 * i + 2] = v.z, x.mn[4 * i + 3] = v.w;
-                x.mx[4 * i] = w.x, x.mx[4 * i + 1] = w.y, x.mx[4 * i + 2] = w.z, x.mx[4 * i + 3] = w.w;
+        for (int i = 0; i < 2; ++i) {
+            const bool ok = j + 8 * i < nb && static_cast<uint32_t>(ph[i]) < static_cast<uint32_t>(p.num_blocks);
+            if (!ok && j + 8 * i < nb)
+                q8_report(p.status, PA_STATUS_BAD_BLOCK);
+            there = there << 1 | (ok ? 1u : 0u);
+            if (ok) {
+                const int64_t at = static_cast<int64_t>(ph[i]) * p.KV + h;
+                const int8_t* src = p.bounds + at * 2 * D + t * 16;
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c)
+                    q8_copy16(to + ((i * kChunks + c) * 32 + lane) * 16, src + c * 64);
+                if (t == i)
+                    q8_copy4(to + 32 * D + (g + 8 * i) * 4, p.k_scale + at);
             }
-            x.ks = __ldg(p.k_scale + at);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    for (int r0 = 0; r0 < p.R; r0 += kSelectRows) {
-        const int rows = min(kSelectRows, p.R - r0), rows4 = (rows + 3) & ~3;
-        // two steps of blocks are on their way, the entries of the third
-        Bounds x, next;
+    for (int r0 = 0; r0 < p.R; r0 += p.chunk) {
+        const int rows = min(p.chunk, p.R - r0), rows8 = (rows + 7) & ~7;
+        // kRing - 1 steps are on their way, the entries of the next
         if (r0 > 0) {
-            phys = j0 < nb ? __ldg(table + j0) : -1;
-            phys1 = j0 + kStep < nb ? __ldg(table + j0 + kStep) : -1;
+#pragma unroll
+            for (int s = 0; s < kRing; ++s)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    phys[s][i] = entry(j0 + s * kStep + 8 * i, nb);
             __syncthreads();
         }
-        fetch(x, j0, phys);
-        fetch(next, j0 + kStep, phys1);
-        int phys2 = j0 + 2 * kStep < nb ? __ldg(table + j0 + 2 * kStep) : -1;
-        for (int r = warp; r < rows4; r += kWarps) {
-            float v[D / 32];
+#pragma unroll
+        for (int s = 0; s < kRing - 1; ++s)
+            issue(j0 + s * kStep, phys[s], s);
+        int ahead[2] = {phys[kRing - 1][0], phys[kRing - 1][1]};
+        for (int r = warp; r < rows8; r += kWarps) {
+            constexpr int kOwn = D / 32;  // channels of a lane
+            float v[kOwn];
             float a = 0.f;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                v[i] = r < rows ? q8_element(p.q, p.dtype, q0 + static_cast<int64_t>(r0 + r) * D + lane * (D / 32) + i) : 0.f;
+            for (int i = 0; i < kOwn; ++i) {
+                v[i] = r < rows ? q8_element(p.q, p.dtype, q0 + static_cast<int64_t>(r0 + r) * D + lane * kOwn + i) : 0.f;
                 a = q8_amax(a, v[i]);
             }
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1)
                 a = fmaxf(a, __shfl_xor_sync(kFullWarp, a, o));
             const float scale = q8_scale_of(a), inv = 1.f / scale;
-            if (lane == 0)
-                steps[r] = scale;
-            int8_t* row = reinterpret_cast<int8_t*>(codes + r * kRow);
+            int sum = 0;
+            uint32_t up[kOwn / 2], down[kOwn / 2];
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const int d = lane * (D / 32) + i, c = q8_code(v[i], scale, inv);
-                int8_t* at = row + (d / (D / 4)) * (kQuarter * 4) + d % (D / 4);
-                at[0] = static_cast<int8_t>(max(c, 0));
-                at[D / 4] = static_cast<int8_t>(min(c, 0));
+            for (int i = 0; i < kOwn; i += 2) {
+                const int c0 = q8_code(v[i], scale, inv), c1 = q8_code(v[i + 1], scale, inv);
+                sum += c0 + c1;
+                const __half2 u = __floats2half2_rn(static_cast<float>(max(c0, 0)), static_cast<float>(max(c1, 0)));
+                const __half2 d = __floats2half2_rn(static_cast<float>(min(c0, 0)), static_cast<float>(min(c1, 0)));
+                up[i / 2] = *reinterpret_cast<const uint32_t*>(&u);
+                down[i / 2] = *reinterpret_cast<const uint32_t*>(&d);
+            }
+            sum = __reduce_add_sync(kFullWarp, sum);
+            if (lane == 0) {
+                steps[r] = scale;
+                offs[r] = static_cast<float>(sum) * (-128.f / 16777216.f);
+            }
+            // channel d: chunk d / 64, lane's part (d % 64) / 16, step (d % 16) / 4 of the chunk
+            const int d = lane * kOwn;
+            uint2* to = codes + ((r >> 3) * kSteps + (d / 64) * 4 + d % 16 / 4) * 32 + (r & 7) * 4 + d % 64 / 16;
+            if constexpr (D == 128) {
+                to[0] = make_uint2(down[0], down[1]);
+                to[kSteps / 2 * 32] = make_uint2(up[0], up[1]);
+            } else {
+                reinterpret_cast<uint32_t*>(to)[d % 4 / 2] = down[0];
+                reinterpret_cast<uint32_t*>(to + kSteps / 2 * 32)[d % 4 / 2] = up[0];
             }
         }
         __syncthreads();
-        int slot = warp * 8 + g;
-        for (int base = j0 - g; base < nb; base += kStep, slot += kWarps * 8) {
+        int slot = warp * 16 + g, stage = 0;
+        for (int base = j0 - g; base < nb; base += kStep, slot += kWarps * 16) {
             const int j = base + g;
-            float best = -INFINITY;
-            bool any = false;
-            for (int r = 0; r < rows; r += 4) {
-                int sum[4];
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+            __syncwarp();  // the scales of the other lanes; the stage filled next has been read
+            issue(j + (kRing - 1) * kStep, ahead, stage == 0 ? kRing - 1 : stage - 1);
+            ahead[0] = entry(j + kRing * kStep, nb);
+            ahead[1] = entry(j + kRing * kStep + 8, nb);
+            const unsigned char* now = ring + stage * kStepBytes(D);
+            const bool ok[2] = {(there >> (2 * kRing - 1) & 1u) != 0, (there >> (2 * kRing - 2) & 1u) != 0};
+            const float ks[2] = {*reinterpret_cast<const float*>(now + 32 * D + g * 4), *reinterpret_cast<const float*>(now + 32 * D + g * 4 + 32)};
+            stage = stage + 1 == kRing ? 0 : stage + 1;
+            float best[2] = {-INFINITY, -INFINITY};
+            bool any[2] = {false, false};
+            for (int r = 0; r < rows; r += 8) {
+                float acc[4];
+                acc[0] = acc[2] = offs[r + 2 * t];
+                acc[1] = acc[3] = offs[r + 2 * t + 1];
+                const uint2* q = codes + (r >> 3) * kSteps * 32 + lane;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint4* c = reinterpret_cast<const uint4*>(codes + (r + k) * kRow + t * kQuarter);
-                    int s = 0;
+                for (int c = 0; c < kChunks; ++c) {
+                    const uint4 va = *reinterpret_cast<const uint4*>(now + (c * 32 + lane) * 16);
+                    const uint4 vb = *reinterpret_cast<const uint4*>(now + ((kChunks + c) * 32 + lane) * 16);
+                    const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
 #pragma unroll
-                    for (int i = 0; i < kWords / 4; ++i) {
-                        const uint4 up = c[i], dn = c[i + D / 64];
-                        s = __dp4a(static_cast<int>(up.x), static_cast<int>(x.mx[4 * i]), s);
-                        s = __dp4a(static_cast<int>(up.y), static_cast<int>(x.mx[4 * i + 1]), s);
-                        s = __dp4a(static_cast<int>(up.z), static_cast<int>(x.mx[4 * i + 2]), s);
-                        s = __dp4a(static_cast<int>(up.w), static_cast<int>(x.mx[4 * i + 3]), s);
-                        s = __dp4a(static_cast<int>(dn.x), static_cast<int>(x.mn[4 * i]), s);
-                        s = __dp4a(static_cast<int>(dn.y), static_cast<int>(x.mn[4 * i + 1]), s);
-                        s = __dp4a(static_cast<int>(dn.z), static_cast<int>(x.mn[4 * i + 2]), s);
-                        s = __dp4a(static_cast<int>(dn.w), static_cast<int>(x.mn[4 * i + 3]), s);
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t ua = wa[i] ^ 0x80808080u, ub = wb[i] ^ 0x80808080u;
+                        const uint32_t a[4] = {__byte_perm(ua, 0, 0x4140), __byte_perm(ub, 0, 0x4140), __byte_perm(ua, 0, 0x4342),
+                                               __byte_perm(ub, 0, 0x4342)};
+                        const uint2 f = q[(c * 4 + i) * 32];
+                        mma_16816<false>(acc, a, f.x, f.y);
                     }
-                    sum[k] = s;
                 }
-                // lane t of the four ends with the total of row r + t
-                const int o0 = __shfl_xor_sync(kFullWarp, t & 1 ? sum[0] : sum[1], 1);
-                const int o1 = __shfl_xor_sync(kFullWarp, t & 1 ? sum[2] : sum[3], 1);
-                const int a0 = (t & 1 ? sum[1] : sum[0]) + o0, a1 = (t & 1 ? sum[3] : sum[2]) + o1;
-                const int o2 = __shfl_xor_sync(kFullWarp, t & 2 ? a0 : a1, 2);
-                const int total = (t & 2 ? a1 : a0) + o2;
-                if (r + t < rows) {
-                    const float score = __fmul_rn(__fmul_rn(steps[r + t], x.ks), static_cast<float>(total));
-                    any |= score == score;
-                    best = fmaxf(best, score);  // (a NaN leaves the other)
-                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (r + 2 * t + (i & 1) < rows) {
+                        const float score = __fmul_rn(__fmul_rn(steps[r + 2 * t + (i & 1)], ks[i >> 1]), acc[i] * 16777216.f);
+                        any[i >> 1] |= score == score;
+                        best[i >> 1] = fmaxf(best[i >> 1], score);  // (a NaN leaves the other)
+                    }
             }
 #pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                best = fmaxf(best, __shfl_xor_sync(kFullWarp, best, o));
-                any |= __shfl_xor_sync(kFullWarp, static_cast<int>(any), o) != 0;
-            }
-            if (j < nb && t == 0) {
-                float s = x.there && any ? best : __int_as_float(0x7fc00000);
-                if (r0 > 0) {
-                    const float before = own[slot];
-                    s = before != before ? s : s != s ? before : fmaxf(s, before);
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) {
+                    best[i] = fmaxf(best[i], __shfl_xor_sync(kFullWarp, best[i], o));
+                    any[i] |= __shfl_xor_sync(kFullWarp, static_cast<int>(any[i]), o) != 0;
                 }
-                own[slot] = s;
-            }
-            x = next;
-            if (base + kStep < nb) {
-                fetch(next, j + 2 * kStep, phys2);
-                phys2 = j + 3 * kStep < nb ? __ldg(table + j + 3 * kStep) : -1;
+                if (j + 8 * i < nb && t == 0) {
+                    float s = ok[i] && any[i] ? best[i] : __int_as_float(0x7fc00000);
+                    if (r0 > 0) {
+                        const float before = own[slot + 8 * i];
+                        s = before != before ? s : s != s ? before : fmaxf(s, before);
+                    }
+                    own[slot + 8 * i] = s;
+                }
             }
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     // to the first CTA; a warp moves its own
     __syncwarp();
@@ -239,8 +278,8 @@ __global__ void __launch_bounds__(T, 768 / T) pa_q8_select_kernel(const __grid_c
         asm volatile("barrier.cluster.wait;" ::: "memory");
         asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(smem_u32(keys)));
     }
-    for (int base = (warp * C + rank) * 8 + lane % 8 + lane / 8 * kStep, slot = warp * 8 + lane % 8 + lane / 8 * kWarps * 8; base < nb;
-         base += 4 * kStep, slot += 4 * kWarps * 8)
+    for (int base = (warp * C + rank) * 16 + lane % 16 + lane / 16 * kStep, slot = warp * 16 + lane % 16 + lane / 16 * kWarps * 16;
+         base < nb; base += 2 * kStep, slot += 2 * kWarps * 16)
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + static_cast<uint32_t>(base) * 4), "r"(score_order(own[slot])) : "memory");
     if (C > 1) {
         asm volatile("barrier.cluster.arrive;" ::: "memory");
@@ -427,14 +466,22 @@ extern "C" int pa_q8_select(const void* q, const int8_t* bounds, const float* k_
     p.cap = o.max_blocks * BLOCK;
     p.dtype = o.dtype;
     // CTAs per segment: as many as have a step of blocks each, up to a cluster of 16,
-    // while the SMs hold them all at once (one each, or three in clusters up to 8)
+    // while the SMs hold them all at once (one each, or two in clusters up to 8)
+    constexpr int T = 256;
+    constexpr size_t kRoom = 224 * 1024;
     int C = 16;
-    while (C > 1 && (static_cast<long long>(B) * KV * C > (C == 16 ? 152 : 456) || 64 * (C / 2) >= o.max_blocks))
+    while (C > 1 && (static_cast<long long>(B) * KV * C > (C == 16 ? 152 : 304) || T / 2 * (C / 2) >= o.max_blocks))
         C /= 2;
-    const int T = 256;
-    const int most = (o.max_blocks + T / 4 * C - 1) / (T / 4 * C) * (T / 4);
-    const int rows = p.R < kSelectRows ? (p.R + 3) & ~3 : kSelectRows;
-    const size_t smem = 4 * (static_cast<size_t>((o.max_blocks + 3) & ~3) + most + static_cast<size_t>(rows) * (D / 2 + 16));
+    const size_t keys = static_cast<size_t>(o.max_blocks + 15) / 16 * 64, ring = T / 32 * kRing * kStepBytes(D);
+    const auto scores = [&](int c) { return c == 1 ? size_t{0} : static_cast<size_t>((o.max_blocks + T / 2 * c - 1) / (T / 2 * c)) * (T / 2) * 4; };
+    const size_t row8 = static_cast<size_t>(8) * 4 * D;  // fragments of eight rows
+    if (keys + scores(C) + ring + row8 > kRoom)
+        C = 1;  // (a very long table: the scores stay where the keys are)
+    // rows together: all, or what there is room for
+    size_t room = (kRoom - keys - scores(C) - ring) / row8 * 8;
+    p.chunk = static_cast<int>(room < kSelectRows ? room : kSelectRows);
+    const size_t rows = p.R < p.chunk ? static_cast<size_t>(p.R + 7) & ~static_cast<size_t>(7) : p.chunk;
+    const size_t smem = keys + scores(C) + ring + rows * 4 * D;
     void* args[] = {&p};
     return q8_launch(D == 64 ? select_kernel<64>(C) : select_kernel<128>(C), dim3(C, B * KV), T, smem,
                      static_cast<cudaStream_t>(stream), args, C);
