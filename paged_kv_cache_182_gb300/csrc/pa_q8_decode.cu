@@ -100,19 +100,21 @@ __device__ __forceinline__ float fast_log2(float x)
 template <int D, int NT, int QP, int C>
 struct Shape {
     static constexpr int kRows = 8 * NT, kSteps = D / 16;
+    // more than eight rows of 16 bits: rows on the 16-row side of the products
+    static constexpr bool kWide = NT >= 2 && QP == 1;
     static constexpr int kWarps = NT == 1 && QP == 1 ? 12 / C : 8, kThreads = kWarps * 32;
-    static constexpr int kJoint = NT * QP == 4 ? 1 : 2;  // MMA groups of a tile taken together
+    static constexpr int kJoint = NT * QP == 4 && QP == 2 ? 1 : 2;  // MMA groups of a tile taken together
     static constexpr int kTileBytes = 2 * kTile * D, kStage = kTileBytes + kMeta;
     static constexpr int kStages = 2 * (D == 128 ? 1 : 2);
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kCharge = kChargeBytes / C / kTileBytes, kJoin = kJoinBytes / kTileBytes;  // in tiles
-    // a warp's state in shared memory: steps of 16 + 4 floats, rows 4 (mod 32) floats
-    // apart, so that neither its writes nor its reads meet a bank twice
-    static constexpr int kStateStep = 20, kStateRow = kSteps * kStateStep + 4, kState = kRows * kStateRow * 4;
+    // A warp's state in shared memory: steps of 16 + 4 floats, rows 4 (mod 32) floats
+    // apart (wide: rows of D + 4, four floats together in an order of their own), so
+    // that neither its writes nor its reads meet a bank twice
+    static constexpr int kStateStep = 20, kStateRow = kWide ? D + 4 : kSteps * kStateStep + 4, kState = kRows * kStateRow * 4;
     static constexpr int kGroup = 2;  // warps' states joined at once beside a ring in use
     static constexpr int kLastGroup = kRing >= kWarps * kState ? kWarps : kWarps / 2;  // ... and in the place of the ring
     static_assert(kRing >= kLastGroup * kState, "states fit");
-    static constexpr bool kQueryShared = NT == 4;
     static constexpr int kQueryBytes = QP * kSteps * NT * 32 * 8;
 };
 
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
     constexpr int kRows = Sh::kRows, kSteps = Sh::kSteps, kTileBytes = Sh::kTileBytes, kStage = Sh::kStage, S = Sh::kStages;
     constexpr int kWarps = Sh::kWarps, kThreads = Sh::kThreads;
     constexpr int kChunks = D / 64;  // 16-byte runs of a key row per lane
-    constexpr bool kQs = Sh::kQueryShared;
+    constexpr bool kWide = Sh::kWide;
     // float16 has a code + 128 as a subnormal number, with no arithmetic: the sum of
     // the row's 128 is taken off the score beforehand.  (Keys only: the values'
     // weights have one sign, and their sum would swamp the output.)
@@ -185,6 +187,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
     constexpr int kRuns = D / 16, kRowsCopy = 32 / kRuns;
     const int copy_run = lane % kRuns;
     const int copy_row = D == 128 ? lane / kRuns : (lane >> 2 & 3) * 2 + (lane >> 4);
+    auto turn_of = [](int x) { return D == 128 ? 2 * x : (x >> 1) * 2; };  // order of a wide state's quads
     uint32_t copy_k, copy_v, read_k, read_v;
     if constexpr (D == 128) {
         copy_k = copy_row * 128 + (copy_run ^ (copy_row & 1) << 2) * 16;
@@ -451,8 +454,11 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
             issue(i, ring + i * kStage);
         return true;
     };
-    float o[kSteps][NT][4];
-    float mx[NT][2], l[NT][2];
+    // values, maxima and sums: by steps of channels and groups of eight rows, two rows
+    // a lane (wide: by 16 rows and eight channels, rows g and g + 8)
+    constexpr int kStats = kWide ? NT : 2 * NT, kOct = D / 8;
+    float o[kSteps * NT][4];
+    float mx[kStats], l[kStats];
     int open = 0;  // pieces of this CTA that leave a record: at most the first and the last
     bool have = false;
     for (;;) {
@@ -471,20 +477,18 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
         const bool more = u < u_end && begin();
         if (have) {
             // ---- the warps' states together
+            auto row_of = [&](int k) { return kWide ? (k >> 1) * 16 + (k & 1) * 8 + g : (k >> 1) * 8 + 2 * t + (k & 1); };
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int k = 0; k < kStats; ++k) {
+                float s = l[k];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int row = nt * 8 + 2 * t + i;
-                    float s = l[nt][i];
-                    s += __shfl_xor_sync(kFullWarp, s, 4);
-                    s += __shfl_xor_sync(kFullWarp, s, 8);
-                    s += __shfl_xor_sync(kFullWarp, s, 16);
-                    if (g == 0) {
-                        sm_m[warp][row] = mx[nt][i];
-                        sm_l[warp][row] = s;
-                    }
+                for (int x = kWide ? 1 : 4; x < (kWide ? 4 : 32); x <<= 1)
+                    s += __shfl_xor_sync(kFullWarp, s, x);
+                if (kWide ? t == 0 : g == 0) {
+                    sm_m[warp][row_of(k)] = mx[k];
+                    sm_l[warp][row_of(k)] = s;
                 }
+            }
             __syncthreads();  // (without a next piece, the rings of all warps are free then)
             constexpr int kQuads = D / 4, kItems = kRows * kQuads;  // four channels each
             constexpr int kPer = (kItems + kThreads - 1) / kThreads;
@@ -499,31 +503,50 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                     __syncthreads();
                 if (warp >= w0 && warp < w0 + group) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int k = 0; k < kStats; ++k) {
+                        const int row = row_of(k);
+                        float m = -INFINITY;
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int row = nt * 8 + 2 * t + i;
-                            float m = -INFINITY;
+                        for (int w = 0; w < kWarps; ++w)
+                            m = fmaxf(m, sm_m[w][row]);
+                        const float f = mx[k] == -INFINITY ? 0.f : fast_exp2(mx[k] - m);
+                        float* to = state + ((warp - w0) * kRows + row) * Sh::kStateRow;
+                        if constexpr (kWide) {  // channels D / 4 t ...: two of eight octets' columns
 #pragma unroll
-                            for (int w = 0; w < kWarps; ++w)
-                                m = fmaxf(m, sm_m[w][row]);
-                            const float f = mx[nt][i] == -INFINITY ? 0.f : fast_exp2(mx[nt][i] - m);
-                            float* to = state + ((warp - w0) * kRows + row) * Sh::kStateRow + 2 * g;
+                            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                                for (int j = 0; j < kOct; j += 4) {
+                                    const int at = (k >> 1) * kOct + j, i = (k & 1) * 2 + e, quad = t * (D / 16) + ((e * kOct + j) / 4 ^ turn_of(t));
+                                    *reinterpret_cast<float4*>(to + quad * 4) = make_float4(o[at][i] * f, o[at + 1][i] * f, o[at + 2][i] * f, o[at + 3][i] * f);
+                                }
+                        } else {
 #pragma unroll
                             for (int s2 = 0; s2 < kSteps; ++s2)  // channels D / 8 g + 2 s2, + 1
-                                *reinterpret_cast<float2*>(to + s2 * Sh::kStateStep) = make_float2(o[s2][nt][i] * f, o[s2][nt][i + 2] * f);
+                                *reinterpret_cast<float2*>(to + 2 * g + s2 * Sh::kStateStep) =
+                                    make_float2(o[s2 * NT + (k >> 1)][k & 1] * f, o[s2 * NT + (k >> 1)][(k & 1) + 2] * f);
                         }
+                    }
                 }
                 __syncthreads();
 #pragma unroll
                 for (int k = 0; k < kPer; ++k) {
                     const int x = tid + k * kThreads, row = x / kQuads, quad = x % kQuads;
                     if (x < kItems) {
-                        const float* at = state + row * Sh::kStateRow + quad / (D / 32) * 2 + quad % (D / 32) * 2 * Sh::kStateStep;
-                        for (int w = 0; w < group; ++w) {
-                            const float2 v0 = *reinterpret_cast<const float2*>(at + w * kRows * Sh::kStateRow);
-                            const float2 v1 = *reinterpret_cast<const float2*>(at + w * kRows * Sh::kStateRow + Sh::kStateStep);
-                            val[k].x += v0.x, val[k].y += v0.y, val[k].z += v1.x, val[k].w += v1.y;
+                        const float* at = state + row * Sh::kStateRow;
+                        if constexpr (kWide) {
+                            const int lane_t = quad / (D / 16);
+                            at += (lane_t * (D / 16) + (quad % (D / 16) ^ turn_of(lane_t))) * 4;
+                            for (int w = 0; w < group; ++w) {
+                                const float4 v = *reinterpret_cast<const float4*>(at + w * kRows * Sh::kStateRow);
+                                val[k].x += v.x, val[k].y += v.y, val[k].z += v.z, val[k].w += v.w;
+                            }
+                        } else {
+                            at += quad / (D / 32) * 2 + quad % (D / 32) * 2 * Sh::kStateStep;
+                            for (int w = 0; w < group; ++w) {
+                                const float2 v0 = *reinterpret_cast<const float2*>(at + w * kRows * Sh::kStateRow);
+                                const float2 v1 = *reinterpret_cast<const float2*>(at + w * kRows * Sh::kStateRow + Sh::kStateStep);
+                                val[k].x += v0.x, val[k].y += v0.y, val[k].z += v1.x, val[k].w += v1.y;
+                            }
                         }
                     }
                 }
@@ -595,8 +618,15 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                     total += back.x + back.y;
                 }
 #pragma unroll
-                for (int q = 0; q < QP; ++q)
-                    sm_q[((q * kSteps + s) * NT + warp) * 32 + lane] = make_uint2(w[q][0], w[q][1]);
+                for (int q = 0; q < QP; ++q) {
+                    if constexpr (kWide) {  // fragments of 16 rows: rows g, g + 8, and again 8 channels on
+                        uint32_t* to = reinterpret_cast<uint32_t*>(sm_q) + ((s * (NT / 2) + warp / 2) * 32 + lane) * 4 + warp % 2;
+                        to[0] = w[q][0];
+                        to[2] = w[q][1];
+                    } else {
+                        sm_q[((q * kSteps + s) * NT + warp) * 32 + lane] = make_uint2(w[q][0], w[q][1]);
+                    }
+                }
             }
             total += __shfl_xor_sync(kFullWarp, total, 1);
             total += __shfl_xor_sync(kFullWarp, total, 2);
@@ -609,8 +639,8 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
             }
         }
         __syncthreads();
-        uint32_t qf[kQs ? 1 : QP][kQs ? 1 : NT][kQs ? 1 : kSteps][2];
-        if constexpr (!kQs) {
+        uint32_t qf[kWide ? 1 : QP][kWide ? 1 : NT][kWide ? 1 : kSteps][2];
+        if constexpr (!kWide) {
 #pragma unroll
             for (int q = 0; q < QP; ++q)
 #pragma unroll
@@ -622,34 +652,27 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                         qf[q][nt][s][1] = w.y;
                     }
         }
-        float rowf[NT][2], off[NT][2];  // of this lane's two score columns
-        auto row_factors = [&]() {
+        float rowf[kStats], off[kStats];  // of this lane's rows (wide: read when they are needed)
+        if constexpr (!kWide) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    rowf[nt][i] = sm_f[nt * 8 + 2 * t + i];
-                    off[nt][i] = sm_off[nt * 8 + 2 * t + i];
-                }
-        };
-        if constexpr (!kQs)
-            row_factors();
+            for (int k = 0; k < kStats; ++k) {
+                rowf[k] = sm_f[(k >> 1) * 8 + 2 * t + (k & 1)];
+                off[k] = sm_off[(k >> 1) * 8 + 2 * t + (k & 1)];
+            }
+        }
         // parts that begin here or before are seen by every row
         const int all_see = row_base + kRows > p.R ? INT_MIN : (p.causal ? n - p.NQ + 1 : n) - kPart;
 
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                mx[nt][i] = -INFINITY;
-                l[nt][i] = 0.f;
-            }
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[s][nt][i] = 0.f;
+        for (int k = 0; k < kStats; ++k) {
+            mx[k] = -INFINITY;
+            l[k] = 0.f;
         }
+#pragma unroll
+        for (int s = 0; s < kSteps * NT; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[s][i] = 0.f;
 
         uint32_t st = ring, fill = ring + (S - 1) * kStage;
         int ahead = S - 1;
@@ -657,11 +680,161 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
             asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");  // this tile's
             __syncwarp();  // the copies of the other lanes; the stage filled next has been read
             issue(ahead++, fill);
+            if constexpr (kWide) {
+                constexpr int M = NT / 2;  // groups of 16 rows
+                float ks[HB], lv[HB], iv[HB];
+                int place[HB];
+#pragma unroll
+                for (int x = 0; x < HB; ++x) {
+                    const uint2 sc = lds8(st + kTileBytes + x * 8);
+                    ks[x] = __uint_as_float(sc.x);
+                    const float vs = fmaxf(__uint_as_float(sc.y), kMinScale);
+                    lv[x] = fast_log2(vs);
+                    iv[x] = fast_rcp(vs);
+                    place[x] = static_cast<int>(lds4(st + kTileBytes + 32 + x * 4));
+                }
+                // ---- S = Q K^T, eight tokens at a time
+                float s[M][4][4];
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            s[m][e][i] = sm_off[m * 16 + (i >> 1) * 8 + g];
+#pragma unroll
+                for (int ch = 0; ch < kChunks; ++ch) {
+                    uint32_t w[4][4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint4 v = lds16(st + e * 8 * D + (read_k ^ ch * 64));
+                        w[e][0] = v.x, w[e][1] = v.y, w[e][2] = v.z, w[e][3] = v.w;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t a[M][4];
+#pragma unroll
+                        for (int m = 0; m < M; ++m) {
+                            const uint4 v = reinterpret_cast<const uint4*>(sm_q)[((ch * 4 + i) * M + m) * 32 + lane];
+                            a[m][0] = v.x, a[m][1] = v.y, a[m][2] = v.z, a[m][3] = v.w;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t u = w[e][i] ^ 0x80808080u, b0 = __byte_perm(u, 0, 0x4140), b1 = __byte_perm(u, 0, 0x4342);
+#pragma unroll
+                            for (int m = 0; m < M; ++m)
+                                mma(s[m][e], a[m], b0, b1);
+                        }
+                    }
+                }
+                // ---- scores in base 2 plus log2 of the value scale, less the maximum; hidden ones -inf
+                bool hide = false, raise = false;
+#pragma unroll
+                for (int x = 0; x < HB; ++x)
+                    hide |= place[x] > all_see;
+                float top[2 * M];
+#pragma unroll
+                for (int k = 0; k < 2 * M; ++k) {
+                    const int m = k >> 1, i0 = (k & 1) * 2;
+                    const float base = mx[k] == -INFINITY ? 0.f : mx[k] - kLift;
+                    top[k] = -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int x = HB == 4 ? e : e >> 1;
+                        const float f = sm_f[m * 16 + (k & 1) * 8 + g] * ks[x], add = lv[x] - base;
+                        s[m][e][i0] = fmaf(s[m][e][i0], f, add);
+                        s[m][e][i0 + 1] = fmaf(s[m][e][i0 + 1], f, add);
+                    }
+                    if (hide) {
+                        const int lim = sm_lim[m * 16 + (k & 1) * 8 + g];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                if ((HB == 4 ? place[e & (HB - 1)] : place[e >> 1] + (e & 1) * 8) + 2 * t + i >= lim)
+                                    s[m][e][i0 + i] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        top[k] = fmaxf(top[k], fmaxf(s[m][e][i0], s[m][e][i0 + 1]));
+                    raise |= top[k] > (mx[k] == -INFINITY ? -INFINITY : kLift + kSlack);
+                }
+                if (__any_sync(kFullWarp, raise)) {
+#pragma unroll
+                    for (int k = 0; k < 2 * M; ++k) {
+                        const int m = k >> 1, i0 = (k & 1) * 2;
+                        const float base = mx[k] == -INFINITY ? 0.f : mx[k] - kLift;
+                        float high = top[k];
+                        high = fmaxf(high, __shfl_xor_sync(kFullWarp, high, 1));
+                        high = fmaxf(high, __shfl_xor_sync(kFullWarp, high, 2));
+                        high = fmaxf(high + base, mx[k]);
+                        const float down = high == -INFINITY ? 1.f : fast_exp2(mx[k] - high);
+                        const float less = high == -INFINITY ? 0.f : base - (high - kLift);
+                        mx[k] = high;
+                        l[k] *= down;
+#pragma unroll
+                        for (int j = 0; j < kOct; ++j) {
+                            o[m * kOct + j][i0] *= down;
+                            o[m * kOct + j][i0 + 1] *= down;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            s[m][e][i0] += less;
+                            s[m][e][i0 + 1] += less;
+                        }
+                    }
+                }
+                // ---- weights, as they are the fragments of P
+                uint32_t pf[2][M][4];
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            w[i] = fast_exp2(s[m][e][i]);
+                        const float inv = iv[HB == 4 ? e : e >> 1];
+                        l[m * 2] = fmaf(w[0] + w[1], inv, l[m * 2]);
+                        l[m * 2 + 1] = fmaf(w[2] + w[3], inv, l[m * 2 + 1]);
+                        pf[e >> 1][m][(e & 1) * 2] = half2_bits(__floats2half2_rn(w[0], w[1]));
+                        pf[e >> 1][m][(e & 1) * 2 + 1] = half2_bits(__floats2half2_rn(w[2], w[3]));
+                    }
+                // ---- O += P V, eight channels at a time
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t sv = st + kTile * D + j * 16 * D;
+                    uint32_t vw[4][D / 32];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (D == 128) {
+                            const uint4 v = lds16(sv + (i >> 1) * 8 * D + (i & 1) * 128 + read_v);
+                            vw[i][0] = v.x, vw[i][1] = v.y, vw[i][2] = v.z, vw[i][3] = v.w;
+                        } else {
+                            const uint2 v = lds8(sv + (i >> 1) * 8 * D + (i & 1) * 256 + read_v);
+                            vw[i][0] = v.x, vw[i][1] = v.y;
+                        }
+                    }
+#pragma unroll
+                    for (int w = 0; w < D / 32; ++w)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const uint32_t pick = half ? 0x7362 : 0x5140;
+                            const uint32_t lo = __byte_perm(vw[0][w], vw[1][w], pick) ^ 0x80808080u;
+                            const uint32_t hi = __byte_perm(vw[2][w], vw[3][w], pick) ^ 0x80808080u;
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t b0 = codes2(lo, i ? 0x4342 : 0x4140), b1 = codes2(hi, i ? 0x4342 : 0x4140);
+#pragma unroll
+                                for (int m = 0; m < M; ++m)
+                                    mma(o[m * kOct + w * 4 + half * 2 + i], pf[j][m], b0, b1);
+                            }
+                        }
+                }
+            } else {
 #pragma unroll 1
             for (int j0 = 0; j0 < 2; j0 += J) {
                 constexpr int B2 = HB / 2;  // blocks of a group of 16
-                if constexpr (kQs)  // (registers are short: from shared memory each time)
-                    row_factors();
                 float ks[J][B2], lv[J][B2], iv[J][B2];
                 int place[J][2];
 #pragma unroll
@@ -686,7 +859,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            sacc[j][nt][i] = off[nt][i & 1];
+                            sacc[j][nt][i] = off[nt * 2 + (i & 1)];
 #pragma unroll
                 for (int ch = 0; ch < kChunks; ++ch) {
                     uint32_t wa[J][4], wb[J][4];
@@ -710,12 +883,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                             for (int q = 0; q < QP; ++q)
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) {
-                                    if constexpr (kQs) {
-                                        const uint2 w = sm_q[((q * kSteps + ch * 4 + i) * NT + nt) * 32 + lane];
-                                        mma(sacc[j][nt], a, w.x, w.y);
-                                    } else {
-                                        mma(sacc[j][nt], a, qf[q][nt][ch * 4 + i][0], qf[q][nt][ch * 4 + i][1]);
-                                    }
+                                    mma(sacc[j][nt], a, qf[q][nt][ch * 4 + i][0], qf[q][nt][ch * 4 + i][1]);
                                 }
                         }
                     }
@@ -729,7 +897,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            sacc[j][nt][i] = fmaf(sacc[j][nt][i], rowf[nt][i & 1] * ks[j][i >> 1 & (B2 - 1)], lv[j][i >> 1 & (B2 - 1)]);
+                            sacc[j][nt][i] = fmaf(sacc[j][nt][i], rowf[nt * 2 + (i & 1)] * ks[j][i >> 1 & (B2 - 1)], lv[j][i >> 1 & (B2 - 1)]);
                 }
                 if (hide) {
 #pragma unroll
@@ -749,7 +917,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                         top[nt][i] = fmaxf(sacc[0][nt][i], sacc[0][nt][i + 2]);
                         if constexpr (J == 2)
                             top[nt][i] = fmaxf(top[nt][i], fmaxf(sacc[J - 1][nt][i], sacc[J - 1][nt][i + 2]));
-                        raise |= top[nt][i] > mx[nt][i] + kSlack;
+                        raise |= top[nt][i] > mx[nt * 2 + i] + kSlack;
                     }
                 if (__any_sync(kFullWarp, raise)) {
 #pragma unroll
@@ -760,14 +928,14 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                             m = fmaxf(m, __shfl_xor_sync(kFullWarp, m, 4));
                             m = fmaxf(m, __shfl_xor_sync(kFullWarp, m, 8));
                             m = fmaxf(m, __shfl_xor_sync(kFullWarp, m, 16));
-                            m = fmaxf(m, mx[nt][i]);
-                            const float down = m == -INFINITY ? 1.f : fast_exp2(mx[nt][i] - m);
-                            mx[nt][i] = m;
-                            l[nt][i] *= down;
+                            m = fmaxf(m, mx[nt * 2 + i]);
+                            const float down = m == -INFINITY ? 1.f : fast_exp2(mx[nt * 2 + i] - m);
+                            mx[nt * 2 + i] = m;
+                            l[nt * 2 + i] *= down;
 #pragma unroll
                             for (int s = 0; s < kSteps; ++s) {
-                                o[s][nt][i] *= down;
-                                o[s][nt][i + 2] *= down;
+                                o[s * NT + nt][i] *= down;
+                                o[s * NT + nt][i + 2] *= down;
                             }
                         }
                 }
@@ -776,7 +944,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     // (a row that has seen nothing: its scores are -inf, and so is what is left of them)
-                    const float base[2] = {fmaxf(mx[nt][0], -3.402823466e38f) - kLift, fmaxf(mx[nt][1], -3.402823466e38f) - kLift};
+                    const float base[2] = {fmaxf(mx[nt * 2], -3.402823466e38f) - kLift, fmaxf(mx[nt * 2 + 1], -3.402823466e38f) - kLift};
 #pragma unroll
                     for (int j = 0; j < J; ++j) {
                         float w[4];
@@ -786,9 +954,9 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             if constexpr (B2 == 1)
-                                l[nt][i] = fmaf(w[i] + w[i + 2], iv[j][0], l[nt][i]);
+                                l[nt * 2 + i] = fmaf(w[i] + w[i + 2], iv[j][0], l[nt * 2 + i]);
                             else
-                                l[nt][i] = fmaf(w[i], iv[j][0], fmaf(w[i + 2], iv[j][B2 - 1], l[nt][i]));
+                                l[nt * 2 + i] = fmaf(w[i], iv[j][0], fmaf(w[i + 2], iv[j][B2 - 1], l[nt * 2 + i]));
                         }
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
@@ -831,7 +999,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
                                 if constexpr (QP == 1) {
-                                    mma(o[2 * w + i][nt], a, pf[j][0][nt][0], pf[j][0][nt][1]);
+                                    mma(o[(2 * w + i) * NT + nt], a, pf[j][0][nt][0], pf[j][0][nt][1]);
                                 } else {
                                     // a group's products by themselves: added to the sums by rounded
                                     // additions (the tensor core's own cut off what does not fit)
@@ -840,12 +1008,13 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                                     mma(d, a, pf[j][0][nt][0], pf[j][0][nt][1]);
 #pragma unroll
                                     for (int y = 0; y < 4; ++y)
-                                        o[2 * w + i][nt][y] += d[y];
+                                        o[(2 * w + i) * NT + nt][y] += d[y];
                                 }
                             }
                         }
                     }
                 }
+            }
             }
             st = st + kStage == ring + S * kStage ? ring : st + kStage;
             fill = fill + kStage == ring + S * kStage ? ring : fill + kStage;
