@@ -110,8 +110,7 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(const __grid_cons
     int2* span = reinterpret_cast<int2*>(smem + 2 * p.B);  // [B] (first new token, rows; -1 refused)
     int* held = reinterpret_cast<int*>(span + p.B);        // [B] blocks it had
     __shared__ int2 part[kPlanWarps];
-    grid_dependents_launch();
-    grid_dependency_wait();
+    grid_begin();
     const int tid = threadIdx.x, B = p.B;
     const bool lead = blockIdx.x == 0;
     const int per = (B + kPlanThreads - 1) / kPlanThreads;  // consecutive sequences per thread

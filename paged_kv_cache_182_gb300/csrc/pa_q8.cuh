@@ -20,6 +20,15 @@ namespace pa {
 constexpr unsigned kFullWarp = 0xffffffffu;
 constexpr float kMinScale = PA_Q8_MIN_SCALE;
 
+// What every kernel here begins with, in this order: a kernel that is let off may read
+// its inputs before this one has ended (pa_opts.inputs_unchanged), and what the kernel
+// ahead of this one writes may be among them.
+__device__ __forceinline__ void grid_begin()
+{
+    grid_dependency_wait();
+    grid_dependents_launch();
+}
+
 __device__ __forceinline__ void q8_report(int* status, int bit)
 {
     if (status)
@@ -197,7 +206,7 @@ inline int q8_sizes(int B, int KV, int D, int BLOCK, int max_blocks, int num_blo
 }
 
 // A launch that may begin before the kernel ahead of it on the stream has ended;
-// the kernel waits for that one before it reads anything (grid_dependency_wait).
+// the kernel waits for that one before it reads anything (grid_begin).
 inline int q8_launch(const void* fn, dim3 grid, int threads, size_t smem, cudaStream_t st, void** args, int cluster = 1)
 {
     if (smem > 40 * 1024 &&  // (48 KB with what a kernel has statically)

@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
     // the row's 128 is taken off the score beforehand.  (Keys only: the values'
     // weights have one sign, and their sum would swamp the output.)
     constexpr bool kSmall = QP == 1;
+    constexpr float kUnit = kSmall ? 8192.f : 1.f;  // 2^13 of the 2^24 by the key scale, 2^11 by the row's factor: neither overflows
     constexpr int J = Sh::kJoint, kCharge = Sh::kCharge;
     extern __shared__ __align__(16) unsigned char smem[];  // ring | query fragments | states | prefix sums
     __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
@@ -177,8 +178,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
     __shared__ float sm_off[kRows];  // what a row's scores begin with (kSmall)
     __shared__ int sm_lim[kRows];  // keys that the row sees
     __shared__ OpenPiece sm_open[2];
-    grid_dependents_launch();
-    grid_dependency_wait();
+    grid_begin();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * S * kStage);
     // a copy takes kRowsCopy rows of D bytes, 16 bytes a lane, whole lines together;
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
             if (t == 0) {
                 const int r = row_base + warp * 8 + g;
                 const float down = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-                sm_f[warp * 8 + g] = p.scale * down * (kSmall ? 16777216.f : 1.f);
+                sm_f[warp * 8 + g] = p.scale * down * (kSmall ? 2048.f : 1.f);
                 sm_off[warp * 8 + g] = kSmall ? total * (-128.f / 16777216.f) : 0.f;
                 sm_lim[warp * 8 + g] = r >= p.R ? 0 : p.causal ? min(n, n - p.NQ + r % p.NQ + 1) : n;
             }
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
 #pragma unroll
                 for (int x = 0; x < HB; ++x) {
                     const uint2 sc = lds8(st + kTileBytes + x * 8);
-                    ks[x] = __uint_as_float(sc.x);
+                    ks[x] = fmaxf(__uint_as_float(sc.x), kMinScale) * kUnit;
                     const float vs = fmaxf(__uint_as_float(sc.y), kMinScale);
                     lv[x] = fast_log2(vs);
                     iv[x] = fast_rcp(vs);
@@ -843,7 +843,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                     for (int x = 0; x < B2; ++x) {
                         const int part = (j0 + j) * B2 + x;
                         const uint2 sc = lds8(st + kTileBytes + part * 8);
-                        ks[j][x] = __uint_as_float(sc.x);
+                        ks[j][x] = fmaxf(__uint_as_float(sc.x), kMinScale) * kUnit;
                         const float vs = fmaxf(__uint_as_float(sc.y), kMinScale);
                         lv[j][x] = fast_log2(vs);
                         iv[j][x] = fast_rcp(vs);
@@ -1104,6 +1104,7 @@ template <int D, int NT, int QP, int C>
 Variant variant(int BLOCK)
 {
     using Sh = Shape<D, NT, QP, C>;
+    static_assert(C > 1 || Sh::kRing + Sh::kQueryBytes + Sh::kGroup * Sh::kState + (kMaxEntries + 1) * 4 + 4096 <= 227 * 1024, "with the arrays of its own");
     return {BLOCK == 8 ? reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 4, C>)
                        : reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 2, C>),
             Sh::kRows, Sh::kThreads, C, Sh::kCharge, static_cast<size_t>(Sh::kRing) + Sh::kQueryBytes + Sh::kGroup * Sh::kState};

@@ -82,13 +82,12 @@ __global__ void __launch_bounds__(T, 512 / T) pa_q8_select_kernel(const __grid_c
     __shared__ __align__(16) uint32_t hist[2][kBins];
     __shared__ uint32_t wide[kWarps][2];
     __shared__ int cnt[kWarps][2];
-    grid_dependents_launch();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int seg = blockIdx.y, b = seg / p.KV, h = seg - b * p.KV;
     const int rank = C == 1 ? 0 : static_cast<int>(blockIdx.x);
     if (C > 1)  // the first CTA's shared memory may be written once it runs
         asm volatile("barrier.cluster.arrive;" ::: "memory");
-    grid_dependency_wait();
+    grid_begin();
     int n = __ldg(p.lens + b);
     const int32_t* table = p.table + static_cast<int64_t>(b) * p.maxb;
     // the cluster's warps take 16 blocks each in turn, a lane those of rows g and g + 8
@@ -468,7 +467,7 @@ extern "C" int pa_q8_select(const void* q, const int8_t* bounds, const float* k_
     // CTAs per segment: as many as have a step of blocks each, up to a cluster of 16,
     // while the SMs hold them all at once (one each, or two in clusters up to 8)
     constexpr int T = 256;
-    constexpr size_t kRoom = 224 * 1024;
+    constexpr size_t kRoom = 223 * 1024;  // (227 KB with the kernel's own arrays)
     int C = 16;
     while (C > 1 && (static_cast<long long>(B) * KV * C > (C == 16 ? 152 : 304) || T / 2 * (C / 2) >= o.max_blocks))
         C /= 2;

@@ -219,8 +219,7 @@ __global__ void __launch_bounds__(append_threads(BLOCK * D), sizeof(T) == 2 ? 67
     constexpr int kRuns = D / 16, kRows = kGroup / kRuns;  // a thread's rows: r, r + kRows (= BLOCK / 2)
     __shared__ float part[2][kThreads / 32];
     __shared__ __align__(16) uint32_t ends[kThreads / 32][2][kRuns * 8];  // lowest, highest codes by warp
-    grid_dependents_launch();
-    grid_dependency_wait();
+    grid_begin();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.z;
     const int h = blockIdx.y * kHeads + tid / kGroup;
@@ -408,8 +407,7 @@ struct ReadParams {
 template <typename T, int D>
 __global__ void __launch_bounds__(kStoreThreads) pa_q8_read_kernel(const __grid_constant__ ReadParams p, int rows_cta)
 {
-    grid_dependents_launch();
-    grid_dependency_wait();
+    grid_begin();
     constexpr int kRuns = D / 16;
     const int tid = threadIdx.x, b = blockIdx.z, kv = blockIdx.y;
     const bool lead = tid == 0 && blockIdx.x == 0 && kv == 0;

@@ -525,6 +525,35 @@ def test_attention_of_queries_of_every_size(pa):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["f32", "bf16"])
+@pytest.mark.parametrize("G", [4, 20])
+def test_attention_of_queries_near_the_largest_number(pa, fmt, G):
+    """Factors of rows and keys stay finite: the softmax is one key, and no output is a NaN."""
+    c = Cache(27, [200] * 2, 1, 64, 16)
+    x = rows_of(c.rng, fmt, 2, G, 1, 64)
+    out = pa.decode_q8((x * 2.0 ** 120).cuda(), *c.cuda(), ints(c.lens), scale=0.125)
+    torch.cuda.synchronize()
+    for b in range(2):
+        K, V = c.rows(b, np.arange(200), 0)
+        np.testing.assert_allclose(as64(out)[b, :, 0], V[(as64(x)[b, :, 0] @ K.T).argmax(1)], rtol=2.0 ** -7, atol=1e-6)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["f32", "f16", "bf16"])
+def test_attention_with_the_smallest_key_scales(pa, fmt):
+    """A key scale below 2^-96 counts as 2^-96, also where the queries are large enough to tell."""
+    c = Cache(28, [200] * 2, 1, 64, 16)
+    c.ks[:] = np.float32(2.0 ** -96)
+    c.ks[c.table[0, :5]] = 0
+    c.ks[c.table[1, 3:]] = np.float32(2.0 ** -110)
+    q = rows_of(c.rng, fmt, 2, 4, 1, 64)
+    if fmt != "f16":
+        q = q * 2.0 ** 90
+        attend(pa, c, q, fmt, True)
+    attend(pa, c, q, fmt, True, scale=2.0 ** 20)
+
+
+@pytest.mark.gpu
 def test_attention_of_what_is_not_finite(pa):
     """A query row that is not finite is its own concern."""
     c = Cache(14, [100], 1, 64, 16)

@@ -290,6 +290,60 @@ def test_selection_over_the_longest_table(pa, B, KV, D, R):
         np.testing.assert_array_equal(cnt[b].cpu().numpy(), wc[0])
 
 
+@pytest.mark.parametrize("maxb,D,R,KV", [(32512, 128, 64, 1), (32480, 128, 300, 1), (30000, 64, 128, 30)])
+def test_selection_where_shared_memory_is_full(pa, maxb, D, R, KV):
+    """Tables whose scores leave room for some of the rows at a time, to the last bytes."""
+    g = torch.Generator().manual_seed(3)
+    pool, c = 200, Cache(0, [8], KV, D, 8)
+    c.bounds = torch.randint(-127, 128, (pool, KV, 2, D), generator=g, dtype=torch.int8).sort(2).values.numpy()
+    c.ks = torch.rand(pool, KV, generator=g).numpy()
+    c.table = torch.randint(0, pool, (1, maxb), generator=g).to(torch.int32).numpy()
+    c.lens = np.array([1500], np.int32)
+    q = torch.randn(1, KV * (R if R <= 128 else R // 10), 1 if R <= 128 else 10, D, generator=g)
+    sel, cnt = pa.select_blocks_q8(q.cuda(), torch.from_numpy(c.bounds).cuda(), torch.from_numpy(c.ks).cuda(),
+                                   torch.from_numpy(c.table).cuda(), ints(c.lens), BLOCK=8, budget=60)
+    torch.cuda.synchronize()
+    ws, wc = c.select(q.numpy(), 60, 0, 1)
+    np.testing.assert_array_equal(sel.cpu().numpy(), ws)
+    np.testing.assert_array_equal(cnt.cpu().numpy(), wc)
+
+
+@pytest.mark.parametrize("op", ["blocks", "append", "read", "select", "decode"])
+def test_a_decode_that_reads_its_inputs_early_behind_them(pa, op):
+    """A decode with inputs_unchanged: the kernel ahead of it writes none of its inputs, the one before that its q."""
+    from test_scored import make
+
+    x, _ = make(41, "f16", [6000, 5000, 300], 16, 2, 128, 16, 1)
+    first = pa.Plan(*x, scale=0.09, causal=True)
+    second = pa.Plan(first.out, *x[1:], scale=1.0, causal=True, inputs_unchanged=True)
+    c = Cache(29, [40, 3], 2, 64, 16, more=8)
+    dev, lens = c.cuda(), ints(c.lens)
+    rows, q = rows_of(c.rng, "f16", 2, 2, 2, 64).cuda(), rows_of(c.rng, "f16", 2, 4, 1, 64).cuda()
+    between = {"blocks": lambda: pa.BlockPlan(dev[4], lens, ints(range(8)), ints([8]), BLOCK=16, width=1),
+               "append": lambda: pa.Q8AppendPlan(rows, rows, *dev, lens),
+               "read": lambda: pa.Q8ReadPlan(*dev, ints([0, 0]), width=4),
+               "select": lambda: pa.Q8SelectPlan(q, torch.from_numpy(c.bounds).cuda(), dev[2], dev[4], lens, BLOCK=16, budget=2),
+               "decode": lambda: pa.Q8Plan(q, *dev, lens, scale=0.125)}[op]()
+    sets = [torch.randn_like(x[0]) for _ in range(2)]
+    want = []
+    for s in sets:
+        x[0].copy_(s)
+        first.run()
+        torch.cuda.synchronize()
+        want.append(second.run().clone())
+        torch.cuda.synchronize()
+    assert not torch.equal(*want)
+    got = []
+    for n in range(40):
+        x[0].copy_(sets[n % 2])
+        first.run()
+        between.run()
+        got.append(second.run().clone())
+    torch.cuda.synchronize()
+    for n, t in enumerate(got):
+        assert torch.equal(t, want[n % 2]), n
+
+
 def test_rows_that_are_one_row(pa):
     """New rows broadcast over sequences and tokens (strides of zero), and many heads."""
     c = Cache(26, [0, 13], 3, 64, 16, more=20)
