@@ -38,7 +38,7 @@ constexpr int kTile = 32;                 // tokens of a tile: two MMA groups of
 constexpr int kMaxEntries = 4096;         // prefix sums in shared memory
 constexpr int kMaxCtas = 304;             // two per SM
 constexpr int kChargeBytes = 32 << 13;    // a piece's start and end count for so many bytes of tiles on an SM
-constexpr int kJoinBytes = 8 << 13;       // joining the pieces of a segment, besides
+constexpr int kJoinBytes = 22 << 13;      // joining the pieces of a segment, besides
 constexpr int kMeta = 64;                 // bytes of a tile's scales and places
 constexpr float kLift = 6.f, kSlack = 8.f;  // weights are 2^(t - m + 6), t - m <= 8
 
@@ -107,7 +107,8 @@ struct Shape {
     static constexpr int kTileBytes = 2 * kTile * D, kStage = kTileBytes + kMeta;
     static constexpr int kStages = 2 * (D == 128 ? 1 : 2);
     static constexpr int kRing = kWarps * kStages * kStage;
-    static constexpr int kCharge = kChargeBytes / C / kTileBytes, kJoin = kJoinBytes / kTileBytes;  // in tiles
+    static constexpr int kCharge = kChargeBytes / C / kTileBytes, kJoin = kJoinBytes / C / kTileBytes;  // in tiles
+    static constexpr int kFull = C == 1 ? 98 : 182;  // CTAs that stream at the memory's rate
     // A warp's state in shared memory: steps of 16 + 4 floats, rows 4 (mod 32) floats
     // apart (wide: rows of D + 4, four floats together in an order of their own), so
     // that neither its writes nor its reads meet a bank twice
@@ -274,14 +275,39 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
     // teams, which costs them another start and end.
     int piece = 0;
     if (segments <= teams) {
-        piece = longest;
+        const int tiles = U - segments * kCharge, least = (tiles << p.lg_team) / Sh::kFull;
+        const int whole = max(longest, least);
+        piece = whole <= max(share, least) + Sh::kJoin ? longest : 0;
         if (segments < teams) {
-            const int cut = max(4, (U - segments * kCharge + teams - segments - 1) / (teams - segments));
-            if (cut + Sh::kJoin < longest)
+            // (tiles / (teams - segments) always does; pieces end on average half a piece early)
+            int cut = static_cast<int>(static_cast<float>(tiles) * fast_rcp(static_cast<float>(teams - segments)));
+            cut = max(4, cut + (cut >> 20) + 1);  // (not below the quotient)
+            if (segments * 4 > teams && longest < 1 << 18 && (segments * 2 < teams || 0.9f * longest * segments > tiles)) {
+                constexpr int kTries = 2;
+                int size[kTries], sum[kTries];
+                float inv[kTries];
+#pragma unroll
+                for (int i = 0; i < kTries; ++i) {
+                    inv[i] = fast_rcp(static_cast<float>(teams) - static_cast<float>(segments) * (0.45f + 0.25f * i));
+                    size[i] = max(4, static_cast<int>(static_cast<float>(tiles) * inv[i]) + 1);
+                    inv[i] = fast_rcp(static_cast<float>(size[i]));
+                    sum[i] = 0;
+                }
+                // ceil(x / size): x - 1/2 is too far from a multiple for the rounding to matter
+                for (int e = lane; e < p.entries; e += 32) {
+                    const float x = static_cast<float>(prefix[e + 1] - prefix[e] - kCharge) - 0.5f;
+#pragma unroll
+                    for (int i = 0; i < kTries; ++i)
+                        sum[i] += static_cast<int>(x * inv[i]) + 1;
+                }
+#pragma unroll
+                for (int i = kTries - 1; i >= 0; --i)
+                    if (__reduce_add_sync(kFullWarp, sum[i]) * copies <= teams)
+                        cut = min(cut, size[i]);
+            }
+            if (cut < longest && max(cut, least) + Sh::kJoin < whole && cut <= share + (segments - 1) * 5 / 4)
                 piece = cut;
         }
-        if ((piece < longest ? piece : piece - Sh::kJoin) > share)
-            piece = 0;
     }
     int u_begin, u_end, first_team = 0, own_pieces = 1;
     if (piece > 0) {
@@ -1112,14 +1138,14 @@ Variant variant(int BLOCK)
 
 // `segments`: of 8 query rows.
 template <int D>
-Variant variant(int BLOCK, int dtype, int R, long long segments, int sms, int entries)
+Variant variant(int BLOCK, int dtype, int R, long long segments, int sms, int entries, bool even)
 {
     if (dtype == PA_F32)
         return R > 8 ? variant<D, 2, 2, 1>(BLOCK) : variant<D, 1, 2, 1>(BLOCK);
     if (R > 8)
         return R > 16 ? variant<D, 4, 1, 1>(BLOCK) : variant<D, 2, 1, 1>(BLOCK);
     const Variant two = variant<D, 1, 1, 2>(BLOCK);
-    return segments > sms / 2 && two.body + 4 * static_cast<size_t>(entries) <= 114000 ? two : variant<D, 1, 1, 1>(BLOCK);
+    return segments > (even ? sms : sms / 2) && two.body + 4 * static_cast<size_t>(entries) <= 114000 ? two : variant<D, 1, 1, 1>(BLOCK);
 }
 
 // Sizes that pa_q8_decode refuses, apart from those of the cache.
@@ -1217,7 +1243,7 @@ extern "C" int pa_q8_decode(const void* q, const int8_t* k_cache, const int8_t* 
         return PA_ERR_CUDA;
     const long long segments = static_cast<long long>(B) * KV;
     const int entries = o.selected ? B * KV : B;
-    const Variant v = D == 64 ? variant<64>(BLOCK, o.dtype, R, segments, sms, entries) : variant<128>(BLOCK, o.dtype, R, segments, sms, entries);
+    const Variant v = D == 64 ? variant<64>(BLOCK, o.dtype, R, segments, sms, entries, o.selected) : variant<128>(BLOCK, o.dtype, R, segments, sms, entries, o.selected);
     DecodeParams p{};
     p.groups = (R + v.rows - 1) / v.rows;
     p.entries = entries;

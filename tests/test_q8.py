@@ -480,6 +480,18 @@ def test_attention_over_many_pieces(pa, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,KV", [(3, 8), (6, 8), (10, 8), (14, 8), (19, 8), (38, 8), (60, 8), (9, 7), (40, 1), (150, 1), (152, 2)])
+def test_attention_of_uneven_batches(pa, B, KV):
+    """Lengths from even to a single long one: whole sequences, equal pieces and shared ranges."""
+    rng = np.random.default_rng(B)
+    for uneven in (0, 1, 4, 20):
+        lens = np.ceil(rng.random(B) ** uneven * (60000 / (B * KV) + 200)).astype(int)
+        lens[rng.integers(B)] = 0
+        c = Cache(30 + uneven, lens.tolist(), KV, 64, 16)
+        attend(pa, c, rows_of(c.rng, "f16", B, KV, 1, 64) * 2, "f16", False)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["f32", "f16", "bf16"])
 def test_attention_with_scales_of_every_size(pa, fmt):
     """Value scales over many powers of two, zeros among them; the weight on small and large ones alike."""
