@@ -23,9 +23,9 @@
  *   new_lens[b]       keep + add, or n when refused
  *   new_free_count    free blocks left on the stack
  *   slots[b][j]       block_table[b][t / BLOCK] * BLOCK + t % BLOCK of token
- *                     t = keep + j for j < add, -1 behind them and when
- *                     refused: the slot_mapping of pa_rotary and
- *                     pa_cache_append
+ *                     t = keep + j for j < add, -1 behind them, when refused
+ *                     and for a block outside the pool: the slot_mapping of
+ *                     pa_rotary and pa_cache_append
  *   positions[b][j]   t, or starts[b] + j with starts (the place in the text,
  *                     after an eviction), for the same rows; -1 for the others
  *

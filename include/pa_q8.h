@@ -126,7 +126,8 @@ int pa_q8_read(const int8_t *k_cache, const int8_t *v_cache, const float *k_scal
  * q [B][H][NQ][D] of dtype, contiguous; selected [B][KV][budget], counts
  * [B][KV] int32.  Limits: max_blocks <= 32768, NQ <= PA_MAX_NQ, H / KV * NQ <=
  * 1024, B * KV <= 32768, keep_first + keep_last <= budget (else
- * PA_ERR_BAD_DIMS).  budget may exceed max_blocks.
+ * PA_ERR_BAD_DIMS).  budget may exceed max_blocks.  Table entries behind a
+ * sequence's blocks may be read, and are not used.
  */
 typedef struct pa_q8_select_opts {
     int max_blocks, num_blocks, dtype;
@@ -156,13 +157,16 @@ int pa_q8_select(const void *q, const int8_t *bounds, const float *k_scale,
  * products; 16-bit queries enter them with their own digits and weights with
  * 11 bits; float32 queries and weights with 22.  out is of q's dtype.
  *
- * Scales have to be finite; one below 2^-96 (0 among them) counts as 2^-96.
+ * Scales have to be finite and key scales below 2^114; one below 2^-96 (0 among
+ * them) counts as 2^-96.  A query row with an infinity or a NaN gives NaN, and
+ * no other row does.
  *
  * workspace: device, 256-byte aligned, pa_q8_workspace_bytes(); its first
  * pa_q8_workspace_zero_bytes() bytes zero before the first use, and every
  * call that completes leaves them zero.  Calls that may overlap on the GPU
  * need workspaces of their own.  Limits: NQ <= PA_MAX_NQ, H / KV * NQ <= 1024;
- * with `selected` B * KV <= 4096.
+ * with `selected` B * KV <= 4096; B * KV * ceil(H / KV * NQ / 8) * (capacity / 32
+ * + 64) < 2^31 (PA_ERR_BAD_DIMS), capacity being max_blocks, or budget, * BLOCK.
  */
 typedef struct pa_q8_opts {
     int max_blocks, num_blocks, dtype;

@@ -2,22 +2,41 @@
 // blocks (include/pa_q8.h).
 //
 // Work: segments (sequence, KV head, group of 8 NT query rows), each a run of
-// 16-token tiles, laid end to end in units of 8 tiles; every CTA takes an equal
-// range of units.  A segment cut between CTAs leaves partial states (maximum,
-// sum, values) in the workspace, and the last CTA to finish one joins them.
+// tiles of 32 tokens.  Teams of up to four CTAs take neighbouring heads of the
+// same tokens, whose cache lines lie together (24 to 64 uneven sequences: 30.5 us,
+// one CTA a team 34.7).  A team takes a segment whole, an equal piece of one, or,
+// where there are more segments than teams, a range of all segments' tiles laid end
+// to end, in which every piece costs a charge besides its tiles (without charges
+// 42 us for the uneven batch, 25 instead of 20 for one long sequence; without whole
+// segments and equal pieces 40 instead of 26 for 32 rows a head).  The states of a
+// segment cut between CTAs (maximum, sum, values) go to the workspace, and the last
+// CTA to finish one joins them: about 4 us, which whole segments save (64 MB of 24
+// even sequences 19 us, of 16, which are cut, 21).  A CTA starts the copies of its
+// next piece before it joins its warps' states of the last.
+//
+// What bounds it: memory, at 6.3 TB/s while it streams (one sequence of 256 MB in
+// 49 us); a call besides costs about 5.7 us before the first tiles are there
+// (lengths, ranges, table, then copies that all begin at once) and 3 to 5 behind
+// the last (65 MB of one sequence 19.5 us).  With 32 query rows a head it is the
+// instructions: 1.5 a cycle, tensor cores 33 %.
 //
 // Tiles: a warp streams its own tiles through a ring of shared memory with
 // 16-byte asynchronous copies, whole lines of 128 bytes together (copies in the
-// order of the fragments, four lines of 32 bytes at once, took up the L1's tags:
-// @), swizzled so that the reads meet no bank twice:
+// order of the fragments, four lines of 32 bytes at once, kept the L1's tags busy:
+// 512 MB of one sequence 124 us instead of 101 at the time), swizzled so that the
+// reads meet no bank twice:
 //   S^T = K Q^T:   lane (g, t) has rows g and g + 8 of K, D / 4 channels in runs
 //                  of 16; the channels' order is the same in Q's fragments;
 //   O^T += V^T P^T: lane (g, t) has tokens 2t, 2t + 1, 2t + 8, 2t + 9 of V,
 //                  channels D / 8 g ...: two tokens' codes interleaved are V^T's
 //                  fragment.
+// More than eight rows of 16 bits take the products' 16-row side instead, S = Q K^T
+// and O += P V (16 x 2048 tokens, 32 rows a head: 27.8 -> 25.5 us).
 // Codes become fp16 exactly (byte u = code + 128 under the exponent of 1024 is
-// 1024 + u; less 1152).  A query row is scaled by a power of two into fp16's
-// range, which loses nothing of a 16-bit row; float32 rows are two fp16 parts.
+// 1024 + u; less 1152).  Keys of 16-bit rows skip the subtraction: u by itself is a
+// subnormal number, and 128 times the row's sum is taken off beforehand.  A query
+// row is scaled by a power of two into fp16's range, which loses nothing of a
+// 16-bit row; float32 rows are two fp16 parts.
 //
 // Scales: the key scale multiplies the score.  The value scale joins the
 // exponent, t = s + log2(v_scale), so that weights times value scale come out of
@@ -38,7 +57,7 @@ constexpr int kTile = 32;                 // tokens of a tile: two MMA groups of
 constexpr int kMaxEntries = 4096;         // prefix sums in shared memory
 constexpr int kMaxCtas = 304;             // two per SM
 constexpr int kChargeBytes = 32 << 13;    // a piece's start and end count for so many bytes of tiles on an SM
-constexpr int kJoinBytes = 22 << 13;      // joining the pieces of a segment, besides
+constexpr int kJoinBytes = 22 << 13;      // joining the pieces of a segment, besides (of 4, 11, 16 and 30 none is better)
 constexpr int kMeta = 64;                 // bytes of a tile's scales and places
 constexpr float kLift = 6.f, kSlack = 8.f;  // weights are 2^(t - m + 6), t - m <= 8
 
@@ -108,7 +127,8 @@ struct Shape {
     static constexpr int kStages = 2 * (D == 128 ? 1 : 2);
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kCharge = kChargeBytes / C / kTileBytes, kJoin = kJoinBytes / C / kTileBytes;  // in tiles
-    static constexpr int kFull = C == 1 ? 98 : 182;  // CTAs that stream at the memory's rate
+    // CTAs that stream at the memory's rate: one of 12 warps takes 64 GB/s, of 6 warps 34.5
+    static constexpr int kFull = C == 1 ? 98 : 182;
     // A warp's state in shared memory: steps of 16 + 4 floats, rows 4 (mod 32) floats
     // apart (wide: rows of D + 4, four floats together in an order of their own), so
     // that neither its writes nor its reads meet a bank twice
@@ -270,9 +290,10 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
     // U = G share + extra: the first `extra` teams take one tile more
     const int share = U / G, extra = U - G * share;
     auto owner_of = [&](int x) { return x < extra * (share + 1) ? x / (share + 1) : extra + (x - extra * (share + 1)) / share; };
-    // Segments whole, or in equal pieces of at most `piece` tiles, one a team, where
-    // the largest is no more than a share: a share starts a second segment on most
-    // teams, which costs them another start and end.
+    // Segments whole, or in equal pieces of at most `piece` tiles, one a team, or the
+    // shares.  Estimates in tiles of one CTA: the longest run of tiles, but no less
+    // than what the memory's rate allows for them all, and what a join costs; of the
+    // shares also that a team starts a second segment.
     int piece = 0;
     if (segments <= teams) {
         const int tiles = U - segments * kCharge, least = (tiles << p.lg_team) / Sh::kFull;
@@ -1136,7 +1157,13 @@ Variant variant(int BLOCK)
             Sh::kRows, Sh::kThreads, C, Sh::kCharge, static_cast<size_t>(Sh::kRing) + Sh::kQueryBytes + Sh::kGroup * Sh::kState};
 }
 
-// `segments`: of 8 query rows.
+// `segments`: of 8 query rows.  One CTA of 12 warps per SM streams a segment twice as
+// fast as one of two with 6 each and keeps up to a segment per SM whole; two fill
+// in for each other's starts and ends, which counts where CTAs take several pieces.
+// 64 MB, one / two: one sequence of 8 heads 19.6 / 23.2 us, 13 even ones 18.2 / 21.9,
+// 40 even ones 29.7 / 25.3, 192 selected lists 24.7 / 16.6; 12 to 19 uneven
+// sequences (28 to 63 MB) 18 to 24 / 16 to 22.  Lists that were selected are mostly
+// of one length, sequences seldom.
 template <int D>
 Variant variant(int BLOCK, int dtype, int R, long long segments, int sms, int entries, bool even)
 {

@@ -8,13 +8,18 @@
 // a subnormal fp16 number as it stands (the row's 128 sum c is taken off
 // beforehand), a code is exact, and all sums are below 2^24 of the unit 2^-24:
 // nothing is rounded, in any order.  (Integer products, dp4a, run at a tenth of
-// the rate here: 42 us for 8 x 8 x 4096 blocks and 4 rows, 40 for 4 x 8 x 2048 and
-// 32 rows.)  A warp has 16 blocks in hand and 16 on their way; table entries are
-// read before the length is known.
+// the rate here: 42 us for 8 x 8 x 4096 blocks and 4 rows, now 25; 40 for 4 x 8 x 2048
+// and 32 rows, now 20.)  A warp has 16 blocks in hand and 16 on their way (three
+// steps, CTAs of 128 threads, or three CTAs per SM at 80 registers: 35 to 49 us for
+// the first); table entries are read before the length is known.
 //
 // The scores go to the first CTA of the cluster, which finds the score of the
 // last block taken by counting them in 256 bins over their range, then over the
 // bin that it falls into, until that bin is taken whole: mostly two rounds.
+//
+// What bounds it: latency.  8 heads of 2048 blocks (one sequence, clusters of 16)
+// take 9.0 us, 24 x 8 x 750 blocks (one CTA each) 17.3 us, 2.2 TB/s: the chain from
+// length to table, bounds, scores, cluster barrier, rounds of bins and places.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -465,7 +470,8 @@ extern "C" int pa_q8_select(const void* q, const int8_t* bounds, const float* k_
     p.cap = o.max_blocks * BLOCK;
     p.dtype = o.dtype;
     // CTAs per segment: as many as have a step of blocks each, up to a cluster of 16,
-    // while the SMs hold them all at once (one each, or two in clusters up to 8)
+    // while the SMs hold them all at once (one each, or two in clusters up to 8).  One
+    // CTA / clusters: 8 x 2048 blocks 25 / 9.5 us, 64 x 4096 47 / 25, 128 x 1024 12.9 / 11.8
     constexpr int T = 256;
     constexpr size_t kRoom = 223 * 1024;  // (227 KB with the kernel's own arrays)
     int C = 16;
