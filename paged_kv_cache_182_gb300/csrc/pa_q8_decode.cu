@@ -8,7 +8,8 @@
 // where there are more segments than teams, a range of all segments' tiles laid end
 // to end, in which every piece costs a charge besides its tiles (without charges
 // 42 us for the uneven batch, 25 instead of 20 for one long sequence; without whole
-// segments and equal pieces 40 instead of 26 for 32 rows a head).  The states of a
+// segments and equal pieces 40 instead of 26 for 32 rows a head).  Of many short
+// segments a warp takes whole ones by itself, and no states are joined.  The states of a
 // segment cut between CTAs (maximum, sum, values) go to the workspace, and the last
 // CTA to finish one joins them: about 4 us, which whole segments save (64 MB of 24
 // even sequences 19 us, of 16, which are cut, 21).  A CTA starts the copies of its
@@ -179,7 +180,8 @@ struct OpenPiece {
     int rows;
 };
 
-template <int D, int NT, int QP, int HB, int C>
+// kMany: more segments than CTAs, so that a warp may take whole ones by itself.
+template <int D, int NT, int QP, int HB, int C, bool kMany>
 __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode_kernel(const __grid_constant__ DecodeParams p)
 {
     using Sh = Shape<D, NT, QP, C>;
@@ -195,9 +197,12 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
     constexpr int J = Sh::kJoint, kCharge = Sh::kCharge;
     extern __shared__ __align__(16) unsigned char smem[];  // ring | query fragments | states | prefix sums
     __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
-    __shared__ float sm_f[kRows];  // of a row's scores: scale * log2(e) / the power of two
-    __shared__ float sm_off[kRows];  // what a row's scores begin with (kSmall)
-    __shared__ int sm_lim[kRows];  // keys that the row sees
+    // (by warp where each has a segment of its own)
+    constexpr int kSets = kMany ? kWarps : 1;
+    static_assert(!kMany || NT == 1);
+    __shared__ float sm_f[kSets * kRows];  // of a row's scores: scale * log2(e) / the power of two
+    __shared__ float sm_off[kSets * kRows];  // what a row's scores begin with (kSmall)
+    __shared__ int sm_lim[kSets * kRows];  // keys that the row sees
     __shared__ OpenPiece sm_open[2];
     grid_begin();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -330,8 +335,23 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                 piece = cut;
         }
     }
+    // Short ones: a warp takes a segment by itself, the next at a distance of all warps of
+    // the grid.  A tile of a warp's own costs about 7 / C of a share's (1.0 us), its start
+    // and end one more; a share its starts (charged) and a join.  8 heads of 128 channels,
+    // by itself / shares: 100 sequences of 64 tokens 8.1 / 20.4 us, of 256 16.9 / 26.6,
+    // of 1024 48 / 51, 40 of 1024 37 / 29; 800 of 64 tokens 32 / 230.
+    const int solo_step = gridDim.x * kWarps, solo_end = segments << p.lg_team;
+    bool solo = false;
+    if (kMany && piece == 0) {
+        const int rounds = (solo_end + solo_step - 1) / solo_step;
+        solo = 7.f * rounds * (longest + 1) <= static_cast<float>(C) * share + 36.f;
+    }
+    const int stride = solo ? 1 : kWarps, rows_at = solo ? warp * kRows : 0;
     int u_begin, u_end, first_team = 0, own_pieces = 1;
-    if (piece > 0) {
+    if (solo) {
+        u_begin = warp * gridDim.x + blockIdx.x;
+        u_end = solo_end;
+    } else if (piece > 0) {
         int e = copies == 1 ? team : team / copies;
         first_team = e * copies;
         if (piece < longest) {
@@ -391,7 +411,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
     uint32_t w_row = 0;                       // of this lane's part of the window: its first row of the pool
     int w_place = 0, blk_next = -1, phys_next = -1;
     auto look_up = [&](int window) {
-        const int tile = first + (window * kWindow + lane / HB) * kWarps;
+        const int tile = first + (window * kWindow + lane / HB) * stride;
         const int place = tile * kTile + kPart * (lane % HB);
         int j = -1;
         if (tile < last && place < tokens) {
@@ -409,7 +429,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
         phys_next = j >= 0 ? __ldg(table + j) : -1;
     };
     auto take_up = [&](int window) {
-        const int tile = first + (window * kWindow + lane / HB) * kWarps;
+        const int tile = first + (window * kWindow + lane / HB) * stride;
         const int in_block = (tile * kTile + kPart * (lane % HB)) & ((1 << p.shift) - 1);
         const bool there = static_cast<uint32_t>(phys_next) < static_cast<uint32_t>(p.num_blocks);
         if (!there && blk_next >= 0)
@@ -419,7 +439,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
         w_place = there ? (blk_next << p.shift) + in_block : INT_MAX - 64;
     };
     auto issue = [&](int k, uint32_t st) {  // the warp's k-th tile
-        if (first + k * kWarps < last) {
+        if (first + k * stride < last) {
             const int at_window = k & (kWindow - 1);
             if (at_window == 0 && k > 0)
                 take_up(k / kWindow);
@@ -450,8 +470,14 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
     // Takes up the piece at tile u and starts its first copies; false when only a
     // charge is left of this CTA's range (the next one has the tiles).
     auto begin = [&]() -> bool {
-        int e = 0;
-        {
+        int e = 0, c;
+        if (solo) {
+            const int all = copies << p.lg_team;
+            e = u / all;
+            c = u - e * all;
+            s_begin = from = 0;
+            s_end = stop = prefix[e + 1] - prefix[e] - kCharge;
+        } else {
             int hi = p.entries;
             while (hi - e > 1) {
                 const int mid = (e + hi) >> 1;
@@ -460,16 +486,16 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                 else
                     hi = mid;
             }
+            const int length = prefix[e + 1] - prefix[e];
+            const int cc = copies == 1 ? 0 : (u - prefix[e] * copies) / length;
+            s_end = prefix[e] * copies + (cc + 1) * length;
+            s_begin = s_end - length + kCharge;  // its first tile, behind the charge
+            from = max(u, s_begin);
+            stop = min(s_end, u_end);
+            if (stop <= s_begin)
+                return false;
+            c = (cc << p.lg_team) + member;
         }
-        const int length = prefix[e + 1] - prefix[e];
-        const int cc = copies == 1 ? 0 : (u - prefix[e] * copies) / length;
-        s_end = prefix[e] * copies + (cc + 1) * length;
-        s_begin = s_end - length + kCharge;  // its first tile, behind the charge
-        from = max(u, s_begin);
-        stop = min(s_end, u_end);
-        if (stop <= s_begin)
-            return false;
-        const int c = (cc << p.lg_team) + member;
         b = p.selected ? e / p.KV : e;
         kh = p.selected ? e - b * p.KV : p.groups == 1 ? c : c / p.groups;
         grp = p.selected ? c : p.groups == 1 ? 0 : c - kh * p.groups;
@@ -480,11 +506,11 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
         nb = (n + (1 << p.shift) - 1) >> p.shift;
         table = p.table + static_cast<int64_t>(b) * p.maxb;
         // this warp's tiles: first, first + kWarps, ... below last
-        first = from - s_begin + warp;
+        first = from - s_begin + (solo ? 0 : warp);
         last = min(stop - s_begin, (tokens + kTile - 1) / kTile);
         look_up(0);
-        if (warp < NT) {
-            const int row = row_base + warp * 8 + g;
+        if (warp < NT || solo) {
+            const int row = row_base + (solo ? 0 : warp * 8) + g;
 #pragma unroll
             for (int ch = 0; ch < kChunks; ++ch) {
                 const int64_t at = ((static_cast<int64_t>(b) * p.KV + kh) * p.R + row) * D + ch * 64 + t * 16;
@@ -520,9 +546,27 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
             sm_open[open] = {c0, count, p.counters + (static_cast<int64_t>(b) * p.KV + kh) * p.groups + grp, out0, rows_left};
         }
         if (have)
-            u = stop;
+            u = solo ? u + solo_step : stop;
         const bool more = u < u_end && begin();
-        if (have) {
+        if (have && solo) {
+            // ---- the warp's own state is all there is
+            if constexpr (kMany) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float sum = l[k];
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1)
+                        sum += __shfl_xor_sync(kFullWarp, sum, x);
+                    const float r = sum == 0.f ? 0.f : 1.f / sum;
+                    if (2 * t + k < rows_left) {
+                        const int64_t to = out0 + (2 * t + k) * D + D / 8 * g;
+#pragma unroll
+                        for (int s2 = 0; s2 < kSteps; s2 += 2)
+                            store_out(p, to + 2 * s2, make_float4(o[s2][k] * r, o[s2][k + 2] * r, o[s2 + 1][k] * r, o[s2 + 1][k + 2] * r));
+                    }
+                }
+            }
+        } else if (have) {
             // ---- the warps' states together
             auto row_of = [&](int k) { return kWide ? (k >> 1) * 16 + (k & 1) * 8 + g : (k >> 1) * 8 + 2 * t + (k & 1); };
 #pragma unroll
@@ -626,7 +670,8 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
         have = true;
 
         // ---- query rows as fragments of B, scaled by a power of two
-        if (warp < NT) {
+        uint32_t qf[kWide ? 1 : QP][kWide ? 1 : NT][kWide ? 1 : kSteps][2];
+        if (warp < NT || solo) {
             float x[kSteps * 4], a = 0.f;
 #pragma unroll
             for (int i = 0; i < kSteps * 4; i += QP == 2 ? 1 : 2) {
@@ -670,6 +715,9 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                         uint32_t* to = reinterpret_cast<uint32_t*>(sm_q) + ((s * (NT / 2) + warp / 2) * 32 + lane) * 4 + warp % 2;
                         to[0] = w[q][0];
                         to[2] = w[q][1];
+                    } else if (solo) {
+                        qf[q][0][s][0] = w[q][0];
+                        qf[q][0][s][1] = w[q][1];
                     } else {
                         sm_q[((q * kSteps + s) * NT + warp) * 32 + lane] = make_uint2(w[q][0], w[q][1]);
                     }
@@ -678,16 +726,18 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
             total += __shfl_xor_sync(kFullWarp, total, 1);
             total += __shfl_xor_sync(kFullWarp, total, 2);
             if (t == 0) {
-                const int r = row_base + warp * 8 + g;
+                const int in = solo ? 0 : warp * 8, r = row_base + in + g, at = rows_at + in + g;
                 const float down = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-                sm_f[warp * 8 + g] = p.scale * down * (kSmall ? 2048.f : 1.f);
-                sm_off[warp * 8 + g] = kSmall ? total * (-128.f / 16777216.f) : 0.f;
-                sm_lim[warp * 8 + g] = r >= p.R ? 0 : p.causal ? min(n, n - p.NQ + r % p.NQ + 1) : n;
+                sm_f[at] = p.scale * down * (kSmall ? 2048.f : 1.f);
+                sm_off[at] = kSmall ? total * (-128.f / 16777216.f) : 0.f;
+                sm_lim[at] = r >= p.R ? 0 : p.causal ? min(n, n - p.NQ + r % p.NQ + 1) : n;
             }
         }
-        __syncthreads();
-        uint32_t qf[kWide ? 1 : QP][kWide ? 1 : NT][kWide ? 1 : kSteps][2];
-        if constexpr (!kWide) {
+        if (solo)
+            __syncwarp();
+        else
+            __syncthreads();
+        if (!kWide && !solo) {
 #pragma unroll
             for (int q = 0; q < QP; ++q)
 #pragma unroll
@@ -703,8 +753,8 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
         if constexpr (!kWide) {
 #pragma unroll
             for (int k = 0; k < kStats; ++k) {
-                rowf[k] = sm_f[(k >> 1) * 8 + 2 * t + (k & 1)];
-                off[k] = sm_off[(k >> 1) * 8 + 2 * t + (k & 1)];
+                rowf[k] = sm_f[rows_at + (k >> 1) * 8 + 2 * t + (k & 1)];
+                off[k] = sm_off[rows_at + (k >> 1) * 8 + 2 * t + (k & 1)];
             }
         }
         // parts that begin here or before are seen by every row
@@ -723,7 +773,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
 
         uint32_t st = ring, fill = ring + (S - 1) * kStage;
         int ahead = S - 1;
-        for (int tile = first; tile < last; tile += kWarps) {
+        for (int tile = first; tile < last; tile += stride) {
             asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");  // this tile's
             __syncwarp();  // the copies of the other lanes; the stage filled next has been read
             issue(ahead++, fill);
@@ -953,7 +1003,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                if (place[j][i >> 1] + g >= sm_lim[nt * 8 + 2 * t + (i & 1)])
+                                if (place[j][i >> 1] + g >= sm_lim[rows_at + nt * 8 + 2 * t + (i & 1)])
                                     sacc[j][nt][i] = -INFINITY;
                 }
                 float top[NT][2];
@@ -1145,6 +1195,7 @@ struct Variant {
     const void* fn;
     int rows, threads, ctas, charge;
     size_t body;  // shared memory apart from the prefix sums
+    const void* many;  // for more segments than CTAs
 };
 
 template <int D, int NT, int QP, int C>
@@ -1152,9 +1203,12 @@ Variant variant(int BLOCK)
 {
     using Sh = Shape<D, NT, QP, C>;
     static_assert(C > 1 || Sh::kRing + Sh::kQueryBytes + Sh::kGroup * Sh::kState + (kMaxEntries + 1) * 4 + 4096 <= 227 * 1024, "with the arrays of its own");
-    return {BLOCK == 8 ? reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 4, C>)
-                       : reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 2, C>),
-            Sh::kRows, Sh::kThreads, C, Sh::kCharge, static_cast<size_t>(Sh::kRing) + Sh::kQueryBytes + Sh::kGroup * Sh::kState};
+    constexpr bool kMany = NT == 1;
+    return {BLOCK == 8 ? reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 4, C, false>)
+                       : reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 2, C, false>),
+            Sh::kRows, Sh::kThreads, C, Sh::kCharge, static_cast<size_t>(Sh::kRing) + Sh::kQueryBytes + Sh::kGroup * Sh::kState,
+            BLOCK == 8 ? reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 4, C, kMany>)
+                       : reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 2, C, kMany>)};
 }
 
 // `segments`: of 8 query rows.  One CTA of 12 warps per SM streams a segment twice as
@@ -1315,5 +1369,5 @@ extern "C" int pa_q8_decode(const void* q, const int8_t* k_cache, const int8_t* 
         p.lg_team = 0;
     p.copies = static_cast<int>(copies >> p.lg_team);
     void* args[] = {&p};
-    return q8_launch(v.fn, dim3(grid), v.threads, v.body + (static_cast<size_t>(entries) + 1) * 4, static_cast<cudaStream_t>(stream), args);
+    return q8_launch(entries * copies > grid ? v.many : v.fn, dim3(grid), v.threads, v.body + (static_cast<size_t>(entries) + 1) * 4, static_cast<cudaStream_t>(stream), args);
 }

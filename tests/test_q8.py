@@ -493,6 +493,23 @@ def test_attention_of_uneven_batches(pa, B, KV):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("B,KV,D,BLOCK,G,NQ", [(330, 1, 64, 8, 3, 2), (60, 8, 128, 16, 1, 1), (700, 1, 128, 32, 2, 1), (41, 8, 64, 64, 2, 4)])
+def test_attention_of_many_short_sequences(pa, fmt, B, KV, D, BLOCK, G, NQ):
+    """More sequences and heads than CTAs, each short, some empty, some longer than the rest; all blocks, and lists of some."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 130, B)
+    lens[rng.integers(0, B, 9)] = 0
+    for longest in (130, 700):
+        lens[rng.integers(0, B, 3)] = longest
+        c = Cache(31, lens.tolist(), KV, D, BLOCK)
+        q = rows_of(c.rng, fmt, B, KV * G, NQ, D) * 2
+        attend(pa, c, q, fmt, True)
+    sel, cnt = c.select(q.float().numpy(), 2, 0, 1)
+    attend(pa, c, q, fmt, False, selected=sel, counts=cnt)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["f32", "f16", "bf16"])
 def test_attention_with_scales_of_every_size(pa, fmt):
     """Value scales over many powers of two, zeros among them; the weight on small and large ones alike."""
     lens = [300, 77]
