@@ -56,7 +56,7 @@ namespace {
 
 constexpr int kTile = 32;                 // tokens of a tile: two MMA groups of 16
 constexpr int kMaxEntries = 4096;         // prefix sums in shared memory
-constexpr int kMaxCtas = 304;             // two per SM
+constexpr int kRecordRows = 304 * 32;     // query rows of all CTAs, at most
 constexpr int kChargeBytes = 32 << 13;    // a piece's start and end count for so many bytes of tiles on an SM
 constexpr int kJoinBytes = 22 << 13;      // joining the pieces of a segment, besides (of 4, 11, 16 and 30 none is better)
 constexpr int kMeta = 64;                 // bytes of a tile's scales and places
@@ -128,13 +128,13 @@ struct Shape {
     static constexpr int kStages = 2 * (D == 128 ? 1 : 2);
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kCharge = kChargeBytes / C / kTileBytes, kJoin = kJoinBytes / C / kTileBytes;  // in tiles
-    // CTAs that stream at the memory's rate: one of 12 warps takes 64 GB/s, of 6 warps 34.5
-    static constexpr int kFull = C == 1 ? 98 : 182;
+    // CTAs that stream at the memory's rate: one of 12 warps takes 64 GB/s, of 6 warps 34.5, of 4 23
+    static constexpr int kFull = C == 1 ? 98 : C == 2 ? 182 : 274;
     // A warp's state in shared memory: steps of 16 + 4 floats, rows 4 (mod 32) floats
     // apart (wide: rows of D + 4, four floats together in an order of their own), so
     // that neither its writes nor its reads meet a bank twice
     static constexpr int kStateStep = 20, kStateRow = kWide ? D + 4 : kSteps * kStateStep + 4, kState = kRows * kStateRow * 4;
-    static constexpr int kGroup = 2;  // warps' states joined at once beside a ring in use
+    static constexpr int kGroup = C == 3 ? 1 : 2;  // warps' states joined at once beside a ring in use
     static constexpr int kLastGroup = kRing >= kWarps * kState ? kWarps : kWarps / 2;  // ... and in the place of the ring
     static_assert(kRing >= kLastGroup * kState, "states fit");
     static constexpr int kQueryBytes = QP * kSteps * NT * 32 * 8;
@@ -1217,7 +1217,10 @@ Variant variant(int BLOCK)
 // 64 MB, one / two: one sequence of 8 heads 19.6 / 23.2 us, 13 even ones 18.2 / 21.9,
 // 40 even ones 29.7 / 25.3, 192 selected lists 24.7 / 16.6; 12 to 19 uneven
 // sequences (28 to 63 MB) 18 to 24 / 16 to 22.  Lists that were selected are mostly
-// of one length, sequences seldom.
+// of one length, sequences seldom.  Three of 4 warps are for as many segments as
+// they still keep whole: 40 sequences of 512 / 1024 tokens 14.1 / 21.1 us (two: 23.3 /
+// 29.2), 40 uneven ones of 43 MB 20.4 (23.7); with fewer segments they are slower (24
+// even sequences 21.7, two: 19.0), with more no better (60 of 512 tokens 26.6, 22.7).
 template <int D>
 Variant variant(int BLOCK, int dtype, int R, long long segments, int sms, int entries, bool even)
 {
@@ -1225,8 +1228,11 @@ Variant variant(int BLOCK, int dtype, int R, long long segments, int sms, int en
         return R > 8 ? variant<D, 2, 2, 1>(BLOCK) : variant<D, 1, 2, 1>(BLOCK);
     if (R > 8)
         return R > 16 ? variant<D, 4, 1, 1>(BLOCK) : variant<D, 2, 1, 1>(BLOCK);
-    const Variant two = variant<D, 1, 1, 2>(BLOCK);
-    return segments > (even ? sms : sms / 2) && two.body + 4 * static_cast<size_t>(entries) <= 114000 ? two : variant<D, 1, 1, 1>(BLOCK);
+    const size_t sums = 4 * static_cast<size_t>(entries);
+    const Variant two = variant<D, 1, 1, 2>(BLOCK), three = variant<D, 1, 1, 3>(BLOCK);
+    if (segments > 2 * sms && segments <= 3 * sms && three.body + sums <= 75000)
+        return three;
+    return segments > (even ? sms : sms / 2) && two.body + sums <= 114000 ? two : variant<D, 1, 1, 1>(BLOCK);
 }
 
 // Sizes that pa_q8_decode refuses, apart from those of the cache.
@@ -1249,8 +1255,8 @@ Workspace workspace_of(int B, int H, int KV, int D, int NQ)
     const size_t groups = (R + 7) / 8;  // at most: passes of 8 rows
     Workspace w;
     w.zero = (static_cast<size_t>(B) * KV * groups * 4 + 255) / 256 * 256;
-    w.ml = static_cast<size_t>(kMaxCtas) * 2 * 32 * 8;
-    w.o = static_cast<size_t>(kMaxCtas) * 2 * 32 * D * 4;
+    w.ml = static_cast<size_t>(kRecordRows) * 2 * 8;
+    w.o = static_cast<size_t>(kRecordRows) * 2 * D * 4;
     w.total = w.zero + w.ml + w.o;
     return w;
 }
@@ -1361,7 +1367,7 @@ extern "C" int pa_q8_decode(const void* q, const int8_t* k_cache, const int8_t* 
     p.budget = o.budget;
     p.causal = o.causal ? 1 : 0;
     p.dtype = o.dtype;
-    const int grid = sms * v.ctas > kMaxCtas ? kMaxCtas : sms * v.ctas;
+    const int grid = sms * v.ctas > kRecordRows / v.rows ? kRecordRows / v.rows : sms * v.ctas;
     // Teams: the copies of one length that run side by side (rows of the same or of
     // neighbouring heads, whose cache lines lie together)
     p.lg_team = copies % 4 == 0 ? 2 : copies % 2 == 0 ? 1 : 0;
