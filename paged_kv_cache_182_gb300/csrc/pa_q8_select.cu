@@ -402,9 +402,10 @@ __global__ void __launch_bounds__(T, 512 / T) pa_q8_select_kernel(const __grid_c
 }
 
 template <int D>
-const void* select_kernel(int C)
+const void* select_kernel(int C, int T)
 {
-    return C == 1   ? reinterpret_cast<const void*>(pa_q8_select_kernel<D, 1, 256>)
+    return T == 128 ? reinterpret_cast<const void*>(pa_q8_select_kernel<D, 1, 128>)
+           : C == 1 ? reinterpret_cast<const void*>(pa_q8_select_kernel<D, 1, 256>)
            : C == 2 ? reinterpret_cast<const void*>(pa_q8_select_kernel<D, 2, 256>)
            : C == 4 ? reinterpret_cast<const void*>(pa_q8_select_kernel<D, 4, 256>)
            : C == 8 ? reinterpret_cast<const void*>(pa_q8_select_kernel<D, 8, 256>)
@@ -469,10 +470,14 @@ extern "C" int pa_q8_select(const void* q, const int8_t* bounds, const float* k_
     p.shift = BLOCK == 8 ? 3 : BLOCK == 16 ? 4 : BLOCK == 32 ? 5 : 6;
     p.cap = o.max_blocks * BLOCK;
     p.dtype = o.dtype;
+    // Smaller CTAs, four per SM, where two per SM do not hold all segments and a table
+    // leaves them the room: 100 x 8 segments of 64 / 256 / 512 blocks 13.5 / 24.4 / 37.2 us
+    // (CTAs of 256 threads: 16.9 / 26.5 / 37.7), 40 x 8 of 64 / 512 7.9 / 21.6 (10.6 / 22.5);
+    // 80 x 8 of 1024 alone are slower, 56.5 (52.6).
+    const int T = static_cast<long long>(B) * KV > 304 && o.max_blocks <= 4096 ? 128 : 256;
     // CTAs per segment: as many as have a step of blocks each, up to a cluster of 16,
     // while the SMs hold them all at once (one each, or two in clusters up to 8).  One
     // CTA / clusters: 8 x 2048 blocks 25 / 9.5 us, 64 x 4096 47 / 25, 128 x 1024 12.9 / 11.8
-    constexpr int T = 256;
     constexpr size_t kRoom = 223 * 1024;  // (227 KB with the kernel's own arrays)
     int C = 16;
     while (C > 1 && (static_cast<long long>(B) * KV * C > (C == 16 ? 152 : 304) || T / 2 * (C / 2) >= o.max_blocks))
@@ -488,6 +493,6 @@ extern "C" int pa_q8_select(const void* q, const int8_t* bounds, const float* k_
     const size_t rows = p.R < p.chunk ? static_cast<size_t>(p.R + 7) & ~static_cast<size_t>(7) : p.chunk;
     const size_t smem = keys + scores(C) + ring + rows * 4 * D;
     void* args[] = {&p};
-    return q8_launch(D == 64 ? select_kernel<64>(C) : select_kernel<128>(C), dim3(C, B * KV), T, smem,
+    return q8_launch(D == 64 ? select_kernel<64>(C, T) : select_kernel<128>(C, T), dim3(C, B * KV), T, smem,
                      static_cast<cudaStream_t>(stream), args, C);
 }

@@ -668,6 +668,29 @@ def test_selection_of_long_sequences(pa):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,KV,D,G,NQ,maxb", [(60, 8, 128, 2, 1, 30), (310, 1, 64, 3, 2, 65), (40, 8, 128, 40, 4, 20), (306, 1, 128, 1, 1, 4096), (306, 1, 64, 2, 1, 4097)])
+def test_selection_of_many_sequences(pa, B, KV, D, G, NQ, maxb):
+    """More sequences and heads than two CTAs an SM; short and long ones, some empty."""
+    rng = np.random.default_rng(B + D)
+    lens = rng.integers(0, min(maxb, 60) * 8, B)
+    lens[:3] = 0, 1, maxb * 8
+    pool = 500
+    c = Cache(32, [8], KV, D, 8)
+    c.bounds = np.sort(rng.integers(-127, 128, (pool, KV, 2, D)).astype(np.int8), 2)
+    c.ks = rng.random((pool, KV)).astype(np.float32)
+    c.table, c.lens = rng.integers(0, pool, (B, maxb)).astype(np.int32), lens.astype(np.int32)
+    q = rows_of(rng, "f16", B, KV * G, NQ, D)
+    st = ints([0])
+    sel, cnt = pa.select_blocks_q8(q.cuda(), torch.from_numpy(c.bounds).cuda(), torch.from_numpy(c.ks).cuda(), ints(c.table), ints(c.lens),
+                                   BLOCK=8, budget=7, keep_first=1, keep_last=2, status=st)
+    torch.cuda.synchronize()
+    ws, wc = c.select(q.float().numpy(), 7, 1, 2)
+    np.testing.assert_array_equal(sel.cpu().numpy(), ws)
+    np.testing.assert_array_equal(cnt.cpu().numpy(), wc)
+    assert int(st) == 0
+
+
+@pytest.mark.gpu
 def test_selection_of_equal_scores(pa):
     """Ties: the lowest blocks; all scores zero, all but a few equal, scales that are no numbers."""
     c = Cache(18, [1000, 990], 2, 64, 16)
