@@ -162,9 +162,10 @@ int pa_q8_select(const void *q, const int8_t *bounds, const float *k_scale,
  * no other row does.
  *
  * workspace: device, 256-byte aligned, pa_q8_workspace_bytes(); its first
- * pa_q8_workspace_zero_bytes() bytes zero before the first use, and every
- * call that completes leaves them zero.  Calls that may overlap on the GPU
- * need workspaces of their own.  Limits: NQ <= PA_MAX_NQ, H / KV * NQ <= 1024;
+ * pa_q8_workspace_zero_bytes() bytes (the same for all sizes) zero before the
+ * first use, and every call that completes leaves them zero: calls of any
+ * sizes that it is large enough for may use it one after another.  Calls that
+ * may overlap on the GPU need workspaces of their own.  Limits: NQ <= PA_MAX_NQ, H / KV * NQ <= 1024;
  * with `selected` B * KV <= 4096; B * KV * ceil(H / KV * NQ / 8) * (capacity / 32
  * + 64) < 2^31 (PA_ERR_BAD_DIMS), capacity being max_blocks, or budget, * BLOCK.
  */

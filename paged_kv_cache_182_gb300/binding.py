@@ -1593,8 +1593,8 @@ class Q8Plan:
     them) against all cached keys, with ``causal`` up to the row's own, or, with
     ``selected`` [B, KV, budget] and ``counts`` [B, KV], against those of the
     selected blocks.  ``run()`` returns out, like q.  A workspace of one's own
-    (uint8, ``q8_workspace_bytes``, zeroed) may be shared by plans whose calls
-    do not overlap on the GPU."""
+    (uint8, ``q8_workspace_bytes``, zeroed) may be shared by plans of any sizes
+    that it is large enough for, as long as their calls do not overlap on the GPU."""
 
     def __init__(self, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, *, scale: float,
                  causal: bool = False, selected=None, counts=None, out=None, workspace=None, status=None):

@@ -57,6 +57,7 @@ namespace {
 constexpr int kTile = 32;                 // tokens of a tile: two MMA groups of 16
 constexpr int kMaxEntries = 4096;         // prefix sums in shared memory
 constexpr int kRecordRows = 304 * 32;     // query rows of all CTAs, at most
+constexpr int kMaxCtas = kRecordRows / 8; // CTAs, at most (passes have 8 query rows or more)
 constexpr int kChargeBytes = 32 << 13;    // a piece's start and end count for so many bytes of tiles on an SM
 constexpr int kJoinBytes = 22 << 13;      // joining the pieces of a segment, besides (of 4, 11, 16 and 30 none is better)
 constexpr int kMeta = 64;                 // bytes of a tile's scales and places
@@ -73,7 +74,7 @@ struct DecodeParams {
     void* out;
     const int32_t* selected;
     const int32_t* counts;
-    int* counters;     // [segments] pieces done
+    int* counters;     // [CTA] pieces done of the cut segment whose first piece the CTA has
     float2* part_ml;   // [CTA][2][8 NT] maximum, sum
     float* part_o;     // [CTA][2][8 NT][D]
     int* status;
@@ -546,7 +547,8 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
         const int rows_left = p.R - row_base;
         if (have && !whole && tid == 0) {
             const int c0 = piece > 0 ? first_team : owner_of(s_begin), count = piece > 0 ? own_pieces : owner_of(s_end - 1) - c0 + 1;
-            sm_open[open] = {c0, count, p.counters + (static_cast<int64_t>(b) * p.KV + kh) * p.groups + grp, out0, rows_left};
+            // (of the segments that begin in a CTA, one at most goes on in the next)
+            sm_open[open] = {c0, count, p.counters + (c0 << p.lg_team) + member, out0, rows_left};
         }
         if (have)
             u = solo ? u + solo_step : stop;
@@ -1248,21 +1250,13 @@ int decode_sizes(int B, int H, int KV, int NQ)
     return PA_OK;
 }
 
-struct Workspace {
-    size_t zero, ml, o, total;
-};
+// The counters lie at the same place whatever the sizes, the records behind them: a
+// workspace may serve calls of unlike sizes in turn, and no record of one is where
+// another has its counters.
+constexpr size_t kZeroBytes = (kMaxCtas * sizeof(int) + 255) / 256 * 256;
+constexpr size_t kMlBytes = static_cast<size_t>(kRecordRows) * 2 * sizeof(float2);
 
-Workspace workspace_of(int B, int H, int KV, int D, int NQ)
-{
-    const size_t R = static_cast<size_t>(H / KV) * NQ;
-    const size_t groups = (R + 7) / 8;  // at most: passes of 8 rows
-    Workspace w;
-    w.zero = (static_cast<size_t>(B) * KV * groups * 4 + 255) / 256 * 256;
-    w.ml = static_cast<size_t>(kRecordRows) * 2 * 8;
-    w.o = static_cast<size_t>(kRecordRows) * 2 * D * 4;
-    w.total = w.zero + w.ml + w.o;
-    return w;
-}
+size_t workspace_bytes(int D) { return kZeroBytes + kMlBytes + static_cast<size_t>(kRecordRows) * 2 * D * sizeof(float); }
 
 }  // namespace
 }  // namespace pa
@@ -1273,14 +1267,14 @@ extern "C" size_t pa_q8_workspace_bytes(int B, int H, int KV, int D, int NQ)
 {
     if (B < 1 || decode_sizes(B, H, KV, NQ) != PA_OK || (D != 64 && D != 128))
         return 0;
-    return workspace_of(B, H, KV, D, NQ).total;
+    return workspace_bytes(D);
 }
 
 extern "C" size_t pa_q8_workspace_zero_bytes(int B, int H, int KV, int D, int NQ)
 {
     if (B < 1 || decode_sizes(B, H, KV, NQ) != PA_OK || (D != 64 && D != 128))
         return 0;
-    return workspace_of(B, H, KV, D, NQ).zero;
+    return kZeroBytes;
 }
 
 extern "C" int pa_q8_decode(const void* q, const int8_t* k_cache, const int8_t* v_cache, const float* k_scale, const float* v_scale,
@@ -1309,13 +1303,13 @@ extern "C" int pa_q8_decode(const void* q, const int8_t* k_cache, const int8_t* 
         !q8_a4(block_table) || !q8_a4(seq_lens) || !q8_a4(o.selected) || !q8_a4(o.counts) || !q8_a4(o.status))
         return PA_ERR_ALIGNMENT;
     const int R = H / KV * NQ;
-    const Workspace ws = workspace_of(B, H, KV, D, NQ);
-    if (!o.workspace || o.workspace_bytes < ws.total || (reinterpret_cast<uintptr_t>(o.workspace) & 255))
+    const size_t need = workspace_bytes(D);
+    if (!o.workspace || o.workspace_bytes < need || (reinterpret_cast<uintptr_t>(o.workspace) & 255))
         return PA_ERR_WORKSPACE;
     const size_t blocks = static_cast<size_t>(o.num_blocks) * KV, pool = blocks * BLOCK * D, b4 = static_cast<size_t>(B) * 4;
     const size_t rows = static_cast<size_t>(B) * H * NQ * D * (o.dtype == PA_F32 ? 4 : 2);
     const Q8Range r[] = {{out, rows, true},
-                         {o.workspace, ws.total, true},
+                         {o.workspace, need, true},
                          {o.status, 4, true},
                          {q, rows, false},
                          {k_cache, pool, false},
@@ -1354,8 +1348,8 @@ extern "C" int pa_q8_decode(const void* q, const int8_t* k_cache, const int8_t* 
     p.counts = o.counts;
     unsigned char* w = static_cast<unsigned char*>(o.workspace);
     p.counters = reinterpret_cast<int*>(w);
-    p.part_ml = reinterpret_cast<float2*>(w + ws.zero);
-    p.part_o = reinterpret_cast<float*>(w + ws.zero + ws.ml);
+    p.part_ml = reinterpret_cast<float2*>(w + kZeroBytes);
+    p.part_o = reinterpret_cast<float*>(w + kZeroBytes + kMlBytes);
     p.status = o.status;
     p.scale = scale * kLog2e;
     p.B = B;
