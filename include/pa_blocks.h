@@ -28,6 +28,14 @@
  *                     pa_rotary and pa_cache_append
  *   positions[b][j]   t, or starts[b] + j with starts (the place in the text,
  *                     after an eviction), for the same rows; -1 for the others
+ *   kept[b]           tokens before the new rows: keep, or n when refused
+ *   granted[b]        new rows that have their blocks: add, or 0 when refused
+ *                     (kept + granted = new_lens)
+ *
+ * A store that takes lengths and counts instead of slots (pa_q8_append) is given
+ * kept and granted, never keep and add: those of a refused sequence, or of one
+ * whose values were clamped, name rows that are not its own (the table's entries
+ * behind its blocks may be of blocks that others have by now).
  *
  * block_table and free_blocks are changed in place: the tables' entries behind
  * need stay as they were, and so do the stack's behind new_free_count but for
@@ -37,7 +45,7 @@
  * share must not be given back.
  *
  * Layouts (row-major, device memory, int32): block_table [B][max_blocks];
- * seq_lens, keep, add, starts, new_lens [B]; free_blocks [num_blocks];
+ * seq_lens, keep, add, starts, new_lens, kept, granted [B]; free_blocks [num_blocks];
  * free_count, new_free_count [1]; slots, positions [B][N].
  *
  * Conditions that only the device sees are OR-ed into *opts->status:
@@ -79,6 +87,8 @@ typedef struct pa_blocks_opts {
     const int32_t *starts;  /* [B], or NULL: positions count the cache */
     int32_t *positions;     /* [B][N], or NULL */
     int *status;            /* device int32 for PA_STATUS_* bits, or NULL */
+    int32_t *kept;          /* [B], or NULL */
+    int32_t *granted;       /* [B], or NULL */
 } pa_blocks_opts;
 
 int pa_plan_blocks(int32_t *block_table, const int32_t *seq_lens, int32_t *free_blocks,

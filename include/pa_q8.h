@@ -69,7 +69,9 @@ extern "C" {
  * A value is off by at most half its block's scale at the time it is stored,
  * and by half of each larger scale that the block gets later.  Rows of the
  * block behind the new ones are left as they were.  Only the sequence's own
- * blocks may be written: a block that two sequences share must be full.
+ * blocks may be written: a block that two sequences share must be full, and the
+ * table has to hold the sequence's own block for every new row or an entry outside
+ * the pool (behind pa_plan_blocks: seq_lens and counts are its kept and granted).
  *
  * k_new, v_new [B][KV][N][D] of dtype with strides {batch, head, row} in
  * elements; columns contiguous.  N at most PA_MAX_PREFILL.  The outputs

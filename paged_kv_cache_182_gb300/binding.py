@@ -135,6 +135,8 @@ class BlocksOpts(ctypes.Structure):
         ("starts", ctypes.c_void_p),
         ("positions", ctypes.c_void_p),
         ("status", ctypes.c_void_p),
+        ("kept", ctypes.c_void_p),
+        ("granted", ctypes.c_void_p),
     ]
 
 
@@ -1352,11 +1354,14 @@ class BlockPlan:
     them, -1 behind a sequence's new rows, and the rows' positions in the cache,
     or counted from ``starts`` (the text, after an eviction).  A sequence that
     the free blocks do not suffice for keeps its length and gets no slots
-    (``PA_STATUS_NO_BLOCKS``)."""
+    (``PA_STATUS_NO_BLOCKS``).  ``kept`` and ``granted`` (int32 [B]) are, after a
+    run, the tokens before each sequence's new rows and the new rows that have
+    their blocks, none of a sequence that was refused: what ``cache_append_q8``
+    takes as ``seq_lens`` and ``counts``."""
 
     def __init__(self, block_table, seq_lens, free_blocks, free_count, *, BLOCK: int, width: int, add=None,
                  keep=None, starts=None, new_lens=None, new_free_count=None, slots=None, positions=None,
-                 status=None):
+                 status=None, kept=None, granted=None):
         if block_table.dim() != 2 or block_table.dtype != torch.int32:
             raise ValueError("block_table must be int32 [B, max_blocks]")
         B, maxb = (int(x) for x in block_table.shape)
@@ -1373,12 +1378,16 @@ class BlockPlan:
         self.new_free_count = _made(new_free_count, (1,), torch.int32, dev, "new_free_count")
         self.slots = _made(slots, (B, width), torch.int32, dev, "slots")
         self.positions = _made(positions, (B, width), torch.int32, dev, "positions")
+        self.kept = _made(kept, (B,), torch.int32, dev, "kept")
+        self.granted = _made(granted, (B,), torch.int32, dev, "granted")
         _same_device(dev, block_table=block_table, seq_lens=seq_lens, free_blocks=free_blocks,
                      free_count=free_count, add=add, keep=keep, starts=starts, new_lens=self.new_lens,
-                     new_free_count=self.new_free_count, slots=self.slots, positions=self.positions)
+                     new_free_count=self.new_free_count, slots=self.slots, positions=self.positions,
+                     kept=self.kept, granted=self.granted)
         self.opts = BlocksOpts(
             max_blocks=maxb, num_blocks=int(free_blocks.shape[0]), add=_dev_ptr(add), keep=_dev_ptr(keep),
-            starts=_dev_ptr(starts), positions=_dev_ptr(self.positions), status=_status_ptr(status, dev))
+            starts=_dev_ptr(starts), positions=_dev_ptr(self.positions), status=_status_ptr(status, dev),
+            kept=_dev_ptr(self.kept), granted=_dev_ptr(self.granted))
         self.device = dev
         self._keep = (block_table, seq_lens, free_blocks, free_count, add, keep, starts, status)
         self._args = _ready((_ptr(block_table), _ptr(seq_lens), _ptr(free_blocks), _ptr(free_count),
@@ -1392,11 +1401,13 @@ class BlockPlan:
 
 
 def plan_blocks(block_table, seq_lens, free_blocks, free_count, *, BLOCK: int, width: int, add=None,
-                keep=None, starts=None, status=None, stream=None):
-    """Block tables and slots of a step (pa_plan_blocks): see ``BlockPlan``."""
+                keep=None, starts=None, status=None, kept=None, granted=None, stream=None):
+    """Block tables and slots of a step (pa_plan_blocks): see ``BlockPlan``; ``kept`` and
+    ``granted``, where given, are filled besides."""
     plan = BlockPlan(block_table, seq_lens, free_blocks, free_count, BLOCK=BLOCK, width=width, add=add,
-                     keep=keep, starts=starts, status=status)
-    return _run_once(plan, stream, plan.new_lens, plan.new_free_count, plan.slots, plan.positions)
+                     keep=keep, starts=starts, status=status, kept=kept, granted=granted)
+    return _run_once(plan, stream, plan.new_lens, plan.new_free_count, plan.slots, plan.positions, plan.kept,
+                     plan.granted)
 
 
 # ------------------------------------------------------------------- cache in 8 bits
@@ -1431,7 +1442,9 @@ class Q8AppendPlan:
     (int8 [num_blocks, BLOCK, KV, D]), with ``k_scale`` / ``v_scale`` (float32
     [num_blocks, KV]) and, if given, ``bounds`` (int8 [num_blocks, KV, 2, D],
     the lowest and highest code of each channel).  A block whose scale grows has
-    its earlier codes rounded again.  ``run()`` returns (k_cache, v_cache,
+    its earlier codes rounded again.  Behind a ``BlockPlan``, ``seq_lens`` and
+    ``counts`` are its ``kept`` and ``granted``: what a refused sequence asked for
+    must not be stored.  ``run()`` returns (k_cache, v_cache,
     k_scale, v_scale)."""
 
     def __init__(self, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, *,

@@ -40,6 +40,8 @@ struct PlanParams {
     int32_t* new_count;
     int32_t* slots;
     int32_t* positions;
+    int32_t* kept;
+    int32_t* granted;
     const int32_t* add;
     const int32_t* keep;
     const int32_t* starts;
@@ -155,8 +157,13 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(const __grid_cons
             granted_more = more;
         if (!ok)
             bad |= fits ? PA_STATUS_NO_BLOCKS : PA_STATUS_BAD_LENGTH;
-        if (lead)
+        if (lead) {
             p.new_lens[b] = ok ? s.keep + s.add : s.n;
+            if (p.kept)
+                p.kept[b] = ok ? s.keep : s.n;
+            if (p.granted)
+                p.granted[b] = ok ? s.add : 0;
+        }
     }
     // blocks taken in all: the largest sum that was granted
     granted_more = __reduce_max_sync(kFullWarp, granted_more);
@@ -251,7 +258,7 @@ extern "C" int pa_plan_blocks(int32_t* block_table, const int32_t* seq_lens, int
         (B > 0 && (!block_table || !seq_lens || !new_lens || (N > 0 && !slots))))
         return PA_ERR_NULL_POINTER;
     const void* all4[] = {block_table, seq_lens, free_blocks, free_count, new_lens, new_free_count, slots,
-                          o.add,       o.keep,   o.starts,    o.positions, o.status};
+                          o.add,       o.keep,   o.starts,    o.positions, o.status, o.kept,         o.granted};
     for (const void* x : all4)
         if (!q8_a4(x))
             return PA_ERR_ALIGNMENT;
@@ -261,8 +268,9 @@ extern "C" int pa_plan_blocks(int32_t* block_table, const int32_t* seq_lens, int
                          {slots, b4 * N, true},                  {o.positions, b4 * N, true},
                          {seq_lens, b4, false},                  {free_count, 4, false},
                          {o.add, b4, false},                     {o.keep, b4, false},
-                         {o.starts, b4, false},                  {o.status, 4, true}};
-    if (q8_overlap(r, 12))
+                         {o.starts, b4, false},                  {o.status, 4, true},
+                         {o.kept, b4, true},                     {o.granted, b4, true}};
+    if (q8_overlap(r, 14))
         return PA_ERR_BAD_DIMS;
     PlanParams p{};
     p.table = block_table;
@@ -273,6 +281,8 @@ extern "C" int pa_plan_blocks(int32_t* block_table, const int32_t* seq_lens, int
     p.new_count = new_free_count;
     p.slots = slots;
     p.positions = N > 0 ? o.positions : nullptr;
+    p.kept = o.kept;
+    p.granted = o.granted;
     p.add = o.add;
     p.keep = o.keep;
     p.starts = o.starts;
