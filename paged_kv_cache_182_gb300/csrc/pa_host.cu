@@ -354,6 +354,33 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 void count_launches(uint64_t n) { g_launches.fetch_add(n); }
 
+bool allow_shared_memory(const void* fn)
+{
+    struct Done {
+        const void* fn;
+        int device;
+    };
+    constexpr int kDone = 256;  // (more are set again at each call)
+    static std::mutex mutex;
+    static Done done[kDone];
+    static int count = 0;
+    int dev = 0, most = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return false;
+    std::lock_guard<std::mutex> lock(mutex);
+    for (int i = 0; i < count; ++i)
+        if (done[i].fn == fn && done[i].device == dev)
+            return true;
+    cudaFuncAttributes attr{};
+    if (device_smem_optin(&most) != PA_OK || cudaFuncGetAttributes(&attr, fn) != cudaSuccess ||
+        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most - static_cast<int>(attr.sharedSizeBytes)) !=
+            cudaSuccess)
+        return false;
+    if (count < kDone)
+        done[count++] = {fn, dev};
+    return true;
+}
+
 }  // namespace pa
 
 using namespace pa;

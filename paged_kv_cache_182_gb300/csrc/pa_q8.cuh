@@ -209,8 +209,7 @@ inline int q8_sizes(int B, int KV, int D, int BLOCK, int max_blocks, int num_blo
 // the kernel waits for that one before it reads anything (grid_begin).
 inline int q8_launch(const void* fn, dim3 grid, int threads, size_t smem, cudaStream_t st, void** args, int cluster = 1)
 {
-    if (smem > 40 * 1024 &&  // (48 KB with what a kernel has statically)
-        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    if (smem > 40 * 1024 && !allow_shared_memory(fn))  // (48 KB with what a kernel has statically)
         return PA_ERR_CUDA;
     if (cluster > 8 && cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return PA_ERR_CUDA;

@@ -106,4 +106,9 @@ bool vjp_tc_splits(int B, int HQ, int HK, int SK, int sms);
 // Adds to the library's count of kernel launches (pa_kernel_launches).
 void count_launches(uint64_t n);
 
+// Lets `fn` have as much dynamic shared memory on the current device as a block may
+// opt in to: the same limit whatever a call needs, so that no call of another host
+// thread lowers it between this one and its launch.
+bool allow_shared_memory(const void* fn);
+
 }  // namespace pa
