@@ -673,8 +673,7 @@ extern "C" int pa_cache_evict(void* k_cache, void* v_cache, const int32_t* block
         move = reinterpret_cast<const void*>(pa_evict_gather);
         smem = static_cast<size_t>(p.rows_item) * rb;
     }
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(move, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    if (smem > 48 * 1024 && !allow_shared_memory(move))
         return PA_ERR_CUDA;
     if (cudaLaunchKernelExC(&cfg, sel, args) != cudaSuccess)
         return PA_ERR_CUDA;

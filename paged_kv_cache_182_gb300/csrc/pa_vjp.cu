@@ -379,9 +379,7 @@ int launch_simt(const VjpParamsOf<kMod>& p, cudaStream_t st, uint64_t* launches)
     if (p.SQ > 0) {
         const size_t smem = (kStatRows * p.D + kStatKeys * (p.D + 1)) * sizeof(float);
         auto fn = vjp_stats_simt<T, kMod>;
-        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-            cudaSuccess)
+        if (!allow_shared_memory(reinterpret_cast<const void*>(fn)))
             return PA_ERR_CUDA;
         const dim3 grid((p.SQ + kStatRows - 1) / kStatRows, p.HQ, p.B);
         fn<<<grid, 256, smem, st>>>(p);
@@ -394,9 +392,7 @@ int launch_simt(const VjpParamsOf<kMod>& p, cudaStream_t st, uint64_t* launches)
                              2 * kMainKeys * 17 + 2 * kMainRows) *
                             sizeof(float);
         auto fn = vjp_main_simt<T, TO, kMod>;
-        if (cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-            cudaSuccess)
+        if (!allow_shared_memory(reinterpret_cast<const void*>(fn)))
             return PA_ERR_CUDA;
         const dim3 grid((p.SK + kMainKeys - 1) / kMainKeys, p.HK, p.B);
         fn<<<grid, 256, smem, st>>>(p);

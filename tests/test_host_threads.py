@@ -34,7 +34,21 @@ def _blocks(pa, B, seed):
     return pa.BlockPlan(ints(np.arange(2 * B).reshape(B, 2)), ints([16] * B), ints(np.arange(2 * B)), ints([0]), BLOCK=16, width=1)
 
 
-@pytest.mark.parametrize("make,sizes", [(_decode, (3, 70)), (_select, (2500, 20000)), (_blocks, (2200, 4096))])
+def _gradient(pa, D, seed):
+    g = torch.Generator("cuda").manual_seed(seed)
+    q, k, v, y, go = (torch.randn(1, 2, 40, D, generator=g, device="cuda") for _ in range(5))
+    return pa.VjpPlan(q, k, v, y, go, scale=0.1, causal=True)
+
+
+def _evict(pa, D, seed):
+    g = torch.Generator("cuda").manual_seed(seed)
+    kc, vc = (torch.randn(8, 16, 100, D, generator=g, device="cuda") for _ in range(2))
+    return pa.EvictPlan(kc, vc, ints([[0, 1, 2]]), ints([40]), torch.rand(1, 48, generator=g, device="cuda"), budget=20,
+                        dst_table=ints([[4, 5]]))
+
+
+@pytest.mark.parametrize("make,sizes", [(_decode, (3, 70)), (_select, (2500, 20000)), (_blocks, (2200, 4096)),
+                                        (_gradient, (64, 256)), (_evict, (128, 160))])
 def test_two_host_threads_at_once(pa, make, sizes):
     """Calls of one kernel that need unlike amounts of shared memory, each on a stream of its own."""
     plans = [make(pa, n, i) for i, n in enumerate(sizes)]
