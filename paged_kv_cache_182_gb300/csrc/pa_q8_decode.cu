@@ -504,7 +504,10 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
         kh = p.selected ? e - b * p.KV : p.groups == 1 ? c : c / p.groups;
         grp = p.selected ? c : p.groups == 1 ? 0 : c - kh * p.groups;
         row_base = grp * kRows;
-        n = min(max(__ldg(p.lens + b), 0), p.cap);
+        const int length = __ldg(p.lens + b);
+        n = min(max(length, 0), p.cap);
+        if (p.selected && length != n)  // (without lists the prefix sums have told)
+            q8_report(p.status, PA_STATUS_BAD_LENGTH);
         sel = p.selected ? p.selected + static_cast<int64_t>(e) * p.budget : nullptr;
         tokens = p.selected ? min(max(__ldg(p.counts + e), 0), p.budget) << p.shift : n;  // places in the list of blocks
         nb = (n + (1 << p.shift) - 1) >> p.shift;
