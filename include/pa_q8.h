@@ -159,8 +159,9 @@ int pa_q8_select(const void *q, const int8_t *bounds, const float *k_scale,
  * products; 16-bit queries enter them with their own digits and weights with
  * 11 bits; float32 queries and weights with 22.  out is of q's dtype.
  *
- * Scales have to be finite and key scales below 2^114; one below 2^-96 (0 among
- * them) counts as 2^-96.  A query row with an infinity or a NaN gives NaN, and
+ * Scales have to be finite, key scales below 2^114 and value scales at most 2^96;
+ * one below 2^-96 (0 among them) counts as 2^-96.  Value scales may lie as far
+ * apart as that: a key's share in the softmax does not depend on its value's.  A query row with an infinity or a NaN gives NaN, and
  * no other row does.
  *
  * workspace: device, 256-byte aligned, pa_q8_workspace_bytes(); its first

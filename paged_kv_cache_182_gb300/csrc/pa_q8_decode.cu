@@ -43,7 +43,11 @@
 // exponent, t = s + log2(v_scale), so that weights times value scale come out of
 // the exponential; the softmax's sum takes them back through 1 / v_scale.  The
 // maximum subtracted is t's: fp16 weights are as exact as their share in the
-// output.  It is raised only when a score passes it by 2^8 (a vote instead of a
+// output.  Where value scales lie far from one, 2^(t - m) may be 0 in float32 for a
+// key whose share in the sum, 2^(s - m), is not small beside the others': from the
+// first scale beyond 2^+-32 on, a warp sums the latter by themselves (a second
+// exponential per weight), and sums are scaled in two steps where 2^d alone is 0
+// (scaled_sum).  Up to 2^96 no weight above 2^-36 of the row's largest is lost.  It is raised only when a score passes it by 2^8 (a vote instead of a
 // reduction per tile; weights stay below 2^14).
 #include <cuda_runtime.h>
 
@@ -62,6 +66,8 @@ constexpr int kChargeBytes = 32 << 13;    // a piece's start and end count for s
 constexpr int kJoinBytes = 22 << 13;      // joining the pieces of a segment, besides (of 4, 11, 16 and 30 none is better)
 constexpr int kMeta = 64;                 // bytes of a tile's scales and places
 constexpr float kLift = 6.f, kSlack = 8.f;  // weights are 2^(t - m + 6), t - m <= 8
+constexpr float kNear = 32.f;             // log2 of value scales that share a weight's exponential with the sum
+constexpr int kNowhere = INT_MAX - 64;    // place of a part of a tile that has no block
 
 struct DecodeParams {
     const void* q;
@@ -112,6 +118,15 @@ __device__ __forceinline__ float fast_log2(float x)
 {
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// l 2^d (d <= 0), also where 2^d by itself would be 0.
+__device__ __forceinline__ float scaled_sum(float l, float d)
+{
+    float y = l * fast_exp2(fmaxf(d, -120.f));
+    if (d < -120.f)
+        y = (l > 3.402823466e38f ? 3.402823466e38f : l) * fast_exp2(-120.f) * fast_exp2(d + 120.f);
     return y;
 }
 
@@ -440,7 +455,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
             q8_report(p.status, PA_STATUS_BAD_BLOCK);
         // (without a block: the first rows of the pool are read in its place, and hidden)
         w_row = there ? (static_cast<uint32_t>(phys_next) << p.shift) + in_block : 0u;
-        w_place = there ? (blk_next << p.shift) + in_block : INT_MAX - 64;
+        w_place = there ? (blk_next << p.shift) + in_block : kNowhere;
     };
     auto issue = [&](int k, uint32_t st) {  // the warp's k-th tile
         if (first + k * stride < last) {
@@ -661,7 +676,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                     m = fmaxf(m, sm_m[w][row]);
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w)
-                    sum = fmaf(sm_l[w][row], sm_m[w][row] == -INFINITY ? 0.f : fast_exp2(sm_m[w][row] - m), sum);
+                    sum += scaled_sum(sm_l[w][row], sm_m[w][row] - m);
                 if (whole) {
                     const float r = sum == 0.f ? 0.f : 1.f / sum;
                     store_out(p, out0 + static_cast<int64_t>(x) * 4, make_float4(val[k].x * r, val[k].y * r, val[k].z * r, val[k].w * r));
@@ -781,6 +796,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
 
         uint32_t st = ring, fill = ring + (S - 1) * kStage;
         int ahead = S - 1;
+        bool apart = false;  // a value scale far from one has been met
         for (int tile = first; tile < last; tile += stride) {
             asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");  // this tile's
             __syncwarp();  // the copies of the other lanes; the stage filled next has been read
@@ -797,6 +813,12 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                     lv[x] = fast_log2(vs);
                     iv[x] = fast_rcp(vs);
                     place[x] = static_cast<int>(lds4(st + kTileBytes + 32 + x * 4));
+                    apart |= fabsf(lv[x]) > kNear && place[x] < kNowhere;
+                }
+                if (apart) {
+#pragma unroll
+                    for (int x = 0; x < HB; ++x)
+                        iv[x] = 0.f;
                 }
                 // ---- S = Q K^T, eight tokens at a time
                 float s[M][4][4];
@@ -875,8 +897,8 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                         high = fmaxf(high + base, mx[k]);
                         const float down = high == -INFINITY ? 1.f : fast_exp2(mx[k] - high);
                         const float less = high == -INFINITY ? 0.f : base - (high - kLift);
+                        l[k] = scaled_sum(l[k], mx[k] - high);
                         mx[k] = high;
-                        l[k] *= down;
 #pragma unroll
                         for (int j = 0; j < kOct; ++j) {
                             o[m * kOct + j][i0] *= down;
@@ -888,6 +910,15 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                             s[m][e][i0 + 1] += less;
                         }
                     }
+                }
+                if (apart) {
+#pragma unroll
+                    for (int m = 0; m < M; ++m)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                l[m * 2 + (i >> 1)] += fast_exp2(s[m][e][i] - lv[HB == 4 ? e : e >> 1]);
                 }
                 // ---- weights, as they are the fragments of P
                 uint32_t pf[2][M][4];
@@ -953,9 +984,17 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                         lv[j][x] = fast_log2(vs);
                         iv[j][x] = fast_rcp(vs);
                         place[j][x] = static_cast<int>(lds4(st + kTileBytes + 32 + part * 4));
+                        apart |= fabsf(lv[j][x]) > kNear && place[j][x] < kNowhere;
                         if constexpr (B2 == 1)
                             place[j][1] = place[j][0] + 8;
                     }
+                if (apart) {
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+#pragma unroll
+                        for (int x = 0; x < B2; ++x)
+                            iv[j][x] = 0.f;
+                }
                 // ---- S^T = K Q^T
                 float sacc[J][NT][4];
 #pragma unroll
@@ -1035,8 +1074,8 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                             m = fmaxf(m, __shfl_xor_sync(kFullWarp, m, 16));
                             m = fmaxf(m, mx[nt * 2 + i]);
                             const float down = m == -INFINITY ? 1.f : fast_exp2(mx[nt * 2 + i] - m);
+                            l[nt * 2 + i] = scaled_sum(l[nt * 2 + i], mx[nt * 2 + i] - m);
                             mx[nt * 2 + i] = m;
-                            l[nt * 2 + i] *= down;
 #pragma unroll
                             for (int s = 0; s < kSteps; ++s) {
                                 o[s * NT + nt][i] *= down;
@@ -1050,6 +1089,13 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                 for (int nt = 0; nt < NT; ++nt) {
                     // (a row that has seen nothing: its scores are -inf, and so is what is left of them)
                     const float base[2] = {fmaxf(mx[nt * 2], -3.402823466e38f) - kLift, fmaxf(mx[nt * 2 + 1], -3.402823466e38f) - kLift};
+                    if (apart) {
+#pragma unroll
+                        for (int j = 0; j < J; ++j)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                l[nt * 2 + (i & 1)] += fast_exp2(sacc[j][nt][i] - base[i & 1] - lv[j][i >> 1 & (B2 - 1)]);
+                    }
 #pragma unroll
                     for (int j = 0; j < J; ++j) {
                         float w[4];
@@ -1177,11 +1223,11 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                     top = fmaxf(top, __shfl_xor_sync(kFullWarp, top, k));
                 top = fmaxf(top, m);
                 const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top), old = m == -INFINITY ? 0.f : fast_exp2(m - top);
-                float part = ml.y * f;
+                float part = scaled_sum(ml.y, ml.x - top);
 #pragma unroll
                 for (int k = 1; k < kQuads; k <<= 1)
                     part += __shfl_xor_sync(kFullWarp, part, k);
-                sum = fmaf(sum, old, part);
+                sum = scaled_sum(sum, m - top) + part;
                 all.x *= old, all.y *= old, all.z *= old, all.w *= old;
                 m = top;
                 for (int i = 0; i < many; i += kBatch) {
