@@ -156,8 +156,9 @@ int pa_q8_select(const void *q, const int8_t *bounds, const float *k_scale,
  * counts twice.
  *
  * Scores, softmax statistics and sums are float32.  Codes are exact in the
- * products; 16-bit queries enter them with their own digits and weights with
- * 11 bits; float32 queries and weights with 22.  out is of q's dtype.
+ * products; 16-bit queries enter them with their own digits, float32 queries
+ * with 22 bits, weights with 22, and with 11 where q is bfloat16 and H / KV * NQ
+ * > 8.  out is of q's dtype.
  *
  * Scales have to be finite, key scales below 2^114 and value scales at most 2^96;
  * one below 2^-96 (0 among them) counts as 2^-96.  Value scales may lie as far

@@ -43,7 +43,12 @@
 // exponent, t = s + log2(v_scale), so that weights times value scale come out of
 // the exponential; the softmax's sum takes them back through 1 / v_scale.  The
 // maximum subtracted is t's: fp16 weights are as exact as their share in the
-// output.  Where value scales lie far from one, 2^(t - m) may be 0 in float32 for a
+// output.  A weight is two fp16 parts, 22 bits, so that fp16 and float32 outputs are
+// off by their own rounding alone (one part: fp16 outputs 2.5e-4 to 2.8e-4 instead of
+// 2.1e-4, and 3 to 5 % less time at eight rows, where memory bounds the call).  Only
+// bfloat16 rows beyond eight a head take one part, 11 bits: their own rounding of 2^-8
+// hides it (1.7e-3 either way), and the second part's products cost 26.4 -> 31.7 us at
+// 32 rows.  Where value scales lie far from one, 2^(t - m) may be 0 in float32 for a
 // key whose share in the sum, 2^(s - m), is not small beside the others': from the
 // first scale beyond 2^+-32 on, a warp sums the latter by themselves (a second
 // exponential per weight), and sums are scaled in two steps where 2^d alone is 0
@@ -130,10 +135,10 @@ __device__ __forceinline__ float scaled_sum(float l, float d)
     return y;
 }
 
-// QP: fp16 parts of a query row and of a weight (2: float32).  HB: blocks a
-// tile may touch (2; 4 where BLOCK is 8).  Query fragments stay in registers, or in
+// QP: fp16 parts of a query row (2: float32).  PW: fp16 parts of a weight.  HB: blocks
+// a tile may touch (2; 4 where BLOCK is 8).  Query fragments stay in registers, or in
 // shared memory where the accumulators of four groups of rows leave no room.
-template <int D, int NT, int QP, int C>
+template <int D, int NT, int QP, int C, int PW>
 struct Shape {
     static constexpr int kRows = 8 * NT, kSteps = D / 16;
     // more than eight rows of 16 bits: rows on the 16-row side of the products
@@ -197,10 +202,10 @@ struct OpenPiece {
 };
 
 // kMany: more segments than CTAs, so that a warp may take whole ones by itself.
-template <int D, int NT, int QP, int HB, int C, bool kMany>
-__global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode_kernel(const __grid_constant__ DecodeParams p)
+template <int D, int NT, int QP, int HB, int C, int PW, bool kMany>
+__global__ void __launch_bounds__(Shape<D, NT, QP, C, PW>::kThreads, C) pa_q8_decode_kernel(const __grid_constant__ DecodeParams p)
 {
-    using Sh = Shape<D, NT, QP, C>;
+    using Sh = Shape<D, NT, QP, C, PW>;
     constexpr int kRows = Sh::kRows, kSteps = Sh::kSteps, kTileBytes = Sh::kTileBytes, kStage = Sh::kStage, S = Sh::kStages;
     constexpr int kWarps = Sh::kWarps, kThreads = Sh::kThreads;
     constexpr int kChunks = D / 64;  // 16-byte runs of a key row per lane
@@ -921,7 +926,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                                 l[m * 2 + (i >> 1)] += fast_exp2(s[m][e][i] - lv[HB == 4 ? e : e >> 1]);
                 }
                 // ---- weights, as they are the fragments of P
-                uint32_t pf[2][M][4];
+                uint32_t pf[2][PW][M][4];
 #pragma unroll
                 for (int m = 0; m < M; ++m)
 #pragma unroll
@@ -933,8 +938,15 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                         const float inv = iv[HB == 4 ? e : e >> 1];
                         l[m * 2] = fmaf(w[0] + w[1], inv, l[m * 2]);
                         l[m * 2 + 1] = fmaf(w[2] + w[3], inv, l[m * 2 + 1]);
-                        pf[e >> 1][m][(e & 1) * 2] = half2_bits(__floats2half2_rn(w[0], w[1]));
-                        pf[e >> 1][m][(e & 1) * 2 + 1] = half2_bits(__floats2half2_rn(w[2], w[3]));
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const __half2 hi = __floats2half2_rn(w[2 * i], w[2 * i + 1]);
+                            pf[e >> 1][0][m][(e & 1) * 2 + i] = half2_bits(hi);
+                            if constexpr (PW == 2) {
+                                const float2 back = __half22float2(hi);
+                                pf[e >> 1][PW - 1][m][(e & 1) * 2 + i] = half2_bits(__floats2half2_rn(w[2 * i] - back.x, w[2 * i + 1] - back.y));
+                            }
+                        }
                     }
                 // ---- O += P V, eight channels at a time
 #pragma unroll
@@ -958,13 +970,19 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                             const uint32_t pick = half ? 0x7362 : 0x5140;
                             const uint32_t lo = __byte_perm(vw[0][w], vw[1][w], pick) ^ 0x80808080u;
                             const uint32_t hi = __byte_perm(vw[2][w], vw[3][w], pick) ^ 0x80808080u;
+                            uint32_t vb[2][2];
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                const uint32_t b0 = codes2(lo, i ? 0x4342 : 0x4140), b1 = codes2(hi, i ? 0x4342 : 0x4140);
-#pragma unroll
-                                for (int m = 0; m < M; ++m)
-                                    mma(o[m * kOct + w * 4 + half * 2 + i], pf[j][m], b0, b1);
+                                vb[i][0] = codes2(lo, i ? 0x4342 : 0x4140);
+                                vb[i][1] = codes2(hi, i ? 0x4342 : 0x4140);
                             }
+#pragma unroll
+                            for (int x = PW - 1; x >= 0; --x)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                                    for (int m = 0; m < M; ++m)
+                                        mma(o[m * kOct + w * 4 + half * 2 + i], pf[j][x][m], vb[i][0], vb[i][1]);
                         }
                 }
             } else {
@@ -1084,7 +1102,8 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                         }
                 }
                 // ---- weights, and as fragments of P^T
-                uint32_t pf[J][QP][NT][2];
+                static_assert(PW == 2);
+                uint32_t pf[J][PW][NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     // (a row that has seen nothing: its scores are -inf, and so is what is left of them)
@@ -1113,10 +1132,8 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                         for (int x = 0; x < 2; ++x) {
                             const __half2 hi = __floats2half2_rn(w[2 * x], w[2 * x + 1]);
                             pf[j][0][nt][x] = movm_trans(half2_bits(hi));
-                            if constexpr (QP == 2) {
-                                const float2 back = __half22float2(hi);
-                                pf[j][QP - 1][nt][x] = movm_trans(half2_bits(__floats2half2_rn(w[2 * x] - back.x, w[2 * x + 1] - back.y)));
-                            }
+                            const float2 back = __half22float2(hi);
+                            pf[j][1][nt][x] = movm_trans(half2_bits(__floats2half2_rn(w[2 * x] - back.x, w[2 * x + 1] - back.y)));
                         }
                     }
                 }
@@ -1143,25 +1160,32 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C>::kThreads, C) pa_q8_decode
                             mixed[x][0] = __byte_perm(vw[2 * x][w], vw[2 * x + 1][w], 0x5140) ^ 0x80808080u;
                             mixed[x][1] = __byte_perm(vw[2 * x][w], vw[2 * x + 1][w], 0x7362) ^ 0x80808080u;
                         }
+                        uint32_t a[2][4];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const uint32_t a[4] = {codes2(mixed[0][i], 0x4140), codes2(mixed[0][i], 0x4342), codes2(mixed[1][i], 0x4140),
-                                                   codes2(mixed[1][i], 0x4342)};
+                            a[i][0] = codes2(mixed[0][i], 0x4140), a[i][1] = codes2(mixed[0][i], 0x4342);
+                            a[i][2] = codes2(mixed[1][i], 0x4140), a[i][3] = codes2(mixed[1][i], 0x4342);
+                        }
+                        if constexpr (QP == 1) {
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                if constexpr (QP == 1) {
-                                    mma(o[(2 * w + i) * NT + nt], a, pf[j][0][nt][0], pf[j][0][nt][1]);
-                                } else {
+                            for (int x = PW - 1; x >= 0; --x)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    mma(o[2 * w + i], a[i], pf[j][x][0][0], pf[j][x][0][1]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
                                     // a group's products by themselves: added to the sums by rounded
                                     // additions (the tensor core's own cut off what does not fit)
                                     float d[4] = {0.f, 0.f, 0.f, 0.f};
-                                    mma(d, a, pf[j][QP - 1][nt][0], pf[j][QP - 1][nt][1]);
-                                    mma(d, a, pf[j][0][nt][0], pf[j][0][nt][1]);
+                                    mma(d, a[i], pf[j][1][nt][0], pf[j][1][nt][1]);
+                                    mma(d, a[i], pf[j][0][nt][0], pf[j][0][nt][1]);
 #pragma unroll
                                     for (int y = 0; y < 4; ++y)
                                         o[(2 * w + i) * NT + nt][y] += d[y];
                                 }
-                            }
                         }
                     }
                 }
@@ -1252,17 +1276,17 @@ struct Variant {
     const void* many;  // for more segments than CTAs
 };
 
-template <int D, int NT, int QP, int C>
+template <int D, int NT, int QP, int C, int PW = 2>
 Variant variant(int BLOCK)
 {
-    using Sh = Shape<D, NT, QP, C>;
+    using Sh = Shape<D, NT, QP, C, PW>;
     static_assert(C > 1 || Sh::kRing + Sh::kQueryBytes + Sh::kGroup * Sh::kState + (kMaxEntries + 1) * 4 + 4096 <= 227 * 1024, "with the arrays of its own");
     constexpr bool kMany = NT == 1;
-    return {BLOCK == 8 ? reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 4, C, false>)
-                       : reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 2, C, false>),
+    return {BLOCK == 8 ? reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 4, C, PW, false>)
+                       : reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 2, C, PW, false>),
             Sh::kRows, Sh::kThreads, C, Sh::kCharge, static_cast<size_t>(Sh::kRing) + Sh::kQueryBytes + Sh::kGroup * Sh::kState,
-            BLOCK == 8 ? reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 4, C, kMany>)
-                       : reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 2, C, kMany>)};
+            BLOCK == 8 ? reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 4, C, PW, kMany>)
+                       : reinterpret_cast<const void*>(pa_q8_decode_kernel<D, NT, QP, 2, C, PW, kMany>)};
 }
 
 // `segments`: of 8 query rows.  One CTA of 12 warps per SM streams a segment twice as
@@ -1280,6 +1304,8 @@ Variant variant(int BLOCK, int dtype, int R, long long segments, int sms, int en
 {
     if (dtype == PA_F32)
         return R > 8 ? variant<D, 2, 2, 1>(BLOCK) : variant<D, 1, 2, 1>(BLOCK);
+    if (R > 8 && dtype == PA_BF16)  // (weights of one part: see above)
+        return R > 16 ? variant<D, 4, 1, 1, 1>(BLOCK) : variant<D, 2, 1, 1, 1>(BLOCK);
     if (R > 8)
         return R > 16 ? variant<D, 4, 1, 1>(BLOCK) : variant<D, 2, 1, 1>(BLOCK);
     const size_t sums = 4 * static_cast<size_t>(entries);
