@@ -1006,7 +1006,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C, PW>::kThreads, C) pa_q8_de
                         if constexpr (B2 == 1)
                             place[j][1] = place[j][0] + 8;
                     }
-                if (apart) {
+                if (__builtin_expect(apart, 0)) {  // (out of the way: float32, 16 rows 28.9 -> 27.4 us; the other form is no faster so)
 #pragma unroll
                     for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -1108,7 +1108,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C, PW>::kThreads, C) pa_q8_de
                 for (int nt = 0; nt < NT; ++nt) {
                     // (a row that has seen nothing: its scores are -inf, and so is what is left of them)
                     const float base[2] = {fmaxf(mx[nt * 2], -3.402823466e38f) - kLift, fmaxf(mx[nt * 2 + 1], -3.402823466e38f) - kLift};
-                    if (apart) {
+                    if (__builtin_expect(apart, 0)) {
 #pragma unroll
                         for (int j = 0; j < J; ++j)
 #pragma unroll

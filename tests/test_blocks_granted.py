@@ -61,6 +61,18 @@ def test_kept_and_granted(pa, spare):
 
 
 @pytest.mark.gpu
+def test_refused_tensors(pa):
+    x = state(3, [16, 5], 16, 8, 4)
+    good = dict(block_table=ints(x[0]), seq_lens=ints(x[1]), free_blocks=ints(x[2]), free_count=ints([x[3]]), BLOCK=16, width=2)
+    for name in ("kept", "granted"):
+        for bad in (ints([0]), ints([0, 0]).long(), ints([0, 0]).cpu(), ints([0, 0, 0, 0])[::2]):
+            with pytest.raises(ValueError):
+                pa.plan_blocks(**good, **{name: bad})
+        with pytest.raises(pa.PagedAttentionError):
+            pa.plan_blocks(**good, **{name: good["seq_lens"]})
+
+
+@pytest.mark.gpu
 def test_a_refused_sequence_stores_nothing(pa):
     """A gives two of its blocks back, B takes them, then A asks for more than there is: A's table still names B's blocks."""
     c = Cache(40, [40, 0], 2, 64, 16, width=3)

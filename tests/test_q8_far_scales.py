@@ -80,3 +80,14 @@ def test_bits_do_not_depend_on_blocks_of_others(pa):
     torch.cuda.synchronize()
     for x in got[1:]:
         assert torch.equal(x, got[0])
+
+
+@pytest.mark.parametrize("G,NQ", [(2, 1), (12, 1), (8, 4)])
+@pytest.mark.parametrize("near,far", [(2.0 ** -96, 4.0), (0.0, 2.0 ** -10), (2.0 ** -60, 1.0)])
+def test_float16_outputs_beside_small_value_scales(pa, G, NQ, near, far):
+    """Zeros and near zeros beside ordinary values, as a padded cache has them."""
+    for B, n, D, BLOCK in ((1, 12000, 64, 8), (2, 500, 128, 16)):
+        c = Cache(64, [n] * B, 1, D, BLOCK)
+        for share in (0.1, 0.9):
+            c.vs = np.where(c.rng.random(c.vs.shape) < share, np.float32(far), np.float32(near)).astype(np.float32)
+            attend(pa, c, rows_of(c.rng, "f16", B, G, NQ, D) * 0.5, "f16", True)
