@@ -56,6 +56,9 @@ struct Sequence {
 
 __device__ __forceinline__ int div_block(const PlanParams& p, int x) { return p.shift >= 0 ? x >> p.shift : x / p.BLOCK; }
 
+// Blocks of x tokens (x + BLOCK may pass 2^31).
+__device__ __forceinline__ int blocks_of(const PlanParams& p, int x) { return x > 0 ? div_block(p, x - 1) + 1 : 0; }
+
 __device__ __forceinline__ Sequence sequence(const PlanParams& p, int b, int& bad)
 {
     Sequence s;
@@ -65,8 +68,8 @@ __device__ __forceinline__ Sequence sequence(const PlanParams& p, int b, int& ba
     s.add = min(max(a, 0), p.N);
     if (s.n != n || (p.keep && s.keep != k) || s.add != a)
         bad |= PA_STATUS_BAD_LENGTH;
-    s.have = div_block(p, s.n + p.BLOCK - 1);
-    s.need = div_block(p, s.keep + s.add + p.BLOCK - 1);
+    s.have = blocks_of(p, s.n);
+    s.need = blocks_of(p, s.keep + s.add);
     return s;
 }
 
@@ -182,7 +185,7 @@ __global__ void __launch_bounds__(kPlanThreads) pa_plan_kernel(const __grid_cons
         if (at < count)
             return p.stack[at];
         const int i = at - count, b = owner(given, B, i);
-        const int need = div_block(p, span[b].x + max(span[b].y, 0) + p.BLOCK - 1);
+        const int need = blocks_of(p, span[b].x + max(span[b].y, 0));
         return p.table[static_cast<int64_t>(b) * p.maxb + need + i - given[b]];
     };
     const int step = gridDim.x * kPlanThreads, me = blockIdx.x * kPlanThreads + tid;

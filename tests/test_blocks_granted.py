@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_blocks import A, ALIGN, DIMS, call, expect, state
+from test_blocks import A, ALIGN, DIMS, call, check, expect, state
 from test_q8 import Cache, as64, ints, rows_of
 from test_q8_together import Loop, feed
 
@@ -58,6 +58,18 @@ def test_kept_and_granted(pa, spare):
             np.testing.assert_array_equal(k.cpu().numpy(), want[0])
             np.testing.assert_array_equal(g.cpu().numpy(), want[1])
             assert torch.equal(k + g, new)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("BLOCK", [2 ** 30 - 1, 2 ** 29, 2 ** 29 - 3])
+def test_the_largest_blocks(pa, BLOCK):
+    """Lengths whose sum with a block passes 2^31."""
+    maxb = (2 ** 30 - 1) // BLOCK
+    pool = (2 ** 31 - 1) // BLOCK
+    lens = np.array([maxb * BLOCK, maxb * BLOCK, 0][: pool + 1])
+    table = np.arange(len(lens) * maxb).reshape(len(lens), maxb) % pool
+    for N, keep in ((1, [0, 1, 0]), (70, [maxb * BLOCK, maxb * BLOCK - 70, 0]), (65536, [maxb * BLOCK - 65535, 5, 0])):
+        check(pa, table, lens, np.full(pool, -1), 0, BLOCK, N, add=[N] * len(lens), keep=keep[: len(lens)], again=False)
 
 
 @pytest.mark.gpu
