@@ -312,6 +312,8 @@ __global__ void __launch_bounds__(append_threads(BLOCK * D), sizeof(T) == 2 ? 67
 #pragma unroll
             for (int i = 0; i < kWarps; ++i)
                 a[kv] = fmaxf(a[kv], part[kv][warp / kWarps * kWarps + i]);
+    } else {
+        __syncwarp();  // (all have read the earlier scales, one stores the new ones)
     }
 
     uint32_t lo[8], hi[8];  // of this thread's keys: lowest and highest code by channel, two a word
