@@ -56,8 +56,12 @@ struct Sequence {
 
 __device__ __forceinline__ int div_block(const PlanParams& p, int x) { return p.shift >= 0 ? x >> p.shift : x / p.BLOCK; }
 
-// Blocks of x tokens (x + BLOCK may pass 2^31).
-__device__ __forceinline__ int blocks_of(const PlanParams& p, int x) { return x > 0 ? div_block(p, x - 1) + 1 : 0; }
+// Blocks of x tokens (x + BLOCK may pass 2^31, not 2^32).
+__device__ __forceinline__ int blocks_of(const PlanParams& p, int x)
+{
+    const uint32_t up = static_cast<uint32_t>(x) + static_cast<uint32_t>(p.BLOCK) - 1u;
+    return static_cast<int>(p.shift >= 0 ? up >> p.shift : up / static_cast<uint32_t>(p.BLOCK));
+}
 
 __device__ __forceinline__ Sequence sequence(const PlanParams& p, int b, int& bad)
 {
