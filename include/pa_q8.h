@@ -116,8 +116,9 @@ int pa_q8_read(const int8_t *k_cache, const int8_t *v_cache, const float *k_scal
  * block first).  selected[b][h][0 .. m-1] are their indices in the table row in
  * ascending order, m = counts[b][h] = min(nb, budget); -1 behind them.
  *
- * The score bounds the queries' products with the block's keys from above, in
- * whole numbers.  For each query row of the KV head (H / KV heads, NQ rows):
+ * The score bounds the products of the quantised queries with the block's
+ * quantised keys from above, in whole numbers (a real product may exceed it by
+ * the row's rounding).  For each query row of the KV head (H / KV heads, NQ rows):
  *   step  = max(largest finite magnitude / 127, 2^-96), as in pa_q8_append
  *   c     = the row's codes by that step, as in pa_q8_append
  *   total = sum over d of max(c[d] * bounds[0][d], c[d] * bounds[1][d])
@@ -156,8 +157,8 @@ int pa_q8_select(const void *q, const int8_t *bounds, const float *k_scale,
  * counts twice.
  *
  * Scores, softmax statistics and sums are float32.  Codes are exact in the
- * products; 16-bit queries enter them with their own digits, float32 queries
- * with 22 bits, weights with 22, and with 11 where q is bfloat16 and H / KV * NQ
+ * products; 16-bit queries enter them with their own digits (those below 2^-35
+ * of the row's largest element are lost), float32 queries with 22 bits, weights with 22, and with 11 where q is bfloat16 and H / KV * NQ
  * > 8.  out is of q's dtype.
  *
  * Scales have to be finite, key scales below 2^114 and value scales at most 2^96;

@@ -3,23 +3,25 @@
 //
 // Work: segments (sequence, KV head, group of 8 NT query rows), each a run of
 // tiles of 32 tokens.  Teams of up to four CTAs take neighbouring heads of the
-// same tokens, whose cache lines lie together (24 to 64 uneven sequences: 30.5 us,
-// one CTA a team 34.7).  A team takes a segment whole, an equal piece of one, or,
+// same tokens, whose cache lines lie together (24 to 64 uneven sequences, 89 MB: 29.6 us,
+// one CTA a team 32.8).  A team takes a segment whole, an equal piece of one, or,
 // where there are more segments than teams, a range of all segments' tiles laid end
 // to end, in which every piece costs a charge besides its tiles (without charges
-// 42 us for the uneven batch, 25 instead of 20 for one long sequence; without whole
-// segments and equal pieces 40 instead of 26 for 32 rows a head).  Of many short
+// 42 us for the uneven batch at the time, 25 instead of 20 for one long sequence; ranges
+// alone, without whole segments and equal pieces, 24.9 instead of 20.1 for 64 MB of 24
+// even sequences).  Of many short
 // segments a warp takes whole ones by itself, and no states are joined.  The states of a
 // segment cut between CTAs (maximum, sum, values) go to the workspace, and the last
 // CTA to finish one joins them: about 4 us, which whole segments save (64 MB of 24
-// even sequences 19 us, of 16, which are cut, 21).  A CTA starts the copies of its
+// even sequences 20 us, of 16, which are cut, 22).  A CTA starts the copies of its
 // next piece before it joins its warps' states of the last.
 //
-// What bounds it: memory, at 6.3 TB/s while it streams (one sequence of 256 MB in
-// 49 us); a call besides costs about 5.7 us before the first tiles are there
-// (lengths, ranges, table, then copies that all begin at once) and 3 to 5 behind
-// the last (65 MB of one sequence 19.5 us).  With 32 query rows a head it is the
-// instructions: 1.5 a cycle on two warps a scheduler, tensor cores active 23 %.
+// What bounds it: memory, at 6.3 TB/s while it streams (one sequence of 268 MB in
+// 54 us, of 537 MB in 97); a call besides costs about 5.7 us before the first tiles are
+// there (lengths, ranges, table, then copies that all begin at once) and 3 to 5 behind
+// the last (67 MB of one sequence 20.6 us).  With 32 query rows a head it is the
+// instructions: 1.3 a cycle on two warps a scheduler, tensor cores active 28 %
+// (fp16, 31.7 us for 16 x 2048 tokens).
 //
 // Tiles: a warp streams its own tiles through a ring of shared memory with
 // 16-byte asynchronous copies, whole lines of 128 bytes together (copies in the
@@ -32,12 +34,13 @@
 //                  channels D / 8 g ...: two tokens' codes interleaved are V^T's
 //                  fragment.
 // More than eight rows of 16 bits take the products' 16-row side instead, S = Q K^T
-// and O += P V (16 x 2048 tokens, 32 rows a head: 27.8 -> 25.5 us).
+// and O += P V (16 x 2048 tokens, 32 rows a head: 27.8 -> 25.5 us, weights of one part).
 // Codes become fp16 exactly (byte u = code + 128 under the exponent of 1024 is
 // 1024 + u; less 1152).  Keys of 16-bit rows skip the subtraction: u by itself is a
 // subnormal number, and 128 times the row's sum is taken off beforehand.  A query
-// row is scaled by a power of two into fp16's range, which loses nothing of a
-// 16-bit row; float32 rows are two fp16 parts.
+// row is scaled by a power of two, its largest element to 2^11: a 16-bit row keeps its
+// digits but for those below 2^-35 of its largest element (fp16's last subnormal);
+// float32 rows are two fp16 parts.
 //
 // Scales: the key scale multiplies the score.  The value scale joins the
 // exponent, t = s + log2(v_scale), so that weights times value scale come out of
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C, PW>::kThreads, C) pa_q8_de
         if (segments < teams) {
             // tiles / (teams - segments) always does; pieces end on average half a piece early,
             // so that two smaller sizes are tried where it counts (0.3 us; nine sequences of
-            // 42 MB 19.9 -> 18.2 us): with few segments they are nearly the same, with nearly as
+            // 64 MB 24.2 -> 21.3 us): with few segments they are nearly the same, with nearly as
             // many as teams there is no room to cut
             int cut = static_cast<int>(static_cast<float>(tiles) * fast_rcp(static_cast<float>(teams - segments)));
             cut = max(4, cut + (cut >> 20) + 1);  // (not below the quotient)
@@ -362,8 +365,8 @@ __global__ void __launch_bounds__(Shape<D, NT, QP, C, PW>::kThreads, C) pa_q8_de
     // Short ones: a warp takes a segment by itself, the next at a distance of all warps of
     // the grid.  A tile of a warp's own costs about 7 / C of a share's (1.0 us), its start
     // and end one more; a share its starts (charged) and a join.  8 heads of 128 channels,
-    // by itself / shares: 100 sequences of 64 tokens 8.1 / 20.4 us, of 256 16.9 / 26.6,
-    // of 1024 48 / 51, 40 of 1024 37 / 29; 800 of 64 tokens 32 / 230.
+    // by itself / shares: 100 sequences of 64 tokens 8.0 / 19.6 us, of 256 17.4 / 27.2,
+    // of 1024 50 / 54.5, 60 of 512 22.7 / 29.0; 800 of 64 tokens 33 / 226.
     const int solo_step = gridDim.x * kWarps, solo_end = segments << p.lg_team;
     bool solo = false;
     if (kMany && piece == 0) {
@@ -1292,13 +1295,13 @@ Variant variant(int BLOCK)
 // `segments`: of 8 query rows.  One CTA of 12 warps per SM streams a segment twice as
 // fast as one of two with 6 each and keeps up to a segment per SM whole; two fill
 // in for each other's starts and ends, which counts where CTAs take several pieces.
-// 64 MB, one / two: one sequence of 8 heads 19.6 / 23.2 us, 13 even ones 18.2 / 21.9,
-// 40 even ones 29.7 / 25.3, 192 selected lists 24.7 / 16.6; 12 to 19 uneven
-// sequences (28 to 63 MB) 18 to 24 / 16 to 22.  Lists that were selected are mostly
+// 64 MB, one / two: one sequence of 8 heads 20.7 / 24.4 us, 13 even ones 19.7 / 23.0,
+// 40 even ones 31.9 / 26.9, 192 selected lists 26.7 / 18.0; 12 to 19 uneven
+// sequences (26 to 51 MB) 20 to 25 / 16 to 21.  Lists that were selected are mostly
 // of one length, sequences seldom.  Three of 4 warps are for as many segments as
-// they still keep whole: 40 sequences of 512 / 1024 tokens 14.1 / 21.1 us (two: 23.3 /
-// 29.2), 40 uneven ones of 43 MB 20.4 (23.7); with fewer segments they are slower (24
-// even sequences 21.7, two: 19.0), with more no better (60 of 512 tokens 26.6, 22.7).
+// they still keep whole: 40 sequences of 512 / 1024 tokens 14.9 / 22.3 us (two: 24.0 /
+// 30.0), 40 uneven ones of 43 MB 21.5 (24.6); with fewer segments they are slower (24
+// even sequences 21.7, two: 20.0), with more no better (60 of 512 tokens 27.4, 22.8).
 template <int D>
 Variant variant(int BLOCK, int dtype, int R, long long segments, int sms, int entries, bool even)
 {

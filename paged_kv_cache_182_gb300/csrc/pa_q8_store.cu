@@ -7,10 +7,14 @@
 // magnitude and their codes.  The largest magnitudes, and for keys the lowest and
 // highest codes by channel, are joined by shuffles and through shared memory.  Earlier
 // codes are read only where the scale grew, and for the bounds.
-// Prompts of 16-bit rows (130 MB, 8 heads of 128 channels): 20.8 us, 6.3 TB/s; the
-// arithmetic of the codes then fills half the issue slots (41 us before ties were
-// corrected in registers, 34 before own scales spared the check).  A step of one row
-// a sequence is a launch and two dependent reads, 3.9 us.
+// Prompts (4 of 3080 rows, 8 heads of 128 channels, bounds): 16-bit rows 19.4 us, 4.0
+// TB/s, float32 31.8 us, 4.0 TB/s (one of 65536 rows 80 us, 5.0, and 147, 4.6).  Neither
+// memory nor arithmetic is full (29 % of the peak, half the issue slots): a CTA lives
+// for one block, and little but the other CTAs covers its chain of length, table, rows,
+// maximum, codes (41 us before ties were corrected in registers, 34 before own scales
+// spared the check).  A step of one row a sequence is a launch and two dependent reads,
+// 3.1 us back to back, 7.4 to 8.3 where every block's scale grows (12.7 with 31 of 32
+// rows there): the earlier codes are then rounded again byte by byte.
 //
 // pa_q8_read_kernel: a thread takes runs of 16 codes, about four one after another,
 // heads and columns innermost: whole lines both ways.  Memory bounds it: 201 MB in
