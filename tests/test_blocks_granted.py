@@ -173,6 +173,26 @@ def test_a_loop_with_too_few_blocks(pa):
 
 
 @pytest.mark.gpu
+def test_two_plans_in_turn(pa):
+    """A loop without copies: each plan's lengths and count are what the other one left."""
+    rng = np.random.default_rng(16)
+    table, lens, stack, count = state(17, [40, 3, 0, 17], 8, 12, 9)
+    t, s, n, c, add, keep = ints(table), ints(stack), ints(lens), ints([count]), ints([0] * 4), ints([0] * 4)
+    one = pa.BlockPlan(t, n, s, c, BLOCK=8, width=20, add=add, keep=keep)
+    two = pa.BlockPlan(t, one.new_lens, s, one.new_free_count, BLOCK=8, width=20, add=add, keep=keep, new_lens=n, new_free_count=c)
+    for step in range(30):
+        k = np.where(rng.random(4) < 0.2, lens // 3, lens)
+        a = rng.integers(0, 21, 4) * (rng.random(4) < 0.5)
+        add.copy_(ints(a)), keep.copy_(ints(k))
+        new, left, slots, pos = (one, two)[step % 2].run()
+        torch.cuda.synchronize()
+        want = expect(table, lens, stack, count, 8, 20, add=a, keep=k)
+        table, stack, lens, count = want[:4]
+        for g, w in zip((t, s, new, left, slots, pos), want):
+            np.testing.assert_array_equal(g.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1))
+
+
+@pytest.mark.gpu
 def test_a_refusal_in_a_graph(pa):
     a, b, rng = Tight(pa, seed=14), Tight(pa, seed=14), np.random.default_rng(15)
     steps, refused = [], 0
